@@ -35,9 +35,9 @@
  *     validated on the host before anything is launched; an invalid argument
  *     returns EDGE0_EINVAL and launches nothing.
  *   - Stream capture into CUDA graphs is supported only for the allocation-free
- *     call (see its section): the first-use uploads above are synchronous, and
- *     the batched path (B > 4) and prefill upload a small per-call table from
- *     host memory.
+ *     call and the projection, cache and attention calls (see their sections): the
+ *     first-use uploads above are synchronous, and the batched path (B > 4) and
+ *     prefill upload a small per-call table from host memory.
  *   - Kernels never trap: a wait that runs out of time records EDGE0_ETIMEOUT in
  *     the route state's control block (read it with edge0_state_error) and the
  *     kernel returns.
@@ -401,6 +401,87 @@ int edge0_pool_stats_ex(const edge0_pool* pool, long long* out, int n);
 int edge0_pool_stats(const edge0_pool* pool, long long* hits, long long* copies);
 int edge0_pool_resident(const edge0_pool* pool, int l, int32_t* slot_of);
 void edge0_pool_destroy(edge0_pool* pool);
+
+/* ---- the block's other half: int4 projections, quantised KV cache, decode attention ----
+ * The pages' decoder block has, besides the MoE part, int4 projections (attention and
+ * linear-attention projections are int4 and LoRA targets, S3.3) and a KV cache whose
+ * growth they name.  These calls are its GB300 form for up to EDGE0_MAX_BATCHED
+ * sequences.  They synchronise nothing, keep no state, copy nothing from the host and
+ * may be captured into a CUDA graph (lengths, positions and page tables are read on
+ * the device at each replay).
+ *
+ * Limits: head_dim 64, 128 or 256; bits 4 or 8; page_tokens a multiple of 16 up to
+ * EDGE0_MAX_PAGE_TOKENS; other values return EDGE0_EUNSUPPORTED. */
+#define EDGE0_MAX_KV_HEADS 64
+#define EDGE0_MAX_Q_PER_KV 64       /* query heads that share one K/V head */
+#define EDGE0_MAX_PAGE_TOKENS 4096
+
+/* Dense int4 projection [S2, S3.1: the int4 affine group-64 format]: y[b] = W x[b],
+ * W [out, in] packed by edge0_pack_q4_rows with E = 1; add the projection's LoRA with
+ * edge0_lora_delta.  x: B rows of `in` fp16, ldx elements apart (16-byte aligned, ldx a
+ * multiple of 8, ldx >= in); y: B rows of `out` fp16, ldy apart (ldy >= out; what lies
+ * between the rows is not touched).  in % 64 == 0, out any; 1 <= B <=
+ * EDGE0_MAX_BATCHED.  fp32 sums, rounded once.  x and y may not overlap. */
+int edge0_q4_linear(const void* packed, int out, int in, const uint16_t* x, long long ldx, int B,
+                    uint16_t* y, long long ldy, cudaStream_t stream);
+
+/* A pool of n_pages pages of K and V codes at `pages` (16-byte aligned, n_pages *
+ * edge0_kv_page_bytes bytes, owned by the caller).  Sequences are lists of pages.
+ * Per (token, kv head, K or V, 64 dims), with mn and mx over the 64 fp16 values:
+ *   s = fp16((mx - mn) / (2^bits - 1)), b = mn, q = rne((x - mn) / s) in
+ *   [0, 2^bits - 1] (0 where s = 0); the group stands for s q + b.  A group with an
+ *   infinity or NaN stands for NaN throughout.
+ * Page: [kv head][strip of 16 tokens][K codes | K (s, b) | V codes | V (s, b)]; a token's
+ * codes are R = head_dim * bits / 8 bytes (4 bits: dim 2j in the low half of byte j), its
+ * 16-byte piece c stored at piece c ^ turn(r) of row r = token % 16, turn(r) = r & 7 for
+ * R >= 128, else (r R / 128) & (R / 16 - 1); (s, b) are fp16 pairs, groups in order. */
+typedef struct {
+    int bits, n_kv_heads, head_dim, page_tokens, n_pages;
+    void* pages;
+} edge0_kv_cache;
+/* bytes of one page; 0 for values outside the limits */
+size_t edge0_kv_page_bytes(int bits, int n_kv_heads, int head_dim, int page_tokens);
+
+/* Rows of a call on B sequences (both calls below): row r of [0, T) belongs to the
+ * sequence b with cu_rows[b] <= r < cu_rows[b + 1] (cu_rows [B + 1], non-decreasing; NULL:
+ * T == B, one row per sequence) and to its position start[b] + r - cu_rows[b], which
+ * lies in page table[b][position / page_tokens] (table [B][W]).  Rows outside
+ * [cu_rows[0], cu_rows[B]) and rows of a sequence with start[b] < 0 (padding) are left
+ * alone.  A position at or behind W * page_tokens or a page outside [0, n_pages) is
+ * recorded as EDGE0_EINVAL in *status (device int set to 0 by the caller, or NULL) and
+ * that row left alone.  table, start, cu_rows: device int32.
+ *
+ * edge0_kv_append: quantises K and V rows into the pages.  k, v: T rows of n_kv_heads *
+ *   head_dim fp16, ldk / ldv elements apart (16-byte aligned, multiples of 8).  A slot is
+ *   written by at most one row of a call: sequences may share pages only where none of
+ *   them writes.
+ * edge0_kv_read: the rows' values fp16(s q + b), k and v [T][n_kv_heads][head_dim]
+ *   (16-byte aligned). */
+int edge0_kv_append(const edge0_kv_cache* cache, const uint16_t* k, long long ldk, const uint16_t* v,
+                    long long ldv, int T, const int32_t* table, int B, int W, const int32_t* start,
+                    const int32_t* cu_rows, int* status, cudaStream_t stream);
+int edge0_kv_read(const edge0_kv_cache* cache, const int32_t* table, int B, int W, const int32_t* start,
+                  const int32_t* cu_rows, int T, uint16_t* k, uint16_t* v, int* status,
+                  cudaStream_t stream);
+
+/* Decode attention, one query token per sequence, over keys and values
+ *   [the shared prefix: positions [0, n_prefix) of the pages `prefix`] then
+ *   [the sequence's own: positions [0, lens[b]) of the pages table[b]],
+ * o[b, i] = sum_j softmax_j(scale q[b, i] . k_j) v_j with K/V head i / (n_q_heads /
+ * n_kv_heads).  The prefix is read once for the whole batch.  q, out: B rows of
+ * n_q_heads * head_dim fp16, ldq / ldo elements apart (16-byte aligned, multiples of 8);
+ * lens [B], table [B][W], prefix: device int32; n_prefix, W: host; 0 < scale <= 1e6.
+ * A sequence without any token gets zeros; lens[b] < 0 marks a padding row, whose
+ * output is left as it was.  lens[b] above W * page_tokens (cut there) and pages
+ * outside [0, n_pages) (page 0 is read in their place) are recorded as EDGE0_EINVAL in
+ * *status as above.  workspace: scratch of edge0_attn_workspace_bytes (16-byte aligned,
+ * not cleared beforehand, nothing kept in it); calls that may overlap on the GPU need
+ * one each.  The result does not depend on the timing of the run. */
+size_t edge0_attn_workspace_bytes(const edge0_kv_cache* cache, int B, int n_q_heads);
+int edge0_attn_decode(const edge0_kv_cache* cache, const uint16_t* q, long long ldq, int B, int n_q_heads,
+                      const int32_t* table, int W, const int32_t* lens, const int32_t* prefix,
+                      int n_prefix, float scale, uint16_t* out, long long ldo, int* status,
+                      void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* ---- allocation-free variant (the paper has no counterpart to this call) ----
  * edge0_moe_int4_forward for callers that cannot allocate memory: code running

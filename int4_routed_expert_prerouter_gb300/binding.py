@@ -6,6 +6,7 @@ library and raises if it is missing -- there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -76,6 +77,11 @@ class RouteState(C.Structure):
                 ("workspace_bytes", C.c_size_t), ("record_h", P), ("record_logits", P)]
 
 
+class KvCacheDesc(C.Structure):
+    _fields_ = [("bits", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int),
+                ("page_tokens", C.c_int), ("n_pages", C.c_int), ("pages", P)]
+
+
 def _declare(L):
     L.edge0_status_string.argtypes = [C.c_int]
     L.edge0_status_string.restype = C.c_char_p
@@ -126,12 +132,23 @@ def _declare(L):
                                      C.c_int, P]
     L.edge0_decode_step.argtypes = [C.POINTER(LayerDesc), C.c_int, P, C.POINTER(RouteState),
                                     C.c_int, C.c_int, P]
+    L.edge0_q4_linear.argtypes = [P, C.c_int, C.c_int, P, C.c_longlong, C.c_int, P, C.c_longlong, P]
+    L.edge0_kv_page_bytes.argtypes = [C.c_int] * 4
+    L.edge0_kv_page_bytes.restype = C.c_size_t
+    L.edge0_kv_append.argtypes = [C.POINTER(KvCacheDesc), P, C.c_longlong, P, C.c_longlong, C.c_int, P, C.c_int,
+                                  C.c_int, P, P, P, P]
+    L.edge0_kv_read.argtypes = [C.POINTER(KvCacheDesc), P, C.c_int, C.c_int, P, P, C.c_int, P, P, P, P]
+    L.edge0_attn_workspace_bytes.argtypes = [C.POINTER(KvCacheDesc), C.c_int, C.c_int]
+    L.edge0_attn_workspace_bytes.restype = C.c_size_t
+    L.edge0_attn_decode.argtypes = [C.POINTER(KvCacheDesc), P, C.c_longlong, C.c_int, C.c_int, P, C.c_int, P, P,
+                                    C.c_int, C.c_float, P, C.c_longlong, P, P, C.c_size_t, P]
     for name in ("edge0_pack_q4_gate_up", "edge0_pack_q4_down", "edge0_pack_q4_rows", "edge0_pack_f16",
                  "edge0_pack_f16_kmajor", "edge0_pack_cols_T", "edge0_state_init",
                  "edge0_state_error", "edge0_prerouter_topk", "edge0_moe_int4_forward",
                  "edge0_lora_delta", "edge0_decode_layer", "edge0_decode_step",
                  "edge0_moe_int4_forward_noalloc", "edge0_state_set_wait_limit", "edge0_noalloc_error",
-                 "edge0_prefill", "edge0_tc_gemm_f16"):
+                 "edge0_prefill", "edge0_tc_gemm_f16", "edge0_q4_linear", "edge0_kv_append", "edge0_kv_read",
+                 "edge0_attn_decode"):
         getattr(L, name).restype = C.c_int
 
 
@@ -145,7 +162,8 @@ EXPORTED = ["edge0_status_string", "edge0_q4_gate_up_packed_bytes", "edge0_pack_
             "edge0_prefill", "edge0_tc_gemm_f16", "edge0_pool_create", "edge0_pool_set_layer",
             "edge0_pool_plan", "edge0_pool_host_prefetch", "edge0_pool_host_copy", "edge0_pool_device_init",
             "edge0_pool_prefetch_async", "edge0_pool_wait", "edge0_pool_inject", "edge0_pool_stats_ex", "edge0_pool_stats",
-            "edge0_pool_resident", "edge0_pool_destroy"]
+            "edge0_pool_resident", "edge0_pool_destroy", "edge0_q4_linear", "edge0_kv_page_bytes",
+            "edge0_kv_append", "edge0_kv_read", "edge0_attn_workspace_bytes", "edge0_attn_decode"]
 
 
 def status_string(code: int) -> str:
@@ -563,3 +581,170 @@ def lora_delta(desc: LoraDesc, v, y, stream=None):
     _check(lib().edge0_lora_delta(C.byref(desc), _ptr(v), B, _ptr(y), _stream(stream)),
            "edge0_lora_delta")
     return y
+
+
+# ------------------------------- projections, KV cache, decode attention ----
+def _need(cond, what):
+    if not cond:
+        raise Edge0Error(EDGE0_EINVAL, what)
+
+
+def _on(t, stream):
+    """Allocations and launches of one call: the tensors' device, the call's stream."""
+    es = contextlib.ExitStack()
+    es.enter_context(torch.cuda.device(t.device))
+    if stream is not None:
+        es.enter_context(torch.cuda.stream(stream))
+    return es
+
+
+def _need_rows(t, what, *shape):
+    """t: fp16 rows of the given trailing shape on a GPU, dense within a row, rows a
+    multiple of 16 bytes apart (a slice of a wider row-major tensor passes)."""
+    _need(t.is_cuda and t.dtype == torch.float16 and t.dim() == 1 + len(shape), f"{what}: fp16 rows on a GPU")
+    _need(tuple(t.shape[1:]) == shape, f"{what}: rows of shape {shape}, not {tuple(t.shape[1:])}")
+    dense = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        _need(stride == dense or size == 1, f"{what}: rows are not dense")
+        dense *= size
+    return dense if t.shape[0] <= 1 else t.stride(0)
+
+
+def _need_i32(t, dev, what, *shape):
+    _need(t.dtype == torch.int32 and t.is_contiguous() and t.device == dev and tuple(t.shape) == shape,
+          f"{what}: int32 {list(shape)}, contiguous, on {dev}")
+    return _ptr(t)
+
+
+def q4_linear(packed: torch.Tensor, out_features: int, x: torch.Tensor, y=None, stream=None) -> torch.Tensor:
+    """y [B, out_features] = W x for x [B, in] fp16 and W packed by pack_q4_rows (one
+    matrix: E = 1).  x and y may be slices of wider rows."""
+    _need(x.dim() == 2 and packed.device == x.device and packed.dtype == torch.uint8, "q4_linear: x [B, in], packed")
+    B, n_in = x.shape
+    ldx = _need_rows(x, "q4_linear: x", n_in)
+    _need(packed.is_contiguous() and packed.numel() == lib().edge0_q4_down_packed_bytes(1, out_features, n_in) > 0,
+          "q4_linear: packed is not a [out_features, in] matrix")
+    with _on(x, stream):
+        if y is None:
+            y = torch.empty(B, out_features, dtype=torch.float16, device=x.device)
+        _need(y.device == x.device and y.shape[0] == B, "q4_linear: y")
+        ldy = _need_rows(y, "q4_linear: y", out_features)
+        if B:
+            _check(lib().edge0_q4_linear(_ptr(packed), out_features, n_in, _ptr(x), ldx, B, _ptr(y), ldy,
+                                         _stream(stream)), "edge0_q4_linear")
+    return y
+
+
+class KVCache:
+    """A pool of quantised K/V pages (edge0_kv_cache): bits 4 or 8 per value, one fp16
+    scale and bias per (token, kv head, 64 dims).  pages: uint8 [n_pages, page bytes]."""
+
+    def __init__(self, n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int, bits: int = 4, device="cuda",
+                 pages=None):
+        self.n_pages, self.page_tokens = n_pages, page_tokens
+        self.n_kv_heads, self.head_dim, self.bits = n_kv_heads, head_dim, bits
+        self.page_bytes = int(lib().edge0_kv_page_bytes(bits, n_kv_heads, head_dim, page_tokens))
+        if self.page_bytes == 0:
+            raise Edge0Error(EDGE0_EUNSUPPORTED, f"KVCache: bits {bits}, {n_kv_heads} heads of {head_dim}, "
+                                                 f"{page_tokens} tokens per page")
+        _need(n_pages > 0, "KVCache: n_pages")
+        if pages is None:
+            pages = torch.zeros(n_pages, self.page_bytes, dtype=torch.uint8, device=device)
+        _need(pages.is_cuda and pages.dtype == torch.uint8 and pages.is_contiguous()
+              and pages.numel() == n_pages * self.page_bytes, "KVCache: pages uint8 [n_pages, page bytes] on a GPU")
+        self.pages = pages
+        self.device = pages.device
+        self.status = torch.zeros(1, dtype=torch.int32, device=pages.device)
+        self.desc = KvCacheDesc(bits, n_kv_heads, head_dim, page_tokens, n_pages, _ptr(pages))
+
+    def error(self) -> int:
+        """What the calls on this cache have recorded since the last error() (waits
+        for the device): EDGE0_OK or EDGE0_EINVAL for a page or position out of range."""
+        torch.cuda.synchronize(self.device)
+        code = int(self.status.item())
+        self.status.zero_()
+        return code
+
+
+def _need_sequences(cache, table, start, cu_rows, T, what):
+    _need(table.dim() == 2, f"{what}: table [B, W]")
+    B, W = table.shape
+    args = (_need_i32(table, cache.device, f"{what}: table", B, W), B, W,
+            _need_i32(start, cache.device, f"{what}: start", B),
+            None if cu_rows is None else _need_i32(cu_rows, cache.device, f"{what}: cu_rows", B + 1))
+    _need(cu_rows is not None or T == B, f"{what}: one row per sequence without cu_rows")
+    return args
+
+
+def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table, start, cu_rows=None, stream=None):
+    """Quantise rows k, v [T, n_kv_heads, head_dim] fp16 into the pages: row r of
+    sequence b goes to position start[b] + r - cu_rows[b] (cu_rows None: row b is
+    sequence b's).  table [B, W], start [B], cu_rows [B + 1]: int32 on the device."""
+    T, shape = k.shape[0], (cache.n_kv_heads, cache.head_dim)
+    _need(k.device == cache.device and v.device == cache.device and v.shape[0] == T, "kv_append: k and v")
+    ldk, ldv = _need_rows(k, "kv_append: k", *shape), _need_rows(v, "kv_append: v", *shape)
+    tb, B, W, st, cu = _need_sequences(cache, table, start, cu_rows, T, "kv_append")
+    with _on(k, stream):
+        _check(lib().edge0_kv_append(C.byref(cache.desc), _ptr(k), ldk, _ptr(v), ldv, T, tb, B, W, st, cu,
+                                     _ptr(cache.status), _stream(stream)), "edge0_kv_append")
+
+
+def kv_read(cache: KVCache, table, start, cu_rows=None, T=None, k=None, v=None, stream=None):
+    """(k, v) [T, n_kv_heads, head_dim] fp16: the values that the rows' pages stand for
+    (rows as in kv_append).  k, v: contiguous outputs to fill, or None for new ones; rows
+    that no sequence has are left as they are."""
+    T = table.shape[0] if T is None else int(T)
+    tb, B, W, st, cu = _need_sequences(cache, table, start, cu_rows, T, "kv_read")
+    shape = (T, cache.n_kv_heads, cache.head_dim)
+    with _on(cache.pages, stream):
+        k, v = (torch.empty(shape, dtype=torch.float16, device=cache.device) if o is None else o for o in (k, v))
+        for o in (k, v):
+            _need(o.device == cache.device and o.dtype == torch.float16 and tuple(o.shape) == shape
+                  and o.is_contiguous(), f"kv_read: outputs fp16 {list(shape)}, contiguous")
+        _check(lib().edge0_kv_read(C.byref(cache.desc), tb, B, W, st, cu, T, _ptr(k), _ptr(v), _ptr(cache.status),
+                                   _stream(stream)), "edge0_kv_read")
+    return k, v
+
+
+def attn_workspace_bytes(cache: KVCache, B: int, n_q_heads: int) -> int:
+    return int(lib().edge0_attn_workspace_bytes(C.byref(cache.desc), B, n_q_heads))
+
+
+def attn_decode(cache: KVCache, q: torch.Tensor, table, lens, prefix=None, n_prefix=0, scale=None, out=None,
+                workspace=None, stream=None) -> torch.Tensor:
+    """Attention of one query token per sequence, q [B, n_q_heads, head_dim] fp16, over
+    the shared prefix (n_prefix tokens of the pages `prefix`, int32) and then the
+    sequence's own lens[b] tokens of the pages table[b].  scale: 1 / sqrt(head_dim)
+    unless given.  out: rows to fill (those of sequences with lens[b] < 0 are left as
+    they are) or None.  workspace: uint8 of attn_workspace_bytes, or None for one of the
+    call's own."""
+    _need(q.dim() == 3 and q.device == cache.device, "attn_decode: q [B, n_q_heads, head_dim]")
+    B, Hq, D = q.shape
+    ldq = _need_rows(q, "attn_decode: q", Hq, cache.head_dim)
+    _need(table.dim() == 2 and table.shape[0] == B, "attn_decode: table [B, W]")
+    W = table.shape[1]
+    tb = _need_i32(table, cache.device, "attn_decode: table", B, W)
+    ln = _need_i32(lens, cache.device, "attn_decode: lens", B)
+    n_prefix = int(n_prefix)
+    _need(n_prefix >= 0, "attn_decode: n_prefix")
+    if n_prefix:
+        _need(prefix is not None and prefix.dim() == 1 and prefix.numel() * cache.page_tokens >= n_prefix,
+              "attn_decode: prefix pages")
+        pf = _need_i32(prefix, cache.device, "attn_decode: prefix", prefix.numel())
+    else:
+        pf = None
+    scale = cache.head_dim ** -0.5 if scale is None else float(scale)
+    nbytes = attn_workspace_bytes(cache, B, Hq)
+    with _on(q, stream):
+        if out is None:
+            out = torch.empty(B, Hq, D, dtype=torch.float16, device=q.device)
+        _need(out.device == q.device and out.shape[0] == B, "attn_decode: out")
+        ldo = _need_rows(out, "attn_decode: out", Hq, cache.head_dim)
+        if workspace is None:
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        _need(workspace.device == q.device and workspace.dtype == torch.uint8 and workspace.is_contiguous(),
+              "attn_decode: workspace")
+        _check(lib().edge0_attn_decode(C.byref(cache.desc), _ptr(q), ldq, B, Hq, tb, W, ln, pf, n_prefix, scale,
+                                       _ptr(out), ldo, _ptr(cache.status), _ptr(workspace), workspace.numel(),
+                                       _stream(stream)), "edge0_attn_decode")
+    return out
