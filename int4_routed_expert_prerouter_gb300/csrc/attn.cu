@@ -1,99 +1,784 @@
-// Decode attention over the quantised KV cache: one query token per sequence,
+// Decode attention over the quantised KV cache, one query token per sequence:
 //     o = sum_j softmax_j(scale q . k_j) v_j
-// over the shared prefix's tokens and the sequence's own, in fp32 with a running
-// maximum and sum.  One CTA per (sequence, query head): its warps take the tokens in
-// turn, a lane holds D / 32 dims; the warps' results are joined in shared memory.
+// over a prefix that all sequences share and over the sequence's own tokens.
+//
+// Work.  A "segment" is one K/V head of one list of pages with up to 8 NT query rows
+// that read it: for a sequence's own pages the head's query group, for the shared
+// prefix the groups of all sequences (so its pages are read once per 8 NT rows, not
+// once per sequence).  The units (16 US tokens) of all segments in a row are cut
+// into equal shares, one per CTA; a segment that falls into several shares leaves
+// partial results (running maximum, sum, unnormalised o) that attn_join_kernel adds up
+// in the order of the units.  Lengths are read on the device, so the launch does
+// not depend on them.
+//
+// Kernel.  The warps of a CTA take the units of its share in turn, each through its
+// own ring of bulk copies (a strip of 16 tokens of one head is one run of bytes).
+// Tokens are the M side of m16n8k16 steps and query rows the N side, so a group of
+// up to 8 query heads wastes nothing:
+//   S^T = K Q^T   codes enter as fp16 subnormals q 2^-24 (exact products, fp32 sums); per 64
+//                 dims S += s acc + b sum(Q), in fp32: scores carry no rounding of K;
+//   O^T = V'^T P' V = s (q - z) + (b + s z), z half the code range: q - z is exact in
+//                 fp16, the weight p s is rounded to fp16 (its only rounding), scaled by a
+//                 power of two 2^-E at least the largest s so far so that it stays
+//                 normal; sum p (b + s z) is kept in fp32 beside it.
+// ldmatrix delivers K codes as A fragments and, transposed, V codes with the
+// token pairs that the A fragments of V^T want; P^T goes from accumulator to
+// B fragment with movmatrix.  The running maximum moves only when a score exceeds
+// it by 2^8, so most units rescale nothing.
 #include "kvcache.cuh"
 
 namespace edge0 {
 namespace {
 
-constexpr int kAttnWarps = 4;
+constexpr int kWarps = 4;
+constexpr int kMaxGrid = 152 * 8;
+constexpr int kMinShare = 2 * kWarps;   // units a CTA takes at least
 
 struct AttnP {
     kv::View c;
     const __half* q;
     long long ldq;
-    int B, Hq;
-    const int* table;
+    int G, H;                // query heads per K/V head, K/V heads
+    // segments: n_seq lists of pages; rows of list i of head h: r -> query
+    // row (i * seq_rows + r / G, h G + r % G)
+    int n_seq, rows, RB, q_step;
+    const int* pages;        // [n_seq][W]
     int W;
-    const int* lens;
-    const int* prefix;
-    int n_prefix;
-    float scale;
-    __half* out;
+    const int* lens;         // [n_seq], or null: every list has n_tok tokens
+    int n_tok;
+    float k;                 // 2^24 scale log2(e): raw scores to the exponent
+    float* part_o;           // [slots][8 NT][D]
+    float2* part_ml;         // [slots][8 NT] (maximum in exponent units, sum)
+    int2* seg;               // [segments] (first slot, slots)
+    __half* out;             // set: segments that one CTA has whole are written here
     long long ldo;
     int* status;
 };
 
-template <int BITS, int D>
-__global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(AttnP p) {
-    constexpr int kN = D / 32;
-    constexpr int kR = kv::row_bytes(BITS, D);
-    __shared__ float ms[kAttnWarps], ls[kAttnWarps], os[kAttnWarps][D];
-    const int b = blockIdx.x, hq = blockIdx.y, h = hq / (p.Hq / p.c.H);
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    long long own = p.lens[b];
-    if (own < 0) return;                                   // a padding row
-    if (own > (long long)p.W * p.c.page_tokens) {
-        own = (long long)p.W * p.c.page_tokens;
-        if (threadIdx.x == 0 && p.status) atomicExch(p.status, EDGE0_EINVAL);
+template <int BITS, int D, int NT>
+struct Cfg {
+    static constexpr int R = kv::row_bytes(BITS, D);
+    static constexpr int CH = R / 16;                 // 16-byte pieces of a row
+    static constexpr int GR = D / kGroup;
+    static constexpr int CPG = CH / GR;               // pieces of a group
+    static constexpr int QW = BITS == 4 ? 4 : 2;      // words of a query fragment per piece
+    static constexpr int STRIP = kv::strip_bytes(BITS, D);
+    static constexpr int HALF = kv::half_bytes(BITS, D);
+    static constexpr int SB = kv::sb_bytes(D);
+    static constexpr int US = STRIP <= 2304 ? 2 : 1;  // strips per unit
+    static constexpr int STAGES = STRIP * US >= 8000 ? 2 : STRIP * US >= 4300 ? (US == 2 ? 2 : 3) : 4;
+    static constexpr int MT = D / 16;
+    // shared memory
+    static constexpr int kRing = kWarps * STAGES * US * STRIP;
+    static constexpr int kQ = NT * CH * 32 * QW * 4;
+    static constexpr int kQsum = NT * 8 * GR * 4;
+    static constexpr int kRedLd = D + 4;
+    static constexpr int kRed = kWarps * 8 * kRedLd * 4;
+    static constexpr int kMl = kWarps * NT * 8 * 8;
+    static constexpr int kSmem = kRing + kQ + kQsum + kRed + kMl + kWarps * STAGES * 8 + 257 * 8 + 64;
+    static constexpr int kMinCtas = NT == 1 && D <= 128 ? 4 : NT == 4 ? 2 : D == 256 && NT == 2 ? 2 : 3;
+};
+
+__device__ __forceinline__ void copy_strip(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+// Waits for a stage's copies, at most kDefaultWaitNs; by a whole warp, which agrees on
+// the answer.
+__device__ __forceinline__ bool wait_copy(uint64_t* bar, uint32_t parity) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        unsigned long long t0, now;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+        do {
+            ok = mbar_try_wait(bar, parity);
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        } while (!ok && now - t0 < kDefaultWaitNs);
     }
-    float q[kN], o[kN], m = -INFINITY, l = 0.f;
-    for (int i = 0; i < kN; ++i) {
-        q[i] = __half2float(p.q[b * p.ldq + (long long)hq * D + lane * kN + i]) * p.scale;
-        o[i] = 0.f;
-    }
-    auto value = [&](const char* half, int rr, float (&x)[kN]) {
-        const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(
-            half + kv::kStrip * kR + rr * kv::sb_bytes(D) + (lane * kN / kGroup) * 4));
-        for (int i = 0; i < kN; ++i) {
-            const int d = lane * kN + i, off = d * BITS / 8;
-            const unsigned char w =
-                *reinterpret_cast<const unsigned char*>(half + rr * kR + (((off >> 4) ^ kv::turn(kR, rr)) << 4) + (off & 15));
-            const int code = BITS == 8 ? w : (d & 1) ? w >> 4 : w & 15;
-            x[i] = fmaf((float)code, sb.x, sb.y);
+    return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float max_over_rows(float v) {   // the 8 lanes of one t
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+__device__ __forceinline__ float sum_over_rows(float v) {
+    v += __shfl_xor_sync(0xffffffffu, v, 4);
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+    return v + __shfl_xor_sync(0xffffffffu, v, 16);
+}
+
+// A fragments of V^T, one 16-dim tile, from two transposed words (tokens 0-7 and 8-15):
+// the codes less z as fp16.  4 bits: tile `j` of the piece holds its nibbles 2j, 2j + 1.
+template <int BITS>
+__device__ __forceinline__ void v_frag(uint32_t x0, uint32_t x1, int j, uint32_t (&A)[4]) {
+    if (BITS == 4) {
+        if (j) {
+            x0 >>= 8;
+            x1 >>= 8;
         }
+        // 0x6400 is 1024: the nibble adds itself (low) or 16 times itself (high)
+        A[0] = hadd2((x0 & 0x000F000Fu) | 0x64006400u, 0xE408E408u);                  // - 1032
+        A[1] = hfma2((x0 & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);     // / 16 - 72
+        A[2] = hadd2((x1 & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
+        A[3] = hfma2((x1 & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+    } else {
+        A[0] = hadd2(__byte_perm(x0, 0x64646464u, 0x4240), 0xE480E480u);              // - 1152
+        A[1] = hadd2(__byte_perm(x0, 0x64646464u, 0x4341), 0xE480E480u);
+        A[2] = hadd2(__byte_perm(x1, 0x64646464u, 0x4240), 0xE480E480u);
+        A[3] = hadd2(__byte_perm(x1, 0x64646464u, 0x4341), 0xE480E480u);
+    }
+}
+
+// first dim of the pair that a lane holds in rows g and g + 8 of tile mt
+template <int BITS>
+__device__ __forceinline__ int dim_of(int mt, int g) {
+    return BITS == 4 ? 32 * (mt >> 1) + 4 * g + 2 * (mt & 1) : 16 * mt + 2 * g;
+}
+
+template <int BITS, int D, int NT>
+__global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_kernel(const AttnP p) {
+    using X = Cfg<BITS, D, NT>;
+    extern __shared__ __align__(128) char smem[];
+    char* ring = smem;
+    uint32_t* sq = reinterpret_cast<uint32_t*>(ring + X::kRing);
+    float* sqsum = reinterpret_cast<float*>(reinterpret_cast<char*>(sq) + X::kQ);
+    float* red = reinterpret_cast<float*>(reinterpret_cast<char*>(sqsum) + X::kQsum);
+    float2* sml = reinterpret_cast<float2*>(reinterpret_cast<char*>(red) + X::kRed);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(sml) + X::kMl);
+    long long* cum = reinterpret_cast<long long*>(bars + kWarps * X::STAGES);
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
+    constexpr int kUnit = 16 * X::US;
+
+    // units before each list: a scan over at most 256 lengths
+    const int per_list = p.H * p.RB;
+    const long long cap = (long long)p.W * p.c.page_tokens;
+    auto tokens_of = [&](int i) -> long long {
+        const long long n = p.lens ? (long long)p.lens[i] : (long long)p.n_tok;
+        return n < 0 ? 0 : n > cap ? cap : n;
     };
-    const long long n = p.n_prefix + own;
-    for (long long j = wid; j < n; j += kAttnWarps) {
-        const bool pre = j < p.n_prefix;
-        const long long pos = pre ? j : j - p.n_prefix;
-        const long long pg = pos / p.c.page_tokens;
-        const int tok = (int)(pos - pg * p.c.page_tokens);
-        int id = pre ? p.prefix[pg] : p.table[(long long)b * p.W + pg];
-        if (id < 0 || id >= p.c.n_pages) {
-            id = 0;
-            if (lane == 0 && p.status) atomicExch(p.status, EDGE0_EINVAL);
+    if (wid == 0) {
+        long long base = 0;
+        for (int i0 = 0; i0 < p.n_seq; i0 += 32) {
+            const int i = i0 + lane;
+            long long n = i < p.n_seq ? (tokens_of(i) + kUnit - 1) / kUnit * per_list : 0;
+            if (i < p.n_seq && p.lens && p.lens[i] > cap && blockIdx.x == 0 && p.status)
+                atomicExch(p.status, EDGE0_EINVAL);
+            const long long mine = n;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const long long o = __shfl_up_sync(0xffffffffu, n, s);
+                if (lane >= s) n += o;
+            }
+            if (i < p.n_seq) cum[i] = base + n - mine;
+            base += __shfl_sync(0xffffffffu, n, 31);
         }
-        const char* strip = p.c.pages + id * p.c.page_bytes +
-                            ((long long)h * (p.c.page_tokens / kv::kStrip) + tok / kv::kStrip) * kv::strip_bytes(BITS, D);
-        float x[kN], s = 0.f;
-        value(strip, tok % kv::kStrip, x);
-        for (int i = 0; i < kN; ++i) s += q[i] * x[i];
-        s = warp_sum(s);
-        const float mn = fmaxf(m, s), f = __expf(m - mn), e = __expf(s - mn);
-        value(strip + kv::half_bytes(BITS, D), tok % kv::kStrip, x);
-        for (int i = 0; i < kN; ++i) o[i] = o[i] * f + e * x[i];
-        l = l * f + e;
-        m = mn;
+        if (lane == 0) cum[p.n_seq] = base;
     }
-    if (lane == 0) {
-        ms[wid] = m;
-        ls[wid] = l;
-    }
-    for (int i = 0; i < kN; ++i) os[wid][lane * kN + i] = o[i];
+    if (tid < kWarps * X::STAGES) mbar_init(&bars[tid], 1);
+    fence_mbar_init();
     __syncthreads();
-    float top = -INFINITY, sum = 0.f;
-    for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, ms[w]);
-    for (int w = 0; w < kAttnWarps; ++w)
-        if (ls[w] != 0.f) sum += ls[w] * __expf(ms[w] - top);
-    for (int d = threadIdx.x; d < D; d += 32 * kAttnWarps) {
-        float v = 0.f;
-        for (int w = 0; w < kAttnWarps; ++w)
-            if (ls[w] != 0.f) v += os[w][d] * __expf(ms[w] - top);
-        p.out[b * p.ldo + (long long)hq * D + d] = __float2half_rn(n > 0 ? v / sum : 0.f);
+    const long long total = cum[p.n_seq];
+    long long share = (total + gridDim.x - 1) / gridDim.x;
+    if (share < kMinShare) share = kMinShare;
+    long long pos = share * blockIdx.x;
+    const long long end = pos + share < total ? pos + share : total;
+
+    char* my_ring = ring + wid * X::STAGES * X::US * X::STRIP;
+    uint64_t* my_bar = bars + wid * X::STAGES;
+    int it = 0;              // units this warp has taken so far: stage and parity
+    bool dead = false;       // a copy did not arrive in time
+    // the lane's row and piece in the 8x8 matrix loads
+    const int lr = (lane & 7) + 8 * ((lane >> 3) & 1);
+    const uint32_t row_off = lr * X::R;
+    const uint32_t piece = ((lane >> 4) ^ kv::turn(X::R, lr)) << 4;
+
+    while (pos < end) {
+        // the segment that holds unit `pos`
+        int lo = 0, hi = p.n_seq;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cum[mid] <= pos) lo = mid;
+            else hi = mid;
+        }
+        // lists without tokens share their successor's start: the search ends at the last one
+        const int seq = lo;
+        const long long n_tok = tokens_of(seq);
+        const long long units = (n_tok + kUnit - 1) / kUnit;
+        const long long in_list = pos - cum[seq];
+        const int hr = (int)(in_list / units);
+        const long long u0 = in_list - hr * units;
+        const int h = hr / p.RB, rb = hr - h * p.RB;
+        const long long u1 = u0 + (end - pos) < units ? u0 + (end - pos) : units;
+        const int sidx = (seq * p.H + h) * p.RB + rb;
+        const int* pages = p.pages + (long long)seq * p.W;
+        const int spp = p.c.page_tokens / kv::kStrip;
+
+        auto issue = [&](long long u, int stage) {   // whole warp
+            const long long s0 = u * X::US;
+            const long long left = (n_tok + 15) / 16 - s0;
+            const int n = left < X::US ? (int)left : X::US;
+            if (lane == 0) mbar_arrive_expect_tx(&my_bar[stage], n * X::STRIP);
+            __syncwarp();
+            if (lane < n) {
+                const long long st = s0 + lane, pg = st / spp;
+                int id = pages[pg];
+                if (id < 0 || id >= p.c.n_pages) {
+                    id = 0;
+                    if (p.status) atomicExch(p.status, EDGE0_EINVAL);
+                }
+                const char* src = p.c.pages + id * p.c.page_bytes + ((long long)h * spp + (st - pg * spp)) * X::STRIP;
+                copy_strip(my_ring + (stage * X::US + lane) * X::STRIP, src, X::STRIP, &my_bar[stage]);
+            }
+            __syncwarp();
+        };
+        long long ahead = dead ? u1 : u0 + wid;
+        int issued = it;
+#pragma unroll 1
+        for (int s = 0; s < X::STAGES - 1; ++s, ahead += kWarps)
+            if (ahead < u1) issue(ahead, issued++ % X::STAGES);
+
+        // query rows of the block as B fragments, and their sums over each 64 dims
+        const int r0 = rb * 8 * NT;
+        for (int i = tid; i < NT * X::CH * 32; i += 32 * kWarps) {
+            const int ln = i & 31, c = (i >> 5) % X::CH, nt = (i >> 5) / X::CH;
+            const int r = r0 + nt * 8 + (ln >> 2), tt = ln & 3;
+            uint32_t w[X::QW];
+#pragma unroll
+            for (int j = 0; j < X::QW; ++j) w[j] = 0;
+            if (r < p.rows) {
+                const __half* src = p.q + (long long)(seq * p.q_step + r / p.G) * p.ldq +
+                                    (long long)(h * p.G + r % p.G) * D + (BITS == 4 ? 32 * c + 8 * tt : 16 * c + 4 * tt);
+                if (BITS == 4) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src);
+                    const uint32_t sixteenth = 0x2C002C00u;
+                    // even nibbles 0,4 | 2,6, odd ones 1,5 | 3,7 (these come in sixteen times as large)
+                    w[0] = __byte_perm(v.x, v.z, 0x5410);
+                    w[1] = __byte_perm(v.y, v.w, 0x5410);
+                    w[2] = hfma2(__byte_perm(v.x, v.z, 0x7632), sixteenth, 0x80008000u);
+                    w[3] = hfma2(__byte_perm(v.y, v.w, 0x7632), sixteenth, 0x80008000u);
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2*>(src);
+                    w[0] = __byte_perm(v.x, v.y, 0x5410);    // dims 0, 2
+                    w[1] = __byte_perm(v.x, v.y, 0x7632);    // dims 1, 3
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < X::QW; ++j) sq[i * X::QW + j] = w[j];
+        }
+        for (int i = wid; i < NT * 8 * X::GR; i += kWarps) {
+            const int r = r0 + i / X::GR, gr = i % X::GR;
+            float s = 0.f;
+            if (r < p.rows) {
+                const __half2 v = *reinterpret_cast<const __half2*>(
+                    p.q + (long long)(seq * p.q_step + r / p.G) * p.ldq + (long long)(h * p.G + r % p.G) * D +
+                    gr * kGroup + 2 * lane);
+                s = __low2float(v) + __high2float(v);
+            }
+            s = warp_sum(s);
+            if (lane == 0) sqsum[i] = s * (1.f / kTwo24);
+        }
+        __syncthreads();
+
+        float O[X::MT][NT][4], beta[NT][X::GR][2], m[NT][2], l[NT][2], thr[NT][2], mu[NT][2], es[X::GR];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int mt = 0; mt < X::MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) O[mt][nt][i] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[nt][i] = thr[nt][i] = -INFINITY;
+                mu[nt][i] = l[nt][i] = 0.f;
+#pragma unroll
+                for (int gr = 0; gr < X::GR; ++gr) beta[nt][gr][i] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int gr = 0; gr < X::GR; ++gr) es[gr] = INFINITY;
+
+#pragma unroll 1
+        for (long long u = dead ? u1 : u0 + wid; u < u1; u += kWarps, ++it) {
+            if (ahead < u1) {
+                issue(ahead, issued++ % X::STAGES);
+                ahead += kWarps;
+            }
+            const int stage = it % X::STAGES;
+            if (!wait_copy(&my_bar[stage], (it / X::STAGES) & 1)) {   // give up: nothing more is issued or read
+                if (lane == 0 && p.status) atomicExch(p.status, EDGE0_ETIMEOUT);
+                dead = true;
+                break;
+            }
+            const char* buf = my_ring + stage * X::US * X::STRIP;
+            const int left = n_tok - u * kUnit < kUnit ? (int)(n_tok - u * kUnit) : kUnit;   // valid tokens
+
+            // scores of the unit, in raw units
+            float S[X::US][NT][4];
+#pragma unroll
+            for (int st = 0; st < X::US; ++st) {
+                const char* kb = buf + st * X::STRIP;
+                const uint32_t ka = smem_u32(kb) + row_off;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) S[st][nt][i] = 0.f;
+                if (st * 16 < left) {
+#pragma unroll
+                    for (int gr = 0; gr < X::GR; ++gr) {
+                        float acc[NT][4];
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
+#pragma unroll
+                        for (int cp = 0; cp < X::CPG; cp += 2) {
+                            const int c0 = gr * X::CPG + cp;
+                            uint32_t w[4];
+                            ldsm4(w, ka + (piece ^ (c0 << 4)));
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const uint32_t wa = w[2 * j], wb = w[2 * j + 1];
+                                if (BITS == 4) {
+                                    const uint32_t A0[4] = {wa & 0x000F000Fu, wb & 0x000F000Fu, (wa >> 8) & 0x000F000Fu,
+                                                            (wb >> 8) & 0x000F000Fu};
+                                    const uint32_t A1[4] = {wa & 0x00F000F0u, wb & 0x00F000F0u, (wa >> 8) & 0x00F000F0u,
+                                                            (wb >> 8) & 0x00F000F0u};
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt) {
+                                        const uint4 f = *reinterpret_cast<const uint4*>(
+                                            sq + ((nt * X::CH + c0 + j) * 32 + lane) * 4);
+                                        mma_16816(acc[nt], A0, f.x, f.y);
+                                        mma_16816(acc[nt], A1, f.z, f.w);
+                                    }
+                                } else {
+                                    const uint32_t A0[4] = {wa & 0x00FF00FFu, wb & 0x00FF00FFu, (wa >> 8) & 0x00FF00FFu,
+                                                            (wb >> 8) & 0x00FF00FFu};
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt) {
+                                        const uint2 f = *reinterpret_cast<const uint2*>(
+                                            sq + ((nt * X::CH + c0 + j) * 32 + lane) * 2);
+                                        mma_16816(acc[nt], A0, f.x, f.y);
+                                    }
+                                }
+                            }
+                        }
+                        const char* sbp = kb + 16 * X::R + gr * 4;
+                        const float2 sa = __half22float2(*reinterpret_cast<const __half2*>(sbp + g * X::SB));
+                        const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(sbp + (g + 8) * X::SB));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const float q0 = sqsum[(nt * 8 + 2 * t) * X::GR + gr];
+                            const float q1 = sqsum[(nt * 8 + 2 * t + 1) * X::GR + gr];
+                            S[st][nt][0] = fmaf(sa.x, acc[nt][0], fmaf(sa.y, q0, S[st][nt][0]));
+                            S[st][nt][1] = fmaf(sa.x, acc[nt][1], fmaf(sa.y, q1, S[st][nt][1]));
+                            S[st][nt][2] = fmaf(sb.x, acc[nt][2], fmaf(sb.y, q0, S[st][nt][2]));
+                            S[st][nt][3] = fmaf(sb.x, acc[nt][3], fmaf(sb.y, q1, S[st][nt][3]));
+                        }
+                    }
+                }
+                if (left < st * 16 + 16) {
+                    const bool a = st * 16 + g < left, b = st * 16 + g + 8 < left;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        S[st][nt][0] = a ? S[st][nt][0] : -INFINITY;
+                        S[st][nt][1] = a ? S[st][nt][1] : -INFINITY;
+                        S[st][nt][2] = b ? S[st][nt][2] : -INFINITY;
+                        S[st][nt][3] = b ? S[st][nt][3] : -INFINITY;
+                    }
+                }
+            }
+
+            // the running maximum moves when a score is 2^8 above it
+            bool up = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int st = 0; st < X::US; ++st)
+                    up = up || S[st][nt][0] > thr[nt][0] || S[st][nt][2] > thr[nt][0] || S[st][nt][1] > thr[nt][1] ||
+                         S[st][nt][3] > thr[nt][1];
+            if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float v = m[nt][i];
+#pragma unroll
+                        for (int st = 0; st < X::US; ++st) v = fmaxf(v, fmaxf(S[st][nt][i], S[st][nt][i + 2]));
+                        v = max_over_rows(v);
+                        if (!(v > thr[nt][i])) v = m[nt][i];      // each row by its own scores alone
+                        const float f = m[nt][i] == -INFINITY ? 0.f : ex2((m[nt][i] - v) * p.k);
+                        m[nt][i] = v;
+                        mu[nt][i] = v == -INFINITY ? 0.f : v * p.k;
+                        thr[nt][i] = v + 8.f / p.k;
+                        l[nt][i] *= f;
+#pragma unroll
+                        for (int gr = 0; gr < X::GR; ++gr) beta[nt][gr][i] *= f;
+#pragma unroll
+                        for (int mt = 0; mt < X::MT; ++mt) {
+                            O[mt][nt][i] *= f;
+                            O[mt][nt][i + 2] *= f;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int st = 0; st < X::US; ++st)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        S[st][nt][i] = ex2(fmaf(S[st][nt][i], p.k, -mu[nt][i & 1]));
+                        l[nt][i & 1] += S[st][nt][i];
+                    }
+
+            // V: scales of the unit's tokens g and g + 8, zero where there is no token
+            float2 vs[X::US][X::GR][2];
+            bool grow = false;
+#pragma unroll
+            for (int st = 0; st < X::US; ++st) {
+                const char* sbp = buf + st * X::STRIP + X::HALF + 16 * X::R;
+#pragma unroll
+                for (int gr = 0; gr < X::GR; ++gr)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float2 sb = make_float2(0.f, 0.f);
+                        if (st * 16 + g + 8 * i < left)
+                            sb = __half22float2(
+                                *reinterpret_cast<const __half2*>(sbp + (g + 8 * i) * X::SB + gr * 4));
+                        sb.y = fmaf(sb.x, BITS == 4 ? 8.f : 128.f, sb.y);
+                        vs[st][gr][i] = sb;
+                        grow = grow || sb.x * es[gr] > 1.f;
+                    }
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int gr = 0; gr < X::GR; ++gr) {
+                    float v = 0.f;
+#pragma unroll
+                    for (int st = 0; st < X::US; ++st) v = fmaxf(v, fmaxf(vs[st][gr][0].x, vs[st][gr][1].x));
+                    v = max_over_rows(v);
+                    if (v * es[gr] > 1.f) {
+                        const unsigned be = __float_as_uint(v) >> 23;      // v < 2^(be - 126)
+                        const float e = __uint_as_float((253u - (be < 250u ? be : 250u)) << 23);
+                        const float f = es[gr] == INFINITY ? 0.f : e / es[gr];
+                        es[gr] = e;
+#pragma unroll
+                        for (int mt = 0; mt < X::MT / X::GR; ++mt)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) O[gr * (X::MT / X::GR) + mt][nt][i] *= f;
+                    }
+                }
+            }
+#pragma unroll
+            for (int st = 0; st < X::US; ++st) {
+                if (st * 16 >= left) continue;
+                const uint32_t va = smem_u32(buf + st * X::STRIP + X::HALF) + row_off;
+#pragma unroll
+                for (int gr = 0; gr < X::GR; ++gr) {
+                    uint32_t b0[NT], b1[NT];
+                    const float e = es[gr] == INFINITY ? 0.f : es[gr];
+                    const float w0 = vs[st][gr][0].x * e, w1 = vs[st][gr][1].x * e;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float* P = S[st][nt];
+                        b0[nt] = transpose8(pack2(P[0] * w0, P[1] * w0));
+                        b1[nt] = transpose8(pack2(P[2] * w1, P[3] * w1));
+                        beta[nt][gr][0] = fmaf(P[0], vs[st][gr][0].y, fmaf(P[2], vs[st][gr][1].y, beta[nt][gr][0]));
+                        beta[nt][gr][1] = fmaf(P[1], vs[st][gr][0].y, fmaf(P[3], vs[st][gr][1].y, beta[nt][gr][1]));
+                    }
+#pragma unroll
+                    for (int cp = 0; cp < X::CPG; cp += 2) {
+                        const int c0 = gr * X::CPG + cp;
+                        uint32_t w[4];
+                        ldsm4t(w, va + (piece ^ (c0 << 4)));
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t A[4];
+                            if (BITS == 4) {
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) {
+                                    v_frag<4>(w[2 * j], w[2 * j + 1], q, A);
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt)
+                                        mma_16816(O[2 * (c0 + j) + q][nt], A, b0[nt], b1[nt]);
+                                }
+                            } else {
+                                v_frag<8>(w[2 * j], w[2 * j + 1], 0, A);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) mma_16816(O[c0 + j][nt], A, b0[nt], b1[nt]);
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();    // every lane has read the stage before it is copied into again
+        }
+
+        // join the warps: maximum, then 8 query rows at a time through shared memory
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                l[nt][i] = sum_over_rows(l[nt][i]);
+#pragma unroll
+                for (int gr = 0; gr < X::GR; ++gr) beta[nt][gr][i] = sum_over_rows(beta[nt][gr][i]);
+                if (g == 0) sml[(wid * NT + nt) * 8 + 2 * t + i] = make_float2(m[nt][i], l[nt][i]);
+            }
+        __syncthreads();
+        const bool whole = u0 == 0 && u1 == units;
+        const bool direct = whole && p.out;
+        const int slot = blockIdx.x + sidx;
+        if (u0 == 0 && tid == 0) {
+            const long long first = pos / share, last = (pos + units - 1) / share;
+            p.seg[sidx] = make_int2(slot, (int)(last - first) + 1);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            // this warp's share of columns 2t, 2t + 1
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int col = 2 * t + i;
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[(w * NT + nt) * 8 + col].x);
+                const float f = m[nt][i] == -INFINITY ? (l[nt][i] == 0.f ? 0.f : l[nt][i]) : ex2((m[nt][i] - top) * p.k);
+                float* dst = red + (wid * 8 + col) * X::kRedLd;
+#pragma unroll
+                for (int mt = 0; mt < X::MT; ++mt) {
+                    const int gr = mt / (X::MT / X::GR);
+                    const float inv = 1.f / es[gr];
+                    const float2 v = make_float2(fmaf(O[mt][nt][i], inv, beta[nt][gr][i]) * f,
+                                                 fmaf(O[mt][nt][i + 2], inv, beta[nt][gr][i]) * f);
+                    *reinterpret_cast<float2*>(dst + dim_of<BITS>(mt, g)) = v;
+                }
+            }
+            __syncthreads();
+            for (int i = tid; i < 8 * D / 4; i += 32 * kWarps) {
+                const int col = i / (D / 4), d = (i % (D / 4)) * 4;
+                const int r = r0 + nt * 8 + col;
+                if (r >= p.rows) continue;
+                float top = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[(w * NT + nt) * 8 + col].x);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 ml = sml[(w * NT + nt) * 8 + col];
+                    sum += ml.x == -INFINITY ? ml.y : ml.y * ex2((ml.x - top) * p.k);
+                }
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float4 a = *reinterpret_cast<const float4*>(red + (w * 8 + col) * X::kRedLd + d);
+                    v.x += a.x;
+                    v.y += a.y;
+                    v.z += a.z;
+                    v.w += a.w;
+                }
+                if (direct) {
+                    const float inv = 1.f / sum;
+                    const uint2 o = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
+                    *reinterpret_cast<uint2*>(p.out + (long long)(seq * p.q_step + r / p.G) * p.ldo +
+                                              (long long)(h * p.G + r % p.G) * D + d) = o;
+                } else {
+                    const long long row = (long long)slot * (8 * NT) + nt * 8 + col;
+                    *reinterpret_cast<float4*>(p.part_o + row * D + d) = v;
+                    if (d == 0) p.part_ml[row] = make_float2(top == -INFINITY ? top : top * p.k, sum);
+                }
+            }
+            __syncthreads();
+        }
+        pos += u1 - u0;
     }
+}
+
+struct JoinP {
+    int B, G, H, D;
+    const int* lens;
+    int n_prefix;
+    // own parts and the prefix's parts
+    int RB[2], rows[2];      // row blocks per head, rows per block
+    const float* part_o[2];
+    const float2* part_ml[2];
+    const int2* seg[2];
+    __half* out;
+    long long ldo;
+};
+
+// One warp per (sequence, query head): its own parts and the prefix's, in order.
+template <int D>
+__global__ void __launch_bounds__(128) attn_join_kernel(const JoinP p) {
+    constexpr int kN = D / 32;
+    const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (row >= p.B * p.G * p.H) return;
+    const int b = row / (p.G * p.H), hq = row - b * p.G * p.H, h = hq / p.G, j = hq - h * p.G;
+    const int len = p.lens[b];
+    if (len < 0) return;
+    __half* out = p.out + (long long)b * p.ldo + (long long)hq * D;
+    const float* o[2];
+    const float2* ml[2];
+    int n[2];
+    long long step[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        n[i] = 0;
+        o[i] = nullptr;
+        ml[i] = nullptr;
+        step[i] = 0;
+        if (i == 0 ? p.n_prefix == 0 : len == 0) continue;
+        const int w = i == 0 ? 1 : 0;     // the prefix first
+        const int r = w ? b * p.G + j : j;
+        const int2 sg = p.seg[w][((w ? 0 : b) * p.H + h) * p.RB[w] + r / p.rows[w]];
+        n[i] = sg.y;
+        const long long at = (long long)sg.x * p.rows[w] + r % p.rows[w];
+        o[i] = p.part_o[w] + at * D;
+        ml[i] = p.part_ml[w] + at;
+        step[i] = p.rows[w];
+    }
+    if (p.n_prefix == 0 && n[1] == 1) return;       // written by the CTA that had it whole
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        for (int s = lane; s < n[i]; s += 32) top = fmaxf(top, ml[i][s * step[i]].x);
+#pragma unroll
+    for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    float sum = 0.f, v[kN];
+#pragma unroll
+    for (int e = 0; e < kN; ++e) v[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        for (int s = 0; s < n[i]; ++s) {
+            const float2 x = ml[i][s * step[i]];
+            const float f = x.x == -INFINITY ? 1.f : ex2(x.x - top);
+            sum = fmaf(x.y, f, sum);
+            const float* src = o[i] + s * step[i] * D + lane * kN;
+#pragma unroll
+            for (int e = 0; e < kN; ++e) v[e] = fmaf(src[e], f, v[e]);
+        }
+    const float inv = n[0] + n[1] ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int e = 0; e < kN; e += 2)
+        *reinterpret_cast<uint32_t*>(out + lane * kN + e) = pack2(v[e] * inv, v[e + 1] * inv);
+}
+
+// Query rows that a CTA of one segment takes, 8 NT: the whole group of one sequence
+// where it fits 16; of the prefix's rows as many as registers hold (32, or 16 of
+// 256-wide heads), fewer when there are fewer.
+int nt_of(int rows, int D, bool prefix) {
+    if (rows <= 8) return 1;
+    return rows <= 16 || D == 256 || !prefix ? 2 : 4;
+}
+
+struct Part {
+    int NT, RB, segs;
+    long long slots, o, ml, seg;      // workspace offsets
+};
+
+// workspace: own parts then the prefix's; returns its size
+long long layout(int B, int G, int H, int D, Part (&part)[2]) {
+    long long at = 0;
+    for (int w = 0; w < 2; ++w) {
+        Part& x = part[w];
+        const int rows = w ? B * G : G;
+        x.NT = nt_of(rows, D, w == 1);
+        x.RB = ceil_div(rows, 8 * x.NT);
+        x.segs = (w ? 1 : B) * H * x.RB;
+        x.slots = (long long)kMaxGrid + x.segs;
+        x.o = at;
+        at += x.slots * 8 * x.NT * D * 4;
+        x.ml = at;
+        at += x.slots * 8 * x.NT * 8;
+        x.seg = at;
+        at += ((long long)x.segs * 8 + 15) / 16 * 16;
+    }
+    return at;
+}
+
+template <int BITS, int D, int NT>
+int launch(const AttnP& p, long long most_units, cudaStream_t stream) {
+    using X = Cfg<BITS, D, NT>;
+    constexpr int kDevices = 64;
+    static int ctas[kDevices];           // per device: CTAs that fill it, set on the first call
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return EDGE0_ECUDA;
+    int n = __atomic_load_n(&ctas[dev], __ATOMIC_ACQUIRE);
+    if (n == 0) {
+        int sms = 0, occ = 0;
+        if (cudaFuncSetAttribute(attn_kernel<BITS, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, X::kSmem) !=
+                cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, attn_kernel<BITS, D, NT>, 32 * kWarps, X::kSmem) !=
+                cudaSuccess ||
+            occ < 1)
+            return EDGE0_ECUDA;
+        n = sms * occ < kMaxGrid ? sms * occ : kMaxGrid;
+        __atomic_store_n(&ctas[dev], n, __ATOMIC_RELEASE);
+    }
+    const long long want = (most_units + kMinShare - 1) / kMinShare;
+    const int grid = want < n ? (int)(want < 1 ? 1 : want) : n;
+    attn_kernel<BITS, D, NT><<<grid, 32 * kWarps, X::kSmem, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? EDGE0_OK : EDGE0_ECUDA;
+}
+
+template <int BITS, int D>
+int launch_nt(const AttnP& p, int NT, cudaStream_t stream) {
+    constexpr int kUnit = 16 * Cfg<BITS, D, 1>::US;
+    const long long cap = p.lens ? (long long)p.W * p.c.page_tokens : p.n_tok;
+    const long long most = (cap + kUnit - 1) / kUnit * p.n_seq * p.H * p.RB;
+    if (NT == 1) return launch<BITS, D, 1>(p, most, stream);
+    if (NT == 2) return launch<BITS, D, 2>(p, most, stream);
+    if constexpr (D <= 128) return launch<BITS, D, 4>(p, most, stream);
+    return EDGE0_EUNSUPPORTED;
+}
+
+int launch_any(const AttnP& p, int bits, int D, int NT, cudaStream_t stream) {
+    if (bits == 4) {
+        if (D == 64) return launch_nt<4, 64>(p, NT, stream);
+        if (D == 128) return launch_nt<4, 128>(p, NT, stream);
+        return launch_nt<4, 256>(p, NT, stream);
+    }
+    if (D == 64) return launch_nt<8, 64>(p, NT, stream);
+    if (D == 128) return launch_nt<8, 128>(p, NT, stream);
+    return launch_nt<8, 256>(p, NT, stream);
 }
 
 }  // namespace
@@ -105,7 +790,8 @@ extern "C" size_t edge0_attn_workspace_bytes(const edge0_kv_cache* cache, int B,
     kv::View c;
     if (kv::view_of(cache, &c) || B <= 0 || B > EDGE0_MAX_BATCHED) return 0;
     if (n_q_heads <= 0 || n_q_heads % c.H || n_q_heads / c.H > EDGE0_MAX_Q_PER_KV) return 0;
-    return 256;
+    Part part[2];
+    return (size_t)layout(B, n_q_heads / c.H, c.H, cache->head_dim, part);
 }
 
 extern "C" int edge0_attn_decode(const edge0_kv_cache* cache, const uint16_t* q, long long ldq, int B, int n_q_heads,
@@ -120,34 +806,57 @@ extern "C" int edge0_attn_decode(const edge0_kv_cache* cache, const uint16_t* q,
     if (n_q_heads / p.c.H > EDGE0_MAX_Q_PER_KV) return EDGE0_EUNSUPPORTED;
     if (n_prefix < 0 || (n_prefix > 0 && !prefix)) return EDGE0_EINVAL;
     if (!(scale > 0.f) || !(scale <= 1e6f)) return EDGE0_EINVAL;
-    const long long width = (long long)n_q_heads * cache->head_dim;
+    const int D = cache->head_dim;
+    const long long width = (long long)n_q_heads * D;
     if (ldq < width || ldq % 8 || ldo < width || ldo % 8) return EDGE0_EINVAL;
     if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) & 15) return EDGE0_EINVAL;
     if (((uintptr_t)table | (uintptr_t)lens | (uintptr_t)prefix | (uintptr_t)status) & 3) return EDGE0_EINVAL;
-    if (workspace_bytes < edge0_attn_workspace_bytes(cache, B, n_q_heads)) return EDGE0_EINVAL;
+    Part part[2];
+    p.H = p.c.H;
+    p.G = n_q_heads / p.H;
+    if ((long long)workspace_bytes < layout(B, p.G, p.H, D, part)) return EDGE0_EINVAL;
+    char* ws = (char*)workspace;
     p.q = (const __half*)q;
     p.ldq = ldq;
-    p.B = B;
-    p.Hq = n_q_heads;
-    p.table = table;
-    p.W = W;
-    p.lens = lens;
-    p.prefix = prefix;
-    p.n_prefix = n_prefix;
-    p.scale = scale;
-    p.out = (__half*)out;
+    p.k = kTwo24 * scale * 1.4426950408889634f;
     p.ldo = ldo;
     p.status = status;
-    const dim3 grid(B, n_q_heads);
-    const int D = cache->head_dim;
-    if (cache->bits == 4) {
-        if (D == 64) attn_kernel<4, 64><<<grid, 32 * kAttnWarps, 0, stream>>>(p);
-        else if (D == 128) attn_kernel<4, 128><<<grid, 32 * kAttnWarps, 0, stream>>>(p);
-        else attn_kernel<4, 256><<<grid, 32 * kAttnWarps, 0, stream>>>(p);
-    } else {
-        if (D == 64) attn_kernel<8, 64><<<grid, 32 * kAttnWarps, 0, stream>>>(p);
-        else if (D == 128) attn_kernel<8, 128><<<grid, 32 * kAttnWarps, 0, stream>>>(p);
-        else attn_kernel<8, 256><<<grid, 32 * kAttnWarps, 0, stream>>>(p);
+    for (int w = 1; w >= 0; --w) {
+        if (w && !n_prefix) continue;
+        p.n_seq = w ? 1 : B;
+        p.rows = w ? B * p.G : p.G;
+        p.RB = part[w].RB;
+        p.q_step = w ? 0 : 1;
+        p.pages = w ? prefix : table;
+        p.W = w ? ceil_div(n_prefix, p.c.page_tokens) : W;
+        p.lens = w ? nullptr : lens;
+        p.n_tok = n_prefix;
+        p.part_o = (float*)(ws + part[w].o);
+        p.part_ml = (float2*)(ws + part[w].ml);
+        p.seg = (int2*)(ws + part[w].seg);
+        p.out = !w && !n_prefix ? (__half*)out : nullptr;
+        rc = launch_any(p, cache->bits, D, part[w].NT, stream);
+        if (rc) return rc;
     }
+    JoinP j;
+    j.B = B;
+    j.G = p.G;
+    j.H = p.H;
+    j.D = D;
+    j.lens = lens;
+    j.n_prefix = n_prefix;
+    for (int w = 0; w < 2; ++w) {
+        j.RB[w] = part[w].RB;
+        j.rows[w] = 8 * part[w].NT;
+        j.part_o[w] = (const float*)(ws + part[w].o);
+        j.part_ml[w] = (const float2*)(ws + part[w].ml);
+        j.seg[w] = (const int2*)(ws + part[w].seg);
+    }
+    j.out = (__half*)out;
+    j.ldo = ldo;
+    const int grid = ceil_div(B * n_q_heads, 4);
+    if (D == 64) attn_join_kernel<64><<<grid, 128, 0, stream>>>(j);
+    else if (D == 128) attn_join_kernel<128><<<grid, 128, 0, stream>>>(j);
+    else attn_join_kernel<256><<<grid, 128, 0, stream>>>(j);
     return cudaGetLastError() == cudaSuccess ? EDGE0_OK : EDGE0_ECUDA;
 }
