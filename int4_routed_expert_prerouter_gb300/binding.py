@@ -584,54 +584,70 @@ def lora_delta(desc: LoraDesc, v, y, stream=None):
 
 
 # ------------------------------- projections, KV cache, decode attention ----
-def _need(cond, what):
-    if not cond:
-        raise Edge0Error(EDGE0_EINVAL, what)
+# These are called once or more per layer and token, so their checks go straight
+# through: plain comparisons, messages formatted only when they are raised.
+def _bad(what):
+    return Edge0Error(EDGE0_EINVAL, what)
 
 
-def _on(t, stream):
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on(index, stream):
     """Allocations and launches of one call: the tensors' device, the call's stream."""
-    es = contextlib.ExitStack()
-    es.enter_context(torch.cuda.device(t.device))
     if stream is not None:
-        es.enter_context(torch.cuda.stream(stream))
-    return es
+        return torch.cuda.stream(stream)      # its device too
+    return _SAME_DEVICE if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
-def _need_rows(t, what, *shape):
-    """t: fp16 rows of the given trailing shape on a GPU, dense within a row, rows a
-    multiple of 16 bytes apart (a slice of a wider row-major tensor passes)."""
-    _need(t.is_cuda and t.dtype == torch.float16 and t.dim() == 1 + len(shape), f"{what}: fp16 rows on a GPU")
-    _need(tuple(t.shape[1:]) == shape, f"{what}: rows of shape {shape}, not {tuple(t.shape[1:])}")
-    dense = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        _need(stride == dense or size == 1, f"{what}: rows are not dense")
-        dense *= size
-    return dense if t.shape[0] <= 1 else t.stride(0)
+def _raw_stream(index, stream):
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
 
 
-def _need_i32(t, dev, what, *shape):
-    _need(t.dtype == torch.int32 and t.is_contiguous() and t.device == dev and tuple(t.shape) == shape,
-          f"{what}: int32 {list(shape)}, contiguous, on {dev}")
-    return _ptr(t)
+def _row_stride(t, what):
+    """Row stride of fp16 rows [T, n] or [T, heads, n] on a GPU that are dense within a row
+    (a slice of a wider row-major tensor passes)."""
+    if t.dtype is not torch.float16 or not t.is_cuda:
+        raise _bad(f"{what}: fp16 on a GPU")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        dense, row = stride[1] == 1 or shape[1] == 1, shape[1]
+    else:
+        row = shape[1] * shape[2]
+        dense = (stride[2] == 1 or shape[2] == 1) and (stride[1] == shape[2] or shape[1] == 1)
+    if not dense:
+        raise _bad(f"{what}: rows that are not dense")
+    # the row stride of one row or none says nothing; the row's own length rounded up does
+    return stride[0] if shape[0] > 1 else (row + 7) // 8 * 8
+
+
+def _i32(t, index, n, what):
+    if t.dtype is not torch.int32 or t.get_device() != index or t.numel() != n or not t.is_contiguous():
+        raise _bad(f"{what}: {n} int32, contiguous, on cuda:{index}")
+    return t.data_ptr()
 
 
 def q4_linear(packed: torch.Tensor, out_features: int, x: torch.Tensor, y=None, stream=None) -> torch.Tensor:
     """y [B, out_features] = W x for x [B, in] fp16 and W packed by pack_q4_rows (one
     matrix: E = 1).  x and y may be slices of wider rows."""
-    _need(x.dim() == 2 and packed.device == x.device and packed.dtype == torch.uint8, "q4_linear: x [B, in], packed")
+    if x.dim() != 2:
+        raise _bad("q4_linear: x [B, in]")
     B, n_in = x.shape
-    ldx = _need_rows(x, "q4_linear: x", n_in)
-    _need(packed.is_contiguous() and packed.numel() == lib().edge0_q4_down_packed_bytes(1, out_features, n_in) > 0,
-          "q4_linear: packed is not a [out_features, in] matrix")
-    with _on(x, stream):
+    ldx = _row_stride(x, "q4_linear: x")
+    index = x.get_device()
+    if (packed.dtype is not torch.uint8 or packed.get_device() != index or not packed.is_contiguous() or n_in % 64
+            or packed.numel() != (out_features + 15) // 16 * (n_in // 64) * 576 or out_features <= 0 or n_in == 0):
+        raise _bad("q4_linear: packed is not an [out_features, in] matrix beside x")
+    with _on(index, stream):
         if y is None:
-            y = torch.empty(B, out_features, dtype=torch.float16, device=x.device)
-        _need(y.device == x.device and y.shape[0] == B, "q4_linear: y")
-        ldy = _need_rows(y, "q4_linear: y", out_features)
+            y, ldy = torch.empty((B, out_features), dtype=torch.float16, device=x.device), out_features
+        else:
+            if y.shape != (B, out_features) or y.get_device() != index:
+                raise _bad("q4_linear: y [B, out_features] beside x")
+            ldy = max(_row_stride(y, "q4_linear: y"), out_features)
         if B:
-            _check(lib().edge0_q4_linear(_ptr(packed), out_features, n_in, _ptr(x), ldx, B, _ptr(y), ldy,
-                                         _stream(stream)), "edge0_q4_linear")
+            _check(lib().edge0_q4_linear(packed.data_ptr(), out_features, n_in, x.data_ptr(), ldx, B, y.data_ptr(), ldy,
+                                         _raw_stream(index, stream)), "edge0_q4_linear")
     return y
 
 
@@ -647,67 +663,83 @@ class KVCache:
         if self.page_bytes == 0:
             raise Edge0Error(EDGE0_EUNSUPPORTED, f"KVCache: bits {bits}, {n_kv_heads} heads of {head_dim}, "
                                                  f"{page_tokens} tokens per page")
-        _need(n_pages > 0, "KVCache: n_pages")
+        if n_pages <= 0:
+            raise _bad("KVCache: n_pages")
         if pages is None:
             pages = torch.zeros(n_pages, self.page_bytes, dtype=torch.uint8, device=device)
-        _need(pages.is_cuda and pages.dtype == torch.uint8 and pages.is_contiguous()
-              and pages.numel() == n_pages * self.page_bytes, "KVCache: pages uint8 [n_pages, page bytes] on a GPU")
+        if (not pages.is_cuda or pages.dtype is not torch.uint8 or not pages.is_contiguous()
+                or pages.numel() != n_pages * self.page_bytes):
+            raise _bad("KVCache: pages uint8 [n_pages, page bytes] on a GPU")
         self.pages = pages
         self.device = pages.device
         self.status = torch.zeros(1, dtype=torch.int32, device=pages.device)
         self.desc = KvCacheDesc(bits, n_kv_heads, head_dim, page_tokens, n_pages, _ptr(pages))
+        self._index, self._desc, self._status = pages.get_device(), C.byref(self.desc), self.status.data_ptr()
+        self._ws_bytes = {}
 
     def error(self) -> int:
         """What the calls on this cache have recorded since the last error() (waits
-        for the device): EDGE0_OK or EDGE0_EINVAL for a page or position out of range."""
+        for the device): EDGE0_OK, EDGE0_EINVAL for a page or position out of range,
+        EDGE0_ETIMEOUT for a copy that did not arrive."""
         torch.cuda.synchronize(self.device)
         code = int(self.status.item())
         self.status.zero_()
+        torch.cuda.synchronize(self.device)
         return code
 
 
-def _need_sequences(cache, table, start, cu_rows, T, what):
-    _need(table.dim() == 2, f"{what}: table [B, W]")
+def _sequences(cache, table, start, cu_rows, T, what):
+    if table.dim() != 2:
+        raise _bad(f"{what}: table [B, W]")
     B, W = table.shape
-    args = (_need_i32(table, cache.device, f"{what}: table", B, W), B, W,
-            _need_i32(start, cache.device, f"{what}: start", B),
-            None if cu_rows is None else _need_i32(cu_rows, cache.device, f"{what}: cu_rows", B + 1))
-    _need(cu_rows is not None or T == B, f"{what}: one row per sequence without cu_rows")
-    return args
+    index = cache._index
+    if cu_rows is None and T != B:
+        raise _bad(f"{what}: one row per sequence without cu_rows")
+    return (_i32(table, index, B * W, "table"), B, W, _i32(start, index, B, "start"),
+            None if cu_rows is None else _i32(cu_rows, index, B + 1, "cu_rows"))
 
 
 def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table, start, cu_rows=None, stream=None):
     """Quantise rows k, v [T, n_kv_heads, head_dim] fp16 into the pages: row r of
     sequence b goes to position start[b] + r - cu_rows[b] (cu_rows None: row b is
     sequence b's).  table [B, W], start [B], cu_rows [B + 1]: int32 on the device."""
-    T, shape = k.shape[0], (cache.n_kv_heads, cache.head_dim)
-    _need(k.device == cache.device and v.device == cache.device and v.shape[0] == T, "kv_append: k and v")
-    ldk, ldv = _need_rows(k, "kv_append: k", *shape), _need_rows(v, "kv_append: v", *shape)
-    tb, B, W, st, cu = _need_sequences(cache, table, start, cu_rows, T, "kv_append")
-    with _on(k, stream):
-        _check(lib().edge0_kv_append(C.byref(cache.desc), _ptr(k), ldk, _ptr(v), ldv, T, tb, B, W, st, cu,
-                                     _ptr(cache.status), _stream(stream)), "edge0_kv_append")
+    T, index = k.shape[0], cache._index
+    shape = (T, cache.n_kv_heads, cache.head_dim)
+    if k.shape != shape or v.shape != shape or k.get_device() != index or v.get_device() != index:
+        raise _bad(f"kv_append: k and v {list(shape)} beside the cache")
+    ldk, ldv = _row_stride(k, "kv_append: k"), _row_stride(v, "kv_append: v")
+    tb, B, W, st, cu = _sequences(cache, table, start, cu_rows, T, "kv_append")
+    with _on(index, stream):
+        _check(lib().edge0_kv_append(cache._desc, k.data_ptr(), ldk, v.data_ptr(), ldv, T, tb, B, W, st, cu,
+                                     cache._status, _raw_stream(index, stream)), "edge0_kv_append")
 
 
 def kv_read(cache: KVCache, table, start, cu_rows=None, T=None, k=None, v=None, stream=None):
     """(k, v) [T, n_kv_heads, head_dim] fp16: the values that the rows' pages stand for
     (rows as in kv_append).  k, v: contiguous outputs to fill, or None for new ones; rows
     that no sequence has are left as they are."""
-    T = table.shape[0] if T is None else int(T)
-    tb, B, W, st, cu = _need_sequences(cache, table, start, cu_rows, T, "kv_read")
-    shape = (T, cache.n_kv_heads, cache.head_dim)
-    with _on(cache.pages, stream):
-        k, v = (torch.empty(shape, dtype=torch.float16, device=cache.device) if o is None else o for o in (k, v))
-        for o in (k, v):
-            _need(o.device == cache.device and o.dtype == torch.float16 and tuple(o.shape) == shape
-                  and o.is_contiguous(), f"kv_read: outputs fp16 {list(shape)}, contiguous")
-        _check(lib().edge0_kv_read(C.byref(cache.desc), tb, B, W, st, cu, T, _ptr(k), _ptr(v), _ptr(cache.status),
-                                   _stream(stream)), "edge0_kv_read")
+    T = table.shape[0] if T is None else T
+    tb, B, W, st, cu = _sequences(cache, table, start, cu_rows, T, "kv_read")
+    index, shape = cache._index, (T, cache.n_kv_heads, cache.head_dim)
+    with _on(index, stream):
+        if k is None and v is None:
+            k = torch.empty(shape, dtype=torch.float16, device=cache.device)
+            v = torch.empty(shape, dtype=torch.float16, device=cache.device)
+        else:
+            k, v = (torch.empty(shape, dtype=torch.float16, device=cache.device) if o is None else o for o in (k, v))
+            for o in (k, v):
+                if o.dtype is not torch.float16 or o.shape != shape or o.get_device() != index or not o.is_contiguous():
+                    raise _bad(f"kv_read: outputs fp16 {list(shape)}, contiguous, beside the cache")
+        _check(lib().edge0_kv_read(cache._desc, tb, B, W, st, cu, T, k.data_ptr(), v.data_ptr(), cache._status,
+                                   _raw_stream(index, stream)), "edge0_kv_read")
     return k, v
 
 
 def attn_workspace_bytes(cache: KVCache, B: int, n_q_heads: int) -> int:
-    return int(lib().edge0_attn_workspace_bytes(C.byref(cache.desc), B, n_q_heads))
+    n = cache._ws_bytes.get((B, n_q_heads))
+    if n is None:
+        n = cache._ws_bytes[B, n_q_heads] = int(lib().edge0_attn_workspace_bytes(cache._desc, B, n_q_heads))
+    return n
 
 
 def attn_decode(cache: KVCache, q: torch.Tensor, table, lens, prefix=None, n_prefix=0, scale=None, out=None,
@@ -718,33 +750,34 @@ def attn_decode(cache: KVCache, q: torch.Tensor, table, lens, prefix=None, n_pre
     unless given.  out: rows to fill (those of sequences with lens[b] < 0 are left as
     they are) or None.  workspace: uint8 of attn_workspace_bytes, or None for one of the
     call's own."""
-    _need(q.dim() == 3 and q.device == cache.device, "attn_decode: q [B, n_q_heads, head_dim]")
+    index = cache._index
+    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.get_device() != index:
+        raise _bad("attn_decode: q [B, n_q_heads, head_dim] beside the cache")
     B, Hq, D = q.shape
-    ldq = _need_rows(q, "attn_decode: q", Hq, cache.head_dim)
-    _need(table.dim() == 2 and table.shape[0] == B, "attn_decode: table [B, W]")
+    ldq = _row_stride(q, "attn_decode: q")
+    if table.dim() != 2 or table.shape[0] != B:
+        raise _bad("attn_decode: table [B, W]")
     W = table.shape[1]
-    tb = _need_i32(table, cache.device, "attn_decode: table", B, W)
-    ln = _need_i32(lens, cache.device, "attn_decode: lens", B)
-    n_prefix = int(n_prefix)
-    _need(n_prefix >= 0, "attn_decode: n_prefix")
+    tb, ln = _i32(table, index, B * W, "attn_decode: table"), _i32(lens, index, B, "attn_decode: lens")
+    pf = None
     if n_prefix:
-        _need(prefix is not None and prefix.dim() == 1 and prefix.numel() * cache.page_tokens >= n_prefix,
-              "attn_decode: prefix pages")
-        pf = _need_i32(prefix, cache.device, "attn_decode: prefix", prefix.numel())
-    else:
-        pf = None
-    scale = cache.head_dim ** -0.5 if scale is None else float(scale)
+        if n_prefix < 0 or prefix is None or prefix.numel() * cache.page_tokens < n_prefix:
+            raise _bad("attn_decode: n_prefix tokens in the pages `prefix`")
+        pf = _i32(prefix, index, prefix.numel(), "attn_decode: prefix")
     nbytes = attn_workspace_bytes(cache, B, Hq)
-    with _on(q, stream):
+    with _on(index, stream):
         if out is None:
-            out = torch.empty(B, Hq, D, dtype=torch.float16, device=q.device)
-        _need(out.device == q.device and out.shape[0] == B, "attn_decode: out")
-        ldo = _need_rows(out, "attn_decode: out", Hq, cache.head_dim)
+            out, ldo = torch.empty((B, Hq, D), dtype=torch.float16, device=cache.device), Hq * D
+        else:
+            if out.shape != q.shape or out.get_device() != index:
+                raise _bad("attn_decode: out like q")
+            ldo = _row_stride(out, "attn_decode: out")
         if workspace is None:
-            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
-        _need(workspace.device == q.device and workspace.dtype == torch.uint8 and workspace.is_contiguous(),
-              "attn_decode: workspace")
-        _check(lib().edge0_attn_decode(C.byref(cache.desc), _ptr(q), ldq, B, Hq, tb, W, ln, pf, n_prefix, scale,
-                                       _ptr(out), ldo, _ptr(cache.status), _ptr(workspace), workspace.numel(),
-                                       _stream(stream)), "edge0_attn_decode")
+            workspace = torch.empty(nbytes or 16, dtype=torch.uint8, device=cache.device)
+        elif workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
+            raise _bad("attn_decode: workspace uint8, contiguous, beside the cache")
+        _check(lib().edge0_attn_decode(cache._desc, q.data_ptr(), ldq, B, Hq, tb, W, ln, pf, n_prefix,
+                                       D ** -0.5 if scale is None else scale, out.data_ptr(), ldo, cache._status,
+                                       workspace.data_ptr(), workspace.numel(), _raw_stream(index, stream)),
+               "edge0_attn_decode")
     return out

@@ -33,6 +33,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kMaxGrid = 152 * 8;
 constexpr int kMinShare = 2 * kWarps;   // units a CTA takes at least
+constexpr int kSegCost = 6;             // what starting and joining a segment costs, in units
 
 struct AttnP {
     kv::View c;
@@ -69,13 +70,14 @@ struct Cfg {
     static constexpr int STAGES = STRIP * US >= 8000 ? 2 : STRIP * US >= 4300 ? (US == 2 ? 2 : 3) : 4;
     static constexpr int MT = D / 16;
     // shared memory
-    static constexpr int kRing = kWarps * STAGES * US * STRIP;
+    static constexpr int kRingBytes = kWarps * STAGES * US * STRIP;
     static constexpr int kQ = NT * CH * 32 * QW * 4;
     static constexpr int kQsum = NT * 8 * GR * 4;
     static constexpr int kRedLd = D + 4;
-    static constexpr int kRed = kWarps * 8 * kRedLd * 4;
+    static constexpr int kRed = kWarps * 8 * kRedLd * 4;   // the ring's memory, once a segment's copies are used up
     static constexpr int kMl = kWarps * NT * 8 * 8;
-    static constexpr int kSmem = kRing + kQ + kQsum + kRed + kMl + kWarps * STAGES * 8 + 257 * 8 + 64;
+    static constexpr int kRing = kRingBytes > kRed ? kRingBytes : kRed;
+    static constexpr int kSmem = kRing + kQ + kQsum + kMl + kWarps * STAGES * 8 + 257 * 8 + 256 * 4;
     static constexpr int kMinCtas = NT == 1 && D <= 128 ? 4 : NT == 4 ? 2 : D == 256 && NT == 2 ? 2 : 3;
 };
 
@@ -181,35 +183,40 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
     char* ring = smem;
     uint32_t* sq = reinterpret_cast<uint32_t*>(ring + X::kRing);
     float* sqsum = reinterpret_cast<float*>(reinterpret_cast<char*>(sq) + X::kQ);
-    float* red = reinterpret_cast<float*>(reinterpret_cast<char*>(sqsum) + X::kQsum);
-    float2* sml = reinterpret_cast<float2*>(reinterpret_cast<char*>(red) + X::kRed);
+    float* red = reinterpret_cast<float*>(ring);
+    float2* sml = reinterpret_cast<float2*>(reinterpret_cast<char*>(sqsum) + X::kQsum);
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(sml) + X::kMl);
     long long* cum = reinterpret_cast<long long*>(bars + kWarps * X::STAGES);
+    int* tokens = reinterpret_cast<int*>(cum + 257);
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
     constexpr int kUnit = 16 * X::US;
 
-    // units before each list: a scan over at most 256 lengths
+    // cost before each list: a scan over at most 256 lengths
     const int per_list = p.H * p.RB;
-    const long long cap = (long long)p.W * p.c.page_tokens;
-    auto tokens_of = [&](int i) -> long long {
-        const long long n = p.lens ? (long long)p.lens[i] : (long long)p.n_tok;
-        return n < 0 ? 0 : n > cap ? cap : n;
-    };
     if (wid == 0) {
+        const long long cap = (long long)p.W * p.c.page_tokens;
         long long base = 0;
         for (int i0 = 0; i0 < p.n_seq; i0 += 32) {
             const int i = i0 + lane;
-            long long n = i < p.n_seq ? (tokens_of(i) + kUnit - 1) / kUnit * per_list : 0;
-            if (i < p.n_seq && p.lens && p.lens[i] > cap && blockIdx.x == 0 && p.status)
-                atomicExch(p.status, EDGE0_EINVAL);
-            const long long mine = n;
+            int n = 0;
+            if (i < p.n_seq) {
+                n = p.lens ? p.lens[i] : p.n_tok;
+                if (n > cap) {
+                    n = (int)cap;
+                    if (blockIdx.x == 0 && p.status) atomicExch(p.status, EDGE0_EINVAL);
+                }
+                n = n < 0 ? 0 : n;
+                tokens[i] = n;
+            }
+            const long long mine = n ? (long long)((n - 1) / kUnit + 1 + kSegCost) * per_list : 0;
+            long long upto = mine;
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
-                const long long o = __shfl_up_sync(0xffffffffu, n, s);
-                if (lane >= s) n += o;
+                const long long o = __shfl_up_sync(0xffffffffu, upto, s);
+                if (lane >= s) upto += o;
             }
-            if (i < p.n_seq) cum[i] = base + n - mine;
-            base += __shfl_sync(0xffffffffu, n, 31);
+            if (i < p.n_seq) cum[i] = base + upto - mine;
+            base += __shfl_sync(0xffffffffu, upto, 31);
         }
         if (lane == 0) cum[p.n_seq] = base;
     }
@@ -218,7 +225,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
     __syncthreads();
     const long long total = cum[p.n_seq];
     long long share = (total + gridDim.x - 1) / gridDim.x;
-    if (share < kMinShare) share = kMinShare;
+    if (share < kMinShare + kSegCost) share = kMinShare + kSegCost;
     long long pos = share * blockIdx.x;
     const long long end = pos + share < total ? pos + share : total;
 
@@ -241,25 +248,29 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
         }
         // lists without tokens share their successor's start: the search ends at the last one
         const int seq = lo;
-        const long long n_tok = tokens_of(seq);
-        const long long units = (n_tok + kUnit - 1) / kUnit;
+        const int n_tok = tokens[seq];
+        const int units = (n_tok - 1) / kUnit + 1, cost = units + kSegCost;
         const long long in_list = pos - cum[seq];
-        const int hr = (int)(in_list / units);
-        const long long u0 = in_list - hr * units;
+        const int hr = in_list < 0x7fffffff ? (int)in_list / cost : (int)(in_list / cost);
+        const long long seg_at = cum[seq] + (long long)hr * cost;
+        const long long first_unit = seg_at + kSegCost;          // where its unit 0 lies
+        const int u0 = pos > first_unit ? (int)(pos - first_unit) : 0;
+        const int u1 = end - first_unit < units ? (int)(end - first_unit) : units;
+        pos = seg_at + cost;
+        if (u1 <= u0) continue;                                  // the share ends before its first unit
         const int h = hr / p.RB, rb = hr - h * p.RB;
-        const long long u1 = u0 + (end - pos) < units ? u0 + (end - pos) : units;
         const int sidx = (seq * p.H + h) * p.RB + rb;
         const int* pages = p.pages + (long long)seq * p.W;
         const int spp = p.c.page_tokens / kv::kStrip;
 
-        auto issue = [&](long long u, int stage) {   // whole warp
-            const long long s0 = u * X::US;
-            const long long left = (n_tok + 15) / 16 - s0;
-            const int n = left < X::US ? (int)left : X::US;
+        auto issue = [&](int u, int stage) {   // whole warp
+            const int s0 = u * X::US;
+            const int left = (n_tok - 1) / 16 + 1 - s0;
+            const int n = left < X::US ? left : X::US;
             if (lane == 0) mbar_arrive_expect_tx(&my_bar[stage], n * X::STRIP);
             __syncwarp();
             if (lane < n) {
-                const long long st = s0 + lane, pg = st / spp;
+                const int st = s0 + lane, pg = st / spp;
                 int id = pages[pg];
                 if (id < 0 || id >= p.c.n_pages) {
                     id = 0;
@@ -270,7 +281,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
             }
             __syncwarp();
         };
-        long long ahead = dead ? u1 : u0 + wid;
+        int ahead = dead ? u1 : u0 + wid;
         int issued = it;
 #pragma unroll 1
         for (int s = 0; s < X::STAGES - 1; ++s, ahead += kWarps)
@@ -337,7 +348,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
         for (int gr = 0; gr < X::GR; ++gr) es[gr] = INFINITY;
 
 #pragma unroll 1
-        for (long long u = dead ? u1 : u0 + wid; u < u1; u += kWarps, ++it) {
+        for (int u = dead ? u1 : u0 + wid; u < u1; u += kWarps, ++it) {
             if (ahead < u1) {
                 issue(ahead, issued++ % X::STAGES);
                 ahead += kWarps;
@@ -349,7 +360,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                 break;
             }
             const char* buf = my_ring + stage * X::US * X::STRIP;
-            const int left = n_tok - u * kUnit < kUnit ? (int)(n_tok - u * kUnit) : kUnit;   // valid tokens
+            const int left = n_tok - u * kUnit < kUnit ? n_tok - u * kUnit : kUnit;   // valid tokens
 
             // scores of the unit, in raw units
             float S[X::US][NT][4];
@@ -554,7 +565,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
             __syncwarp();    // every lane has read the stage before it is copied into again
         }
 
-        // join the warps: maximum, then 8 query rows at a time through shared memory
+        // join the warps: maximum, then 8 query rows at a time through the ring's memory
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -569,8 +580,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
         const bool direct = whole && p.out;
         const int slot = blockIdx.x + sidx;
         if (u0 == 0 && tid == 0) {
-            const long long first = pos / share, last = (pos + units - 1) / share;
-            p.seg[sidx] = make_int2(slot, (int)(last - first) + 1);
+            const long long last = (first_unit + units - 1) / share;
+            p.seg[sidx] = make_int2(slot, (int)(last - blockIdx.x) + 1);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -625,9 +636,9 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                     if (d == 0) p.part_ml[row] = make_float2(top == -INFINITY ? top : top * p.k, sum);
                 }
             }
+            fence_proxy_async_smem();    // copies of the next segment go where these values are
             __syncthreads();
         }
-        pos += u1 - u0;
     }
 }
 
@@ -686,6 +697,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinP p) {
     for (int e = 0; e < kN; ++e) v[e] = 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
+#pragma unroll 4
         for (int s = 0; s < n[i]; ++s) {
             const float2 x = ml[i][s * step[i]];
             const float f = x.x == -INFINITY ? 1.f : ex2(x.x - top);
@@ -753,7 +765,7 @@ int launch(const AttnP& p, long long most_units, cudaStream_t stream) {
         n = sms * occ < kMaxGrid ? sms * occ : kMaxGrid;
         __atomic_store_n(&ctas[dev], n, __ATOMIC_RELEASE);
     }
-    const long long want = (most_units + kMinShare - 1) / kMinShare;
+    const long long want = (most_units + kMinShare + kSegCost - 1) / (kMinShare + kSegCost);
     const int grid = want < n ? (int)(want < 1 ? 1 : want) : n;
     attn_kernel<BITS, D, NT><<<grid, 32 * kWarps, X::kSmem, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? EDGE0_OK : EDGE0_ECUDA;
@@ -763,7 +775,7 @@ template <int BITS, int D>
 int launch_nt(const AttnP& p, int NT, cudaStream_t stream) {
     constexpr int kUnit = 16 * Cfg<BITS, D, 1>::US;
     const long long cap = p.lens ? (long long)p.W * p.c.page_tokens : p.n_tok;
-    const long long most = (cap + kUnit - 1) / kUnit * p.n_seq * p.H * p.RB;
+    const long long most = ((cap + kUnit - 1) / kUnit + kSegCost) * p.n_seq * p.H * p.RB;
     if (NT == 1) return launch<BITS, D, 1>(p, most, stream);
     if (NT == 2) return launch<BITS, D, 2>(p, most, stream);
     if constexpr (D <= 128) return launch<BITS, D, 4>(p, most, stream);
