@@ -25,7 +25,7 @@
 // token pairs that the A fragments of V^T want; P^T goes from accumulator to
 // B fragment with movmatrix.  The running maximum moves only when a score exceeds
 // it by 2^8, so most units rescale nothing.
-#include "kvcache.cuh"
+#include "attn.cuh"
 
 namespace edge0 {
 namespace {
@@ -117,25 +117,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
     return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float max_over_rows(float v) {   // the 8 lanes of one t
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
@@ -651,6 +632,7 @@ struct JoinP {
     const float* part_o[2];
     const float2* part_ml[2];
     const int2* seg[2];
+    int splits;              // > 0: the prefix's parts come from attn_prefix_kernel, so many per block
     __half* out;
     long long ldo;
 };
@@ -678,7 +660,8 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinP p) {
         if (i == 0 ? p.n_prefix == 0 : len == 0) continue;
         const int w = i == 0 ? 1 : 0;     // the prefix first
         const int r = w ? b * p.G + j : j;
-        const int2 sg = p.seg[w][((w ? 0 : b) * p.H + h) * p.RB[w] + r / p.rows[w]];
+        const int block = ((w ? 0 : b) * p.H + h) * p.RB[w] + r / p.rows[w];
+        const int2 sg = w && p.splits ? make_int2(block * p.splits, p.splits) : p.seg[w][block];
         n[i] = sg.y;
         const long long at = (long long)sg.x * p.rows[w] + r % p.rows[w];
         o[i] = p.part_o[w] + at * D;
@@ -720,25 +703,37 @@ int nt_of(int rows, int D, bool prefix) {
     return rows <= 16 || D == 256 || !prefix ? 2 : 4;
 }
 
+// The prefix's rows per K/V head from which the fifth-generation tensor cores take it.
+constexpr int kPrefixFrom = 33;
+constexpr int kSmsAssumed = 152;      // for the workspace's size; a card with fewer needs less
+
 struct Part {
-    int NT, RB, segs;
+    int NT, RB, segs, splits, tiles;  // NT == 0: attn_prefix_kernel
+    int rows;                         // rows per block
     long long slots, o, ml, seg;      // workspace offsets
 };
 
 // workspace: own parts then the prefix's; returns its size
-long long layout(int B, int G, int H, int D, Part (&part)[2]) {
+long long layout(int B, int G, int H, int D, int n_prefix, Part (&part)[2]) {
     long long at = 0;
     for (int w = 0; w < 2; ++w) {
         Part& x = part[w];
         const int rows = w ? B * G : G;
-        x.NT = nt_of(rows, D, w == 1);
-        x.RB = ceil_div(rows, 8 * x.NT);
+        x.NT = w && rows >= kPrefixFrom ? 0 : nt_of(rows, D, w == 1);
+        x.rows = x.NT ? 8 * x.NT : kPrefixRows;
+        x.RB = ceil_div(rows, x.rows);
         x.segs = (w ? 1 : B) * H * x.RB;
-        x.slots = (long long)kMaxGrid + x.segs;
+        x.splits = x.tiles = 0;
+        if (x.NT == 0) {
+            prefix_shares(n_prefix > 0 ? n_prefix : 1, x.segs, D, kSmsAssumed, &x.splits, &x.tiles);
+            x.slots = 2 * kSmsAssumed + x.segs;
+        } else {
+            x.slots = (long long)kMaxGrid + x.segs;
+        }
         x.o = at;
-        at += x.slots * 8 * x.NT * D * 4;
+        at += x.slots * x.rows * D * 4;
         x.ml = at;
-        at += x.slots * 8 * x.NT * 8;
+        at += x.slots * x.rows * 8;
         x.seg = at;
         at += ((long long)x.segs * 8 + 15) / 16 * 16;
     }
@@ -803,7 +798,7 @@ extern "C" size_t edge0_attn_workspace_bytes(const edge0_kv_cache* cache, int B,
     if (kv::view_of(cache, &c) || B <= 0 || B > EDGE0_MAX_BATCHED) return 0;
     if (n_q_heads <= 0 || n_q_heads % c.H || n_q_heads / c.H > EDGE0_MAX_Q_PER_KV) return 0;
     Part part[2];
-    return (size_t)layout(B, n_q_heads / c.H, c.H, cache->head_dim, part);
+    return (size_t)layout(B, n_q_heads / c.H, c.H, cache->head_dim, 0, part);
 }
 
 extern "C" int edge0_attn_decode(const edge0_kv_cache* cache, const uint16_t* q, long long ldq, int B, int n_q_heads,
@@ -826,7 +821,7 @@ extern "C" int edge0_attn_decode(const edge0_kv_cache* cache, const uint16_t* q,
     Part part[2];
     p.H = p.c.H;
     p.G = n_q_heads / p.H;
-    if ((long long)workspace_bytes < layout(B, p.G, p.H, D, part)) return EDGE0_EINVAL;
+    if ((long long)workspace_bytes < layout(B, p.G, p.H, D, n_prefix, part)) return EDGE0_EINVAL;
     char* ws = (char*)workspace;
     p.q = (const __half*)q;
     p.ldq = ldq;
@@ -835,6 +830,13 @@ extern "C" int edge0_attn_decode(const edge0_kv_cache* cache, const uint16_t* q,
     p.status = status;
     for (int w = 1; w >= 0; --w) {
         if (w && !n_prefix) continue;
+        if (part[w].NT == 0) {
+            const PrefixP x{p.c, p.q, ldq, p.G, p.H, B * p.G, part[w].RB, part[w].splits, part[w].tiles, prefix, n_prefix,
+                            scale * 1.4426950408889634f, (float*)(ws + part[w].o), (float2*)(ws + part[w].ml), status};
+            rc = prefix_launch(x, cache->bits, D, stream);
+            if (rc) return rc;
+            continue;
+        }
         p.n_seq = w ? 1 : B;
         p.rows = w ? B * p.G : p.G;
         p.RB = part[w].RB;
@@ -859,11 +861,12 @@ extern "C" int edge0_attn_decode(const edge0_kv_cache* cache, const uint16_t* q,
     j.n_prefix = n_prefix;
     for (int w = 0; w < 2; ++w) {
         j.RB[w] = part[w].RB;
-        j.rows[w] = 8 * part[w].NT;
+        j.rows[w] = part[w].rows;
         j.part_o[w] = (const float*)(ws + part[w].o);
         j.part_ml[w] = (const float2*)(ws + part[w].ml);
         j.seg[w] = (const int2*)(ws + part[w].seg);
     }
+    j.splits = part[1].NT ? 0 : part[1].splits;
     j.out = (__half*)out;
     j.ldo = ldo;
     const int grid = ceil_div(B * n_q_heads, 4);

@@ -1,0 +1,49 @@
+// What the attention kernels share: the description of a prefix's work on the
+// fifth-generation tensor cores (attn_prefix.cu), launched by attn.cu.
+#pragma once
+#include "kvcache.cuh"
+
+namespace edge0 {
+
+constexpr int kPrefixRows = 128;     // query rows of a CTA: the rows of one accumulator
+constexpr int kPrefixTile = 64;      // tokens per step
+
+struct PrefixP {
+    kv::View c;
+    const __half* q;
+    long long ldq;
+    int G, H, rows;                  // query heads per K/V head, K/V heads, query rows per K/V head
+    int RB, splits, tiles_per_split; // row blocks; shares of the prefix, each of so many tiles
+    const int* pages;
+    int n_tok;
+    float k;                         // scale log2(e)
+    float* part_o;                   // [(h RB + rb) splits + share][kPrefixRows][D]
+    float2* part_ml;                 // [..][kPrefixRows] (maximum in exponent units, sum)
+    int* status;
+};
+
+// shares of the prefix that fill the card for `segs` (K/V head, row block) pairs
+void prefix_shares(int n_tok, int segs, int D, int sms, int* splits, int* tiles_per_split);
+int prefix_launch(const PrefixP& p, int bits, int D, cudaStream_t stream);
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+}  // namespace edge0
