@@ -18,13 +18,14 @@
 //   S^T = K Q^T   codes enter as fp16 subnormals q 2^-24 (exact products, fp32 sums); per 64
 //                 dims S += s acc + b sum(Q), in fp32: scores carry no rounding of K;
 //   O^T = V'^T P' V = s (q - z) + (b + s z), z half the code range: q - z is exact in
-//                 fp16, the weight p s is rounded to fp16 (its only rounding), scaled by a
-//                 power of two 2^-E at least the largest s so far so that it stays
-//                 normal; sum p (b + s z) is kept in fp32 beside it.
+//                 fp16, the weight p s is rounded to fp16 (its only rounding);
+//                 sum p (b + s z) is kept in fp32 beside it.
+// The exponents' reference is the running maximum plus the exponent of the largest V
+// scale so far, so that p s stays within fp16's normal range whatever the scales.
 // ldmatrix delivers K codes as A fragments and, transposed, V codes with the
 // token pairs that the A fragments of V^T want; P^T goes from accumulator to
-// B fragment with movmatrix.  The running maximum moves only when a score exceeds
-// it by 2^8, so most units rescale nothing.
+// B fragment with movmatrix.  The reference moves only when a score exceeds it by 2^8
+// or a scale by 2^6, so most units rescale nothing.
 #include "attn.cuh"
 
 namespace edge0 {
@@ -310,7 +311,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
         }
         __syncthreads();
 
-        float O[X::MT][NT][4], beta[NT][X::GR][2], m[NT][2], l[NT][2], thr[NT][2], mu[NT][2], es[X::GR];
+        float O[X::MT][NT][4], beta[NT][X::GR][2], m[NT][2], l[NT][2], thr[NT][2], mu[NT][2];
+        float e = 0.f, thr_s = 0.f;          // exponent of a score: k S - mu, mu = k m + e
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -325,9 +327,6 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                 for (int gr = 0; gr < X::GR; ++gr) beta[nt][gr][i] = 0.f;
             }
         }
-#pragma unroll
-        for (int gr = 0; gr < X::GR; ++gr) es[gr] = INFINITY;
-
 #pragma unroll 1
         for (int u = dead ? u1 : u0 + wid; u < u1; u += kWarps, ++it) {
             if (ahead < u1) {
@@ -419,8 +418,28 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                 }
             }
 
-            // the running maximum moves when a score is 2^8 above it
-            bool up = false;
+            // V's scales of the unit's tokens g and g + 8, zero where there is no token
+            float2 vs[X::US][X::GR][2];
+            float top_s = 0.f;
+#pragma unroll
+            for (int st = 0; st < X::US; ++st) {
+                const char* sbp = buf + st * X::STRIP + X::HALF + 16 * X::R;
+#pragma unroll
+                for (int gr = 0; gr < X::GR; ++gr)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float2 sb = make_float2(0.f, 0.f);
+                        if (st * 16 + g + 8 * i < left)
+                            sb = __half22float2(
+                                *reinterpret_cast<const __half2*>(sbp + (g + 8 * i) * X::SB + gr * 4));
+                        sb.y = fmaf(sb.x, BITS == 4 ? 8.f : 128.f, sb.y);
+                        vs[st][gr][i] = sb;
+                        top_s = fmaxf(top_s, sb.x);
+                    }
+            }
+
+            // the reference moves when a score is 2^8 above it or a scale 2^6
+            bool up = top_s > thr_s;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -428,6 +447,12 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                     up = up || S[st][nt][0] > thr[nt][0] || S[st][nt][2] > thr[nt][0] || S[st][nt][1] > thr[nt][1] ||
                          S[st][nt][3] > thr[nt][1];
             if (__any_sync(0xffffffffu, up)) {
+                top_s = max_over_rows(top_s);
+                if (top_s > thr_s) {
+                    const int be = (int)(__float_as_uint(top_s) >> 23);      // top_s < 2^(be - 126)
+                    e = (float)((be < 240 ? be : 240) - 126);
+                    thr_s = __uint_as_float((unsigned)((int)e + 6 + 127) << 23);
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -437,9 +462,10 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                         for (int st = 0; st < X::US; ++st) v = fmaxf(v, fmaxf(S[st][nt][i], S[st][nt][i + 2]));
                         v = max_over_rows(v);
                         if (!(v > thr[nt][i])) v = m[nt][i];      // each row by its own scores alone
-                        const float f = m[nt][i] == -INFINITY ? 0.f : ex2((m[nt][i] - v) * p.k);
+                        const float to = v == -INFINITY ? 0.f : fmaf(v, p.k, e);
+                        const float f = m[nt][i] == -INFINITY ? 0.f : ex2(mu[nt][i] - to);
                         m[nt][i] = v;
-                        mu[nt][i] = v == -INFINITY ? 0.f : v * p.k;
+                        mu[nt][i] = to;
                         thr[nt][i] = v + 8.f / p.k;
                         l[nt][i] *= f;
 #pragma unroll
@@ -461,46 +487,6 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                         l[nt][i & 1] += S[st][nt][i];
                     }
 
-            // V: scales of the unit's tokens g and g + 8, zero where there is no token
-            float2 vs[X::US][X::GR][2];
-            bool grow = false;
-#pragma unroll
-            for (int st = 0; st < X::US; ++st) {
-                const char* sbp = buf + st * X::STRIP + X::HALF + 16 * X::R;
-#pragma unroll
-                for (int gr = 0; gr < X::GR; ++gr)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float2 sb = make_float2(0.f, 0.f);
-                        if (st * 16 + g + 8 * i < left)
-                            sb = __half22float2(
-                                *reinterpret_cast<const __half2*>(sbp + (g + 8 * i) * X::SB + gr * 4));
-                        sb.y = fmaf(sb.x, BITS == 4 ? 8.f : 128.f, sb.y);
-                        vs[st][gr][i] = sb;
-                        grow = grow || sb.x * es[gr] > 1.f;
-                    }
-            }
-            if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                for (int gr = 0; gr < X::GR; ++gr) {
-                    float v = 0.f;
-#pragma unroll
-                    for (int st = 0; st < X::US; ++st) v = fmaxf(v, fmaxf(vs[st][gr][0].x, vs[st][gr][1].x));
-                    v = max_over_rows(v);
-                    if (v * es[gr] > 1.f) {
-                        const unsigned be = __float_as_uint(v) >> 23;      // v < 2^(be - 126)
-                        const float e = __uint_as_float((253u - (be < 250u ? be : 250u)) << 23);
-                        const float f = es[gr] == INFINITY ? 0.f : e / es[gr];
-                        es[gr] = e;
-#pragma unroll
-                        for (int mt = 0; mt < X::MT / X::GR; ++mt)
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) O[gr * (X::MT / X::GR) + mt][nt][i] *= f;
-                    }
-                }
-            }
 #pragma unroll
             for (int st = 0; st < X::US; ++st) {
                 if (st * 16 >= left) continue;
@@ -508,8 +494,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
 #pragma unroll
                 for (int gr = 0; gr < X::GR; ++gr) {
                     uint32_t b0[NT], b1[NT];
-                    const float e = es[gr] == INFINITY ? 0.f : es[gr];
-                    const float w0 = vs[st][gr][0].x * e, w1 = vs[st][gr][1].x * e;
+                    const float w0 = vs[st][gr][0].x, w1 = vs[st][gr][1].x;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const float* P = S[st][nt];
@@ -554,7 +539,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                 l[nt][i] = sum_over_rows(l[nt][i]);
 #pragma unroll
                 for (int gr = 0; gr < X::GR; ++gr) beta[nt][gr][i] = sum_over_rows(beta[nt][gr][i]);
-                if (g == 0) sml[(wid * NT + nt) * 8 + 2 * t + i] = make_float2(m[nt][i], l[nt][i]);
+                if (g == 0) sml[(wid * NT + nt) * 8 + 2 * t + i] =
+                                make_float2(m[nt][i] == -INFINITY ? -INFINITY : mu[nt][i], l[nt][i]);
             }
         __syncthreads();
         const bool whole = u0 == 0 && u1 == units;
@@ -573,14 +559,12 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                 float top = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[(w * NT + nt) * 8 + col].x);
-                const float f = m[nt][i] == -INFINITY ? (l[nt][i] == 0.f ? 0.f : l[nt][i]) : ex2((m[nt][i] - top) * p.k);
+                const float f = m[nt][i] == -INFINITY ? (l[nt][i] == 0.f ? 0.f : l[nt][i]) : ex2(mu[nt][i] - top);
                 float* dst = red + (wid * 8 + col) * X::kRedLd;
 #pragma unroll
                 for (int mt = 0; mt < X::MT; ++mt) {
-                    const int gr = mt / (X::MT / X::GR);
-                    const float inv = 1.f / es[gr];
-                    const float2 v = make_float2(fmaf(O[mt][nt][i], inv, beta[nt][gr][i]) * f,
-                                                 fmaf(O[mt][nt][i + 2], inv, beta[nt][gr][i]) * f);
+                    const float add = beta[nt][mt / (X::MT / X::GR)][i];
+                    const float2 v = make_float2((O[mt][nt][i] + add) * f, (O[mt][nt][i + 2] + add) * f);
                     *reinterpret_cast<float2*>(dst + dim_of<BITS>(mt, g)) = v;
                 }
             }
@@ -595,7 +579,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float2 ml = sml[(w * NT + nt) * 8 + col];
-                    sum += ml.x == -INFINITY ? ml.y : ml.y * ex2((ml.x - top) * p.k);
+                    sum += ml.x == -INFINITY ? ml.y : ml.y * ex2(ml.x - top);
                 }
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -614,7 +598,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                 } else {
                     const long long row = (long long)slot * (8 * NT) + nt * 8 + col;
                     *reinterpret_cast<float4*>(p.part_o + row * D + d) = v;
-                    if (d == 0) p.part_ml[row] = make_float2(top == -INFINITY ? top : top * p.k, sum);
+                    if (d == 0) p.part_ml[row] = make_float2(top, sum);
                 }
             }
             fence_proxy_async_smem();    // copies of the next segment go where these values are

@@ -3,25 +3,28 @@
 //
 // One CTA: 128 query rows (sequence, head of one K/V head's group) x a share of the
 // prefix, 64 tokens a step.  Per step
-//   warps 4-7   turn the tile's codes into fp16 (code - z, z half the code range: exact) in
-//               shared memory, K as K-major, V as MN-major operand tiles, and its scales
-//               into fp32 tables; the next tile's codes are loaded into registers meanwhile;
-//   warp 4      issues S_g = Q_g K_g^T per 64 dims g, then O_g += P'_g V_g, accumulators and P'
-//               (over S, which is read by then) in TMEM;
-//   warps 0-3   a thread per row: S = sum_g s_g S_g + (b_g + z s_g) sum Q_g, running maximum
-//               and sum, weights p, P'_g = fp16(p s_g 2^-E_g) and sum_j p (b_g + z s_g) in fp32.
+//   warps 8-11  turn a strip of codes each into fp16 (code - z, z half the code range: exact)
+//               in shared memory, K as K-major, V as MN-major operand tiles, and its scales
+//               into fp32 tables; the next step's codes are loaded into registers meanwhile;
+//   thread 0    issues S_g = Q_g K_g^T per 64 dims g, and once the weights are there
+//               O_g += P'_g V_g; accumulators and P' (over S, which is read by then) in TMEM;
+//   warps 0-7   two threads per row, 32 tokens each: S = sum_g s_g S_g + (b_g + z s_g) sum Q_g,
+//               running maximum and sum, weights p, P'_g = fp16(p s_g), and
+//               sum_j p (b_g + z s_g) in fp32.
 // So the scores carry no rounding of K, and each weight is rounded once (to fp16, 2^-11 of
-// itself; 2^-E_g keeps it normal).  o = 2^E_g O_g + sum p (b_g + z s_g).
-// The running maximum moves only when a score exceeds it by 2^8, and the accumulators
-// are then rescaled in TMEM.  Two CTAs per SM (D <= 128): one's tensor steps run under
-// the other's softmax.
+// itself).  o = (O_g + sum p (b_g + z s_g)) / sum p.  The exponents' reference is the
+// running maximum plus the exponent of the largest scale so far, so that p s stays within
+// fp16's normal range whatever the scales; it moves only when a score exceeds it by
+// 2^8 or a scale by 2^6, and the accumulators are then rescaled in TMEM.
+// Two CTAs per SM (D <= 128): one's tensor steps run under the other's softmax.
 #include "attn.cuh"
 #include "tc05.cuh"
 
 namespace edge0 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kSoftmax = 256;             // threads of the softmax warps
+constexpr int kThreads = kSoftmax + 128;  // and the operand warps
 constexpr int kRowsQ = kPrefixRows;
 constexpr int kTile = kPrefixTile;
 
@@ -30,14 +33,13 @@ struct Cfg {
     static constexpr int R = kv::row_bytes(BITS, D);
     static constexpr int CH = R / 16;
     static constexpr int GR = D / kGroup;
-    static constexpr int SB = kv::sb_bytes(D);
     static constexpr int STRIP = kv::strip_bytes(BITS, D);
     static constexpr int HALF = kv::half_bytes(BITS, D);
-    static constexpr int NP = CH / 2;                       // 16-byte pieces of K (and of V) per thread and tile
+    static constexpr int NP = CH / 2;                       // 16-byte pieces of K (and of V) per thread and step
     static constexpr int kQ = kRowsQ * D * 2;
     static constexpr int kOp = kTile * D * 2;               // one operand tile
     static constexpr int kTab = 4 * GR * kTile * 4;         // K s, K c, V s, V c
-    static constexpr int kStage = 2 * kOp + kTab + 16;      // + 2^-E per 64 dims
+    static constexpr int kStage = 2 * kOp + kTab;
     static constexpr int kSmem = kQ + 2 * kStage;
     static constexpr int kCols = GR * kTile + D <= 128 ? 128 : GR * kTile + D <= 256 ? 256 : 512;
     static constexpr int kCtas = D <= 128 ? 2 : 1;
@@ -97,11 +99,25 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, u
         "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
-// MN-major operand tile without swizzle: 8 tokens x 16 bytes (8 dims) blocks, the blocks of
-// consecutive tokens 128 bytes apart (leading offset), of consecutive dims kTile * 16 (stride)
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)((kTile * 16) >> 4) << 32) |
-           (1ull << 46);
+// Operand descriptors: the low word advances with the address, the high word is fixed.
+// MN-major tile without swizzle: blocks of 8 tokens x 16 bytes (8 dims); the blocks of
+// consecutive tokens lie 128 bytes apart (leading offset), of consecutive dims kTile * 16 (stride).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t leading) { return (saddr >> 4) | ((leading >> 4) << 16); }
+__device__ __forceinline__ uint64_t desc(uint32_t lo, uint32_t stride) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"((stride >> 4) | (1u << 14)));
+    return d;
+}
+// whether any of the softmax threads wants it
+__device__ __forceinline__ bool any_softmax(bool want) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 256, p;\n"
+        " selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)want)
+        : "memory");
+    return r != 0;
 }
 
 // codes of 8 dims less z as fp16; 4 bits: one word, dims in the order 0 4 1 5 2 6 3 7;
@@ -145,9 +161,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
     constexpr int GR = X::GR;
     constexpr float kZ = BITS == 4 ? 8.f : 128.f;
     extern __shared__ __align__(1024) char smem[];
-    __shared__ uint64_t full[2], freed[2], s_ready, p_ready;
+    __shared__ uint64_t full[2], freed[2], s_ready;
     __shared__ uint32_t taddr_s;
     __shared__ int dead;
+    __shared__ float part_max[2][kRowsQ], part_sum[2][1 + GR][kRowsQ];
     char* sQ = smem;
     const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
     const int h = blockIdx.z, rb = blockIdx.y;
@@ -166,172 +183,120 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             mbar_init(&freed[i], 1);
         }
         mbar_init(&s_ready, 1);
-        mbar_init(&p_ready, 4);
         fence_mbar_init();
         dead = 0;
     }
-    // queries, K-major, 8 dims in the order of the codes
-    for (int i = tid; i < kRowsQ * (D / 8); i += kThreads) {
-        const int r = (i & 7) + 8 * (i / (8 * (D / 8))), c8 = (i >> 3) % (D / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r0 + r < p.rows) {
-            const int row = r0 + r;
-            v = *reinterpret_cast<const uint4*>(p.q + (long long)(row / p.G) * p.ldq +
-                                                (long long)(h * p.G + row % p.G) * D + 8 * c8);
-            if (BITS == 4)
-                v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                               __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+    if (wid < 8) {
+        // queries, K-major, 8 dims in the order of the codes
+        for (int i = tid; i < kRowsQ * (D / 8); i += kSoftmax) {
+            const int r = (i & 7) + 8 * (i / (8 * (D / 8))), c8 = (i >> 3) % (D / 8);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (r0 + r < p.rows) {
+                const int row = r0 + r;
+                v = *reinterpret_cast<const uint4*>(p.q + (long long)(row / p.G) * p.ldq +
+                                                    (long long)(h * p.G + row % p.G) * D + 8 * c8);
+                if (BITS == 4)
+                    v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                   __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+            }
+            *reinterpret_cast<uint4*>(sQ + (c8 >> 1) * (kRowsQ * 32) + tc::kstep_off(r, (c8 & 1) * 8)) = v;
         }
-        *reinterpret_cast<uint4*>(sQ + (c8 >> 1) * (kRowsQ * 32) + tc::kstep_off(r, (c8 & 1) * 8)) = v;
+        tc::fence_async_smem();
     }
-    tc::fence_async_smem();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tm = taddr_s;
 
-    if (wid >= 4) {
+    if (wid >= 8) {
         // ---------------------------------------------------------- operands
-        const int dt = tid - 128;
+        const int w = wid - 8;                                 // strip of the tile
         const int spp = p.c.page_tokens / kv::kStrip;
         const int last_strip = (p.n_tok - 1) / kv::kStrip;
+        int strip = t0 * (kTile / 16) + w, pg = strip / spp, in_page = strip - pg * spp;
+        // the strip's place in the pool; behind the last token, that strip again
+        auto page_of = [&]() -> int {
+            if (strip > last_strip) {
+                strip = last_strip;
+                pg = strip / spp;
+                in_page = strip - pg * spp;
+            }
+            return p.pages[pg];
+        };
+        int id = page_of();
         uint4 rk[X::NP], rv[X::NP];
-        uint32_t rs[2][GR];
-        auto load = [&](int tile) {
-            // byte offsets of the tile's four strips, one per lane of four
-            int st = tile * (kTile / 16) + (lane & 3);
-            st = st < last_strip ? st : last_strip;
-            const int pg = st / spp;
-            int id = p.pages[pg];
+        uint32_t rs[GR];                                       // (s, b) words: K's, then V's
+        auto load = [&]() {
             if (id < 0 || id >= p.c.n_pages) {
                 id = 0;
                 if (p.status) atomicExch(p.status, EDGE0_EINVAL);
             }
-            const long long off = id * p.c.page_bytes + ((long long)h * spp + (st - pg * spp)) * X::STRIP;
+            const char* base = p.c.pages + id * p.c.page_bytes + ((long long)h * spp + in_page) * X::STRIP;
 #pragma unroll
             for (int j = 0; j < X::NP; ++j) {
-                const int i = j * 128 + dt, c = (i >> 3) % X::CH, tok = (i & 7) + 8 * ((i >> 3) / X::CH);
-                const char* src = p.c.pages + __shfl_sync(0xffffffffu, off, tok >> 4) + (tok & 15) * X::R +
-                                  ((c ^ kv::turn(X::R, tok & 15)) << 4);
+                const int i = j * 32 + lane, c = (i >> 3) % X::CH, tok = (i & 7) + 8 * ((i >> 3) / X::CH);
+                const char* src = base + tok * X::R + ((c ^ kv::turn(X::R, tok)) << 4);
                 rk[j] = *reinterpret_cast<const uint4*>(src);
                 rv[j] = *reinterpret_cast<const uint4*>(src + X::HALF);
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int tok = lane + 32 * i;
-                const char* src = p.c.pages + __shfl_sync(0xffffffffu, off, tok >> 4) + 16 * X::R + (tok & 15) * X::SB +
-                                  (wid == 5 ? X::HALF : 0);
-                if (wid == 5 || wid == 6)
-#pragma unroll
-                    for (int gr = 0; gr < GR; ++gr) rs[i][gr] = reinterpret_cast<const uint32_t*>(src)[gr];
+            for (int j = 0; j < GR; ++j) {
+                const int i = j * 32 + lane;                   // word of the strip's 2 x 16 GR
+                const bool v = i >= 16 * GR;
+                rs[j] = *reinterpret_cast<const uint32_t*>(base + (v ? X::HALF : 0) + 16 * X::R + (i - (v ? 16 * GR : 0)) * 4);
             }
+            // the next tile's strip, its page's number under way by then
+            strip += kTile / 16;
+            in_page += kTile / 16;
+            while (in_page >= spp) {
+                in_page -= spp;
+                ++pg;
+            }
+            id = page_of();
         };
-        float es[GR];
-#pragma unroll
-        for (int gr = 0; gr < GR; ++gr) es[gr] = 0.f;
         auto put = [&](int i) {
             char* stage = smem + X::kQ + (i & 1) * X::kStage;
             char *sK = stage, *sV = stage + X::kOp;
             float* tab = reinterpret_cast<float*>(stage + 2 * X::kOp);
 #pragma unroll
             for (int j = 0; j < X::NP; ++j) {
-                const int q = j * 128 + dt, c = (q >> 3) % X::CH, tok = (q & 7) + 8 * ((q >> 3) / X::CH);
+                const int q = j * 32 + lane, c = (q >> 3) % X::CH, tok = 16 * w + (q & 7) + 8 * ((q >> 3) / X::CH);
                 const uint32_t k4[4] = {rk[j].x, rk[j].y, rk[j].z, rk[j].w}, v4[4] = {rv[j].x, rv[j].y, rv[j].z, rv[j].w};
-                constexpr int kW = BITS == 4 ? 1 : 2;      // words per 8 dims
+                constexpr int kW = BITS == 4 ? 1 : 2;          // words per 8 dims
 #pragma unroll
-                for (int w = 0; w < 4 / kW; ++w) {
-                    const int c8 = c * (4 / kW) + w;       // 8 dims
+                for (int x = 0; x < 4 / kW; ++x) {
+                    const int c8 = c * (4 / kW) + x;           // 8 dims
                     *reinterpret_cast<uint4*>(sK + (c8 >> 1) * (kTile * 32) + tc::kstep_off(tok, (c8 & 1) * 8)) =
-                        codes8<BITS>(k4[w * kW], k4[w * kW + kW - 1]);
+                        codes8<BITS>(k4[x * kW], k4[x * kW + kW - 1]);
                     *reinterpret_cast<uint4*>(sV + c8 * (kTile * 16) + tok * 16) =
-                        codes8<BITS>(v4[w * kW], v4[w * kW + kW - 1]);
+                        codes8<BITS>(v4[x * kW], v4[x * kW + kW - 1]);
                 }
             }
-            if (wid == 5 || wid == 6) {
-                const int left = p.n_tok - (t0 + i) * kTile;
-                float* at = tab + (wid == 5 ? 2 * GR * kTile : 0);
+            const int left = p.n_tok - (t0 + i) * kTile;
 #pragma unroll
-                for (int gr = 0; gr < GR; ++gr) {
-                    float2 sb[2];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        sb[q] = __half22float2(*reinterpret_cast<const __half2*>(&rs[q][gr]));
-                        if (lane + 32 * q >= left) sb[q] = make_float2(0.f, 0.f);
-                        sb[q].y = fmaf(sb[q].x, kZ, sb[q].y);
-                    }
-                    if (wid == 5) {
-                        // 2^-E: the largest scale so far to at most 64
-                        float top = fmaxf(sb[0].x, sb[1].x);
-#pragma unroll
-                        for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-                        if (top > 0.f && (es[gr] == 0.f || top * es[gr] > 64.f)) {
-                            const unsigned be = __float_as_uint(top) >> 23;
-                            es[gr] = __uint_as_float((253u - (be < 250u ? be : 250u)) << 23);
-                        }
-                        sb[0].x *= es[gr];
-                        sb[1].x *= es[gr];
-                        if (lane == 0) tab[4 * GR * kTile + gr] = es[gr];
-                    }
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        at[gr * kTile + lane + 32 * q] = sb[q].x;
-                        at[(GR + gr) * kTile + lane + 32 * q] = sb[q].y;
-                    }
-                }
+            for (int j = 0; j < GR; ++j) {
+                const int q = j * 32 + lane, v = q >= 16 * GR ? 1 : 0, e = q - v * 16 * GR;
+                const int tok = 16 * w + e / GR, gr = e % GR;
+                float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&rs[j]));
+                if (tok >= left) sb = make_float2(0.f, 0.f);
+                tab[(2 * v * GR + gr) * kTile + tok] = sb.x;
+                tab[((2 * v + 1) * GR + gr) * kTile + tok] = fmaf(sb.x, kZ, sb.y);
             }
             tc::fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[i & 1]);
         };
-        auto put_when_free = [&](int i) -> bool {
-            if (i >= 2 && !__all_sync(0xffffffffu, wait_bar(&freed[i & 1], ((i >> 1) - 1) & 1, &dead))) return false;
+        load();
+        for (int i = 0; i < n; ++i) {
+            if (i >= 2 && !__all_sync(0xffffffffu, wait_bar(&freed[i & 1], ((i >> 1) - 1) & 1, &dead))) break;
             put(i);
-            if (i + 1 < n) load(t0 + i + 1);
-            return true;
-        };
-        load(t0);
-        if (wid == 4) {
-            const uint32_t id_s = tc::idesc_f16(kRowsQ, kTile), id_o = tc::idesc_f16(kRowsQ, kGroup) | (1u << 16);
-            bool ok = put_when_free(0);
-            for (int i = 0; i < n && ok; ++i) {
-                const uint32_t sK = smem_u32(smem + X::kQ + (i & 1) * X::kStage), sV = sK + X::kOp;
-                ok = wait_bar(&full[i & 1], (i >> 1) & 1, &dead);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (lane == 0) {
-                    tc::fence_after_sync();
-                    const uint32_t a0 = smem_u32(sQ);
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        tc::mma_f16(tm + (ks / 4) * kTile, tc::smem_desc(a0 + ks * (kRowsQ * 32)),
-                                    tc::smem_desc(sK + ks * (kTile * 32)), id_s, ks % 4 != 0);
-                    tc::mma_commit(&s_ready);
-                }
-                __syncwarp();
-                if (i + 1 < n) ok = put_when_free(i + 1);
-                ok = ok && wait_bar(&p_ready, i & 1, &dead);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (lane == 0) {
-                    tc::fence_after_sync();
-#pragma unroll
-                    for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-                        for (int kk = 0; kk < kTile / 16; ++kk)
-                            mma_f16_ta(tm + GR * kTile + gr * kGroup, tm + gr * kTile + kk * 8,
-                                       desc_mn(sV + gr * (kGroup / 8) * (kTile * 16) + kk * 256), id_o, i > 0 || kk > 0);
-                    tc::mma_commit(&freed[i & 1]);
-                }
-                __syncwarp();
-            }
-        } else {
-            for (int i = 0; i < n; ++i)
-                if (!put_when_free(i)) break;
+            if (i + 1 < n) load();
         }
     } else {
         // ----------------------------------------------------------- softmax
-        const uint32_t my = tm + ((uint32_t)(32 * wid) << 16);
-        const int row = 32 * wid + lane;
+        const int hf = wid >> 2, quad = wid & 3;               // 32 tokens, 32 rows
+        const uint32_t my = tm + ((uint32_t)(32 * quad) << 16);
+        const int row = 32 * quad + lane;
         f2 qs[GR];
 #pragma unroll
         for (int gr = 0; gr < GR; ++gr) {
@@ -350,108 +315,135 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             }
             qs[gr] = pk(s, s);
         }
-        float m = -INFINITY, thr = -INFINITY, es[GR];
+        // exponent of a score: k S - mu, mu = k m + e; m the running maximum, 2^e the scales'
+        float m = -INFINITY, thr = -INFINITY, e = 0.f, thr_s = 0.f, mu = 0.f;
         f2 l2 = 0, beta[GR];
 #pragma unroll
-        for (int gr = 0; gr < GR; ++gr) {
-            es[gr] = 0.f;
-            beta[gr] = 0;
-        }
+        for (int gr = 0; gr < GR; ++gr) beta[gr] = 0;
         const f2 k2 = pk(p.k, p.k);
+        auto issue_scores = [&](int i) {                       // thread 0: S = Q K^T of tile i
+            const uint32_t sK = desc_lo(smem_u32(smem + X::kQ + (i & 1) * X::kStage), tc::kLbo);
+            const uint32_t a0 = desc_lo(smem_u32(sQ), tc::kLbo);
+            if (!wait_bar(&full[i & 1], (i >> 1) & 1, &dead)) return;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                tc::mma_f16(tm + (ks / 4) * kTile, desc(a0 + ks * (kRowsQ * 32 / 16), tc::kSbo),
+                            desc(sK + ks * (kTile * 32 / 16), tc::kSbo), tc::idesc_f16(kRowsQ, kTile), ks % 4 != 0);
+            tc::mma_commit(&s_ready);
+        };
+        if (tid == 0) issue_scores(0);
+        __syncwarp();
         bool ok = true;
         for (int i = 0; i < n; ++i) {
             const char* stage = smem + X::kQ + (i & 1) * X::kStage;
             const float* tab = reinterpret_cast<const float*>(stage + 2 * X::kOp);
+            const float* mine = tab + hf * 32;
+            // (after a wait that gave up the rest runs through without waiting: the warps
+            // meet at barriers in every step)
             ok = wait_bar(&full[i & 1], (i >> 1) & 1, &dead) && wait_bar(&s_ready, i & 1, &dead);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+            __syncwarp();
             tc::fence_after_sync();
-            f2 S[kTile / 2];
+            // 16 tokens of one group at a time, the next ones under way meanwhile
+            f2 S[16];
+            uint32_t raw[2][16];
+            tmem_ld16(my + hf * 32, raw[0]);
+            float top_s = fmaxf(tab[2 * GR * kTile + lane], tab[2 * GR * kTile + lane + 32]);
 #pragma unroll
-            for (int c = 0; c < kTile / 16; ++c) {
+            for (int gr = 1; gr < GR; ++gr)
+                top_s = fmaxf(top_s, fmaxf(tab[(2 * GR + gr) * kTile + lane], tab[(2 * GR + gr) * kTile + lane + 32]));
+            tc::tmem_wait_ld();
 #pragma unroll
-                for (int gr = 0; gr < GR; ++gr) {
-                    uint32_t a[16];
-                    tmem_ld16(my + gr * kTile + c * 16, a);
-                    tc::tmem_wait_ld();
-                    const ulonglong2* ks = reinterpret_cast<const ulonglong2*>(tab + gr * kTile + c * 16);
-                    const ulonglong2* kc = reinterpret_cast<const ulonglong2*>(tab + (GR + gr) * kTile + c * 16);
+            for (int q = 0; q < GR * 2; ++q) {
+                const int c = q / GR, gr = q % GR;
+                if (q + 1 < GR * 2) tmem_ld16(my + ((q + 1) % GR) * kTile + hf * 32 + ((q + 1) / GR) * 16, raw[(q + 1) & 1]);
+                const uint32_t(&a)[16] = raw[q & 1];
+                const ulonglong2* ks = reinterpret_cast<const ulonglong2*>(mine + gr * kTile + c * 16);
+                const ulonglong2* kc = reinterpret_cast<const ulonglong2*>(mine + (GR + gr) * kTile + c * 16);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const ulonglong2 s4 = ks[j], c4 = kc[j];
-                        const f2 x0 = pk(__uint_as_float(a[4 * j]), __uint_as_float(a[4 * j + 1]));
-                        const f2 x1 = pk(__uint_as_float(a[4 * j + 2]), __uint_as_float(a[4 * j + 3]));
-                        f2& d0 = S[c * 8 + 2 * j];
-                        f2& d1 = S[c * 8 + 2 * j + 1];
-                        d0 = fma2(x0, s4.x, gr ? fma2(c4.x, qs[gr], d0) : mul2(c4.x, qs[gr]));
-                        d1 = fma2(x1, s4.y, gr ? fma2(c4.y, qs[gr], d1) : mul2(c4.y, qs[gr]));
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const ulonglong2 s4 = ks[j], c4 = kc[j];
+                    const f2 x0 = pk(__uint_as_float(a[4 * j]), __uint_as_float(a[4 * j + 1]));
+                    const f2 x1 = pk(__uint_as_float(a[4 * j + 2]), __uint_as_float(a[4 * j + 3]));
+                    f2& d0 = S[c * 8 + 2 * j];
+                    f2& d1 = S[c * 8 + 2 * j + 1];
+                    d0 = fma2(x0, s4.x, gr ? fma2(c4.x, qs[gr], d0) : mul2(c4.x, qs[gr]));
+                    d1 = fma2(x1, s4.y, gr ? fma2(c4.y, qs[gr], d1) : mul2(c4.y, qs[gr]));
                 }
+                if (q + 1 < GR * 2) tc::tmem_wait_ld();
             }
-            const int left = p.n_tok - (t0 + i) * kTile;
-            if (left < kTile) {
+            const int left = p.n_tok - (t0 + i) * kTile - hf * 32;
+            if (left < 32) {
 #pragma unroll
-                for (int j = 0; j < kTile / 2; ++j) {
+                for (int j = 0; j < 16; ++j) {
                     float a, b;
                     unpk(S[j], a, b);
                     S[j] = pk(2 * j < left ? a : -INFINITY, 2 * j + 1 < left ? b : -INFINITY);
                 }
             }
-            float mx = -INFINITY;
+            float mx4[4];
 #pragma unroll
-            for (int j = 0; j < kTile / 2; ++j) {
+            for (int j = 0; j < 4; ++j) mx4[j] = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
                 float a, b;
                 unpk(S[j], a, b);
-                mx = fmaxf(mx, fmaxf(a, b));
+                mx4[j & 3] = fmaxf(mx4[j & 3], fmaxf(a, b));
             }
-            float f = 1.f;
-            if (mx > thr) {              // 2^8 above the running maximum
-                f = m == -INFINITY ? 0.f : ex2((m - mx) * p.k);
-                m = mx;
-                thr = m + 8.f / p.k;
-                float a, b;
-                unpk(l2, a, b);
-                l2 = pk(a * f, b * f);
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+            // (this barrier also ends every read of S before P' goes over it)
+            if (any_softmax(mx > thr || top_s > thr_s)) {
+                part_max[hf][row] = mx;
 #pragma unroll
-                for (int gr = 0; gr < GR; ++gr) beta[gr] = mul2(beta[gr], pk(f, f));
-            }
-            float fg[GR];
-            bool change = false;
+                for (int s = 16; s; s >>= 1) top_s = fmaxf(top_s, __shfl_xor_sync(0xffffffffu, top_s, s));
+                named_bar_sync(2, kSoftmax);
+                const float both = fmaxf(mx, part_max[hf ^ 1][row]);
+                if (top_s > thr_s) {
+                    const int be = (int)(__float_as_uint(top_s) >> 23);      // top_s < 2^(be - 126)
+                    e = (float)((be < 240 ? be : 240) - 126);
+                    thr_s = __uint_as_float((unsigned)((int)e + 6 + 127) << 23);
+                }
+                const bool first = m == -INFINITY;
+                if (both > thr) {
+                    m = both;
+                    thr = m + 8.f / p.k;
+                }
+                const float to = m == -INFINITY ? 0.f : fmaf(m, p.k, e);
+                const float f = first ? 0.f : ex2(mu - to);
+                mu = to;
+                const f2 ff = pk(f, f);
+                l2 = mul2(l2, ff);
 #pragma unroll
-            for (int gr = 0; gr < GR; ++gr) {
-                const float e = tab[4 * GR * kTile + gr];
-                fg[gr] = e == es[gr] ? f : es[gr] == 0.f ? 0.f : f * (e / es[gr]);
-                es[gr] = e;
-                change = change || fg[gr] != 1.f;
-            }
-            // (the first tile overwrites the accumulators)
-            if (i > 0 && __any_sync(0xffffffffu, change)) {
+                for (int gr = 0; gr < GR; ++gr) beta[gr] = mul2(beta[gr], ff);
+                // (the first tile overwrites the accumulators)
+                if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t a[16];
+                        const uint32_t at = my + GR * kTile + hf * (D / 2) + c * 16;
+                        tmem_ld16(at, a);
+                        tc::tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
-                    uint32_t a[16];
-                    tmem_ld16(my + GR * kTile + c * 16, a);
-                    tc::tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * fg[c / 4]);
-                    tmem_st16(my + GR * kTile + c * 16, a);
+                        for (int j = 0; j < 16; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * f);
+                        tmem_st16(at, a);
+                    }
                 }
             }
-            const float mu = m == -INFINITY ? 0.f : -m * p.k;
-            const f2 mu2 = pk(mu, mu);
+            const f2 mu2 = pk(-mu, -mu);
 #pragma unroll
-            for (int c = 0; c < kTile / 16; ++c) {
+            for (int c = 0; c < 2; ++c) {
                 f2 pr[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     float a, b;
                     unpk(fma2(S[c * 8 + j], k2, mu2), a, b);
                     pr[j] = pk(ex2(a), ex2(b));
-                    l2 = add2(l2, pr[j]);
                 }
+                l2 = add2(l2, add2(add2(add2(pr[0], pr[1]), add2(pr[2], pr[3])), add2(add2(pr[4], pr[5]), add2(pr[6], pr[7]))));
 #pragma unroll
                 for (int gr = 0; gr < GR; ++gr) {
-                    const ulonglong2* vs = reinterpret_cast<const ulonglong2*>(tab + (2 * GR + gr) * kTile + c * 16);
-                    const ulonglong2* vc = reinterpret_cast<const ulonglong2*>(tab + (3 * GR + gr) * kTile + c * 16);
+                    const ulonglong2* vs = reinterpret_cast<const ulonglong2*>(mine + (2 * GR + gr) * kTile + c * 16);
+                    const ulonglong2* vc = reinterpret_cast<const ulonglong2*>(mine + (3 * GR + gr) * kTile + c * 16);
                     uint32_t w[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -463,34 +455,55 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                         w[2 * j + 1] = pack2(a, b);
                         beta[gr] = fma2(pr[2 * j], c4.x, fma2(pr[2 * j + 1], c4.y, beta[gr]));
                     }
-                    tmem_st8(my + gr * kTile + c * 8, w);
+                    tmem_st8(my + gr * kTile + hf * 16 + c * 8, w);
                 }
             }
             tmem_wait_st();
             tc::fence_before_sync();
+            named_bar_sync(3, kSoftmax);
+            if (tid == 0) {
+                const uint32_t sV = desc_lo(smem_u32(stage) + X::kOp, 128);
+                tc::fence_after_sync();
+#pragma unroll
+                for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        mma_f16_ta(tm + GR * kTile + gr * kGroup, tm + gr * kTile + kk * 8,
+                                   desc(sV + (gr * (kGroup / 8) * (kTile * 16) + kk * 256) / 16, kTile * 16),
+                                   tc::idesc_f16(kRowsQ, kGroup) | (1u << 16), i > 0 || kk > 0);
+                tc::mma_commit(&freed[i & 1]);
+                if (i + 1 < n) issue_scores(i + 1);
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready);
         }
-        if (ok) ok = __all_sync(0xffffffffu, wait_bar(&freed[(n - 1) & 1], ((n - 1) >> 1) & 1, &dead));
-        if (ok) {
+        // the two threads of a row add up their sums, each writes half of the dims
+        float a, b;
+        unpk(l2, a, b);
+        part_sum[hf][0][row] = a + b;
+#pragma unroll
+        for (int gr = 0; gr < GR; ++gr) {
+            unpk(beta[gr], a, b);
+            part_sum[hf][1 + gr][row] = a + b;
+        }
+        ok = wait_bar(&freed[(n - 1) & 1], ((n - 1) >> 1) & 1, &dead) && ok;
+        named_bar_sync(2, kSoftmax);
+        if (__all_sync(0xffffffffu, ok)) {
             tc::fence_after_sync();
             const long long slot = ((long long)h * p.RB + rb) * p.splits + blockIdx.x;
-            float* dst = p.part_o + (slot * kRowsQ + row) * D;
+            float* dst = p.part_o + (slot * kRowsQ + row) * D + hf * (D / 2);
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-                uint32_t a[16];
-                tmem_ld16(my + GR * kTile + c * 16, a);
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t r[16];
+                tmem_ld16(my + GR * kTile + hf * (D / 2) + c * 16, r);
+                const int gr = (hf * (D / 2) + c * 16) / kGroup;
+                const float add = part_sum[0][1 + gr][row] + part_sum[1][1 + gr][row];
                 tc::tmem_wait_ld();
-                const int gr = c / 4;
-                float x, y;
-                unpk(beta[gr], x, y);
-                const float inv = es[gr] == 0.f ? 0.f : 1.f / es[gr], add = x + y;
                 float v[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     // column j of 8 dims holds dim 0 4 1 5 2 6 3 7 (4 bits)
                     const int d = BITS == 4 ? (j & 8) + ((j & 1) << 2) + ((j & 7) >> 1) : j;
-                    v[d] = fmaf(__uint_as_float(a[j]), inv, add);
+                    v[d] = __uint_as_float(r[j]) + add;
                 }
                 if (r0 + row < p.rows)
 #pragma unroll
@@ -498,10 +511,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                         reinterpret_cast<float4*>(dst + c * 16)[j] =
                             make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             }
-            float a, b;
-            unpk(l2, a, b);
-            if (r0 + row < p.rows)
-                p.part_ml[slot * kRowsQ + row] = make_float2(m == -INFINITY ? m : m * p.k, a + b);
+            if (hf == 0 && r0 + row < p.rows)
+                p.part_ml[slot * kRowsQ + row] =
+                    make_float2(m == -INFINITY ? m : mu, part_sum[0][0][row] + part_sum[1][0][row]);
         }
     }
     tc::fence_before_sync();
