@@ -8,13 +8,21 @@
 // kernel rounds the fp32 product (x - mn) * (1 / s), and where that lies next to
 // a border it decides by the sign of (x - mn) - (q +- 1/2) s, which fp32 holds
 // exactly there.
+//
+// Both kernels move rows of fp16 and bytes of codes.  A thread keeps its place in the
+// row and goes through its CTA's rows.  Written: 16 dims per thread, 8 from each half of
+// a group (four threads share its minimum, maximum and reciprocal); the next row's
+// values are loaded while one is worked on, the first ones before the rows' places are
+// known.  Read: 8 dims per thread, so that a warp's 16-byte stores lie side by side, four
+// rows at a time.
 #include "kvcache.cuh"
 
 namespace edge0 {
 namespace {
 
 constexpr int kKvThreads = 256;
-constexpr int kMaxRowsPerCta = 16;
+constexpr int kMaxRowsPerCta = 32;
+constexpr int kReadRows = 4;         // rows that a reading thread has under way
 
 // Where the rows of a CTA go: byte offset of each row's page, its token in the page.
 struct RowPlace {
@@ -83,108 +91,154 @@ __device__ __forceinline__ char* strip_of(const kv::View& c, const RowPlace& p, 
            ((long long)h * (c.page_tokens / kv::kStrip) + p.token / kv::kStrip) * kv::strip_bytes(BITS, D);
 }
 
-// Quantises 8 values of a group spread over 8 lanes; codes packed little end first
+// q of one value where the fp32 product may lie next to a border, or above the top code
+// where s was rounded down
+__device__ __forceinline__ float settle(float x, float mn, float s, float r, float top) {
+    const float d = x - mn, off = fmaf(-r, s, d);
+    if (fabsf(fabsf(off) - 0.5f * s) < 4e-4f * s) {
+        // d + lo is the exact x - mn; the border (r +- 1/2) s and d - border are exact
+        const float bb = d - x;
+        const float lo = (x - (d - bb)) + (-mn - bb);
+        const float side = off > 0.f ? 0.5f : -0.5f;
+        const float e = (d - (r + side) * s) + lo;
+        const float up = r + side + 0.5f, down = r + side - 0.5f;
+        r = e > 0.f ? up : e < 0.f ? down : ((int)up & 1) == 0 ? up : down;
+    }
+    return fminf(fmaxf(r, 0.f), top);
+}
+
+// Quantises 16 values of a group spread over 4 lanes; codes packed little end first
 template <int BITS>
-__device__ __forceinline__ void quantise8(const uint4& raw, uint32_t (&word)[2], __half2& sb) {
+__device__ __forceinline__ void quantise16(const uint4 (&raw)[2], uint32_t (&word)[BITS / 2], __half2& sb) {
     constexpr float kTop = (float)((1 << BITS) - 1);
-    const __half2* h2 = reinterpret_cast<const __half2*>(&raw);
-    float x[8];
+    constexpr float kRound = 12582912.f;                 // 1.5 2^23: an fp32 sum with it is a whole number
+    const __half2* h2 = reinterpret_cast<const __half2*>(raw);
+    // (minimum, minus maximum) in one register; a NaN stays
+    __half2 lo2 = h2[0], hi2 = h2[0];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(h2[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+    for (int i = 1; i < 8; ++i) {
+        lo2 = __hmin2_nan(lo2, h2[i]);
+        hi2 = __hmax2_nan(hi2, h2[i]);
     }
-    float mn = x[0], mx = x[0];
-    bool fine = true;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        mn = fminf(mn, x[i]);
-        mx = fmaxf(mx, x[i]);
-        fine = fine && isfinite(x[i]);
-    }
-    unsigned bad = fine ? 0u : 1u;
-#pragma unroll
-    for (int k = 1; k < 8; k <<= 1) {
-        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, k));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-        bad |= __shfl_xor_sync(0xffffffffu, bad, k);
-    }
-    const __half s16 = __float2half_rn(__fdiv_rn(mx - mn, kTop));
+    __half2 w = __hmin2_nan(__halves2half2(__low2half(lo2), __hneg(__low2half(hi2))),
+                            __halves2half2(__high2half(lo2), __hneg(__high2half(hi2))));
+    w = __hmin2_nan(w, __shfl_xor_sync(0xffffffffu, w, 1));
+    w = __hmin2_nan(w, __shfl_xor_sync(0xffffffffu, w, 2));
+    const float mn = __low2float(w), mx = -__high2float(w);
+    // (mx - mn) / kTop rounded to nearest: with the rounded reciprocal one residual step is exact
+    const float range = mx - mn, s0 = range * (1.f / kTop);
+    const __half s16 = __float2half_rn(fmaf(fmaf(-s0, kTop, range), 1.f / kTop, s0));
     const float s = __half2float(s16);
-    uint32_t q[8];
-    if (bad || s == 0.f) {
+    const bool bad = !isfinite(mn) || !isfinite(mx);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = 0;
-    } else {
-        const float inv = __frcp_rn(s);
+    for (int i = 0; i < BITS / 2; ++i) word[i] = 0;
+    if (!bad && s != 0.f) {
+        float inv;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+        float r[16], off = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float d = x[i] - mn;
-            float r = rintf(d * inv);
-            // next to a border: compare x - mn with the border itself.  d + lo is the
-            // exact x - mn; the border (r +- 1/2) s and d - border are exact
-            const float off = fmaf(-r, s, d);
-            if (fabsf(fabsf(off) - 0.5f * s) < 1e-3f * s) {
-                const float bb = d - x[i];
-                const float lo = (x[i] - (d - bb)) + (-mn - bb);
-                const float side = off > 0.f ? 0.5f : -0.5f;
-                const float border = (r + side) * s;
-                const float e = (d - border) + lo;
-                const float up = r + side + 0.5f, down = r + side - 0.5f;
-                const bool even_up = ((int)up & 1) == 0;
-                r = e > 0.f ? up : e < 0.f ? down : even_up ? up : down;
-            }
-            q[i] = (uint32_t)fminf(fmaxf(r, 0.f), kTop);
+            const float2 f = __half22float2(h2[i]);
+            const float d0 = f.x - mn, d1 = f.y - mn;
+            r[2 * i] = fmaf(d0, inv, kRound) - kRound;
+            r[2 * i + 1] = fmaf(d1, inv, kRound) - kRound;
+            off = fmaxf(off, fmaxf(fabsf(fmaf(-r[2 * i], s, d0)), fabsf(fmaf(-r[2 * i + 1], s, d1))));
         }
-    }
-    if (BITS == 4) {
-        word[0] = 0;
+        // r is settled unless a residual comes to half a step (the residuals are off by at most
+        // the rounding of d, 255 x 2^-24 of a step)
+        if (off > 0.49998f * s || range * inv > kTop + 0.5f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) word[0] |= q[i] << (4 * i);
-        word[1] = 0;
-    } else {
-        word[0] = q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24);
-        word[1] = q[4] | (q[5] << 8) | (q[6] << 16) | (q[7] << 24);
+            for (int i = 0; i < 8; ++i) {
+                const float2 f = __half22float2(h2[i]);
+                r[2 * i] = settle(f.x, mn, s, r[2 * i], kTop);
+                r[2 * i + 1] = settle(f.y, mn, s, r[2 * i + 1], kTop);
+            }
+        }
+        constexpr int kPer = 32 / BITS;                  // codes per word
+#pragma unroll
+        for (int i = 15; i >= 0; --i)
+            word[i / kPer] = word[i / kPer] * (1 << BITS) + (__float_as_uint(r[i] + kRound) & 0xffu);
     }
     const __half nan16 = __ushort_as_half((unsigned short)0x7fff);
     sb = bad ? __halves2half2(nan16, nan16) : __halves2half2(s16, __float2half_rn(mn));
 }
 
+// A thread's place in K's and V's heads, the same in every row it takes; threads of short
+// rows share a CTA's rows.
+struct Place {
+    int j, sub, step;       // place in the row, first row, rows apart
+    __device__ Place(int per_row) {
+        const int par = per_row >= kKvThreads ? 1 : kKvThreads / per_row;
+        sub = threadIdx.x / per_row;
+        j = threadIdx.x - sub * per_row;
+        step = par;
+        if (per_row >= kKvThreads) {
+            sub = 0;
+            j = threadIdx.x;
+        } else if (sub >= par) {
+            sub = 1 << 20;   // a thread left over
+        }
+    }
+};
+
 template <int BITS, int D>
-__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(kv::View c, Rows rows, int rows_per_cta,
-                                                               const __half* __restrict__ k, long long ldk,
-                                                               const __half* __restrict__ v, long long ldv) {
+__global__ void __launch_bounds__(kKvThreads, 4) kv_append_kernel(kv::View c, Rows rows, int rows_per_cta,
+                                                                  const __half* __restrict__ k, long long ldk,
+                                                                  const __half* __restrict__ v, long long ldv) {
     constexpr int kR = kv::row_bytes(BITS, D);
     __shared__ int cu_s[EDGE0_MAX_BATCHED + 1];
     __shared__ RowPlace place[kMaxRowsPerCta];
     const int r0 = blockIdx.x * rows_per_cta;
-    place_rows(c, rows, r0, rows_per_cta, cu_s, place);
-    const int per_row = 2 * c.H * (D / 8);          // threads' worth of work per row, a multiple of 8
-    const int n = rows_per_cta * per_row;
-    for (int i0 = 0; i0 < n; i0 += kKvThreads) {
-        const int i = i0 + threadIdx.x;
-        const int row = i < n ? i / per_row : 0, j = i < n ? i - row * per_row : 0;
-        const RowPlace p = place[row];
-        const bool live = i < n && p.page >= 0;     // the same for the 8 lanes of a group
-        const int which = j / (c.H * (D / 8)), hj = j - which * c.H * (D / 8);
-        const int h = hj / (D / 8), i8 = hj % (D / 8);
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (live)
-            raw = *reinterpret_cast<const uint4*>((which ? v + (r0 + row) * ldv : k + (r0 + row) * ldk) +
-                                                  (long long)h * D + 8 * i8);
-        uint32_t word[2];
+    const int n = min(rows_per_cta, rows.T - r0);
+    const int half_row = c.H * (D / 16), per_row = 2 * half_row;   // threads' worth of work per row
+    const Place me(per_row);
+    // steps: the rows, for one place in the row after the other; every thread of the CTA
+    // takes all of them (the quantiser's shuffles are the whole warp's)
+    const int per_place = (n + me.step - 1) / me.step;
+    const int steps = per_place * ((per_row + kKvThreads - 1) / kKvThreads);
+    auto fetch = [&](int j, int row, uint4 (&raw)[2]) {
+        raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
+        if (row < n && j < per_row) {
+            const int which = j >= half_row, hj = j - which * half_row;
+            const int dim = (hj / (D / 16)) * D + ((hj % (D / 16)) >> 2) * kGroup + (hj & 3) * 8;      // and dim + 32
+            const uint4* x = reinterpret_cast<const uint4*>((which ? v + (r0 + row) * ldv : k + (r0 + row) * ldk) + dim);
+            raw[0] = x[0];
+            raw[1] = x[4];
+        }
+    };
+    int j = me.j, row = me.sub;
+    uint4 next[2];
+    fetch(j, row, next);
+    place_rows(c, rows, r0, n, cu_s, place);
+    for (int i = 0, at_row = 0; i < steps; ++i) {
+        const uint4 raw[2] = {next[0], next[1]};
+        const int now_j = j, now_row = row;
+        row += me.step;
+        if (++at_row == per_place) {
+            at_row = 0;
+            row = me.sub;
+            j += kKvThreads;
+        }
+        if (i + 1 < steps) fetch(j, row, next);
+        uint32_t word[BITS / 2];
         __half2 sb;
-        quantise8<BITS>(raw, word, sb);
-        if (!live) continue;
-        char* half = strip_of<BITS, D>(c, p, h) + which * kv::half_bytes(BITS, D);
+        quantise16<BITS>(raw, word, sb);
+        if (now_row >= n || now_j >= per_row) continue;
+        const RowPlace p = place[now_row];
+        if (p.page < 0) continue;
+        const int which = now_j >= half_row, hj = now_j - which * half_row, h = hj / (D / 16), at = hj % (D / 16);
         const int rr = p.token % kv::kStrip;
-        const int off = i8 * BITS;                  // byte of the row
-        char* dst = half + rr * kR + (((off >> 4) ^ kv::turn(kR, rr)) << 4) + (off & 15);
-        if (BITS == 4) *reinterpret_cast<uint32_t*>(dst) = word[0];
-        else *reinterpret_cast<uint2*>(dst) = make_uint2(word[0], word[1]);
-        if (i8 % 8 == 0)
-            *reinterpret_cast<__half2*>(half + kv::kStrip * kR + rr * kv::sb_bytes(D) + (i8 / 8) * 4) = sb;
+        char* half = c.pages + p.page + ((long long)h * (c.page_tokens / kv::kStrip) + p.token / kv::kStrip) * kv::strip_bytes(BITS, D) +
+                     which * kv::half_bytes(BITS, D);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int off = ((at >> 2) * kGroup + (at & 3) * 8 + 32 * x) * BITS / 8;     // byte of the row of codes
+            char* dst = half + rr * kR + (((off >> 4) ^ kv::turn(kR, rr)) << 4) + (off & 15);
+            if (BITS == 4) *reinterpret_cast<uint32_t*>(dst) = word[x];
+            else *reinterpret_cast<uint2*>(dst) = make_uint2(word[2 * x], word[2 * x + 1]);
+        }
+        if (at % 4 == 0)
+            *reinterpret_cast<__half2*>(half + kv::kStrip * kR + rr * kv::sb_bytes(D) + (at / 4) * 4) = sb;
     }
 }
 
@@ -196,50 +250,61 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(kv::View c, Rows ro
     __shared__ RowPlace place[kMaxRowsPerCta];
     const int r0 = blockIdx.x * rows_per_cta;
     place_rows(c, rows, r0, rows_per_cta, cu_s, place);
-    const int per_row = 2 * c.H * (D / 8);
-    const int n = rows_per_cta * per_row;
-    for (int i = threadIdx.x; i < n; i += kKvThreads) {
-        const int row = i / per_row, j = i - row * per_row;
-        const RowPlace p = place[row];
-        if (p.page < 0) continue;
-        const int which = j / (c.H * (D / 8)), hj = j - which * c.H * (D / 8);
-        const int h = hj / (D / 8), i8 = hj % (D / 8);
-        const char* half = strip_of<BITS, D>(c, p, h) + which * kv::half_bytes(BITS, D);
-        const int rr = p.token % kv::kStrip;
-        const int off = i8 * BITS;
-        const char* src = half + rr * kR + (((off >> 4) ^ kv::turn(kR, rr)) << 4) + (off & 15);
-        uint32_t w0, w1 = 0;
-        if (BITS == 4) {
-            w0 = *reinterpret_cast<const uint32_t*>(src);
-        } else {
-            const uint2 w = *reinterpret_cast<const uint2*>(src);
-            w0 = w.x;
-            w1 = w.y;
-        }
-        const float2 sb = __half22float2(
-            *reinterpret_cast<const __half2*>(half + kv::kStrip * kR + rr * kv::sb_bytes(D) + (i8 / 8) * 4));
-        __half2 o[4];
+    const int half_row = c.H * (D / 8), per_row = 2 * half_row;
+    const Place me(per_row);
+    for (int j = me.j; j < per_row; j += kKvThreads) {
+        const int which = j >= half_row, hj = j - which * half_row, h = hj / (D / 8), at = hj % (D / 8);
+        __half* dst = (which ? v : k) + hj * 8;
+        const int off = at * BITS;
+        const char* head = c.pages + (long long)h * (c.page_tokens / kv::kStrip) * kv::strip_bytes(BITS, D) +
+                           which * kv::half_bytes(BITS, D);
+        for (int base = 0; base < rows_per_cta; base += kReadRows * me.step) {
+            uint32_t w[kReadRows][BITS / 4], sbw[kReadRows];
+            bool live[kReadRows];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t a, b;
-            if (BITS == 4) {
-                a = (w0 >> (8 * q)) & 15u;
-                b = (w0 >> (8 * q + 4)) & 15u;
-            } else {
-                const uint32_t w = q < 2 ? w0 : w1;
-                a = (w >> (16 * (q & 1))) & 255u;
-                b = (w >> (16 * (q & 1) + 8)) & 255u;
+            for (int u = 0; u < kReadRows; ++u) {
+                const int row = base + me.sub + u * me.step;
+                RowPlace p;
+                p.page = -1;
+                if (row < rows_per_cta) p = place[row];
+                live[u] = p.page >= 0;
+                if (live[u]) {
+                    const int rr = p.token % kv::kStrip;
+                    const char* half = head + p.page + (p.token / kv::kStrip) * kv::strip_bytes(BITS, D);
+                    const char* src = half + rr * kR + (((off >> 4) ^ kv::turn(kR, rr)) << 4) + (off & 15);
+                    if (BITS == 4) {
+                        w[u][0] = *reinterpret_cast<const uint32_t*>(src);
+                    } else {
+                        const uint2 x = *reinterpret_cast<const uint2*>(src);
+                        w[u][0] = x.x;
+                        w[u][BITS / 4 - 1] = x.y;
+                    }
+                    sbw[u] = *reinterpret_cast<const uint32_t*>(half + kv::kStrip * kR + rr * kv::sb_bytes(D) + (at / 8) * 4);
+                }
             }
-            o[q] = __floats2half2_rn(fmaf((float)a, sb.x, sb.y), fmaf((float)b, sb.x, sb.y));
+#pragma unroll
+            for (int u = 0; u < kReadRows; ++u) {
+                if (!live[u]) continue;
+                const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&sbw[u]));
+                uint4 o;
+                __half2* o2 = reinterpret_cast<__half2*>(&o);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    constexpr int kPer = 32 / BITS;
+                    const uint32_t x = w[u][2 * q / kPer] >> (2 * q % kPer * BITS);
+                    o2[q] = __floats2half2_rn(fmaf((float)(x & ((1 << BITS) - 1)), sb.x, sb.y),
+                                              fmaf((float)((x >> BITS) & ((1 << BITS) - 1)), sb.x, sb.y));
+                }
+                const int row = base + me.sub + u * me.step;
+                *reinterpret_cast<uint4*>(dst + (long long)(r0 + row) * (c.H * D)) = o;
+            }
         }
-        __half* out = (which ? v : k) + ((long long)(r0 + row) * c.H + h) * D + 8 * i8;
-        *reinterpret_cast<uint4*>(out) = *reinterpret_cast<uint4*>(o);
     }
 }
 
-// rows per CTA: about four CTAs per SM of a full card, at most kMaxRowsPerCta
+// rows per CTA: about eight CTAs per SM of a full card, at most kMaxRowsPerCta
 int rows_per_cta(int T) {
-    const int r = ceil_div(T, 152 * 4);
+    const int r = ceil_div(T, 152 * 8);
     return r < 1 ? 1 : r > kMaxRowsPerCta ? kMaxRowsPerCta : r;
 }
 
