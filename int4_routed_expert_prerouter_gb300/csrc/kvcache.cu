@@ -24,10 +24,10 @@ constexpr int kKvThreads = 256;
 constexpr int kMaxRowsPerCta = 32;
 constexpr int kReadRows = 4;         // rows that a reading thread has under way
 
-// Where the rows of a CTA go: byte offset of each row's page, its token in the page.
+// Where the rows of a CTA go.
 struct RowPlace {
-    long long page;   // byte offset of the page, or -1: nothing to do
-    int token;        // token within the page
+    long long strip;  // byte offset of the row's strip of head 0 in the pool, or -1: nothing to do
+    int row;          // row of the strip
 };
 
 struct Rows {
@@ -40,7 +40,8 @@ struct Rows {
 };
 
 // The places of rows r0 .. r0 + n - 1 (n <= kMaxRowsPerCta), by the whole CTA.
-__device__ void place_rows(const kv::View& c, const Rows& rows, int r0, int n, int* cu_s, RowPlace* out) {
+__device__ void place_rows(const kv::View& c, int strip_bytes, const Rows& rows, int r0, int n, int* cu_s,
+                           RowPlace* out) {
     if (rows.cu) {
         for (int i = threadIdx.x; i <= rows.B; i += kKvThreads) cu_s[i] = rows.cu[i];
         __syncthreads();
@@ -48,8 +49,8 @@ __device__ void place_rows(const kv::View& c, const Rows& rows, int r0, int n, i
     if (threadIdx.x < n) {
         const int r = r0 + threadIdx.x;
         RowPlace p;
-        p.page = -1;
-        p.token = 0;
+        p.strip = -1;
+        p.row = 0;
         int b = r;
         long long pos = 0;
         bool in = r < rows.T;
@@ -72,8 +73,9 @@ __device__ void place_rows(const kv::View& c, const Rows& rows, int r0, int n, i
                 int id = -1;
                 if (pos >= 0 && pg < rows.W) id = rows.table[(long long)b * rows.W + pg];
                 if (id >= 0 && id < c.n_pages) {
-                    p.page = (long long)id * c.page_bytes;
-                    p.token = (int)(pos - pg * c.page_tokens);
+                    const int token = (int)(pos - pg * c.page_tokens);
+                    p.strip = (long long)id * c.page_bytes + (long long)(token / kv::kStrip) * strip_bytes;
+                    p.row = token % kv::kStrip;
                 } else if (rows.status) {
                     atomicExch(rows.status, EDGE0_EINVAL);
                 }
@@ -82,13 +84,6 @@ __device__ void place_rows(const kv::View& c, const Rows& rows, int r0, int n, i
         out[threadIdx.x] = p;
     }
     __syncthreads();
-}
-
-// byte address of the strip of (head h, token) in its page
-template <int BITS, int D>
-__device__ __forceinline__ char* strip_of(const kv::View& c, const RowPlace& p, int h) {
-    return c.pages + p.page +
-           ((long long)h * (c.page_tokens / kv::kStrip) + p.token / kv::kStrip) * kv::strip_bytes(BITS, D);
 }
 
 // q of one value where the fp32 product may lie next to a border, or above the top code
@@ -135,29 +130,32 @@ __device__ __forceinline__ void quantise16(const uint4 (&raw)[2], uint32_t (&wor
     if (!bad && s != 0.f) {
         float inv;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-        float r[16], off = 0.f;
+        float t[16], off = 0.f;                          // kRound + q
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float2 f = __half22float2(h2[i]);
             const float d0 = f.x - mn, d1 = f.y - mn;
-            r[2 * i] = fmaf(d0, inv, kRound) - kRound;
-            r[2 * i + 1] = fmaf(d1, inv, kRound) - kRound;
-            off = fmaxf(off, fmaxf(fabsf(fmaf(-r[2 * i], s, d0)), fabsf(fmaf(-r[2 * i + 1], s, d1))));
+            t[2 * i] = fmaf(d0, inv, kRound);
+            t[2 * i + 1] = fmaf(d1, inv, kRound);
+            off = fmaxf(off, fmaxf(fabsf(fmaf(kRound - t[2 * i], s, d0)), fabsf(fmaf(kRound - t[2 * i + 1], s, d1))));
         }
-        // r is settled unless a residual comes to half a step (the residuals are off by at most
+        // q is settled unless a residual comes to half a step (the residuals are off by at most
         // the rounding of d, 255 x 2^-24 of a step)
         if (off > 0.49998f * s || range * inv > kTop + 0.5f) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float2 f = __half22float2(h2[i]);
-                r[2 * i] = settle(f.x, mn, s, r[2 * i], kTop);
-                r[2 * i + 1] = settle(f.y, mn, s, r[2 * i + 1], kTop);
+                t[2 * i] = settle(f.x, mn, s, t[2 * i] - kRound, kTop) + kRound;
+                t[2 * i + 1] = settle(f.y, mn, s, t[2 * i + 1] - kRound, kTop) + kRound;
             }
         }
+        // the low bits of t are q; what its high bits add up to in a word comes off at the end
         constexpr int kPer = 32 / BITS;                  // codes per word
+        constexpr uint32_t kHigh = 0x4B400000u * (BITS == 4 ? 0x11111111u : 0x01010101u);
 #pragma unroll
-        for (int i = 15; i >= 0; --i)
-            word[i / kPer] = word[i / kPer] * (1 << BITS) + (__float_as_uint(r[i] + kRound) & 0xffu);
+        for (int i = 15; i >= 0; --i) word[i / kPer] = word[i / kPer] * (1 << BITS) + __float_as_uint(t[i]);
+#pragma unroll
+        for (int i = 0; i < BITS / 2; ++i) word[i] -= kHigh;
     }
     const __half nan16 = __ushort_as_half((unsigned short)0x7fff);
     sb = bad ? __halves2half2(nan16, nan16) : __halves2half2(s16, __float2half_rn(mn));
@@ -192,53 +190,51 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv_append_kernel(kv::View c, Ro
     const int n = min(rows_per_cta, rows.T - r0);
     const int half_row = c.H * (D / 16), per_row = 2 * half_row;   // threads' worth of work per row
     const Place me(per_row);
-    // steps: the rows, for one place in the row after the other; every thread of the CTA
-    // takes all of them (the quantiser's shuffles are the whole warp's)
-    const int per_place = (n + me.step - 1) / me.step;
-    const int steps = per_place * ((per_row + kKvThreads - 1) / kKvThreads);
-    auto fetch = [&](int j, int row, uint4 (&raw)[2]) {
-        raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
-        if (row < n && j < per_row) {
-            const int which = j >= half_row, hj = j - which * half_row;
-            const int dim = (hj / (D / 16)) * D + ((hj % (D / 16)) >> 2) * kGroup + (hj & 3) * 8;      // and dim + 32
-            const uint4* x = reinterpret_cast<const uint4*>((which ? v + (r0 + row) * ldv : k + (r0 + row) * ldk) + dim);
-            raw[0] = x[0];
-            raw[1] = x[4];
-        }
-    };
-    int j = me.j, row = me.sub;
-    uint4 next[2];
-    fetch(j, row, next);
-    place_rows(c, rows, r0, n, cu_s, place);
-    for (int i = 0, at_row = 0; i < steps; ++i) {
-        const uint4 raw[2] = {next[0], next[1]};
-        const int now_j = j, now_row = row;
-        row += me.step;
-        if (++at_row == per_place) {
-            at_row = 0;
-            row = me.sub;
-            j += kKvThreads;
-        }
-        if (i + 1 < steps) fetch(j, row, next);
-        uint32_t word[BITS / 2];
-        __half2 sb;
-        quantise16<BITS>(raw, word, sb);
-        if (now_row >= n || now_j >= per_row) continue;
-        const RowPlace p = place[now_row];
-        if (p.page < 0) continue;
-        const int which = now_j >= half_row, hj = now_j - which * half_row, h = hj / (D / 16), at = hj % (D / 16);
-        const int rr = p.token % kv::kStrip;
-        char* half = c.pages + p.page + ((long long)h * (c.page_tokens / kv::kStrip) + p.token / kv::kStrip) * kv::strip_bytes(BITS, D) +
+    const int last = (per_row + kKvThreads - 1) / kKvThreads * kKvThreads;     // whole warps: the quantiser's shuffles
+    bool placed = false;
+    for (int j = me.j; j < last; j += kKvThreads) {
+        const int which = j >= half_row, hj = j - which * half_row, h = hj / (D / 16), at = hj % (D / 16);
+        const int dim = (at >> 2) * kGroup + (at & 3) * 8;                     // and dim + 32
+        const long long ld = which ? ldv : ldk;
+        const __half* src = (which ? v : k) + (long long)r0 * ld + h * D + dim;
+        char* head = c.pages + (long long)h * (c.page_tokens / kv::kStrip) * kv::strip_bytes(BITS, D) +
                      which * kv::half_bytes(BITS, D);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int off = ((at >> 2) * kGroup + (at & 3) * 8 + 32 * x) * BITS / 8;     // byte of the row of codes
-            char* dst = half + rr * kR + (((off >> 4) ^ kv::turn(kR, rr)) << 4) + (off & 15);
-            if (BITS == 4) *reinterpret_cast<uint32_t*>(dst) = word[x];
-            else *reinterpret_cast<uint2*>(dst) = make_uint2(word[2 * x], word[2 * x + 1]);
+        const int off0 = dim * BITS / 8, off1 = (dim + 32) * BITS / 8;         // bytes of the row of codes
+        auto fetch = [&](int row, uint4 (&raw)[2]) {
+            raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
+            if (row < n && j < per_row) {
+                const uint4* x = reinterpret_cast<const uint4*>(src + row * ld);
+                raw[0] = x[0];
+                raw[1] = x[4];
+            }
+        };
+        uint4 next[2];
+        fetch(me.sub, next);
+        if (!placed) place_rows(c, kv::strip_bytes(BITS, D), rows, r0, n, cu_s, place);
+        placed = true;
+        for (int base = 0; base < n; base += me.step) {
+            const int row = base + me.sub;
+            const uint4 raw[2] = {next[0], next[1]};
+            if (base + me.step < n) fetch(row + me.step, next);
+            uint32_t word[BITS / 2];
+            __half2 sb;
+            quantise16<BITS>(raw, word, sb);
+            if (row >= n || j >= per_row) continue;
+            const RowPlace p = place[row];
+            if (p.strip < 0) continue;
+            char* half = head + p.strip;
+            char* codes = half + p.row * kR;
+            const int turn = kv::turn(kR, p.row) << 4;
+            if (BITS == 4) {
+                *reinterpret_cast<uint32_t*>(codes + (off0 ^ turn)) = word[0];
+                *reinterpret_cast<uint32_t*>(codes + (off1 ^ turn)) = word[1];
+            } else {
+                *reinterpret_cast<uint2*>(codes + (off0 ^ turn)) = make_uint2(word[0], word[1]);
+                *reinterpret_cast<uint2*>(codes + (off1 ^ turn)) = make_uint2(word[BITS / 2 - 2], word[BITS / 2 - 1]);
+            }
+            if (at % 4 == 0)
+                *reinterpret_cast<__half2*>(half + kv::kStrip * kR + p.row * kv::sb_bytes(D) + (at / 4) * 4) = sb;
         }
-        if (at % 4 == 0)
-            *reinterpret_cast<__half2*>(half + kv::kStrip * kR + rr * kv::sb_bytes(D) + (at / 4) * 4) = sb;
     }
 }
 
@@ -249,7 +245,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(kv::View c, Rows ro
     __shared__ int cu_s[EDGE0_MAX_BATCHED + 1];
     __shared__ RowPlace place[kMaxRowsPerCta];
     const int r0 = blockIdx.x * rows_per_cta;
-    place_rows(c, rows, r0, rows_per_cta, cu_s, place);
+    place_rows(c, kv::strip_bytes(BITS, D), rows, r0, rows_per_cta, cu_s, place);
     const int half_row = c.H * (D / 8), per_row = 2 * half_row;
     const Place me(per_row);
     for (int j = me.j; j < per_row; j += kKvThreads) {
@@ -265,13 +261,13 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(kv::View c, Rows ro
             for (int u = 0; u < kReadRows; ++u) {
                 const int row = base + me.sub + u * me.step;
                 RowPlace p;
-                p.page = -1;
+                p.strip = -1;
                 if (row < rows_per_cta) p = place[row];
-                live[u] = p.page >= 0;
+                live[u] = p.strip >= 0;
                 if (live[u]) {
-                    const int rr = p.token % kv::kStrip;
-                    const char* half = head + p.page + (p.token / kv::kStrip) * kv::strip_bytes(BITS, D);
-                    const char* src = half + rr * kR + (((off >> 4) ^ kv::turn(kR, rr)) << 4) + (off & 15);
+                    const int rr = p.row;
+                    const char* half = head + p.strip;
+                    const char* src = half + rr * kR + (off ^ (kv::turn(kR, rr) << 4));
                     if (BITS == 4) {
                         w[u][0] = *reinterpret_cast<const uint32_t*>(src);
                     } else {
