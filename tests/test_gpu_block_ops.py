@@ -490,7 +490,9 @@ def test_decode_steps_of_a_block_eager_and_captured(bits):
     assert cache.error() == 0
     # step by step against the plain forms, fed with what the pages hold
     got_k, got_v = binding.kv_read(cache, table, i32(np.zeros(B)), i32(np.arange(B + 1) * steps), B * steps)
-    rows = binding.q4_linear(w["qkv"], (H * G + 2 * H) * D, hs.flatten(0, 1)).view(steps, B, -1).cpu().numpy()
+    # (the steps' own calls again: another number of rows adds its fp32 sums up in another order, and a sum
+    # next to a border of fp16 may then round to the other side)
+    rows = torch.stack([binding.q4_linear(w["qkv"], (H * G + 2 * H) * D, hs[t]) for t in range(steps)]).cpu().numpy()
     for t in (0, 1, steps - 1):
         want = hs[t].cpu().numpy().astype(np.float64) @ Wqkv.T
         b1 = q4_bound(pqkv, hs[t].cpu().numpy().astype(np.float64), want, d)
