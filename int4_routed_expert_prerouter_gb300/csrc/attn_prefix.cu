@@ -6,16 +6,22 @@
 //   warps 8-11  turn a strip of codes each into fp16 (code - z, z half the code range: exact)
 //               in shared memory, K as K-major, V as MN-major operand tiles, and its scales
 //               into fp32 tables; the next step's codes are loaded into registers meanwhile;
-//   thread 0    issues S_g = Q_g K_g^T per 64 dims g, and once the weights are there
-//               O_g += P'_g V_g; accumulators and P' (over S, which is read by then) in TMEM;
-//   warps 0-7   two threads per row, 32 tokens each: S = sum_g s_g S_g + (b_g + z s_g) sum Q_g,
-//               running maximum and sum, weights p, P'_g = fp16(p s_g), and
-//               sum_j p (b_g + z s_g) in fp32.
-// So the scores carry no rounding of K, and each weight is rounded once (to fp16, 2^-11 of
-// itself).  o = (O_g + sum p (b_g + z s_g)) / sum p.  The exponents' reference is the
-// running maximum plus the exponent of the largest scale so far, so that p s stays within
+//   thread 0    issues the scores' products, and once the weights are there O_g += P'_g V_g for
+//               each 64 dims g; accumulators and P' (over the scores, which are read by
+//               then) in TMEM;
+//   warps 0-7   32 rows x 32 tokens each: S, running maximum and sum, weights p,
+//               P'_g = fp16(p s_g), and sum_j p (b_g + z s_g) in fp32.
+// Scores: with K = s (code - z + r), r = b / s + z, a group's product is
+// Q_g (code - z) + mean(Q_g) 64 r; the second term is one more step of 16 of the same
+// product, its factors split into two fp16 each, so that S = sum_g s_g S_g carries no
+// rounding of K beyond 2^-22.  Each weight is rounded once (to fp16, 2^-11 of itself).
+// o = (O_g + sum p (b_g + z s_g)) / sum p.  The exponents' reference is the running
+// maximum plus the exponent of the largest scale so far, so that p s stays within
 // fp16's normal range whatever the scales; it moves only when a score exceeds it by
 // 2^8 or a scale by 2^6, and the accumulators are then rescaled in TMEM.
+// The accumulators are read and P' written as 8-column fragments (a lane: 2 tokens of
+// 4 rows): a token's scales, read from shared memory, serve 4 rows; with a row per
+// thread reading them alone took 2000 cycles a step.
 // Two CTAs per SM (D <= 128): one's tensor steps run under the other's softmax.
 #include "attn.cuh"
 #include "tc05.cuh"
@@ -37,10 +43,12 @@ struct Cfg {
     static constexpr int HALF = kv::half_bytes(BITS, D);
     static constexpr int NP = CH / 2;                       // 16-byte pieces of K (and of V) per thread and step
     static constexpr int kQ = kRowsQ * D * 2;
+    static constexpr int kMean = GR * kRowsQ * 32;          // means of Q_g, a step of 16 each
     static constexpr int kOp = kTile * D * 2;               // one operand tile
-    static constexpr int kTab = 4 * GR * kTile * 4;         // K s, K c, V s, V c
-    static constexpr int kStage = 2 * kOp + kTab;
-    static constexpr int kSmem = kQ + 2 * kStage;
+    static constexpr int kOffs = kTile * 32;                // r of the tile's tokens, a step of 16
+    static constexpr int kTab = 3 * GR * kTile * 4;         // K s; V (s, b + z s)
+    static constexpr int kStage = 2 * kOp + kOffs + kTab;
+    static constexpr int kSmem = kQ + kMean + 2 * kStage;
     static constexpr int kCols = GR * kTile + D <= 128 ? 128 : GR * kTile + D <= 256 ? 256 : 512;
     static constexpr int kCtas = D <= 128 ? 2 : 1;
 };
@@ -69,23 +77,26 @@ __device__ __forceinline__ f2 add2(f2 a, f2 b) {
     return r;
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
+// 16 rows x 32 columns of fp32: lane (g, t) = (lane / 4, lane % 4) holds of each 8-column block
+// columns 2t, 2t + 1 of row g (r[4j], r[4j + 1]) and of row g + 8 (r[4j + 2], r[4j + 3])
+__device__ __forceinline__ void tmem_ld_frag(uint32_t a, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(a)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st_frag(uint32_t a, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(a),
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(a),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(a), "r"(r[0]), "r"(r[1]),
+// 16 rows x 32 columns of fp16 in pairs: of each 8-column block row g (r[2j]) and row g + 8 (r[2j + 1])
+__device__ __forceinline__ void tmem_st_pairs(uint32_t a, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(a), "r"(r[0]), "r"(r[1]),
                  "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
@@ -120,24 +131,34 @@ __device__ __forceinline__ bool any_softmax(bool want) {
     return r != 0;
 }
 
-// codes of 8 dims less z as fp16; 4 bits: one word, dims in the order 0 4 1 5 2 6 3 7;
-// 8 bits: two words, in order
-template <int BITS>
+// codes of 8 dims less z as fp16 (of K times 2^-10); 4 bits: one word, dims in the order
+// 0 4 1 5 2 6 3 7; 8 bits: two words, in order.  0x6400 is 1024: a code below it adds itself,
+// a nibble 4 bits up 16 times itself.
+template <int BITS, bool K>
 __device__ __forceinline__ uint4 codes8(uint32_t w0, uint32_t w1) {
     uint4 r;
     if (BITS == 4) {
+        constexpr uint32_t m0 = K ? 0x14001400u : 0x3C003C00u, a0 = K ? 0xBC08BC08u : 0xE408E408u;   // 2^-10 | 1
+        constexpr uint32_t m1 = K ? 0x04000400u : 0x2C002C00u, a1 = K ? 0xAC80AC80u : 0xD480D480u;   // 2^-14 | 2^-4
         const uint32_t h = w0 >> 8;
-        r.x = hadd2((w0 & 0x000F000Fu) | 0x64006400u, 0xE408E408u);                  // 1024 + n - 1032
-        r.y = hfma2((w0 & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);     // (1024 + 16 n) / 16 - 72
-        r.z = hadd2((h & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
-        r.w = hfma2((h & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+        r.x = hfma2((w0 & 0x000F000Fu) | 0x64006400u, m0, a0);
+        r.y = hfma2((w0 & 0x00F000F0u) | 0x64006400u, m1, a1);
+        r.z = hfma2((h & 0x000F000Fu) | 0x64006400u, m0, a0);
+        r.w = hfma2((h & 0x00F000F0u) | 0x64006400u, m1, a1);
     } else {
-        r.x = hadd2(__byte_perm(w0, 0x64646464u, 0x4140), 0xE480E480u);              // 1024 + n - 1152
-        r.y = hadd2(__byte_perm(w0, 0x64646464u, 0x4342), 0xE480E480u);
-        r.z = hadd2(__byte_perm(w1, 0x64646464u, 0x4140), 0xE480E480u);
-        r.w = hadd2(__byte_perm(w1, 0x64646464u, 0x4342), 0xE480E480u);
+        constexpr uint32_t m = K ? 0x14001400u : 0x3C003C00u, a = K ? 0xBC80BC80u : 0xE480E480u;
+        r.x = hfma2(__byte_perm(w0, 0x64646464u, 0x4140), m, a);
+        r.y = hfma2(__byte_perm(w0, 0x64646464u, 0x4342), m, a);
+        r.z = hfma2(__byte_perm(w1, 0x64646464u, 0x4140), m, a);
+        r.w = hfma2(__byte_perm(w1, 0x64646464u, 0x4342), m, a);
     }
     return r;
+}
+// v = hi + lo 2^-11-ish: two fp16 in one word
+__device__ __forceinline__ uint32_t split(float v) {
+    const __half hi = __float2half_rn(v);
+    const __half2 r = __halves2half2(hi, __float2half_rn(v - __half2float(hi)));
+    return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 // Waits for a phase of a barrier; gives up after kDefaultWaitNs or when another thread did.
@@ -160,12 +181,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
     using X = Cfg<BITS, D>;
     constexpr int GR = X::GR;
     constexpr float kZ = BITS == 4 ? 8.f : 128.f;
-    extern __shared__ __align__(1024) char smem[];
+    extern __shared__ __align__(128) char smem[];
     __shared__ uint64_t full[2], freed[2], s_ready;
     __shared__ uint32_t taddr_s;
     __shared__ int dead;
-    __shared__ float part_max[2][kRowsQ], part_sum[2][1 + GR][kRowsQ];
-    char* sQ = smem;
+    __shared__ float part_max[2][kRowsQ];
+    char *sQ = smem, *sM = smem + X::kQ, *stages = sM + X::kMean;
     const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
     const int h = blockIdx.z, rb = blockIdx.y;
     const int t0 = blockIdx.x * p.tiles_per_split;
@@ -201,8 +222,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             }
             *reinterpret_cast<uint4*>(sQ + (c8 >> 1) * (kRowsQ * 32) + tc::kstep_off(r, (c8 & 1) * 8)) = v;
         }
-        tc::fence_async_smem();
+        // means' and offsets' tiles: zero where nothing is written below
+        for (int i = tid; i < X::kMean / 16; i += kSoftmax) reinterpret_cast<uint4*>(sM)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < X::kOffs / 16; i += kSoftmax)
+            for (int s = 0; s < 2; ++s)
+                reinterpret_cast<uint4*>(stages + s * X::kStage + 2 * X::kOp)[i] = make_uint4(0, 0, 0, 0);
+        named_bar_sync(2, kSoftmax);
+        for (int i = tid; i < kRowsQ * GR; i += kSoftmax) {
+            const int r = i % kRowsQ, gr = i / kRowsQ;
+            float s = 0.f;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const int c8 = gr * 8 + c;
+                const uint4 v = *reinterpret_cast<const uint4*>(sQ + (c8 >> 1) * (kRowsQ * 32) + tc::kstep_off(r, (c8 & 1) * 8));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+                    s += f.x + f.y;
+                }
+            }
+            const uint32_t hl = split(s * (1.f / kGroup));     // (hi, lo), against (hi, hi, lo, lo) of r
+            *reinterpret_cast<uint2*>(sM + gr * (kRowsQ * 32) + tc::kstep_off(r, 4 * gr)) = make_uint2(hl, hl);
+        }
     }
+    tc::fence_async_smem();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -210,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
 
     if (wid >= 8) {
         // ---------------------------------------------------------- operands
+        if (X::kCtas == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
         const int w = wid - 8;                                 // strip of the tile
         const int spp = p.c.page_tokens / kv::kStrip;
         const int last_strip = (p.n_tok - 1) / kv::kStrip;
@@ -255,9 +300,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             id = page_of();
         };
         auto put = [&](int i) {
-            char* stage = smem + X::kQ + (i & 1) * X::kStage;
-            char *sK = stage, *sV = stage + X::kOp;
-            float* tab = reinterpret_cast<float*>(stage + 2 * X::kOp);
+            char* stage = stages + (i & 1) * X::kStage;
+            char *sK = stage, *sV = stage + X::kOp, *sR = stage + 2 * X::kOp;
+            float* tab_k = reinterpret_cast<float*>(sR + X::kOffs);
+            float* tab_v = tab_k + GR * kTile;
 #pragma unroll
             for (int j = 0; j < X::NP; ++j) {
                 const int q = j * 32 + lane, c = (q >> 3) % X::CH, tok = 16 * w + (q & 7) + 8 * ((q >> 3) / X::CH);
@@ -267,9 +313,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                 for (int x = 0; x < 4 / kW; ++x) {
                     const int c8 = c * (4 / kW) + x;           // 8 dims
                     *reinterpret_cast<uint4*>(sK + (c8 >> 1) * (kTile * 32) + tc::kstep_off(tok, (c8 & 1) * 8)) =
-                        codes8<BITS>(k4[x * kW], k4[x * kW + kW - 1]);
+                        codes8<BITS, true>(k4[x * kW], k4[x * kW + kW - 1]);
                     *reinterpret_cast<uint4*>(sV + c8 * (kTile * 16) + tok * 16) =
-                        codes8<BITS>(v4[x * kW], v4[x * kW + kW - 1]);
+                        codes8<BITS, false>(v4[x * kW], v4[x * kW + kW - 1]);
                 }
             }
             const int left = p.n_tok - (t0 + i) * kTile;
@@ -278,9 +324,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                 const int q = j * 32 + lane, v = q >= 16 * GR ? 1 : 0, e = q - v * 16 * GR;
                 const int tok = 16 * w + e / GR, gr = e % GR;
                 float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&rs[j]));
-                if (tok >= left) sb = make_float2(0.f, 0.f);
-                tab[(2 * v * GR + gr) * kTile + tok] = sb.x;
-                tab[((2 * v + 1) * GR + gr) * kTile + tok] = fmaf(sb.x, kZ, sb.y);
+                const bool none = tok >= left;
+                if (v) {
+                    float* at = tab_v + ((tok >> 1) * GR + gr) * 4 + (tok & 1);
+                    at[0] = none ? 0.f : sb.x;
+                    at[2] = none ? 0.f : fmaf(sb.x, kZ, sb.y);
+                } else {
+                    // a constant group (s = 0, codes 0): b = 1 (0 - z + b + z)
+                    const bool flat = sb.x == 0.f;
+                    const float off = flat ? sb.y + kZ : __fdividef(sb.y, sb.x) + kZ;
+                    tab_k[(tok >> 1) * 2 * GR + 2 * gr + (tok & 1)] = none ? 0.f : (flat ? 1.f : sb.x) * p.k * 1024.f;
+                    const uint32_t hl = split(none ? 0.f : off * (kGroup / 1024.f));
+                    *reinterpret_cast<uint2*>(sR + tc::kstep_off(tok, 4 * gr)) =
+                        make_uint2(__byte_perm(hl, hl, 0x1010), __byte_perm(hl, hl, 0x3232));
+                }
             }
             tc::fence_async_smem();
             __syncwarp();
@@ -294,168 +351,184 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
         }
     } else {
         // ----------------------------------------------------------- softmax
-        const int hf = wid >> 2, quad = wid & 3;               // 32 tokens, 32 rows
+        // 128 x 64 + 256 x 88 registers: what the CTA was launched with (384 x 80)
+        if (X::kCtas == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;\n");
+        const int hf = wid >> 2, quad = wid & 3, g = lane >> 2, t = lane & 3;      // 32 tokens, 32 rows
         const uint32_t my = tm + ((uint32_t)(32 * quad) << 16);
-        const int row = 32 * quad + lane;
-        f2 qs[GR];
+        // rows 32 quad + 16 rh + g + 8 k, index 2 rh + k; weight of a score: 2^(S - mu), S in
+        // exponent units, mu the running maximum plus e, 2^e the scales'
+        float mu[4], l[4], beta[4][GR], e = 0.f, thr_s = 0.f;
 #pragma unroll
-        for (int gr = 0; gr < GR; ++gr) {
-            float s = 0.f;
+        for (int r = 0; r < 4; ++r) {
+            mu[r] = l[r] = 0.f;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const int c8 = gr * 8 + c;
-                const uint4 v = *reinterpret_cast<const uint4*>(sQ + (c8 >> 1) * (kRowsQ * 32) +
-                                                                tc::kstep_off(row, (c8 & 1) * 8));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-                    s += f.x + f.y;
-                }
-            }
-            qs[gr] = pk(s, s);
+            for (int gr = 0; gr < GR; ++gr) beta[r][gr] = 0.f;
         }
-        // exponent of a score: k S - mu, mu = k m + e; m the running maximum, 2^e the scales'
-        float m = -INFINITY, thr = -INFINITY, e = 0.f, thr_s = 0.f, mu = 0.f;
-        f2 l2 = 0, beta[GR];
-#pragma unroll
-        for (int gr = 0; gr < GR; ++gr) beta[gr] = 0;
-        const f2 k2 = pk(p.k, p.k);
-        auto issue_scores = [&](int i) {                       // thread 0: S = Q K^T of tile i
-            const uint32_t sK = desc_lo(smem_u32(smem + X::kQ + (i & 1) * X::kStage), tc::kLbo);
-            const uint32_t a0 = desc_lo(smem_u32(sQ), tc::kLbo);
+        auto issue_scores = [&](int i) {                       // thread 0: the products of tile i
+            const uint32_t k0 = smem_u32(stages + (i & 1) * X::kStage);
+            const uint32_t sK = desc_lo(k0, tc::kLbo), sR = desc_lo(k0 + 2 * X::kOp, tc::kLbo);
+            const uint32_t a0 = desc_lo(smem_u32(sQ), tc::kLbo), m0 = desc_lo(smem_u32(sM), tc::kLbo);
             if (!wait_bar(&full[i & 1], (i >> 1) & 1, &dead)) return;
             tc::fence_after_sync();
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                tc::mma_f16(tm + (ks / 4) * kTile, desc(a0 + ks * (kRowsQ * 32 / 16), tc::kSbo),
-                            desc(sK + ks * (kTile * 32 / 16), tc::kSbo), tc::idesc_f16(kRowsQ, kTile), ks % 4 != 0);
+            for (int gr = 0; gr < GR; ++gr) {
+#pragma unroll
+                for (int ks = 4 * gr; ks < 4 * gr + 4; ++ks)
+                    tc::mma_f16(tm + gr * kTile, desc(a0 + ks * (kRowsQ * 32 / 16), tc::kSbo),
+                                desc(sK + ks * (kTile * 32 / 16), tc::kSbo), tc::idesc_f16(kRowsQ, kTile), ks % 4 != 0);
+                tc::mma_f16(tm + gr * kTile, desc(m0 + gr * (kRowsQ * 32 / 16), tc::kSbo), desc(sR, tc::kSbo),
+                            tc::idesc_f16(kRowsQ, kTile), true);
+            }
             tc::mma_commit(&s_ready);
         };
         if (tid == 0) issue_scores(0);
         __syncwarp();
         bool ok = true;
         for (int i = 0; i < n; ++i) {
-            const char* stage = smem + X::kQ + (i & 1) * X::kStage;
-            const float* tab = reinterpret_cast<const float*>(stage + 2 * X::kOp);
-            const float* mine = tab + hf * 32;
+            const char* stage = stages + (i & 1) * X::kStage;
+            const float* tab_k = reinterpret_cast<const float*>(stage + 2 * X::kOp + X::kOffs);
+            const float* tab_v = tab_k + GR * kTile;
+            const float* mk = tab_k + (hf * 16 + t) * 2 * GR;      // this lane's pairs of tokens, 4 apart
+            const float* mv = tab_v + (hf * 16 + t) * 4 * GR;
             // (after a wait that gave up the rest runs through without waiting: the warps
             // meet at barriers in every step)
             ok = wait_bar(&full[i & 1], (i >> 1) & 1, &dead) && wait_bar(&s_ready, i & 1, &dead);
             __syncwarp();
             tc::fence_after_sync();
-            // 16 tokens of one group at a time, the next ones under way meanwhile
-            f2 S[16];
-            uint32_t raw[2][16];
-            tmem_ld16(my + hf * 32, raw[0]);
-            float top_s = fmaxf(tab[2 * GR * kTile + lane], tab[2 * GR * kTile + lane + 32]);
+            float top_s = 0.f;
 #pragma unroll
-            for (int gr = 1; gr < GR; ++gr)
-                top_s = fmaxf(top_s, fmaxf(tab[(2 * GR + gr) * kTile + lane], tab[(2 * GR + gr) * kTile + lane + 32]));
-            tc::tmem_wait_ld();
+            for (int gr = 0; gr < GR; ++gr) {
+                const float2 v = *reinterpret_cast<const float2*>(tab_v + (lane * GR + gr) * 4);
+                top_s = fmaxf(top_s, fmaxf(v.x, v.y));
+            }
+            f2 S[2][4][2];                                     // [rh][8 tokens][k]: tokens 2t, 2t + 1
+            const int left = p.n_tok - (t0 + i) * kTile - hf * 32 - 2 * t;     // of this lane's tokens
+            float mx[4];
 #pragma unroll
-            for (int q = 0; q < GR * 2; ++q) {
-                const int c = q / GR, gr = q % GR;
-                if (q + 1 < GR * 2) tmem_ld16(my + ((q + 1) % GR) * kTile + hf * 32 + ((q + 1) / GR) * 16, raw[(q + 1) & 1]);
-                const uint32_t(&a)[16] = raw[q & 1];
-                const ulonglong2* ks = reinterpret_cast<const ulonglong2*>(mine + gr * kTile + c * 16);
-                const ulonglong2* kc = reinterpret_cast<const ulonglong2*>(mine + (GR + gr) * kTile + c * 16);
+            for (int rh = 0; rh < 2; ++rh) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const ulonglong2 s4 = ks[j], c4 = kc[j];
-                    const f2 x0 = pk(__uint_as_float(a[4 * j]), __uint_as_float(a[4 * j + 1]));
-                    const f2 x1 = pk(__uint_as_float(a[4 * j + 2]), __uint_as_float(a[4 * j + 3]));
-                    f2& d0 = S[c * 8 + 2 * j];
-                    f2& d1 = S[c * 8 + 2 * j + 1];
-                    d0 = fma2(x0, s4.x, gr ? fma2(c4.x, qs[gr], d0) : mul2(c4.x, qs[gr]));
-                    d1 = fma2(x1, s4.y, gr ? fma2(c4.y, qs[gr], d1) : mul2(c4.y, qs[gr]));
+                for (int gr = 0; gr < GR; ++gr) {
+                    uint32_t raw[16];
+                    tmem_ld_frag(my + ((uint32_t)(16 * rh) << 16) + gr * kTile + hf * 32, raw);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const f2 s2 = *reinterpret_cast<const f2*>(mk + j * 8 * GR + 2 * gr);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const f2 x = pk(__uint_as_float(raw[4 * j + 2 * k]), __uint_as_float(raw[4 * j + 2 * k + 1]));
+                            S[rh][j][k] = fma2(x, s2, gr ? S[rh][j][k] : pk(-mu[2 * rh + k], -mu[2 * rh + k]));
+                        }
+                    }
                 }
-                if (q + 1 < GR * 2) tc::tmem_wait_ld();
-            }
-            const int left = p.n_tok - (t0 + i) * kTile - hf * 32;
-            if (left < 32) {
+                if (left < 26) {                               // tokens behind the last
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float a, b;
-                    unpk(S[j], a, b);
-                    S[j] = pk(2 * j < left ? a : -INFINITY, 2 * j + 1 < left ? b : -INFINITY);
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float a, b;
+                            unpk(S[rh][j][k], a, b);
+                            S[rh][j][k] = pk(8 * j < left ? a : -INFINITY, 8 * j + 1 < left ? b : -INFINITY);
+                        }
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float a[4], b[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) unpk(S[rh][j][k], a[j], b[j]);
+                    mx[2 * rh + k] = fmaxf(fmaxf(fmaxf(a[0], b[0]), fmaxf(a[1], b[1])), fmaxf(fmaxf(a[2], b[2]), fmaxf(a[3], b[3])));
                 }
             }
-            float mx4[4];
+            const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // (this barrier also ends every read of the scores before P' goes over them)
+            if (any_softmax(i == 0 || most > 8.f - e || top_s > thr_s)) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mx4[j] = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                float a, b;
-                unpk(S[j], a, b);
-                mx4[j & 3] = fmaxf(mx4[j & 3], fmaxf(a, b));
-            }
-            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-            // (this barrier also ends every read of S before P' goes over it)
-            if (any_softmax(mx > thr || top_s > thr_s)) {
-                part_max[hf][row] = mx;
+                for (int r = 0; r < 4; ++r) {
+                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+                    if (t == 0) part_max[hf][32 * quad + 16 * (r >> 1) + g + 8 * (r & 1)] = mx[r];
+                }
 #pragma unroll
                 for (int s = 16; s; s >>= 1) top_s = fmaxf(top_s, __shfl_xor_sync(0xffffffffu, top_s, s));
                 named_bar_sync(2, kSoftmax);
-                const float both = fmaxf(mx, part_max[hf ^ 1][row]);
+                const float e0 = e;
                 if (top_s > thr_s) {
                     const int be = (int)(__float_as_uint(top_s) >> 23);      // top_s < 2^(be - 126)
                     e = (float)((be < 240 ? be : 240) - 126);
                     thr_s = __uint_as_float((unsigned)((int)e + 6 + 127) << 23);
                 }
-                const bool first = m == -INFINITY;
-                if (both > thr) {
-                    m = both;
-                    thr = m + 8.f / p.k;
+                float f[4];
+                bool move = false;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float both = fmaxf(mx[r], part_max[hf ^ 1][32 * quad + 16 * (r >> 1) + g + 8 * (r & 1)]);
+                    float by = e0 - e;                         // old reference less the new one
+                    if ((i == 0 || both > 8.f - e0) && both != -INFINITY) by -= both + e0;
+                    const float to = mu[r] - by;
+                    f[r] = i ? ex2(by) : 0.f;
+                    mu[r] = to;
+                    move = move || by != 0.f;
+                    l[r] *= f[r];
+#pragma unroll
+                    for (int gr = 0; gr < GR; ++gr) beta[r][gr] *= f[r];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) S[r >> 1][j][r & 1] = add2(S[r >> 1][j][r & 1], pk(by, by));
                 }
-                const float to = m == -INFINITY ? 0.f : fmaf(m, p.k, e);
-                const float f = first ? 0.f : ex2(mu - to);
-                mu = to;
-                const f2 ff = pk(f, f);
-                l2 = mul2(l2, ff);
-#pragma unroll
-                for (int gr = 0; gr < GR; ++gr) beta[gr] = mul2(beta[gr], ff);
                 // (the first tile overwrites the accumulators)
-                if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+                if (i > 0 && __any_sync(0xffffffffu, move)) {
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
+                    for (int c = 0; c < D / 64 * 2; ++c) {
+                        const int rh = c & 1;
                         uint32_t a[16];
-                        const uint32_t at = my + GR * kTile + hf * (D / 2) + c * 16;
-                        tmem_ld16(at, a);
+                        const uint32_t at = my + ((uint32_t)(16 * rh) << 16) + GR * kTile + hf * (D / 2) + (c >> 1) * 32;
+                        tmem_ld_frag(at, a);
                         tc::tmem_wait_ld();
+                        const float f0 = rh ? f[2] : f[0], f1 = rh ? f[3] : f[1];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * f);
-                        tmem_st16(at, a);
+                        for (int j = 0; j < 16; ++j)
+                            a[j] = __float_as_uint(__uint_as_float(a[j]) * (j & 2 ? f1 : f0));
+                        tmem_st_frag(at, a);
                     }
                 }
             }
-            const f2 mu2 = pk(-mu, -mu);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                f2 pr[8];
+            for (int rh = 0; rh < 2; ++rh) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float a, b;
-                    unpk(fma2(S[c * 8 + j], k2, mu2), a, b);
-                    pr[j] = pk(ex2(a), ex2(b));
-                }
-                l2 = add2(l2, add2(add2(add2(pr[0], pr[1]), add2(pr[2], pr[3])), add2(add2(pr[4], pr[5]), add2(pr[6], pr[7]))));
-#pragma unroll
-                for (int gr = 0; gr < GR; ++gr) {
-                    const ulonglong2* vs = reinterpret_cast<const ulonglong2*>(mine + (2 * GR + gr) * kTile + c * 16);
-                    const ulonglong2* vc = reinterpret_cast<const ulonglong2*>(mine + (3 * GR + gr) * kTile + c * 16);
-                    uint32_t w[8];
+                for (int k = 0; k < 2; ++k) {
+                    f2 sum = 0;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const ulonglong2 s4 = vs[j], c4 = vc[j];
                         float a, b;
-                        unpk(mul2(pr[2 * j], s4.x), a, b);
-                        w[2 * j] = pack2(a, b);
-                        unpk(mul2(pr[2 * j + 1], s4.y), a, b);
-                        w[2 * j + 1] = pack2(a, b);
-                        beta[gr] = fma2(pr[2 * j], c4.x, fma2(pr[2 * j + 1], c4.y, beta[gr]));
+                        unpk(S[rh][j][k], a, b);
+                        S[rh][j][k] = pk(ex2(a), ex2(b));
+                        sum = j ? add2(sum, S[rh][j][k]) : S[rh][j][k];
                     }
-                    tmem_st8(my + gr * kTile + hf * 16 + c * 8, w);
+                    float a, b;
+                    unpk(sum, a, b);
+                    l[2 * rh + k] += a + b;
+                }
+#pragma unroll
+                for (int gr = 0; gr < GR; ++gr) {
+                    uint32_t w[8];
+                    f2 acc[2] = {0, 0};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const ulonglong2 sc = *reinterpret_cast<const ulonglong2*>(mv + j * 16 * GR + gr * 4);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float a, b;
+                            unpk(mul2(S[rh][j][k], sc.x), a, b);
+                            w[2 * j + k] = pack2(a, b);
+                            acc[k] = j ? fma2(S[rh][j][k], sc.y, acc[k]) : mul2(S[rh][j][k], sc.y);
+                        }
+                    }
+                    tmem_st_pairs(my + ((uint32_t)(16 * rh) << 16) + gr * kTile + hf * 16, w);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float a, b;
+                        unpk(acc[k], a, b);
+                        beta[2 * rh + k][gr] += a + b;
+                    }
                 }
             }
             tmem_wait_st();
@@ -476,44 +549,57 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             }
             __syncwarp();
         }
-        // the two threads of a row add up their sums, each writes half of the dims
-        float a, b;
-        unpk(l2, a, b);
-        part_sum[hf][0][row] = a + b;
-#pragma unroll
-        for (int gr = 0; gr < GR; ++gr) {
-            unpk(beta[gr], a, b);
-            part_sum[hf][1 + gr][row] = a + b;
-        }
         ok = wait_bar(&freed[(n - 1) & 1], ((n - 1) >> 1) & 1, &dead) && ok;
+        // a row's sums: its 4 lanes, then both halves of the tokens (over the queries, done with by now)
+        float* sums = reinterpret_cast<float*>(sQ);            // [hf][1 + GR][row]
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 32 * quad + 16 * (r >> 1) + g + 8 * (r & 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            if (t == 0) sums[hf * (1 + GR) * kRowsQ + row] = l[r];
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr) {
+                beta[r][gr] += __shfl_xor_sync(0xffffffffu, beta[r][gr], 1);
+                beta[r][gr] += __shfl_xor_sync(0xffffffffu, beta[r][gr], 2);
+                if (t == 0) sums[(hf * (1 + GR) + 1 + gr) * kRowsQ + row] = beta[r][gr];
+            }
+        }
         named_bar_sync(2, kSoftmax);
         if (__all_sync(0xffffffffu, ok)) {
             tc::fence_after_sync();
             const long long slot = ((long long)h * p.RB + rb) * p.splits + blockIdx.x;
-            float* dst = p.part_o + (slot * kRowsQ + row) * D + hf * (D / 2);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t r[16];
-                tmem_ld16(my + GR * kTile + hf * (D / 2) + c * 16, r);
-                const int gr = (hf * (D / 2) + c * 16) / kGroup;
-                const float add = part_sum[0][1 + gr][row] + part_sum[1][1 + gr][row];
+            for (int c = 0; c < D / 64 * 2; ++c) {
+                const int rh = c & 1, d0 = hf * (D / 2) + (c >> 1) * 32, gr = d0 / kGroup;
+                uint32_t a[16];
+                tmem_ld_frag(my + ((uint32_t)(16 * rh) << 16) + GR * kTile + d0, a);
                 tc::tmem_wait_ld();
-                float v[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    // column j of 8 dims holds dim 0 4 1 5 2 6 3 7 (4 bits)
-                    const int d = BITS == 4 ? (j & 8) + ((j & 1) << 2) + ((j & 7) >> 1) : j;
-                    v[d] = __uint_as_float(r[j]) + add;
+                for (int k = 0; k < 2; ++k) {
+                    const int row = 32 * quad + 16 * rh + g + 8 * k;
+                    const float add = sums[(1 + gr) * kRowsQ + row] + sums[(1 + GR + 1 + gr) * kRowsQ + row];
+                    float* dst = p.part_o + (slot * kRowsQ + row) * D + d0;
+                    if (r0 + row < p.rows)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float x = __uint_as_float(a[4 * j + 2 * k]) + add, y = __uint_as_float(a[4 * j + 2 * k + 1]) + add;
+                            if (BITS == 4) {                   // columns 2t, 2t + 1 hold dims t, t + 4
+                                dst[8 * j + t] = x;
+                                dst[8 * j + t + 4] = y;
+                            } else {
+                                *reinterpret_cast<float2*>(dst + 8 * j + 2 * t) = make_float2(x, y);
+                            }
+                        }
                 }
-                if (r0 + row < p.rows)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        reinterpret_cast<float4*>(dst + c * 16)[j] =
-                            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             }
-            if (hf == 0 && r0 + row < p.rows)
-                p.part_ml[slot * kRowsQ + row] =
-                    make_float2(m == -INFINITY ? m : mu, part_sum[0][0][row] + part_sum[1][0][row]);
+            if (hf == 0 && t == 0)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 32 * quad + 16 * (r >> 1) + g + 8 * (r & 1);
+                    if (r0 + row < p.rows)
+                        p.part_ml[slot * kRowsQ + row] = make_float2(mu[r], sums[row] + sums[(1 + GR) * kRowsQ + row]);
+                }
         }
     }
     tc::fence_before_sync();
