@@ -6,9 +6,9 @@
 //   warps 8-11  turn a strip of codes each into fp16 (code - z, z half the code range: exact)
 //               in shared memory, K as K-major, V as MN-major operand tiles, and its scales
 //               into fp32 tables; the next step's codes are loaded into registers meanwhile;
-//   thread 0    issues the scores' products, and once the weights are there O_g += P'_g V_g for
-//               each 64 dims g; accumulators and P' (over the scores, which are read by
-//               then) in TMEM;
+//   warp 0      issues the scores' products, and once the weights are there O_g += P'_g V_g for
+//               each 64 dims g; accumulators and P' (over the scores that the same warp has
+//               read) in TMEM;
 //   warps 0-7   32 rows x 32 tokens each: S, running maximum and sum, weights p,
 //               P'_g = fp16(p s_g), and sum_j p (b_g + z s_g) in fp32.
 // Scores: with K = s (code - z + r), r = b / s + z, a group's product is
@@ -102,14 +102,38 @@ __device__ __forceinline__ void tmem_st_pairs(uint32_t a, const uint32_t (&r)[8]
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] B[smem]; B MN-major
-__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// Matrix steps and their commit, issued by the lane with `lead` set: the whole warp comes
+// here together, so that the descriptors are warp-uniform values (from a branch that one
+// thread takes alone a step and its commit took twice as long).
+// D[tmem] (+)= A[smem] B[smem]^T
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t lead) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
         : "memory");
 }
+// D[tmem] (+)= A[tmem] B[smem]; B MN-major
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t lead) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t lead) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elect() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(r));
+    return r;
+}
+
 // Operand descriptors: the low word advances with the address, the high word is fixed.
 // MN-major tile without swizzle: blocks of 8 tokens x 16 bytes (8 dims); the blocks of
 // consecutive tokens lie 128 bytes apart (leading offset), of consecutive dims kTile * 16 (stride).
@@ -119,14 +143,14 @@ __device__ __forceinline__ uint64_t desc(uint32_t lo, uint32_t stride) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"((stride >> 4) | (1u << 14)));
     return d;
 }
-// whether any of the softmax threads wants it
-__device__ __forceinline__ bool any_softmax(bool want) {
+// whether any thread of the two warps that share 32 rows wants it
+__device__ __forceinline__ bool any_of_rows(int quad, bool want) {
     uint32_t r;
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 256, p;\n"
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 64, p;\n"
         " selp.u32 %0, 1, 0, q;\n}\n"
         : "=r"(r)
-        : "r"((uint32_t)want)
+        : "r"((uint32_t)want), "r"(4 + quad)
         : "memory");
     return r != 0;
 }
@@ -187,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
     __shared__ int dead;
     __shared__ float part_max[2][kRowsQ];
     char *sQ = smem, *sM = smem + X::kQ, *stages = sM + X::kMean;
-    const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, wid = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int h = blockIdx.z, rb = blockIdx.y;
     const int t0 = blockIdx.x * p.tiles_per_split;
     const int all = (p.n_tok - 1) / kTile + 1;
@@ -364,25 +388,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
 #pragma unroll
             for (int gr = 0; gr < GR; ++gr) beta[r][gr] = 0.f;
         }
-        auto issue_scores = [&](int i) {                       // thread 0: the products of tile i
-            const uint32_t k0 = smem_u32(stages + (i & 1) * X::kStage);
+        const uint32_t a0 = desc_lo(smem_u32(sQ), tc::kLbo), m0 = desc_lo(smem_u32(sM), tc::kLbo);
+        const uint32_t st0 = smem_u32(stages);
+        auto issue_scores = [&](int i, uint32_t lead) {        // warp 0: the products of tile i
+            const uint32_t k0 = st0 + (i & 1) * X::kStage;
             const uint32_t sK = desc_lo(k0, tc::kLbo), sR = desc_lo(k0 + 2 * X::kOp, tc::kLbo);
-            const uint32_t a0 = desc_lo(smem_u32(sQ), tc::kLbo), m0 = desc_lo(smem_u32(sM), tc::kLbo);
-            if (!wait_bar(&full[i & 1], (i >> 1) & 1, &dead)) return;
+            if (!__all_sync(0xffffffffu, wait_bar(&full[i & 1], (i >> 1) & 1, &dead))) return;
             tc::fence_after_sync();
 #pragma unroll
             for (int gr = 0; gr < GR; ++gr) {
 #pragma unroll
                 for (int ks = 4 * gr; ks < 4 * gr + 4; ++ks)
-                    tc::mma_f16(tm + gr * kTile, desc(a0 + ks * (kRowsQ * 32 / 16), tc::kSbo),
-                                desc(sK + ks * (kTile * 32 / 16), tc::kSbo), tc::idesc_f16(kRowsQ, kTile), ks % 4 != 0);
-                tc::mma_f16(tm + gr * kTile, desc(m0 + gr * (kRowsQ * 32 / 16), tc::kSbo), desc(sR, tc::kSbo),
-                            tc::idesc_f16(kRowsQ, kTile), true);
+                    mma_ss(tm + gr * kTile, desc(a0 + ks * (kRowsQ * 32 / 16), tc::kSbo),
+                           desc(sK + ks * (kTile * 32 / 16), tc::kSbo), tc::idesc_f16(kRowsQ, kTile), ks % 4 != 0, lead);
+                mma_ss(tm + gr * kTile, desc(m0 + gr * (kRowsQ * 32 / 16), tc::kSbo), desc(sR, tc::kSbo),
+                       tc::idesc_f16(kRowsQ, kTile), true, lead);
             }
-            tc::mma_commit(&s_ready);
+            commit(&s_ready, lead);
         };
-        if (tid == 0) issue_scores(0);
-        __syncwarp();
+        if (wid == 0) issue_scores(0, elect());
         bool ok = true;
         for (int i = 0; i < n; ++i) {
             const char* stage = stages + (i & 1) * X::kStage;
@@ -405,22 +429,27 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             const int left = p.n_tok - (t0 + i) * kTile - hf * 32 - 2 * t;     // of this lane's tokens
             float mx[4];
 #pragma unroll
-            for (int rh = 0; rh < 2; ++rh) {
+            for (int gr = 0; gr < GR; ++gr) {
+                f2 s2[4];                                      // a token's scale serves the lane's four rows
 #pragma unroll
-                for (int gr = 0; gr < GR; ++gr) {
-                    uint32_t raw[16];
-                    tmem_ld_frag(my + ((uint32_t)(16 * rh) << 16) + gr * kTile + hf * 32, raw);
-                    tc::tmem_wait_ld();
+                for (int j = 0; j < 4; ++j) s2[j] = *reinterpret_cast<const f2*>(mk + j * 8 * GR + 2 * gr);
+                uint32_t raw[2][16];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const f2 s2 = *reinterpret_cast<const f2*>(mk + j * 8 * GR + 2 * gr);
+                for (int rh = 0; rh < 2; ++rh)
+                    tmem_ld_frag(my + ((uint32_t)(16 * rh) << 16) + gr * kTile + hf * 32, raw[rh]);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int rh = 0; rh < 2; ++rh)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const f2 x = pk(__uint_as_float(raw[4 * j + 2 * k]), __uint_as_float(raw[4 * j + 2 * k + 1]));
-                            S[rh][j][k] = fma2(x, s2, gr ? S[rh][j][k] : pk(-mu[2 * rh + k], -mu[2 * rh + k]));
+                            const f2 v = pk(__uint_as_float(raw[rh][4 * j + 2 * k]), __uint_as_float(raw[rh][4 * j + 2 * k + 1]));
+                            S[rh][j][k] = fma2(v, s2[j], gr ? S[rh][j][k] : pk(-mu[2 * rh + k], -mu[2 * rh + k]));
                         }
-                    }
-                }
+            }
+#pragma unroll
+            for (int rh = 0; rh < 2; ++rh) {
                 if (left < 26) {                               // tokens behind the last
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -440,8 +469,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                 }
             }
             const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            // (this barrier also ends every read of the scores before P' goes over them)
-            if (any_softmax(i == 0 || most > 8.f - e || top_s > thr_s)) {
+            if (any_of_rows(quad, i == 0 || most > 8.f - e || top_s > thr_s)) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
@@ -450,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                 }
 #pragma unroll
                 for (int s = 16; s; s >>= 1) top_s = fmaxf(top_s, __shfl_xor_sync(0xffffffffu, top_s, s));
-                named_bar_sync(2, kSoftmax);
+                named_bar_sync(8 + quad, 64);
                 const float e0 = e;
                 if (top_s > thr_s) {
                     const int be = (int)(__float_as_uint(top_s) >> 23);      // top_s < 2^(be - 126)
@@ -492,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                 }
             }
 #pragma unroll
-            for (int rh = 0; rh < 2; ++rh) {
+            for (int rh = 0; rh < 2; ++rh)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     f2 sum = 0;
@@ -508,21 +536,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                     l[2 * rh + k] += a + b;
                 }
 #pragma unroll
-                for (int gr = 0; gr < GR; ++gr) {
+            for (int gr = 0; gr < GR; ++gr) {
+                ulonglong2 sc[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sc[j] = *reinterpret_cast<const ulonglong2*>(mv + j * 16 * GR + gr * 4);
+#pragma unroll
+                for (int rh = 0; rh < 2; ++rh) {
                     uint32_t w[8];
                     f2 acc[2] = {0, 0};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const ulonglong2 sc = *reinterpret_cast<const ulonglong2*>(mv + j * 16 * GR + gr * 4);
+                    for (int j = 0; j < 4; ++j)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             float a, b;
-                            unpk(mul2(S[rh][j][k], sc.x), a, b);
+                            unpk(mul2(S[rh][j][k], sc[j].x), a, b);
                             w[2 * j + k] = pack2(a, b);
-                            acc[k] = j ? fma2(S[rh][j][k], sc.y, acc[k]) : mul2(S[rh][j][k], sc.y);
+                            acc[k] = j ? fma2(S[rh][j][k], sc[j].y, acc[k]) : mul2(S[rh][j][k], sc[j].y);
                         }
-                    }
-                    tmem_st_pairs(my + ((uint32_t)(16 * rh) << 16) + gr * kTile + hf * 16, w);
+                    tmem_st_pairs(my + ((uint32_t)(16 * rh) << 16) + gr * kTile + hf * 32, w);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         float a, b;
@@ -534,18 +565,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             tmem_wait_st();
             tc::fence_before_sync();
             named_bar_sync(3, kSoftmax);
-            if (tid == 0) {
-                const uint32_t sV = desc_lo(smem_u32(stage) + X::kOp, 128);
+            if (wid == 0) {
+                const uint32_t lead = elect();
+                const uint32_t sV = desc_lo(st0 + (i & 1) * X::kStage + X::kOp, 128);
                 tc::fence_after_sync();
 #pragma unroll
                 for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        mma_f16_ta(tm + GR * kTile + gr * kGroup, tm + gr * kTile + kk * 8,
-                                   desc(sV + (gr * (kGroup / 8) * (kTile * 16) + kk * 256) / 16, kTile * 16),
-                                   tc::idesc_f16(kRowsQ, kGroup) | (1u << 16), i > 0 || kk > 0);
-                tc::mma_commit(&freed[i & 1]);
-                if (i + 1 < n) issue_scores(i + 1);
+                        mma_ts(tm + GR * kTile + gr * kGroup, tm + gr * kTile + (kk >> 1) * 32 + (kk & 1) * 8,
+                               desc(sV + (gr * (kGroup / 8) * (kTile * 16) + kk * 256) / 16, kTile * 16),
+                               tc::idesc_f16(kRowsQ, kGroup) | (1u << 16), i > 0 || kk > 0, lead);
+                commit(&freed[i & 1], lead);
+                if (i + 1 < n) issue_scores(i + 1, lead);
             }
             __syncwarp();
         }
