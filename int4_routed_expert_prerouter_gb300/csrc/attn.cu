@@ -72,8 +72,9 @@ struct Cfg {
     static constexpr int MT = D / 16;
     // shared memory
     static constexpr int kRingBytes = kWarps * STAGES * US * STRIP;
-    static constexpr int kQ = NT * CH * 32 * QW * 4;
-    static constexpr int kQsum = NT * 8 * GR * 4;
+    static constexpr bool kQRegs = NT == 1;           // query fragments stay in registers
+    static constexpr int kQ = kQRegs ? 0 : NT * CH * 32 * QW * 4;
+    static constexpr int kQsum = kQRegs ? 0 : NT * 8 * GR * 4;
     static constexpr int kRedLd = D + 4;
     static constexpr int kRed = kWarps * 8 * kRedLd * 4;   // the ring's memory, once a segment's copies are used up
     static constexpr int kMl = kWarps * NT * 8 * 8;
@@ -116,7 +117,7 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
     return r;
 }
 __device__ __forceinline__ float max_over_rows(float v) {   // the 8 lanes of one t
@@ -158,9 +159,46 @@ __device__ __forceinline__ int dim_of(int mt, int g) {
     return BITS == 4 ? 32 * (mt >> 1) + 4 * g + 2 * (mt & 1) : 16 * mt + 2 * g;
 }
 
+// (s, b) words of a token, one per group
+template <int GR>
+__device__ __forceinline__ void load_sb(const char* p, uint32_t (&w)[GR]) {
+    if (GR == 1) {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if (GR == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x;
+        w[GR - 1] = v.y;
+    } else {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x;
+        w[1 % GR] = v.y;
+        w[2 % GR] = v.z;
+        w[3 % GR] = v.w;
+    }
+}
+__device__ __forceinline__ float2 sb_of(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+
+// B fragment words of one piece of one query row (lane t's dims; zeros where there is no row)
+template <int BITS>
+__device__ __forceinline__ void q_frag(const __half* src, bool there, uint32_t* w) {
+    if (BITS == 4) {
+        // even nibbles 0,4 | 2,6, odd ones 1,5 | 3,7 (these come in sixteen times as large)
+        const uint4 v = there ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
+        w[0] = __byte_perm(v.x, v.z, 0x5410);
+        w[1] = __byte_perm(v.y, v.w, 0x5410);
+        w[2] = hfma2(__byte_perm(v.x, v.z, 0x7632), 0x2C002C00u, 0x80008000u);
+        w[3] = hfma2(__byte_perm(v.y, v.w, 0x7632), 0x2C002C00u, 0x80008000u);
+    } else {
+        const uint2 v = there ? *reinterpret_cast<const uint2*>(src) : make_uint2(0, 0);
+        w[0] = __byte_perm(v.x, v.y, 0x5410);    // dims 0, 2
+        w[1] = __byte_perm(v.x, v.y, 0x7632);    // dims 1, 3
+    }
+}
+
 template <int BITS, int D, int NT>
 __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_kernel(const AttnP p) {
     using X = Cfg<BITS, D, NT>;
+    constexpr int GR = X::GR, QW = X::QW;
     extern __shared__ __align__(128) char smem[];
     char* ring = smem;
     uint32_t* sq = reinterpret_cast<uint32_t*>(ring + X::kRing);
@@ -173,40 +211,47 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
     constexpr int kUnit = 16 * X::US;
 
-    // cost before each list: a scan over at most 256 lengths
+    // lengths, and the cost before each list: a scan over at most 256 of them
     const int per_list = p.H * p.RB;
-    if (wid == 0) {
+    {
         const long long cap = (long long)p.W * p.c.page_tokens;
-        long long base = 0;
-        for (int i0 = 0; i0 < p.n_seq; i0 += 32) {
-            const int i = i0 + lane;
-            int n = 0;
-            if (i < p.n_seq) {
-                n = p.lens ? p.lens[i] : p.n_tok;
-                if (n > cap) {
-                    n = (int)cap;
-                    if (blockIdx.x == 0 && p.status) atomicExch(p.status, EDGE0_EINVAL);
-                }
-                n = n < 0 ? 0 : n;
-                tokens[i] = n;
+        for (int i = tid; i < p.n_seq; i += 32 * kWarps) {
+            int n = p.lens ? p.lens[i] : p.n_tok;
+            if (n > cap) {
+                n = (int)cap;
+                if (blockIdx.x == 0 && p.status) atomicExch(p.status, EDGE0_EINVAL);
             }
-            const long long mine = n ? (long long)((n - 1) / kUnit + 1 + kSegCost) * per_list : 0;
-            long long upto = mine;
+            tokens[i] = n < 0 ? 0 : n;
+        }
+        if (tid < kWarps * X::STAGES) mbar_init(&bars[tid], 1);
+        fence_mbar_init();
+        __syncthreads();
+        if (wid == 0) {
+            long long part[8], sum = 0;
+            if (lane * 8 < p.n_seq) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int n = lane * 8 + j < p.n_seq ? tokens[lane * 8 + j] : 0;
+                    part[j] = sum;
+                    sum += n ? (long long)((n - 1) / kUnit + 1 + kSegCost) * per_list : 0;
+                }
+            }
+            long long upto = sum;
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
                 const long long o = __shfl_up_sync(0xffffffffu, upto, s);
                 if (lane >= s) upto += o;
             }
-            if (i < p.n_seq) cum[i] = base + upto - mine;
-            base += __shfl_sync(0xffffffffu, upto, 31);
+            if (lane * 8 < p.n_seq)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (lane * 8 + j < p.n_seq) cum[lane * 8 + j] = upto - sum + part[j];
+            if (lane == 31) cum[p.n_seq] = upto;
         }
-        if (lane == 0) cum[p.n_seq] = base;
+        __syncthreads();
     }
-    if (tid < kWarps * X::STAGES) mbar_init(&bars[tid], 1);
-    fence_mbar_init();
-    __syncthreads();
     const long long total = cum[p.n_seq];
-    long long share = (total + gridDim.x - 1) / gridDim.x;
+    long long share = total < 0x7fffffff ? ((unsigned)total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
     if (share < kMinShare + kSegCost) share = kMinShare + kSegCost;
     long long pos = share * blockIdx.x;
     const long long end = pos + share < total ? pos + share : total;
@@ -219,17 +264,20 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
     const int lr = (lane & 7) + 8 * ((lane >> 3) & 1);
     const uint32_t row_off = lr * X::R;
     const uint32_t piece = ((lane >> 4) ^ kv::turn(X::R, lr)) << 4;
+    const int spp = p.c.page_tokens / kv::kStrip;
+    // copies per unit: one where a unit's strips always lie in one page
+    const int cpu = X::US == 1 || spp % X::US == 0 ? 1 : X::US;
 
+    int seq = 0;
     while (pos < end) {
-        // the segment that holds unit `pos`
-        int lo = 0, hi = p.n_seq;
+        // the list that holds `pos`; one without tokens shares its successor's start, the search ends behind it
+        int lo = seq, hi = p.n_seq;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (cum[mid] <= pos) lo = mid;
             else hi = mid;
         }
-        // lists without tokens share their successor's start: the search ends at the last one
-        const int seq = lo;
+        seq = lo;
         const int n_tok = tokens[seq];
         const int units = (n_tok - 1) / kUnit + 1, cost = units + kSegCost;
         const long long in_list = pos - cum[seq];
@@ -243,75 +291,106 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
         const int h = hr / p.RB, rb = hr - h * p.RB;
         const int sidx = (seq * p.H + h) * p.RB + rb;
         const int* pages = p.pages + (long long)seq * p.W;
-        const int spp = p.c.page_tokens / kv::kStrip;
+        const int n_strips = (n_tok - 1) / kv::kStrip + 1;
 
-        auto issue = [&](int u, int stage) {   // whole warp
-            const int s0 = u * X::US;
-            const int left = (n_tok - 1) / 16 + 1 - s0;
-            const int n = left < X::US ? left : X::US;
-            if (lane == 0) mbar_arrive_expect_tx(&my_bar[stage], n * X::STRIP);
-            __syncwarp();
-            if (lane < n) {
-                const int st = s0 + lane, pg = st / spp;
-                int id = pages[pg];
-                if (id < 0 || id >= p.c.n_pages) {
-                    id = 0;
-                    if (p.status) atomicExch(p.status, EDGE0_EINVAL);
-                }
-                const char* src = p.c.pages + id * p.c.page_bytes + ((long long)h * spp + (st - pg * spp)) * X::STRIP;
-                copy_strip(my_ring + (stage * X::US + lane) * X::STRIP, src, X::STRIP, &my_bar[stage]);
-            }
-            __syncwarp();
+        // Copies: lane i prepares the address of the warp's i-th copy from here on (32 / cpu
+        // units), and the page number of the one 32 copies later.
+        const int per_batch = 32 / cpu;
+        int batch = dead ? u1 : u0 + wid, in_batch = 0;          // first unit of the batch; units of it issued
+        auto strip_at = [&](int unit0) {                         // this lane's strip, behind the last: any valid one
+            const int s = (unit0 + kWarps * (lane / cpu)) * X::US + (cpu == 1 ? 0 : lane % cpu);
+            return s < n_strips ? s : n_strips - 1;
         };
-        int ahead = dead ? u1 : u0 + wid;
+        auto address = [&](int unit0, int id) -> const char* {
+            const int s = strip_at(unit0);
+            if (id < 0 || id >= p.c.n_pages) {
+                id = 0;
+                if (p.status) atomicExch(p.status, EDGE0_EINVAL);
+            }
+            return p.c.pages + id * p.c.page_bytes + ((long long)h * spp + s % spp) * X::STRIP;
+        };
+        const char* src = address(batch, pages[strip_at(batch) / spp]);
+        int id_later = pages[strip_at(batch + kWarps * per_batch) / spp];
         int issued = it;
+        auto issue = [&]() {                                     // the whole warp: the next unit, if there is one
+            const int u = batch + kWarps * in_batch;
+            if (u >= u1) return;
+            const int stage = issued % X::STAGES;
+            const int n = min(X::US, n_strips - u * X::US);
+            if (lane == in_batch * cpu) mbar_arrive_expect_tx(&my_bar[stage], n * X::STRIP);
+            if (cpu == 1) {
+                if (lane == in_batch) copy_strip(my_ring + stage * X::US * X::STRIP, src, n * X::STRIP, &my_bar[stage]);
+            } else {
+                __syncwarp();
+                const int s = lane - in_batch * cpu;
+                if (s >= 0 && s < n) copy_strip(my_ring + (stage * X::US + s) * X::STRIP, src, X::STRIP, &my_bar[stage]);
+            }
+            ++issued;
+            if (++in_batch == per_batch) {
+                in_batch = 0;
+                batch += kWarps * per_batch;
+                src = address(batch, id_later);
+                id_later = pages[strip_at(batch + kWarps * per_batch) / spp];
+            }
+        };
 #pragma unroll 1
-        for (int s = 0; s < X::STAGES - 1; ++s, ahead += kWarps)
-            if (ahead < u1) issue(ahead, issued++ % X::STAGES);
+        for (int s = 0; s < X::STAGES - 1; ++s) issue();
 
-        // query rows of the block as B fragments, and their sums over each 64 dims
+        // query rows of the block as B fragments; their sums over each 64 dims are
+        // matrix steps against ones (16 where the fragment holds a sixteenth)
         const int r0 = rb * 8 * NT;
-        for (int i = tid; i < NT * X::CH * 32; i += 32 * kWarps) {
-            const int ln = i & 31, c = (i >> 5) % X::CH, nt = (i >> 5) / X::CH;
-            const int r = r0 + nt * 8 + (ln >> 2), tt = ln & 3;
-            uint32_t w[X::QW];
+        uint32_t qf[X::kQRegs ? X::CH : 1][QW];
+        float qs[X::kQRegs ? GR : 1][2];
+        const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+        const uint32_t sixteens[4] = {0x4C004C00u, 0x4C004C00u, 0x4C004C00u, 0x4C004C00u};
+        auto q_at = [&](int r, int c) {
+            return p.q + (long long)(seq * p.q_step + r / p.G) * p.ldq + (long long)(h * p.G + r % p.G) * D +
+                   (BITS == 4 ? 32 * c + 8 * t : 16 * c + 4 * t);
+        };
+        auto sums_of = [&](const uint32_t* f, int gr, float (&sum)[4]) {     // f: fragments of a row block
 #pragma unroll
-            for (int j = 0; j < X::QW; ++j) w[j] = 0;
-            if (r < p.rows) {
-                const __half* src = p.q + (long long)(seq * p.q_step + r / p.G) * p.ldq +
-                                    (long long)(h * p.G + r % p.G) * D + (BITS == 4 ? 32 * c + 8 * tt : 16 * c + 4 * tt);
-                if (BITS == 4) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(src);
-                    const uint32_t sixteenth = 0x2C002C00u;
-                    // even nibbles 0,4 | 2,6, odd ones 1,5 | 3,7 (these come in sixteen times as large)
-                    w[0] = __byte_perm(v.x, v.z, 0x5410);
-                    w[1] = __byte_perm(v.y, v.w, 0x5410);
-                    w[2] = hfma2(__byte_perm(v.x, v.z, 0x7632), sixteenth, 0x80008000u);
-                    w[3] = hfma2(__byte_perm(v.y, v.w, 0x7632), sixteenth, 0x80008000u);
-                } else {
-                    const uint2 v = *reinterpret_cast<const uint2*>(src);
-                    w[0] = __byte_perm(v.x, v.y, 0x5410);    // dims 0, 2
-                    w[1] = __byte_perm(v.x, v.y, 0x7632);    // dims 1, 3
+            for (int c = gr * X::CPG; c < (gr + 1) * X::CPG; ++c) {
+                const uint32_t* w = f + c * QW;
+                if (c == gr * X::CPG) mma_16816_first(sum, ones, w[0], w[1]);
+                else mma_16816_v(sum, ones, w[0], w[1]);
+                if (BITS == 4) mma_16816_v(sum, sixteens, w[QW - 2], w[QW - 1]);
+            }
+        };
+        if constexpr (X::kQRegs) {
+            const int r = r0 + g;
+#pragma unroll
+            for (int c = 0; c < X::CH; ++c) q_frag<BITS>(q_at(r < p.rows ? r : 0, c), r < p.rows, qf[c]);
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr) {
+                float sum[4];
+                sums_of(&qf[0][0], gr, sum);
+                qs[gr][0] = sum[0] * (1.f / kTwo24);
+                qs[gr][1] = sum[1] * (1.f / kTwo24);
+            }
+        } else {
+            for (int nt = wid; nt < NT; nt += kWarps) {
+                const int r = r0 + nt * 8 + g;
+                uint32_t f[X::CH][QW];
+#pragma unroll
+                for (int c = 0; c < X::CH; ++c) {
+                    q_frag<BITS>(q_at(r < p.rows ? r : 0, c), r < p.rows, f[c]);
+#pragma unroll
+                    for (int j = 0; j < QW; ++j) sq[((nt * X::CH + c) * 32 + lane) * QW + j] = f[c][j];
+                }
+#pragma unroll
+                for (int gr = 0; gr < GR; ++gr) {
+                    float sum[4];
+                    sums_of(&f[0][0], gr, sum);
+                    if (g == 0) {
+                        sqsum[(nt * 8 + 2 * t) * GR + gr] = sum[0] * (1.f / kTwo24);
+                        sqsum[(nt * 8 + 2 * t + 1) * GR + gr] = sum[1] * (1.f / kTwo24);
+                    }
                 }
             }
-#pragma unroll
-            for (int j = 0; j < X::QW; ++j) sq[i * X::QW + j] = w[j];
+            __syncthreads();
         }
-        for (int i = wid; i < NT * 8 * X::GR; i += kWarps) {
-            const int r = r0 + i / X::GR, gr = i % X::GR;
-            float s = 0.f;
-            if (r < p.rows) {
-                const __half2 v = *reinterpret_cast<const __half2*>(
-                    p.q + (long long)(seq * p.q_step + r / p.G) * p.ldq + (long long)(h * p.G + r % p.G) * D +
-                    gr * kGroup + 2 * lane);
-                s = __low2float(v) + __high2float(v);
-            }
-            s = warp_sum(s);
-            if (lane == 0) sqsum[i] = s * (1.f / kTwo24);
-        }
-        __syncthreads();
 
-        float O[X::MT][NT][4], beta[NT][X::GR][2], m[NT][2], l[NT][2], thr[NT][2], mu[NT][2];
+        float O[X::MT][NT][4], beta[NT][GR][2], m[NT][2], l[NT][2], thr[NT][2], mu[NT][2];
         float e = 0.f, thr_s = 0.f;          // exponent of a score: k S - mu, mu = k m + e
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -324,15 +403,13 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                 m[nt][i] = thr[nt][i] = -INFINITY;
                 mu[nt][i] = l[nt][i] = 0.f;
 #pragma unroll
-                for (int gr = 0; gr < X::GR; ++gr) beta[nt][gr][i] = 0.f;
+                for (int gr = 0; gr < GR; ++gr) beta[nt][gr][i] = 0.f;
             }
         }
+
 #pragma unroll 1
         for (int u = dead ? u1 : u0 + wid; u < u1; u += kWarps, ++it) {
-            if (ahead < u1) {
-                issue(ahead, issued++ % X::STAGES);
-                ahead += kWarps;
-            }
+            issue();
             const int stage = it % X::STAGES;
             if (!wait_copy(&my_bar[stage], (it / X::STAGES) & 1)) {   // give up: nothing more is issued or read
                 if (lane == 0 && p.status) atomicExch(p.status, EDGE0_ETIMEOUT);
@@ -348,105 +425,108 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
             for (int st = 0; st < X::US; ++st) {
                 const char* kb = buf + st * X::STRIP;
                 const uint32_t ka = smem_u32(kb) + row_off;
+                uint32_t wa[GR], wb[GR];
+                load_sb<GR>(kb + 16 * X::R + g * X::SB, wa);
+                load_sb<GR>(kb + 16 * X::R + (g + 8) * X::SB, wb);
+                // (a strip behind the last token holds what was there before; it is masked below)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int gr = 0; gr < GR; ++gr) {
+                    float acc[NT][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) S[st][nt][i] = 0.f;
-                if (st * 16 < left) {
+                    for (int cp = 0; cp < X::CPG; cp += 2) {
+                        const int c0 = gr * X::CPG + cp;
+                        uint32_t w[4];
+                        ldsm4(w, ka + (piece ^ (c0 << 4)));
 #pragma unroll
-                    for (int gr = 0; gr < X::GR; ++gr) {
-                        float acc[NT][4];
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t x = w[2 * j], y = w[2 * j + 1];
+                            constexpr uint32_t kLow = BITS == 4 ? 0x000F000Fu : 0x00FF00FFu;
+                            const uint32_t A0[4] = {x & kLow, y & kLow, (x >> 8) & kLow, (y >> 8) & kLow};
+                            const uint32_t A1[4] = {x & 0x00F000F0u, y & 0x00F000F0u, (x >> 8) & 0x00F000F0u,
+                                                    (y >> 8) & 0x00F000F0u};
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                            for (int nt = 0; nt < NT; ++nt) {
+                                uint32_t f[QW];
+                                if constexpr (X::kQRegs) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
-#pragma unroll
-                        for (int cp = 0; cp < X::CPG; cp += 2) {
-                            const int c0 = gr * X::CPG + cp;
-                            uint32_t w[4];
-                            ldsm4(w, ka + (piece ^ (c0 << 4)));
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const uint32_t wa = w[2 * j], wb = w[2 * j + 1];
-                                if (BITS == 4) {
-                                    const uint32_t A0[4] = {wa & 0x000F000Fu, wb & 0x000F000Fu, (wa >> 8) & 0x000F000Fu,
-                                                            (wb >> 8) & 0x000F000Fu};
-                                    const uint32_t A1[4] = {wa & 0x00F000F0u, wb & 0x00F000F0u, (wa >> 8) & 0x00F000F0u,
-                                                            (wb >> 8) & 0x00F000F0u};
-#pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt) {
-                                        const uint4 f = *reinterpret_cast<const uint4*>(
-                                            sq + ((nt * X::CH + c0 + j) * 32 + lane) * 4);
-                                        mma_16816(acc[nt], A0, f.x, f.y);
-                                        mma_16816(acc[nt], A1, f.z, f.w);
-                                    }
+                                    for (int i = 0; i < QW; ++i) f[i] = qf[c0 + j][i];
+                                } else if constexpr (QW == 4) {
+                                    const uint4 v = *reinterpret_cast<const uint4*>(sq + ((nt * X::CH + c0 + j) * 32 + lane) * 4);
+                                    f[0] = v.x, f[1] = v.y, f[QW - 2] = v.z, f[QW - 1] = v.w;
                                 } else {
-                                    const uint32_t A0[4] = {wa & 0x00FF00FFu, wb & 0x00FF00FFu, (wa >> 8) & 0x00FF00FFu,
-                                                            (wb >> 8) & 0x00FF00FFu};
-#pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt) {
-                                        const uint2 f = *reinterpret_cast<const uint2*>(
-                                            sq + ((nt * X::CH + c0 + j) * 32 + lane) * 2);
-                                        mma_16816(acc[nt], A0, f.x, f.y);
-                                    }
+                                    const uint2 v = *reinterpret_cast<const uint2*>(sq + ((nt * X::CH + c0 + j) * 32 + lane) * 2);
+                                    f[0] = v.x, f[1] = v.y;
                                 }
+                                if (cp + j == 0) mma_16816_first(acc[nt], A0, f[0], f[1]);
+                                else mma_16816_v(acc[nt], A0, f[0], f[1]);
+                                if (BITS == 4) mma_16816_v(acc[nt], A1, f[QW - 2], f[QW - 1]);
                             }
                         }
-                        const char* sbp = kb + 16 * X::R + gr * 4;
-                        const float2 sa = __half22float2(*reinterpret_cast<const __half2*>(sbp + g * X::SB));
-                        const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(sbp + (g + 8) * X::SB));
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const float q0 = sqsum[(nt * 8 + 2 * t) * X::GR + gr];
-                            const float q1 = sqsum[(nt * 8 + 2 * t + 1) * X::GR + gr];
-                            S[st][nt][0] = fmaf(sa.x, acc[nt][0], fmaf(sa.y, q0, S[st][nt][0]));
-                            S[st][nt][1] = fmaf(sa.x, acc[nt][1], fmaf(sa.y, q1, S[st][nt][1]));
-                            S[st][nt][2] = fmaf(sb.x, acc[nt][2], fmaf(sb.y, q0, S[st][nt][2]));
-                            S[st][nt][3] = fmaf(sb.x, acc[nt][3], fmaf(sb.y, q1, S[st][nt][3]));
-                        }
                     }
-                }
-                if (left < st * 16 + 16) {
-                    const bool a = st * 16 + g < left, b = st * 16 + g + 8 < left;
+                    const float2 sa = sb_of(wa[gr]), sb = sb_of(wb[gr]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        S[st][nt][0] = a ? S[st][nt][0] : -INFINITY;
-                        S[st][nt][1] = a ? S[st][nt][1] : -INFINITY;
-                        S[st][nt][2] = b ? S[st][nt][2] : -INFINITY;
-                        S[st][nt][3] = b ? S[st][nt][3] : -INFINITY;
+                        float q0, q1;
+                        if constexpr (X::kQRegs) {
+                            q0 = qs[gr][0];
+                            q1 = qs[gr][1];
+                        } else {
+                            q0 = sqsum[(nt * 8 + 2 * t) * GR + gr];
+                            q1 = sqsum[(nt * 8 + 2 * t + 1) * GR + gr];
+                        }
+                        float(&s)[4] = S[st][nt];
+                        s[0] = fmaf(sa.x, acc[nt][0], gr ? fmaf(sa.y, q0, s[0]) : sa.y * q0);
+                        s[1] = fmaf(sa.x, acc[nt][1], gr ? fmaf(sa.y, q1, s[1]) : sa.y * q1);
+                        s[2] = fmaf(sb.x, acc[nt][2], gr ? fmaf(sb.y, q0, s[2]) : sb.y * q0);
+                        s[3] = fmaf(sb.x, acc[nt][3], gr ? fmaf(sb.y, q1, s[3]) : sb.y * q1);
                     }
                 }
             }
 
-            // V's scales of the unit's tokens g and g + 8, zero where there is no token
-            float2 vs[X::US][X::GR][2];
-            float top_s = 0.f;
+            // V's scales of the unit's tokens g and g + 8: (s, b + z s)
+            float2 vs[X::US][GR][2];
 #pragma unroll
-            for (int st = 0; st < X::US; ++st) {
-                const char* sbp = buf + st * X::STRIP + X::HALF + 16 * X::R;
+            for (int st = 0; st < X::US; ++st)
 #pragma unroll
-                for (int gr = 0; gr < X::GR; ++gr)
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t w[GR];
+                    load_sb<GR>(buf + st * X::STRIP + X::HALF + 16 * X::R + (g + 8 * i) * X::SB, w);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float2 sb = make_float2(0.f, 0.f);
-                        if (st * 16 + g + 8 * i < left)
-                            sb = __half22float2(
-                                *reinterpret_cast<const __half2*>(sbp + (g + 8 * i) * X::SB + gr * 4));
-                        sb.y = fmaf(sb.x, BITS == 4 ? 8.f : 128.f, sb.y);
-                        vs[st][gr][i] = sb;
-                        top_s = fmaxf(top_s, sb.x);
+                    for (int gr = 0; gr < GR; ++gr) {
+                        const float2 sb = sb_of(w[gr]);
+                        vs[st][gr][i] = make_float2(sb.x, fmaf(sb.x, BITS == 4 ? 8.f : 128.f, sb.y));
                     }
+                }
+            if (left < kUnit) {              // tokens that are not there: no weight, whatever the bytes
+#pragma unroll
+                for (int st = 0; st < X::US; ++st)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (st * 16 + g + 8 * i >= left) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) S[st][nt][2 * i] = S[st][nt][2 * i + 1] = -INFINITY;
+#pragma unroll
+                            for (int gr = 0; gr < GR; ++gr) vs[st][gr][i] = make_float2(0.f, 0.f);
+                        }
             }
 
             // the reference moves when a score is 2^8 above it or a scale 2^6
-            bool up = top_s > thr_s;
+            float top_s = 0.f;
+            bool up = false;
+#pragma unroll
+            for (int st = 0; st < X::US; ++st)
+#pragma unroll
+                for (int gr = 0; gr < GR; ++gr) top_s = fmaxf(top_s, fmaxf(vs[st][gr][0].x, vs[st][gr][1].x));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int st = 0; st < X::US; ++st)
-                    up = up || S[st][nt][0] > thr[nt][0] || S[st][nt][2] > thr[nt][0] || S[st][nt][1] > thr[nt][1] ||
-                         S[st][nt][3] > thr[nt][1];
-            if (__any_sync(0xffffffffu, up)) {
+                for (int i = 0; i < 2; ++i) {
+                    float v = fmaxf(S[0][nt][i], S[0][nt][i + 2]);
+#pragma unroll
+                    for (int st = 1; st < X::US; ++st) v = fmaxf(v, fmaxf(S[st][nt][i], S[st][nt][i + 2]));
+                    up = up || v > thr[nt][i];
+                }
+            if (__any_sync(0xffffffffu, up || top_s > thr_s)) {
                 top_s = max_over_rows(top_s);
                 if (top_s > thr_s) {
                     const int be = (int)(__float_as_uint(top_s) >> 23);      // top_s < 2^(be - 126)
@@ -469,7 +549,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                         thr[nt][i] = v + 8.f / p.k;
                         l[nt][i] *= f;
 #pragma unroll
-                        for (int gr = 0; gr < X::GR; ++gr) beta[nt][gr][i] *= f;
+                        for (int gr = 0; gr < GR; ++gr) beta[nt][gr][i] *= f;
 #pragma unroll
                         for (int mt = 0; mt < X::MT; ++mt) {
                             O[mt][nt][i] *= f;
@@ -480,28 +560,26 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
 #pragma unroll
             for (int st = 0; st < X::US; ++st)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        S[st][nt][i] = ex2(fmaf(S[st][nt][i], p.k, -mu[nt][i & 1]));
-                        l[nt][i & 1] += S[st][nt][i];
-                    }
-
+                    for (int i = 0; i < 4; ++i) S[st][nt][i] = ex2(fmaf(S[st][nt][i], p.k, -mu[nt][i & 1]));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) l[nt][i] += S[st][nt][i] + S[st][nt][i + 2];
+                }
 #pragma unroll
             for (int st = 0; st < X::US; ++st) {
-                if (st * 16 >= left) continue;
                 const uint32_t va = smem_u32(buf + st * X::STRIP + X::HALF) + row_off;
 #pragma unroll
-                for (int gr = 0; gr < X::GR; ++gr) {
+                for (int gr = 0; gr < GR; ++gr) {
                     uint32_t b0[NT], b1[NT];
-                    const float w0 = vs[st][gr][0].x, w1 = vs[st][gr][1].x;
+                    const float2 v0 = vs[st][gr][0], v1 = vs[st][gr][1];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const float* P = S[st][nt];
-                        b0[nt] = transpose8(pack2(P[0] * w0, P[1] * w0));
-                        b1[nt] = transpose8(pack2(P[2] * w1, P[3] * w1));
-                        beta[nt][gr][0] = fmaf(P[0], vs[st][gr][0].y, fmaf(P[2], vs[st][gr][1].y, beta[nt][gr][0]));
-                        beta[nt][gr][1] = fmaf(P[1], vs[st][gr][0].y, fmaf(P[3], vs[st][gr][1].y, beta[nt][gr][1]));
+                        const float(&P)[4] = S[st][nt];
+                        b0[nt] = transpose8(pack2(P[0] * v0.x, P[1] * v0.x));
+                        b1[nt] = transpose8(pack2(P[2] * v1.x, P[3] * v1.x));
+                        beta[nt][gr][0] = fmaf(P[0], v0.y, fmaf(P[2], v1.y, beta[nt][gr][0]));
+                        beta[nt][gr][1] = fmaf(P[1], v0.y, fmaf(P[3], v1.y, beta[nt][gr][1]));
                     }
 #pragma unroll
                     for (int cp = 0; cp < X::CPG; cp += 2) {
@@ -509,22 +587,15 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                         uint32_t w[4];
                         ldsm4t(w, va + (piece ^ (c0 << 4)));
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            uint32_t A[4];
-                            if (BITS == 4) {
+                        for (int j = 0; j < 2; ++j)
 #pragma unroll
-                                for (int q = 0; q < 2; ++q) {
-                                    v_frag<4>(w[2 * j], w[2 * j + 1], q, A);
+                            for (int q = 0; q < (BITS == 4 ? 2 : 1); ++q) {
+                                uint32_t A[4];
+                                v_frag<BITS>(w[2 * j], w[2 * j + 1], q, A);
 #pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt)
-                                        mma_16816(O[2 * (c0 + j) + q][nt], A, b0[nt], b1[nt]);
-                                }
-                            } else {
-                                v_frag<8>(w[2 * j], w[2 * j + 1], 0, A);
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) mma_16816(O[c0 + j][nt], A, b0[nt], b1[nt]);
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma_16816_v(O[(BITS == 4 ? 2 : 1) * (c0 + j) + q][nt], A, b0[nt], b1[nt]);
                             }
-                        }
                     }
                 }
             }
@@ -538,7 +609,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
             for (int i = 0; i < 2; ++i) {
                 l[nt][i] = sum_over_rows(l[nt][i]);
 #pragma unroll
-                for (int gr = 0; gr < X::GR; ++gr) beta[nt][gr][i] = sum_over_rows(beta[nt][gr][i]);
+                for (int gr = 0; gr < GR; ++gr) beta[nt][gr][i] = sum_over_rows(beta[nt][gr][i]);
                 if (g == 0) sml[(wid * NT + nt) * 8 + 2 * t + i] =
                                 make_float2(m[nt][i] == -INFINITY ? -INFINITY : mu[nt][i], l[nt][i]);
             }
@@ -563,7 +634,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                 float* dst = red + (wid * 8 + col) * X::kRedLd;
 #pragma unroll
                 for (int mt = 0; mt < X::MT; ++mt) {
-                    const float add = beta[nt][mt / (X::MT / X::GR)][i];
+                    const float add = beta[nt][mt / (X::MT / GR)][i];
                     const float2 v = make_float2((O[mt][nt][i] + add) * f, (O[mt][nt][i + 2] + add) * f);
                     *reinterpret_cast<float2*>(dst + dim_of<BITS>(mt, g)) = v;
                 }

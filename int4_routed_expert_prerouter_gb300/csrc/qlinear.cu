@@ -25,18 +25,6 @@ constexpr int kChunk = 4;               // groups per bulk copy
 constexpr int kChunkBytes = kChunk * kQ4Unit;
 constexpr int kPartLd = 20;             // floats per token of a warp's part: its stores then miss each other's banks
 
-// matrix steps that the compiler may move among the loads
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
-
 __device__ __forceinline__ void copy_bulk(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
                      smem_u32(dst)),
@@ -190,10 +178,10 @@ __global__ void __launch_bounds__(kThreadsQ) q4_few_kernel(const char* __restric
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float acc[4];
-                        mma_first(acc, A[0], xa[nt].x, xa[nt].y);
-                        mma(acc, A[1], xa[nt].z, xa[nt].w);
-                        mma(acc, A[2], xb[nt].x, xb[nt].y);
-                        mma(acc, A[3], xb[nt].z, xb[nt].w);
+                        mma_16816_first(acc, A[0], xa[nt].x, xa[nt].y);
+                        mma_16816_v(acc, A[1], xa[nt].z, xa[nt].w);
+                        mma_16816_v(acc, A[2], xb[nt].x, xb[nt].y);
+                        mma_16816_v(acc, A[3], xb[nt].z, xb[nt].w);
                         float(&o)[4] = y4[r][nt];
                         o[0] = fmaf(s0, acc[0], fmaf(sb0.y, xs[nt].x, o[0]));
                         o[1] = fmaf(s0, acc[1], fmaf(sb0.y, xs[nt].y, o[1]));
@@ -353,18 +341,18 @@ __global__ void __launch_bounds__(256, 2) q4_many_kernel(const char* __restrict_
                 const uint32_t(&b)[4][4] = bf[np & 1];
                 float acc[2][4];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) mma_first(acc[j], A[0], b[0][2 * j], b[0][2 * j + 1]);
+                for (int j = 0; j < 2; ++j) mma_16816_first(acc[j], A[0], b[0][2 * j], b[0][2 * j + 1]);
 #pragma unroll
                 for (int s = 1; s < 4; ++s)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) mma(acc[j], A[s], b[s][2 * j], b[s][2 * j + 1]);
+                    for (int j = 0; j < 2; ++j) mma_16816_v(acc[j], A[s], b[s][2 * j], b[s][2 * j + 1]);
                 if ((np & 3) == rw) {                         // each row-warp adds up its share of the tokens
                     float sum[2][4];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        mma_first(sum[j], ones, b[0][2 * j], b[0][2 * j + 1]);
+                        mma_16816_first(sum[j], ones, b[0][2 * j], b[0][2 * j + 1]);
 #pragma unroll
-                        for (int s = 1; s < 4; ++s) mma(sum[j], ones, b[s][2 * j], b[s][2 * j + 1]);
+                        for (int s = 1; s < 4; ++s) mma_16816_v(sum[j], ones, b[s][2 * j], b[s][2 * j + 1]);
                         if (g == 0)
                             *reinterpret_cast<float2*>(&xs[step & 1][half][(2 * np + j) * 8 + 2 * t]) =
                                 make_float2(sum[j][0], sum[j][1]);
