@@ -33,8 +33,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMaxGrid = 152 * 8;
-constexpr int kMinShare = 2 * kWarps;   // units a CTA takes at least
-constexpr int kSegCost = 6;             // what starting and joining a segment costs, in units
+constexpr int kMinShare = kWarps;       // units a CTA takes at least
+constexpr int kSegCost = 8;             // what starting and joining a segment costs, in units
 
 struct AttnP {
     kv::View c;
@@ -55,6 +55,7 @@ struct AttnP {
     __half* out;             // set: segments that one CTA has whole are written here
     long long ldo;
     int* status;
+    bool early;              // launched before the prefix's kernel has ended
 };
 
 template <int BITS, int D, int NT>
@@ -208,9 +209,12 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(sml) + X::kMl);
     long long* cum = reinterpret_cast<long long*>(bars + kWarps * X::STAGES);
     int* tokens = reinterpret_cast<int*>(cum + 257);
+    __shared__ int first_seq;
+    __shared__ long long share_s;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
     constexpr int kUnit = 16 * X::US;
 
+    launch_dependents();     // attn_join_kernel, which waits for this kernel's end
     // lengths, and the cost before each list: a scan over at most 256 of them
     const int per_list = p.H * p.RB;
     {
@@ -227,32 +231,38 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
         fence_mbar_init();
         __syncthreads();
         if (wid == 0) {
-            long long part[8], sum = 0;
-            if (lane * 8 < p.n_seq) {
+            long long part[9], sum = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int n = lane * 8 + j < p.n_seq ? tokens[lane * 8 + j] : 0;
-                    part[j] = sum;
-                    sum += n ? (long long)((n - 1) / kUnit + 1 + kSegCost) * per_list : 0;
-                }
+            for (int j = 0; j < 8; ++j) {
+                const int n = lane * 8 + j < p.n_seq ? tokens[lane * 8 + j] : 0;
+                part[j] = sum;
+                sum += n ? (long long)((n - 1) / kUnit + 1 + kSegCost) * per_list : 0;
             }
+            part[8] = sum;
             long long upto = sum;
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
                 const long long o = __shfl_up_sync(0xffffffffu, upto, s);
                 if (lane >= s) upto += o;
             }
-            if (lane * 8 < p.n_seq)
+            const long long total = __shfl_sync(0xffffffffu, upto, 31), before = upto - sum;
+            long long share = total < 0x7fffffff ? ((unsigned)total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
+            if (share < kMinShare + kSegCost) share = kMinShare + kSegCost;
+            const long long at = share * blockIdx.x - before;    // this CTA's first position, from this lane's lists on
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (lane * 8 + j < p.n_seq) cum[lane * 8 + j] = upto - sum + part[j];
-            if (lane == 31) cum[p.n_seq] = upto;
+            for (int j = 0; j < 8; ++j)
+                if (lane * 8 + j < p.n_seq) {
+                    cum[lane * 8 + j] = before + part[j];
+                    if (at >= part[j] && at < part[j + 1]) first_seq = lane * 8 + j;
+                }
+            if (lane == 31) {
+                cum[p.n_seq] = total;
+                share_s = share;
+            }
         }
         __syncthreads();
     }
-    const long long total = cum[p.n_seq];
-    long long share = total < 0x7fffffff ? ((unsigned)total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
-    if (share < kMinShare + kSegCost) share = kMinShare + kSegCost;
+    const long long total = cum[p.n_seq], share = share_s;
     long long pos = share * blockIdx.x;
     const long long end = pos + share < total ? pos + share : total;
 
@@ -268,16 +278,9 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
     // copies per unit: one where a unit's strips always lie in one page
     const int cpu = X::US == 1 || spp % X::US == 0 ? 1 : X::US;
 
-    int seq = 0;
+    int seq = pos < total ? first_seq : 0;
     while (pos < end) {
-        // the list that holds `pos`; one without tokens shares its successor's start, the search ends behind it
-        int lo = seq, hi = p.n_seq;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (cum[mid] <= pos) lo = mid;
-            else hi = mid;
-        }
-        seq = lo;
+        while (cum[seq + 1] <= pos) ++seq;                       // (lists without tokens take no room)
         const int n_tok = tokens[seq];
         const int units = (n_tok - 1) / kUnit + 1, cost = units + kSegCost;
         const long long in_list = pos - cum[seq];
@@ -676,6 +679,9 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
             __syncthreads();
         }
     }
+    // The prefix's kernel may still be running (this one is launched early and does not
+    // need it): its end is this kernel's end, so that the join finds both parts.
+    wait_predecessor();
 }
 
 struct JoinP {
@@ -692,62 +698,83 @@ struct JoinP {
     long long ldo;
 };
 
-// One warp per (sequence, query head): its own parts and the prefix's, in order.
+// One CTA per (sequence, query head): the prefix's parts, then its own, dealt to the four
+// warps in turn; bound by the latency of a few dependent reads, so the first parts are
+// on their way before the weights are known.
 template <int D>
 __global__ void __launch_bounds__(128) attn_join_kernel(const JoinP p) {
-    constexpr int kN = D / 32;
-    const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (row >= p.B * p.G * p.H) return;
+    constexpr int kN = D / 32, kBatch = 4;
+    __shared__ float acc[4][D];
+    const int row = blockIdx.x, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int b = row / (p.G * p.H), hq = row - b * p.G * p.H, h = hq / p.G, j = hq - h * p.G;
     const int len = p.lens[b];
+    wait_predecessor();
     if (len < 0) return;
-    __half* out = p.out + (long long)b * p.ldo + (long long)hq * D;
-    const float* o[2];
-    const float2* ml[2];
-    int n[2];
-    long long step[2];
+    // parts of the prefix [0, n0) and own parts [n0, n0 + n1)
+    int n0 = 0, n1 = 0;
+    const float* o[2] = {nullptr, nullptr};
+    const float2* ml[2] = {nullptr, nullptr};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        n[i] = 0;
-        o[i] = nullptr;
-        ml[i] = nullptr;
-        step[i] = 0;
-        if (i == 0 ? p.n_prefix == 0 : len == 0) continue;
-        const int w = i == 0 ? 1 : 0;     // the prefix first
+    for (int w = 0; w < 2; ++w) {
+        if (w ? p.n_prefix == 0 : len == 0) continue;
         const int r = w ? b * p.G + j : j;
         const int block = ((w ? 0 : b) * p.H + h) * p.RB[w] + r / p.rows[w];
         const int2 sg = w && p.splits ? make_int2(block * p.splits, p.splits) : p.seg[w][block];
-        n[i] = sg.y;
         const long long at = (long long)sg.x * p.rows[w] + r % p.rows[w];
-        o[i] = p.part_o[w] + at * D;
-        ml[i] = p.part_ml[w] + at;
-        step[i] = p.rows[w];
+        (w ? n0 : n1) = sg.y;
+        o[w ? 0 : 1] = p.part_o[w] + at * D;
+        ml[w ? 0 : 1] = p.part_ml[w] + at;
     }
-    if (p.n_prefix == 0 && n[1] == 1) return;       // written by the CTA that had it whole
-    float top = -INFINITY;
+    if (p.n_prefix == 0 && n1 == 1) return;         // written by the CTA that had it whole
+    const int n = n0 + n1;
+    const long long step0 = p.rows[1], step1 = p.rows[0];
+    auto ml_of = [&](int s) { return s < n0 ? ml[0][s * step0] : ml[1][(s - n0) * step1]; };
+    float v[kN], part[kBatch][kN];
+    auto fetch = [&](int s0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        for (int s = lane; s < n[i]; s += 32) top = fmaxf(top, ml[i][s * step[i]].x);
+        for (int u = 0; u < kBatch; ++u) {
+            const int s = s0 + 4 * u;
+            if (s < n) {
+                const float* src = (s < n0 ? o[0] + s * step0 * D : o[1] + (s - n0) * step1 * D) + lane * kN;
+#pragma unroll
+                for (int e = 0; e < kN; ++e) part[u][e] = src[e];
+            }
+        }
+    };
+    fetch(wid);
+    float top = -INFINITY, sum = 0.f;
+    for (int s = lane; s < n; s += 32) top = fmaxf(top, ml_of(s).x);
 #pragma unroll
     for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-    float sum = 0.f, v[kN];
+    auto weight = [&](float m) { return m == -INFINITY ? 1.f : ex2(m - top); };     // (a part of NaN keeps its NaN)
+    for (int s = lane; s < n; s += 32) {
+        const float2 x = ml_of(s);
+        sum = fmaf(x.y, weight(x.x), sum);
+    }
+    sum = warp_sum(sum);
 #pragma unroll
     for (int e = 0; e < kN; ++e) v[e] = 0.f;
+    for (int s0 = wid; s0 < n; s0 += 4 * kBatch) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll 4
-        for (int s = 0; s < n[i]; ++s) {
-            const float2 x = ml[i][s * step[i]];
-            const float f = x.x == -INFINITY ? 1.f : ex2(x.x - top);
-            sum = fmaf(x.y, f, sum);
-            const float* src = o[i] + s * step[i] * D + lane * kN;
+        for (int u = 0; u < kBatch; ++u) {
+            const int s = s0 + 4 * u;
+            if (s < n) {
+                const float f = weight(ml_of(s).x);
 #pragma unroll
-            for (int e = 0; e < kN; ++e) v[e] = fmaf(src[e], f, v[e]);
+                for (int e = 0; e < kN; ++e) v[e] = fmaf(part[u][e], f, v[e]);
+            }
         }
-    const float inv = n[0] + n[1] ? 1.f / sum : 0.f;
+        fetch(s0 + 4 * kBatch);
+    }
 #pragma unroll
-    for (int e = 0; e < kN; e += 2)
-        *reinterpret_cast<uint32_t*>(out + lane * kN + e) = pack2(v[e] * inv, v[e + 1] * inv);
+    for (int e = 0; e < kN; ++e) acc[wid][lane * kN + e] = v[e];
+    __syncthreads();
+    const float inv = n ? 1.f / sum : 0.f;          // no token at all: zeros
+    __half* out = p.out + (long long)b * p.ldo + (long long)hq * D;
+    for (int d = 2 * threadIdx.x; d < D; d += 256)
+        *reinterpret_cast<uint32_t*>(out + d) =
+            pack2(((acc[0][d] + acc[1][d]) + (acc[2][d] + acc[3][d])) * inv,
+                  ((acc[0][d + 1] + acc[1][d + 1]) + (acc[2][d + 1] + acc[3][d + 1])) * inv);
 }
 
 // Query rows that a CTA of one segment takes, 8 NT: the whole group of one sequence
@@ -817,8 +844,7 @@ int launch(const AttnP& p, long long most_units, cudaStream_t stream) {
     }
     const long long want = (most_units + kMinShare + kSegCost - 1) / (kMinShare + kSegCost);
     const int grid = want < n ? (int)(want < 1 ? 1 : want) : n;
-    attn_kernel<BITS, D, NT><<<grid, 32 * kWarps, X::kSmem, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? EDGE0_OK : EDGE0_ECUDA;
+    return launch_kernel(attn_kernel<BITS, D, NT>, dim3(grid), 32 * kWarps, X::kSmem, stream, p.early, p);
 }
 
 template <int BITS, int D>
@@ -904,6 +930,7 @@ extern "C" int edge0_attn_decode(const edge0_kv_cache* cache, const uint16_t* q,
         p.part_ml = (float2*)(ws + part[w].ml);
         p.seg = (int2*)(ws + part[w].seg);
         p.out = !w && !n_prefix ? (__half*)out : nullptr;
+        p.early = !w && n_prefix;
         rc = launch_any(p, cache->bits, D, part[w].NT, stream);
         if (rc) return rc;
     }
@@ -924,9 +951,8 @@ extern "C" int edge0_attn_decode(const edge0_kv_cache* cache, const uint16_t* q,
     j.splits = part[1].NT ? 0 : part[1].splits;
     j.out = (__half*)out;
     j.ldo = ldo;
-    const int grid = ceil_div(B * n_q_heads, 4);
-    if (D == 64) attn_join_kernel<64><<<grid, 128, 0, stream>>>(j);
-    else if (D == 128) attn_join_kernel<128><<<grid, 128, 0, stream>>>(j);
-    else attn_join_kernel<256><<<grid, 128, 0, stream>>>(j);
-    return cudaGetLastError() == cudaSuccess ? EDGE0_OK : EDGE0_ECUDA;
+    const int grid = B * n_q_heads;
+    if (D == 64) return launch_kernel(attn_join_kernel<64>, dim3(grid), 128, 0, stream, true, j);
+    if (D == 128) return launch_kernel(attn_join_kernel<128>, dim3(grid), 128, 0, stream, true, j);
+    return launch_kernel(attn_join_kernel<256>, dim3(grid), 128, 0, stream, true, j);
 }

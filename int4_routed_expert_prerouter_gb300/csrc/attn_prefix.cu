@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
     const int n = min(p.tiles_per_split, all - t0);
     const int r0 = rb * kRowsQ;
 
+    launch_dependents();     // the sequences' own parts do not need this kernel's results
     if (wid == 0) {
         tc::tmem_alloc(&taddr_s, X::kCols);
         tc::tmem_relinquish();
@@ -652,15 +653,22 @@ int launch(const PrefixP& p, cudaStream_t stream) {
             return EDGE0_ECUDA;
         __atomic_store_n(&set[dev], 1, __ATOMIC_RELEASE);
     }
-    attn_prefix_kernel<BITS, D><<<dim3(p.splits, p.RB, p.H), kThreads, Cfg<BITS, D>::kSmem, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? EDGE0_OK : EDGE0_ECUDA;
+    return launch_kernel(attn_prefix_kernel<BITS, D>, dim3(p.splits, p.RB, p.H), kThreads, Cfg<BITS, D>::kSmem, stream,
+                         false, p);
 }
 
 }  // namespace
 
+// Two CTAs per SM overlap tensor steps and softmax, but a share costs a start and a partial
+// result: at least kShareTiles steps each while every SM has one.  (17 shares of 3 steps
+// against 9 of 6, 64 x 4 query rows per head: 21.3 and 21.2 us, and 2.8 us less to join;
+// 9 shares of 15 against 4 of 32, 256 x 8 rows: 44.3 and 55.1 us.)
 void prefix_shares(int n_tok, int segs, int D, int sms, int* splits, int* tiles_per_split) {
+    constexpr int kShareTiles = 6;
     const int tiles = (n_tok - 1) / kTile + 1;
-    int s = sms * (D <= 128 ? 2 : 1) / segs;
+    int s = tiles / kShareTiles;
+    const int most = sms * (D <= 128 ? 2 : 1) / segs, least = sms / segs;
+    s = s > most ? most : s < least ? least : s;
     s = s < 1 ? 1 : s > tiles ? tiles : s;
     *tiles_per_split = ceil_div(tiles, s);
     *splits = ceil_div(tiles, *tiles_per_split);
