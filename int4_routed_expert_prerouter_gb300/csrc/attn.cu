@@ -17,9 +17,11 @@
 // up to 8 query heads wastes nothing:
 //   S^T = K Q^T   codes enter as fp16 subnormals q 2^-24 (exact products, fp32 sums); per 64
 //                 dims S += s acc + b sum(Q), in fp32: scores carry no rounding of K;
-//   O^T = V'^T P' V = s (q - z) + (b + s z), z half the code range: q - z is exact in
-//                 fp16, the weight p s is rounded to fp16 (its only rounding);
-//                 sum p (b + s z) is kept in fp32 beside it.
+//   O^T = V'^T P' V = s (q - z + r), z half the code range, r = b / s + z: q - z is
+//                 exact in fp16, the weight p s is rounded to fp16 (its only rounding),
+//                 and sum p s r, of the rounded weights, is kept in fp32 beside it: the
+//                 error is that of a rounded weight on the exact V.  (With sum p (b + s z)
+//                 of the unrounded weights it was a sixth larger.)
 // The exponents' reference is the running maximum plus the exponent of the largest V
 // scale so far, so that p s stays within fp16's normal range whatever the scales.
 // ldmatrix delivers K codes as A fragments and, transposed, V codes with the
@@ -177,6 +179,7 @@ __device__ __forceinline__ void load_sb(const char* p, uint32_t (&w)[GR]) {
         w[3 % GR] = v.w;
     }
 }
+// two fp16 of a word
 __device__ __forceinline__ float2 sb_of(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
 // B fragment words of one piece of one query row (lane t's dims; zeros where there is no row)
@@ -213,6 +216,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
     __shared__ long long share_s;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
     constexpr int kUnit = 16 * X::US;
+    constexpr float kZ = BITS == 4 ? 8.f : 128.f;
 
     launch_dependents();     // attn_join_kernel, which waits for this kernel's end
     // lengths, and the cost before each list: a scan over at most 256 of them
@@ -486,31 +490,44 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                 }
             }
 
-            // V's scales of the unit's tokens g and g + 8: (s, b + z s)
+            // V's scales of the unit's tokens g and g + 8: (s, r).  A token that is not there gets no
+            // weight, whatever its bytes.
             float2 vs[X::US][GR][2];
+            bool flat = false;
 #pragma unroll
             for (int st = 0; st < X::US; ++st)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     uint32_t w[GR];
                     load_sb<GR>(buf + st * X::STRIP + X::HALF + 16 * X::R + (g + 8 * i) * X::SB, w);
+                    if (left < kUnit && st * 16 + g + 8 * i >= left) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) S[st][nt][2 * i] = S[st][nt][2 * i + 1] = -INFINITY;
+#pragma unroll
+                        for (int gr = 0; gr < GR; ++gr) w[gr] = 1;           // s = 2^-24, b = 0
+                    }
 #pragma unroll
                     for (int gr = 0; gr < GR; ++gr) {
                         const float2 sb = sb_of(w[gr]);
-                        vs[st][gr][i] = make_float2(sb.x, fmaf(sb.x, BITS == 4 ? 8.f : 128.f, sb.y));
+                        float inv;
+                        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(sb.x));
+                        vs[st][gr][i] = make_float2(sb.x, fmaf(sb.y, inv, kZ));
+                        flat = flat || sb.x == 0.f;
                     }
                 }
-            if (left < kUnit) {              // tokens that are not there: no weight, whatever the bytes
+            if (__any_sync(0xffffffffu, flat)) {     // constant groups (s = 0, codes 0): b = |b| (0 - z + z +- 1)
 #pragma unroll
                 for (int st = 0; st < X::US; ++st)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        if (st * 16 + g + 8 * i >= left) {
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) S[st][nt][2 * i] = S[st][nt][2 * i + 1] = -INFINITY;
-#pragma unroll
-                            for (int gr = 0; gr < GR; ++gr) vs[st][gr][i] = make_float2(0.f, 0.f);
-                        }
+                        for (int gr = 0; gr < GR; ++gr)
+                            if (vs[st][gr][i].x == 0.f) {
+                                const float b = __half2float(*reinterpret_cast<const __half*>(
+                                    buf + st * X::STRIP + X::HALF + 16 * X::R + (g + 8 * i) * X::SB + gr * 4 + 2));
+                                vs[st][gr][i] = b == 0.f ? make_float2(1.f / kTwo24, kZ)
+                                                         : make_float2(fabsf(b), kZ + copysignf(1.f, b));
+                            }
             }
 
             // the reference moves when a score is 2^8 above it or a scale 2^6
@@ -579,10 +596,12 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const float(&P)[4] = S[st][nt];
-                        b0[nt] = transpose8(pack2(P[0] * v0.x, P[1] * v0.x));
-                        b1[nt] = transpose8(pack2(P[2] * v1.x, P[3] * v1.x));
-                        beta[nt][gr][0] = fmaf(P[0], v0.y, fmaf(P[2], v1.y, beta[nt][gr][0]));
-                        beta[nt][gr][1] = fmaf(P[1], v0.y, fmaf(P[3], v1.y, beta[nt][gr][1]));
+                        const uint32_t h0 = pack2(P[0] * v0.x, P[1] * v0.x), h1 = pack2(P[2] * v1.x, P[3] * v1.x);
+                        const float2 f0 = sb_of(h0), f1 = sb_of(h1);         // the rounded weights
+                        b0[nt] = transpose8(h0);
+                        b1[nt] = transpose8(h1);
+                        beta[nt][gr][0] = fmaf(f0.x, v0.y, fmaf(f1.x, v1.y, beta[nt][gr][0]));
+                        beta[nt][gr][1] = fmaf(f0.y, v0.y, fmaf(f1.y, v1.y, beta[nt][gr][1]));
                     }
 #pragma unroll
                     for (int cp = 0; cp < X::CPG; cp += 2) {

@@ -10,12 +10,12 @@
 //               each 64 dims g; accumulators and P' (over the scores that the same warp has
 //               read) in TMEM;
 //   warps 0-7   32 rows x 32 tokens each: S, running maximum and sum, weights p,
-//               P'_g = fp16(p s_g), and sum_j p (b_g + z s_g) in fp32.
+//               P'_g = fp16(p s_g), and sum_j P'_g r_g in fp32.
 // Scores: with K = s (code - z + r), r = b / s + z, a group's product is
 // Q_g (code - z) + mean(Q_g) 64 r; the second term is one more step of 16 of the same
 // product, its factors split into two fp16 each, so that S = sum_g s_g S_g carries no
-// rounding of K beyond 2^-22.  Each weight is rounded once (to fp16, 2^-11 of itself).
-// o = (O_g + sum p (b_g + z s_g)) / sum p.  The exponents' reference is the running
+// rounding of K beyond 2^-22.  Each weight is rounded once (to fp16, 2^-11 of itself):
+// with V = s (code - z + r) likewise, o = (O_g + sum P'_g r_g) / sum p.  The exponents' reference is the running
 // maximum plus the exponent of the largest scale so far, so that p s stays within
 // fp16's normal range whatever the scales; it moves only when a score exceeds it by
 // 2^8 or a scale by 2^6, and the accumulators are then rescaled in TMEM.
@@ -46,7 +46,7 @@ struct Cfg {
     static constexpr int kMean = GR * kRowsQ * 32;          // means of Q_g, a step of 16 each
     static constexpr int kOp = kTile * D * 2;               // one operand tile
     static constexpr int kOffs = kTile * 32;                // r of the tile's tokens, a step of 16
-    static constexpr int kTab = 3 * GR * kTile * 4;         // K s; V (s, b + z s)
+    static constexpr int kTab = 3 * GR * kTile * 4;         // K s; V (s, r)
     static constexpr int kStage = 2 * kOp + kOffs + kTab;
     static constexpr int kSmem = kQ + kMean + 2 * kStage;
     static constexpr int kCols = GR * kTile + D <= 128 ? 128 : GR * kTile + D <= 256 ? 256 : 512;
@@ -350,13 +350,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                 const int tok = 16 * w + e / GR, gr = e % GR;
                 float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&rs[j]));
                 const bool none = tok >= left;
+                const bool flat = sb.x == 0.f;                 // a constant group: codes 0
                 if (v) {
+                    // b = |b| (0 - z + z +- 1)
                     float* at = tab_v + ((tok >> 1) * GR + gr) * 4 + (tok & 1);
-                    at[0] = none ? 0.f : sb.x;
-                    at[2] = none ? 0.f : fmaf(sb.x, kZ, sb.y);
+                    const float s = !flat ? sb.x : sb.y == 0.f ? 1.f / kTwo24 : fabsf(sb.y);
+                    at[0] = none ? 0.f : s;
+                    at[2] = none ? 0.f : __fdividef(sb.y, s) + kZ;
                 } else {
-                    // a constant group (s = 0, codes 0): b = 1 (0 - z + b + z)
-                    const bool flat = sb.x == 0.f;
+                    // b = 1 (0 - z + b + z)
                     const float off = flat ? sb.y + kZ : __fdividef(sb.y, sb.x) + kZ;
                     tab_k[(tok >> 1) * 2 * GR + 2 * gr + (tok & 1)] = none ? 0.f : (flat ? 1.f : sb.x) * p.k * 1024.f;
                     const uint32_t hl = split(none ? 0.f : off * (kGroup / 1024.f));
@@ -552,7 +554,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                             float a, b;
                             unpk(mul2(S[rh][j][k], sc[j].x), a, b);
                             w[2 * j + k] = pack2(a, b);
-                            acc[k] = j ? fma2(S[rh][j][k], sc[j].y, acc[k]) : mul2(S[rh][j][k], sc[j].y);
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[2 * j + k]));
+                            acc[k] = j ? fma2(pk(f.x, f.y), sc[j].y, acc[k]) : mul2(pk(f.x, f.y), sc[j].y);
                         }
                     tmem_st_pairs(my + ((uint32_t)(16 * rh) << 16) + gr * kTile + hf * 32, w);
 #pragma unroll
