@@ -232,26 +232,35 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
         fence_mbar_init();
         dead = 0;
     }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = taddr_s;
+
     if (wid < 8) {
-        // queries, K-major, 8 dims in the order of the codes
-        for (int i = tid; i < kRowsQ * (D / 8); i += kSoftmax) {
-            const int r = (i & 7) + 8 * (i / (8 * (D / 8))), c8 = (i >> 3) % (D / 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r0 + r < p.rows) {
-                const int row = r0 + r;
-                v = *reinterpret_cast<const uint4*>(p.q + (long long)(row / p.G) * p.ldq +
-                                                    (long long)(h * p.G + row % p.G) * D + 8 * c8);
-                if (BITS == 4)
-                    v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                                   __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-            }
-            *reinterpret_cast<uint4*>(sQ + (c8 >> 1) * (kRowsQ * 32) + tc::kstep_off(r, (c8 & 1) * 8)) = v;
+        // queries, K-major, 8 dims in the order of the codes; a thread's pieces 16 rows (of D = 128) apart
+        constexpr int kC8 = D / 8, kApart = kSoftmax / kC8, kPer = kRowsQ / kApart;
+        const int c8 = (tid >> 3) % kC8, rq = (tid & 7) + 8 * (tid / (8 * kC8));
+        uint4 v[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int row = r0 + rq + kApart * j;
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (row < p.rows)
+                v[j] = *reinterpret_cast<const uint4*>(p.q + (long long)(row / p.G) * p.ldq +
+                                                       (long long)(h * p.G + row % p.G) * D + 8 * c8);
         }
-        // means' and offsets' tiles: zero where nothing is written below
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int r = rq + kApart * j;
+            const uint4 x = v[j];
+            *reinterpret_cast<uint4*>(sQ + (c8 >> 1) * (kRowsQ * 32) + tc::kstep_off(r, (c8 & 1) * 8)) =
+                BITS == 4 ? make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                                       __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632))
+                          : x;
+        }
+        // the means' tiles: zero where nothing is written below
         for (int i = tid; i < X::kMean / 16; i += kSoftmax) reinterpret_cast<uint4*>(sM)[i] = make_uint4(0, 0, 0, 0);
-        for (int i = tid; i < X::kOffs / 16; i += kSoftmax)
-            for (int s = 0; s < 2; ++s)
-                reinterpret_cast<uint4*>(stages + s * X::kStage + 2 * X::kOp)[i] = make_uint4(0, 0, 0, 0);
         named_bar_sync(2, kSoftmax);
         for (int i = tid; i < kRowsQ * GR; i += kSoftmax) {
             const int r = i % kRowsQ, gr = i / kRowsQ;
@@ -270,13 +279,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             const uint32_t hl = split(s * (1.f / kGroup));     // (hi, lo), against (hi, hi, lo, lo) of r
             *reinterpret_cast<uint2*>(sM + gr * (kRowsQ * 32) + tc::kstep_off(r, 4 * gr)) = make_uint2(hl, hl);
         }
+        tc::fence_async_smem();
+        named_bar_sync(2, kSoftmax);
     }
-    tc::fence_async_smem();
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
-    const uint32_t tm = taddr_s;
-
     if (wid >= 8) {
         // ---------------------------------------------------------- operands
         if (X::kCtas == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
@@ -371,6 +376,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             if (lane == 0) mbar_arrive(&full[i & 1]);
         };
         load();
+        // the offsets' tiles of this warp's tokens in both stages: zero where put() writes nothing
+        {
+            char* sR = stages + (lane >> 4) * X::kStage + 2 * X::kOp;
+            *reinterpret_cast<uint4*>(sR + tc::kstep_off(16 * w + (lane & 15), 0)) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(sR + tc::kstep_off(16 * w + (lane & 15), 8)) = make_uint4(0, 0, 0, 0);
+            __syncwarp();
+        }
         for (int i = 0; i < n; ++i) {
             if (i >= 2 && !__all_sync(0xffffffffu, wait_bar(&freed[i & 1], ((i >> 1) - 1) & 1, &dead))) break;
             put(i);
@@ -586,8 +598,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             __syncwarp();
         }
         ok = wait_bar(&freed[(n - 1) & 1], ((n - 1) >> 1) & 1, &dead) && ok;
-        // a row's sums: its 4 lanes, then both halves of the tokens (over the queries, done with by now)
-        float* sums = reinterpret_cast<float*>(sQ);            // [hf][1 + GR][row]
+        // a row's sums: its 4 lanes, then both halves of the tokens (all operands are done with by now)
+        float* sums = reinterpret_cast<float*>(smem);          // [hf][1 + GR][row]
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int row = 32 * quad + 16 * (r >> 1) + g + 8 * (r & 1);
@@ -605,6 +617,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
         if (__all_sync(0xffffffffu, ok)) {
             tc::fence_after_sync();
             const long long slot = ((long long)h * p.RB + rb) * p.splits + blockIdx.x;
+            // rows of o in shared memory, 16 bytes apart so that eight of them do not share banks, and
+            // from there in one copy each
+            constexpr int kLd = D + 4;
+            float* rows = reinterpret_cast<float*>(smem + 2 * (1 + GR) * kRowsQ * 4);
 #pragma unroll
             for (int c = 0; c < D / 64 * 2; ++c) {
                 const int rh = c & 1, d0 = hf * (D / 2) + (c >> 1) * 32, gr = d0 / kGroup;
@@ -615,19 +631,29 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                 for (int k = 0; k < 2; ++k) {
                     const int row = 32 * quad + 16 * rh + g + 8 * k;
                     const float add = sums[(1 + gr) * kRowsQ + row] + sums[(1 + GR + 1 + gr) * kRowsQ + row];
-                    float* dst = p.part_o + (slot * kRowsQ + row) * D + d0;
-                    if (r0 + row < p.rows)
+                    float* dst = rows + row * kLd + d0;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float x = __uint_as_float(a[4 * j + 2 * k]) + add, y = __uint_as_float(a[4 * j + 2 * k + 1]) + add;
-                            if (BITS == 4) {                   // columns 2t, 2t + 1 hold dims t, t + 4
-                                dst[8 * j + t] = x;
-                                dst[8 * j + t + 4] = y;
-                            } else {
-                                *reinterpret_cast<float2*>(dst + 8 * j + 2 * t) = make_float2(x, y);
-                            }
+                    for (int j = 0; j < 4; ++j) {
+                        const float x = __uint_as_float(a[4 * j + 2 * k]) + add, y = __uint_as_float(a[4 * j + 2 * k + 1]) + add;
+                        if (BITS == 4) {                       // columns 2t, 2t + 1 hold dims t, t + 4
+                            dst[8 * j + t] = x;
+                            dst[8 * j + t + 4] = y;
+                        } else {
+                            *reinterpret_cast<float2*>(dst + 8 * j + 2 * t) = make_float2(x, y);
                         }
+                    }
                 }
+            }
+            tc::fence_async_smem();
+            named_bar_sync(8 + quad, 64);                      // both halves of these 32 rows
+            if (hf == 0) {
+                const int row = 32 * quad + lane;
+                if (r0 + row < p.rows)
+                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(
+                                     p.part_o + (slot * kRowsQ + row) * D),
+                                 "r"(smem_u32(rows + row * kLd)), "r"(D * 4)
+                                 : "memory");
+                asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
             }
             if (hf == 0 && t == 0)
 #pragma unroll
@@ -636,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                     if (r0 + row < p.rows)
                         p.part_ml[slot * kRowsQ + row] = make_float2(mu[r], sums[row] + sums[(1 + GR) * kRowsQ + row]);
                 }
+            if (hf == 0) asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
         }
     }
     tc::fence_before_sync();
