@@ -6,7 +6,6 @@ library and raises if it is missing -- there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import os
 
@@ -590,39 +589,42 @@ def _bad(what):
     return Edge0Error(EDGE0_EINVAL, what)
 
 
-_SAME_DEVICE = contextlib.nullcontext()
-
-
-def _on(index, stream):
-    """Allocations and launches of one call: the tensors' device, the call's stream."""
+def _guard(index, stream):
+    """The context of a call whose allocations and launches are not the current device's and
+    stream's: that stream (its device too), or that device; None where they are."""
     if stream is not None:
-        return torch.cuda.stream(stream)      # its device too
-    return _SAME_DEVICE if index == torch.cuda.current_device() else torch.cuda.device(index)
+        return torch.cuda.stream(stream)
+    return None if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
 def _raw_stream(index, stream):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
 
 
+_f16, _i32_t, _u8 = torch.float16, torch.int32, torch.uint8
+
+
 def _row_stride(t, what):
     """Row stride of fp16 rows [T, n] or [T, heads, n] on a GPU that are dense within a row
     (a slice of a wider row-major tensor passes)."""
-    if t.dtype is not torch.float16 or not t.is_cuda:
+    if t.dtype is not _f16 or not t.is_cuda:
         raise _bad(f"{what}: fp16 on a GPU")
     shape, stride = t.shape, t.stride()
     if len(shape) == 2:
-        dense, row = stride[1] == 1 or shape[1] == 1, shape[1]
+        n, row = shape
+        if stride[1] != 1 and row != 1:
+            raise _bad(f"{what}: rows that are not dense")
     else:
-        row = shape[1] * shape[2]
-        dense = (stride[2] == 1 or shape[2] == 1) and (stride[1] == shape[2] or shape[1] == 1)
-    if not dense:
-        raise _bad(f"{what}: rows that are not dense")
+        n, heads, width = shape
+        row = heads * width
+        if (stride[2] != 1 and width != 1) or (stride[1] != width and heads != 1):
+            raise _bad(f"{what}: rows that are not dense")
     # the row stride of one row or none says nothing; the row's own length rounded up does
-    return stride[0] if shape[0] > 1 else (row + 7) // 8 * 8
+    return stride[0] if n > 1 else (row + 7) // 8 * 8
 
 
-def _i32(t, index, n, what):
-    if t.dtype is not torch.int32 or t.get_device() != index or t.numel() != n or not t.is_contiguous():
+def _ints(t, index, n, what):
+    if t.dtype is not _i32_t or t.get_device() != index or t.numel() != n or not t.is_contiguous():
         raise _bad(f"{what}: {n} int32, contiguous, on cuda:{index}")
     return t.data_ptr()
 
@@ -630,24 +632,33 @@ def _i32(t, index, n, what):
 def q4_linear(packed: torch.Tensor, out_features: int, x: torch.Tensor, y=None, stream=None) -> torch.Tensor:
     """y [B, out_features] = W x for x [B, in] fp16 and W packed by pack_q4_rows (one
     matrix: E = 1).  x and y may be slices of wider rows."""
+    index = x.get_device()
+    guard = _guard(index, stream)
+    if guard is not None:
+        with guard:
+            return _q4_linear(packed, out_features, x, y, index, stream)
+    return _q4_linear(packed, out_features, x, y, index, None)
+
+
+def _q4_linear(packed, out_features, x, y, index, stream):
     if x.dim() != 2:
         raise _bad("q4_linear: x [B, in]")
-    B, n_in = x.shape
     ldx = _row_stride(x, "q4_linear: x")
-    index = x.get_device()
-    if (packed.dtype is not torch.uint8 or packed.get_device() != index or not packed.is_contiguous() or n_in % 64
+    B, n_in = x.shape
+    if (packed.dtype is not _u8 or packed.get_device() != index or not packed.is_contiguous() or n_in % 64
             or packed.numel() != (out_features + 15) // 16 * (n_in // 64) * 576 or out_features <= 0 or n_in == 0):
         raise _bad("q4_linear: packed is not an [out_features, in] matrix beside x")
-    with _on(index, stream):
-        if y is None:
-            y, ldy = torch.empty((B, out_features), dtype=torch.float16, device=x.device), out_features
-        else:
-            if y.shape != (B, out_features) or y.get_device() != index:
-                raise _bad("q4_linear: y [B, out_features] beside x")
-            ldy = max(_row_stride(y, "q4_linear: y"), out_features)
-        if B:
-            _check(lib().edge0_q4_linear(packed.data_ptr(), out_features, n_in, x.data_ptr(), ldx, B, y.data_ptr(), ldy,
-                                         _raw_stream(index, stream)), "edge0_q4_linear")
+    if y is None:
+        y, ldy = torch.empty((B, out_features), dtype=_f16, device=x.device), out_features
+    else:
+        if y.shape != (B, out_features) or y.get_device() != index:
+            raise _bad("q4_linear: y [B, out_features] beside x")
+        ldy = max(_row_stride(y, "q4_linear: y"), out_features)
+    if B:
+        code = (_lib or lib()).edge0_q4_linear(packed.data_ptr(), out_features, n_in, x.data_ptr(), ldx, B, y.data_ptr(), ldy,
+                                               _raw_stream(index, stream))
+        if code:
+            raise Edge0Error(code, "edge0_q4_linear")
     return y
 
 
@@ -695,50 +706,68 @@ def _sequences(cache, table, start, cu_rows, T, what):
     index = cache._index
     if cu_rows is None and T != B:
         raise _bad(f"{what}: one row per sequence without cu_rows")
-    return (_i32(table, index, B * W, "table"), B, W, _i32(start, index, B, "start"),
-            None if cu_rows is None else _i32(cu_rows, index, B + 1, "cu_rows"))
+    return (_ints(table, index, B * W, "table"), B, W, _ints(start, index, B, "start"),
+            None if cu_rows is None else _ints(cu_rows, index, B + 1, "cu_rows"))
 
 
 def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table, start, cu_rows=None, stream=None):
     """Quantise rows k, v [T, n_kv_heads, head_dim] fp16 into the pages: row r of
     sequence b goes to position start[b] + r - cu_rows[b] (cu_rows None: row b is
     sequence b's).  table [B, W], start [B], cu_rows [B + 1]: int32 on the device."""
+    guard = _guard(cache._index, stream)
+    if guard is not None:
+        with guard:
+            return _kv_append(cache, k, v, table, start, cu_rows, stream)
+    return _kv_append(cache, k, v, table, start, cu_rows, None)
+
+
+def _kv_append(cache, k, v, table, start, cu_rows, stream):
     T, index = k.shape[0], cache._index
     shape = (T, cache.n_kv_heads, cache.head_dim)
     if k.shape != shape or v.shape != shape or k.get_device() != index or v.get_device() != index:
         raise _bad(f"kv_append: k and v {list(shape)} beside the cache")
     ldk, ldv = _row_stride(k, "kv_append: k"), _row_stride(v, "kv_append: v")
     tb, B, W, st, cu = _sequences(cache, table, start, cu_rows, T, "kv_append")
-    with _on(index, stream):
-        _check(lib().edge0_kv_append(cache._desc, k.data_ptr(), ldk, v.data_ptr(), ldv, T, tb, B, W, st, cu,
-                                     cache._status, _raw_stream(index, stream)), "edge0_kv_append")
+    code = _lib.edge0_kv_append(cache._desc, k.data_ptr(), ldk, v.data_ptr(), ldv, T, tb, B, W, st, cu, cache._status,
+                                _raw_stream(index, stream))
+    if code:
+        raise Edge0Error(code, "edge0_kv_append")
 
 
 def kv_read(cache: KVCache, table, start, cu_rows=None, T=None, k=None, v=None, stream=None):
     """(k, v) [T, n_kv_heads, head_dim] fp16: the values that the rows' pages stand for
     (rows as in kv_append).  k, v: contiguous outputs to fill, or None for new ones; rows
     that no sequence has are left as they are."""
+    guard = _guard(cache._index, stream)
+    if guard is not None:
+        with guard:
+            return _kv_read(cache, table, start, cu_rows, T, k, v, stream)
+    return _kv_read(cache, table, start, cu_rows, T, k, v, None)
+
+
+def _kv_read(cache, table, start, cu_rows, T, k, v, stream):
     T = table.shape[0] if T is None else T
     tb, B, W, st, cu = _sequences(cache, table, start, cu_rows, T, "kv_read")
     index, shape = cache._index, (T, cache.n_kv_heads, cache.head_dim)
-    with _on(index, stream):
-        if k is None and v is None:
-            k = torch.empty(shape, dtype=torch.float16, device=cache.device)
-            v = torch.empty(shape, dtype=torch.float16, device=cache.device)
-        else:
-            k, v = (torch.empty(shape, dtype=torch.float16, device=cache.device) if o is None else o for o in (k, v))
-            for o in (k, v):
-                if o.dtype is not torch.float16 or o.shape != shape or o.get_device() != index or not o.is_contiguous():
-                    raise _bad(f"kv_read: outputs fp16 {list(shape)}, contiguous, beside the cache")
-        _check(lib().edge0_kv_read(cache._desc, tb, B, W, st, cu, T, k.data_ptr(), v.data_ptr(), cache._status,
-                                   _raw_stream(index, stream)), "edge0_kv_read")
+    out = []
+    for o in (k, v):
+        if o is None:
+            o = torch.empty(shape, dtype=_f16, device=cache.device)
+        elif o.dtype is not _f16 or o.shape != shape or o.get_device() != index or not o.is_contiguous():
+            raise _bad(f"kv_read: outputs fp16 {list(shape)}, contiguous, beside the cache")
+        out.append(o)
+    k, v = out
+    code = _lib.edge0_kv_read(cache._desc, tb, B, W, st, cu, T, k.data_ptr(), v.data_ptr(), cache._status,
+                              _raw_stream(index, stream))
+    if code:
+        raise Edge0Error(code, "edge0_kv_read")
     return k, v
 
 
 def attn_workspace_bytes(cache: KVCache, B: int, n_q_heads: int) -> int:
     n = cache._ws_bytes.get((B, n_q_heads))
     if n is None:
-        n = cache._ws_bytes[B, n_q_heads] = int(lib().edge0_attn_workspace_bytes(cache._desc, B, n_q_heads))
+        n = cache._ws_bytes[B, n_q_heads] = int(_lib.edge0_attn_workspace_bytes(cache._desc, B, n_q_heads))
     return n
 
 
@@ -750,6 +779,14 @@ def attn_decode(cache: KVCache, q: torch.Tensor, table, lens, prefix=None, n_pre
     unless given.  out: rows to fill (those of sequences with lens[b] < 0 are left as
     they are) or None.  workspace: uint8 of attn_workspace_bytes, or None for one of the
     call's own."""
+    guard = _guard(cache._index, stream)
+    if guard is not None:
+        with guard:
+            return _attn_decode(cache, q, table, lens, prefix, n_prefix, scale, out, workspace, stream)
+    return _attn_decode(cache, q, table, lens, prefix, n_prefix, scale, out, workspace, None)
+
+
+def _attn_decode(cache, q, table, lens, prefix, n_prefix, scale, out, workspace, stream):
     index = cache._index
     if q.dim() != 3 or q.shape[2] != cache.head_dim or q.get_device() != index:
         raise _bad("attn_decode: q [B, n_q_heads, head_dim] beside the cache")
@@ -758,26 +795,28 @@ def attn_decode(cache: KVCache, q: torch.Tensor, table, lens, prefix=None, n_pre
     if table.dim() != 2 or table.shape[0] != B:
         raise _bad("attn_decode: table [B, W]")
     W = table.shape[1]
-    tb, ln = _i32(table, index, B * W, "attn_decode: table"), _i32(lens, index, B, "attn_decode: lens")
+    tb, ln = _ints(table, index, B * W, "attn_decode: table"), _ints(lens, index, B, "attn_decode: lens")
     pf = None
     if n_prefix:
         if n_prefix < 0 or prefix is None or prefix.numel() * cache.page_tokens < n_prefix:
             raise _bad("attn_decode: n_prefix tokens in the pages `prefix`")
-        pf = _i32(prefix, index, prefix.numel(), "attn_decode: prefix")
+        pf = _ints(prefix, index, prefix.numel(), "attn_decode: prefix")
+    if out is None:
+        out, ldo = torch.empty((B, Hq, D), dtype=_f16, device=cache.device), Hq * D
+    else:
+        if out.shape != q.shape or out.get_device() != index:
+            raise _bad("attn_decode: out like q")
+        ldo = _row_stride(out, "attn_decode: out")
     nbytes = attn_workspace_bytes(cache, B, Hq)
-    with _on(index, stream):
-        if out is None:
-            out, ldo = torch.empty((B, Hq, D), dtype=torch.float16, device=cache.device), Hq * D
-        else:
-            if out.shape != q.shape or out.get_device() != index:
-                raise _bad("attn_decode: out like q")
-            ldo = _row_stride(out, "attn_decode: out")
-        if workspace is None:
-            workspace = torch.empty(nbytes or 16, dtype=torch.uint8, device=cache.device)
-        elif workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
+    if workspace is None:
+        workspace = torch.empty(nbytes or 16, dtype=_u8, device=cache.device)
+    else:
+        if workspace.dtype is not _u8 or workspace.get_device() != index or not workspace.is_contiguous():
             raise _bad("attn_decode: workspace uint8, contiguous, beside the cache")
-        _check(lib().edge0_attn_decode(cache._desc, q.data_ptr(), ldq, B, Hq, tb, W, ln, pf, n_prefix,
-                                       D ** -0.5 if scale is None else scale, out.data_ptr(), ldo, cache._status,
-                                       workspace.data_ptr(), workspace.numel(), _raw_stream(index, stream)),
-               "edge0_attn_decode")
+        nbytes = workspace.numel()
+    code = _lib.edge0_attn_decode(cache._desc, q.data_ptr(), ldq, B, Hq, tb, W, ln, pf, n_prefix,
+                                  D ** -0.5 if scale is None else scale, out.data_ptr(), ldo, cache._status,
+                                  workspace.data_ptr(), nbytes, _raw_stream(index, stream))
+    if code:
+        raise Edge0Error(code, "edge0_attn_decode")
     return out

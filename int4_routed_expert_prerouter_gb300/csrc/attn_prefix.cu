@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                     if (r0 + row < p.rows)
                         p.part_ml[slot * kRowsQ + row] = make_float2(mu[r], sums[row] + sums[(1 + GR) * kRowsQ + row]);
                 }
-            if (hf == 0) asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+            if (hf == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
         }
     }
     tc::fence_before_sync();
