@@ -428,9 +428,10 @@ int edge0_q4_linear(const void* packed, int out, int in, const uint16_t* x, long
 /* A pool of n_pages pages of K and V codes at `pages` (16-byte aligned, n_pages *
  * edge0_kv_page_bytes bytes, owned by the caller).  Sequences are lists of pages.
  * Per (token, kv head, K or V, 64 dims), with mn and mx over the 64 fp16 values:
- *   s = fp16((mx - mn) / (2^bits - 1)), b = mn, q = rne((x - mn) / s) in
- *   [0, 2^bits - 1] (0 where s = 0); the group stands for s q + b.  A group with an
- *   infinity or NaN stands for NaN throughout.
+ *   s = fp16((mx - mn) / (2^bits - 1)) (the next fp16 below where (2^bits - 1) s + mn
+ *   would round to infinity), b = mn, q = rne((x - mn) / s) in [0, 2^bits - 1] (0
+ *   where s = 0); the group stands for s q + b.  A group with an infinity or NaN stands
+ *   for NaN throughout.
  * Page: [kv head][strip of 16 tokens][K codes | K (s, b) | V codes | V (s, b)]; a token's
  * codes are R = head_dim * bits / 8 bytes (4 bits: dim 2j in the low half of byte j), its
  * 16-byte piece c stored at piece c ^ turn(r) of row r = token % 16, turn(r) = r & 7 for

@@ -728,6 +728,8 @@ def _kv_append(cache, k, v, table, start, cu_rows, stream):
         raise _bad(f"kv_append: k and v {list(shape)} beside the cache")
     ldk, ldv = _row_stride(k, "kv_append: k"), _row_stride(v, "kv_append: v")
     tb, B, W, st, cu = _sequences(cache, table, start, cu_rows, T, "kv_append")
+    if T == 0:
+        return
     code = _lib.edge0_kv_append(cache._desc, k.data_ptr(), ldk, v.data_ptr(), ldv, T, tb, B, W, st, cu, cache._status,
                                 _raw_stream(index, stream))
     if code:
@@ -757,6 +759,8 @@ def _kv_read(cache, table, start, cu_rows, T, k, v, stream):
             raise _bad(f"kv_read: outputs fp16 {list(shape)}, contiguous, beside the cache")
         out.append(o)
     k, v = out
+    if T == 0:
+        return k, v
     code = _lib.edge0_kv_read(cache._desc, tb, B, W, st, cu, T, k.data_ptr(), v.data_ptr(), cache._status,
                               _raw_stream(index, stream))
     if code:
@@ -807,6 +811,8 @@ def _attn_decode(cache, q, table, lens, prefix, n_prefix, scale, out, workspace,
         if out.shape != q.shape or out.get_device() != index:
             raise _bad("attn_decode: out like q")
         ldo = _row_stride(out, "attn_decode: out")
+    if B == 0:
+        return out
     nbytes = attn_workspace_bytes(cache, B, Hq)
     if workspace is None:
         workspace = torch.empty(nbytes or 16, dtype=_u8, device=cache.device)

@@ -83,7 +83,7 @@ struct Cfg {
     static constexpr int kMl = kWarps * NT * 8 * 8;
     static constexpr int kRing = kRingBytes > kRed ? kRingBytes : kRed;
     static constexpr int kSmem = kRing + kQ + kQsum + kMl + kWarps * STAGES * 8 + 257 * 8 + 256 * 4;
-    static constexpr int kMinCtas = NT == 1 && D <= 128 ? 4 : NT == 4 ? 2 : D == 256 && NT == 2 ? 2 : 3;
+    static constexpr int kMinCtas = NT == 1 && D <= 128 ? 4 : NT == 4 || (D == 256 && NT == 2) ? 2 : 3;
 };
 
 __device__ __forceinline__ void copy_strip(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -797,15 +797,20 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinP p) {
 }
 
 // Query rows that a CTA of one segment takes, 8 NT: the whole group of one sequence
-// where it fits 16; of the prefix's rows as many as registers hold (32, or 16 of
-// 256-wide heads), fewer when there are fewer.
+// where it fits 16; of the prefix's rows up to 32 of 64-wide heads (of wider ones the
+// accumulators of 32 rows do not fit the registers).
 int nt_of(int rows, int D, bool prefix) {
     if (rows <= 8) return 1;
-    return rows <= 16 || D == 256 || !prefix ? 2 : 4;
+    return rows <= 16 || D != 64 || !prefix ? 2 : 4;
 }
 
-// The prefix's rows per K/V head from which the fifth-generation tensor cores take it.
-constexpr int kPrefixFrom = 33;
+// The prefix's rows per K/V head from which the fifth-generation tensor cores take it (a step
+// of theirs costs the same for any number of rows up to 128).  Measured on prefixes of 700
+// to 16,000 tokens, this file's kernel against theirs, us: D = 128, 16 rows 12-21 and 12-34,
+// 32 rows 17-35 and 11-34; D = 64, 32 rows 11-23 and 10-29, 64 rows 12-26 and 10-30, from
+// there on theirs hold while this one's grow; D = 256, 32 rows 15-44 and 14-54, 64 rows
+// 15-65 and 15-55.
+int prefix_from(int D) { return D == 64 ? 65 : D == 128 ? 17 : 33; }
 constexpr int kSmsAssumed = 152;      // for the workspace's size; a card with fewer needs less
 
 struct Part {
@@ -820,7 +825,7 @@ long long layout(int B, int G, int H, int D, int n_prefix, Part (&part)[2]) {
     for (int w = 0; w < 2; ++w) {
         Part& x = part[w];
         const int rows = w ? B * G : G;
-        x.NT = w && rows >= kPrefixFrom ? 0 : nt_of(rows, D, w == 1);
+        x.NT = w && rows >= prefix_from(D) ? 0 : nt_of(rows, D, w == 1);
         x.rows = x.NT ? 8 * x.NT : kPrefixRows;
         x.RB = ceil_div(rows, x.rows);
         x.segs = (w ? 1 : B) * H * x.RB;
@@ -873,7 +878,7 @@ int launch_nt(const AttnP& p, int NT, cudaStream_t stream) {
     const long long most = ((cap + kUnit - 1) / kUnit + kSegCost) * p.n_seq * p.H * p.RB;
     if (NT == 1) return launch<BITS, D, 1>(p, most, stream);
     if (NT == 2) return launch<BITS, D, 2>(p, most, stream);
-    if constexpr (D <= 128) return launch<BITS, D, 4>(p, most, stream);
+    if constexpr (D == 64) return launch<BITS, D, 4>(p, most, stream);
     return EDGE0_EUNSUPPORTED;
 }
 

@@ -3,7 +3,8 @@
 //
 // Per (token, kv head, K or V, 64 dims): mn, mx over the 64 fp16 values;
 //     s = fp16((mx - mn) / (2^bits - 1)), b = mn,
-//     q = clamp(rne((x - mn) / s), 0, 2^bits - 1)    (0 where s = 0),
+//     q = clamp(rne((x - mn) / s), 0, 2^bits - 1)    (0 where s = 0);
+// s one fp16 step less where (2^bits - 1) s + b would round to infinity,
 // and the stored group stands for s q + b.  q is the exact quotient's rounding: the
 // kernel rounds the fp32 product (x - mn) * (1 / s), and where that lies next to
 // a border it decides by the sign of (x - mn) - (q +- 1/2) s, which fp32 holds
@@ -122,7 +123,9 @@ __device__ __forceinline__ void quantise16(const uint4 (&raw)[2], uint32_t (&wor
     const float mn = __low2float(w), mx = -__high2float(w);
     // (mx - mn) / kTop rounded to nearest: with the rounded reciprocal one residual step is exact
     const float range = mx - mn, s0 = range * (1.f / kTop);
-    const __half s16 = __float2half_rn(fmaf(fmaf(-s0, kTop, range), 1.f / kTop, s0));
+    __half s16 = __float2half_rn(fmaf(fmaf(-s0, kTop, range), 1.f / kTop, s0));
+    // a scale rounded up must not carry the top code over fp16's range (65520 rounds to infinity)
+    if (fmaf(__half2float(s16), kTop, mn) >= 65520.f) s16 = __ushort_as_half(__half_as_ushort(s16) - 1);
     const float s = __half2float(s16);
     const bool bad = !isfinite(mn) || !isfinite(mx);
 #pragma unroll
@@ -346,10 +349,10 @@ extern "C" int edge0_kv_append(const edge0_kv_cache* cache, const uint16_t* k, l
     const Rows rows{table, B, W, start, cu_rows, T, status};
     rc = check_rows(rows);
     if (rc) return rc;
+    if (T == 0) return EDGE0_OK;
     const long long width = (long long)cache->n_kv_heads * cache->head_dim;
     if (!k || !v || (((uintptr_t)k | (uintptr_t)v) & 15) || ldk % 8 || ldv % 8 || ldk < width || ldv < width)
         return EDGE0_EINVAL;
-    if (T == 0) return EDGE0_OK;
     const int per = rows_per_cta(T);
     EDGE0_KV_DISPATCH(cache->bits, cache->head_dim,
                       (kv_append_kernel<BT, DD><<<ceil_div(T, per), kKvThreads, 0, stream>>>(
@@ -366,8 +369,8 @@ extern "C" int edge0_kv_read(const edge0_kv_cache* cache, const int32_t* table, 
     const Rows rows{table, B, W, start, cu_rows, T, status};
     rc = check_rows(rows);
     if (rc) return rc;
-    if (!k || !v || (((uintptr_t)k | (uintptr_t)v) & 15)) return EDGE0_EINVAL;
     if (T == 0) return EDGE0_OK;
+    if (!k || !v || (((uintptr_t)k | (uintptr_t)v) & 15)) return EDGE0_EINVAL;
     const int per = rows_per_cta(T);
     EDGE0_KV_DISPATCH(cache->bits, cache->head_dim,
                       (kv_read_kernel<BT, DD><<<ceil_div(T, per), kKvThreads, 0, stream>>>(c, rows, per, (__half*)k,

@@ -22,6 +22,8 @@ def quantise(x, bits):
     w = np.where(bad[..., None], 0.0, g.astype(np.float64))
     mn, mx = w.min(-1), w.max(-1)
     s = ((mx - mn).astype(np.float32) / np.float32(top)).astype(np.float16)
+    over = s.astype(np.float64) * top + mn >= 65520          # would round to infinity: the next fp16 below
+    s = np.where(over, (s.view(np.uint16) - over).astype(np.uint16).view(np.float16), s)
     d = np.where(s == 0, 1.0, s.astype(np.float64))
     q = np.clip(np.rint((w - mn[..., None]) / d[..., None]), 0, top)
     q = np.where((s == 0)[..., None] | bad[..., None], 0, q).astype(np.uint8)

@@ -109,6 +109,14 @@ def test_reference_quantiser():
     x[1], x[2], x[3] = 15.0, 2.5, 3.5
     q, s, b = ref.quantise(x, 4)
     assert s[0] == 1 and q[2] == 2 and q[3] == 4
+    # the widest range: no finite value comes back as infinity
+    for bits in (4, 8):
+        x = np.linspace(-65504, 65504, 64).astype(np.float16)
+        q, s, b = ref.quantise(x, bits)
+        assert np.isfinite(ref.values(q, s, b).astype(np.float16)).all()
+        x[:] = np.linspace(60000, 65504, 64)
+        q, s, b = ref.quantise(x, bits)
+        assert np.isfinite(ref.values(q, s, b).astype(np.float16)).all()
     # a non-finite value marks its group only
     x = np.ones(128, np.float16)
     x[70] = np.inf

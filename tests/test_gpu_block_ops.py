@@ -226,6 +226,35 @@ def test_kv_round_trip_error_and_poisoned_groups():
         assert np.array_equal(bad, want)
 
 
+def test_kv_widest_ranges_stay_finite():
+    H, D, page, T = 1, 64, 16, 64
+    rng = np.random.default_rng(8)
+    x = (rng.uniform(-1, 1, (T, H, D)) * 65504).astype(np.float16)
+    x[:, :, 0], x[:, :, 1] = -65504, 65504
+    x[1::2] = np.abs(x[1::2])
+    for bits in (4, 8):
+        cache = binding.KVCache(4, page, H, D, bits, device=DEV)
+        table, start, cu = i32([[0, 1, 2, 3]]), i32([0]), i32([0, T])
+        binding.kv_append(cache, dev(x), dev(x), table, start, cu)
+        k, v = binding.kv_read(cache, table, start, cu, T)
+        q, s, b = ref.quantise(x, bits)
+        want = ref.values(q, s, b, np.float32).astype(np.float16)
+        assert torch.isfinite(k).all() and np.array_equal(k.cpu().numpy(), want) and torch.equal(k, v)
+
+
+def test_kv_and_attention_calls_without_rows():
+    cache = binding.KVCache(2, 16, 1, 64, 4, device=DEV)
+    none = torch.empty(0, 1, 64, dtype=torch.float16, device=DEV)
+    binding.kv_append(cache, none, none, i32([[0]]), i32([0]), i32([0, 0]))
+    k, v = binding.kv_read(cache, i32([[0]]), i32([0]), i32([0, 0]), 0)
+    assert k.shape == v.shape == (0, 1, 64) and not cache.pages.any()
+    o = binding.attn_decode(cache, torch.empty(0, 2, 64, dtype=torch.float16, device=DEV), i32(np.zeros((0, 1))), i32(np.zeros(0)))
+    assert o.shape == (0, 2, 64)
+    y = binding.q4_linear(torch.zeros(576, dtype=torch.uint8, device=DEV), 16, torch.empty(0, 64, dtype=torch.float16, device=DEV))
+    assert y.shape == (0, 16)
+    assert cache.error() == 0
+
+
 def test_kv_slices_of_a_fused_projection_and_one_row_per_sequence():
     H, D, page, B = 2, 64, 32, 6
     wide = torch.randn(B, 4 * H * D + 8, device=DEV).half()
@@ -370,6 +399,71 @@ def test_attention_empty_and_padding_rows():
 @pytest.mark.parametrize("bits", [4, 8])
 def test_attention_ranges(bits, kw):
     run_attention(bits, 128, 2, 8, 64, [0, 1, 40, 513], 200, **kw)
+
+
+@pytest.mark.parametrize("bits,D,B", [(4, 128, 1), (8, 64, 2), (4, 64, 40), (8, 128, 9), (4, 256, 9)])
+def test_attention_constant_groups(bits, D, B):
+    """Constant groups (s = 0) of every kind among the tokens: zeros, one value, tiny and large."""
+    rng = np.random.default_rng(B)
+    H, G, page, n, P = 1, 4, 16, 75, 90
+    x = rng.standard_normal((12, 2, page, H, D))
+    for i, c in enumerate((0.0, -0.0, 1.5, -1.5, 2.0 ** -24, -3e-5, 9.0)):
+        x[:, :, i::11, :, :64] = c
+        x[i, :, :, :, D - 64:] = c
+    codes, s, b = ref.quantise(x.astype(np.float16), bits)
+    assert (s == 0).any()
+    val = ref.values(codes, s, b)
+    cache = binding.KVCache(12, page, H, D, bits, pages=dev(ref.page_image(codes, s, b, bits)))
+    table = np.stack([rng.permutation(12)[:5] for _ in range(B)])
+    pre = rng.permutation(12)[:6]
+    q = rng.standard_normal((B, H * G, D)).astype(np.float16)
+    got = binding.attn_decode(cache, dev(q), i32(table), i32([n] * B), i32(pre), P).cpu().numpy().astype(np.float64)
+    z = 2.0 ** (bits - 1)
+    sw, bw = (np.repeat(a[:, 1].astype(np.float64), 64, -1) for a in (s, b))
+    flat = lambda a, pages, m: a[pages].reshape(-1, H, D)[:m]
+    # a constant group's value b is |b| times (0 - z) + (z +- 1): its part that meets a code is z |b|
+    parts = np.where(sw == 0, (2 * z + 1) * np.abs(bw), np.abs(sw * (codes[:, 1].astype(np.float64) - z)) + np.abs(sw * z + bw))
+    big = np.where(sw == 0, np.abs(bw), sw) * z
+    for i in range(B):
+        k, v, pp, zz = (np.concatenate([flat(a, pre, P), flat(a, table[i], n)]) for a in (val[:, 0], val[:, 1], parts, big))
+        want, bound = ref.attention(q[i].astype(np.float64), k, v, pp, zz, D ** -0.5)
+        assert (np.abs(got[i] - want) <= bound).all()
+
+
+def test_attention_captured_without_a_call_before():
+    """A process whose first attention, cache and projection calls are inside a capture."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from int4_routed_expert_prerouter_gb300 import binding as b
+dev = "cuda:0"
+cache = b.KVCache(40, 16, 2, 128, 4, device=dev)
+k = torch.randn(96, 2, 128, device=dev).half()
+i = lambda a: torch.tensor(a, dtype=torch.int32, device=dev)
+table, start, cu = i([[*range(6)]]), i([0]), i([0, 96])
+q = torch.randn(24, 8, 128, device=dev).half()
+own, lens, pre = i([[6 + j % 30] for j in range(24)]), i([j % 17 for j in range(24)]), i([*range(6)])
+w = torch.zeros(48 * 9 * 16, dtype=torch.uint8, device=dev)[:576 * 4].contiguous()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    b.kv_append(cache, k, k, table, start, cu)
+    o = b.attn_decode(cache, q, own, lens, pre, 90)
+    y = b.q4_linear(w, 16, q.view(48, 512)[:3, :256].contiguous())
+g.replay()
+torch.cuda.synchronize()
+first = o.clone()
+g.replay()
+e = b.attn_decode(cache, q, own, lens, pre, 90)
+torch.cuda.synchronize()
+assert torch.equal(first, o) and torch.equal(e, o) and o.isfinite().all() and o.any() and cache.error() == 0
+print("captured")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_attention_scores_that_grow_along_the_context():
