@@ -412,9 +412,11 @@ void edge0_pool_destroy(edge0_pool* pool);
  *
  * Limits: head_dim 64, 128 or 256; bits 4 or 8; page_tokens a multiple of 16 up to
  * EDGE0_MAX_PAGE_TOKENS; other values return EDGE0_EUNSUPPORTED. */
-#define EDGE0_MAX_KV_HEADS 64
-#define EDGE0_MAX_Q_PER_KV 64       /* query heads that share one K/V head */
-#define EDGE0_MAX_PAGE_TOKENS 4096
+enum {
+    EDGE0_MAX_KV_HEADS = 64,
+    EDGE0_MAX_Q_PER_KV = 64,        /* query heads that share one K/V head */
+    EDGE0_MAX_PAGE_TOKENS = 4096
+};
 
 /* Dense int4 projection [S2, S3.1: the int4 affine group-64 format]: y[b] = W x[b],
  * W [out, in] packed by edge0_pack_q4_rows with E = 1; add the projection's LoRA with

@@ -29,6 +29,7 @@
 // B fragment with movmatrix.  The reference moves only when a score exceeds it by 2^8
 // or a scale by 2^6, so most units rescale nothing.
 #include "attn.cuh"
+#include "mma.cuh"
 
 namespace edge0 {
 namespace {

@@ -14,6 +14,7 @@
 // ring of asynchronous copies, the weights straight into registers two groups ahead,
 // and the group sums of x are one more matrix step against ones.
 #include "common.cuh"
+#include "mma.cuh"
 
 namespace edge0 {
 namespace {
