@@ -192,14 +192,14 @@ def test_kv_read_returns_the_values(bits, D, H, page):
     table = rng.permutation(12).reshape(4, 3)
     k0 = torch.full((T, H, D), 5.0, dtype=torch.float16, device=DEV)
     k, v = binding.kv_read(cache, i32(table), i32(start), i32(cu), T, k=k0, v=k0.clone())
-    x32 = ref.values(c.codes, c.s, c.b, np.float32).astype(np.float16)     # one rounding of s q + b
+    exact = ref.values(c.codes, c.s, c.b).astype(np.float16)              # one rounding of s q + b
     for which, got in enumerate((k.cpu().numpy(), v.cpu().numpy())):
         want = np.full((T, H, D), 5.0, np.float16)
         for b in range(4):
             for i in range(counts[b]):
                 pos = start[b] + i
                 if start[b] >= 0:
-                    want[cu[b] + i] = x32[table[b, pos // page], which, pos % page]
+                    want[cu[b] + i] = exact[table[b, pos // page], which, pos % page]
         assert np.array_equal(got, want)
 
 
@@ -238,7 +238,7 @@ def test_kv_widest_ranges_stay_finite():
         binding.kv_append(cache, dev(x), dev(x), table, start, cu)
         k, v = binding.kv_read(cache, table, start, cu, T)
         q, s, b = ref.quantise(x, bits)
-        want = ref.values(q, s, b, np.float32).astype(np.float16)
+        want = ref.values(q, s, b).astype(np.float16)
         assert torch.isfinite(k).all() and np.array_equal(k.cpu().numpy(), want) and torch.equal(k, v)
 
 
@@ -593,9 +593,9 @@ def test_decode_steps_of_a_block_eager_and_captured(bits):
         assert (np.abs(rows[t] - want) <= b1).all()
     kk = rows[:, :, H * G * D:].reshape(steps, B, 2, H, D)
     q_, s_, b_ = ref.quantise(np.ascontiguousarray(kk), bits)
-    v32 = ref.values(q_, s_, b_, np.float32).astype(np.float16)
-    assert np.array_equal(got_k.view(B, steps, H, D).cpu().numpy(), v32[:, :, 0].transpose(1, 0, 2, 3))
-    assert np.array_equal(got_v.view(B, steps, H, D).cpu().numpy(), v32[:, :, 1].transpose(1, 0, 2, 3))
+    v16 = ref.values(q_, s_, b_).astype(np.float16)
+    assert np.array_equal(got_k.view(B, steps, H, D).cpu().numpy(), v16[:, :, 0].transpose(1, 0, 2, 3))
+    assert np.array_equal(got_v.view(B, steps, H, D).cpu().numpy(), v16[:, :, 1].transpose(1, 0, 2, 3))
     # captured: one graph of the step replayed, lengths advancing on the device
     cache2, lens2 = fresh()
     h_in = hs[0].clone()
