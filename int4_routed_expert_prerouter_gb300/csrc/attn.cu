@@ -22,12 +22,17 @@
 //                 and sum p s r, of the rounded weights, is kept in fp32 beside it: the
 //                 error is that of a rounded weight on the exact V.  (With sum p (b + s z)
 //                 of the unrounded weights it was a sixth larger.)
-// The exponents' reference is the running maximum plus the exponent of the largest V
-// scale so far, so that p s stays within fp16's normal range whatever the scales.
+// Both factors of p s have a reference: the running maximum of the row's scores, and the
+// power of two 2^e above the largest V scale so far.  p s / 2^e times 2^7 uses fp16's range
+// to its top, so that it is normal down to 2^-21 of the largest; where a scale is
+// below 2^-9 of the reference (there r = b / s + z can be large), sum p s r takes the
+// unrounded weights instead, whose error does not grow with r.  Scores are formed less
+// their reference from the first term on, and e stays out of that sum, so that
+// neither is lost to the other's magnitude.
 // ldmatrix delivers K codes as A fragments and, transposed, V codes with the
 // token pairs that the A fragments of V^T want; P^T goes from accumulator to
-// B fragment with movmatrix.  The reference moves only when a score exceeds it by 2^8
-// or a scale by 2^6, so most units rescale nothing.
+// B fragment with movmatrix.  A reference moves only when exceeded by 2^4, so most units
+// rescale nothing.
 #include "attn.cuh"
 #include "mma.cuh"
 
@@ -53,7 +58,7 @@ struct AttnP {
     int n_tok;
     float k;                 // 2^24 scale log2(e): raw scores to the exponent
     float* part_o;           // [slots][8 NT][D]
-    float2* part_ml;         // [slots][8 NT] (maximum in exponent units, sum)
+    float2* part_ml;         // [slots][8 NT] (reference in exponent units, sum)
     int2* seg;               // [segments] (first slot, slots)
     __half* out;             // set: segments that one CTA has whole are written here
     long long ldo;
@@ -398,8 +403,10 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
             __syncthreads();
         }
 
-        float O[X::MT][NT][4], beta[NT][GR][2], m[NT][2], l[NT][2], thr[NT][2], mu[NT][2];
-        float e = 0.f, thr_s = 0.f;          // exponent of a score: k S - mu, mu = k m + e
+        // Weight of a score S: 2^(k (S - m)), m the row's reference; of a code beside it, s / es 2^kUp
+        // times that, es = 2^e the scales' reference.
+        float O[X::MT][NT][4], beta[NT][GR][2], m[NT][2], l[NT][2];
+        float es = 0.f, high = -INFINITY;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -408,8 +415,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                 for (int i = 0; i < 4; ++i) O[mt][nt][i] = 0.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                m[nt][i] = thr[nt][i] = -INFINITY;
-                mu[nt][i] = l[nt][i] = 0.f;
+                m[nt][i] = l[nt][i] = 0.f;
 #pragma unroll
                 for (int gr = 0; gr < GR; ++gr) beta[nt][gr][i] = 0.f;
             }
@@ -427,7 +433,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
             const char* buf = my_ring + stage * X::US * X::STRIP;
             const int left = n_tok - u * kUnit < kUnit ? n_tok - u * kUnit : kUnit;   // valid tokens
 
-            // scores of the unit, in raw units
+            // scores of the unit less their references, in raw units
             float S[X::US][NT][4];
 #pragma unroll
             for (int st = 0; st < X::US; ++st) {
@@ -483,10 +489,10 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                             q1 = sqsum[(nt * 8 + 2 * t + 1) * GR + gr];
                         }
                         float(&s)[4] = S[st][nt];
-                        s[0] = fmaf(sa.x, acc[nt][0], gr ? fmaf(sa.y, q0, s[0]) : sa.y * q0);
-                        s[1] = fmaf(sa.x, acc[nt][1], gr ? fmaf(sa.y, q1, s[1]) : sa.y * q1);
-                        s[2] = fmaf(sb.x, acc[nt][2], gr ? fmaf(sb.y, q0, s[2]) : sb.y * q0);
-                        s[3] = fmaf(sb.x, acc[nt][3], gr ? fmaf(sb.y, q1, s[3]) : sb.y * q1);
+                        s[0] = fmaf(sa.x, acc[nt][0], fmaf(sa.y, q0, gr ? s[0] : -m[nt][0]));
+                        s[1] = fmaf(sa.x, acc[nt][1], fmaf(sa.y, q1, gr ? s[1] : -m[nt][1]));
+                        s[2] = fmaf(sb.x, acc[nt][2], fmaf(sb.y, q0, gr ? s[2] : -m[nt][0]));
+                        s[3] = fmaf(sb.x, acc[nt][3], fmaf(sb.y, q1, gr ? s[3] : -m[nt][1]));
                     }
                 }
             }
@@ -494,50 +500,42 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
             // V's scales of the unit's tokens g and g + 8: (s, r).  A token that is not there gets no
             // weight, whatever its bytes.
             float2 vs[X::US][GR][2];
-            bool flat = false;
 #pragma unroll
             for (int st = 0; st < X::US; ++st)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     uint32_t w[GR];
                     load_sb<GR>(buf + st * X::STRIP + X::HALF + 16 * X::R + (g + 8 * i) * X::SB, w);
-                    if (left < kUnit && st * 16 + g + 8 * i >= left) {
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) S[st][nt][2 * i] = S[st][nt][2 * i + 1] = -INFINITY;
-#pragma unroll
-                        for (int gr = 0; gr < GR; ++gr) w[gr] = 1;           // s = 2^-24, b = 0
-                    }
 #pragma unroll
                     for (int gr = 0; gr < GR; ++gr) {
                         const float2 sb = sb_of(w[gr]);
                         float inv;
                         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(sb.x));
                         vs[st][gr][i] = make_float2(sb.x, fmaf(sb.y, inv, kZ));
-                        flat = flat || sb.x == 0.f;
                     }
                 }
-            if (__any_sync(0xffffffffu, flat)) {     // constant groups (s = 0, codes 0): b = |b| (0 - z + z +- 1)
+            if (left < kUnit)
 #pragma unroll
                 for (int st = 0; st < X::US; ++st)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
+                        if (st * 16 + g + 8 * i >= left) {
 #pragma unroll
-                        for (int gr = 0; gr < GR; ++gr)
-                            if (vs[st][gr][i].x == 0.f) {
-                                const float b = __half2float(*reinterpret_cast<const __half*>(
-                                    buf + st * X::STRIP + X::HALF + 16 * X::R + (g + 8 * i) * X::SB + gr * 4 + 2));
-                                vs[st][gr][i] = b == 0.f ? make_float2(1.f / kTwo24, kZ)
-                                                         : make_float2(fabsf(b), kZ + copysignf(1.f, b));
-                            }
-            }
+                            for (int nt = 0; nt < NT; ++nt) S[st][nt][2 * i] = S[st][nt][2 * i + 1] = -INFINITY;
+#pragma unroll
+                            for (int gr = 0; gr < GR; ++gr) vs[st][gr][i] = make_float2(es, kZ);
+                        }
 
-            // the reference moves when a score is 2^8 above it or a scale 2^6
-            float top_s = 0.f;
-            bool up = false;
+            // a score more than 2^kRise above its reference, a scale outside [es kLowS, es kHighS]?
+            float most_s = 0.f, least_s = INFINITY;
+            bool look = false, tiny = false;
 #pragma unroll
             for (int st = 0; st < X::US; ++st)
 #pragma unroll
-                for (int gr = 0; gr < GR; ++gr) top_s = fmaxf(top_s, fmaxf(vs[st][gr][0].x, vs[st][gr][1].x));
+                for (int gr = 0; gr < GR; ++gr) {
+                    most_s = fmaxf(most_s, fmaxf(vs[st][gr][0].x, vs[st][gr][1].x));
+                    least_s = fminf(least_s, fminf(vs[st][gr][0].x, vs[st][gr][1].x));
+                }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -545,45 +543,69 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                     float v = fmaxf(S[0][nt][i], S[0][nt][i + 2]);
 #pragma unroll
                     for (int st = 1; st < X::US; ++st) v = fmaxf(v, fmaxf(S[st][nt][i], S[st][nt][i + 2]));
-                    up = up || v > thr[nt][i];
+                    look = look || v > high;
                 }
-            if (__any_sync(0xffffffffu, up || top_s > thr_s)) {
-                top_s = max_over_rows(top_s);
-                if (top_s > thr_s) {
-                    const int be = (int)(__float_as_uint(top_s) >> 23);      // top_s < 2^(be - 126)
-                    e = (float)((be < 240 ? be : 240) - 126);
-                    thr_s = __uint_as_float((unsigned)((int)e + 6 + 127) << 23);
+            if (__any_sync(0xffffffffu, look || most_s > es * kHighS || least_s < es * kLowS)) {
+                most_s = 0.f;
+                least_s = INFINITY;
+#pragma unroll
+                for (int st = 0; st < X::US; ++st)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (st * 16 + g + 8 * i < left)
+#pragma unroll
+                            for (int gr = 0; gr < GR; ++gr) {
+                                if (vs[st][gr][i].x == 0.f) {    // a constant group, codes 0: b = |b| (0 - z + z +- 1)
+                                    const float b = __half2float(*reinterpret_cast<const __half*>(
+                                        buf + st * X::STRIP + X::HALF + 16 * X::R + (g + 8 * i) * X::SB + gr * 4 + 2));
+                                    vs[st][gr][i] = b == 0.f ? make_float2(1.f / kTwo24, kZ)
+                                                             : make_float2(fabsf(b), kZ + copysignf(1.f, b));
+                                }
+                                most_s = fmaxf(most_s, vs[st][gr][i].x);
+                                least_s = fminf(least_s, vs[st][gr][i].x);
+                            }
+                most_s = max_over_rows(most_s);
+                float f_s = 1.f;
+                if (most_s > es * kHighS) {
+                    const uint32_t be = __float_as_uint(most_s) >> 23;        // most_s < 2^(be - 126)
+                    const float to = __uint_as_float(((be < 240 ? be : 240) + 1) << 23);
+                    f_s = es * reciprocal2(to);
+                    es = to;
                 }
+                tiny = __any_sync(0xffffffffu, least_s < es * kLowS);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float v = m[nt][i];
+                        float v = fmaxf(S[0][nt][i], S[0][nt][i + 2]);
 #pragma unroll
-                        for (int st = 0; st < X::US; ++st) v = fmaxf(v, fmaxf(S[st][nt][i], S[st][nt][i + 2]));
+                        for (int st = 1; st < X::US; ++st) v = fmaxf(v, fmaxf(S[st][nt][i], S[st][nt][i + 2]));
                         v = max_over_rows(v);
-                        if (!(v > thr[nt][i])) v = m[nt][i];      // each row by its own scores alone
-                        const float to = v == -INFINITY ? 0.f : fmaf(v, p.k, e);
-                        const float f = m[nt][i] == -INFINITY ? 0.f : ex2(mu[nt][i] - to);
-                        m[nt][i] = v;
-                        mu[nt][i] = to;
-                        thr[nt][i] = v + 8.f / p.k;
+                        if (!(v > high)) v = 0.f;      // each row by its own scores alone
+                        const float f = high == -INFINITY ? 0.f : ex2(-v * p.k);      // (nothing to move at first)
+                        m[nt][i] += v;
+#pragma unroll
+                        for (int st = 0; st < X::US; ++st) {
+                            S[st][nt][i] -= v;
+                            S[st][nt][i + 2] -= v;
+                        }
                         l[nt][i] *= f;
 #pragma unroll
-                        for (int gr = 0; gr < GR; ++gr) beta[nt][gr][i] *= f;
+                        for (int gr = 0; gr < GR; ++gr) beta[nt][gr][i] *= f * f_s;
 #pragma unroll
                         for (int mt = 0; mt < X::MT; ++mt) {
-                            O[mt][nt][i] *= f;
-                            O[mt][nt][i + 2] *= f;
+                            O[mt][nt][i] *= f * f_s;
+                            O[mt][nt][i + 2] *= f * f_s;
                         }
                     }
+                high = kRise / p.k;
             }
 #pragma unroll
             for (int st = 0; st < X::US; ++st)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) S[st][nt][i] = ex2(fmaf(S[st][nt][i], p.k, -mu[nt][i & 1]));
+                    for (int i = 0; i < 4; ++i) S[st][nt][i] = ex2(S[st][nt][i] * p.k);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) l[nt][i] += S[st][nt][i] + S[st][nt][i + 2];
                 }
@@ -594,11 +616,17 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                 for (int gr = 0; gr < GR; ++gr) {
                     uint32_t b0[NT], b1[NT];
                     const float2 v0 = vs[st][gr][0], v1 = vs[st][gr][1];
+                    const float up = kUp * reciprocal2(es);
+                    const float u0 = v0.x * up, u1 = v1.x * up;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const float(&P)[4] = S[st][nt];
-                        const uint32_t h0 = pack2(P[0] * v0.x, P[1] * v0.x), h1 = pack2(P[2] * v1.x, P[3] * v1.x);
-                        const float2 f0 = sb_of(h0), f1 = sb_of(h1);         // the rounded weights
+                        const uint32_t h0 = pack2(P[0] * u0, P[1] * u0), h1 = pack2(P[2] * u1, P[3] * u1);
+                        float2 f0 = sb_of(h0), f1 = sb_of(h1);               // the rounded weights
+                        if (tiny) {
+                            f0 = make_float2(P[0] * u0, P[1] * u0);
+                            f1 = make_float2(P[2] * u1, P[3] * u1);
+                        }
                         b0[nt] = transpose8(h0);
                         b1[nt] = transpose8(h1);
                         beta[nt][gr][0] = fmaf(f0.x, v0.y, fmaf(f1.x, v1.y, beta[nt][gr][0]));
@@ -626,6 +654,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
         }
 
         // join the warps: maximum, then 8 query rows at a time through the ring's memory
+        const bool any = high != -INFINITY;                      // this warp had a unit
+        const float down = es * (1.f / kUp);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -634,7 +664,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
 #pragma unroll
                 for (int gr = 0; gr < GR; ++gr) beta[nt][gr][i] = sum_over_rows(beta[nt][gr][i]);
                 if (g == 0) sml[(wid * NT + nt) * 8 + 2 * t + i] =
-                                make_float2(m[nt][i] == -INFINITY ? -INFINITY : mu[nt][i], l[nt][i]);
+                                make_float2(any ? __fmul_rn(m[nt][i], p.k) : -INFINITY, l[nt][i]);
             }
         __syncthreads();
         const bool whole = u0 == 0 && u1 == units;
@@ -653,7 +683,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                 float top = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[(w * NT + nt) * 8 + col].x);
-                const float f = m[nt][i] == -INFINITY ? (l[nt][i] == 0.f ? 0.f : l[nt][i]) : ex2(mu[nt][i] - top);
+                const float f = any ? ex2(__fmul_rn(m[nt][i], p.k) - top) * down : 0.f;   // (not one fused step: `top` is rounded)
                 float* dst = red + (wid * 8 + col) * X::kRedLd;
 #pragma unroll
                 for (int mt = 0; mt < X::MT; ++mt) {
@@ -673,7 +703,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float2 ml = sml[(w * NT + nt) * 8 + col];
-                    sum += ml.x == -INFINITY ? ml.y : ml.y * ex2(ml.x - top);
+                    sum += ml.x == -INFINITY ? 0.f : ml.y * ex2(ml.x - top);
                 }
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll

@@ -8,6 +8,11 @@ namespace edge0 {
 constexpr int kPrefixRows = 128;     // query rows of a CTA: the rows of one accumulator
 constexpr int kPrefixTile = 64;      // tokens per step
 
+// Both factors of a weight p s have a reference, es = 2^e the scales': p <= 2^kRise and s <=
+// es kHighS, so that p s / es kUp < 2^15 stays within fp16.  Below es kLowS p s may leave
+// fp16's normal range while it still counts.
+constexpr float kRise = 4.f, kHighS = 16.f, kUp = 128.f, kLowS = 1.f / 512;
+
 struct PrefixP {
     kv::View c;
     const __half* q;
@@ -51,6 +56,8 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 1 / x of a power of two
+__device__ __forceinline__ float reciprocal2(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);

@@ -15,10 +15,10 @@
 // Q_g (code - z) + mean(Q_g) 64 r; the second term is one more step of 16 of the same
 // product, its factors split into two fp16 each, so that S = sum_g s_g S_g carries no
 // rounding of K beyond 2^-22.  Each weight is rounded once (to fp16, 2^-11 of itself):
-// with V = s (code - z + r) likewise, o = (O_g + sum P'_g r_g) / sum p.  The exponents' reference is the running
-// maximum plus the exponent of the largest scale so far, so that p s stays within
-// fp16's normal range whatever the scales; it moves only when a score exceeds it by
-// 2^8 or a scale by 2^6, and the accumulators are then rescaled in TMEM.
+// with V = s (code - z + r) likewise, o = (O_g + sum P'_g r_g) / sum p.  Scores have the running
+// maximum, scales a power of two above the largest so far as reference (kUp, kRise, kLow:
+// attn.cuh); a reference moves only when exceeded by 2^4, and the accumulators are
+// then rescaled in TMEM.
 // The accumulators are read and P' written as 8-column fragments (a lane: 2 tokens of
 // 4 rows): a token's scales, read from shared memory, serve 4 rows; with a row per
 // thread reading them alone took 2000 cycles a step.
@@ -395,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
         const int hf = wid >> 2, quad = wid & 3, g = lane >> 2, t = lane & 3;      // 32 tokens, 32 rows
         const uint32_t my = tm + ((uint32_t)(32 * quad) << 16);
         // rows 32 quad + 16 rh + g + 8 k, index 2 rh + k; weight of a score: 2^(S - mu), S in
-        // exponent units, mu the running maximum plus e, 2^e the scales'
-        float mu[4], l[4], beta[4][GR], e = 0.f, thr_s = 0.f;
+        // exponent units, mu the running maximum; of a code beside it s / es kUp times that
+        float mu[4], l[4], beta[4][GR], es = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             mu[r] = l[r] = 0.f;
@@ -434,12 +434,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             ok = wait_bar(&full[i & 1], (i >> 1) & 1, &dead) && wait_bar(&s_ready, i & 1, &dead);
             __syncwarp();
             tc::fence_after_sync();
-            float top_s = 0.f;
+            float most_s = 0.f, least_s = INFINITY;            // (0: no token)
 #pragma unroll
             for (int gr = 0; gr < GR; ++gr) {
                 const float2 v = *reinterpret_cast<const float2*>(tab_v + (lane * GR + gr) * 4);
-                top_s = fmaxf(top_s, fmaxf(v.x, v.y));
+                most_s = fmaxf(most_s, fmaxf(v.x, v.y));
+                least_s = fminf(least_s, fminf(v.x == 0.f ? INFINITY : v.x, v.y == 0.f ? INFINITY : v.y));
             }
+            bool tiny = false;
             f2 S[2][4][2];                                     // [rh][8 tokens][k]: tokens 2t, 2t + 1
             const int left = p.n_tok - (t0 + i) * kTile - hf * 32 - 2 * t;     // of this lane's tokens
             float mx[4];
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                 }
             }
             const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            if (any_of_rows(quad, i == 0 || most > 8.f - e || top_s > thr_s)) {
+            if (any_of_rows(quad, i == 0 || most > kRise || most_s > es * kHighS || least_s < es * kLowS)) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
@@ -492,30 +494,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                     if (t == 0) part_max[hf][32 * quad + 16 * (r >> 1) + g + 8 * (r & 1)] = mx[r];
                 }
 #pragma unroll
-                for (int s = 16; s; s >>= 1) top_s = fmaxf(top_s, __shfl_xor_sync(0xffffffffu, top_s, s));
+                for (int s = 16; s; s >>= 1) most_s = fmaxf(most_s, __shfl_xor_sync(0xffffffffu, most_s, s));
                 named_bar_sync(8 + quad, 64);
-                const float e0 = e;
-                if (top_s > thr_s) {
-                    const int be = (int)(__float_as_uint(top_s) >> 23);      // top_s < 2^(be - 126)
-                    e = (float)((be < 240 ? be : 240) - 126);
-                    thr_s = __uint_as_float((unsigned)((int)e + 6 + 127) << 23);
+                float f_s = 1.f;
+                if (most_s > es * kHighS) {
+                    const uint32_t be = __float_as_uint(most_s) >> 23;        // most_s < 2^(be - 126)
+                    const float to = __uint_as_float(((be < 240 ? be : 240) + 1) << 23);
+                    f_s = es * reciprocal2(to);
+                    es = to;
                 }
+                tiny = __any_sync(0xffffffffu, least_s < es * kLowS);
                 float f[4];
-                bool move = false;
+                bool move = f_s != 1.f;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float both = fmaxf(mx[r], part_max[hf ^ 1][32 * quad + 16 * (r >> 1) + g + 8 * (r & 1)]);
-                    float by = e0 - e;                         // old reference less the new one
-                    if ((i == 0 || both > 8.f - e0) && both != -INFINITY) by -= both + e0;
-                    const float to = mu[r] - by;
-                    f[r] = i ? ex2(by) : 0.f;
-                    mu[r] = to;
+                    const float by = (i == 0 || both > kRise) && both != -INFINITY ? both : 0.f;
+                    mu[r] += by;
+                    f[r] = i ? ex2(-by) : 0.f;
                     move = move || by != 0.f;
                     l[r] *= f[r];
+                    f[r] *= f_s;
 #pragma unroll
                     for (int gr = 0; gr < GR; ++gr) beta[r][gr] *= f[r];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) S[r >> 1][j][r & 1] = add2(S[r >> 1][j][r & 1], pk(by, by));
+                    for (int j = 0; j < 4; ++j) S[r >> 1][j][r & 1] = add2(S[r >> 1][j][r & 1], pk(-by, -by));
                 }
                 // (the first tile overwrites the accumulators)
                 if (i > 0 && __any_sync(0xffffffffu, move)) {
@@ -552,9 +555,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                 }
 #pragma unroll
             for (int gr = 0; gr < GR; ++gr) {
+                const float up = kUp * reciprocal2(es);
                 ulonglong2 sc[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sc[j] = *reinterpret_cast<const ulonglong2*>(mv + j * 16 * GR + gr * 4);
+                for (int j = 0; j < 4; ++j) {
+                    sc[j] = *reinterpret_cast<const ulonglong2*>(mv + j * 16 * GR + gr * 4);
+                    sc[j].x = mul2(sc[j].x, pk(up, up));
+                }
 #pragma unroll
                 for (int rh = 0; rh < 2; ++rh) {
                     uint32_t w[8];
@@ -577,6 +584,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                         beta[2 * rh + k][gr] += a + b;
                     }
                 }
+            }
+            if (tiny) {
+                const float up = kUp * reciprocal2(es);        // what the rounding took from sum p s r
+#pragma unroll
+                for (int gr = 0; gr < GR; ++gr)
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 v = *reinterpret_cast<const float4*>(mv + j * 16 * GR + gr * 4);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            f2 x = S[r >> 1][0][r & 1];
+#pragma unroll
+                            for (int i = 1; i < 4; ++i) x = j == i ? S[r >> 1][i][r & 1] : x;
+                            float a, b;
+                            unpk(x, a, b);
+                            a *= v.x * up;
+                            b *= v.y * up;
+                            const uint32_t h = pack2(a, b);
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                            beta[r][gr] = fmaf(a - f.x, v.z, fmaf(b - f.y, v.w, beta[r][gr]));
+                        }
+                    }
             }
             tmem_wait_st();
             tc::fence_before_sync();
@@ -620,6 +649,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             // rows of o in shared memory, 16 bytes apart so that eight of them do not share banks, and
             // from there in one copy each
             constexpr int kLd = D + 4;
+            const float down = es * (1.f / kUp);
             float* rows = reinterpret_cast<float*>(smem + 2 * (1 + GR) * kRowsQ * 4);
 #pragma unroll
             for (int c = 0; c < D / 64 * 2; ++c) {
@@ -634,7 +664,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                     float* dst = rows + row * kLd + d0;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float x = __uint_as_float(a[4 * j + 2 * k]) + add, y = __uint_as_float(a[4 * j + 2 * k + 1]) + add;
+                        const float x = (__uint_as_float(a[4 * j + 2 * k]) + add) * down;
+                        const float y = (__uint_as_float(a[4 * j + 2 * k + 1]) + add) * down;
                         if (BITS == 4) {                       // columns 2t, 2t + 1 hold dims t, t + 4
                             dst[8 * j + t] = x;
                             dst[8 * j + t + 4] = y;

@@ -88,8 +88,10 @@ def attention(q, k, v, parts, sz, scale):
     With p the normalised weights the bound adds up
     - the result's rounding: half an fp16 step, 2^-11 |o|, and 2^-24 where that is subnormal;
     - the rounding of each weight to fp16 when it meets a code: 2^-11 of its term of V's
-      parts; where p s is below fp16's normal range 2^-25 of the largest s (at most
-      doubled to a power of two), times the code's distance from z;
+      parts; where p s is below fp16's normal range half its subnormal step, 2^-25 of 2^e
+      2^-7 (2^e the largest s, at most doubled to a power of two), times the code's distance
+      from z, and, while s >= 2^-9 2^e (so that p < 2^-12 of the reference, which is within
+      a factor 2^4 below the maximum), times r = b / s + z: |v| / s in all, 2^-23 |v|;
     - the weights' own error a_j = the fp32 score's (D / 16 matrix steps and D / 64 group sums
       of terms that add up to at most |q| (3 max |k| of the group), each off by 2^-23, and the
       exponent's argument by 2^-22 of itself) + 2^-20 of the exponential: p a on V's parts
@@ -111,5 +113,6 @@ def attention(q, k, v, parts, sz, scale):
         mag = 3 * np.abs(kk).reshape(n, -1, GROUP).max(-1).repeat(GROUP, -1)
         a = scale * (mag @ np.abs(q[h])) * (D / 16 + D / 64) * 2.0 ** -23 + np.abs(sc) * 2.0 ** -22 + 2.0 ** -20
         bound[h] += (2.0 ** -11 + p @ a) * np.abs(o[h]) + (p * (2.0 ** -11 + a + (n / 16 + 64) * 2.0 ** -23)) @ pp
-        bound[h] += n * 2.0 ** -25 * 2 * big.max(0) / total
+        bound[h] += n * 2.0 ** -32 * 2 * big.max(0) / total
+        bound[h] += 2.0 ** -23 / total * (np.abs(vv) * (p * total <= 2.0 ** -12)[:, None]).sum(0)
     return o, bound

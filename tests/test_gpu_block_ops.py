@@ -487,6 +487,76 @@ def test_attention_scores_that_grow_along_the_context():
     assert (np.abs(got - want) <= bound).all()
 
 
+@pytest.mark.parametrize("bits,D,B", [(4, 128, 1), (8, 64, 2), (4, 64, 20), (8, 128, 9), (4, 256, 9)])
+def test_attention_scores_of_any_magnitude(bits, D, B):
+    """Scores up to 10^16, each far from the next: the largest one's token alone, whose weight
+    is exactly 1: the result's rounding, 2^-11 of it, and fp32 sums of its two parts.  The
+    weight times s is exact in fp16 while that is normal; below, half a subnormal step of units
+    of 2^-7 2^e, 2^e at most twice the largest s: 2^-25 2^-7 2 max(s), times |q - z| <= z."""
+    rng = np.random.default_rng(D)
+    H, G, page, n, P = 1, 4, 16, 150, 90
+    for size, scale in ((1.0, 1e6), (200.0, 1e6), (200.0, 1.0)):
+        x = rng.standard_normal((16, 2, page, H, D))
+        x[:, 0] = rng.permutation(np.arange(1, 257)).reshape(16, page, 1, 1) * size * np.where(np.arange(D) % 2, 1.0, 0.5)
+        x[:, 1] *= 2.0 ** rng.integers(-12, 12, (16, page, 1, 1))
+        codes, s, b = ref.quantise(x.astype(np.float16), bits)
+        val = ref.values(codes, s, b)
+        cache = binding.KVCache(16, page, H, D, bits, pages=dev(ref.page_image(codes, s, b, bits)))
+        table = np.stack([rng.permutation(10) for _ in range(B)])
+        pre = np.arange(10, 16)
+        u = np.where(np.arange(D) % 2, 1.0, 0.5) * size
+        q = (np.stack([u, -u, u / 2, -u / 2])[None] * 2.0 ** -rng.integers(0, 3, (B, 1, 1))).astype(np.float16)
+        got = binding.attn_decode(cache, dev(q), i32(table), i32([n] * B), i32(pre), P, scale).cpu().numpy().astype(np.float64)
+        z = 2.0 ** (bits - 1)
+        sw, bw = (np.repeat(a[:, 1].astype(np.float64), 64, -1) for a in (s, b))
+        parts = np.abs(sw * (codes[:, 1].astype(np.float64) - z)) + np.abs(sw * z + bw)
+        step = 2.0 ** -32 * 2 * s[:, 1].astype(np.float64).max() * z
+        flat = lambda a, pages, m: a[pages].reshape(-1, D)[:m]
+        for i in range(B):
+            k, v, pp = (np.concatenate([flat(a, pre, P), flat(a, table[i], n)]) for a in (val[:, 0], val[:, 1], parts))
+            sc = scale * q[i].astype(np.float64) @ k.T
+            top = np.sort(sc, 1)
+            assert (top[:, -1] - top[:, -2] > 100).all()
+            at = sc.argmax(1)
+            assert (np.abs(got[i] - v[at]) <= 2.0 ** -11 * np.abs(v[at]) + 2.0 ** -24 + 2.0 ** -20 * pp[at] + step).all()
+
+
+@pytest.mark.parametrize("bits,D,B", [(4, 128, 1), (8, 64, 2), (4, 64, 20), (8, 128, 9), (4, 256, 9)])
+def test_attention_one_token_of_large_values(bits, D, B):
+    """Values that differ by a few fp16 steps (b far above s) beside a token whose values span the
+    type's range and whose weight is next to nothing."""
+    rng = np.random.default_rng(D + bits)
+    H, G, page, n, P = 1, 4, 16, 75, 90
+    x = rng.standard_normal((12, 2, page, H, D))
+    u = rng.standard_normal(D)
+    x[:, 1] = 1.0 + 2.0 ** -10 * rng.integers(0, 3, x[:, 1].shape)
+    x[::2, 1, :, :, :64] *= -1000.0
+    for page_no, tok in ((0, 3), (7, 9)):
+        x[page_no, 0, tok] = -3.0 * u
+        x[page_no, 1, tok] = rng.uniform(-1, 1, (H, D)) * 30000
+        x[page_no, 1, tok, :, ::64] = 30000
+    codes, s, b = ref.quantise(x.astype(np.float16), bits)
+    val = ref.values(codes, s, b)
+    cache = binding.KVCache(12, page, H, D, bits, pages=dev(ref.page_image(codes, s, b, bits)))
+    q = np.stack([np.stack([u, 1.1 * u, 0.9 * u, u])] * B).astype(np.float16)
+    z = 2.0 ** (bits - 1)
+    sw, bw = (np.repeat(a[:, 1].astype(np.float64), 64, -1) for a in (s, b))
+    flat_s = sw == 0
+    parts = np.where(flat_s, (2 * z + 1) * np.abs(bw), np.abs(sw * (codes[:, 1].astype(np.float64) - z)) + np.abs(sw * z + bw))
+    big = np.where(flat_s, np.abs(bw), sw) * z
+    flat = lambda a, pages, m: a[pages].reshape(-1, H, D)[:m]
+    for P in (0, 90):
+        table = np.stack([rng.permutation(6) for _ in range(B)])
+        pre = 6 + rng.permutation(6)
+        got = binding.attn_decode(cache, dev(q), i32(table), i32([n] * B), i32(pre), P).cpu().numpy().astype(np.float64)
+        for i in range(B):
+            k, v, pp, zz = (np.concatenate([flat(a, pre, P), flat(a, table[i], n)]) for a in (val[:, 0], val[:, 1], parts, big))
+            # near-constant groups: z s is far below |b|, so V's parts are V's own size
+            want, bound = ref.attention(q[i].astype(np.float64), k, v, pp, zz, D ** -0.5)
+            err = np.abs(got[i] - want)
+            assert (err <= bound).all(), (P, i, (err / bound).max())
+
+
 def test_attention_nan_reaches_only_its_own_rows():
     H, G, D, page = 2, 4, 128, 16
     args, clean = run_attention(4, D, H, G, page, [20, 33, 16], 10)
