@@ -415,15 +415,17 @@ void edge0_pool_destroy(edge0_pool* pool);
 enum {
     EDGE0_MAX_KV_HEADS = 64,
     EDGE0_MAX_Q_PER_KV = 64,        /* query heads that share one K/V head */
-    EDGE0_MAX_PAGE_TOKENS = 4096
+    EDGE0_MAX_PAGE_TOKENS = 4096,
+    EDGE0_MAX_LINEAR = 1 << 28,     /* outputs or inputs of a projection */
+    EDGE0_MAX_PREFIX = 1 << 30      /* tokens of a shared prefix */
 };
 
 /* Dense int4 projection [S2, S3.1: the int4 affine group-64 format]: y[b] = W x[b],
  * W [out, in] packed by edge0_pack_q4_rows with E = 1; add the projection's LoRA with
  * edge0_lora_delta.  x: B rows of `in` fp16, ldx elements apart (16-byte aligned, ldx a
  * multiple of 8, ldx >= in); y: B rows of `out` fp16, ldy apart (ldy >= out; what lies
- * between the rows is not touched).  in % 64 == 0, out any; 1 <= B <=
- * EDGE0_MAX_BATCHED.  fp32 sums, rounded once.  x and y may not overlap. */
+ * between the rows is not touched).  in % 64 == 0, out any, both up to EDGE0_MAX_LINEAR;
+ * 1 <= B <= EDGE0_MAX_BATCHED.  fp32 sums, rounded once.  x and y may not overlap. */
 int edge0_q4_linear(const void* packed, int out, int in, const uint16_t* x, long long ldx, int B,
                     uint16_t* y, long long ldy, cudaStream_t stream);
 
@@ -473,7 +475,8 @@ int edge0_kv_read(const edge0_kv_cache* cache, const int32_t* table, int B, int 
  * o[b, i] = sum_j softmax_j(scale q[b, i] . k_j) v_j with K/V head i / (n_q_heads /
  * n_kv_heads).  The prefix is read once for the whole batch.  q, out: B rows of
  * n_q_heads * head_dim fp16, ldq / ldo elements apart (16-byte aligned, multiples of 8);
- * lens [B], table [B][W], prefix: device int32; n_prefix, W: host; 0 < scale <= 1e6.
+ * lens [B], table [B][W], prefix: device int32; n_prefix <= EDGE0_MAX_PREFIX, W: host;
+ * 0 < scale <= 1e6.
  * A sequence without any token gets zeros; lens[b] < 0 marks a padding row, whose
  * output is left as it was.  lens[b] above W * page_tokens (cut there) and pages
  * outside [0, n_pages) (page 0 is read in their place) are recorded as EDGE0_EINVAL in

@@ -948,6 +948,7 @@ extern "C" int edge0_attn_decode(const edge0_kv_cache* cache, const uint16_t* q,
     if (n_q_heads <= 0 || n_q_heads % p.c.H) return EDGE0_EINVAL;
     if (n_q_heads / p.c.H > EDGE0_MAX_Q_PER_KV) return EDGE0_EUNSUPPORTED;
     if (n_prefix < 0 || (n_prefix > 0 && !prefix)) return EDGE0_EINVAL;
+    if (n_prefix > EDGE0_MAX_PREFIX) return EDGE0_EUNSUPPORTED;
     if (!(scale > 0.f) || !(scale <= 1e6f)) return EDGE0_EINVAL;
     const int D = cache->head_dim;
     const long long width = (long long)n_q_heads * D;

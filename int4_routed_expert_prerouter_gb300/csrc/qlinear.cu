@@ -431,6 +431,7 @@ extern "C" int edge0_q4_linear(const void* packed, int out, int in, const uint16
                                uint16_t* y, long long ldy, cudaStream_t stream) {
     if (!packed || !x || !y || out <= 0 || in <= 0 || in % kGroup) return EDGE0_EINVAL;
     if (B <= 0 || B > EDGE0_MAX_BATCHED || ldx < in || ldx % 8 || ldy < out) return EDGE0_EINVAL;
+    if (out > EDGE0_MAX_LINEAR || in > EDGE0_MAX_LINEAR) return EDGE0_EUNSUPPORTED;    // row and byte counts are ints
     if ((((uintptr_t)packed | (uintptr_t)x) & 15) || ((uintptr_t)y & 1)) return EDGE0_EINVAL;
     const char* w = (const char*)packed;
     const __half* xh = (const __half*)x;
@@ -443,7 +444,7 @@ extern "C" int edge0_q4_linear(const void* packed, int out, int in, const uint16
     // few tokens at once: as many as shared memory holds beside the rings; two row tiles
     // together once that still leaves every SM two CTAs' worth of them
     const int RT = n_rt >= 4 * sms ? 2 : 1;
-    int tokens = B <= kFewTokens ? B : 0;
+    int tokens = B <= kFewTokens && in <= kFewSmem / 2 ? B : 0;
     while (tokens && few_layout(in, tokens, tokens > 8 ? 2 : 1, RT).total > kFewSmem)
         tokens = tokens > 8 ? 8 : tokens / 2;
     if (tokens) {

@@ -44,6 +44,8 @@ def test_q4_linear_refusals(lib):
                dict(ldx=120), dict(ldx=132), dict(ldy=47), dict(x=C.c_void_p((1 << 20) + 8)),
                dict(w=C.c_void_p((1 << 20) + 8)), dict(y=C.c_void_p((1 << 20) + 1))):
         assert call(**kw) == EINVAL, kw
+    most = 1 << 28
+    assert call(out=most + 1, ldy=most + 1) == EUNSUP and call(n=most + 64, ldx=most + 64) == EUNSUP
 
 
 def test_cache_refusals(lib):
@@ -89,6 +91,7 @@ def test_attention_refusals(lib):
         assert call(**kw) == EINVAL, kw
     assert call(Hq=2 * 65, ldq=1 << 15, ldo=1 << 15) == EUNSUP
     assert call(c=desc(bits=3)) == EUNSUP
+    assert call(P=(1 << 30) + 1) == EUNSUP
     ws = lib.edge0_attn_workspace_bytes
     assert ws(C.byref(ok), 2, 8) > 0
     assert ws(C.byref(ok), 0, 8) == ws(C.byref(ok), 257, 8) == ws(C.byref(ok), 2, 7) == ws(C.byref(ok), 2, 130) == 0
