@@ -6,20 +6,32 @@
 // Nibbles enter m16n8k16 steps as fp16 subnormals (exact products, fp32 sums); the
 // group's scale and bias are applied to the fp32 sums.
 //
-// Few tokens (q4_few_kernel): bound by the weights' bytes.  A CTA takes row tiles in
+// Few tokens (q4_few_kernel).  Its floor is the weights' bytes.  A CTA takes row tiles in
 // turn, its eight warps a slice of the groups each, through rings of bulk copies (a
-// slice is one run of bytes); x and its group sums stay in shared memory.
-// More tokens (q4_many_kernel): bound by the matrix steps.  64 rows x up to 64 tokens per
-// CTA, four warps for the even groups and four for the odd ones; x comes through a
-// ring of asynchronous copies, the weights straight into registers two groups ahead,
-// and the group sums of x are one more matrix step against ones.
+// slice is one run of bytes); x and its group sums stay in shared memory, laid down
+// once.  A warp has its 16 rows for all tokens, so a nibble is unpacked once.  Measured:
+// 65,537 x 2048 at one token 17.3 us, 4.4 TB/s of weights, 0.64 of what a copy reaches:
+// the unpacking's instructions (issue slots 54 % taken) and the step's join across
+// warps, not the memory, are the limit; 5120 x 2048 at 7 tokens 6.6 us and
+// 2048 x 2048 at one token 2.9 us are launch, one latency of x, one of the weights and
+// the join.
+// More tokens (q4_many_kernel).  64 rows x 32 tokens per CTA, four warps for the even
+// groups and four for the odd ones, x and weights through one ring, four groups
+// between two barriers; the group sums of x are one more matrix step against ones.
+// A CTA alone on its SM is bound by latency (0.8 us per step of four groups, with two 1.3 us:
+// the matrix pipe is half taken then).  6144 x 1536 at 64 tokens 11.1 us, 109
+// TFLOP/s; 20,000 x 2048 at 256 tokens 103 us, 205 TFLOP/s.  Against it: 64 tokens per
+// CTA 13.9 and 105 us; 32 rows 13.6 us in the first; weights straight into registers,
+// two groups between barriers, 12.5 us in the first.
 #include "common.cuh"
 #include "mma.cuh"
 
 namespace edge0 {
 namespace {
 
-constexpr int kFewTokens = 16;          // most tokens of q4_few_kernel
+// Most tokens of q4_few_kernel.  Against q4_many_kernel, us: 1,000 x 2048 at 16 and 17 tokens 6.6 and
+// 9.1, 5120 x 2048 10.6 and 9.7, 20,000 x 2048 16 and 21.
+constexpr int kFewTokens = 16;
 constexpr int kWarps = 8;
 constexpr int kThreadsQ = 32 * kWarps;
 constexpr int kChunk = 4;               // groups per bulk copy
@@ -109,26 +121,48 @@ __global__ void __launch_bounds__(kThreadsQ) q4_few_kernel(const char* __restric
     };
     for (int s = 0; s < kStages - 1; ++s) issue();
 
-    // x: lane t's 16 inputs of a group (2t, 2t + 1, 2t + 8, 2t + 9 of each 16) side by side
-    for (int i = tid; i < nb * n_g * 4; i += kThreadsQ) {
-        const int tt = i & 3, c = (i >> 2) % n_g, b = (i >> 2) / n_g;
-        const __half* src = x + (long long)(b0 + b) * ldx + c * kGroup + 2 * tt;
-        uint32_t v[8];
-        float s = 0.f;
+    // x: lane t's 16 inputs of a group (2t, 2t + 1, 2t + 8, 2t + 9 of each 16) side by side.  A
+    // thread takes 16-byte pieces (piece p of a group: word p of each t), four under way at a time;
+    // the four groups of a warp start with a different t each, so that they miss each other's banks.
+    const int pieces = n_g * 8, all_pieces = nb * pieces;
+    for (int i0 = tid; i0 < all_pieces; i0 += 4 * kThreadsQ) {
+        uint4 v[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[j] = *reinterpret_cast<const uint32_t*>(src + 8 * j);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[j]));
-            s += f.x + f.y;
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * kThreadsQ, b = i / pieces;
+            if (i < all_pieces) v[j] = *reinterpret_cast<const uint4*>(x + (long long)(b0 + b) * ldx + (i - b * pieces) * 8);
         }
-        uint4* dst = reinterpret_cast<uint4*>(smem + L.x + b * L.ld + c * 128 + tt * 32);
-        dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
-        dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
-        // (a group's four threads are four lanes of one warp, all in the loop)
-        const unsigned quad = 0xfu << (lane & ~3);
-        s += __shfl_xor_sync(quad, s, 1);
-        s += __shfl_xor_sync(quad, s, 2);
-        if (tt == 0) xsum[c * 8 * NT + b] = s;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * kThreadsQ, b = i / pieces, at = i - b * pieces, c = at >> 3, q = at & 7;
+            if (i >= all_pieces) break;
+            const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&v[j].x));
+            const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&v[j].y));
+            const float2 f2 = __half22float2(*reinterpret_cast<const __half2*>(&v[j].z));
+            const float2 f3 = __half22float2(*reinterpret_cast<const __half2*>(&v[j].w));
+            float sum = ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
+            // (a group's eight threads are eight lanes of one warp, all here)
+            const unsigned octet = 0xffu << (lane & ~7);
+            sum += __shfl_xor_sync(octet, sum, 1);
+            sum += __shfl_xor_sync(octet, sum, 2);
+            sum += __shfl_xor_sync(octet, sum, 4);
+            if (q == 0) xsum[c * 8 * NT + b] = sum;
+            uint32_t w0 = v[j].x, w1 = v[j].y, w2 = v[j].z, w3 = v[j].w;
+            const int turn = (lane >> 3) & 3;
+            if (turn & 1) {
+                const uint32_t o = w0;
+                w0 = w1, w1 = w2, w2 = w3, w3 = o;
+            }
+            if (turn & 2) {
+                const uint32_t o0 = w0, o1 = w1;
+                w0 = w2, w1 = w3, w2 = o0, w3 = o1;
+            }
+            char* dst = smem + L.x + b * L.ld + c * 128 + q * 4;
+            *reinterpret_cast<uint32_t*>(dst + turn * 32) = w0;
+            *reinterpret_cast<uint32_t*>(dst + ((turn + 1) & 3) * 32) = w1;
+            *reinterpret_cast<uint32_t*>(dst + ((turn + 2) & 3) * 32) = w2;
+            *reinterpret_cast<uint32_t*>(dst + ((turn + 3) & 3) * 32) = w3;
+        }
     }
     __syncthreads();
 
@@ -223,6 +257,12 @@ __global__ void __launch_bounds__(kThreadsQ) q4_few_kernel(const char* __restric
     }
 }
 
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
 // 16 bytes, or zeros where there is nothing to copy
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
@@ -234,159 +274,169 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
-constexpr int kManyStages = 3;
+constexpr int kManyTok = 32;            // tokens of a CTA
+constexpr int kStep = 4;                // groups between two barriers
+constexpr int kManyStages = 4;          // steps under way: x of the tokens, the four row tiles' units
+constexpr int kManyStage = kStep * (kManyTok * 128 + 4 * kQ4Unit);
+constexpr int kManySmem = kManyStages * kManyStage;
 
-// NT: 8-token blocks per CTA (4 or 8)
-template <int NT>
 __global__ void __launch_bounds__(256, 2) q4_many_kernel(const char* __restrict__ w, int out, int in,
                                                       const __half* __restrict__ x, long long ldx, int B,
                                                       __half* __restrict__ y, long long ldy) {
-    constexpr int kTok = 8 * NT, kTile = kTok * 128;          // tokens; bytes of one group of them
+    constexpr int kTok = kManyTok, NT = kTok / 8, kTile = kTok * 128;     // kTile: bytes of one group of them
+    constexpr int kStages = kManyStages, kStage = kManyStage, kJ = kStep / 2;
     extern __shared__ __align__(128) char smem[];
     char* ring = smem;
-    __shared__ float xs[2][2][kTok];
+    __shared__ float xs[2][kStep][kTok];
+    __shared__ uint64_t full[kStages];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
     const int half = wid >> 2, rw = wid & 3;                  // parity of this warp's groups, its 16 rows
     const int n_g = in / kGroup, n_rt = ceil_div(out, kRowTile);
     const int rt = blockIdx.x * 4 + rw, b0 = blockIdx.y * kTok, nb = min(kTok, B - b0);
     const bool rows = rt < n_rt;
-    const int steps = (n_g + 1) / 2;                          // a step is two groups
+    const int steps = ceil_div(n_g, kStep);
 
-    // this thread's 16-byte pieces of a step: piece c of tokens b, b + 32.. of either group
+    // this thread's 16-byte pieces of a step: piece pc of token pb, of each group
     const int pc = tid & 7, pb = tid >> 3;
-    const __half* px = x + (long long)(b0 + pb) * ldx + pc * 8;
+    const __half* px = x + (long long)(b0 + min(pb, nb - 1)) * ldx + pc * 8;
     const uint32_t pdst = smem_u32(ring) + pb * 128 + ((pc ^ (pb & 7)) << 4);
+    const int tiles = min(4, n_rt - (int)blockIdx.x * 4);
+    const char* wsrc = w + (long long)blockIdx.x * 4 * n_g * kQ4Unit;
     auto fetch = [&](int step) {
         if (step < steps) {
-            const uint32_t dst = pdst + (step % kManyStages) * 2 * kTile;
-            const __half* src = px + step * 2 * kGroup;
-#pragma unroll
-            for (int j = 0; j < kTok / 32; ++j) {
-                const bool there = pb + 32 * j < nb;
-                const __half* row = src + (there ? (long long)(32 * j) * ldx : -(long long)pb * ldx);
-                cp_async16(dst + j * 32 * 128, row, there);
-                if (2 * step + 1 < n_g) cp_async16(dst + j * 32 * 128 + kTile, row + kGroup, there);
+            const int at = (step % kStages) * kStage;
+            if (tid == 0) {
+                const uint32_t bytes = min(kStep, n_g - kStep * step) * kQ4Unit;
+                uint64_t* bar = &full[step % kStages];
+                mbar_arrive_expect_tx(bar, tiles * bytes);
+                for (int i = 0; i < tiles; ++i)
+                    copy_bulk(ring + at + kStep * kTile + i * kStep * kQ4Unit, wsrc + ((long long)i * n_g + kStep * step) * kQ4Unit,
+                              bytes, bar);
             }
+            const __half* src = px + step * kStep * kGroup;
+            const int have = n_g - kStep * step;
+#pragma unroll
+            for (int q = 0; q < kStep; ++q)
+                if (q < have) cp_async16(pdst + at + q * kTile, src + q * kGroup, pb < nb);
         }
         cp_commit();
     };
-    const char* tile = w + (long long)(rows ? rt : 0) * n_g * kQ4Unit;
-    uint4 qn[2];
-    uint2 sn[2];
-    auto weights = [&](int step, int slot) {
-        const int c = 2 * step + half;
-        if (c < n_g) {
-            qn[slot] = __ldg(reinterpret_cast<const uint4*>(tile + (long long)c * kQ4Unit + 16 * lane));
-            sn[slot] = __ldg(reinterpret_cast<const uint2*>(tile + (long long)c * kQ4Unit + 512 + 8 * g));
-        }
-    };
-    weights(0, 0);
-    weights(1, 1);
-    for (int s = 0; s < kManyStages - 1; ++s) fetch(s);
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    for (int s = 0; s < kStages - 1; ++s) fetch(s);
 
     float y4[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) y4[nt][i] = 0.f;
-    float bias0 = 0.f, bias1 = 0.f;                           // of the group before: its sums come a step later
+    float2 bias[kJ];                                          // of the step before: x's sums come a step later
     const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
-    auto add_bias = [&](int step) {
+    auto add_bias = [&](int step, int j) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float2 v = *reinterpret_cast<const float2*>(&xs[step & 1][half][nt * 8 + 2 * t]);
-            y4[nt][0] = fmaf(bias0, v.x, y4[nt][0]);
-            y4[nt][1] = fmaf(bias0, v.y, y4[nt][1]);
-            y4[nt][2] = fmaf(bias1, v.x, y4[nt][2]);
-            y4[nt][3] = fmaf(bias1, v.y, y4[nt][3]);
+            const float2 v = *reinterpret_cast<const float2*>(&xs[step & 1][2 * j + half][nt * 8 + 2 * t]);
+            y4[nt][0] = fmaf(bias[j].x, v.x, y4[nt][0]);
+            y4[nt][1] = fmaf(bias[j].x, v.y, y4[nt][1]);
+            y4[nt][2] = fmaf(bias[j].y, v.x, y4[nt][2]);
+            y4[nt][3] = fmaf(bias[j].y, v.y, y4[nt][3]);
         }
     };
     // ldmatrix rows of this lane: token (lane & 7) + 8 (lane >> 4), 16-byte half (lane >> 3) & 1 of a k step
     const int lt = (lane & 7) + 8 * (lane >> 4), lh = (lane >> 3) & 1;
-    for (int step = 0; step < steps; ++step) {
-        cp_wait<kManyStages - 2>();
-        __syncthreads();
-        fetch(step + kManyStages - 1);
-        if (step > 0) add_bias(step - 1);
-        const bool mine = 2 * step + half < n_g;
-        if (mine) {
-            const uint4 q = step & 1 ? qn[1] : qn[0];
-            const uint2 sbw = step & 1 ? sn[1] : sn[0];
-            if (step & 1) weights(step + 2, 1);
-            else weights(step + 2, 0);
-            const uint32_t words[4] = {q.x, q.y, q.z, q.w};
-            const float2 sb0 = __half22float2(*reinterpret_cast<const __half2*>(&sbw.x));
-            const float2 sb1 = __half22float2(*reinterpret_cast<const __half2*>(&sbw.y));
-            const float s0 = sb0.x * kTwo24, s1 = sb1.x * (kTwo24 / 16.f);
-            bias0 = sb0.y;
-            bias1 = sb1.y;
-            uint32_t A[4][4];
+    auto group = [&](int step, int j, const char* stage) {    // group 2 j + half of the step
+        const int c = 2 * j + half;
+        // (a row tile behind the last: whatever is there, its rows are not written)
+        const char* unit = stage + kStep * kTile + (rw * kStep + c) * kQ4Unit;
+        const uint4 q = *reinterpret_cast<const uint4*>(unit + 16 * lane);
+        const uint2 sbw = *reinterpret_cast<const uint2*>(unit + 512 + 8 * g);
+        const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+        const float2 sb0 = __half22float2(*reinterpret_cast<const __half2*>(&sbw.x));
+        const float2 sb1 = __half22float2(*reinterpret_cast<const __half2*>(&sbw.y));
+        const float s0 = sb0.x * kTwo24, s1 = sb1.x * (kTwo24 / 16.f);
+        bias[j] = make_float2(sb0.y, sb1.y);
+        uint32_t A[4][4];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) q4_masks(words[s], A[s]);
-            const uint32_t base = smem_u32(ring) + ((step % kManyStages) * 2 + half) * kTile;
-            // two 8-token blocks at a time, the next blocks' fragments under way meanwhile
-            uint32_t bf[2][4][4];
-            auto frags = [&](int np, uint32_t (&b)[4][4]) {
-                const uint32_t at = base + (np * 16 + lt) * 128;
+        for (int s = 0; s < 4; ++s) q4_masks(words[s], A[s]);
+        const uint32_t base = smem_u32(stage) + c * kTile;
+        uint32_t b[4][2][4];
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-                                 : "=r"(b[s][0]), "=r"(b[s][1]), "=r"(b[s][2]), "=r"(b[s][3])
-                                 : "r"(at + (((2 * s + lh) ^ (lt & 7)) << 4))
-                                 : "memory");
-            };
-            frags(0, bf[0]);
+        for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int np = 0; np < NT / 2; ++np) {
-                if (np + 1 < NT / 2) frags(np + 1, bf[(np + 1) & 1]);
-                const uint32_t(&b)[4][4] = bf[np & 1];
-                float acc[2][4];
+            for (int np = 0; np < 2; ++np) ldsm4(b[s][np], base + (np * 16 + lt) * 128 + (((2 * s + lh) ^ (lt & 7)) << 4));
+        float acc[NT][4], sum[4];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) mma_16816_first(acc[j], A[0], b[0][2 * j], b[0][2 * j + 1]);
+        for (int s = 0; s < 4; ++s)
 #pragma unroll
-                for (int s = 1; s < 4; ++s)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) mma_16816_v(acc[j], A[s], b[s][2 * j], b[s][2 * j + 1]);
-                if ((np & 3) == rw) {                         // each row-warp adds up its share of the tokens
-                    float sum[2][4];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        mma_16816_first(sum[j], ones, b[0][2 * j], b[0][2 * j + 1]);
-#pragma unroll
-                        for (int s = 1; s < 4; ++s) mma_16816_v(sum[j], ones, b[s][2 * j], b[s][2 * j + 1]);
-                        if (g == 0)
-                            *reinterpret_cast<float2*>(&xs[step & 1][half][(2 * np + j) * 8 + 2 * t]) =
-                                make_float2(sum[j][0], sum[j][1]);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float(&o)[4] = y4[2 * np + j];
-                    o[0] = fmaf(s0, acc[j][0], o[0]);
-                    o[1] = fmaf(s0, acc[j][1], o[1]);
-                    o[2] = fmaf(s1, acc[j][2], o[2]);
-                    o[3] = fmaf(s1, acc[j][3], o[3]);
-                }
+            for (int i = 0; i < NT; ++i) {                    // blocks next to each other: none waits for the one before
+                const uint32_t x0 = b[s][i >> 1][2 * (i & 1)], x1 = b[s][i >> 1][2 * (i & 1) + 1];
+                if (s == 0) mma_16816_first(acc[i], A[0], x0, x1);
+                else mma_16816_v(acc[i], A[s], x0, x1);
             }
+        // each row-warp adds up x of one of the four blocks
+        uint32_t xb[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) ldsm4(xb[h], base + (rw * 8 + (lane & 7)) * 128 + (((4 * h + (lane >> 3)) ^ (lane & 7)) << 4));
+        mma_16816_first(sum, ones, xb[0][0], xb[0][1]);
+        mma_16816_v(sum, ones, xb[0][2], xb[0][3]);
+        mma_16816_v(sum, ones, xb[1][0], xb[1][1]);
+        mma_16816_v(sum, ones, xb[1][2], xb[1][3]);
+        if (g == 0) *reinterpret_cast<float2*>(&xs[step & 1][c][rw * 8 + 2 * t]) = make_float2(sum[0], sum[1]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            y4[i][0] = fmaf(s0, acc[i][0], y4[i][0]);
+            y4[i][1] = fmaf(s0, acc[i][1], y4[i][1]);
+            y4[i][2] = fmaf(s1, acc[i][2], y4[i][2]);
+            y4[i][3] = fmaf(s1, acc[i][3], y4[i][3]);
+        }
+    };
+    bool dead = false;
+    for (int step = 0; step < steps; ++step) {
+        const char* stage = ring + (step % kStages) * kStage;
+        cp_wait<kStages - 2>();
+        if (!dead && !wait_copy(&full[step % kStages], (uint32_t)(step / kStages) & 1)) dead = true;
+        __syncthreads();                                      // the stage of the step before is free, too
+        fetch(step + kStages - 1);
+        if (step > 0)
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) add_bias(step - 1, j);
+        const int have = n_g - kStep * step;
+        if (have >= kStep) {
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) group(step, j, stage);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kJ; ++j)
+                if (2 * j + half < have) group(step, j, stage);
         }
     }
     __syncthreads();
-    if (2 * (steps - 1) + half < n_g) add_bias(steps - 1);
+    const int have = n_g - kStep * (steps - 1);
+#pragma unroll
+    for (int j = 0; j < kJ; ++j)
+        if (2 * j + half < have) add_bias(steps - 1, j);
+    if (dead)                                                 // a copy that never came: NaN marks the rows
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y4[nt][i] = __int_as_float(0x7fffffff);
     // the odd groups' sums through shared memory
     cp_wait<0>();
     __syncthreads();
-    float* other = reinterpret_cast<float*>(ring);            // [4][kTok / 2 pairs ..][lane] as written
+    float4* other = reinterpret_cast<float4*>(ring);          // [row tile][8-token block][lane]
     if (half == 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-            *reinterpret_cast<float4*>(other + ((rw * NT + nt) * 32 + lane) * 4) =
-                make_float4(y4[nt][0], y4[nt][1], y4[nt][2], y4[nt][3]);
+            other[(rw * NT + nt) * 32 + lane] = make_float4(y4[nt][0], y4[nt][1], y4[nt][2], y4[nt][3]);
     __syncthreads();
     if (half == 0 && rows) {
         const int r0 = rt * kRowTile + g;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float4 o = *reinterpret_cast<const float4*>(other + ((rw * NT + nt) * 32 + lane) * 4);
+            const float4 o = other[(rw * NT + nt) * 32 + lane];
             const float v[4] = {y4[nt][0] + o.x, y4[nt][1] + o.y, y4[nt][2] + o.z, y4[nt][3] + o.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -398,7 +448,6 @@ __global__ void __launch_bounds__(256, 2) q4_many_kernel(const char* __restrict_
 }
 
 constexpr int kFewSmem = 220 * 1024;
-constexpr int many_smem(int NT) { return kManyStages * 2 * 8 * NT * 128; }
 
 // what a device needs before its first launch
 int setup(int dev, int* sms) {
@@ -412,8 +461,7 @@ int setup(int dev, int* sms) {
         for (const void* f : few)
             if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem) != cudaSuccess)
                 return EDGE0_ECUDA;
-        if (cudaFuncSetAttribute(q4_many_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, many_smem(8)) !=
-                cudaSuccess ||
+        if (cudaFuncSetAttribute(q4_many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kManySmem) != cudaSuccess ||
             cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return EDGE0_ECUDA;
         __atomic_store_n(&known[dev], n, __ATOMIC_RELEASE);
@@ -455,12 +503,7 @@ extern "C" int edge0_q4_linear(const void* packed, int out, int in, const uint16
                           : (RT == 1 ? q4_few_kernel<2, 1> : q4_few_kernel<2, 2>);
         f<<<grid, kThreadsQ, smem, stream>>>(w, out, in, xh, ldx, B, tokens, yh, ldy);
     } else {
-        // 64 tokens per CTA where that fills the card, else 32
-        const int rows = ceil_div(n_rt, 4);
-        if (B > 32 && rows * ceil_div(B, 64) >= sms)
-            q4_many_kernel<8><<<dim3(rows, ceil_div(B, 64)), 256, many_smem(8), stream>>>(w, out, in, xh, ldx, B, yh, ldy);
-        else
-            q4_many_kernel<4><<<dim3(rows, ceil_div(B, 32)), 256, many_smem(4), stream>>>(w, out, in, xh, ldx, B, yh, ldy);
+        q4_many_kernel<<<dim3(ceil_div(n_rt, 4), ceil_div(B, kManyTok)), 256, kManySmem, stream>>>(w, out, in, xh, ldx, B, yh, ldy);
     }
     return cudaGetLastError() == cudaSuccess ? EDGE0_OK : EDGE0_ECUDA;
 }
