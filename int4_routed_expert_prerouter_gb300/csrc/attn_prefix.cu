@@ -53,30 +53,6 @@ struct Cfg {
     static constexpr int kCtas = D <= 128 ? 2 : 1;
 };
 
-typedef unsigned long long f2;      // two packed fp32
-
-__device__ __forceinline__ f2 pk(float a, float b) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpk(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // 16 rows x 32 columns of fp32: lane (g, t) = (lane / 4, lane % 4) holds of each 8-column block
 // columns 2t, 2t + 1 of row g (r[4j], r[4j + 1]) and of row g + 8 (r[4j + 2], r[4j + 3])
 __device__ __forceinline__ void tmem_ld_frag(uint32_t a, uint32_t (&r)[16]) {

@@ -6,16 +6,20 @@
 //     q = clamp(rne((x - mn) / s), 0, 2^bits - 1)    (0 where s = 0);
 // s one fp16 step less where (2^bits - 1) s + b would round to infinity,
 // and the stored group stands for s q + b.  q is the exact quotient's rounding: the
-// kernel rounds the fp32 product (x - mn) * (1 / s), and where that lies next to
-// a border it decides by the sign of (x - mn) - (q +- 1/2) s, which fp32 holds
-// exactly there.
+// kernel rounds the fp32 products of x - mn with a little less and a little more than
+// 1 / s, and where these differ it decides by the sign of (x - mn) - (q +- 1/2) s, which
+// fp32 holds exactly there.
 //
-// Both kernels move rows of fp16 and bytes of codes.  A thread keeps its place in the
-// row and goes through its CTA's rows.  Written: 16 dims per thread, 8 from each half of
-// a group (four threads share its minimum, maximum and reciprocal); the next row's
-// values are loaded while one is worked on, the first ones before the rows' places are
-// known.  Read: 8 dims per thread, so that a warp's 16-byte stores lie side by side, four
-// rows at a time.
+// Both kernels move rows of fp16 and bytes of codes: the floor is these bytes.  A thread keeps
+// its place in the row and goes through its CTA's rows.  Written: 16 dims per thread, 8
+// from each half of a group (four threads share its minimum, maximum and reciprocal); the
+// next row's values are loaded while one is worked on, the first ones before the rows'
+// places are known.  Read: 8 dims per thread, so that a warp's 16-byte stores lie side by
+// side, four rows at a time.
+// Measured: 8,192 rows of 8 x 128 dims written as 8 bits and read back 22.9 us, 80 MB at 3.5
+// TB/s (a copy: 6.8), one third of it start-up of two launches, places and first loads;
+// 63,001 such rows of 4 bits read 57 us, 331 MB at 5.8 TB/s; one row for each of 64
+// sequences written and read 6.6 us, two launches' latency.
 #include "kvcache.cuh"
 
 namespace edge0 {
@@ -133,18 +137,22 @@ __device__ __forceinline__ void quantise16(const uint4 (&raw)[2], uint32_t (&wor
     if (!bad && s != 0.f) {
         float inv;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-        float t[16], off = 0.f;                          // kRound + q
+        // Quotients with a reciprocal a little below and a little above: the exact one lies between
+        // (its error is at most 2^-23 of the reciprocal and 2^-24 of d), so where both round
+        // to the same number it does too.
+        const f2 lo = pk(inv * (1.f - 0x1.8p-22f), inv * (1.f - 0x1.8p-22f));
+        const f2 hi = pk(inv * (1.f + 0x1.8p-22f), inv * (1.f + 0x1.8p-22f));
+        const f2 from = pk(-mn, -mn), round = pk(kRound, kRound);
+        float t[16];                                     // kRound + q
+        f2 differ = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float2 f = __half22float2(h2[i]);
-            const float d0 = f.x - mn, d1 = f.y - mn;
-            t[2 * i] = fmaf(d0, inv, kRound);
-            t[2 * i + 1] = fmaf(d1, inv, kRound);
-            off = fmaxf(off, fmaxf(fabsf(fmaf(kRound - t[2 * i], s, d0)), fabsf(fmaf(kRound - t[2 * i + 1], s, d1))));
+            const f2 d = add2(pk(f.x, f.y), from), below = fma2(d, lo, round);
+            differ |= below ^ fma2(d, hi, round);
+            unpk(below, t[2 * i], t[2 * i + 1]);
         }
-        // q is settled unless a residual comes to half a step (the residuals are off by at most
-        // the rounding of d, 255 x 2^-24 of a step)
-        if (off > 0.49998f * s || range * inv > kTop + 0.5f) {
+        if (differ != 0 || range * inv > kTop + 0.5f) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float2 f = __half22float2(h2[i]);
@@ -208,7 +216,7 @@ struct Place {
 };
 
 template <int BITS, int D>
-__global__ void __launch_bounds__(kKvThreads, 3) kv_append_kernel(kv::View c, Rows rows, int rows_per_cta,
+__global__ void __launch_bounds__(kKvThreads, 4) kv_append_kernel(kv::View c, Rows rows, int rows_per_cta,
                                                                   const __half* __restrict__ k, long long ldk,
                                                                   const __half* __restrict__ v, long long ldv) {
     constexpr int kR = kv::row_bytes(BITS, D);
@@ -317,9 +325,10 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(kv::View c, Rows ro
     }
 }
 
-// rows per CTA: so many that about `ctas` CTAs per SM cover T, at most `most`.  Measured, us
-// (written: 8,192 rows of 8 x 128 dims, with their reading; read: 63,001 such rows): written 4
-// or 8 per SM 27.7 and 29.0; read at most 16, 32 or 64 rows 59.4, 62.6 and 68.9.
+// rows per CTA: so many that `ctas` CTAs per SM, as many as are resident at once, cover T, at most
+// `most`.  Measured, us, 8,192 rows of 8 x 128 dims as 8 bits: written with 4 resident CTAs (64
+// registers) 12, with 3 and rows for 4 per SM 17; then read with rows for 5 or 8 per SM 22.9
+// and 23.3 both together; 63,001 rows read at most 16, 32 or 64 at a time 57, 62 and 69.
 int rows_per_cta(int T, int ctas, int most) {
     const int r = ceil_div(T, 152 * ctas);
     return r < 1 ? 1 : r > most ? most : r;
@@ -389,7 +398,7 @@ extern "C" int edge0_kv_read(const edge0_kv_cache* cache, const int32_t* table, 
     if (rc) return rc;
     if (T == 0) return EDGE0_OK;
     if (!k || !v || (((uintptr_t)k | (uintptr_t)v) & 15)) return EDGE0_EINVAL;
-    const int per = rows_per_cta(T, 8, 16);
+    const int per = rows_per_cta(T, 5, 16);
     EDGE0_KV_DISPATCH(cache->bits, cache->head_dim,
                       (kv_read_kernel<BT, DD><<<ceil_div(T, per), kKvThreads, 0, stream>>>(c, rows, per, (__half*)k,
                                                                                          (__half*)v)));
