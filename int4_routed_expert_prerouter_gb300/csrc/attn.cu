@@ -786,8 +786,16 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinP p) {
             const int s = s0 + 4 * u;
             if (s < n) {
                 const float* src = (s < n0 ? o[0] + s * step0 * D : o[1] + (s - n0) * step1 * D) + lane * kN;
+                if constexpr (kN == 2) {
+                    const float2 x = *reinterpret_cast<const float2*>(src);
+                    part[u][0] = x.x, part[u][1] = x.y;
+                } else {
 #pragma unroll
-                for (int e = 0; e < kN; ++e) part[u][e] = src[e];
+                    for (int e = 0; e < kN; e += 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(src + e);
+                        part[u][e] = x.x, part[u][e + 1] = x.y, part[u][e + 2] = x.z, part[u][e + 3] = x.w;
+                    }
+                }
             }
         }
     };
