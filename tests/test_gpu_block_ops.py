@@ -382,6 +382,14 @@ def test_attention_lengths(bits, lens, P):
     run_attention(bits, 128, 2, 4, 64, lens, P, seed=len(lens))
 
 
+@pytest.mark.parametrize("bits,D,P", [(4, 128, 0), (8, 64, 40), (8, 256, 0), (4, 256, 130)])
+def test_attention_one_long_sequence_in_a_large_batch(bits, D, P):
+    # its parts are many, the other sequences' rows have none, one or two
+    lens = [int(n) for n in np.random.default_rng(D).integers(0, 40, 129)]
+    lens[77], lens[5] = 16001, 700
+    run_attention(bits, D, 1, 8, 64, lens, P, seed=3, pad=(0, 128))
+
+
 def test_attention_many_query_heads():
     run_attention(4, 64, 1, 64, 16, [33, 0, 7], 50)
     run_attention(8, 128, 2, 33, 32, [64, 1], 130)
