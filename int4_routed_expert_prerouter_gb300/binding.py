@@ -594,7 +594,7 @@ def _guard(index, stream):
     stream's: that stream (its device too), or that device; None where they are."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    return None if index == torch.cuda.current_device() else torch.cuda.device(index)
+    return None if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
 
 
 def _raw_stream(index, stream):
@@ -649,7 +649,7 @@ def _q4_linear(packed, out_features, x, y, index, stream):
             or packed.numel() != (out_features + 15) // 16 * (n_in // 64) * 576 or out_features <= 0 or n_in == 0):
         raise _bad("q4_linear: packed is not an [out_features, in] matrix beside x")
     if y is None:
-        y, ldy = torch.empty((B, out_features), dtype=_f16, device=x.device), out_features
+        y, ldy = x.new_empty((B, out_features)), out_features
     else:
         if y.shape != (B, out_features) or y.get_device() != index:
             raise _bad("q4_linear: y [B, out_features] beside x")
@@ -686,7 +686,7 @@ class KVCache:
         self.status = torch.zeros(1, dtype=torch.int32, device=pages.device)
         self.desc = KvCacheDesc(bits, n_kv_heads, head_dim, page_tokens, n_pages, _ptr(pages))
         self._index, self._desc, self._status = pages.get_device(), C.byref(self.desc), self.status.data_ptr()
-        self._ws_bytes = {}
+        self._ws_bytes, self._ws = {}, {}
 
     def error(self) -> int:
         """What the calls on this cache have recorded since the last error() (waits
@@ -775,14 +775,27 @@ def attn_workspace_bytes(cache: KVCache, B: int, n_q_heads: int) -> int:
     return n
 
 
+def _workspace(cache, nbytes, handle):
+    """Scratch of a call that was given none: one buffer per cache and stream, whose calls run one
+    after the other; a call that is being captured gets its own, from the graph's pool, because
+    graphs may replay beside other work of the stream they were captured on."""
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(nbytes, dtype=_u8, device=cache.device)
+    ws = cache._ws.get(handle)
+    if ws is None or ws.numel() < nbytes:
+        ws = cache._ws[handle] = torch.empty(nbytes, dtype=_u8, device=cache.device)
+    return ws
+
+
 def attn_decode(cache: KVCache, q: torch.Tensor, table, lens, prefix=None, n_prefix=0, scale=None, out=None,
                 workspace=None, stream=None) -> torch.Tensor:
     """Attention of one query token per sequence, q [B, n_q_heads, head_dim] fp16, over
     the shared prefix (n_prefix tokens of the pages `prefix`, int32) and then the
     sequence's own lens[b] tokens of the pages table[b].  scale: 1 / sqrt(head_dim)
     unless given.  out: rows to fill (those of sequences with lens[b] < 0 are left as
-    they are) or None.  workspace: uint8 of attn_workspace_bytes, or None for one of the
-    call's own."""
+    they are) or None.  workspace: uint8 of attn_workspace_bytes, not used by anything else
+    while the call runs, or None for one that the cache keeps per stream (a captured call:
+    one of its own)."""
     guard = _guard(cache._index, stream)
     if guard is not None:
         with guard:
@@ -806,23 +819,24 @@ def _attn_decode(cache, q, table, lens, prefix, n_prefix, scale, out, workspace,
             raise _bad("attn_decode: n_prefix tokens in the pages `prefix`")
         pf = _ints(prefix, index, prefix.numel(), "attn_decode: prefix")
     if out is None:
-        out, ldo = torch.empty((B, Hq, D), dtype=_f16, device=cache.device), Hq * D
+        out, ldo = q.new_empty((B, Hq, D)), Hq * D
     else:
         if out.shape != q.shape or out.get_device() != index:
             raise _bad("attn_decode: out like q")
         ldo = _row_stride(out, "attn_decode: out")
     if B == 0:
         return out
-    nbytes = attn_workspace_bytes(cache, B, Hq)
+    handle = _raw_stream(index, stream)
     if workspace is None:
-        workspace = torch.empty(nbytes or 16, dtype=_u8, device=cache.device)
+        nbytes = attn_workspace_bytes(cache, B, Hq)
+        workspace = _workspace(cache, nbytes or 16, handle)
     else:
         if workspace.dtype is not _u8 or workspace.get_device() != index or not workspace.is_contiguous():
             raise _bad("attn_decode: workspace uint8, contiguous, beside the cache")
         nbytes = workspace.numel()
     code = _lib.edge0_attn_decode(cache._desc, q.data_ptr(), ldq, B, Hq, tb, W, ln, pf, n_prefix,
                                   D ** -0.5 if scale is None else scale, out.data_ptr(), ldo, cache._status,
-                                  workspace.data_ptr(), nbytes, _raw_stream(index, stream))
+                                  workspace.data_ptr(), nbytes, handle)
     if code:
         raise Edge0Error(code, "edge0_attn_decode")
     return out

@@ -709,6 +709,39 @@ def test_two_captured_graphs_with_their_own_workspaces_overlap():
     assert torch.equal(outs[0], a) and torch.equal(outs[1], b)
 
 
+def test_kept_workspaces_are_not_shared_across_streams_and_graphs():
+    """Calls without a workspace: eager ones on two streams and replays of a graph captured on one
+    of them, all under way together, and one of another size in between."""
+    a, _ = run_attention(4, 128, 2, 4, 64, [700, 0, 33, 1200], 500)
+    b, _ = run_attention(8, 64, 2, 8, 32, [3000, 15, 900], 0, seed=4)
+    args = (a[0],) + a[1:]
+    want = binding.attn_decode(*args)
+    q1 = a[1][:1].contiguous()
+    small = binding.attn_decode(a[0], q1, a[2][:1].contiguous(), a[3][:1].contiguous(), a[4], a[5])
+    other = binding.attn_decode(*b)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [[], [], []]
+    with torch.cuda.stream(one):
+        binding.attn_decode(*args)
+    one.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=one):
+        captured = binding.attn_decode(*args)
+    for _ in range(20):
+        with torch.cuda.stream(one):
+            outs[0].append(binding.attn_decode(*args))
+            outs[1].append(binding.attn_decode(a[0], q1, a[2][:1].contiguous(), a[3][:1].contiguous(), a[4], a[5]))
+        with torch.cuda.stream(two):
+            g.replay()
+            outs[2].append(captured.clone())
+            outs[0].append(binding.attn_decode(*args))
+        assert torch.equal(binding.attn_decode(*b), other)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs[0] + outs[2])
+    assert all(torch.equal(o, small) for o in outs[1])
+
+
 def test_binding_refuses_what_does_not_fit():
     E = binding.Edge0Error
     cache = binding.KVCache(4, 16, 2, 64, 4, device=DEV)
