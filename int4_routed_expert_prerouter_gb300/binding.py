@@ -649,7 +649,8 @@ def _q4_linear(packed, out_features, x, y, index, stream):
             or packed.numel() != (out_features + 15) // 16 * (n_in // 64) * 576 or out_features <= 0 or n_in == 0):
         raise _bad("q4_linear: packed is not an [out_features, in] matrix beside x")
     if y is None:
-        y, ldy = x.new_empty((B, out_features)), out_features
+        # (x.new_empty would cost the launch behind it 3 us more)
+        y, ldy = torch.empty((B, out_features), dtype=_f16, device=x.device), out_features
     else:
         if y.shape != (B, out_features) or y.get_device() != index:
             raise _bad("q4_linear: y [B, out_features] beside x")
@@ -819,7 +820,7 @@ def _attn_decode(cache, q, table, lens, prefix, n_prefix, scale, out, workspace,
             raise _bad("attn_decode: n_prefix tokens in the pages `prefix`")
         pf = _ints(prefix, index, prefix.numel(), "attn_decode: prefix")
     if out is None:
-        out, ldo = q.new_empty((B, Hq, D)), Hq * D
+        out, ldo = torch.empty((B, Hq, D), dtype=_f16, device=cache.device), Hq * D
     else:
         if out.shape != q.shape or out.get_device() != index:
             raise _bad("attn_decode: out like q")
