@@ -35,7 +35,7 @@
 // bounds it are the instructions that unpack the codes and take care of scales (64 % of the issue
 // slots, 61 % of the integer and half-precision pipe); the matrix pipe is a quarter taken.
 // Four CTAs of four warps per SM (128 registers each); with three, and query fragments read
-// from shared memory, 133 us.  One sequence of 777 tokens 10.3 us: two launches and
+// from shared memory, 133 us.  One sequence of 777 tokens 10.2 us: two launches and
 // the reads that wait for one another (length, page, codes; shares, sums, parts).
 //
 // ldmatrix delivers K codes as A fragments and, transposed, V codes with the
@@ -72,7 +72,7 @@ struct AttnP {
     __half* out;             // set: segments that one CTA has whole are written here
     long long ldo;
     int* status;
-    bool early;              // launched before the prefix's kernel has ended
+    bool after_prefix;       // begins while the prefix's kernel runs, which has waited for what came before
 };
 
 template <int BITS, int D, int NT>
@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
     constexpr int kUnit = 16 * X::US;
     constexpr float kZ = BITS == 4 ? 8.f : 128.f;
 
+    if (!p.after_prefix) wait_predecessor();
     launch_dependents();     // attn_join_kernel, which waits for this kernel's end
     // lengths, and the cost before each list: a scan over at most 256 of them
     const int per_list = p.H * p.RB;
@@ -738,8 +739,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
             __syncthreads();
         }
     }
-    // The prefix's kernel may still be running (this one is launched early and does not
-    // need it): its end is this kernel's end, so that the join finds both parts.
+    // The prefix's kernel may still be running, which this one does not need: its end comes
+    // before this kernel's, so that the join finds both parts.
     wait_predecessor();
 }
 
@@ -871,6 +872,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinP p) {
     __shared__ float acc[4][D];
     const int len = p.lens[blockIdx.x / (p.G * p.H)];
     wait_predecessor();
+    launch_dependents();
     const RowParts x(p, blockIdx.x, len, D);
     if (!x.done) join_by_cta<D>(p, x, acc);
 }
@@ -887,6 +889,7 @@ __global__ void __launch_bounds__(128) attn_join_rows_kernel(const JoinP p) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, row = blockIdx.x * 4 + wid;
     const int len = row < p.n_rows ? p.lens[row / (p.G * p.H)] : -1;
     wait_predecessor();
+    launch_dependents();
     bool alone = false;
     if (row < p.n_rows) {
         const RowParts x(p, row, len, D);
@@ -986,7 +989,7 @@ int launch(const AttnP& p, long long most_units, cudaStream_t stream) {
     }
     const long long want = (most_units + kMinShare + kSegCost - 1) / (kMinShare + kSegCost);
     const int grid = want < n ? (int)(want < 1 ? 1 : want) : n;
-    return launch_kernel(attn_kernel<BITS, D, NT>, dim3(grid), 32 * kWarps, X::kSmem, stream, p.early, p);
+    return launch_early(attn_kernel<BITS, D, NT>, dim3(grid), 32 * kWarps, X::kSmem, stream, p);
 }
 
 template <int BITS, int D>
@@ -1013,10 +1016,10 @@ int launch_any(const AttnP& p, int bits, int D, int NT, cudaStream_t stream) {
 
 template <int D>
 int launch_join(const JoinP& j, int rows, cudaStream_t stream) {
-    if (rows < kManyRows) return launch_kernel(attn_join_kernel<D>, dim3(rows), 128, 0, stream, true, j);
+    if (rows < kManyRows) return launch_early(attn_join_kernel<D>, dim3(rows), 128, 0, stream, j);
     JoinP many = j;
     many.n_rows = rows;
-    return launch_kernel(attn_join_rows_kernel<D>, dim3(ceil_div(rows, 4)), 128, 0, stream, true, many);
+    return launch_early(attn_join_rows_kernel<D>, dim3(ceil_div(rows, 4)), 128, 0, stream, many);
 }
 
 }  // namespace
@@ -1081,7 +1084,7 @@ extern "C" int edge0_attn_decode(const edge0_kv_cache* cache, const uint16_t* q,
         p.part_ml = (float2*)(ws + part[w].ml);
         p.seg = (int2*)(ws + part[w].seg);
         p.out = !w && !n_prefix ? (__half*)out : nullptr;
-        p.early = !w && n_prefix;
+        p.after_prefix = !w && n_prefix;
         rc = launch_any(p, cache->bits, D, part[w].NT, stream);
         if (rc) return rc;
     }

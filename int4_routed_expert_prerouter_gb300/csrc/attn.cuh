@@ -2,6 +2,7 @@
 // fifth-generation tensor cores (attn_prefix.cu), launched by attn.cu.
 #pragma once
 #include "kvcache.cuh"
+#include "launch.cuh"
 
 namespace edge0 {
 
@@ -30,26 +31,6 @@ struct PrefixP {
 // shares of the prefix that fill the card for `segs` (K/V head, row block) pairs
 void prefix_shares(int n_tok, int segs, int D, int sms, int* splits, int* tiles_per_split);
 int prefix_launch(const PrefixP& p, int bits, int D, cudaStream_t stream);
-
-// Launches that overlap: a kernel that lets its successor in the stream start early
-// (launch_dependents), and waits for its predecessor where it needs its results
-// (wait_predecessor; a kernel launched without `early` has none to wait for).
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
-__device__ __forceinline__ void wait_predecessor() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
-template <typename P>
-inline int launch_kernel(void (*f)(P), dim3 grid, int threads, int smem, cudaStream_t stream, bool early, const P& p) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = early ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, f, p) == cudaSuccess ? EDGE0_OK : EDGE0_ECUDA;
-}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;

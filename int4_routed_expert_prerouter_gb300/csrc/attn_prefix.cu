@@ -199,7 +199,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
     const int n = min(p.tiles_per_split, all - t0);
     const int r0 = rb * kRowsQ;
 
-    launch_dependents();     // the sequences' own parts do not need this kernel's results
     if (wid == 0) {
         tc::tmem_alloc(&taddr_s, X::kCols);
         tc::tmem_relinquish();
@@ -217,6 +216,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tm = taddr_s;
+    launch_dependents();     // the sequences' own parts do not need this kernel's results
 
     if (wid < 8) {
         // queries, K-major, 8 dims in the order of the codes; a thread's pieces 16 rows (of D = 128) apart
@@ -695,8 +695,10 @@ int launch(const PrefixP& p, cudaStream_t stream) {
             return EDGE0_ECUDA;
         __atomic_store_n(&set[dev], 1, __ATOMIC_RELEASE);
     }
-    return launch_kernel(attn_prefix_kernel<BITS, D>, dim3(p.splits, p.RB, p.H), kThreads, Cfg<BITS, D>::kSmem, stream,
-                         false, p);
+    // (Not launch_early: CTAs that are placed while the kernel before still holds its SMs share SMs
+    // that others leave empty; 64 sequences behind 3,100 tokens 39.5 us, so 36.1.)
+    attn_prefix_kernel<BITS, D><<<dim3(p.splits, p.RB, p.H), kThreads, Cfg<BITS, D>::kSmem, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? EDGE0_OK : EDGE0_ECUDA;
 }
 
 }  // namespace

@@ -16,11 +16,12 @@
 // next row's values are loaded while one is worked on, the first ones before the rows'
 // places are known.  Read: 8 dims per thread, so that a warp's 16-byte stores lie side by
 // side, four rows at a time.
-// Measured: 8,192 rows of 8 x 128 dims written as 8 bits and read back 22.9 us, 80 MB at 3.5
+// Measured: 8,192 rows of 8 x 128 dims written as 8 bits and read back 21.6 us, 80 MB at 3.7
 // TB/s (a copy: 6.8), one third of it start-up of two launches, places and first loads;
 // 63,001 such rows of 4 bits read 57 us, 331 MB at 5.8 TB/s; one row for each of 64
-// sequences written and read 6.6 us, two launches' latency.
+// sequences written and read 5.7 us, two launches' latency.
 #include "kvcache.cuh"
+#include "launch.cuh"
 
 namespace edge0 {
 namespace {
@@ -217,8 +218,8 @@ struct Place {
 
 template <int BITS, int D>
 __global__ void __launch_bounds__(kKvThreads, 4) kv_append_kernel(kv::View c, Rows rows, int rows_per_cta,
-                                                                  const __half* __restrict__ k, long long ldk,
-                                                                  const __half* __restrict__ v, long long ldv) {
+                                                                  const __half* k, long long ldk,
+                                                                  const __half* v, long long ldv) {
     constexpr int kR = kv::row_bytes(BITS, D);
     __shared__ int cu_s[EDGE0_MAX_BATCHED + 1];
     __shared__ RowPlace place[kMaxRowsPerCta];
@@ -227,6 +228,8 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv_append_kernel(kv::View c, Ro
     const int half_row = c.H * (D / 16), per_row = 2 * half_row;   // threads' worth of work per row
     const Place me(per_row);
     const int last = (per_row + kKvThreads - 1) / kKvThreads * kKvThreads;     // whole warps: the quantiser's shuffles
+    wait_predecessor();
+    launch_dependents();
     bool placed = false;
     for (int j = me.j; j < last; j += kKvThreads) {
         const int which = j >= half_row, hj = j - which * half_row, h = hj / (D / 16), at = hj % (D / 16);
@@ -276,11 +279,13 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv_append_kernel(kv::View c, Ro
 
 template <int BITS, int D>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(kv::View c, Rows rows, int rows_per_cta,
-                                                             __half* __restrict__ k, __half* __restrict__ v) {
+                                                             __half* k, __half* v) {
     constexpr int kR = kv::row_bytes(BITS, D);
     __shared__ int cu_s[EDGE0_MAX_BATCHED + 1];
     __shared__ RowPlace place[kMaxRowsPerCta];
     const int r0 = blockIdx.x * rows_per_cta;
+    wait_predecessor();
+    launch_dependents();
     place_rows(c, kv::strip_bytes(BITS, D), rows, r0, rows_per_cta, cu_s, place);
     const int half_row = c.H * (D / 8), per_row = 2 * half_row;
     const Place me(per_row);
@@ -346,16 +351,16 @@ int check_rows(const Rows& r) {
 
 using namespace edge0;
 
-#define EDGE0_KV_DISPATCH(bits, D, CALL)                                  \
+#define EDGE0_KV_DISPATCH(bits, D, ...)                                  \
     do {                                                                  \
         if ((bits) == 4) {                                                \
-            if ((D) == 64) { constexpr int BT = 4, DD = 64; CALL; }       \
-            else if ((D) == 128) { constexpr int BT = 4, DD = 128; CALL; } \
-            else { constexpr int BT = 4, DD = 256; CALL; }                \
+            if ((D) == 64) { constexpr int BT = 4, DD = 64; __VA_ARGS__; }       \
+            else if ((D) == 128) { constexpr int BT = 4, DD = 128; __VA_ARGS__; } \
+            else { constexpr int BT = 4, DD = 256; __VA_ARGS__; }                \
         } else {                                                          \
-            if ((D) == 64) { constexpr int BT = 8, DD = 64; CALL; }       \
-            else if ((D) == 128) { constexpr int BT = 8, DD = 128; CALL; } \
-            else { constexpr int BT = 8, DD = 256; CALL; }                \
+            if ((D) == 64) { constexpr int BT = 8, DD = 64; __VA_ARGS__; }       \
+            else if ((D) == 128) { constexpr int BT = 8, DD = 128; __VA_ARGS__; } \
+            else { constexpr int BT = 8, DD = 256; __VA_ARGS__; }                \
         }                                                                 \
     } while (0)
 
@@ -382,9 +387,9 @@ extern "C" int edge0_kv_append(const edge0_kv_cache* cache, const uint16_t* k, l
         return EDGE0_EINVAL;
     const int per = rows_per_cta(T, 4, kMaxRowsPerCta);
     EDGE0_KV_DISPATCH(cache->bits, cache->head_dim,
-                      (kv_append_kernel<BT, DD><<<ceil_div(T, per), kKvThreads, 0, stream>>>(
-                          c, rows, per, (const __half*)k, ldk, (const __half*)v, ldv)));
-    return cudaGetLastError() == cudaSuccess ? EDGE0_OK : EDGE0_ECUDA;
+                      rc = launch_early(kv_append_kernel<BT, DD>, dim3(ceil_div(T, per)), kKvThreads, 0, stream, c, rows, per,
+                                        (const __half*)k, ldk, (const __half*)v, ldv));
+    return rc;
 }
 
 extern "C" int edge0_kv_read(const edge0_kv_cache* cache, const int32_t* table, int B, int W, const int32_t* start,
@@ -400,7 +405,7 @@ extern "C" int edge0_kv_read(const edge0_kv_cache* cache, const int32_t* table, 
     if (!k || !v || (((uintptr_t)k | (uintptr_t)v) & 15)) return EDGE0_EINVAL;
     const int per = rows_per_cta(T, 5, 16);
     EDGE0_KV_DISPATCH(cache->bits, cache->head_dim,
-                      (kv_read_kernel<BT, DD><<<ceil_div(T, per), kKvThreads, 0, stream>>>(c, rows, per, (__half*)k,
-                                                                                         (__half*)v)));
-    return cudaGetLastError() == cudaSuccess ? EDGE0_OK : EDGE0_ECUDA;
+                      rc = launch_early(kv_read_kernel<BT, DD>, dim3(ceil_div(T, per)), kKvThreads, 0, stream, c, rows, per,
+                                        (__half*)k, (__half*)v));
+    return rc;
 }

@@ -1,0 +1,35 @@
+// Launches that overlap.  A kernel launched by launch_early may begin while its predecessor in
+// the stream is still running, once every CTA of that one has said launch_dependents() or ended;
+// wait_predecessor() returns when the predecessor has ended and what it wrote can be read.
+// Every kernel launched so waits before it reads or writes global memory, and says
+// launch_dependents() only then: whoever has begun knows that all that came before its
+// predecessor has ended.  (One does not wait, attn_kernel behind the prefix's kernel, which is launched
+// in plain order and so has itself begun behind all else.)  (A kernel of another kind before or after it sees plain stream order.)
+// (No __restrict__ on what such a kernel reads: the compiler may move a load that it takes for
+// constant above the wait.)
+// What it saves is the launch's latency: an append and a read of 64 rows 6.6 -> 5.7 us, a projection
+// 65,537 x 2048 of one token 17.4 -> 16.6.
+#pragma once
+#include "internal.cuh"
+
+namespace edge0 {
+
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_predecessor() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
+template <typename... A>
+inline int launch_early(void (*f)(A...), dim3 grid, int threads, int smem, cudaStream_t stream, A... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, f, args...) == cudaSuccess ? EDGE0_OK : EDGE0_ECUDA;
+}
+
+}  // namespace edge0

@@ -10,20 +10,21 @@
 // turn, its eight warps a slice of the groups each, through rings of bulk copies (a
 // slice is one run of bytes); x and its group sums stay in shared memory, laid down
 // once.  A warp has its 16 rows for all tokens, so a nibble is unpacked once.  Measured:
-// 65,537 x 2048 at one token 17.3 us, 4.4 TB/s of weights, 0.64 of what a copy reaches:
+// 65,537 x 2048 at one token 16.5 us, 4.6 TB/s of weights, 0.68 of what a copy reaches:
 // the unpacking's instructions (issue slots 54 % taken) and the step's join across
-// warps, not the memory, are the limit; 5120 x 2048 at 7 tokens 6.6 us and
-// 2048 x 2048 at one token 2.9 us are launch, one latency of x, one of the weights and
+// warps, not the memory, are the limit; 5120 x 2048 at 7 tokens 6.0 us and
+// 2048 x 2048 at one token 2.5 us are launch, one latency of x, one of the weights and
 // the join.
 // More tokens (q4_many_kernel).  64 rows x 32 tokens per CTA, four warps for the even
 // groups and four for the odd ones, x and weights through one ring, four groups
 // between two barriers; the group sums of x are one more matrix step against ones.
 // A CTA alone on its SM is bound by latency (0.8 us per step of four groups, with two 1.3 us:
-// the matrix pipe is half taken then).  6144 x 1536 at 64 tokens 11.1 us, 109
+// the matrix pipe is half taken then).  6144 x 1536 at 64 tokens 10.5 us, 115
 // TFLOP/s; 20,000 x 2048 at 256 tokens 103 us, 205 TFLOP/s.  Against it: 64 tokens per
-// CTA 13.9 and 105 us; 32 rows 13.6 us in the first; weights straight into registers,
+// CTA 13.9 and 105 us (against 11.1 and 103, all in plain launch order); 32 rows 13.6 us in the first; weights straight into registers,
 // two groups between barriers, 12.5 us in the first.
 #include "common.cuh"
+#include "launch.cuh"
 #include "mma.cuh"
 
 namespace edge0 {
@@ -78,9 +79,9 @@ __host__ __device__ inline FewLayout few_layout(int in, int tokens, int NT, int 
 }
 
 template <int NT, int RT>
-__global__ void __launch_bounds__(kThreadsQ) q4_few_kernel(const char* __restrict__ w, int out, int in,
-                                                           const __half* __restrict__ x, long long ldx, int B, int tokens,
-                                                           __half* __restrict__ y, long long ldy) {
+__global__ void __launch_bounds__(kThreadsQ) q4_few_kernel(const char* w, int out, int in,
+                                                           const __half* x, long long ldx, int B, int tokens,
+                                                           __half* y, long long ldy) {
     constexpr int kStages = few_stages(RT);
     extern __shared__ __align__(128) char smem[];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -119,6 +120,8 @@ __global__ void __launch_bounds__(kThreadsQ) q4_few_kernel(const char* __restric
             }
         }
     };
+    wait_predecessor();
+    launch_dependents();
     for (int s = 0; s < kStages - 1; ++s) issue();
 
     // x: lane t's 16 inputs of a group (2t, 2t + 1, 2t + 8, 2t + 9 of each 16) side by side.  A
@@ -280,9 +283,9 @@ constexpr int kManyStages = 4;          // steps under way: x of the tokens, the
 constexpr int kManyStage = kStep * (kManyTok * 128 + 4 * kQ4Unit);
 constexpr int kManySmem = kManyStages * kManyStage;
 
-__global__ void __launch_bounds__(256, 2) q4_many_kernel(const char* __restrict__ w, int out, int in,
-                                                      const __half* __restrict__ x, long long ldx, int B,
-                                                      __half* __restrict__ y, long long ldy) {
+__global__ void __launch_bounds__(256, 2) q4_many_kernel(const char* w, int out, int in,
+                                                      const __half* x, long long ldx, int B,
+                                                      __half* y, long long ldy) {
     constexpr int kTok = kManyTok, NT = kTok / 8, kTile = kTok * 128;     // kTile: bytes of one group of them
     constexpr int kStages = kManyStages, kStage = kManyStage, kJ = kStep / 2;
     extern __shared__ __align__(128) char smem[];
@@ -326,6 +329,8 @@ __global__ void __launch_bounds__(256, 2) q4_many_kernel(const char* __restrict_
         fence_mbar_init();
     }
     __syncthreads();
+    wait_predecessor();
+    launch_dependents();
     for (int s = 0; s < kStages - 1; ++s) fetch(s);
 
     float y4[NT][4];
@@ -501,9 +506,8 @@ extern "C" int edge0_q4_linear(const void* packed, int out, int in, const uint16
         const dim3 grid(n_t < most ? n_t : most, ceil_div(B, tokens));
         auto* f = NT == 1 ? (RT == 1 ? q4_few_kernel<1, 1> : q4_few_kernel<1, 2>)
                           : (RT == 1 ? q4_few_kernel<2, 1> : q4_few_kernel<2, 2>);
-        f<<<grid, kThreadsQ, smem, stream>>>(w, out, in, xh, ldx, B, tokens, yh, ldy);
-    } else {
-        q4_many_kernel<<<dim3(ceil_div(n_rt, 4), ceil_div(B, kManyTok)), 256, kManySmem, stream>>>(w, out, in, xh, ldx, B, yh, ldy);
+        return launch_early(f, grid, kThreadsQ, smem, stream, w, out, in, xh, ldx, B, tokens, yh, ldy);
     }
-    return cudaGetLastError() == cudaSuccess ? EDGE0_OK : EDGE0_ECUDA;
+    return launch_early(q4_many_kernel, dim3(ceil_div(n_rt, 4), ceil_div(B, kManyTok)), 256, kManySmem, stream, w, out, in, xh, ldx,
+                        B, yh, ldy);
 }

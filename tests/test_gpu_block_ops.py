@@ -742,6 +742,84 @@ def test_kept_workspaces_are_not_shared_across_streams_and_graphs():
     assert all(torch.equal(o, small) for o in outs[1])
 
 
+def test_calls_right_behind_their_producers_and_consumers():
+    """Every kernel may begin before its predecessor has ended: chains in which each call reads what
+    the one before wrote and overwrites what the one before read, eager and captured, with copies,
+    fills, events from another stream and kernels of other kinds between them."""
+    rng = np.random.default_rng(9)
+    H, G, D, page, B = 2, 4, 128, 64, 40
+    trip, _, _ = q4_case(2 * H * D, 512, seed=2)
+    packed = binding.pack_q4_rows(trip)
+    cache = binding.KVCache(B + 4, page, H, D, 4, device=DEV)
+    table, pre = i32(np.arange(B)[:, None]), i32([B, B + 1, B + 2])
+    old = torch.randn(192, H, D, device=DEV).half()
+    binding.kv_append(cache, old, old, pre[None].contiguous(), i32([0]), i32([0, 192]))
+    clean = cache.pages.clone()
+    xs = [dev(rng.standard_normal((B, 512)).astype(np.float16)) for _ in range(6)]
+    big = torch.zeros(1 << 22, device=DEV)
+    other = torch.cuda.Stream()
+
+    def buffers():
+        return dict(x=torch.empty(B, 512, device=DEV).half(), kv=torch.empty(B, 2 * H * D, device=DEV).half(),
+                    k=torch.empty(B, H, D, device=DEV).half(), v=torch.empty(B, H, D, device=DEV).half(),
+                    o=torch.zeros(B, G * H, D, device=DEV).half(), pos=torch.zeros(B, dtype=torch.int32, device=DEV),
+                    lens=torch.zeros(B, dtype=torch.int32, device=DEV),
+                    ws=torch.empty(binding.attn_workspace_bytes(cache, B, G * H), dtype=torch.uint8, device=DEV))
+
+    def chain(b, wait, n_prefix):
+        got = []
+        step = torch.cuda.current_stream().synchronize if wait else lambda: None
+        cache.pages.copy_(clean)
+        b["pos"].zero_()
+        b["lens"].fill_(1)
+        for x in xs:
+            b["x"].copy_(x)
+            step()
+            binding.q4_linear(packed, 2 * H * D, b["x"], y=b["kv"])
+            step()
+            k, v = b["kv"][:, :H * D].unflatten(1, (H, D)), b["kv"][:, H * D:].unflatten(1, (H, D))
+            binding.kv_append(cache, k, v, table, b["pos"])
+            step()
+            binding.kv_read(cache, table, b["pos"], k=b["k"], v=b["v"])
+            step()
+            q = torch.cat([b["k"], b["v"]] * 2, 1)
+            step()
+            binding.attn_decode(cache, q, table, b["lens"], pre, n_prefix, out=b["o"], workspace=b["ws"])
+            step()
+            ev = torch.cuda.Event()
+            ev.record()
+            with torch.cuda.stream(other):
+                other.wait_event(ev)
+                got.append(b["o"].clone())
+                big.add_(1)
+                back = torch.cuda.Event()
+                back.record()
+            torch.cuda.current_stream().wait_event(back)
+            binding.attn_decode(cache, b["o"], table, b["lens"], pre, n_prefix, out=b["o"].new_empty(b["o"].shape), workspace=b["ws"])
+            binding.q4_linear(packed, 2 * H * D, b["x"], y=b["kv"])       # overwritten while the last call may still run
+            got.append(b["kv"].clone())
+            b["pos"] += 1
+            b["lens"] += 1
+            step()
+        return got
+
+    for n_prefix in (0, 5, 190):
+        b = buffers()
+        want = [t.clone() for t in chain(b, True, n_prefix)]
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for a, w in zip(chain(b, False, n_prefix), want):
+                torch.cuda.synchronize()
+                assert torch.equal(a, w)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs = chain(b, False, n_prefix)
+        for _ in range(5):
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, w) for a, w in zip(outs, want))
+
+
 def test_binding_refuses_what_does_not_fit():
     E = binding.Edge0Error
     cache = binding.KVCache(4, 16, 2, 64, 4, device=DEV)
