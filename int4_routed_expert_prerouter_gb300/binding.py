@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import threading
 
 import numpy as np
 import torch
@@ -687,7 +688,7 @@ class KVCache:
         self.status = torch.zeros(1, dtype=torch.int32, device=pages.device)
         self.desc = KvCacheDesc(bits, n_kv_heads, head_dim, page_tokens, n_pages, _ptr(pages))
         self._index, self._desc, self._status = pages.get_device(), C.byref(self.desc), self.status.data_ptr()
-        self._ws_bytes, self._ws = {}, {}
+        self._ws_bytes, self._ws, self._ws_lock = {}, {}, threading.Lock()
 
     def error(self) -> int:
         """What the calls on this cache have recorded since the last error() (waits
@@ -776,18 +777,6 @@ def attn_workspace_bytes(cache: KVCache, B: int, n_q_heads: int) -> int:
     return n
 
 
-def _workspace(cache, nbytes, handle):
-    """Scratch of a call that was given none: one buffer per cache and stream, whose calls run one
-    after the other; a call that is being captured gets its own, from the graph's pool, because
-    graphs may replay beside other work of the stream they were captured on."""
-    if torch._C._cuda_isCurrentStreamCapturing():
-        return torch.empty(nbytes, dtype=_u8, device=cache.device)
-    ws = cache._ws.get(handle)
-    if ws is None or ws.numel() < nbytes:
-        ws = cache._ws[handle] = torch.empty(nbytes, dtype=_u8, device=cache.device)
-    return ws
-
-
 def attn_decode(cache: KVCache, q: torch.Tensor, table, lens, prefix=None, n_prefix=0, scale=None, out=None,
                 workspace=None, stream=None) -> torch.Tensor:
     """Attention of one query token per sequence, q [B, n_q_heads, head_dim] fp16, over
@@ -828,16 +817,29 @@ def _attn_decode(cache, q, table, lens, prefix, n_prefix, scale, out, workspace,
     if B == 0:
         return out
     handle = _raw_stream(index, stream)
-    if workspace is None:
-        nbytes = attn_workspace_bytes(cache, B, Hq)
-        workspace = _workspace(cache, nbytes or 16, handle)
-    else:
+
+    def call(ws, nbytes):
+        return _lib.edge0_attn_decode(cache._desc, q.data_ptr(), ldq, B, Hq, tb, W, ln, pf, n_prefix,
+                                      D ** -0.5 if scale is None else scale, out.data_ptr(), ldo, cache._status,
+                                      ws.data_ptr(), nbytes, handle)
+
+    if workspace is not None:
         if workspace.dtype is not _u8 or workspace.get_device() != index or not workspace.is_contiguous():
             raise _bad("attn_decode: workspace uint8, contiguous, beside the cache")
-        nbytes = workspace.numel()
-    code = _lib.edge0_attn_decode(cache._desc, q.data_ptr(), ldq, B, Hq, tb, W, ln, pf, n_prefix,
-                                  D ** -0.5 if scale is None else scale, out.data_ptr(), ldo, cache._status,
-                                  workspace.data_ptr(), nbytes, handle)
+        code = call(workspace, workspace.numel())
+    else:
+        nbytes = attn_workspace_bytes(cache, B, Hq)
+        if torch._C._cuda_isCurrentStreamCapturing():
+            # a graph may replay beside other work of the stream it was captured on: from its pool
+            code = call(torch.empty(nbytes or 16, dtype=_u8, device=cache.device), nbytes)
+        else:
+            # one per cache and stream, whose calls run one after the other; the lock keeps the
+            # launches of two threads' calls from mixing
+            with cache._ws_lock:
+                ws = cache._ws.get(handle)
+                if ws is None or ws.numel() < nbytes:
+                    ws = cache._ws[handle] = torch.empty(nbytes or 16, dtype=_u8, device=cache.device)
+                code = call(ws, nbytes)
     if code:
         raise Edge0Error(code, "edge0_attn_decode")
     return out

@@ -3,12 +3,12 @@
 // wait_predecessor() returns when the predecessor has ended and what it wrote can be read.
 // Every kernel launched so waits before it reads or writes global memory, and says
 // launch_dependents() only then: whoever has begun knows that all that came before its
-// predecessor has ended.  (One does not wait, attn_kernel behind the prefix's kernel, which is launched
-// in plain order and so has itself begun behind all else.)  (A kernel of another kind before or after it sees plain stream order.)
-// (No __restrict__ on what such a kernel reads: the compiler may move a load that it takes for
-// constant above the wait.)
-// What it saves is the launch's latency: an append and a read of 64 rows 6.6 -> 5.7 us, a projection
-// 65,537 x 2048 of one token 17.4 -> 16.6.
+// predecessor has ended.  (One waits at its end only: attn_kernel behind the prefix's kernel, which
+// has itself begun behind all that came before.)  Kernels of other kinds before and after see
+// plain stream order.  Nothing that such a kernel reads is __restrict__: the compiler may move a
+// load that it takes for constant above the wait.
+// What it saves is the launch's latency: an append and a read of 64 rows 6.6 -> 5.7 us, a
+// projection 65,537 x 2048 of one token 17.4 -> 16.5.
 #pragma once
 #include "internal.cuh"
 

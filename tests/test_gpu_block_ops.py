@@ -1,6 +1,7 @@
 """Projection, KV-cache and attention calls on the GPU against their plain 64-bit
 forms (block_ref), at the sizes, masks and layouts where they can go wrong."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -740,6 +741,33 @@ def test_kept_workspaces_are_not_shared_across_streams_and_graphs():
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs[0] + outs[2])
     assert all(torch.equal(o, small) for o in outs[1])
+
+
+def test_calls_of_several_threads_on_one_stream():
+    # without workspaces of their own: the threads' launches share a stream and what the cache keeps for it
+    cases = [run_attention(4, 128, 2, 4, 64, [700, 0, 33, 1200], 500), run_attention(4, 128, 2, 4, 64, [40] * 33, 30, seed=1)]
+    shared = cases[0][0][0]
+    (_, q1, t1, l1, p1, P1, s1), want1 = cases[0]
+    q2 = q1[:2].contiguous() * 0.5
+    want2 = binding.attn_decode(shared, q2, t1[:2].contiguous(), l1[:2].contiguous(), p1, P1, s1)
+    torch.cuda.synchronize()
+    outs = [[] for _ in range(6)]
+
+    def work(i):
+        for _ in range(60):
+            if i % 2:
+                outs[i].append(binding.attn_decode(shared, q2, t1[:2].contiguous(), l1[:2].contiguous(), p1, P1, s1))
+            else:
+                outs[i].append(binding.attn_decode(shared, q1, t1, l1, p1, P1, s1))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i, got in enumerate(outs):
+        assert len(got) == 60 and all(torch.equal(o, want2 if i % 2 else want1) for o in got)
 
 
 def test_calls_right_behind_their_producers_and_consumers():
