@@ -482,7 +482,8 @@ int edge0_kv_read(const edge0_kv_cache* cache, const int32_t* table, int B, int 
  * outside [0, n_pages) (page 0 is read in their place) are recorded as EDGE0_EINVAL in
  * *status as above.  workspace: scratch of edge0_attn_workspace_bytes (16-byte aligned,
  * not cleared beforehand, nothing kept in it); calls that may overlap on the GPU, or whose
- * launches threads may mix on one stream, need one each.  The result does not depend on the timing of the run. */
+ * launches threads may mix on one stream, need one each.  The result does not depend
+ * on the timing of the run. */
 size_t edge0_attn_workspace_bytes(const edge0_kv_cache* cache, int B, int n_q_heads);
 int edge0_attn_decode(const edge0_kv_cache* cache, const uint16_t* q, long long ldq, int B, int n_q_heads,
                       const int32_t* table, int W, const int32_t* lens, const int32_t* prefix,
