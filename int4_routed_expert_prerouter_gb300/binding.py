@@ -632,7 +632,7 @@ def _ints(t, index, n, what):
 
 def q4_linear(packed: torch.Tensor, out_features: int, x: torch.Tensor, y=None, stream=None) -> torch.Tensor:
     """y [B, out_features] = W x for x [B, in] fp16 and W packed by pack_q4_rows (one
-    matrix: E = 1).  x and y may be slices of wider rows."""
+    matrix: E = 1).  x and y may be slices of wider rows; y's rows may not overlap (no expanded y)."""
     index = x.get_device()
     guard = _guard(index, stream)
     if guard is not None:
@@ -655,7 +655,7 @@ def _q4_linear(packed, out_features, x, y, index, stream):
     else:
         if y.shape != (B, out_features) or y.get_device() != index:
             raise _bad("q4_linear: y [B, out_features] beside x")
-        ldy = max(_row_stride(y, "q4_linear: y"), out_features)
+        ldy = _row_stride(y, "q4_linear: y")        # (the call refuses rows that overlap: ldy < out_features)
     if B:
         code = (_lib or lib()).edge0_q4_linear(packed.data_ptr(), out_features, n_in, x.data_ptr(), ldx, B, y.data_ptr(), ldy,
                                                _raw_stream(index, stream))
