@@ -406,7 +406,7 @@ void edge0_pool_destroy(edge0_pool* pool);
  * The pages' decoder block has, besides the MoE part, int4 projections (attention and
  * linear-attention projections are int4 and LoRA targets, S3.3) and a KV cache whose
  * growth they name.  These calls are its GB300 form for up to EDGE0_MAX_BATCHED
- * sequences.  They synchronise nothing, keep no state, copy nothing from the host and
+ * sequences.  They synchronise nothing, keep no state (but the limit of their waits), copy nothing from the host and
  * may be captured into a CUDA graph (lengths, positions and page tables are read on
  * the device at each replay).
  *
@@ -419,6 +419,12 @@ enum {
     EDGE0_MAX_LINEAR = 1 << 28,     /* outputs or inputs of a projection */
     EDGE0_MAX_PREFIX = 1 << 30      /* tokens of a shared prefix */
 };
+
+/* Limit, in ns, of each wait for a copy inside the projection and attention kernels launched (or
+ * captured) from now on, by any thread of the process; 2 s unless set.  0: every wait counts as run out
+ * at once.  A wait that runs out is given up: the attention calls record EDGE0_ETIMEOUT in
+ * *status, the projection writes NaN to the outputs that it lacks weights of. */
+void edge0_block_set_wait_limit(unsigned long long wait_ns);
 
 /* Dense int4 projection [S2, S3.1: the int4 affine group-64 format]: y[b] = W x[b],
  * W [out, in] packed by edge0_pack_q4_rows with E = 1; add the projection's LoRA with

@@ -133,6 +133,8 @@ def _declare(L):
     L.edge0_decode_step.argtypes = [C.POINTER(LayerDesc), C.c_int, P, C.POINTER(RouteState),
                                     C.c_int, C.c_int, P]
     L.edge0_q4_linear.argtypes = [P, C.c_int, C.c_int, P, C.c_longlong, C.c_int, P, C.c_longlong, P]
+    L.edge0_block_set_wait_limit.argtypes = [C.c_ulonglong]
+    L.edge0_block_set_wait_limit.restype = None
     L.edge0_kv_page_bytes.argtypes = [C.c_int] * 4
     L.edge0_kv_page_bytes.restype = C.c_size_t
     L.edge0_kv_append.argtypes = [C.POINTER(KvCacheDesc), P, C.c_longlong, P, C.c_longlong, C.c_int, P, C.c_int,
@@ -163,7 +165,8 @@ EXPORTED = ["edge0_status_string", "edge0_q4_gate_up_packed_bytes", "edge0_pack_
             "edge0_pool_plan", "edge0_pool_host_prefetch", "edge0_pool_host_copy", "edge0_pool_device_init",
             "edge0_pool_prefetch_async", "edge0_pool_wait", "edge0_pool_inject", "edge0_pool_stats_ex", "edge0_pool_stats",
             "edge0_pool_resident", "edge0_pool_destroy", "edge0_q4_linear", "edge0_kv_page_bytes",
-            "edge0_kv_append", "edge0_kv_read", "edge0_attn_workspace_bytes", "edge0_attn_decode"]
+            "edge0_kv_append", "edge0_kv_read", "edge0_attn_workspace_bytes", "edge0_attn_decode",
+            "edge0_block_set_wait_limit"]
 
 
 def status_string(code: int) -> str:
@@ -628,6 +631,12 @@ def _ints(t, index, n, what):
     if t.dtype is not _i32_t or t.get_device() != index or t.numel() != n or not t.is_contiguous():
         raise _bad(f"{what}: {n} int32, contiguous, on cuda:{index}")
     return t.data_ptr()
+
+
+def set_wait_limit(wait_ns: int = 2_000_000_000):
+    """Limit of each wait inside the projection and attention kernels launched from now on
+    (edge0_block_set_wait_limit); 0: every wait counts as run out at once."""
+    lib().edge0_block_set_wait_limit(int(wait_ns))
 
 
 def q4_linear(packed: torch.Tensor, out_features: int, x: torch.Tensor, y=None, stream=None) -> torch.Tensor:

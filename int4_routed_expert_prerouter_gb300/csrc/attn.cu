@@ -44,6 +44,7 @@
 // rescale nothing.
 #include "attn.cuh"
 #include "mma.cuh"
+#include "wait.cuh"
 
 namespace edge0 {
 namespace {
@@ -72,6 +73,7 @@ struct AttnP {
     __half* out;             // set: segments that one CTA has whole are written here
     long long ldo;
     int* status;
+    unsigned long long wait_ns;   // limit of a wait for a copy
     bool after_prefix;       // begins while the prefix's kernel runs, which has waited for what came before
 };
 
@@ -106,20 +108,6 @@ __device__ __forceinline__ void copy_strip(void* dst, const void* src, uint32_t 
                      smem_u32(dst)),
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
-}
-// Waits for a stage's copies, at most kDefaultWaitNs; by a whole warp, which agrees on
-// the answer.
-__device__ __forceinline__ bool wait_copy(uint64_t* bar, uint32_t parity) {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!ok) {
-        unsigned long long t0, now;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-        do {
-            ok = mbar_try_wait(bar, parity);
-            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-        } while (!ok && now - t0 < kDefaultWaitNs);
-    }
-    return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
@@ -289,7 +277,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
     char* my_ring = ring + wid * X::STAGES * X::US * X::STRIP;
     uint64_t* my_bar = bars + wid * X::STAGES;
     int it = 0;              // units this warp has taken so far: stage and parity
-    bool dead = false;       // a copy did not arrive in time
+    bool dead = p.wait_ns == 0;   // a copy did not arrive in time
+    if (dead && tid == 0 && p.status) atomicExch(p.status, EDGE0_ETIMEOUT);
     // the lane's row and piece in the 8x8 matrix loads
     const int lr = (lane & 7) + 8 * ((lane >> 3) & 1);
     const uint32_t row_off = lr * X::R;
@@ -435,7 +424,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
         for (int u = dead ? u1 : u0 + wid; u < u1; u += kWarps, ++it) {
             issue();
             const int stage = it % X::STAGES;
-            if (!wait_copy(&my_bar[stage], (it / X::STAGES) & 1)) {   // give up: nothing more is issued or read
+            if (!wait_copy(&my_bar[stage], (it / X::STAGES) & 1, p.wait_ns)) {
+                drain_copies_call(my_bar, it, issued, X::STAGES);     // give up: nothing more is issued or read
                 if (lane == 0 && p.status) atomicExch(p.status, EDGE0_ETIMEOUT);
                 dead = true;
                 break;
@@ -1063,6 +1053,7 @@ extern "C" int edge0_attn_decode(const edge0_kv_cache* cache, const uint16_t* q,
     p.k = kTwo24 * scale * 1.4426950408889634f;
     p.ldo = ldo;
     p.status = status;
+    p.wait_ns = block_wait_limit();
     for (int w = 1; w >= 0; --w) {
         if (w && !n_prefix) continue;
         if (part[w].NT == 0) {

@@ -26,6 +26,7 @@
 #include "common.cuh"
 #include "launch.cuh"
 #include "mma.cuh"
+#include "wait.cuh"
 
 namespace edge0 {
 namespace {
@@ -45,20 +46,6 @@ __device__ __forceinline__ void copy_bulk(void* dst, const void* src, uint32_t b
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
-// Waits for a copy, at most kDefaultWaitNs; the whole warp agrees on the answer.
-__device__ __forceinline__ bool wait_copy(uint64_t* bar, uint32_t parity) {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!ok) {
-        unsigned long long t0, now;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-        do {
-            ok = mbar_try_wait(bar, parity);
-            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-        } while (!ok && now - t0 < kDefaultWaitNs);
-    }
-    return __all_sync(0xffffffffu, ok);
-}
-
 // Shared memory of q4_few_kernel: rings, x in fragment order, group sums, partial sums.
 // RT: row tiles taken together (2 where there are enough of them: x's fragments, the
 // joins and the barrier then serve both).
@@ -81,7 +68,7 @@ __host__ __device__ inline FewLayout few_layout(int in, int tokens, int NT, int 
 template <int NT, int RT>
 __global__ void __launch_bounds__(kThreadsQ) q4_few_kernel(const char* w, int out, int in,
                                                            const __half* x, long long ldx, int B, int tokens,
-                                                           __half* y, long long ldy) {
+                                                           __half* y, long long ldy, unsigned long long wait_ns) {
     constexpr int kStages = few_stages(RT);
     extern __shared__ __align__(128) char smem[];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -98,7 +85,7 @@ __global__ void __launch_bounds__(kThreadsQ) q4_few_kernel(const char* w, int ou
     __syncwarp();
     // this warp's groups of every row tile, in chunks
     const int c0 = n_g * wid / kWarps, c1 = n_g * (wid + 1) / kWarps;
-    const int chunks = (c1 - c0 + kChunk - 1) / kChunk;
+    const int chunks = wait_ns ? (c1 - c0 + kChunk - 1) / kChunk : 0;      // (limit 0: given up from the start)
     const int n_t = ceil_div(n_rt, RT);                      // steps over the row tiles
     int next_t = blockIdx.x, next_chunk = 0, issued = 0;
     auto issue = [&]() {
@@ -174,7 +161,7 @@ __global__ void __launch_bounds__(kThreadsQ) q4_few_kernel(const char* w, int ou
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) xrow[nt] = smem + L.x + min(nt * 8 + g, nb - 1) * L.ld + t * 32;
     int it = 0, buf = 0;
-    bool dead = false;
+    bool dead = wait_ns == 0;
     for (int rt = blockIdx.x; rt < n_t; rt += gridDim.x, buf ^= 1) {
         float y4[RT][NT][4];
 #pragma unroll
@@ -186,7 +173,10 @@ __global__ void __launch_bounds__(kThreadsQ) q4_few_kernel(const char* w, int ou
         for (int ch = 0; ch < chunks && !dead; ++ch, ++it) {
             issue();
             const int st = it % kStages;
-            if (!wait_copy(&bar[st], (uint32_t)(it / kStages) & 1)) {
+            if (!wait_copy(&bar[st], (uint32_t)(it / kStages) & 1, wait_ns)) {
+                // (inline or called as leaves the other ways their registers: each 2 % faster in its place)
+                if (RT == 2) drain_copies(bar, it, issued, kStages);
+                else drain_copies_call(bar, it, issued, kStages);
                 dead = true;                     // a copy that never came: NaN marks the rows from here on
                 break;
             }
@@ -285,7 +275,7 @@ constexpr int kManySmem = kManyStages * kManyStage;
 
 __global__ void __launch_bounds__(256, 2) q4_many_kernel(const char* w, int out, int in,
                                                       const __half* x, long long ldx, int B,
-                                                      __half* y, long long ldy) {
+                                                      __half* y, long long ldy, unsigned long long wait_ns) {
     constexpr int kTok = kManyTok, NT = kTok / 8, kTile = kTok * 128;     // kTile: bytes of one group of them
     constexpr int kStages = kManyStages, kStage = kManyStage, kJ = kStep / 2;
     extern __shared__ __align__(128) char smem[];
@@ -305,10 +295,11 @@ __global__ void __launch_bounds__(256, 2) q4_many_kernel(const char* w, int out,
     const uint32_t pdst = smem_u32(ring) + pb * 128 + ((pc ^ (pb & 7)) << 4);
     const int tiles = min(4, n_rt - (int)blockIdx.x * 4);
     const char* wsrc = w + (long long)blockIdx.x * 4 * n_g * kQ4Unit;
+    int good = wait_ns ? steps : 0;                           // steps whose weights this warp has seen arrive
     auto fetch = [&](int step) {
         if (step < steps) {
             const int at = (step % kStages) * kStage;
-            if (tid == 0) {
+            if (tid == 0 && step < good + kStages - 1) {
                 const uint32_t bytes = min(kStep, n_g - kStep * step) * kQ4Unit;
                 uint64_t* bar = &full[step % kStages];
                 mbar_arrive_expect_tx(bar, tiles * bytes);
@@ -398,11 +389,10 @@ __global__ void __launch_bounds__(256, 2) q4_many_kernel(const char* w, int out,
             y4[i][3] = fmaf(s1, acc[i][3], y4[i][3]);
         }
     };
-    bool dead = false;
     for (int step = 0; step < steps; ++step) {
         const char* stage = ring + (step % kStages) * kStage;
         cp_wait<kStages - 2>();
-        if (!dead && !wait_copy(&full[step % kStages], (uint32_t)(step / kStages) & 1)) dead = true;
+        if (step < good && !wait_copy(&full[step % kStages], (uint32_t)(step / kStages) & 1, wait_ns)) good = step;
         __syncthreads();                                      // the stage of the step before is free, too
         fetch(step + kStages - 1);
         if (step > 0)
@@ -423,11 +413,13 @@ __global__ void __launch_bounds__(256, 2) q4_many_kernel(const char* w, int out,
 #pragma unroll
     for (int j = 0; j < kJ; ++j)
         if (2 * j + half < have) add_bias(steps - 1, j);
-    if (dead)                                                 // a copy that never came: NaN marks the rows
+    if (good < steps) {                                       // a copy that never came: NaN marks the rows
+        if (wid == 0) drain_copies(full, good, min(good + kStages - 1, steps), kStages);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) y4[nt][i] = __int_as_float(0x7fffffff);
+    }
     // the odd groups' sums through shared memory
     cp_wait<0>();
     __syncthreads();
@@ -454,6 +446,8 @@ __global__ void __launch_bounds__(256, 2) q4_many_kernel(const char* w, int out,
 
 constexpr int kFewSmem = 220 * 1024;
 
+unsigned long long wait_limit = kDefaultWaitNs;
+
 // what a device needs before its first launch
 int setup(int dev, int* sms) {
     constexpr int kDevices = 64;
@@ -476,9 +470,16 @@ int setup(int dev, int* sms) {
 }
 
 }  // namespace
+
+unsigned long long block_wait_limit() { return __atomic_load_n(&wait_limit, __ATOMIC_RELAXED); }
+
 }  // namespace edge0
 
 using namespace edge0;
+
+extern "C" void edge0_block_set_wait_limit(unsigned long long wait_ns) {
+    __atomic_store_n(&wait_limit, wait_ns, __ATOMIC_RELAXED);
+}
 
 extern "C" int edge0_q4_linear(const void* packed, int out, int in, const uint16_t* x, long long ldx, int B,
                                uint16_t* y, long long ldy, cudaStream_t stream) {
@@ -506,8 +507,9 @@ extern "C" int edge0_q4_linear(const void* packed, int out, int in, const uint16
         const dim3 grid(n_t < most ? n_t : most, ceil_div(B, tokens));
         auto* f = NT == 1 ? (RT == 1 ? q4_few_kernel<1, 1> : q4_few_kernel<1, 2>)
                           : (RT == 1 ? q4_few_kernel<2, 1> : q4_few_kernel<2, 2>);
-        return launch_early(f, grid, kThreadsQ, smem, stream, w, out, in, xh, ldx, B, tokens, yh, ldy);
+        return launch_early(f, grid, kThreadsQ, smem, stream, w, out, in, xh, ldx, B, tokens, yh, ldy,
+                            block_wait_limit());
     }
     return launch_early(q4_many_kernel, dim3(ceil_div(n_rt, 4), ceil_div(B, kManyTok)), 256, kManySmem, stream, w, out, in, xh, ldx,
-                        B, yh, ldy);
+                        B, yh, ldy, block_wait_limit());
 }
