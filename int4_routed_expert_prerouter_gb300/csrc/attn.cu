@@ -1058,7 +1058,7 @@ extern "C" int edge0_attn_decode(const edge0_kv_cache* cache, const uint16_t* q,
         if (w && !n_prefix) continue;
         if (part[w].NT == 0) {
             const PrefixP x{p.c, p.q, ldq, p.G, p.H, B * p.G, part[w].RB, part[w].splits, part[w].tiles, prefix, n_prefix,
-                            scale * 1.4426950408889634f, (float*)(ws + part[w].o), (float2*)(ws + part[w].ml), status};
+                            scale * 1.4426950408889634f, (float*)(ws + part[w].o), (float2*)(ws + part[w].ml), status, p.wait_ns};
             rc = prefix_launch(x, cache->bits, D, stream);
             if (rc) return rc;
             continue;

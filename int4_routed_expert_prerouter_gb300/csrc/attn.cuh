@@ -26,6 +26,7 @@ struct PrefixP {
     float* part_o;                   // [(h RB + rb) splits + share][kPrefixRows][D]
     float2* part_ml;                 // [..][kPrefixRows] (maximum in exponent units, sum)
     int* status;
+    unsigned long long wait_ns;      // limit of a wait
 };
 
 // shares of the prefix that fill the card for `segs` (K/V head, row block) pairs

@@ -30,6 +30,7 @@
 // and two CTAs are what shared memory, tensor memory (2 x 256 columns) and registers hold.
 #include "attn.cuh"
 #include "tc05.cuh"
+#include "wait.cuh"
 
 namespace edge0 {
 namespace {
@@ -124,17 +125,20 @@ __device__ __forceinline__ uint64_t desc(uint32_t lo, uint32_t stride) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"((stride >> 4) | (1u << 14)));
     return d;
 }
-// whether any thread of the two warps that share 32 rows wants it
-__device__ __forceinline__ bool any_of_rows(int quad, bool want) {
+// whether any of the threads that meet at a barrier wants it
+template <int THREADS>
+__device__ __forceinline__ bool any_of(int barrier, bool want) {
     uint32_t r;
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 64, p;\n"
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n"
         " selp.u32 %0, 1, 0, q;\n}\n"
         : "=r"(r)
-        : "r"((uint32_t)want), "r"(4 + quad)
+        : "r"((uint32_t)want), "r"(barrier), "n"(THREADS)
         : "memory");
     return r != 0;
 }
+// ... the two warps that share 32 rows
+__device__ __forceinline__ bool any_of_rows(int quad, bool want) { return any_of<64>(4 + quad, want); }
 
 // codes of 8 dims less z as fp16 (of K times 2^-10); 4 bits: one word, dims in the order
 // 0 4 1 5 2 6 3 7; 8 bits: two words, in order.  0x6400 is 1024: a code below it adds itself,
@@ -166,15 +170,15 @@ __device__ __forceinline__ uint32_t split(float v) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Waits for a phase of a barrier; gives up after kDefaultWaitNs or when another thread did.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead) {
+// Waits for a phase of a barrier; gives up after `limit` ns or when another thread did.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead, unsigned long long limit) {
     if (mbar_try_wait(bar, parity)) return true;
     unsigned long long t0, now;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
     for (;;) {
         if (mbar_try_wait(bar, parity)) return true;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-        if (*dead || now - t0 > kDefaultWaitNs) {
+        if (*dead || now - t0 > limit) {
             *dead = 1;
             return false;
         }
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
     constexpr int GR = X::GR;
     constexpr float kZ = BITS == 4 ? 8.f : 128.f;
     extern __shared__ __align__(128) char smem[];
-    __shared__ uint64_t full[2], freed[2], s_ready;
+    __shared__ uint64_t full[2], freed[2], s_ready, drained;
     __shared__ uint32_t taddr_s;
     __shared__ int dead;
     __shared__ float part_max[2][kRowsQ];
@@ -209,8 +213,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             mbar_init(&freed[i], 1);
         }
         mbar_init(&s_ready, 1);
+        mbar_init(&drained, 1);
         fence_mbar_init();
-        dead = 0;
+        dead = p.wait_ns == 0;                                 // (limit 0: given up from the start)
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -365,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             __syncwarp();
         }
         for (int i = 0; i < n; ++i) {
-            if (i >= 2 && !__all_sync(0xffffffffu, wait_bar(&freed[i & 1], ((i >> 1) - 1) & 1, &dead))) break;
+            if (i >= 2 && !__all_sync(0xffffffffu, wait_bar(&freed[i & 1], ((i >> 1) - 1) & 1, &dead, p.wait_ns))) break;
             put(i);
             if (i + 1 < n) load();
         }
@@ -389,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
         auto issue_scores = [&](int i, uint32_t lead) {        // warp 0: the products of tile i
             const uint32_t k0 = st0 + (i & 1) * X::kStage;
             const uint32_t sK = desc_lo(k0, tc::kLbo), sR = desc_lo(k0 + 2 * X::kOp, tc::kLbo);
-            if (!__all_sync(0xffffffffu, wait_bar(&full[i & 1], (i >> 1) & 1, &dead))) return;
+            if (!__all_sync(0xffffffffu, wait_bar(&full[i & 1], (i >> 1) & 1, &dead, p.wait_ns))) return;
             tc::fence_after_sync();
 #pragma unroll
             for (int gr = 0; gr < GR; ++gr) {
@@ -403,16 +408,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             commit(&s_ready, lead);
         };
         if (wid == 0) issue_scores(0, elect());
-        bool ok = true;
         for (int i = 0; i < n; ++i) {
             const char* stage = stages + (i & 1) * X::kStage;
             const float* tab_k = reinterpret_cast<const float*>(stage + 2 * X::kOp + X::kOffs);
             const float* tab_v = tab_k + GR * kTile;
             const float* mk = tab_k + (hf * 16 + t) * 2 * GR;      // this lane's pairs of tokens, 4 apart
             const float* mv = tab_v + (hf * 16 + t) * 4 * GR;
-            // (after a wait that gave up the rest runs through without waiting: the warps
-            // meet at barriers in every step)
-            ok = wait_bar(&full[i & 1], (i >> 1) & 1, &dead) && wait_bar(&s_ready, i & 1, &dead);
+            // (after a wait that gave up the warps go on to where all meet, and leave together)
+            (void)(wait_bar(&full[i & 1], (i >> 1) & 1, &dead, p.wait_ns) && wait_bar(&s_ready, i & 1, &dead, p.wait_ns));
             __syncwarp();
             tc::fence_after_sync();
             float most_s = 0.f, least_s = INFINITY;            // (0: no token)
@@ -590,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             }
             tmem_wait_st();
             tc::fence_before_sync();
-            named_bar_sync(3, kSoftmax);
+            if (any_of<kSoftmax>(3, *(volatile int*)&dead)) break;
             if (wid == 0) {
                 const uint32_t lead = elect();
                 const uint32_t sV = desc_lo(st0 + (i & 1) * X::kStage + X::kOp, 128);
@@ -607,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             }
             __syncwarp();
         }
-        ok = wait_bar(&freed[(n - 1) & 1], ((n - 1) >> 1) & 1, &dead) && ok;
+        const bool ok = !*(volatile int*)&dead && wait_bar(&freed[(n - 1) & 1], ((n - 1) >> 1) & 1, &dead, p.wait_ns);
         // a row's sums: its 4 lanes, then both halves of the tokens (all operands are done with by now)
         float* sums = reinterpret_cast<float*>(smem);          // [hf][1 + GR][row]
 #pragma unroll
@@ -623,8 +626,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                 if (t == 0) sums[(hf * (1 + GR) + 1 + gr) * kRowsQ + row] = beta[r][gr];
             }
         }
-        named_bar_sync(2, kSoftmax);
-        if (__all_sync(0xffffffffu, ok)) {
+        if (!any_of<kSoftmax>(2, !ok)) {
             tc::fence_after_sync();
             const long long slot = ((long long)h * p.RB + rb) * p.splits + blockIdx.x;
             // rows of o in shared memory, 16 bytes apart so that eight of them do not share banks, and
@@ -679,8 +681,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (tid == 0 && dead && p.status) atomicExch(p.status, EDGE0_ETIMEOUT);
-    if (wid == 0) tc::tmem_dealloc(tm, X::kCols);
+    if (wid == 0) {
+        if (dead) {              // matrix steps under way still read shared memory and write the accumulators
+            commit(&drained, elect());
+            wait_copy(&drained, 0, kDefaultWaitNs);
+            if (lane == 0 && p.status) atomicExch(p.status, EDGE0_ETIMEOUT);
+        }
+        tc::tmem_dealloc(tm, X::kCols);
+    }
 }
 
 template <int BITS, int D>

@@ -65,3 +65,17 @@ def test_own_contexts_without_waiting(no_waiting, bits, D, G):
         no_waiting(lambda: binding.attn_decode(cache, q, table, lens))
         assert cache.error() == binding.EDGE0_ETIMEOUT
         assert torch.equal(binding.attn_decode(cache, q, table, lens), clean) and cache.error() == binding.EDGE0_OK
+
+
+@pytest.mark.parametrize("bits,D,B,G", [(4, 128, 5, 4), (8, 128, 70, 4), (4, 256, 9, 8), (8, 256, 20, 16), (4, 64, 33, 4), (8, 64, 17, 16)])
+@pytest.mark.parametrize("P", [30, 700, 2051])
+def test_prefix_on_the_tensor_cores_without_waiting(no_waiting, bits, D, B, G, P):
+    H, page = 2, 64
+    cache = filled(bits, D, H, page, 40, D + G)
+    table, lens, pre = i32(np.zeros((B, 1))), i32(np.zeros(B)), i32(np.random.default_rng(1).permutation(40))
+    q = torch.randn(B, H * G, D, device=DEV).half()
+    clean = binding.attn_decode(cache, q, table, lens, pre, P)
+    for _ in range(3):
+        no_waiting(lambda: binding.attn_decode(cache, q, table, lens, pre, P))
+        assert cache.error() == binding.EDGE0_ETIMEOUT
+        assert torch.equal(binding.attn_decode(cache, q, table, lens, pre, P), clean) and cache.error() == binding.EDGE0_OK
