@@ -422,8 +422,8 @@ enum {
 
 /* Limit, in ns, of each wait for a copy inside the projection and attention kernels launched (or
  * captured) from now on, by any thread of the process; 2 s unless set.  0: every wait counts as run out
- * at once.  A wait that runs out is given up: the attention calls record EDGE0_ETIMEOUT in
- * *status, the projection writes NaN to the outputs that it lacks weights of. */
+ * at once.  A wait that runs out is given up: rows that lack weights or tokens for it get NaN, and
+ * the attention calls record EDGE0_ETIMEOUT in *status. */
 void edge0_block_set_wait_limit(unsigned long long wait_ns);
 
 /* Dense int4 projection [S2, S3.1: the int4 affine group-64 format]: y[b] = W x[b],
@@ -486,7 +486,7 @@ int edge0_kv_read(const edge0_kv_cache* cache, const int32_t* table, int B, int 
  * A sequence without any token gets zeros; lens[b] < 0 marks a padding row, whose
  * output is left as it was.  lens[b] above W * page_tokens (cut there) and pages
  * outside [0, n_pages) (page 0 is read in their place) are recorded as EDGE0_EINVAL in
- * *status as above.  workspace: scratch of edge0_attn_workspace_bytes (16-byte aligned,
+ * *status as above, a wait that ran out as EDGE0_ETIMEOUT (its rows get NaN).  workspace: scratch of edge0_attn_workspace_bytes (16-byte aligned,
  * not cleared beforehand, nothing kept in it); calls that may overlap on the GPU, or whose
  * launches threads may mix on one stream, need one each.  The result does not depend
  * on the timing of the run. */

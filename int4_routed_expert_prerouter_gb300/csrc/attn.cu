@@ -663,8 +663,10 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                 l[nt][i] = sum_over_rows(l[nt][i]);
 #pragma unroll
                 for (int gr = 0; gr < GR; ++gr) beta[nt][gr][i] = sum_over_rows(beta[nt][gr][i]);
+                // (a warp that gave up lacks tokens: NaN marks its rows)
                 if (g == 0) sml[(wid * NT + nt) * 8 + 2 * t + i] =
-                                make_float2(any ? __fmul_rn(m[nt][i], p.k) : -INFINITY, l[nt][i]);
+                                dead ? make_float2(0.f, __int_as_float(0x7fffffff))
+                                     : make_float2(any ? __fmul_rn(m[nt][i], p.k) : -INFINITY, l[nt][i]);
             }
         __syncthreads();
         const bool whole = u0 == 0 && u1 == units;

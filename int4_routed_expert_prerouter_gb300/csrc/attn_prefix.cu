@@ -626,9 +626,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                 if (t == 0) sums[(hf * (1 + GR) + 1 + gr) * kRowsQ + row] = beta[r][gr];
             }
         }
-        if (!any_of<kSoftmax>(2, !ok)) {
+        const long long slot = ((long long)h * p.RB + rb) * p.splits + blockIdx.x;
+        if (any_of<kSoftmax>(2, !ok)) {
+            // tokens are lacking: a sum of NaN marks the rows, whatever was in the slot before
+            if (tid < kRowsQ && r0 + tid < p.rows)
+                p.part_ml[slot * kRowsQ + tid] = make_float2(0.f, __int_as_float(0x7fffffff));
+        } else {
             tc::fence_after_sync();
-            const long long slot = ((long long)h * p.RB + rb) * p.splits + blockIdx.x;
             // rows of o in shared memory, 16 bytes apart so that eight of them do not share banks, and
             // from there in one copy each
             constexpr int kLd = D + 4;

@@ -79,3 +79,26 @@ def test_prefix_on_the_tensor_cores_without_waiting(no_waiting, bits, D, B, G, P
         no_waiting(lambda: binding.attn_decode(cache, q, table, lens, pre, P))
         assert cache.error() == binding.EDGE0_ETIMEOUT
         assert torch.equal(binding.attn_decode(cache, q, table, lens, pre, P), clean) and cache.error() == binding.EDGE0_OK
+
+
+@pytest.mark.parametrize("bits,D,B,G,P", [(4, 128, 6, 4, 0), (8, 256, 3, 2, 0), (8, 64, 6, 16, 0), (4, 128, 2, 4, 300), (8, 64, 3, 8, 200),
+                                          (4, 128, 33, 4, 700), (8, 64, 40, 8, 1500), (4, 256, 20, 8, 300)])
+def test_rows_that_lack_tokens_are_nan(no_waiting, bits, D, B, G, P):
+    """Not what an earlier call left in the workspace, nor a softmax over fewer tokens; rows without
+    any token and padding rows as ever."""
+    H, page = 2, 64
+    cache = filled(bits, D, H, page, 40, D + G)
+    rng = np.random.default_rng(2)
+    table, pre = i32(rng.integers(0, 40, (B, 12))), i32(rng.permutation(40))
+    n = rng.integers(1, 12 * page, B)
+    n[0], n[1] = 0, -1
+    lens = i32(n)
+    q, other = torch.randn(2, B, H * G, D, device=DEV).half()
+    ws = torch.empty(binding.attn_workspace_bytes(cache, B, H * G), dtype=torch.uint8, device=DEV)
+    clean = binding.attn_decode(cache, q, table, lens, pre, P, workspace=ws, out=torch.full_like(q, 5.0))
+    for _ in range(2):
+        got = no_waiting(lambda: binding.attn_decode(cache, other, table, lens, pre, P, workspace=ws, out=torch.full_like(q, 5.0)))
+        assert torch.isnan(got[2:]).all() and (got[1] == 5).all()
+        assert torch.isnan(got[0]).all() if P else not got[0].any()
+        assert cache.error() == binding.EDGE0_ETIMEOUT
+        assert torch.equal(binding.attn_decode(cache, q, table, lens, pre, P, workspace=ws, out=torch.full_like(q, 5.0)), clean)
