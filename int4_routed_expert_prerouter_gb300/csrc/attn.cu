@@ -15,8 +15,11 @@
 // own ring of bulk copies (a strip of 16 tokens of one head is one run of bytes).
 // Tokens are the M side of m16n8k16 steps and query rows the N side, so a group of
 // up to 8 query heads wastes nothing:
-//   S^T = K Q^T   codes enter as fp16 subnormals q 2^-24 (exact products, fp32 sums); per 64
-//                 dims S += s acc + b sum(Q), in fp32: scores carry no rounding of K;
+//   S^T = K Q^T   codes enter as fp16 subnormals q 2^-24 (exact products, fp32 sums); nibbles
+//                 4 bits up come in 16 times as large, into sums of their own that are
+//                 taken down in fp32 (Q / 16 in fp16 loses bits below 2^-10; nibbles shifted down
+//                 cost 7 % on long contexts); per 64 dims S += s acc + b sum(Q), in fp32:
+//                 scores carry no rounding of K or Q;
 //   O^T = V'^T P' V = s (q - z + r), z half the code range, r = b / s + z: q - z is
 //                 exact in fp16, the weight p s is rounded to fp16 (its only rounding),
 //                 and sum p s r, of the rounded weights, is kept in fp32 beside it: the
@@ -189,12 +192,12 @@ __device__ __forceinline__ float2 sb_of(uint32_t w) { return __half22float2(*rei
 template <int BITS>
 __device__ __forceinline__ void q_frag(const __half* src, bool there, uint32_t* w) {
     if (BITS == 4) {
-        // even nibbles 0,4 | 2,6, odd ones 1,5 | 3,7 (these come in sixteen times as large)
+        // even nibbles 0,4 | 2,6, odd ones 1,5 | 3,7
         const uint4 v = there ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
         w[0] = __byte_perm(v.x, v.z, 0x5410);
         w[1] = __byte_perm(v.y, v.w, 0x5410);
-        w[2] = hfma2(__byte_perm(v.x, v.z, 0x7632), 0x2C002C00u, 0x80008000u);
-        w[3] = hfma2(__byte_perm(v.y, v.w, 0x7632), 0x2C002C00u, 0x80008000u);
+        w[2] = __byte_perm(v.x, v.z, 0x7632);
+        w[3] = __byte_perm(v.y, v.w, 0x7632);
     } else {
         const uint2 v = there ? *reinterpret_cast<const uint2*>(src) : make_uint2(0, 0);
         w[0] = __byte_perm(v.x, v.y, 0x5410);    // dims 0, 2
@@ -349,12 +352,11 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
         for (int s = 0; s < X::STAGES - 1; ++s) issue();
 
         // query rows of the block as B fragments; their sums over each 64 dims are
-        // matrix steps against ones (16 where the fragment holds a sixteenth)
+        // matrix steps against ones
         const int r0 = rb * 8 * NT;
         uint32_t qf[X::kQRegs ? X::CH : 1][QW];
         float qs[X::kQRegs ? GR : 1][2];
         const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
-        const uint32_t sixteens[4] = {0x4C004C00u, 0x4C004C00u, 0x4C004C00u, 0x4C004C00u};
         auto q_at = [&](int r, int c) {
             return p.q + (long long)(seq * p.q_step + r / p.G) * p.ldq + (long long)(h * p.G + r % p.G) * D +
                    (BITS == 4 ? 32 * c + 8 * t : 16 * c + 4 * t);
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                 const uint32_t* w = f + c * QW;
                 if (c == gr * X::CPG) mma_16816_first(sum, ones, w[0], w[1]);
                 else mma_16816_v(sum, ones, w[0], w[1]);
-                if (BITS == 4) mma_16816_v(sum, sixteens, w[QW - 2], w[QW - 1]);
+                if (BITS == 4) mma_16816_v(sum, ones, w[QW - 2], w[QW - 1]);
             }
         };
         if constexpr (X::kQRegs) {
@@ -445,7 +447,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                 // (a strip behind the last token holds what was there before; it is masked below)
 #pragma unroll
                 for (int gr = 0; gr < GR; ++gr) {
-                    float acc[NT][4];
+                    float acc[NT][4], odd[NT][4];              // odd: of the nibbles 4 bits up
 #pragma unroll
                     for (int cp = 0; cp < X::CPG; cp += 2) {
                         const int c0 = gr * X::CPG + cp;
@@ -473,13 +475,19 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                                 }
                                 if (cp + j == 0) mma_16816_first(acc[nt], A0, f[0], f[1]);
                                 else mma_16816_v(acc[nt], A0, f[0], f[1]);
-                                if (BITS == 4) mma_16816_v(acc[nt], A1, f[QW - 2], f[QW - 1]);
+                                if (BITS == 4 && cp + j == 0) mma_16816_first(odd[nt], A1, f[QW - 2], f[QW - 1]);
+                                else if (BITS == 4) mma_16816_v(odd[nt], A1, f[QW - 2], f[QW - 1]);
                             }
                         }
                     }
                     const float2 sa = sb_of(wa[gr]), sb = sb_of(wb[gr]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
+                        if (BITS == 4)
+#pragma unroll
+                            for (int i = 0; i < 4; i += 2)
+                                unpk(fma2(pk(odd[nt][i], odd[nt][i + 1]), pk(1.f / 16, 1.f / 16), pk(acc[nt][i], acc[nt][i + 1])),
+                                     acc[nt][i], acc[nt][i + 1]);
                         float q0, q1;
                         if constexpr (X::kQRegs) {
                             q0 = qs[gr][0];
@@ -489,10 +497,9 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                             q1 = sqsum[(nt * 8 + 2 * t + 1) * GR + gr];
                         }
                         float(&s)[4] = S[st][nt];
-                        s[0] = fmaf(sa.x, acc[nt][0], fmaf(sa.y, q0, gr ? s[0] : -m[nt][0]));
-                        s[1] = fmaf(sa.x, acc[nt][1], fmaf(sa.y, q1, gr ? s[1] : -m[nt][1]));
-                        s[2] = fmaf(sb.x, acc[nt][2], fmaf(sb.y, q0, gr ? s[2] : -m[nt][0]));
-                        s[3] = fmaf(sb.x, acc[nt][3], fmaf(sb.y, q1, gr ? s[3] : -m[nt][1]));
+                        const f2 qq = pk(q0, q1), mm = pk(-m[nt][0], -m[nt][1]);
+                        unpk(fma2(pk(sa.x, sa.x), pk(acc[nt][0], acc[nt][1]), fma2(pk(sa.y, sa.y), qq, gr ? pk(s[0], s[1]) : mm)), s[0], s[1]);
+                        unpk(fma2(pk(sb.x, sb.x), pk(acc[nt][2], acc[nt][3]), fma2(pk(sb.y, sb.y), qq, gr ? pk(s[2], s[3]) : mm)), s[2], s[3]);
                     }
                 }
             }
