@@ -13,8 +13,9 @@
 //               P'_g = fp16(p s_g), and sum_j P'_g r_g in fp32.
 // Scores: with K = s (code - z + r), r = b / s + z, a group's product is
 // Q_g (code - z) + mean(Q_g) 64 r; the second term is one more step of 16 of the same
-// product, its factors split into two fp16 each, so that S = sum_g s_g S_g carries no
-// rounding of K beyond 2^-22.  Each weight is rounded once (to fp16, 2^-11 of itself):
+// product, its factors split into two fp16 each (the mean's second one 2^11 times as large,
+// which a subnormal mean needs), so that S = sum_g s_g S_g carries no rounding of K or Q beyond
+// 2^-22.  Each weight is rounded once (to fp16, 2^-11 of itself):
 // with V = s (code - z + r) likewise, o = (O_g + sum P'_g r_g) / sum p.  Scores have the running
 // maximum, scales a power of two above the largest so far as reference (kUp, kRise, kLow:
 // attn.cuh); a reference moves only when exceeded by 2^4, and the accumulators are
@@ -163,10 +164,11 @@ __device__ __forceinline__ uint4 codes8(uint32_t w0, uint32_t w1) {
     }
     return r;
 }
-// v = hi + lo 2^-11-ish: two fp16 in one word
+// v = hi + lo 2^-k: two fp16 in one word, lo of 2^k times what hi leaves
+template <int K>
 __device__ __forceinline__ uint32_t split(float v) {
     const __half hi = __float2half_rn(v);
-    const __half2 r = __halves2half2(hi, __float2half_rn(v - __half2float(hi)));
+    const __half2 r = __halves2half2(hi, __float2half_rn((v - __half2float(hi)) * (float)(1 << K)));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
@@ -262,7 +264,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                     s += f.x + f.y;
                 }
             }
-            const uint32_t hl = split(s * (1.f / kGroup));     // (hi, lo), against (hi, hi, lo, lo) of r
+            // A mean is a multiple of 2^-30 (the queries' step is 2^-24 at least), 2^11 times what its first
+            // fp16 leaves one of 2^-19: exact, or within 2^-24 of the mean, however small the queries.
+            const uint32_t hl = split<11>(s * (1.f / kGroup));
             *reinterpret_cast<uint2*>(sM + gr * (kRowsQ * 32) + tc::kstep_off(r, 4 * gr)) = make_uint2(hl, hl);
         }
         tc::fence_async_smem();
@@ -352,9 +356,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                     // b = 1 (0 - z + b + z)
                     const float off = flat ? sb.y + kZ : __fdividef(sb.y, sb.x) + kZ;
                     tab_k[(tok >> 1) * 2 * GR + 2 * gr + (tok & 1)] = none ? 0.f : (flat ? 1.f : sb.x) * p.k * 1024.f;
-                    const uint32_t hl = split(none ? 0.f : off * (kGroup / 1024.f));
+                    // (hi, 2^11 lo) of the mean against (off, off / 2^11), then against what these leave
+                    const uint32_t a = split<0>(none ? 0.f : off * (kGroup / 1024.f));
+                    const uint32_t b = split<0>(none ? 0.f : off * (kGroup / 1024.f / 2048.f));
                     *reinterpret_cast<uint2*>(sR + tc::kstep_off(tok, 4 * gr)) =
-                        make_uint2(__byte_perm(hl, hl, 0x1010), __byte_perm(hl, hl, 0x3232));
+                        make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
                 }
             }
             tc::fence_async_smem();

@@ -65,3 +65,26 @@ def test_small_queries_over_own_contexts(bits, D, H, G, size):
         want, bound = ref.attention(q[b].astype(np.float64), *tokens_of(c, lists[b], lens[b], [], 0), scale)
         err = np.abs(got[b] - want)
         assert (err <= bound).all(), (b, (err / bound).max())
+
+
+# (bits, D, H, G, sequences): from so many query rows per K/V head on the prefix runs on the fifth-generation tensor cores
+PREFIX = [(4, 64, 1, 8, 9), (4, 128, 2, 4, 6), (4, 256, 1, 16, 3), (8, 64, 1, 8, 9), (8, 128, 2, 4, 6), (8, 256, 1, 16, 3)]
+
+
+@pytest.mark.parametrize("size", [1e-3, 1e-4, 1e-5, 1e-6])
+@pytest.mark.parametrize("bits,D,H,G,B", PREFIX + [(4, 64, 1, 4, 2), (8, 128, 1, 4, 3)])
+def test_small_queries_over_a_shared_prefix(bits, D, H, G, B, size):
+    """As above; K's mean over each 64 dims is far from zero, so that the queries' sums count."""
+    rng = np.random.default_rng(D + G)
+    c = ref.Cache(14, 64, H, D, bits, rng, k_offset=2.0)
+    pre, P = list(range(13)), 777
+    q = rng.standard_normal((B, H * G, D)) * size
+    q[B - 1] *= 2.0 ** rng.integers(-12, 13, (H * G, 1))
+    q = q.astype(np.float16)
+    scale = D ** -0.5 / size
+    lens = [5 * (b % 2) for b in range(B)]
+    got = call(c, q, [[13]] * B, lens, pre, P, scale)
+    for b in range(B):
+        want, bound = ref.attention(q[b].astype(np.float64), *tokens_of(c, [13], lens[b], pre, P), scale)
+        err = np.abs(got[b] - want)
+        assert (err <= bound).all(), (b, (err / bound).max())
