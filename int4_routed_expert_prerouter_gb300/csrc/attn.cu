@@ -27,11 +27,12 @@
 //                 of the unrounded weights it was a sixth larger.)
 // Both factors of p s have a reference: the running maximum of the row's scores, and the
 // power of two 2^e above the largest V scale so far.  p s / 2^e times 2^7 uses fp16's range
-// to its top, so that it is normal down to 2^-21 of the largest; where a scale is
-// below 2^-9 of the reference (there r = b / s + z can be large), sum p s r takes the
-// unrounded weights instead, whose error does not grow with r.  Scores are formed less
-// their reference from the first term on, and e stays out of that sum, so that
-// neither is lost to the other's magnitude.
+// to its top, so that it is normal down to 2^-21 of the largest.  Where a scale is below 2^-9
+// of the reference (a token of large V may have raised it, whatever its own weight; r = b / s
+// + z can be large there), sum p s r takes the unrounded weights, and what the rounding took
+// from subnormal ones enters in a second product, 2^24 times on codes 2^-24 times: weights
+// are then good to 2^-48 of the range.  Scores are formed less their reference from the first
+// term on, and e stays out of that sum, so that neither is lost to the other's magnitude.
 //
 // The floor is the pages' bytes.  Measured: four sequences of 100,003 to 131,072 tokens, 8 K/V
 // heads of 128 dims at 4 bits, 115 us, 549 MB at 4.8 TB/s, 0.70 of what a copy reaches: what
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
         // Weight of a score S: 2^(k (S - m)), m the row's reference; of a code beside it, s / es 2^kUp
         // times that, es = 2^e the scales' reference.
         float O[X::MT][NT][4], beta[NT][GR][2], m[NT][2], l[NT][2];
-        float es = 0.f, high = -INFINITY;
+        float es = 0x1p-40f, high = -INFINITY;                   // (below any scale: the first one moves it)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -565,11 +566,10 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                                 if (vs[st][gr][i].x == 0.f) {    // a constant group, codes 0: b = |b| (0 - z + z +- 1)
                                     const float b = __half2float(*reinterpret_cast<const __half*>(
                                         buf + st * X::STRIP + X::HALF + 16 * X::R + (g + 8 * i) * X::SB + gr * 4 + 2));
-                                    vs[st][gr][i] = b == 0.f ? make_float2(1.f / kTwo24, kZ)
-                                                             : make_float2(fabsf(b), kZ + copysignf(1.f, b));
+                                    vs[st][gr][i] = make_float2(fabsf(b), b == 0.f ? kZ : kZ + copysignf(1.f, b));
                                 }
                                 most_s = fmaxf(most_s, vs[st][gr][i].x);
-                                least_s = fminf(least_s, vs[st][gr][i].x);
+                                if (vs[st][gr][i].x != 0.f) least_s = fminf(least_s, vs[st][gr][i].x);   // (zeros: no weight)
                             }
                 most_s = max_over_rows(most_s);
                 float f_s = 1.f;
@@ -616,6 +616,50 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
 #pragma unroll
                     for (int i = 0; i < 2; ++i) l[nt][i] += S[st][nt][i] + S[st][nt][i + 2];
                 }
+            if (__builtin_expect(tiny, 0)) {
+                // Weights below fp16's normal range: what the rounding took from them, 2^24 times, on the codes
+                // 2^-24 times (exact as subnormals); from all weights, in the offsets' sum.
+                const float up = kUp * reciprocal2(es);
+                auto taken = [](float w) { return w - __half2float(__float2half_rn(w)); };
+                auto rest = [&](float w) { return fabsf(w) < 0x1p-14f ? taken(w) * kTwo24 : 0.f; };
+#pragma unroll
+                for (int st = 0; st < X::US; ++st) {
+                    const uint32_t va = smem_u32(buf + st * X::STRIP + X::HALF) + row_off;
+#pragma unroll
+                    for (int gr = 0; gr < GR; ++gr) {
+                        uint32_t b0[NT], b1[NT];
+                        const float2 v0 = vs[st][gr][0], v1 = vs[st][gr][1];
+                        const float u0 = v0.x * up, u1 = v1.x * up;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const float(&P)[4] = S[st][nt];
+                            b0[nt] = transpose8(pack2(rest(P[0] * u0), rest(P[1] * u0)));
+                            b1[nt] = transpose8(pack2(rest(P[2] * u1), rest(P[3] * u1)));
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                beta[nt][gr][i] = fmaf(taken(P[i] * u0), v0.y, fmaf(taken(P[i + 2] * u1), v1.y, beta[nt][gr][i]));
+                        }
+#pragma unroll
+                        for (int cp = 0; cp < X::CPG; cp += 2) {
+                            const int c0 = gr * X::CPG + cp;
+                            uint32_t w[4];
+                            ldsm4t(w, va + (piece ^ (c0 << 4)));
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                                for (int q = 0; q < (BITS == 4 ? 2 : 1); ++q) {
+                                    uint32_t A[4];
+                                    v_frag<BITS>(w[2 * j], w[2 * j + 1], q, A);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) A[i] = hfma2(A[i], 0x00010001u, 0x80008000u);
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt)
+                                        mma_16816_v(O[(BITS == 4 ? 2 : 1) * (c0 + j) + q][nt], A, b0[nt], b1[nt]);
+                                }
+                        }
+                    }
+                }
+            }
 #pragma unroll
             for (int st = 0; st < X::US; ++st) {
                 const uint32_t va = smem_u32(buf + st * X::STRIP + X::HALF) + row_off;
@@ -629,11 +673,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<BITS, D, NT>::kMinCtas) attn_
                     for (int nt = 0; nt < NT; ++nt) {
                         const float(&P)[4] = S[st][nt];
                         const uint32_t h0 = pack2(P[0] * u0, P[1] * u0), h1 = pack2(P[2] * u1, P[3] * u1);
-                        float2 f0 = sb_of(h0), f1 = sb_of(h1);               // the rounded weights
-                        if (tiny) {
-                            f0 = make_float2(P[0] * u0, P[1] * u0);
-                            f1 = make_float2(P[2] * u1, P[3] * u1);
-                        }
+                        const float2 f0 = sb_of(h0), f1 = sb_of(h1);         // the rounded weights
                         b0[nt] = transpose8(h0);
                         b1[nt] = transpose8(h1);
                         beta[nt][gr][0] = fmaf(f0.x, v0.y, fmaf(f1.x, v1.y, beta[nt][gr][0]));

@@ -88,3 +88,66 @@ def test_small_queries_over_a_shared_prefix(bits, D, H, G, B, size):
         want, bound = ref.attention(q[b].astype(np.float64), *tokens_of(c, [13], lens[b], pre, P), scale)
         err = np.abs(got[b] - want)
         assert (err <= bound).all(), (b, (err / bound).max())
+
+
+def row_bound(q, k, v, parts, sz, scale):
+    """ref.attention with a bound that does not grow with the largest V: o [Hq, D], bound.  As there:
+    the result's rounding, the weights' rounding to fp16, their own errors a_j, fp32 sums.  In place
+    of its terms for weights below fp16's normal range, with p the softmax weights before they are
+    normalised (the largest between 2^-4 and 1), es the power of two above the largest s so far (at
+    most 2^17, as s <= 65504) and w = 128 p s / es the fp16 weight, whose rounding is off by no more
+    than w itself:
+    - s >= 2^-9 es, then p < 2^-12: half a subnormal step, 2^-25 es / 128 <= 2^-23 s, times |q - z| <= z
+      and times r: min(p, 2^-23) (|s z| + |v|);
+    - s below 2^-9 es: what the rounding leaves is carried in units of 2^-48, off by 2^-49 es / 128
+      <= 2^-39 at most, times |q - z| <= 128."""
+    Hq, D = q.shape
+    n, H, _ = k.shape
+    G = Hq // H
+    o, bound = np.zeros((Hq, D)), np.full((Hq, D), 2.0 ** -24)
+    for h in range(Hq):
+        kk, vv, pp, big = (a[:, h // G] for a in (k, v, parts, sz))
+        sc = scale * (kk @ q[h])
+        p = np.exp(sc - sc.max())
+        total = p.sum()
+        o[h] = p @ vv / total
+        mag = 3 * np.abs(kk).reshape(n, -1, 64).max(-1).repeat(64, -1)
+        a = scale * (mag @ np.abs(q[h])) * (D / 16 + D / 64) * 2.0 ** -23 + np.abs(sc) * 2.0 ** -22 + 2.0 ** -20
+        bound[h] += (2.0 ** -11 + p @ a / total) * np.abs(o[h]) + (p * (2.0 ** -11 + a + (n / 16 + 64) * 2.0 ** -23)) @ pp / total
+        bound[h] += (np.where(p < 2.0 ** -8, np.minimum(p, 2.0 ** -23), 0) @ (big + np.abs(vv)) + n * 2.0 ** -32) / total
+    return o, bound
+
+
+def outlier_case(bits, D, H, G, size, rng, at, groups):
+    """A cache of V's of `size` whose tokens `at` hold V's up to 30,000 in some groups of 64 dims and a
+    key against all queries but the last of each group of heads, which sees nothing else."""
+    c = ref.Cache(14, 64, H, D, bits, rng)
+    x = c.x.astype(np.float16)                       # [pages, 2, tokens, H, D]
+    x[:, 1] = (rng.standard_normal(x[:, 1].shape) * size).astype(np.float16)
+    u = rng.standard_normal(D)
+    u *= (40.0 * D ** 0.5 / (u @ u)) ** 0.5          # u . u / sqrt(D) = 40
+    for t in at:
+        x[t // 64, 0, t % 64] = (-u).astype(np.float16)
+        for g in groups:
+            x[t // 64, 1, t % 64, :, 64 * g:64 * g + 64] = (rng.uniform(-1, 1, (H, 64)) * 30000).astype(np.float16)
+    c.codes, c.s, c.b = ref.quantise(x, bits)
+    c.image, c.x = ref.page_image(c.codes, c.s, c.b, bits), ref.values(c.codes, c.s, c.b)
+    q = u + 0.3 * rng.standard_normal((H * G, D))
+    q[G - 1::G] = -u
+    return c, q
+
+
+@pytest.mark.parametrize("size", [1.0, 1e-2, 1e-3, 1e-4])
+@pytest.mark.parametrize("bits,D,H,G", SHAPES)
+def test_large_values_without_weight_in_own_contexts(bits, D, H, G, size):
+    """Tokens of next to no weight and large values leave the small values of the others alone, before
+    and behind them, also where another query sees those tokens only."""
+    rng = np.random.default_rng(D + G + bits)
+    c, q = outlier_case(bits, D, H, G, size, rng, range(3, 832, 24), range(D // 128 + 1))
+    lens, lists = [777, 40, 330], [list(range(13)), [0], list(range(13))]
+    qs = np.stack([q, q * 0.9, q * 1.1]).astype(np.float16)
+    got = call(c, qs, lists, lens, [], 0, D ** -0.5)
+    for b in range(3):
+        want, bound = row_bound(qs[b].astype(np.float64), *tokens_of(c, lists[b], lens[b], [], 0), D ** -0.5)
+        err = np.abs(got[b] - want)
+        assert (err <= bound).all(), (b, (err / bound).max())
