@@ -17,9 +17,10 @@
 // which a subnormal mean needs), so that S = sum_g s_g S_g carries no rounding of K or Q beyond
 // 2^-22.  Each weight is rounded once (to fp16, 2^-11 of itself):
 // with V = s (code - z + r) likewise, o = (O_g + sum P'_g r_g) / sum p.  Scores have the running
-// maximum, scales a power of two above the largest so far as reference (kUp, kRise, kLow:
+// maximum, scales a power of two above the largest so far as reference (kUp, kRise, kLowS:
 // attn.cuh); a reference moves only when exceeded by 2^4, and the accumulators are
-// then rescaled in TMEM.
+// then rescaled in TMEM.  A tile with a scale below 2^-9 of the reference gets a second product,
+// of what the rounding took from its subnormal weights.
 // The accumulators are read and P' written as 8-column fragments (a lane: 2 tokens of
 // 4 rows): a token's scales, read from shared memory, serve 4 rows; with a row per
 // thread reading them alone took 2000 cycles a step.
@@ -40,6 +41,7 @@ constexpr int kSoftmax = 256;             // threads of the softmax warps
 constexpr int kThreads = kSoftmax + 128;  // and the operand warps
 constexpr int kRowsQ = kPrefixRows;
 constexpr int kTile = kPrefixTile;
+constexpr int kAgain = 1, kLeave = 2;     // after a tile's product: another one for it; a wait ran out
 
 template <int BITS, int D>
 struct Cfg {
@@ -193,9 +195,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
     constexpr int GR = X::GR;
     constexpr float kZ = BITS == 4 ? 8.f : 128.f;
     extern __shared__ __align__(128) char smem[];
-    __shared__ uint64_t full[2], freed[2], s_ready, drained;
+    __shared__ uint64_t full[2], freed[2], s_ready, again, drained;
     __shared__ uint32_t taddr_s;
-    __shared__ int dead;
+    __shared__ int dead, n_again, next_s[2];
     __shared__ float part_max[2][kRowsQ];
     char *sQ = smem, *sM = smem + X::kQ, *stages = sM + X::kMean;
     const int tid = threadIdx.x, wid = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -215,8 +217,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
             mbar_init(&freed[i], 1);
         }
         mbar_init(&s_ready, 1);
+        mbar_init(&again, 1);
         mbar_init(&drained, 1);
         fence_mbar_init();
+        n_again = 0;
         dead = p.wait_ns == 0;                                 // (limit 0: given up from the start)
     }
     tc::fence_before_sync();
@@ -349,9 +353,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                 if (v) {
                     // b = |b| (0 - z + z +- 1)
                     float* at = tab_v + ((tok >> 1) * GR + gr) * 4 + (tok & 1);
-                    const float s = !flat ? sb.x : sb.y == 0.f ? 1.f / kTwo24 : fabsf(sb.y);
+                    const float s = flat ? fabsf(sb.y) : sb.x;     // (zeros: no weight, as where there is no token)
                     at[0] = none ? 0.f : s;
-                    at[2] = none ? 0.f : __fdividef(sb.y, s) + kZ;
+                    at[2] = none || s == 0.f ? 0.f : __fdividef(sb.y, s) + kZ;
                 } else {
                     // b = 1 (0 - z + b + z)
                     const float off = flat ? sb.y + kZ : __fdividef(sb.y, sb.x) + kZ;
@@ -388,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
         const uint32_t my = tm + ((uint32_t)(32 * quad) << 16);
         // rows 32 quad + 16 rh + g + 8 k, index 2 rh + k; weight of a score: 2^(S - mu), S in
         // exponent units, mu the running maximum; of a code beside it s / es kUp times that
-        float mu[4], l[4], beta[4][GR], es = 0.f;
+        float mu[4], l[4], beta[4][GR], es = 0x1p-40f;          // (below any scale: the first one moves it)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             mu[r] = l[r] = 0.f;
@@ -412,6 +416,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                        tc::idesc_f16(kRowsQ, kTile), true, lead);
             }
             commit(&s_ready, lead);
+        };
+        auto issue_values = [&](int i, bool accumulate, uint32_t lead) {   // warp 0: O_g (+)= P'_g V_g of tile i
+            const uint32_t sV = desc_lo(st0 + (i & 1) * X::kStage + X::kOp, 128);
+            tc::fence_after_sync();
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                    mma_ts(tm + GR * kTile + gr * kGroup, tm + gr * kTile + (kk >> 1) * 32 + (kk & 1) * 8,
+                           desc(sV + (gr * (kGroup / 8) * (kTile * 16) + kk * 256) / 16, kTile * 16),
+                           tc::idesc_f16(kRowsQ, kGroup) | (1u << 16), accumulate || kk > 0, lead);
         };
         if (wid == 0) issue_scores(0, elect());
         for (int i = 0; i < n; ++i) {
@@ -575,46 +590,73 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, D>::kCtas) attn_prefix_ker
                     }
                 }
             }
-            if (tiny) {
-                const float up = kUp * reciprocal2(es);        // what the rounding took from sum p s r
-#pragma unroll
-                for (int gr = 0; gr < GR; ++gr)
-#pragma unroll 1
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 v = *reinterpret_cast<const float4*>(mv + j * 16 * GR + gr * 4);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            f2 x = S[r >> 1][0][r & 1];
-#pragma unroll
-                            for (int i = 1; i < 4; ++i) x = j == i ? S[r >> 1][i][r & 1] : x;
-                            float a, b;
-                            unpk(x, a, b);
-                            a *= v.x * up;
-                            b *= v.y * up;
-                            const uint32_t h = pack2(a, b);
-                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                            beta[r][gr] = fmaf(a - f.x, v.z, fmaf(b - f.y, v.w, beta[r][gr]));
-                        }
-                    }
-            }
             tmem_wait_st();
             tc::fence_before_sync();
-            if (any_of<kSoftmax>(3, *(volatile int*)&dead)) break;
+            if (wid == 0) *(volatile int*)&next_s[i & 1] = *(volatile int*)&dead ? kLeave : tiny ? kAgain : 0;
+            named_bar_sync(3, kSoftmax);
+            // what all warps do, whatever each has seen (a barrier that reduces a flag took 1 us of 68)
+            const int next = *(volatile int*)&next_s[i & 1];
+            if (next == kLeave) break;
             if (wid == 0) {
                 const uint32_t lead = elect();
-                const uint32_t sV = desc_lo(st0 + (i & 1) * X::kStage + X::kOp, 128);
+                issue_values(i, i > 0, lead);
+                commit(next ? &again : &freed[i & 1], lead);
+                if (!next && i + 1 < n) issue_scores(i + 1, lead);
+            }
+            __syncwarp();
+            if (__builtin_expect(next, 0)) {
+                // Weights below fp16's normal range: what the rounding took from them, 2^24 times, on V's codes
+                // 2^-24 times (exact as subnormals), in another product; from all weights, in the offsets' sum.
+                (void)wait_bar(&again, n_again & 1, &dead, p.wait_ns);     // the weights and codes have been used
+                __syncwarp();
                 tc::fence_after_sync();
+                const float up = kUp * reciprocal2(es);
+                auto taken = [](float w) { return w - __half2float(__float2half_rn(w)); };
+                auto rest = [&](float w) { return fabsf(w) < 0x1p-14f ? taken(w) * kTwo24 : 0.f; };
 #pragma unroll
                 for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk)
-                        mma_ts(tm + GR * kTile + gr * kGroup, tm + gr * kTile + (kk >> 1) * 32 + (kk & 1) * 8,
-                               desc(sV + (gr * (kGroup / 8) * (kTile * 16) + kk * 256) / 16, kTile * 16),
-                               tc::idesc_f16(kRowsQ, kGroup) | (1u << 16), i > 0 || kk > 0, lead);
-                commit(&freed[i & 1], lead);
-                if (i + 1 < n) issue_scores(i + 1, lead);
+                    for (int rh = 0; rh < 2; ++rh) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 v = *reinterpret_cast<const float4*>(mv + j * 16 * GR + gr * 4);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                float a, b;
+                                unpk(S[rh][j][k], a, b);
+                                a *= v.x * up;
+                                b *= v.y * up;
+                                w[2 * j + k] = pack2(rest(a), rest(b));
+                                float& sum = beta[2 * rh + k][gr];
+                                sum = fmaf(taken(a), v.z, fmaf(taken(b), v.w, sum));
+                            }
+                        }
+                        tmem_st_pairs(my + ((uint32_t)(16 * rh) << 16) + gr * kTile + hf * 32, w);
+                    }
+                uint4* codes = reinterpret_cast<uint4*>(stages + (i & 1) * X::kStage + X::kOp);
+#pragma unroll 1
+                for (int c = tid; c < X::kOp / 16; c += kSoftmax) {
+                    uint4 v = codes[c];
+                    v.x = hfma2(v.x, 0x00010001u, 0x80008000u);
+                    v.y = hfma2(v.y, 0x00010001u, 0x80008000u);
+                    v.z = hfma2(v.z, 0x00010001u, 0x80008000u);
+                    v.w = hfma2(v.w, 0x00010001u, 0x80008000u);
+                    codes[c] = v;
+                }
+                tc::fence_async_smem();
+                tmem_wait_st();
+                tc::fence_before_sync();
+                if (any_of<kSoftmax>(3, *(volatile int*)&dead)) break;
+                if (tid == 0) ++n_again;
+                if (wid == 0) {
+                    const uint32_t lead = elect();
+                    issue_values(i, true, lead);
+                    commit(&freed[i & 1], lead);
+                    if (i + 1 < n) issue_scores(i + 1, lead);
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
         const bool ok = !*(volatile int*)&dead && wait_bar(&freed[(n - 1) & 1], ((n - 1) >> 1) & 1, &dead, p.wait_ns);
         // a row's sums: its 4 lanes, then both halves of the tokens (all operands are done with by now)

@@ -151,3 +151,53 @@ def test_large_values_without_weight_in_own_contexts(bits, D, H, G, size):
         want, bound = row_bound(qs[b].astype(np.float64), *tokens_of(c, lists[b], lens[b], [], 0), D ** -0.5)
         err = np.abs(got[b] - want)
         assert (err <= bound).all(), (b, (err / bound).max())
+
+
+@pytest.mark.parametrize("size", [1.0, 1e-2, 1e-3, 1e-4])
+@pytest.mark.parametrize("bits,D,H,G,B", PREFIX + [(4, 64, 1, 4, 2), (8, 128, 1, 4, 3)])
+def test_large_values_without_weight_in_a_shared_prefix(bits, D, H, G, B, size):
+    """As above, in the prefix (pages 0 to 12, in any order) and in the sequences' own tokens behind it."""
+    rng = np.random.default_rng(D + G + bits)
+    c, q = outlier_case(bits, D, H, G, size, rng, range(3, 896, 24), range(D // 128 + 1))
+    pre, P = rng.permutation(13).tolist(), 12 * 64 + 9
+    qs = np.stack([q * (1 + 0.02 * b) for b in range(B)]).astype(np.float16)
+    lens = [17 * (b % 3) for b in range(B)]
+    got = call(c, qs, [[13]] * B, lens, pre, P, D ** -0.5)
+    for b in range(B):
+        want, bound = row_bound(qs[b].astype(np.float64), *tokens_of(c, [13], lens[b], pre, P), D ** -0.5)
+        err = np.abs(got[b] - want)
+        assert (err <= bound).all(), (b, (err / bound).max())
+
+
+@pytest.mark.parametrize("bits,D,H,G,B", PREFIX + [(4, 128, 1, 4, 1), (8, 64, 1, 16, 1)])
+def test_zero_and_constant_groups_beside_large_values(bits, D, H, G, B):
+    """Groups of zeros (a whole tile of them first) and constant ones beside tokens of every size."""
+    rng = np.random.default_rng(D * bits + B)
+    c = ref.Cache(14, 64, H, D, bits, rng)
+    x = c.x.astype(np.float16)
+    x[:, 1] = (rng.standard_normal(x[:, 1].shape) * 1e-3).astype(np.float16)
+    x[:2, 1] = 0
+    for i, v in enumerate((0.0, 1e-3, -1e-3, 2.0 ** -24, -300.0, 0.0)):
+        x[2 + i::6, 1, i::7, :, :64] = v
+    u = rng.standard_normal(D)
+    u *= (40.0 * D ** 0.5 / (u @ u)) ** 0.5
+    for t in range(3, 64, 24):
+        x[2:, 0, t] = (-u).astype(np.float16)
+        x[2:, 1, t] = (rng.uniform(-1, 1, (H, D)) * 30000).astype(np.float16)
+    c.codes, c.s, c.b = ref.quantise(x, bits)
+    c.image, c.x = ref.page_image(c.codes, c.s, c.b, bits), ref.values(c.codes, c.s, c.b)
+    q = np.stack([u + 0.3 * rng.standard_normal((H * G, D))] * B).astype(np.float16)
+    sw, bw = (np.repeat(a[:, 1].astype(np.float64), 64, -1) for a in (c.s, c.b))
+    z = 2.0 ** (bits - 1)
+    # a constant group's value b is |b| times (0 - z) + (z +- 1): its part that meets a code is z |b|
+    parts = np.where(sw == 0, (2 * z + 1) * np.abs(bw), np.abs(sw * (c.codes[:, 1].astype(np.float64) - z)) + np.abs(sw * z + bw))
+    big = np.where(sw == 0, np.abs(bw), sw) * z
+    flat = lambda a, pages, m: a[np.asarray(pages)].reshape(-1, H, D)[:m]
+    for P, n in ((777, 60), (0, 860), (128, 0)):
+        pre, own = list(range(13)), [13] if P else list(range(14))
+        got = call(c, q, [own] * B, [n] * B, pre, P, D ** -0.5)
+        for b in range(B):
+            k, v, pp, zz = (np.concatenate([flat(a, pre, P), flat(a, own, n)]) for a in (c.x[:, 0], c.x[:, 1], parts, big))
+            want, bound = row_bound(q[b].astype(np.float64), k, v, pp, zz, D ** -0.5)
+            err = np.abs(got[b] - want)
+            assert (err <= bound).all(), (P, n, b, (err / bound).max())
