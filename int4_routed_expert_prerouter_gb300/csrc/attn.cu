@@ -64,7 +64,7 @@ struct AttnP {
     long long ldq;
     int G, H;                // query heads per K/V head, K/V heads
     // segments: n_seq lists of pages; rows of list i of head h: r -> query
-    // row (i * seq_rows + r / G, h G + r % G)
+    // row (i * q_step + r / G, h G + r % G)
     int n_seq, rows, RB, q_step;
     const int* pages;        // [n_seq][W]
     int W;
@@ -909,7 +909,7 @@ __device__ __forceinline__ void join_by_cta(const JoinP& p, const RowParts& x, f
 template <int D>
 __global__ void __launch_bounds__(128) attn_join_kernel(const JoinP p) {
     __shared__ float acc[4][D];
-    const int len = p.lens[blockIdx.x / (p.G * p.H)];
+    const int len = p.lens[blockIdx.x / (p.G * p.H)];      // before the wait: see launch.cuh
     wait_predecessor();
     launch_dependents();
     const RowParts x(p, blockIdx.x, len, D);
@@ -926,7 +926,7 @@ __global__ void __launch_bounds__(128) attn_join_rows_kernel(const JoinP p) {
     __shared__ float acc[4][D];
     __shared__ int many[4];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, row = blockIdx.x * 4 + wid;
-    const int len = row < p.n_rows ? p.lens[row / (p.G * p.H)] : -1;
+    const int len = row < p.n_rows ? p.lens[row / (p.G * p.H)] : -1;      // before the wait: see launch.cuh
     wait_predecessor();
     launch_dependents();
     bool alone = false;
