@@ -593,6 +593,10 @@ def _bad(what):
     return Edge0Error(EDGE0_EINVAL, what)
 
 
+_INT_MAX = 0x7fffffff       # counts are C ints: a larger one would arrive as another number
+_MAX_LINEAR, _MAX_PREFIX = 1 << 28, 1 << 30      # EDGE0_MAX_LINEAR, EDGE0_MAX_PREFIX
+
+
 def _guard(index, stream):
     """The context of a call whose allocations and launches are not the current device's and
     stream's: that stream (its device too), or that device; None where they are."""
@@ -658,6 +662,8 @@ def _q4_linear(packed, out_features, x, y, index, stream):
     if (packed.dtype is not _u8 or packed.get_device() != index or not packed.is_contiguous() or n_in % 64
             or packed.numel() != (out_features + 15) // 16 * (n_in // 64) * 576 or out_features <= 0 or n_in == 0):
         raise _bad("q4_linear: packed is not an [out_features, in] matrix beside x")
+    if out_features > _MAX_LINEAR or n_in > _MAX_LINEAR or B > _INT_MAX:
+        raise Edge0Error(EDGE0_EUNSUPPORTED, "q4_linear: outputs, inputs or rows beyond the limit")
     if y is None:
         # (x.new_empty would cost the launch behind it 3 us more)
         y, ldy = torch.empty((B, out_features), dtype=_f16, device=x.device), out_features
@@ -717,6 +723,8 @@ def _sequences(cache, table, start, cu_rows, T, what):
     index = cache._index
     if cu_rows is None and T != B:
         raise _bad(f"{what}: one row per sequence without cu_rows")
+    if B > _INT_MAX or W > _INT_MAX or T > _INT_MAX:
+        raise Edge0Error(EDGE0_EUNSUPPORTED, f"{what}: rows, sequences or pages beyond 2^31 - 1")
     return (_ints(table, index, B * W, "table"), B, W, _ints(start, index, B, "start"),
             None if cu_rows is None else _ints(cu_rows, index, B + 1, "cu_rows"))
 
@@ -749,7 +757,7 @@ def _kv_append(cache, k, v, table, start, cu_rows, stream):
 
 def kv_read(cache: KVCache, table, start, cu_rows=None, T=None, k=None, v=None, stream=None):
     """(k, v) [T, n_kv_heads, head_dim] fp16: the values that the rows' pages stand for
-    (rows as in kv_append).  k, v: contiguous outputs to fill, or None for new ones; rows
+    (rows as in kv_append).  T: rows of the call, as many as sequences unless given.  k, v: contiguous outputs to fill, or None for new ones; rows
     that no sequence has are left as they are."""
     guard = _guard(cache._index, stream)
     if guard is not None:
@@ -811,11 +819,15 @@ def _attn_decode(cache, q, table, lens, prefix, n_prefix, scale, out, workspace,
     if table.dim() != 2 or table.shape[0] != B:
         raise _bad("attn_decode: table [B, W]")
     W = table.shape[1]
+    if W > _INT_MAX:
+        raise Edge0Error(EDGE0_EUNSUPPORTED, "attn_decode: pages beyond 2^31 - 1")
     tb, ln = _ints(table, index, B * W, "attn_decode: table"), _ints(lens, index, B, "attn_decode: lens")
     pf = None
     if n_prefix:
         if n_prefix < 0 or prefix is None or prefix.numel() * cache.page_tokens < n_prefix:
             raise _bad("attn_decode: n_prefix tokens in the pages `prefix`")
+        if n_prefix > _MAX_PREFIX:
+            raise Edge0Error(EDGE0_EUNSUPPORTED, "attn_decode: n_prefix beyond the limit")
         pf = _ints(prefix, index, prefix.numel(), "attn_decode: prefix")
     if out is None:
         out, ldo = torch.empty((B, Hq, D), dtype=_f16, device=cache.device), Hq * D
