@@ -703,7 +703,7 @@ class KVCache:
         self.status = torch.zeros(1, dtype=torch.int32, device=pages.device)
         self.desc = KvCacheDesc(bits, n_kv_heads, head_dim, page_tokens, n_pages, _ptr(pages))
         self._index, self._desc, self._status = pages.get_device(), C.byref(self.desc), self.status.data_ptr()
-        self._ws_bytes, self._ws, self._ws_lock = {}, {}, threading.Lock()
+        self._ws_bytes = {}
 
     def error(self) -> int:
         """What the calls on this cache have recorded since the last error() (waits
@@ -794,6 +794,19 @@ def attn_workspace_bytes(cache: KVCache, B: int, n_q_heads: int) -> int:
     return n
 
 
+# Workspaces of attention calls that bring none: one per device and stream, for all caches (a model
+# has a cache per layer, and its calls run one after the other); the lock keeps the launches of two
+# threads' calls from mixing.
+_kept, _kept_lock = {}, threading.Lock()
+
+
+def release_workspaces():
+    """Give back the workspaces kept for attention calls without one (each as large as the largest
+    call on its stream needed); a later call makes a new one.  Calls under way are not disturbed."""
+    with _kept_lock:
+        _kept.clear()
+
+
 def attn_decode(cache: KVCache, q: torch.Tensor, table, lens, prefix=None, n_prefix=0, scale=None, out=None,
                 workspace=None, stream=None) -> torch.Tensor:
     """Attention of one query token per sequence, q [B, n_q_heads, head_dim] fp16, over
@@ -801,8 +814,8 @@ def attn_decode(cache: KVCache, q: torch.Tensor, table, lens, prefix=None, n_pre
     sequence's own lens[b] tokens of the pages table[b].  scale: 1 / sqrt(head_dim)
     unless given.  out: rows to fill (those of sequences with lens[b] < 0 are left as
     they are) or None.  workspace: uint8 of attn_workspace_bytes, not used by anything else
-    while the call runs, or None for one that the cache keeps per stream (a captured call:
-    one of its own)."""
+    while the call runs, or None for one that is kept per device and stream until
+    release_workspaces() (a captured call: one of its own)."""
     guard = _guard(cache._index, stream)
     if guard is not None:
         with guard:
@@ -854,12 +867,10 @@ def _attn_decode(cache, q, table, lens, prefix, n_prefix, scale, out, workspace,
             # a graph may replay beside other work of the stream it was captured on: from its pool
             code = call(torch.empty(nbytes or 16, dtype=_u8, device=cache.device), nbytes)
         else:
-            # one per cache and stream, whose calls run one after the other; the lock keeps the
-            # launches of two threads' calls from mixing
-            with cache._ws_lock:
-                ws = cache._ws.get(handle)
+            with _kept_lock:
+                ws = _kept.get((index, handle))
                 if ws is None or ws.numel() < nbytes:
-                    ws = cache._ws[handle] = torch.empty(nbytes or 16, dtype=_u8, device=cache.device)
+                    ws = _kept[index, handle] = torch.empty(nbytes or 16, dtype=_u8, device=cache.device)
                 code = call(ws, nbytes)
     if code:
         raise Edge0Error(code, "edge0_attn_decode")
