@@ -69,10 +69,12 @@ def test_small_queries_over_own_contexts(bits, D, H, G, size):
 
 # (bits, D, H, G, sequences): from so many query rows per K/V head on the prefix runs on the fifth-generation tensor cores
 PREFIX = [(4, 64, 1, 8, 9), (4, 128, 2, 4, 6), (4, 256, 1, 16, 3), (8, 64, 1, 8, 9), (8, 128, 2, 4, 6), (8, 256, 1, 16, 3)]
+# fewer rows: the kernel of the own contexts, 8, 16 and 32 rows at a time
+FEW = [(4, 64, 1, 4, 2), (8, 128, 1, 4, 3), (4, 128, 1, 4, 1), (8, 64, 1, 16, 1), (4, 64, 1, 8, 5), (8, 64, 1, 16, 3), (4, 256, 1, 8, 3)]
 
 
 @pytest.mark.parametrize("size", [1e-3, 1e-4, 1e-5, 1e-6])
-@pytest.mark.parametrize("bits,D,H,G,B", PREFIX + [(4, 64, 1, 4, 2), (8, 128, 1, 4, 3)])
+@pytest.mark.parametrize("bits,D,H,G,B", PREFIX + FEW)
 def test_small_queries_over_a_shared_prefix(bits, D, H, G, B, size):
     """As above; K's mean over each 64 dims is far from zero, so that the queries' sums count."""
     rng = np.random.default_rng(D + G)
@@ -154,7 +156,7 @@ def test_large_values_without_weight_in_own_contexts(bits, D, H, G, size):
 
 
 @pytest.mark.parametrize("size", [1.0, 1e-2, 1e-3, 1e-4])
-@pytest.mark.parametrize("bits,D,H,G,B", PREFIX + [(4, 64, 1, 4, 2), (8, 128, 1, 4, 3)])
+@pytest.mark.parametrize("bits,D,H,G,B", PREFIX + FEW)
 def test_large_values_without_weight_in_a_shared_prefix(bits, D, H, G, B, size):
     """As above, in the prefix (pages 0 to 12, in any order) and in the sequences' own tokens behind it."""
     rng = np.random.default_rng(D + G + bits)
@@ -169,7 +171,7 @@ def test_large_values_without_weight_in_a_shared_prefix(bits, D, H, G, B, size):
         assert (err <= bound).all(), (b, (err / bound).max())
 
 
-@pytest.mark.parametrize("bits,D,H,G,B", PREFIX + [(4, 128, 1, 4, 1), (8, 64, 1, 16, 1)])
+@pytest.mark.parametrize("bits,D,H,G,B", PREFIX + FEW)
 def test_zero_and_constant_groups_beside_large_values(bits, D, H, G, B):
     """Groups of zeros (a whole tile of them first) and constant ones beside tokens of every size."""
     rng = np.random.default_rng(D * bits + B)
