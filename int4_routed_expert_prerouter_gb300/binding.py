@@ -794,17 +794,25 @@ def attn_workspace_bytes(cache: KVCache, B: int, n_q_heads: int) -> int:
     return n
 
 
-# Workspaces of attention calls that bring none: one per device and stream, for all caches (a model
-# has a cache per layer, and its calls run one after the other); the lock keeps the launches of two
-# threads' calls from mixing.
-_kept, _kept_lock = {}, threading.Lock()
+class _Kept:
+    """The workspace of a device's stream for attention calls that bring none, for all caches (a model
+    has one per layer, and its calls run one after the other); the lock keeps the launches of two
+    threads' calls from mixing."""
+    __slots__ = ("lock", "ws", "nbytes")
+
+    def __init__(self):
+        self.lock, self.ws, self.nbytes = threading.Lock(), None, -1
+
+
+_kept = {}          # (device, stream) -> _Kept
 
 
 def release_workspaces():
     """Give back the workspaces kept for attention calls without one (each as large as the largest
     call on its stream needed); a later call makes a new one.  Calls under way are not disturbed."""
-    with _kept_lock:
-        _kept.clear()
+    for kept in list(_kept.values()):
+        with kept.lock:
+            kept.ws, kept.nbytes = None, -1
 
 
 def attn_decode(cache: KVCache, q: torch.Tensor, table, lens, prefix=None, n_prefix=0, scale=None, out=None,
@@ -867,11 +875,11 @@ def _attn_decode(cache, q, table, lens, prefix, n_prefix, scale, out, workspace,
             # a graph may replay beside other work of the stream it was captured on: from its pool
             code = call(torch.empty(nbytes or 16, dtype=_u8, device=cache.device), nbytes)
         else:
-            with _kept_lock:
-                ws = _kept.get((index, handle))
-                if ws is None or ws.numel() < nbytes:
-                    ws = _kept[index, handle] = torch.empty(nbytes or 16, dtype=_u8, device=cache.device)
-                code = call(ws, nbytes)
+            kept = _kept.get((index, handle)) or _kept.setdefault((index, handle), _Kept())
+            with kept.lock:
+                if kept.nbytes < nbytes:
+                    kept.ws, kept.nbytes = torch.empty(nbytes or 16, dtype=_u8, device=cache.device), nbytes
+                code = call(kept.ws, nbytes)
     if code:
         raise Edge0Error(code, "edge0_attn_decode")
     return out
