@@ -406,9 +406,9 @@ void edge0_pool_destroy(edge0_pool* pool);
  * The pages' decoder block has, besides the MoE part, int4 projections (attention and
  * linear-attention projections are int4 and LoRA targets, S3.3) and a KV cache whose
  * growth they name.  These calls are its GB300 form for up to EDGE0_MAX_BATCHED
- * sequences.  They synchronise nothing, keep no state (but the limit of their waits), copy nothing from the host and
- * may be captured into a CUDA graph (lengths, positions and page tables are read on
- * the device at each replay).
+ * sequences.  They synchronise nothing, keep no state (but the limit of their waits), copy
+ * nothing from the host and may be captured into a CUDA graph (lengths, positions and
+ * page tables are read on the device at each replay).
  *
  * Limits: head_dim 64, 128 or 256; bits 4 or 8; page_tokens a multiple of 16 up to
  * EDGE0_MAX_PAGE_TOKENS; other values return EDGE0_EUNSUPPORTED. */
@@ -420,10 +420,11 @@ enum {
     EDGE0_MAX_PREFIX = 1 << 30      /* tokens of a shared prefix */
 };
 
-/* Limit, in ns, of each wait for a copy inside the projection and attention kernels launched (or
- * captured) from now on, by any thread of the process; 2 s unless set.  0: every wait counts as run out
- * at once.  A wait that runs out is given up: rows that lack weights or tokens for it get NaN, and
- * the attention calls record EDGE0_ETIMEOUT in *status. */
+/* Limit, in ns, of each wait for a copy or a matrix step inside the projection and attention
+ * kernels launched (or captured) from now on, by any thread of the process; 2 s unless set.
+ * 0: every wait counts as run out at once.  A wait that runs out is given up: rows that
+ * lack weights or tokens for it get NaN, and the attention calls record EDGE0_ETIMEOUT in
+ * *status. */
 void edge0_block_set_wait_limit(unsigned long long wait_ns);
 
 /* Dense int4 projection [S2, S3.1: the int4 affine group-64 format]: y[b] = W x[b],
@@ -431,7 +432,8 @@ void edge0_block_set_wait_limit(unsigned long long wait_ns);
  * edge0_lora_delta.  x: B rows of `in` fp16, ldx elements apart (16-byte aligned, ldx a
  * multiple of 8, ldx >= in); y: B rows of `out` fp16, ldy apart (ldy >= out; what lies
  * between the rows is not touched).  in % 64 == 0, out any, both up to EDGE0_MAX_LINEAR;
- * 1 <= B <= EDGE0_MAX_BATCHED.  fp32 sums, rounded once.  x and y may not overlap. */
+ * 1 <= B <= EDGE0_MAX_BATCHED.  fp32 sums per group of s sum(q x) + b sum(x), rounded once at
+ * the end (so that an infinity in x[b] mostly gives NaN).  x and y may not overlap. */
 int edge0_q4_linear(const void* packed, int out, int in, const uint16_t* x, long long ldx, int B,
                     uint16_t* y, long long ldy, cudaStream_t stream);
 
@@ -484,12 +486,14 @@ int edge0_kv_read(const edge0_kv_cache* cache, const int32_t* table, int B, int 
  * lens [B], table [B][W], prefix: device int32; n_prefix <= EDGE0_MAX_PREFIX, W: host;
  * 0 < scale <= 1e6.
  * A sequence without any token gets zeros; lens[b] < 0 marks a padding row, whose
- * output is left as it was.  lens[b] above W * page_tokens (cut there) and pages
- * outside [0, n_pages) (page 0 is read in their place) are recorded as EDGE0_EINVAL in
- * *status as above, a wait that ran out as EDGE0_ETIMEOUT (its rows get NaN).  workspace: scratch of edge0_attn_workspace_bytes (16-byte aligned,
- * not cleared beforehand, nothing kept in it); calls that may overlap on the GPU, or whose
- * launches threads may mix on one stream, need one each.  The result does not depend
- * on the timing of the run. */
+ * output is left as it was.  Scores, softmax statistics and sums are fp32; the softmax
+ * weight times V's scale is rounded to fp16 (2^-11 of its term) before it meets V's codes.
+ * lens[b] above W * page_tokens (cut there) and pages outside [0, n_pages) (page 0 is read
+ * in their place) are recorded as EDGE0_EINVAL in *status as above, a wait that ran out as
+ * EDGE0_ETIMEOUT (its rows get NaN).  workspace: scratch of edge0_attn_workspace_bytes
+ * (16-byte aligned, not cleared beforehand, nothing kept in it); calls that may overlap on
+ * the GPU, or whose launches threads may mix on one stream, need one each.  The result does
+ * not depend on the timing of the run. */
 size_t edge0_attn_workspace_bytes(const edge0_kv_cache* cache, int B, int n_q_heads);
 int edge0_attn_decode(const edge0_kv_cache* cache, const uint16_t* q, long long ldq, int B, int n_q_heads,
                       const int32_t* table, int W, const int32_t* lens, const int32_t* prefix,

@@ -35,11 +35,11 @@
 // term on, and e stays out of that sum, so that neither is lost to the other's magnitude.
 //
 // The floor is the pages' bytes.  Measured: four sequences of 100,003 to 131,072 tokens, 8 K/V
-// heads of 128 dims at 4 bits, 115 us, 549 MB at 4.8 TB/s, 0.70 of what a copy reaches: what
+// heads of 128 dims at 4 bits, 112.5 us, 549 MB at 4.9 TB/s, 0.72 of what a copy reaches: what
 // bounds it are the instructions that unpack the codes and take care of scales (64 % of the issue
 // slots, 61 % of the integer and half-precision pipe); the matrix pipe is a quarter taken.
 // Four CTAs of four warps per SM (128 registers each); with three, and query fragments read
-// from shared memory, 133 us.  One sequence of 777 tokens 10.2 us: two launches and
+// from shared memory, 133 us.  One sequence of 777 tokens 10.5 us: two launches and
 // the reads that wait for one another (length, page, codes; shares, sums, parts).
 //
 // ldmatrix delivers K codes as A fragments and, transposed, V codes with the
