@@ -477,6 +477,63 @@ int edge0_kv_read(const edge0_kv_cache* cache, const int32_t* table, int B, int 
                   const int32_t* cu_rows, int T, uint16_t* k, uint16_t* v, int* status,
                   cudaStream_t stream);
 
+/* Moves inside the pages (codes and (s, b) pairs as they are, nothing is rounded).
+ *
+ * edge0_kv_compact: rows kept by a sequence drawn together, as after drafted tokens have been
+ *   accepted in part, or tokens of a context dropped.  Row r of the call (sequences, table, start,
+ *   cu_rows, T as in edge0_kv_append) is copied from the sequence's position src[r] to its position
+ *   start[b] + r - cu_rows[b], with the result as if all rows were read before any is written.  src [T]: device
+ *   int32, src[r] >= the position it goes to (equal: nothing to do); one below it, a position at or behind
+ *   W * page_tokens and a page outside [0, n_pages) are recorded as EDGE0_EINVAL in *status
+ *   and that row left alone.  No page that a sequence of the call writes may be read or written by
+ *   another one of it.
+ * edge0_kv_copy_pages: page src[i] copied to page dst[i] for i < n (device int32), as for a
+ *   sequence that goes on from another's context with pages of its own.  Entries with a negative src or
+ *   dst are skipped; ones at or above n_pages are recorded as EDGE0_EINVAL and skipped.  The pages
+ *   written have to be different from one another and from those read (but for src[i] == dst[i]). */
+int edge0_kv_compact(const edge0_kv_cache* cache, const int32_t* table, int B, int W, const int32_t* start,
+                     const int32_t* src, const int32_t* cu_rows, int T, int* status, cudaStream_t stream);
+int edge0_kv_copy_pages(const edge0_kv_cache* cache, const int32_t* src, const int32_t* dst, int n, int* status,
+                        cudaStream_t stream);
+
+/* Rotary positions: of each head's first rot_dim dims the pairs (i, i + rot_dim / 2)
+ * (EDGE0_ROPE_HALF) or (2 i, 2 i + 1) (EDGE0_ROPE_INTERLEAVED), i < rot_dim / 2, at position n
+ *   (a, b) -> m (a cos(n f_i) - b sin(n f_i), a sin(n f_i) + b cos(n f_i));
+ * the other dims stay as they are.
+ *
+ * edge0_rope_turns (HOST): the frequencies f_i from base^(-2 i / rot_dim) and a scaling for long
+ *   contexts, by `factor` >= 1 where there is one:
+ *     EDGE0_ROPE_PLAIN   as they are
+ *     EDGE0_ROPE_LINEAR  all divided by factor
+ *     EDGE0_ROPE_BASE    base times factor^(rot_dim / (rot_dim - 2)): the slowest pair's divided by factor
+ *     EDGE0_ROPE_RAMP    between f_i and f_i / factor by the pair's number: unchanged up to the pair that turns
+ *                        `high` times over trained_len tokens, f_i / factor from the one that turns `low` times on,
+ *                        linear between (both pair numbers rounded outwards); m = 1 + 0.1 ln(factor)
+ *     EDGE0_ROPE_BANDS   between f_i and f_i / factor by the turns t of the pair over trained_len tokens:
+ *                        f_i from t >= high on, f_i / factor for t <= low, linear in t between
+ *   m = 1 but for RAMP.  turns [rot_dim / 2] receives f_i / (2 pi) 2^64, the fraction of a turn per
+ *   position that edge0_rope takes; radians [rot_dim / 2] f_i itself, or NULL.  Frequencies of a caller's own
+ *   go straight into such a table.
+ * edge0_rope: q and (n_k_heads > 0) k, rows of n heads * head_dim fp16, ld elements apart (16-byte
+ *   aligned, multiples of 8), into q_out and k_out (the input itself, with the same ld, or memory that does
+ *   not overlap it).  Rows, start and cu_rows as in edge0_kv_append (any number of rows and
+ *   positions without cu_rows); rows outside the sequences and of sequences with
+ *   start[b] < 0 are left alone.  turns: DEVICE (8-byte aligned).  head_dim a multiple of 8 up to 512,
+ *   rot_dim even.  Angles are exact to a turn's 2^-53 times the position, cosines, sines and sums
+ *   fp32, rounded once.  backward: the transpose instead (angles negated, m kept), which takes the
+ *   gradient of the outputs to that of the inputs. */
+enum { EDGE0_ROPE_HALF = 0, EDGE0_ROPE_INTERLEAVED = 1 };
+enum { EDGE0_ROPE_PLAIN = 0, EDGE0_ROPE_LINEAR = 1, EDGE0_ROPE_BASE = 2, EDGE0_ROPE_RAMP = 3, EDGE0_ROPE_BANDS = 4 };
+typedef struct {
+    int rot_dim, scaling;
+    double base, factor, trained_len, low, high;
+} edge0_rope_spec;
+int edge0_rope_turns(const edge0_rope_spec* spec, unsigned long long* turns, double* radians, float* magnitude);
+int edge0_rope(const unsigned long long* turns, int head_dim, int rot_dim, int layout, float magnitude, int backward,
+               const uint16_t* q, long long ldq, int n_q_heads, uint16_t* q_out, long long ldqo, const uint16_t* k,
+               long long ldk, int n_k_heads, uint16_t* k_out, long long ldko, int T, const int32_t* start,
+               const int32_t* cu_rows, int B, cudaStream_t stream);
+
 /* Decode attention, one query token per sequence, over keys and values
  *   [the shared prefix: positions [0, n_prefix) of the pages `prefix`] then
  *   [the sequence's own: positions [0, lens[b]) of the pages table[b]],

@@ -82,6 +82,11 @@ class KvCacheDesc(C.Structure):
                 ("page_tokens", C.c_int), ("n_pages", C.c_int), ("pages", P)]
 
 
+class RopeSpec(C.Structure):
+    _fields_ = [("rot_dim", C.c_int), ("scaling", C.c_int), ("base", C.c_double), ("factor", C.c_double),
+                ("trained_len", C.c_double), ("low", C.c_double), ("high", C.c_double)]
+
+
 def _declare(L):
     L.edge0_status_string.argtypes = [C.c_int]
     L.edge0_status_string.restype = C.c_char_p
@@ -144,13 +149,18 @@ def _declare(L):
     L.edge0_attn_workspace_bytes.restype = C.c_size_t
     L.edge0_attn_decode.argtypes = [C.POINTER(KvCacheDesc), P, C.c_longlong, C.c_int, C.c_int, P, C.c_int, P, P,
                                     C.c_int, C.c_float, P, C.c_longlong, P, P, C.c_size_t, P]
+    L.edge0_kv_compact.argtypes = [C.POINTER(KvCacheDesc), P, C.c_int, C.c_int, P, P, P, C.c_int, P, P]
+    L.edge0_kv_copy_pages.argtypes = [C.POINTER(KvCacheDesc), P, P, C.c_int, P, P]
+    L.edge0_rope_turns.argtypes = [C.POINTER(RopeSpec), P, P, C.POINTER(C.c_float)]
+    L.edge0_rope.argtypes = [P, C.c_int, C.c_int, C.c_int, C.c_float, C.c_int, P, C.c_longlong, C.c_int, P, C.c_longlong,
+                             P, C.c_longlong, C.c_int, P, C.c_longlong, C.c_int, P, P, C.c_int, P]
     for name in ("edge0_pack_q4_gate_up", "edge0_pack_q4_down", "edge0_pack_q4_rows", "edge0_pack_f16",
                  "edge0_pack_f16_kmajor", "edge0_pack_cols_T", "edge0_state_init",
                  "edge0_state_error", "edge0_prerouter_topk", "edge0_moe_int4_forward",
                  "edge0_lora_delta", "edge0_decode_layer", "edge0_decode_step",
                  "edge0_moe_int4_forward_noalloc", "edge0_state_set_wait_limit", "edge0_noalloc_error",
                  "edge0_prefill", "edge0_tc_gemm_f16", "edge0_q4_linear", "edge0_kv_append", "edge0_kv_read",
-                 "edge0_attn_decode"):
+                 "edge0_attn_decode", "edge0_kv_compact", "edge0_kv_copy_pages", "edge0_rope_turns", "edge0_rope"):
         getattr(L, name).restype = C.c_int
 
 
@@ -166,7 +176,7 @@ EXPORTED = ["edge0_status_string", "edge0_q4_gate_up_packed_bytes", "edge0_pack_
             "edge0_pool_prefetch_async", "edge0_pool_wait", "edge0_pool_inject", "edge0_pool_stats_ex", "edge0_pool_stats",
             "edge0_pool_resident", "edge0_pool_destroy", "edge0_q4_linear", "edge0_kv_page_bytes",
             "edge0_kv_append", "edge0_kv_read", "edge0_attn_workspace_bytes", "edge0_attn_decode",
-            "edge0_block_set_wait_limit"]
+            "edge0_block_set_wait_limit", "edge0_kv_compact", "edge0_kv_copy_pages", "edge0_rope_turns", "edge0_rope"]
 
 
 def status_string(code: int) -> str:
@@ -787,6 +797,50 @@ def _kv_read(cache, table, start, cu_rows, T, k, v, stream):
     return k, v
 
 
+def kv_compact(cache: KVCache, table, start, src, cu_rows=None, stream=None):
+    """Draw kept rows of the cache together: row r of sequence b moves from its position
+    src[r] to start[b] + r - cu_rows[b] (rows as in kv_append), codes as they are, as if all were read
+    before any is written.  src [T] int32 on the device, src[r] at or behind the place it goes to."""
+    guard = _guard(cache._index, stream)
+    if guard is not None:
+        with guard:
+            return _kv_compact(cache, table, start, src, cu_rows, stream)
+    return _kv_compact(cache, table, start, src, cu_rows, None)
+
+
+def _kv_compact(cache, table, start, src, cu_rows, stream):
+    T = src.numel()
+    tb, B, W, st, cu = _sequences(cache, table, start, cu_rows, T, "kv_compact")
+    sp = _ints(src, cache._index, T, "kv_compact: src")
+    if T == 0:
+        return
+    code = _lib.edge0_kv_compact(cache._desc, tb, B, W, st, sp, cu, T, cache._status, _raw_stream(cache._index, stream))
+    if code:
+        raise Edge0Error(code, "edge0_kv_compact")
+
+
+def kv_copy_pages(cache: KVCache, src, dst, stream=None):
+    """Copy pages src[i] to pages dst[i] (int32 on the device; entries with a negative number
+    ask for nothing).  The pages written differ from one another and from those read."""
+    guard = _guard(cache._index, stream)
+    if guard is not None:
+        with guard:
+            return _kv_copy_pages(cache, src, dst, stream)
+    return _kv_copy_pages(cache, src, dst, None)
+
+
+def _kv_copy_pages(cache, src, dst, stream):
+    n, index = src.numel(), cache._index
+    if n > _INT_MAX:
+        raise Edge0Error(EDGE0_EUNSUPPORTED, "kv_copy_pages: pages beyond 2^31 - 1")
+    sp, dp = _ints(src, index, n, "kv_copy_pages: src"), _ints(dst, index, n, "kv_copy_pages: dst")
+    if n == 0:
+        return
+    code = _lib.edge0_kv_copy_pages(cache._desc, sp, dp, n, cache._status, _raw_stream(index, stream))
+    if code:
+        raise Edge0Error(code, "edge0_kv_copy_pages")
+
+
 def attn_workspace_bytes(cache: KVCache, B: int, n_q_heads: int) -> int:
     n = cache._ws_bytes.get((B, n_q_heads))
     if n is None:
@@ -883,3 +937,92 @@ def _attn_decode(cache, q, table, lens, prefix, n_prefix, scale, out, workspace,
     if code:
         raise Edge0Error(code, "edge0_attn_decode")
     return out
+
+
+# ------------------------------------------------------- rotary positions ----
+_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+_ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
+
+
+class RopePlan:
+    """Frequencies of rotary positions on a GPU (edge0_rope_turns): the first rot_dim of head_dim
+    dims turn, in pairs (i, i + rot_dim / 2) ("half") or (2 i, 2 i + 1) ("interleaved").
+    scaling, for contexts `factor` times as long as the trained one: "plain" (none), "linear",
+    "base", "ramp" (trained_len; low, high: turns over it between which it acts) or "bands"
+    (likewise).  magnitude: of the outputs, the scaling's own unless given.  radians: frequencies per
+    position of the caller's own, [rot_dim / 2] between 0 and pi, instead of base and scaling."""
+
+    def __init__(self, head_dim: int, rot_dim=None, base=10000.0, layout="half", scaling="plain", factor=1.0,
+                 trained_len=0.0, low=0.0, high=0.0, magnitude=None, radians=None, device="cuda"):
+        rot_dim = head_dim if rot_dim is None else rot_dim
+        if layout not in _ROPE_LAYOUTS or scaling not in _ROPE_SCALINGS:
+            raise _bad("RopePlan: layout half or interleaved; scaling " + ", ".join(_ROPE_SCALINGS))
+        if rot_dim < 2 or rot_dim % 2 or rot_dim > head_dim:
+            raise _bad("RopePlan: rot_dim even, from 2 to head_dim")
+        if head_dim % 8 or head_dim > 512:
+            raise Edge0Error(EDGE0_EUNSUPPORTED, "RopePlan: head_dim a multiple of 8 up to 512")
+        self.head_dim, self.rot_dim, self.layout = head_dim, rot_dim, _ROPE_LAYOUTS[layout]
+        turns, own = np.empty(rot_dim // 2, np.uint64), C.c_float(1.0)
+        if radians is None:
+            self.radians = np.empty(rot_dim // 2, np.float64)
+            spec = RopeSpec(rot_dim, _ROPE_SCALINGS[scaling], base, factor, trained_len, low, high)
+            _check(lib().edge0_rope_turns(C.byref(spec), turns.ctypes.data, self.radians.ctypes.data, C.byref(own)), "edge0_rope_turns")
+        else:
+            self.radians = np.array(radians, np.float64).reshape(-1)
+            if self.radians.shape != (rot_dim // 2,) or not ((self.radians >= 0) & (self.radians <= np.pi)).all():
+                raise _bad("RopePlan: radians [rot_dim / 2], from 0 to pi per position")
+            turns[:] = np.rint(self.radians / (2 * np.pi) * 2.0 ** 64).astype(np.uint64)
+        self.magnitude = float(own.value if magnitude is None else magnitude)
+        if not 0 < self.magnitude < float("inf"):
+            raise _bad("RopePlan: magnitude")
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        if not self.turns.is_cuda:
+            raise _bad("RopePlan: a GPU as device")
+        self._index = self.turns.get_device()
+
+
+def rope(plan: RopePlan, q: torch.Tensor, k, start, cu_rows=None, q_out=None, k_out=None, backward=False, stream=None):
+    """Rotary positions on q [T, n_q_heads, head_dim] and k [T, n_k_heads, head_dim] (or None),
+    fp16, which may be slices of wider rows; returns both.  Row r of sequence b stands at position
+    start[b] + r - cu_rows[b] (cu_rows None: row r at position start[r]).  q_out, k_out: rows to fill (q and k
+    themselves to turn them in place) or None for new ones; rows of no sequence or of one with
+    start[b] < 0 are left as they are.  backward: the transpose, from the outputs' gradients to the inputs'."""
+    guard = _guard(plan._index, stream)
+    if guard is not None:
+        with guard:
+            return _rope(plan, q, k, start, cu_rows, q_out, k_out, backward, stream)
+    return _rope(plan, q, k, start, cu_rows, q_out, k_out, backward, None)
+
+
+def _rope(plan, q, k, start, cu_rows, q_out, k_out, backward, stream):
+    index, args, outs, T = plan._index, [], [], q.shape[0]
+    for x, o in ((q, q_out), (k, k_out)):
+        if x is None:
+            args += [None, 0, 0, None, 0]
+            outs.append(None)
+            continue
+        if x.dim() != 3 or x.shape[0] != T or x.shape[2] != plan.head_dim or x.get_device() != index:
+            raise _bad("rope: q and k [T, heads, head_dim] beside the plan")
+        ldx, heads = _row_stride(x, "rope: q, k"), x.shape[1]
+        if o is None:
+            o, ldo = torch.empty(x.shape, dtype=_f16, device=x.device), heads * plan.head_dim
+        else:
+            if o.shape != x.shape or o.get_device() != index:
+                raise _bad("rope: outputs like q and k")
+            ldo = _row_stride(o, "rope: outputs")
+        args += [x.data_ptr(), ldx, heads, o.data_ptr(), ldo]
+        outs.append(o)
+    B = start.numel()
+    if cu_rows is None and T != B:
+        raise _bad("rope: one position per row without cu_rows")
+    if B > _INT_MAX or T > _INT_MAX:
+        raise Edge0Error(EDGE0_EUNSUPPORTED, "rope: rows or sequences beyond 2^31 - 1")
+    st = _ints(start, index, B, "rope: start")
+    cu = None if cu_rows is None else _ints(cu_rows, index, B + 1, "rope: cu_rows")
+    if T:
+        code = _lib.edge0_rope(plan.turns.data_ptr(), plan.head_dim, plan.rot_dim, plan.layout, plan.magnitude, bool(backward),
+                               args[0], args[1], args[2], args[3], args[4], args[5], args[6], args[7], args[8], args[9],
+                               T, st, cu, B, _raw_stream(index, stream))
+        if code:
+            raise Edge0Error(code, "edge0_rope")
+    return outs[0], outs[1]
