@@ -557,6 +557,25 @@ int edge0_attn_decode(const edge0_kv_cache* cache, const uint16_t* q, long long 
                       int n_prefix, float scale, uint16_t* out, long long ldo, int* status,
                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* Causal attention of packed prompts.  q: T rows of n_q_heads * head_dim fp16, k and v: Tk rows of
+ * n_kv_heads * head_dim, out like q; ldq, ldk, ldv, ldo elements apart (16-byte aligned,
+ * multiples of 8).  Sequence b has the rows [cu_rows[b], cu_rows[b + 1]) and the keys
+ * [cu_keys[b], cu_keys[b + 1]) (both [B + 1], non-decreasing, within [0, T] and [0, Tk]; cu_keys NULL: T == Tk,
+ * keys as rows); its rows are the last n_q of its n_k tokens: row i sees the keys j <= i + n_k - n_q,
+ *   o[i, h] = sum_j softmax_j(scale q[i, h] . k_j) v_j with K/V head h / (n_q_heads / n_kv_heads).
+ * A row that sees no key gets zeros; rows that no sequence has are left as they were.  What
+ * a row does not see has no influence on it, infinities and NaN included.  Scores, softmax statistics and sums
+ * are fp32; a weight is rounded to fp16 (2^-11 of itself) before it meets v.  head_dim 64, 128 or 256;
+ * 1 <= B <= EDGE0_MAX_BATCHED; 0 < scale <= 1e6; T * heads per K/V head below 2^31 - 512 and Tk up to 2^30, else EDGE0_EUNSUPPORTED.
+ * A wait that runs out gives the rows that lack something NaN.  workspace: scratch of
+ * edge0_attn_prompt_workspace_bytes (0: width not supported), as for edge0_attn_decode.  The result does not
+ * depend on the timing of the run. */
+size_t edge0_attn_prompt_workspace_bytes(int head_dim);
+int edge0_attn_prompt(const uint16_t* q, long long ldq, int T, int n_q_heads, const uint16_t* k, long long ldk,
+                      const uint16_t* v, long long ldv, int Tk, int n_kv_heads, int head_dim, const int32_t* cu_rows,
+                      const int32_t* cu_keys, int B, float scale, uint16_t* out, long long ldo, void* workspace,
+                      size_t workspace_bytes, cudaStream_t stream);
+
 /* ---- allocation-free variant (the paper has no counterpart to this call) ----
  * edge0_moe_int4_forward for callers that cannot allocate memory: code running
  * in an allocator-free part of a serving loop, code whose memory budget was fixed

@@ -149,6 +149,10 @@ def _declare(L):
     L.edge0_attn_workspace_bytes.restype = C.c_size_t
     L.edge0_attn_decode.argtypes = [C.POINTER(KvCacheDesc), P, C.c_longlong, C.c_int, C.c_int, P, C.c_int, P, P,
                                     C.c_int, C.c_float, P, C.c_longlong, P, P, C.c_size_t, P]
+    L.edge0_attn_prompt_workspace_bytes.argtypes = [C.c_int]
+    L.edge0_attn_prompt_workspace_bytes.restype = C.c_size_t
+    L.edge0_attn_prompt.argtypes = [P, C.c_longlong, C.c_int, C.c_int, P, C.c_longlong, P, C.c_longlong, C.c_int, C.c_int, C.c_int,
+                                    P, P, C.c_int, C.c_float, P, C.c_longlong, P, C.c_size_t, P]
     L.edge0_kv_compact.argtypes = [C.POINTER(KvCacheDesc), P, C.c_int, C.c_int, P, P, P, C.c_int, P, P]
     L.edge0_kv_copy_pages.argtypes = [C.POINTER(KvCacheDesc), P, P, C.c_int, P, P]
     L.edge0_rope_turns.argtypes = [C.POINTER(RopeSpec), P, P, C.POINTER(C.c_float)]
@@ -160,7 +164,8 @@ def _declare(L):
                  "edge0_lora_delta", "edge0_decode_layer", "edge0_decode_step",
                  "edge0_moe_int4_forward_noalloc", "edge0_state_set_wait_limit", "edge0_noalloc_error",
                  "edge0_prefill", "edge0_tc_gemm_f16", "edge0_q4_linear", "edge0_kv_append", "edge0_kv_read",
-                 "edge0_attn_decode", "edge0_kv_compact", "edge0_kv_copy_pages", "edge0_rope_turns", "edge0_rope"):
+                 "edge0_attn_decode", "edge0_kv_compact", "edge0_kv_copy_pages", "edge0_rope_turns", "edge0_rope",
+                 "edge0_attn_prompt"):
         getattr(L, name).restype = C.c_int
 
 
@@ -176,7 +181,8 @@ EXPORTED = ["edge0_status_string", "edge0_q4_gate_up_packed_bytes", "edge0_pack_
             "edge0_pool_prefetch_async", "edge0_pool_wait", "edge0_pool_inject", "edge0_pool_stats_ex", "edge0_pool_stats",
             "edge0_pool_resident", "edge0_pool_destroy", "edge0_q4_linear", "edge0_kv_page_bytes",
             "edge0_kv_append", "edge0_kv_read", "edge0_attn_workspace_bytes", "edge0_attn_decode",
-            "edge0_block_set_wait_limit", "edge0_kv_compact", "edge0_kv_copy_pages", "edge0_rope_turns", "edge0_rope"]
+            "edge0_block_set_wait_limit", "edge0_kv_compact", "edge0_kv_copy_pages", "edge0_rope_turns", "edge0_rope",
+            "edge0_attn_prompt_workspace_bytes", "edge0_attn_prompt"]
 
 
 def status_string(code: int) -> str:
@@ -869,6 +875,23 @@ def release_workspaces():
             kept.ws, kept.nbytes = None, -1
 
 
+def _with_workspace(call, workspace, nbytes, index, handle, device, what):
+    """call(workspace, its bytes) with the caller's workspace, else with the one kept for the stream
+    (nbytes of it), else, where a graph is captured, with one of the call's own."""
+    if workspace is not None:
+        if workspace.dtype is not _u8 or workspace.get_device() != index or not workspace.is_contiguous():
+            raise _bad(f"{what}: workspace uint8, contiguous, beside the inputs")
+        return call(workspace, workspace.numel())
+    if torch._C._cuda_isCurrentStreamCapturing():
+        # a graph may replay beside other work of the stream it was captured on: from its pool
+        return call(torch.empty(nbytes or 16, dtype=_u8, device=device), nbytes)
+    kept = _kept.get((index, handle)) or _kept.setdefault((index, handle), _Kept())
+    with kept.lock:
+        if kept.nbytes < nbytes:
+            kept.ws, kept.nbytes = torch.empty(nbytes or 16, dtype=_u8, device=device), nbytes
+        return call(kept.ws, nbytes)
+
+
 def attn_decode(cache: KVCache, q: torch.Tensor, table, lens, prefix=None, n_prefix=0, scale=None, out=None,
                 workspace=None, stream=None) -> torch.Tensor:
     """Attention of one query token per sequence, q [B, n_q_heads, head_dim] fp16, over
@@ -919,21 +942,8 @@ def _attn_decode(cache, q, table, lens, prefix, n_prefix, scale, out, workspace,
                                       D ** -0.5 if scale is None else scale, out.data_ptr(), ldo, cache._status,
                                       ws.data_ptr(), nbytes, handle)
 
-    if workspace is not None:
-        if workspace.dtype is not _u8 or workspace.get_device() != index or not workspace.is_contiguous():
-            raise _bad("attn_decode: workspace uint8, contiguous, beside the cache")
-        code = call(workspace, workspace.numel())
-    else:
-        nbytes = attn_workspace_bytes(cache, B, Hq)
-        if torch._C._cuda_isCurrentStreamCapturing():
-            # a graph may replay beside other work of the stream it was captured on: from its pool
-            code = call(torch.empty(nbytes or 16, dtype=_u8, device=cache.device), nbytes)
-        else:
-            kept = _kept.get((index, handle)) or _kept.setdefault((index, handle), _Kept())
-            with kept.lock:
-                if kept.nbytes < nbytes:
-                    kept.ws, kept.nbytes = torch.empty(nbytes or 16, dtype=_u8, device=cache.device), nbytes
-                code = call(kept.ws, nbytes)
+    nbytes = attn_workspace_bytes(cache, B, Hq) if workspace is None else 0
+    code = _with_workspace(call, workspace, nbytes, index, handle, cache.device, "attn_decode")
     if code:
         raise Edge0Error(code, "edge0_attn_decode")
     return out
@@ -1026,3 +1036,63 @@ def _rope(plan, q, k, start, cu_rows, q_out, k_out, backward, stream):
         if code:
             raise Edge0Error(code, "edge0_rope")
     return outs[0], outs[1]
+
+
+# ------------------------------------------------- attention of whole prompts ----
+_prompt_ws = {}     # head_dim -> bytes
+
+
+def attn_prompt_workspace_bytes(head_dim: int) -> int:
+    n = _prompt_ws.get(head_dim)
+    if n is None:
+        n = _prompt_ws[head_dim] = int(lib().edge0_attn_prompt_workspace_bytes(head_dim))
+    return n
+
+
+def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows, cu_keys=None, scale=None, out=None, workspace=None,
+                stream=None) -> torch.Tensor:
+    """Causal attention of packed prompts: q [T, n_q_heads, head_dim], k, v [Tk, n_kv_heads, head_dim]
+    fp16, which may be slices of wider rows.  Sequence b has the rows cu_rows[b] to cu_rows[b + 1] of q and
+    the keys cu_keys[b] to cu_keys[b + 1] (cu_keys None: keys as rows); its rows are the last of its
+    tokens, so that row i sees the keys up to i + n_keys - n_rows (none: zeros).  cu_rows, cu_keys [B + 1]: int32 on the
+    device.  scale: 1 / sqrt(head_dim) unless given.  out: rows to fill (those of no sequence are left as
+    they are) or None.  workspace: uint8 of attn_prompt_workspace_bytes, or None for the one kept per device
+    and stream (attn_decode)."""
+    index = q.get_device()
+    guard = _guard(index, stream)
+    if guard is not None:
+        with guard:
+            return _attn_prompt(q, k, v, cu_rows, cu_keys, scale, out, workspace, index, stream)
+    return _attn_prompt(q, k, v, cu_rows, cu_keys, scale, out, workspace, index, None)
+
+
+def _attn_prompt(q, k, v, cu_rows, cu_keys, scale, out, workspace, index, stream):
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[2] != q.shape[2] or k.get_device() != index or v.get_device() != index:
+        raise _bad("attn_prompt: q [T, n_q_heads, head_dim], k and v [Tk, n_kv_heads, head_dim] on one GPU")
+    T, Hq, D = q.shape
+    Tk, H, _ = k.shape
+    ldq, ldk, ldv = _row_stride(q, "attn_prompt: q"), _row_stride(k, "attn_prompt: k"), _row_stride(v, "attn_prompt: v")
+    B = cu_rows.numel() - 1
+    if B < 1:
+        raise _bad("attn_prompt: cu_rows [B + 1]")
+    if T > _INT_MAX or Tk > _INT_MAX or B > _INT_MAX or Hq > _INT_MAX:
+        raise Edge0Error(EDGE0_EUNSUPPORTED, "attn_prompt: rows or sequences beyond 2^31 - 1")
+    cu = _ints(cu_rows, index, B + 1, "attn_prompt: cu_rows")
+    ck = None if cu_keys is None else _ints(cu_keys, index, B + 1, "attn_prompt: cu_keys")
+    if out is None:
+        out, ldo = torch.empty((T, Hq, D), dtype=_f16, device=q.device), Hq * D
+    else:
+        if out.shape != q.shape or out.get_device() != index:
+            raise _bad("attn_prompt: out like q")
+        ldo = _row_stride(out, "attn_prompt: out")
+    L = _lib or lib()
+    handle = _raw_stream(index, stream)
+
+    def call(ws, nbytes):
+        return L.edge0_attn_prompt(q.data_ptr(), ldq, T, Hq, k.data_ptr(), ldk, v.data_ptr(), ldv, Tk, H, D, cu, ck, B,
+                                   D ** -0.5 if scale is None else scale, out.data_ptr(), ldo, ws.data_ptr(), nbytes, handle)
+
+    code = _with_workspace(call, workspace, attn_prompt_workspace_bytes(D) if workspace is None else 0, index, handle, q.device, "attn_prompt")
+    if code:
+        raise Edge0Error(code, "edge0_attn_prompt")
+    return out

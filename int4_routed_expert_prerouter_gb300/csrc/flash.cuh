@@ -1,0 +1,740 @@
+// Attention of many query rows per K/V head on the fifth-generation tensor cores: what attention of
+// packed prompts (attn_prompt.cu) and of drafted tokens over the quantised cache (attn_tree.cu) share.
+//
+//     o_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(scale q_i . k_j) over the tokens j that row i sees.
+//
+// Rows.  A K/V head's query rows of a sequence in the order (token, head of the group): a block
+// of them shares every K and V tile that it reads, whatever the number of query heads per K/V head, and
+// ragged sequences leave at most one block partly empty per K/V head.
+//
+// Streams.  With up to 128 dims a block has two streams, each a softmax warpgroup with a score tile
+// and an accumulator of 128 rows in TMEM (512 columns in all): two row tiles on the same K/V tiles, or, of a
+// block of at most 128 rows, one row tile on alternate K/V tiles, added up at the end.  While one stream's
+// scores become weights the tensor core works for the other.  256 dims: one stream, whose next scores
+// are formed (in a second buffer) while the present ones become weights.
+//
+// Step of a stream.  S = Q K^T (128 x 128) into TMEM; a thread reads its row, takes the maximum, forms the
+// weights 2^(S c - ref + 11) and writes them as fp16 over the scores; O += P V with P from TMEM.  The
+// reference moves only when exceeded by 2^4 (the accumulator is then rescaled in TMEM), so that
+// weights lie within 2^15 and stay normal in fp16 down to 2^-25 of the largest; their rounding, 2^-11 of each,
+// is the only one beside the result's.  Statistics and sums are fp32.
+//
+// Shares.  All blocks of all sequences and heads in a row, each at the cost of the tokens it sees, are cut
+// into equal shares, one per CTA, from lengths read on the device; a cut that falls into a block
+// too small to be worth it moves to the block's edge.  Blocks cut leave parts (reference, sum, fp32 o),
+// which flash_join adds up in the order of the tokens: the same bits on every run.
+#pragma once
+#include "kvcache.cuh"
+#include "launch.cuh"
+#include "tc05.cuh"
+#include "wait.cuh"
+
+namespace edge0 {
+namespace flash {
+
+constexpr int kTile = 128;            // tokens per step
+constexpr int kRowsQ = 128;           // rows of an accumulator
+constexpr int kMaxCtas = 160;         // shares at most (an SM each)
+constexpr int kMinSplit = 8;          // tiles that a block has at least to be cut
+constexpr int kMinShare = 4;          // tiles that a share has at least
+constexpr float kRise = 4.f;          // how far scores may exceed the reference, as a power of two
+constexpr float kUp = 11.f;           // weights are 2^kUp times as large: kRise + kUp = 15
+constexpr int kSoftmax = 256;         // threads of the two softmax warpgroups
+
+template <int D>
+struct Shape {
+    static constexpr int kStreams = D <= 128 ? 2 : 1;
+    static constexpr int kBlock = kStreams * kRowsQ;          // rows of a block
+    static constexpr int kEntry = D == 256 ? 64 : kTile;      // tokens of a ring entry
+    static constexpr int kEntries = kTile / kEntry;           // entries of a K (or V) tile
+    static constexpr int kEntryBytes = kEntry * D * 2;
+    static constexpr int kChunks = D / 64;                    // 128-byte swizzled columns of an operand
+    static constexpr int kQBytes = kRowsQ * D * 2;
+    // TMEM columns: scores (or weights) of a stream or buffer, accumulators behind both
+    static constexpr int kO = 2 * kTile;
+};
+
+// A block, or the place of a cut in it; tile > 0: inside.
+struct Place {
+    int b, h, t, tile;
+};
+__device__ __forceinline__ bool same_block(const Place& x, const Place& y) { return x.b == y.b && x.h == y.h && x.t == y.t; }
+
+// Rows and keys of a sequence: its n_q rows begin at row q0, its n_k keys at k0; its row i sees at most the keys
+// before i + 1 + off; all see those before ctx.
+struct Seq {
+    int q0, n_q, k0, n_k, off, ctx;
+};
+
+struct Item {
+    int b, h;
+    Seq s;
+    int row0, rows;       // (token, head) rows of the block
+    int lo, hi, tiles;    // the share's tiles, all of them
+    int clear;            // tiles that every row sees in whole
+    int part;             // slot of the share's part, -1: the share has the block whole
+
+    template <int D>
+    __device__ __forceinline__ bool pair() const { return Shape<D>::kStreams == 2 && rows > kRowsQ; }
+    // tiles of a stream: all of them, or every other one
+    template <int D>
+    __device__ __forceinline__ int of_stream(int s) const {
+        const int n = hi - lo;
+        return Shape<D>::kStreams == 1 || pair<D>() ? n : (n + 1 - s) >> 1;
+    }
+    template <int D>
+    __device__ __forceinline__ int tile_of(int s, int j) const {
+        return lo + (Shape<D>::kStreams == 1 || pair<D>() ? j : 2 * j + s);
+    }
+};
+
+// ----------------------------------------------------------------- shares ----
+// Costs count a (row of a token's group, token) pair as 1 / block rows of it: a block costs the tokens its last row
+// sees times G, and one tile more.
+template <int R>
+struct Costs {
+    long long per;        // cost of a tile: kTile G
+    long long off, all;   // off G, n_k G
+    int blocks;
+
+    __device__ Costs(const Seq& s, int G) {
+        per = (long long)kTile * G;
+        off = (long long)s.off * G;
+        all = (long long)s.n_k * G;
+        blocks = (int)(((long long)s.n_q * G + R - 1) / R);
+    }
+    __device__ long long tokens(int t) const {        // times G
+        if (t == blocks - 1) return all;
+        const long long v = off + (long long)R * (t + 1);
+        return v < 0 ? 0 : v < all ? v : all;
+    }
+    __device__ long long before(int t) const {        // cost of the blocks 0 .. t - 1, t < blocks
+        long long from = off >= 0 ? 0 : -off / R;     // the first block with off + R (t + 1) > 0
+        if (from > t) from = t;
+        const long long n = t - from;
+        return t * per + n * off + R * ((long long)t * (t + 1) - from * (from + 1)) / 2;
+    }
+    __device__ long long total() const { return blocks ? before(blocks - 1) + per + all : 0; }
+};
+
+// The places of the cuts `first` and first + 1 of the CTAs' shares, by the whole CTA of `threads` >= 256;
+// prefix: [EDGE0_MAX_BATCHED + 1] of scratch.
+template <int D, class Src>
+__device__ void find_share(const Src& p, int cta, int ctas, long long* prefix, Place* out, int threads) {
+    constexpr int R = Shape<D>::kBlock;
+    const int tid = threadIdx.x;
+    long long mine = 0;
+    if (tid < p.B) mine = Costs<R>(p.seq(tid), p.G).total() * p.H;
+    if (tid < EDGE0_MAX_BATCHED) prefix[tid + 1] = mine;
+    __syncthreads();
+    if (tid < 32) {                                   // 8 sequences a lane
+        long long v[8], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = sum += prefix[1 + 8 * tid + i];
+        long long scan = sum;
+#pragma unroll
+        for (int s = 1; s < 32; s *= 2) {
+            const long long o = __shfl_up_sync(0xffffffffu, scan, s);
+            if (tid >= s) scan += o;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) prefix[1 + 8 * tid + i] = v[i] + scan - sum;
+        if (tid == 0) prefix[0] = 0;
+    }
+    __syncthreads();
+    if (tid == 0 || tid == 32) {
+        const long long all = prefix[p.B], least = (long long)kMinShare * kTile * p.G;
+        long long share = (all + ctas - 1) / ctas;
+        if (share < least) share = least;             // (so that two cuts never fall on one tile of a block)
+        const int i = cta + (tid == 32);
+        const long long x = share * i;
+        Place at{p.B, 0, 0, 0};
+        if (x < all) {
+            int lo = 0, hi = p.B;                     // the last b with prefix[b] <= x
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (prefix[mid] <= x) lo = mid;
+                else hi = mid;
+            }
+            const Costs<R> c(p.seq(lo), p.G);
+            const long long head = c.total();
+            long long in = x - prefix[lo];
+            at.b = lo;
+            at.h = (int)(in / head);
+            in -= at.h * head;
+            int t0 = 0, t1 = c.blocks;
+            while (t1 - t0 > 1) {
+                const int mid = (t0 + t1) >> 1;
+                if (c.before(mid) <= in) t0 = mid;
+                else t1 = mid;
+            }
+            at.t = t0;
+            in -= c.before(t0);
+            const long long seen = c.tokens(t0), cost = seen + c.per;
+            const int tiles = (int)((seen + c.per - 1) / c.per);
+            int tile = (int)((in - c.per / 2) / c.per);             // the nearest, less the block's own cost
+            if (in < c.per) tile = 0;
+            if (tiles < kMinSplit || cost * 8 <= share) tile = 2 * in > cost ? tiles : 0;
+            if (tile >= tiles && tile > 0) {          // the next block's start
+                tile = 0;
+                if (++at.t == c.blocks) {
+                    at.t = 0;
+                    if (++at.h == p.H) {
+                        at.h = 0;
+                        do ++at.b;
+                        while (at.b < p.B && prefix[at.b + 1] == prefix[at.b]);
+                    }
+                }
+            }
+            at.tile = tile;
+        }
+        out[tid == 32] = at;
+    }
+    __syncthreads();
+}
+
+// Goes through a share's blocks.
+template <int D, class Src>
+struct Walk {
+    const Src& p;
+    Place at, end;
+    Seq s;
+    int blocks, cta;
+    bool inside;          // the share begins inside a block
+
+    __device__ Walk(const Src& p, const Place* cut, int cta) : p(p), at(cut[0]), end(cut[1]), cta(cta), inside(cut[0].tile > 0) { enter(); }
+    __device__ void enter() {
+        while (at.b < p.B) {
+            s = p.seq(at.b);
+            blocks = (int)(((long long)s.n_q * p.G + Shape<D>::kBlock - 1) / Shape<D>::kBlock);
+            if (blocks) break;
+            ++at.b;
+        }
+    }
+    // the next piece of work; false: none is left
+    __device__ bool next(Item& x) {
+        for (;;) {
+            const bool last = same_block(at, end);
+            if (at.b >= p.B || (last && end.tile <= at.tile)) return false;
+            if (at.b > end.b || (at.b == end.b && (at.h > end.h || (at.h == end.h && at.t > end.t)))) return false;
+            constexpr int R = Shape<D>::kBlock;
+            const int all = s.n_q * p.G;
+            x.b = at.b;
+            x.h = at.h;
+            x.s = s;
+            x.row0 = at.t * R;
+            x.rows = min(R, all - x.row0);
+            const int seen = p.seen(s, (x.row0 + x.rows - 1) / p.G);
+            x.tiles = (seen + kTile - 1) / kTile;
+            x.clear = p.seen_by_all(s, x.row0 / p.G) / kTile;
+            x.lo = min(at.tile, x.tiles);
+            x.hi = last ? min(end.tile, x.tiles) : x.tiles;
+            const bool from = at.tile > 0;
+            x.part = x.lo == 0 && !last ? -1 : 2 * cta + (from ? 0 : 1);
+            if (last) {
+                at.tile = end.tile;
+            } else {
+                at.tile = 0;
+                if (++at.t == blocks) {
+                    at.t = 0;
+                    if (++at.h == p.H) {
+                        at.h = 0;
+                        ++at.b;
+                        enter();
+                    }
+                }
+            }
+            return true;
+        }
+    }
+};
+
+// ----------------------------------------------------- matrix steps, TMEM ----
+// A 128-byte-swizzled operand: columns of 64 values (128 bytes) of all rows, one after the other; the 16-byte
+// piece c of row r of a column lies at piece c ^ (r & 7).
+__device__ __forceinline__ uint32_t swizzled(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); }
+
+// Descriptors of such operands; the low word advances with the address.  K-major: 8-row blocks 1024
+// bytes apart.  MN-major (rows are the product's inner dimension): 8-row blocks 1024 bytes
+// apart likewise, columns `apart` bytes.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t apart) { return (saddr >> 4) | ((apart >> 4) << 16); }
+__device__ __forceinline__ uint64_t desc128(uint32_t lo) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"((1024u >> 4) | (1u << 14) | (2u << 29)));
+    return d;
+}
+// Matrix steps and their commit, issued by the lane with `lead` set of a warp that comes here together.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t lead) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t lead) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t lead) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elect() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(r));
+    return r;
+}
+#define EDGE0_R4(r, i) "=r"((r)[i]), "=r"((r)[i + 1]), "=r"((r)[i + 2]), "=r"((r)[i + 3])
+#define EDGE0_I4(r, i) "r"((r)[i]), "r"((r)[i + 1]), "r"((r)[i + 2]), "r"((r)[i + 3])
+// 32 columns of the thread's lane
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : EDGE0_R4(r, 0), EDGE0_R4(r, 4), EDGE0_R4(r, 8), EDGE0_R4(r, 12), EDGE0_R4(r, 16), EDGE0_R4(r, 20), EDGE0_R4(r, 24),
+          EDGE0_R4(r, 28)
+        : "r"(a)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(a),
+        EDGE0_I4(r, 0), EDGE0_I4(r, 4), EDGE0_I4(r, 8), EDGE0_I4(r, 12), EDGE0_I4(r, 16), EDGE0_I4(r, 20), EDGE0_I4(r, 24),
+        EDGE0_I4(r, 28)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// -------------------------------------------------------------------- CTA ----
+constexpr int kMaxStages = 8;
+struct Control {
+    uint64_t full[kMaxStages];      // a ring entry has arrived
+    uint64_t clean[kMaxStages];     // ... and been looked through
+    uint64_t freed[kMaxStages];     // ... and is done with
+    uint64_t q_full[2];             // a stream's queries are in place
+    uint64_t s_full[2];             // scores of a stream (two streams) or a buffer (one)
+    uint64_t p_full[2];             // ... have become weights
+    uint64_t o_step[2];             // one stream: the product with V of a tile of this buffer is done
+    uint64_t o_last[2];             // a stream's last product of a block is done
+    uint64_t drained;
+    Place cut[2];
+    uint32_t tmem;
+    int dead;                       // a wait ran out: nothing more is issued, what is not done becomes NaN
+    int special[kMaxStages * 2];    // numbers of the share's blocks with non-finite V that some rows do not see, by their last bits
+    float2 ml[kRowsQ];              // the second stream's (reference, sum)
+};
+
+// Where a block of the share (numbers from 1, of those with tiles) is marked: whoever looks V through runs no more than the
+// ring's entries ahead.
+__device__ __forceinline__ volatile int& special_of(Control& c, int number) {
+    return *(volatile int*)&c.special[number & (kMaxStages * 2 - 1)];
+}
+// Waits for a phase of a barrier, by a whole warp, which agrees on the answer; gives up after `limit` ns
+// or when another warp did.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, Control& c, unsigned long long limit) {
+    bool ok = !*(volatile int*)&c.dead && mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+        unsigned long long t0, now;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+        while (!ok) {
+            if (*(volatile int*)&c.dead) break;
+            ok = mbar_try_wait(bar, parity);
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+            if (!ok && now - t0 > limit) *(volatile int*)&c.dead = 1;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+    }
+    return ok;
+}
+
+// Place of a tile's first entry in the ring, counted from the block's first: K tiles run `lead` ahead of V's.
+__device__ __forceinline__ int k_entry(int i, int lead) { return i < lead ? i : 2 * i - lead + 1; }
+__device__ __forceinline__ int v_entry(int i, int lead, int n) { return i + min(n, lead + i); }
+
+struct Out {
+    __half* out;
+    long long ldo;
+    float* part_o;        // [2 kMaxCtas][block rows][D]
+    float2* part_ml;      // [2 kMaxCtas][block rows]
+    Place* places;        // [CTAs + 1]: where the shares begin
+    float c;              // scale log2(e)
+    unsigned long long wait_ns;
+};
+
+// -------------------------------------------------------- the matrix warp ----
+// Ring entries: STAGES of Shape<D>::kEntryBytes at `ring`; queries of a stream at q + stream * kQBytes (and, with
+// Src::kExtra, one step of 16 more of the scores' product at xq + stream * kRowsQ * 32 against xk + stage * kEntry * 32).
+template <int D, int STAGES, class Src>
+__device__ __forceinline__ void matrix_warp(const Src& p, Control& c, uint32_t q, uint32_t ring, uint32_t xq, uint32_t xk) {
+    using X = Shape<D>;
+    constexpr int E = X::kEntries;
+    constexpr uint32_t kIdS = (1u << 4) | ((uint32_t)(X::kEntry >> 3) << 17) | ((uint32_t)(kRowsQ >> 4) << 24);
+    constexpr uint32_t kIdO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRowsQ >> 4) << 24);
+    const uint32_t tm = c.tmem;
+    Walk<D, Src> walk(p, c.cut, blockIdx.x);
+    Item x;
+    int base = 0;                               // ring entries before the block's, in tiles
+    uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
+    const uint32_t lead_lane = elect();
+    while (walk.next(x)) {
+        const int n = x.hi - x.lo;
+        if (n == 0) continue;
+        const bool pair = x.pair<D>();
+        const int lead = pair ? 1 : 2;
+        auto scores = [&](int s, int i, int buf, bool release) {        // of the share's tile i
+            bool ok = true;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int at = (base + k_entry(i, lead)) * E + e, stage = at % STAGES;
+                ok = wait_phase(&c.full[stage], (at / STAGES) & 1, c, p.o.wait_ns);
+                if (!ok) break;
+                tc::fence_after_sync();
+                const uint32_t a = desc_lo(q + s * X::kQBytes, 16), b = desc_lo(ring + stage * X::kEntryBytes, 16);
+                const uint32_t d = tm + buf * kTile + e * X::kEntry;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_ss(d, desc128(a + (ks >> 2) * (kRowsQ * 128 / 16) + (ks & 3) * 2),
+                           desc128(b + (ks >> 2) * (X::kEntry * 128 / 16) + (ks & 3) * 2), kIdS, ks > 0, lead_lane);
+                if (Src::kExtra)
+                    mma_ss(d, tc::smem_desc(xq + s * (kRowsQ * 32)), tc::smem_desc(xk + stage * (X::kEntry * 32)), kIdS, true, lead_lane);
+                if (release) commit(&c.freed[stage], lead_lane);
+            }
+            if (ok) commit(&c.s_full[buf], lead_lane);
+        };
+        auto values = [&](int s, int i, int j, int buf, bool release, bool last) {
+            bool ok = wait_phase(&c.p_full[buf], n_p[buf] & 1, c, p.o.wait_ns);
+            ++n_p[buf];
+            const uint32_t d = tm + X::kO + s * D;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int at = (base + v_entry(i, lead, n)) * E + e, stage = at % STAGES;
+                ok = ok && wait_phase(&c.clean[stage], (at / STAGES) & 1, c, p.o.wait_ns);
+                if (!ok) break;
+                tc::fence_after_sync();
+                const uint32_t b = desc_lo(ring + stage * X::kEntryBytes, X::kEntry * 128);
+#pragma unroll
+                for (int kk = 0; kk < X::kEntry / 16; ++kk)
+                    mma_ts(d, tm + buf * kTile + (e * (X::kEntry / 16) + kk) * 8, desc128(b + kk * (2048 / 16)), kIdO,
+                           j > 0 || e > 0 || kk > 0, lead_lane);
+                if (release) commit(&c.freed[stage], lead_lane);
+            }
+            if (ok && X::kStreams == 1) commit(&c.o_step[buf], lead_lane);
+            if (ok && last) commit(&c.o_last[s], lead_lane);
+        };
+        if constexpr (X::kStreams == 2) {
+            const int n1 = x.of_stream<D>(1), n0 = x.of_stream<D>(0);
+            auto tile = [&](int s, int j) { return x.tile_of<D>(s, j) - x.lo; };
+            wait_phase(&c.q_full[0], n_q[0]++ & 1, c, p.o.wait_ns);
+            scores(0, 0, 0, !pair);
+            if (n1) {
+                wait_phase(&c.q_full[1], n_q[1]++ & 1, c, p.o.wait_ns);
+                scores(1, tile(1, 0), 1, true);
+            }
+            for (int j = 0; j < n0; ++j) {
+                values(0, tile(0, j), j, 0, !pair, j + 1 == n0);
+                if (j + 1 < n0) scores(0, tile(0, j + 1), 0, !pair);
+                if (j < n1) {
+                    values(1, tile(1, j), j, 1, true, j + 1 == n1);
+                    if (j + 1 < n1) scores(1, tile(1, j + 1), 1, true);
+                }
+            }
+        } else {
+            wait_phase(&c.q_full[0], n_q[0]++ & 1, c, p.o.wait_ns);
+            // (a block's tile i has the score buffer (base + i) % 2: base counts two tiles, K's and V's, for each)
+            const int g = base / 2;
+            scores(0, 0, g & 1, true);
+            for (int j = 0; j < n; ++j) {
+                if (j + 1 < n) scores(0, j + 1, (g + j + 1) & 1, true);
+                values(0, j, j, (g + j) & 1, true, j + 1 == n);
+            }
+        }
+        base += 2 * n;
+    }
+}
+
+// ------------------------------------------------- the softmax warpgroups ----
+// Thread: one row of stream s.
+template <int D, class Src>
+__device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_smem, char* xq_smem) {
+    using X = Shape<D>;
+    const int s = threadIdx.x >> 7, quad = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = threadIdx.x & 127;
+    if (s >= X::kStreams) return;
+    const uint32_t tm = c.tmem + ((uint32_t)(32 * quad) << 16), o_at = tm + X::kO + s * D;
+    char* my_q = q_smem + s * X::kQBytes;
+    Walk<D, Src> walk(p, c.cut, blockIdx.x);
+    Item x;
+    uint32_t n_s[2] = {0, 0}, n_last = 0;
+    int base = 0, number = 0;
+    while (walk.next(x)) {
+        if (x.hi > x.lo) ++number;
+        const bool pair = x.pair<D>();
+        const int n = x.of_stream<D>(s);
+        const int local = pair ? s * kRowsQ + row : row;
+        const bool live = local < x.rows;
+        const int at = x.row0 + (live ? local : 0), token = at / p.G, head = x.h * p.G + at - token * p.G;
+        const typename Src::Row view(p, x, token);
+        float cc = p.o.c;                        // from a score to the exponent
+        if (n > 0) {
+            p.load_queries(x, live, token, head, my_q, xq_smem + s * (kRowsQ * 32), row, cc);
+            tc::fence_async_smem();
+            mbar_arrive(&c.q_full[s]);
+        }
+        float ref = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            const int buf = X::kStreams == 2 ? s : (base + j) & 1;
+            const uint32_t s_at = tm + buf * kTile;
+            ok = wait_phase(&c.s_full[buf], n_s[buf] & 1, c, p.o.wait_ns);
+            ++n_s[buf];
+            if (!ok) continue;
+            tc::fence_after_sync();
+            uint32_t v[kTile];
+#pragma unroll
+            for (int k = 0; k < kTile; k += 32) tmem_ld32(s_at + k, v + k);
+            tc::tmem_wait_ld();
+            const int tile = x.tile_of<D>(s, j);
+            if (tile >= x.clear) {
+#pragma unroll
+                for (int k = 0; k < kTile; k += 32) {
+                    const uint32_t seen = view.seen(p, x, tile * kTile + k);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!((seen >> i) & 1)) v[k + i] = 0xff800000u;      // -infinity
+                }
+            }
+            float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < kTile; k += 8)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], fmaxf(__uint_as_float(v[k + 2 * i]), __uint_as_float(v[k + 2 * i + 1])));
+            const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * cc;
+            const bool move = most > ref + kRise || (most > ref && ref == -INFINITY);
+            if (__any_sync(0xffffffffu, move)) {
+                const float to = move ? most : ref, f = to == ref ? 1.f : ex2(ref - to);
+                l *= f;
+                ref = to;
+                if (X::kStreams == 1 && j > 0) {
+                    // the product of the tile before, the other buffer's latest (with two streams it was issued
+                    // before these scores)
+                    const int g = base + j - 1;
+                    ok = wait_phase(&c.o_step[g & 1], (g >> 1) & 1, c, p.o.wait_ns);
+                    tc::fence_after_sync();
+                }
+                if (j > 0) {
+#pragma unroll 1
+                    for (int k = 0; k < D; k += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_at + k, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st32(o_at + k, o);
+                    }
+                }
+            }
+            const float sub = ref == -INFINITY ? 0.f : kUp - ref;
+            const f2 c2 = pk(cc, cc), sub2 = pk(sub, sub);
+            f2 sum[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < kTile; k += 2) {
+                float a, b;
+                unpk(fma2(pk(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, sub2), a, b);
+                a = ex2(a);
+                b = ex2(b);
+                sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pk(a, b));
+                v[k >> 1] = pack2(a, b);
+                if ((k & 63) == 62) tmem_st32(s_at + (k >> 6) * 32, v + (k >> 6) * 32);
+            }
+            float a, b;
+            unpk(add2(sum[0], sum[1]), a, b);
+            l += a + b;
+            tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.p_full[buf]);
+        }
+        if (X::kStreams == 1) base += n;
+        if (n > 0) {
+            ok = wait_phase(&c.o_last[s], n_last++ & 1, c, p.o.wait_ns) && ok;
+            tc::fence_after_sync();
+        }
+        if (!ok) l = __int_as_float(0x7fffffff);
+        const bool fix = n > 0 && special_of(c, number) == number;
+
+        // a block of one row tile: the second stream's sums and accumulator come through its query rows' memory
+        float f0 = 1.f, f1 = 0.f;
+        const bool merge = X::kStreams == 2 && !pair && x.of_stream<D>(1) > 0;
+        if (merge) {
+            if (s == 1) c.ml[row] = make_float2(ref, l);
+            named_bar_sync(1, kSoftmax);
+            if (s == 0) {
+                const float2 other = c.ml[row];
+                const float top = fmaxf(ref, other.x);
+                if (top != -INFINITY) {
+                    f0 = ex2(ref - top);
+                    f1 = ex2(other.x - top);
+                }
+                l = l * f0 + other.y * f1;      // (a sum of NaN stays one)
+                ref = top;
+            }
+        }
+        const bool whole = x.part < 0;
+        const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        const float nan = l != l ? l : 0.f;
+        __half* out = p.o.out + (long long)(x.s.q0 + token) * p.o.ldo + (long long)head * D;
+        float* part = p.o.part_o + ((long long)x.part * X::kBlock + local) * D;
+        const bool writes = live && (s == 0 || pair);
+        float* swap = reinterpret_cast<float*>(q_smem + X::kQBytes * (X::kStreams - 1));      // [D / 2][kRowsQ]
+#pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+            if (merge && k % (D / 2) == 0) {
+                if (k) named_bar_sync(2, kSoftmax);                 // the first half has been read
+                if (s == 1) {
+#pragma unroll 1
+                    for (int i = 0; i < D / 2; i += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_at + k + i, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) swap[(i + e) * kRowsQ + row] = __uint_as_float(o[e]);
+                    }
+                    named_bar_sync(3, kSoftmax);
+                } else {
+                    named_bar_sync(3, kSoftmax);
+                }
+            }
+            if (X::kStreams == 2 && !pair && s == 1) continue;
+            float o[32];
+            if (n > 0) {
+                uint32_t raw[32];
+                tmem_ld32(o_at + k, raw);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(raw[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            }
+            if (merge) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = o[i] * f0 + swap[(k % (D / 2) + i) * kRowsQ + row] * f1;
+            }
+            if (fix && live) p.add_special(x, view, token, k, o);
+            if (l == 0.f || l != l) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = nan;
+            }
+            if (writes && whole) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8)
+                    *reinterpret_cast<uint4*>(out + k + i) =
+                        make_uint4(pack2(o[i] * inv, o[i + 1] * inv), pack2(o[i + 2] * inv, o[i + 3] * inv),
+                                   pack2(o[i + 4] * inv, o[i + 5] * inv), pack2(o[i + 6] * inv, o[i + 7] * inv));
+            } else if (writes) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<float4*>(part + k + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            }
+        }
+        if (writes && !whole) p.o.part_ml[(long long)x.part * X::kBlock + local] = make_float2(ref, l);
+        if (merge) named_bar_sync(2, kSoftmax);                     // the second half has been read
+        tc::fence_before_sync();
+    }
+}
+
+// Start of a CTA.  Barriers' counts: an entry's arrival 1 (full_count), its release 1 + free_extra.
+__device__ __forceinline__ void control_init(Control& c, int full_count, int clean_count, int free_count, bool dead) {
+    for (int i = 0; i < kMaxStages; ++i) {
+        mbar_init(&c.full[i], full_count);
+        mbar_init(&c.clean[i], clean_count);
+        mbar_init(&c.freed[i], free_count);
+    }
+    for (int i = 0; i < 2; ++i) {
+        mbar_init(&c.q_full[i], kRowsQ);
+        mbar_init(&c.s_full[i], 1);
+        mbar_init(&c.p_full[i], 4);
+        mbar_init(&c.o_last[i], 1);
+        mbar_init(&c.o_step[i], 1);
+    }
+    mbar_init(&c.drained, 1);
+    fence_mbar_init();
+    c.dead = dead;
+    for (int i = 0; i < kMaxStages * 2; ++i) c.special[i] = 0;
+}
+
+// ------------------------------------------------------------------- join ----
+// A CTA of four warps: 32 rows of the block that the cut in front of share blockIdx.x + 1 is the first to fall into.
+template <int D, class Src>
+__global__ void __launch_bounds__(128) flash_join(const Src p) {
+    constexpr int kN = D / 32, R = Shape<D>::kBlock;
+    wait_predecessor();
+    launch_dependents();
+    const int i = blockIdx.x + 1, ctas = gridDim.x + 1, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const Place at = p.o.places[i];
+    if (at.tile == 0) return;
+    const Place before = p.o.places[i - 1];
+    if (before.tile > 0 && same_block(before, at)) return;
+    int last = i;                                   // the last share that begins in the block
+    while (last + 1 < ctas) {
+        const Place z = p.o.places[last + 1];
+        if (z.tile == 0 || !same_block(z, at)) break;
+        ++last;
+    }
+    const Seq s = p.seq(at.b);
+    const int row0 = at.t * R, rows = min(R, s.n_q * p.G - row0);
+    for (int local = blockIdx.y * 32 + wid; local < min(rows, blockIdx.y * 32 + 32); local += 4) {
+        float top = -INFINITY;
+        auto slot = [&](int cta) { return (long long)(2 * cta + (cta == i - 1 ? 1 : 0)) * R + local; };
+        for (int k = i - 1 + lane; k <= last; k += 32) top = fmaxf(top, p.o.part_ml[slot(k)].x);
+#pragma unroll
+        for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        float v[kN], l = 0.f;
+#pragma unroll
+        for (int e = 0; e < kN; ++e) v[e] = 0.f;
+        for (int k = i - 1; k <= last; ++k) {
+            const float2 ml = p.o.part_ml[slot(k)];
+            const float* o = p.o.part_o + slot(k) * D;
+            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+            l += ml.y != ml.y ? ml.y : ml.y * f;
+#pragma unroll
+            for (int e = 0; e < kN; ++e) v[e] = fmaf(o[e * 32 + lane], f, v[e]);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int r = row0 + local, token = r / p.G, head = at.h * p.G + r - token * p.G;
+        __half* out = p.o.out + (long long)(s.q0 + token) * p.o.ldo + (long long)head * D;
+#pragma unroll
+        for (int e = 0; e < kN; ++e) out[e * 32 + lane] = __float2half_rn(v[e] * inv);
+    }
+}
+
+// workspace: places, parts' statistics, parts
+template <int D>
+inline long long workspace_bytes() {
+    return (long long)(kMaxCtas + 1) * sizeof(Place) + 15 + 2ll * kMaxCtas * Shape<D>::kBlock * (D * 4 + 8) + 16;
+}
+template <int D>
+inline void lay_out(char* ws, Out* o) {
+    o->places = (Place*)ws;
+    char* at = ws + ((kMaxCtas + 1) * sizeof(Place) + 15) / 16 * 16;
+    o->part_ml = (float2*)at;
+    o->part_o = (float*)(at + 2ll * kMaxCtas * Shape<D>::kBlock * 8);
+}
+
+}  // namespace flash
+}  // namespace edge0
