@@ -576,6 +576,27 @@ int edge0_attn_prompt(const uint16_t* q, long long ldq, int T, int n_q_heads, co
                       const int32_t* cu_keys, int B, float scale, uint16_t* out, long long ldo, void* workspace,
                       size_t workspace_bytes, cudaStream_t stream);
 
+/* Attention of drafted tokens over the cache, several rows per sequence: row r of the call belongs to
+ * the sequence b with cu_rows[b] <= r < cu_rows[b + 1] (cu_rows [B + 1], non-decreasing, within [0, T]) and is its
+ * drafted token i = r - cu_rows[b], whose K and V lie at its position lens[b] + i (edge0_kv_append with
+ * start = lens and these cu_rows).  It sees the context, the positions before lens[b], and of the sequence's drafted tokens
+ *   with mask: token j where bit j % 32 of mask[r][j / 32] is set (mask [T][mask_words], device;
+ *     its own and its ancestors' in a tree; bits behind the sequence's tokens count for nothing, and
+ *     tokens behind 32 mask_words are seen by no row);
+ *   with mask NULL (mask_words 0): those up to itself, as for the next part of a prompt.
+ * q, out: T rows of n_q_heads * head_dim fp16, ldq / ldo elements apart (16-byte aligned, multiples of 8); table
+ * [B][W], lens [B], cu_rows: device int32.  Softmax, scale, the sharing of K/V heads, the workspace and waits
+ * that run out as in edge0_attn_decode; V enters as edge0_kv_read returns it and K rounded to fp16 but for an
+ * offset that a group's 64 dims share (2^-11 of what is left).  A row that sees nothing gets zeros, rows of no sequence and of one with
+ * lens[b] < 0 are left as they were, and what a row does not see has no influence on it.  Tokens behind
+ * W * page_tokens (they are cut off), sequences of more than 32 mask_words drafted tokens and pages outside [0, n_pages)
+ * (page 0 is read in their place) are recorded as EDGE0_EINVAL in *status. */
+size_t edge0_attn_tree_workspace_bytes(const edge0_kv_cache* cache);
+int edge0_attn_tree(const edge0_kv_cache* cache, const uint16_t* q, long long ldq, int T, int n_q_heads,
+                    const int32_t* table, int B, int W, const int32_t* lens, const int32_t* cu_rows, const uint32_t* mask,
+                    int mask_words, float scale, uint16_t* out, long long ldo, int* status, void* workspace,
+                    size_t workspace_bytes, cudaStream_t stream);
+
 /* ---- allocation-free variant (the paper has no counterpart to this call) ----
  * edge0_moe_int4_forward for callers that cannot allocate memory: code running
  * in an allocator-free part of a serving loop, code whose memory budget was fixed

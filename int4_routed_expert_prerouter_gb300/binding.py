@@ -153,6 +153,10 @@ def _declare(L):
     L.edge0_attn_prompt_workspace_bytes.restype = C.c_size_t
     L.edge0_attn_prompt.argtypes = [P, C.c_longlong, C.c_int, C.c_int, P, C.c_longlong, P, C.c_longlong, C.c_int, C.c_int, C.c_int,
                                     P, P, C.c_int, C.c_float, P, C.c_longlong, P, C.c_size_t, P]
+    L.edge0_attn_tree_workspace_bytes.argtypes = [C.POINTER(KvCacheDesc)]
+    L.edge0_attn_tree_workspace_bytes.restype = C.c_size_t
+    L.edge0_attn_tree.argtypes = [C.POINTER(KvCacheDesc), P, C.c_longlong, C.c_int, C.c_int, P, C.c_int, C.c_int, P, P, P, C.c_int,
+                                  C.c_float, P, C.c_longlong, P, P, C.c_size_t, P]
     L.edge0_kv_compact.argtypes = [C.POINTER(KvCacheDesc), P, C.c_int, C.c_int, P, P, P, C.c_int, P, P]
     L.edge0_kv_copy_pages.argtypes = [C.POINTER(KvCacheDesc), P, P, C.c_int, P, P]
     L.edge0_rope_turns.argtypes = [C.POINTER(RopeSpec), P, P, C.POINTER(C.c_float)]
@@ -165,7 +169,7 @@ def _declare(L):
                  "edge0_moe_int4_forward_noalloc", "edge0_state_set_wait_limit", "edge0_noalloc_error",
                  "edge0_prefill", "edge0_tc_gemm_f16", "edge0_q4_linear", "edge0_kv_append", "edge0_kv_read",
                  "edge0_attn_decode", "edge0_kv_compact", "edge0_kv_copy_pages", "edge0_rope_turns", "edge0_rope",
-                 "edge0_attn_prompt"):
+                 "edge0_attn_prompt", "edge0_attn_tree"):
         getattr(L, name).restype = C.c_int
 
 
@@ -182,7 +186,7 @@ EXPORTED = ["edge0_status_string", "edge0_q4_gate_up_packed_bytes", "edge0_pack_
             "edge0_pool_resident", "edge0_pool_destroy", "edge0_q4_linear", "edge0_kv_page_bytes",
             "edge0_kv_append", "edge0_kv_read", "edge0_attn_workspace_bytes", "edge0_attn_decode",
             "edge0_block_set_wait_limit", "edge0_kv_compact", "edge0_kv_copy_pages", "edge0_rope_turns", "edge0_rope",
-            "edge0_attn_prompt_workspace_bytes", "edge0_attn_prompt"]
+            "edge0_attn_prompt_workspace_bytes", "edge0_attn_prompt", "edge0_attn_tree_workspace_bytes", "edge0_attn_tree"]
 
 
 def status_string(code: int) -> str:
@@ -1095,4 +1099,70 @@ def _attn_prompt(q, k, v, cu_rows, cu_keys, scale, out, workspace, index, stream
     code = _with_workspace(call, workspace, attn_prompt_workspace_bytes(D) if workspace is None else 0, index, handle, q.device, "attn_prompt")
     if code:
         raise Edge0Error(code, "edge0_attn_prompt")
+    return out
+
+
+# --------------------------------------- attention of drafted tokens ----
+def attn_tree_workspace_bytes(cache: KVCache) -> int:
+    n = cache._ws_bytes.get("tree")
+    if n is None:
+        n = cache._ws_bytes["tree"] = int(lib().edge0_attn_tree_workspace_bytes(cache._desc))
+    return n
+
+
+def attn_tree(cache: KVCache, q: torch.Tensor, table, lens, cu_rows, mask=None, scale=None, out=None, workspace=None,
+              stream=None) -> torch.Tensor:
+    """Attention of drafted tokens, q [T, n_q_heads, head_dim] fp16, over the cache: the rows cu_rows[b] to
+    cu_rows[b + 1] are sequence b's, whose K and V lie behind its lens[b] tokens (kv_append with start = lens
+    and these cu_rows).  A row sees the context and of its sequence's drafted tokens those whose bits
+    are set in its row of mask [T, words] int32 (bit j % 32 of word j / 32: token j), or those up to itself where mask is None.
+    table [B, W], lens [B], cu_rows [B + 1]: int32 on the device.  scale: 1 / sqrt(head_dim) unless given.  out:
+    rows to fill (those of no sequence and of one with lens[b] < 0 are left as they are) or None.  workspace:
+    uint8 of attn_tree_workspace_bytes, or None for the one kept per device and stream (attn_decode)."""
+    guard = _guard(cache._index, stream)
+    if guard is not None:
+        with guard:
+            return _attn_tree(cache, q, table, lens, cu_rows, mask, scale, out, workspace, stream)
+    return _attn_tree(cache, q, table, lens, cu_rows, mask, scale, out, workspace, None)
+
+
+def _attn_tree(cache, q, table, lens, cu_rows, mask, scale, out, workspace, stream):
+    index = cache._index
+    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.get_device() != index:
+        raise _bad("attn_tree: q [T, n_q_heads, head_dim] beside the cache")
+    T, Hq, D = q.shape
+    ldq = _row_stride(q, "attn_tree: q")
+    if table.dim() != 2:
+        raise _bad("attn_tree: table [B, W]")
+    B, W = table.shape
+    if T > _INT_MAX or B > _INT_MAX or W > _INT_MAX or Hq > _INT_MAX:
+        raise Edge0Error(EDGE0_EUNSUPPORTED, "attn_tree: rows, sequences or pages beyond 2^31 - 1")
+    tb, ln = _ints(table, index, B * W, "attn_tree: table"), _ints(lens, index, B, "attn_tree: lens")
+    cu, mp, words = _ints(cu_rows, index, B + 1, "attn_tree: cu_rows"), None, 0
+    if mask is not None:
+        if mask.dim() != 2 or mask.shape[0] != T or mask.shape[1] == 0:
+            raise _bad("attn_tree: mask [T, words]")
+        words = mask.shape[1]
+        if words > _INT_MAX:
+            raise Edge0Error(EDGE0_EUNSUPPORTED, "attn_tree: mask words beyond 2^31 - 1")
+        mp = _ints(mask, index, T * words, "attn_tree: mask")
+        if T == 0:
+            mp, words = None, 0
+    if out is None:
+        out, ldo = torch.empty((T, Hq, D), dtype=_f16, device=cache.device), Hq * D
+    else:
+        if out.shape != q.shape or out.get_device() != index:
+            raise _bad("attn_tree: out like q")
+        ldo = _row_stride(out, "attn_tree: out")
+    handle = _raw_stream(index, stream)
+
+    def call(ws, nbytes):
+        return _lib.edge0_attn_tree(cache._desc, q.data_ptr(), ldq, T, Hq, tb, B, W, ln, cu, mp, words,
+                                    D ** -0.5 if scale is None else scale, out.data_ptr(), ldo, cache._status, ws.data_ptr(), nbytes,
+                                    handle)
+
+    code = _with_workspace(call, workspace, attn_tree_workspace_bytes(cache) if workspace is None else 0, index, handle, cache.device,
+                           "attn_tree")
+    if code:
+        raise Edge0Error(code, "edge0_attn_tree")
     return out

@@ -17,7 +17,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libedge0.so")
 SOURCES = ["decode1.cu", "engine.cu", "batch.cu", "pool.cu", "api.cu", "pack.cu", "lora.cu", "noalloc.cu",
            "tcgemm.cu", "qlinear.cu", "kvcache.cu", "attn.cu",
-           "attn_prefix.cu", "rope.cu", "kvmove.cu", "attn_prompt.cu"]
+           "attn_prefix.cu", "rope.cu", "kvmove.cu", "attn_prompt.cu", "attn_tree.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -30,7 +30,9 @@ struct PromptP {
 
 template <int D>
 struct Prompt : PromptP {
-    static constexpr bool kExtra = false;
+    static constexpr bool kExtra = false, kLooked = true;
+    static constexpr int kHeld = kTile;
+    __host__ __device__ static constexpr int dim_of(int column) { return column; }
 
     // (numbers outside [0, T] are cut, so that nothing beside the rows is touched whatever they say)
     __device__ Seq seq(int b) const {
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_prompt_kernel(const __grid_
     tc::fence_before_sync();
     wait_predecessor();
     launch_dependents();
-    find_share<D>(static_cast<const Src&>(p), blockIdx.x, gridDim.x, reinterpret_cast<long long*>(smem), c.cut, kThreadsF);
+    find_share<D>(static_cast<const Src&>(p), blockIdx.x, gridDim.x, reinterpret_cast<long long*>(smem), c.cut);
     tc::fence_after_sync();
     if (joins && threadIdx.x == 0) p.o.places[blockIdx.x] = c.cut[0];
 
@@ -128,82 +130,55 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_prompt_kernel(const __grid_
         if (wid == 8) {
             matrix_warp<D, R::kStages, Src>(p, c, smem_u32(smem), smem_u32(ring), 0, 0);
         } else if (wid == 9) {
-            Walk<D, Src> walk(p, c.cut, blockIdx.x);
-            Item x;
+            Feed<D, Src> feed(p, c.cut, blockIdx.x);
             int at = 0;
             bool ok = p.o.wait_ns != 0;
             const uint32_t lead_lane = elect();
-            auto put = [&](const CUtensorMap* map, int i) {
+            for (; ok && feed.next(); ++at) {
+                const int stage = at % R::kStages;
+                if (at >= R::kStages) ok = wait_phase(&c.freed[stage], (at / R::kStages - 1) & 1, c, p.o.wait_ns);
+                if (!ok) break;
+                if (lead_lane) {
+                    mbar_arrive_expect_tx(&c.full[stage], X::kEntryBytes);
 #pragma unroll
-                for (int e = 0; e < X::kEntries; ++e, ++at) {
-                    const int stage = at % R::kStages;
-                    if (at >= R::kStages) ok = ok && wait_phase(&c.freed[stage], (at / R::kStages - 1) & 1, c, p.o.wait_ns);
-                    if (!ok) return;
-                    if (lead_lane) {
-                        mbar_arrive_expect_tx(&c.full[stage], X::kEntryBytes);
-#pragma unroll
-                        for (int k = 0; k < X::kChunks; ++k)
-                            tma_load(smem_u32(ring) + stage * X::kEntryBytes + k * (X::kEntry * 128), map, 64 * k, x.h,
-                                     x.s.k0 + (x.lo + i) * kTile + e * X::kEntry, &c.full[stage]);
-                    }
-                    __syncwarp();
+                    for (int k = 0; k < X::kChunks; ++k)
+                        tma_load(smem_u32(ring) + stage * X::kEntryBytes + k * (X::kEntry * 128), feed.value ? &map_v : &map_k, 64 * k,
+                                 feed.x.h, feed.x.s.k0 + feed.token(), &c.full[stage]);
                 }
-            };
-            while (ok && walk.next(x)) {
-                const int n = x.hi - x.lo, lead = x.pair<D>() ? 1 : 2;
-                for (int i = 0; i < min(lead, n); ++i) put(&map_k, i);
-                for (int i = 0; i < n && ok; ++i) {
-                    put(&map_v, i);
-                    if (i + lead < n) put(&map_k, i + lead);
-                }
+                __syncwarp();
             }
             // nothing may land in this memory when it has become another CTA's
             if (!ok) drain_copies_call(c.full, at > R::kStages ? at - R::kStages : 0, at, R::kStages);
         } else {
-            Walk<D, Src> walk(p, c.cut, blockIdx.x);
-            Item x;
-            int at = 0, number = 0;
-            auto look = [&](bool v, int i) {
-#pragma unroll 1
-                for (int e = 0; e < X::kEntries; ++e, ++at) {
-                    const int stage = at % R::kStages;
-                    if (!wait_phase(&c.full[stage], (at / R::kStages) & 1, c, p.o.wait_ns)) continue;
-                    const int token = (x.lo + i) * kTile + e * X::kEntry;
-                    if (v && x.lo + i >= x.clear) {
-                        char* entry = ring + stage * X::kEntryBytes;
-                        bool found = false;
+            Feed<D, Src> feed(p, c.cut, blockIdx.x);
+            for (int at = 0; feed.next(); ++at) {
+                const int stage = at % R::kStages;
+                if (!wait_phase(&c.full[stage], (at / R::kStages) & 1, c, p.o.wait_ns)) continue;
+                const Item& x = feed.x;
+                if (feed.value && x.lo + feed.tile >= x.clear) {
+                    char* entry = ring + stage * X::kEntryBytes;
+                    const int left = x.s.n_k - feed.token();
+                    bool found = false;
 #pragma unroll 4
-                        for (int k = (wid - 10) * 32 + lane; k < X::kEntryBytes / 16; k += 64) {
-                            uint4* piece = reinterpret_cast<uint4*>(entry) + k;
-                            const int row = (k >> 3) & (X::kEntry - 1);
-                            uint4 w = *piece;
-                            const uint32_t bx = __vcmpeq2(w.x & 0x7C007C00u, 0x7C007C00u), by = __vcmpeq2(w.y & 0x7C007C00u, 0x7C007C00u),
-                                           bz = __vcmpeq2(w.z & 0x7C007C00u, 0x7C007C00u), bw = __vcmpeq2(w.w & 0x7C007C00u, 0x7C007C00u);
-                            const bool behind = token + row >= x.s.n_k, bad = (bx | by | bz | bw) != 0;
-                            if (behind) {
-                                *piece = make_uint4(0, 0, 0, 0);
-                            } else if (bad) {
-                                *piece = make_uint4(w.x & ~bx, w.y & ~by, w.z & ~bz, w.w & ~bw);
-                                found = true;
-                            }
+                    for (int k = (wid - 10) * 32 + lane; k < X::kEntryBytes / 16; k += 64) {
+                        uint4* piece = reinterpret_cast<uint4*>(entry) + k;
+                        const uint4 w = *piece;
+                        const uint32_t bx = __vcmpeq2(w.x & 0x7C007C00u, 0x7C007C00u), by = __vcmpeq2(w.y & 0x7C007C00u, 0x7C007C00u),
+                                       bz = __vcmpeq2(w.z & 0x7C007C00u, 0x7C007C00u), bw = __vcmpeq2(w.w & 0x7C007C00u, 0x7C007C00u);
+                        if (((k >> 3) & (X::kEntry - 1)) >= left) {
+                            *piece = make_uint4(0, 0, 0, 0);
+                        } else if ((bx | by | bz | bw) != 0) {
+                            *piece = make_uint4(w.x & ~bx, w.y & ~by, w.z & ~bz, w.w & ~bw);
+                            found = true;
                         }
-                        if (found) special_of(c, number) = number;
-                        tc::fence_async_smem();
                     }
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&c.clean[stage]);
-                        mbar_arrive(&c.freed[stage]);
-                    }
+                    if (found) special_of(c, feed.number) = feed.number;
+                    tc::fence_async_smem();
                 }
-            };
-            while (walk.next(x)) {
-                const int n = x.hi - x.lo, lead = x.pair<D>() ? 1 : 2;
-                if (n > 0) ++number;
-                for (int i = 0; i < min(lead, n); ++i) look(false, i);
-                for (int i = 0; i < n; ++i) {
-                    look(true, i);
-                    if (i + lead < n) look(false, i + lead);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&c.clean[stage]);
+                    mbar_arrive(&c.freed[stage]);
                 }
             }
         }

@@ -117,10 +117,10 @@ struct Costs {
     __device__ long long total() const { return blocks ? before(blocks - 1) + per + all : 0; }
 };
 
-// The places of the cuts `first` and first + 1 of the CTAs' shares, by the whole CTA of `threads` >= 256;
+// The places of the cuts `first` and first + 1 of the CTAs' shares, by the whole CTA of at least 256 threads;
 // prefix: [EDGE0_MAX_BATCHED + 1] of scratch.
 template <int D, class Src>
-__device__ void find_share(const Src& p, int cta, int ctas, long long* prefix, Place* out, int threads) {
+__device__ void find_share(const Src& p, int cta, int ctas, long long* prefix, Place* out) {
     constexpr int R = Shape<D>::kBlock;
     const int tid = threadIdx.x;
     long long mine = 0;
@@ -378,6 +378,34 @@ struct Out {
 };
 
 // -------------------------------------------------------- the matrix warp ----
+// A ring's entries in their order: K tiles run ahead of V's, by one where two streams share the tiles, else by two.
+template <int D, class Src>
+struct Feed {
+    Walk<D, Src> walk;
+    Item x;
+    int n = 0, lead = 0, k = 0, v = 0, e = Shape<D>::kEntries, number = 0;
+    bool value = false;   // the entry is of V
+    int tile = 0;         // of the share's part of the block
+
+    __device__ Feed(const Src& p, const Place* cut, int cta) : walk(p, cut, cta) {}
+    __device__ bool next() {
+        if (++e < Shape<D>::kEntries) return true;
+        e = 0;
+        while (v == n) {
+            if (!walk.next(x)) return false;
+            n = x.hi - x.lo;
+            lead = x.pair<D>() ? 1 : 2;
+            k = v = 0;
+            if (n > 0) ++number;
+        }
+        value = k == min(n, v + lead);
+        tile = value ? v++ : k++;
+        return true;
+    }
+    // first token of the entry
+    __device__ int token() const { return (x.lo + tile) * kTile + e * Shape<D>::kEntry; }
+};
+
 // Ring entries: STAGES of Shape<D>::kEntryBytes at `ring`; queries of a stream at q + stream * kQBytes (and, with
 // Src::kExtra, one step of 16 more of the scores' product at xq + stream * kRowsQ * 32 against xk + stage * kEntry * 32).
 template <int D, int STAGES, class Src>
@@ -424,7 +452,7 @@ __device__ __forceinline__ void matrix_warp(const Src& p, Control& c, uint32_t q
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const int at = (base + v_entry(i, lead, n)) * E + e, stage = at % STAGES;
-                ok = ok && wait_phase(&c.clean[stage], (at / STAGES) & 1, c, p.o.wait_ns);
+                ok = ok && wait_phase(Src::kLooked ? &c.clean[stage] : &c.full[stage], (at / STAGES) & 1, c, p.o.wait_ns);
                 if (!ok) break;
                 tc::fence_after_sync();
                 const uint32_t b = desc_lo(ring + stage * X::kEntryBytes, X::kEntry * 128);
@@ -504,25 +532,32 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
             ++n_s[buf];
             if (!ok) continue;
             tc::fence_after_sync();
-            uint32_t v[kTile];
-#pragma unroll
-            for (int k = 0; k < kTile; k += 32) tmem_ld32(s_at + k, v + k);
-            tc::tmem_wait_ld();
+            constexpr int kN = Src::kHeld;           // scores held in registers; fewer than all are read twice
+            uint32_t v[kN];
             const int tile = x.tile_of<D>(s, j);
-            if (tile >= x.clear) {
+            auto read = [&](int from) {
 #pragma unroll
-                for (int k = 0; k < kTile; k += 32) {
-                    const uint32_t seen = view.seen(p, x, tile * kTile + k);
+                for (int k = 0; k < kN; k += 32) tmem_ld32(s_at + from + k, v + k);
+                tc::tmem_wait_ld();
+                if (tile >= x.clear) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (!((seen >> i) & 1)) v[k + i] = 0xff800000u;      // -infinity
+                    for (int k = 0; k < kN; k += 32) {
+                        const uint32_t seen = view.seen(p, x, tile * kTile + from + k);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!((seen >> i) & 1)) v[k + i] = 0xff800000u;      // -infinity
+                    }
                 }
-            }
+            };
             float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int k = 0; k < kTile; k += 8)
+            for (int from = 0; from < kTile; from += kN) {
+                read(from);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], fmaxf(__uint_as_float(v[k + 2 * i]), __uint_as_float(v[k + 2 * i + 1])));
+                for (int k = 0; k < kN; k += 8)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], fmaxf(__uint_as_float(v[k + 2 * i]), __uint_as_float(v[k + 2 * i + 1])));
+            }
             const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * cc;
             const bool move = most > ref + kRise || (most > ref && ref == -INFINITY);
             if (__any_sync(0xffffffffu, move)) {
@@ -552,14 +587,18 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
             const f2 c2 = pk(cc, cc), sub2 = pk(sub, sub);
             f2 sum[2] = {0, 0};
 #pragma unroll
-            for (int k = 0; k < kTile; k += 2) {
-                float a, b;
-                unpk(fma2(pk(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, sub2), a, b);
-                a = ex2(a);
-                b = ex2(b);
-                sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pk(a, b));
-                v[k >> 1] = pack2(a, b);
-                if ((k & 63) == 62) tmem_st32(s_at + (k >> 6) * 32, v + (k >> 6) * 32);
+            for (int from = 0; from < kTile; from += kN) {
+                if (kN < kTile) read(from);          // (weights lie over scores that have been read for good)
+#pragma unroll
+                for (int k = 0; k < kN; k += 2) {
+                    float a, b;
+                    unpk(fma2(pk(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, sub2), a, b);
+                    a = ex2(a);
+                    b = ex2(b);
+                    sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pk(a, b));
+                    v[k >> 1] = pack2(a, b);
+                    if ((k & 63) == 62) tmem_st32(s_at + ((from + k) >> 6) * 32, v + (k >> 6) * 32);
+                }
             }
             float a, b;
             unpk(add2(sum[0], sum[1]), a, b);
@@ -620,20 +659,20 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
                 }
             }
             if (X::kStreams == 2 && !pair && s == 1) continue;
-            float o[32];
+            float o[32];                            // dims k .. k + 31
             if (n > 0) {
                 uint32_t raw[32];
                 tmem_ld32(o_at + k, raw);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(raw[i]);
+                for (int i = 0; i < 32; ++i) {
+                    float a = __uint_as_float(raw[i]);
+                    if (merge) a = a * f0 + swap[(k % (D / 2) + i) * kRowsQ + row] * f1;
+                    o[(i & ~7) + Src::dim_of(i & 7)] = a;
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = 0.f;
-            }
-            if (merge) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = o[i] * f0 + swap[(k % (D / 2) + i) * kRowsQ + row] * f1;
             }
             if (fix && live) p.add_special(x, view, token, k, o);
             if (l == 0.f || l != l) {
