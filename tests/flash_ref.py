@@ -7,7 +7,7 @@ import torch
 
 def attend(q, k, v, seen, scale, k_abs=None, k_mag=None, rounded=0.0):
     """q [n, Hq, D], k, v [m, H, D] float64, seen [n, m] -> o [n, Hq, D] and how far an fp16 result may
-    be off.  Rows that see nothing: zeros, exactly.
+    be off.  Rows that see nothing: zeros, exactly.  A NaN in v is one in the rows that see it, and in no others.
 
     With p the normalised weights the bound adds up
     - the result's rounding: half an fp16 step, 2^-11 |o|, and 2^-25 where that is subnormal;
@@ -27,13 +27,15 @@ def attend(q, k, v, seen, scale, k_abs=None, k_mag=None, rounded=0.0):
     some = seen.any(1)
     for h in range(Hq):
         kk, vv = k[:, h // (Hq // H)], v[:, h // (Hq // H)]
+        nan = torch.isnan(vv)
+        vv = vv.masked_fill(nan, 0.0)
         s = scale * (q[:, h] @ kk.T)
         s = s.masked_fill(~seen, -math.inf)
         top = s.amax(1, keepdim=True)
         e = torch.exp(s - torch.where(torch.isinf(top), torch.zeros_like(top), top))
         total = e.sum(1, keepdim=True)
         p = e / torch.where(some[:, None], total, torch.ones_like(total))
-        o[:, h] = p @ vv
+        o[:, h] = (p @ vv).masked_fill(seen.double() @ nan.double() > 0, math.nan)
         ka = kk.abs() if k_abs is None else k_abs[:, h // (Hq // H)]
         a = scale * (q[:, h].abs() @ ka.T) * (D / 16 + 1) * 2.0 ** -23 + s.masked_fill(~seen, 0.0).abs() * 2.0 ** -21 + 2.0 ** -20
         if k_mag is not None:
@@ -49,3 +51,9 @@ def attend(q, k, v, seen, scale, k_abs=None, k_mag=None, rounded=0.0):
 
 def causal(n, m, device):
     return torch.arange(m, device=device)[None, :] <= torch.arange(n, device=device)[:, None] + (m - n)
+
+
+def close(got, o, bound):
+    """Whether got lies within its bound of o, NaN where that is."""
+    nan = torch.isnan(o)
+    return bool((torch.isnan(got) == nan).all()) and bool(((got.double() - o).abs() <= bound)[~nan].all())
