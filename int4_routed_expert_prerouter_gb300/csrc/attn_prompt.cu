@@ -30,9 +30,6 @@ struct PromptP {
 
 template <int D>
 struct Prompt : PromptP {
-    static constexpr bool kExtra = false, kLooked = true;
-    static constexpr int kHeld = kTile;
-    __host__ __device__ static constexpr int dim_of(int column) { return column; }
 
     // (numbers outside [0, T] are cut, so that nothing beside the rows is touched whatever they say)
     __device__ Seq seq(int b) const {
@@ -48,16 +45,13 @@ struct Prompt : PromptP {
     __device__ static int seen(const Seq& s, int token) { return min(max(token + 1 + s.off, 0), s.n_k); }
     __device__ static int seen_by_all(const Seq& s, int token) { return seen(s, token); }
 
-    struct Row {
-        int n;                         // keys that the row sees
-        __device__ Row(const Prompt&, const Item& x, int token) : n(Prompt::seen(x.s, token)) {}
-        __device__ uint32_t seen(const Prompt&, const Item&, int from) const {
-            const int k = n - from;
-            return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1;
-        }
-    };
+    // which of the tokens from .. from + 31 a row sees, as bits
+    __device__ static uint32_t seen_word(const Item& x, int token, int from) {
+        const int k = seen(x.s, token) - from;
+        return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1;
+    }
 
-    __device__ void load_queries(const Item& x, bool live, int token, int head, char* dst, char*, int row, float&) const {
+    __device__ void load_queries(const Item& x, bool live, int token, int head, char* dst, int row) const {
         const __half* src = q + (long long)(x.s.q0 + token) * ldq + (long long)head * D;
 #pragma unroll
         for (int c0 = 0; c0 < D / 8; c0 += 8) {
@@ -70,9 +64,9 @@ struct Prompt : PromptP {
         }
     }
     // adds the infinities and NaN that the row sees of the tiles looked through (dims k .. k + 31)
-    __device__ void add_special(const Item& x, const Row& r, int, int k, float (&o)[32]) const {
+    __device__ void add_special(const Item& x, int token, int k, float (&o)[32]) const {
         const __half* at = v + (long long)x.h * D + k;
-        for (int j = max(x.clear, x.lo) * kTile; j < min(r.n, x.hi * kTile); ++j)
+        for (int j = max(x.clear, x.lo) * kTile; j < min(seen(x.s, token), x.hi * kTile); ++j)
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
                 const float f = __half2float(at[(long long)(x.s.k0 + j) * ldv + i]);
@@ -117,26 +111,26 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_prompt_kernel(const __grid_
     tc::fence_before_sync();
     wait_predecessor();
     launch_dependents();
-    find_share<D>(static_cast<const Src&>(p), blockIdx.x, gridDim.x, reinterpret_cast<long long*>(smem), c.cut);
+    find_share<X>(static_cast<const Src&>(p), blockIdx.x, gridDim.x, reinterpret_cast<long long*>(smem), c.cut);
     tc::fence_after_sync();
     if (joins && threadIdx.x == 0) p.o.places[blockIdx.x] = c.cut[0];
 
     // registers: 256 x 208 + 128 x 88, what the CTA was launched with (384 x 168)
     if (wid < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
-        softmax_warps<D, Src>(p, c, smem, nullptr);
+        softmax_warps<D, Src>(p, c, smem);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
         if (wid == 8) {
-            matrix_warp<D, R::kStages, Src>(p, c, smem_u32(smem), smem_u32(ring), 0, 0);
+            matrix_warp<D, R::kStages, Src>(p, c, smem_u32(smem), smem_u32(ring));
         } else if (wid == 9) {
-            Feed<D, Src> feed(p, c.cut, blockIdx.x);
+            Feed<X, Src> feed(p, c.cut, blockIdx.x);
             int at = 0;
             bool ok = p.o.wait_ns != 0;
             const uint32_t lead_lane = elect();
             for (; ok && feed.next(); ++at) {
                 const int stage = at % R::kStages;
-                if (at >= R::kStages) ok = wait_phase(&c.freed[stage], (at / R::kStages - 1) & 1, c, p.o.wait_ns);
+                if (at >= R::kStages) ok = wait_phase(&c.freed[stage], (at / R::kStages - 1) & 1, c.dead, p.o.wait_ns);
                 if (!ok) break;
                 if (lead_lane) {
                     mbar_arrive_expect_tx(&c.full[stage], X::kEntryBytes);
@@ -150,10 +144,10 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_prompt_kernel(const __grid_
             // nothing may land in this memory when it has become another CTA's
             if (!ok) drain_copies_call(c.full, at > R::kStages ? at - R::kStages : 0, at, R::kStages);
         } else {
-            Feed<D, Src> feed(p, c.cut, blockIdx.x);
+            Feed<X, Src> feed(p, c.cut, blockIdx.x);
             for (int at = 0; feed.next(); ++at) {
                 const int stage = at % R::kStages;
-                if (!wait_phase(&c.full[stage], (at / R::kStages) & 1, c, p.o.wait_ns)) continue;
+                if (!wait_phase(&c.full[stage], (at / R::kStages) & 1, c.dead, p.o.wait_ns)) continue;
                 const Item& x = feed.x;
                 if (feed.value && x.lo + feed.tile >= x.clear) {
                     char* entry = ring + stage * X::kEntryBytes;
@@ -243,7 +237,7 @@ int launch(const PromptP& base, const uint16_t* k, long long ldk, char* ws, cuda
     }
     Prompt<D> p;
     static_cast<PromptP&>(p) = base;
-    lay_out<D>(ws, &p.o);
+    lay_out<Shape<D>>(ws, &p.o);
     CUtensorMap mk, mv;
     // without any key nothing is loaded, but a map has to describe something: the queries
     const bool none = p.Tk == 0;
@@ -253,11 +247,11 @@ int launch(const PromptP& base, const uint16_t* k, long long ldk, char* ws, cuda
     if (rc) return rc;
     // blocks at most: no more CTAs than that
     const long long blocks = ((long long)p.T * p.G / Shape<D>::kBlock + p.B) * p.H;
-    const bool joins = (p.Tk + kTile - 1) / kTile >= kMinSplit;
+    const bool joins = (p.Tk + kTile - 1) / kTile >= Shape<D>::kMinSplit;
     const int grid = joins || blocks > sms ? sms : (int)blocks;
     rc = launch_early(attn_prompt_kernel<D>, dim3(grid), kThreadsF, R::kSmem, stream, p, mk, mv, joins);
     if (rc || !joins || grid < 2) return rc;
-    return launch_early(flash_join<D, Prompt<D>>, dim3(grid - 1, Shape<D>::kBlock / 32), 128, 0, stream, p);
+    return launch_early(flash_join<Shape<D>, Prompt<D>>, dim3(grid - 1, Shape<D>::kBlock / 32), 128, 0, stream, p);
 }
 
 }  // namespace
@@ -266,9 +260,9 @@ int launch(const PromptP& base, const uint16_t* k, long long ldk, char* ws, cuda
 using namespace edge0;
 
 extern "C" size_t edge0_attn_prompt_workspace_bytes(int head_dim) {
-    return head_dim == 64    ? flash::workspace_bytes<64>()
-           : head_dim == 128 ? flash::workspace_bytes<128>()
-           : head_dim == 256 ? flash::workspace_bytes<256>()
+    return head_dim == 64    ? flash::workspace_bytes<flash::Shape<64>>()
+           : head_dim == 128 ? flash::workspace_bytes<flash::Shape<128>>()
+           : head_dim == 256 ? flash::workspace_bytes<flash::Shape<256>>()
                              : 0;
 }
 

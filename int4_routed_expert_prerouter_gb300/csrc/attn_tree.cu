@@ -1,20 +1,23 @@
 // Attention of drafted tokens over the quantised KV cache: each sequence's rows see its context and,
 // of the tokens drafted behind it, those that a mask names (a tree's ancestors) or those up to
-// themselves.  The mathematics, the blocks and their shares: flash.cuh.
+// themselves.  Blocks of 128 rows (token, head of the group) and their shares: flash.cuh.
 //
-// K and V enter the tensor core as fp16 operands made from the codes in shared memory.
-//   V = fp16(s q + b), the value that edge0_kv_read returns: its rounding weighs as much as that of the weight it meets.
-//   K = fp16(s q + m) + o, m = 1024 s + fp16(-(1024 + z) s) a number near -z s (z half the code range), o = b - m exact in
-//   fp32: what is rounded is the distance from the group's middle, so that an offset shared by the group's
-//   64 dims, whatever its size, takes nothing from it.  1024 s and -(1024 + z) s are what one fused step on codes with
-//   1024 in front of them needs.  o . sum(Q of the group) is one more step of 16 of the scores' product, both
-//   factors split into two fp16 (to 2^-22); a query row is scaled by a power of two before, so that its sums
-//   stay in range whatever its size.  Groups with s above kWide (that step would leave fp16) take code - z + 1/2 and
-//   s apart.
+// K and V enter the tensor core as exact fp16 operands, code - z (z half the code range), so that the weights' rounding
+// to fp16 is the only one beside the result's; an earlier form with the values s q + b themselves as operands
+// was off by 4.3e-4 of the outputs' size against 64 bits, this one by 2.9e-4 (plain form: 2.1e-4).  Per group g of 64 dims
+//   S = sum_g s_g S_g,       S_g = Q_g (code - z) + 64 mean(Q_g) r_g,   r = b / s + z;
+//   o = sum_g P'_g V'_g,     P'_g = fp16(p m_g 2^10),  V' = (code - z) 2^e and r'_g = b / m + z 2^e beside it,
+// s = m 2^e with m in [1, 2): a weight's place in fp16's range does not depend on V's scales.  The mean's and the offsets'
+// products are part of the same matrix steps (one more step of 16 for S, two more columns for o), each factor as
+// two fp16 (2^-22).
 //
-// Warps: 0-7 softmax, 8 the matrix steps, 9 copies strips' halves (16 tokens of K or of V, one run of bytes)
-// into a ring of raw ones, 10-15 turn those into operand entries.  16 tokens of 4-bit codes and 128 dims are
-// 1,152 bytes; raw entries keep about 40 KB under way per SM, which the latency of memory asks for.
+// A step: 64 tokens (32 of 256-wide heads).  Tensor memory holds two buffers of scores (one for 256; weights lie
+// over the scores they come from), the accumulators and, up to 128 dims, the queries; with those in shared
+// memory a step's products would read them from there each time.
+// Warps: 0-7 softmax, 16-row fragments of four rows a lane, so that a token's scales, read from shared memory, serve
+// four rows, and half of a step's tokens each; the block's rows are dealt 16 to a quarter of tensor memory, so that
+// up to 64 rows cost all warps half; 8 the matrix steps; 9 copies strips' halves (16 tokens of K or of V, one run of
+// bytes) into a ring of raw ones; 10-15 turn those into operands and tables.
 #include "flash.cuh"
 
 namespace edge0 {
@@ -22,30 +25,50 @@ namespace {
 
 using namespace flash;
 
-constexpr int kThreadsF = kSoftmax + 256;
 constexpr int kMakers = 6;               // warps that turn codes into operands
+constexpr int kThreadsT = kSoftmax + 64 + 32 * kMakers;
 constexpr int kMaxRaw = 40;              // raw entries
-constexpr float kWide = 48.f;
+constexpr int kExt = 16;                 // columns of V' beside a group's 64 dims
+constexpr float kUpV = 1024.f;           // weights are that many times as large: p <= 2^4, m < 2.2
 
-template <int BITS, int D>
-struct Shapes {
-    using X = Shape<D>;
-    static constexpr int kStages = D == 64 ? 5 : 3;
-    static constexpr int kR = kv::row_bytes(BITS, D), kHalf = kv::half_bytes(BITS, D);
-    static constexpr int kGroups = D / kGroup;
-    static constexpr int kUnits = X::kEntry / kv::kStrip;            // raw entries of an operand entry
-    static constexpr int kXk = X::kEntry * 32;                       // a K entry's offsets
-    // shared memory
-    static constexpr int kXq = X::kStreams * X::kQBytes;
-    static constexpr int kRing = kXq + X::kStreams * kRowsQ * 32;
-    static constexpr int kXkAt = kRing + kStages * X::kEntryBytes;
-    static constexpr int kRaw = kXkAt + kStages * kXk;
-    static constexpr int kRoom = 232448 - 1024 - (int)sizeof(Control) - 2 * kMaxRaw * 8 - kRaw;
+template <int BITS_, int D>
+struct Tile {
+    // what the shares go by
+    static constexpr int kD = D, kBlock = kRowsQ, kTile = D == 256 ? 32 : 64, kEntries = 1, kEntry = kTile, kMinSplit = 8, kMinShare = 4;
+    static constexpr int kBufs = D == 256 ? 1 : 2;                   // of scores
+    __host__ __device__ static constexpr int lead(int) { return kBufs; }
+
+    static constexpr int BITS = BITS_, GR = D / kGroup, kR = kv::row_bytes(BITS, D), kHalf = kv::half_bytes(BITS, D);
+    static constexpr int kUnits = kTile / kv::kStrip;                // raw entries of a tile's K or V
+    static constexpr int kCols = kGroup + kExt;
+    static constexpr bool kQTmem = D <= 128;
+    // TMEM columns
+    static constexpr int kScores = GR * kTile, kO = kBufs * kScores, kQ = kO + GR * kCols, kAll = kQ + (kQTmem ? D / 2 + 8 * GR : 0);
+    static_assert(kAll <= 512, "tensor memory");
+    // shared memory: queries and their means (wide heads), K stages [operand | offsets | table], V stages
+    // [operand with the extra columns | table], raw entries
+    static constexpr int kStages = D == 256 ? 2 : 4;
+    static constexpr int kQBytes = kQTmem ? 0 : kRowsQ * D * 2, kMean = kQTmem ? 0 : GR * kRowsQ * 32;
+    static constexpr int kTable = GR * kTile * 4;
+    static constexpr int kKOffs = kTile * D * 2, kKTab = kKOffs + kTile * 32, kKStage = kKTab + kTable;
+    static constexpr int kVTab = GR * kCols * kTile * 2, kVStage = kVTab + kTable;
+    static constexpr int kK = kQBytes + kMean, kV = kK + kStages * kKStage, kRaw = kV + kStages * kVStage;
+    static constexpr int kControlBytes = 4096;
+    static constexpr int kRoom = 232448 - 128 - kControlBytes - kRaw;
     static constexpr int kRaws = kRoom / kHalf < kMaxRaw ? kRoom / kHalf : kMaxRaw;
-    static constexpr int kControl = kRaw + kRaws * kHalf;
-    static constexpr int kBars = kControl + (int)sizeof(Control);
-    static constexpr int kSmem = kBars + 2 * kMaxRaw * 8 + 1024;
-    static_assert(kRing % 1024 == 0 && kRaw % 16 == 0 && kControl % 16 == 0 && kRaws >= 2 * kUnits && sizeof(Control) % 8 == 0, "layout");
+    static constexpr int kControl = kRaw + kRaws * kHalf, kSmem = kControl + kControlBytes + 128;
+    static_assert(kKStage % 128 == 0 && kVStage % 128 == 0 && kHalf % 16 == 0 && kRaws >= 2 * kUnits, "layout");
+};
+
+struct TreeControl {
+    uint64_t k_full[4], k_freed[4], v_full[4], v_freed[4];           // stages
+    uint64_t raw_full[kMaxRaw], raw_freed[kMaxRaw];
+    uint64_t q_full, s_full[2], p_full[2], o_step[2], o_last, drained;
+    Place cut[2];
+    uint32_t tmem;
+    int dead;
+    int special[16];      // numbers of the share's blocks with NaN of V that some rows do not see, by their last bits
+    float part_max[2][kRowsQ], sums[2][kRowsQ];
 };
 
 struct TreeP {
@@ -62,12 +85,9 @@ struct TreeP {
     int* status;
 };
 
-template <int BITS, int D>
+template <class X>
 struct Tree : TreeP {
-    static constexpr bool kExtra = true, kLooked = false;
-    static constexpr int kHeld = 64;
-    // columns of 4-bit V: the codes of a word in the order that masking gives them
-    __host__ __device__ static constexpr int dim_of(int column) { return BITS == 4 ? (column >> 1) + 4 * (column & 1) : column; }
+    static constexpr int D = X::kD, BITS = X::BITS;
 
     __device__ Seq seq(int b) const {
         Seq s;
@@ -88,25 +108,18 @@ struct Tree : TreeP {
     }
     __device__ int seen(const Seq& s, int token) const { return mask ? s.n_k : min(token + 1 + s.off, s.n_k); }
     __device__ int seen_by_all(const Seq& s, int token) const { return mask ? min(s.ctx, s.n_k) : seen(s, token); }
-
-    struct Row {
-        int n;                           // tokens that the row sees, or with a mask those it may see
-        const unsigned* bits;
-        __device__ Row(const Tree& p, const Item& x, int token)
-            : n(p.seen(x.s, token)), bits(p.mask ? p.mask + (long long)(x.s.q0 + token) * p.words : nullptr) {}
-        __device__ uint32_t seen(const Tree& p, const Item& x, int from) const {
-            const int k = n - from, d = from - x.s.ctx;
-            uint32_t v = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1;
-            if (bits && d > -32) {
-                auto word = [&](int i) -> uint32_t { return i < p.words ? bits[i] : 0u; };
-                // drafted tokens d .. d + 31; those below 0 are the context's
-                v &= d < 0 ? (word(0) << -d) | ((1u << -d) - 1)
-                           : __funnelshift_r(word(d >> 5), word((d >> 5) + 1), d & 31);
-            }
-            return v;
+    // which of the tokens from .. from + 31 a row sees, as bits
+    __device__ uint32_t seen_word(const Item& x, int token, int from) const {
+        const int k = seen(x.s, token) - from, d = from - x.s.ctx;
+        uint32_t v = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1;
+        if (mask && d > -32) {
+            const unsigned* bits = mask + (long long)(x.s.q0 + token) * words;
+            auto word = [&](int i) -> uint32_t { return i < words ? bits[i] : 0u; };
+            // drafted tokens d .. d + 31; those below 0 are the context's
+            v &= d < 0 ? (word(0) << -d) | ((1u << -d) - 1) : __funnelshift_r(word(d >> 5), word((d >> 5) + 1), d & 31);
         }
-    };
-
+        return v;
+    }
     // the half strip that a token lies in
     __device__ const char* place(int b, int h, int token, bool value) const {
         const int pg = token / c.page_tokens, in = token - pg * c.page_tokens;
@@ -118,236 +131,639 @@ struct Tree : TreeP {
         return c.pages + id * c.page_bytes + ((long long)h * (c.page_tokens / kv::kStrip) + in / kv::kStrip) * kv::strip_bytes(BITS, D) +
                (value ? kv::half_bytes(BITS, D) : 0);
     }
-
-    __device__ void load_queries(const Item& x, bool live, int token, int head, char* dst, char* sums, int row, float& cc) const {
-        const uint4* src = reinterpret_cast<const uint4*>(q + (long long)(x.s.q0 + token) * ldq + (long long)head * D);
-        uint32_t top = 0;                                            // largest magnitude's bits, two at a time
-#pragma unroll 8
-        for (int i = 0; i < D / 8; ++i) {
-            const uint4 v = live ? src[i] : make_uint4(0, 0, 0, 0);
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-        }
-        top = max(top & 0xffffu, top >> 16);
-        // the row times 2^e: its largest value in [8, 16) where a normal fp16 factor does that
-        int e = top == 0 ? 0 : 18 - (int)(top >> 10);
-        e = max(-14, min(15, e));
-        const uint32_t f = (uint32_t)(15 + e) << 10, f2x = f | f << 16;
-        cc *= __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll 1
-        for (int g = 0; g < D / kGroup; ++g) {
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                uint4 v = live ? src[8 * g + i] : make_uint4(0, 0, 0, 0);
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    w[k] = hfma2(w[k], f2x, 0x80008000u);            // (a product by a power of two; -0 changes nothing)
-                    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-                    sum += t.x + t.y;
-                }
-                if (BITS == 4)
-                    v = make_uint4(__byte_perm(w[0], w[2], 0x5410), __byte_perm(w[0], w[2], 0x7632), __byte_perm(w[1], w[3], 0x5410),
-                                   __byte_perm(w[1], w[3], 0x7632));
-                else
-                    v = make_uint4(w[0], w[1], w[2], w[3]);
-                *reinterpret_cast<uint4*>(dst + g * (kRowsQ * 128) + swizzled(row, i)) = v;
+    // groups of V with a NaN among the drafted tokens that a row sees, as bits (they enter the product as zeros)
+    __device__ uint32_t nan_groups(const Item& x, int token) const {
+        uint32_t v = 0;
+        for (int j = max(x.s.ctx, x.lo * X::kTile); j < min(x.s.n_k, x.hi * X::kTile); ++j) {
+            if (!(seen_word(x, token, j) & 1)) continue;
+            const char* sb = place(x.b, x.h, j, true) + 16 * X::kR + (j % 16) * kv::sb_bytes(D);
+            for (int g = 0; g < X::GR; ++g) {
+                const __half2 h = reinterpret_cast<const __half2*>(sb)[g];
+                if (__hisnan(__low2half(h)) || __hisnan(__high2half(h))) v |= 1u << g;
             }
-            // (hi, hi / 2^11, what hi leaves) against (offset's hi, 2^11 times what that leaves, hi)
-            const __half hi = __float2half_rn(sum), small = __float2half_rn(__half2float(hi) * 0x1p-11f),
-                         lo = __float2half_rn(sum - __half2float(hi));
-            const __half2 a = __halves2half2(hi, small), b = __halves2half2(lo, __ushort_as_half(0));
-            *reinterpret_cast<uint2*>(sums + tc::kstep_off(row, 4 * g)) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
         }
-    }
-    // NaN of V's groups among the drafted tokens that the row sees (they enter the product as zeros)
-    __device__ void add_special(const Item& x, const Row& r, int, int k, float (&o)[32]) const {
-        for (int j = max(x.s.ctx, x.lo * kTile); j < min(x.s.n_k, x.hi * kTile); ++j) {
-            if (!(r.seen(*this, x, j) & 1)) continue;
-            const __half2 sb = *reinterpret_cast<const __half2*>(place(x.b, x.h, j, true) + 16 * kv::row_bytes(BITS, D) +
-                                                                 (j % 16) * kv::sb_bytes(D) + k / kGroup * 4);
-            if (__hisnan(__low2half(sb)) || __hisnan(__high2half(sb)))
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __int_as_float(0x7fffffff);
-        }
+        return v;
     }
 };
 
-// 1024 + code, two dims a word: 4 bits: dims (0, 4), (1, 5), (2, 6), (3, 7) of the word; 8 bits: in order
-template <int BITS>
-__device__ __forceinline__ void raised(uint32_t w0, uint32_t w1, uint32_t (&r)[4]) {
-    if (BITS == 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = ((w0 >> (4 * i)) & 0x000F000Fu) | 0x64006400u;
-    } else {
-        r[0] = __byte_perm(w0, 0x64646464u, 0x4140);
-        r[1] = __byte_perm(w0, 0x64646464u, 0x4342);
-        r[2] = __byte_perm(w1, 0x64646464u, 0x4140);
-        r[3] = __byte_perm(w1, 0x64646464u, 0x4342);
-    }
+// ------------------------------------------------ fragments, matrix steps ----
+// 16 rows x 8 N columns of fp32: lane (g, t) = (lane / 4, lane % 4) holds of each 8-column block columns 2t, 2t + 1 of
+// row g (r[4j], r[4j + 1]) and of row g + 8 (r[4j + 2], r[4j + 3])
+template <int N>
+__device__ __forceinline__ void ld_frag(uint32_t a, uint32_t (&r)[4 * N]) {
+    static_assert(N == 1 || N == 2 || N == 4, "");
+    if constexpr (N == 4)
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+                     : EDGE0_R4(r, 0), EDGE0_R4(r, 4), EDGE0_R4(r, 8), EDGE0_R4(r, 12)
+                     : "r"(a)
+                     : "memory");
+    else if constexpr (N == 2)
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                     : EDGE0_R4(r, 0), EDGE0_R4(r, 4)
+                     : "r"(a)
+                     : "memory");
+    else
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];\n" : EDGE0_R4(r, 0) : "r"(a) : "memory");
 }
-__device__ __forceinline__ uint32_t twice(__half h) {
-    const __half2 v = __halves2half2(h, h);
-    return *reinterpret_cast<const uint32_t*>(&v);
+__device__ __forceinline__ void st_frag2(uint32_t a, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(a), EDGE0_I4(r, 0), EDGE0_I4(r, 4)
+                 : "memory");
+}
+// 16 rows x 8 N columns of fp16 in pairs: of each 8-column block row g (r[2j]) and row g + 8 (r[2j + 1])
+template <int N>
+__device__ __forceinline__ void st_pairs(uint32_t a, const uint32_t (&r)[2 * N]) {
+    if constexpr (N == 4)
+        asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(a), EDGE0_I4(r, 0), EDGE0_I4(r, 4)
+                     : "memory");
+    else
+        asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), EDGE0_I4(r, 0) : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(a), EDGE0_I4(r, 0), EDGE0_I4(r, 4)
+                 : "memory");
+}
+// whether any of the 64 threads that meet at a barrier wants it
+__device__ __forceinline__ bool any_of_64(int barrier, bool want) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)want), "r"(barrier)
+        : "memory");
+    return r != 0;
+}
+// an operand's descriptor without swizzle: 8 x 16-byte blocks, `leading` in the low word and `stride` apart
+__device__ __forceinline__ uint64_t desc_plain(uint32_t lo, uint32_t stride) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"((stride >> 4) | (1u << 14)));
+    return d;
+}
+// v = hi + lo 2^-k: two fp16 in one word, lo of 2^k times what hi leaves
+template <int K>
+__device__ __forceinline__ uint32_t split(float v) {
+    const __half hi = __float2half_rn(v);
+    const __half2 r = __halves2half2(hi, __float2half_rn((v - __half2float(hi)) * (float)(1 << K)));
+    return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// A raw entry (16 tokens) into rows row0 .. row0 + 15 of an operand entry, by a warp.  V's tokens from `left` on are zeros,
-// and so are groups of NaN from `drafted` on, which some rows may not see: true where there are any.
-template <int BITS, int D>
-__device__ __forceinline__ bool make_rows(const char* raw, char* entry, char* offsets, int row0, bool value, int left, int drafted) {
-    using Z = Shapes<BITS, D>;
-    constexpr int CH = Z::kR / 16, kPer = BITS == 4 ? 4 : 2;         // pieces of a row, 8-dim words per piece
+// ----------------------------------------------------------------- makers ----
+// (code - z) 2^e of 8 dims, e <= 5 (or, in two steps, up to where that leaves fp16); 4 bits: one word, dims in the order
+// 0 4 1 5 2 6 3 7; 8 bits: two words, in order.  0x6400 is 1024: a code below it adds itself, a nibble 4 bits up 16
+// times itself.  one: 2^e, or 0 for a group that has to come out as zeros.
+template <int BITS>
+__device__ __forceinline__ uint4 codes8(uint32_t w0, uint32_t w1, int e, bool none) {
+    const uint32_t up = (uint32_t)(e << 10) * 0x10001u;
+    const uint32_t m0 = none ? 0u : 0x3C003C00u + up, a0 = none ? 0u : (BITS == 4 ? 0xE408E408u : 0xE480E480u) + up;
+    uint4 r;
+    if (BITS == 4) {
+        const uint32_t m1 = none ? 0u : 0x2C002C00u + up, a1 = none ? 0u : 0xD480D480u + up, h = w0 >> 8;
+        r.x = hfma2((w0 & 0x000F000Fu) | 0x64006400u, m0, a0);
+        r.y = hfma2((w0 & 0x00F000F0u) | 0x64006400u, m1, a1);
+        r.z = hfma2((h & 0x000F000Fu) | 0x64006400u, m0, a0);
+        r.w = hfma2((h & 0x00F000F0u) | 0x64006400u, m1, a1);
+    } else {
+        r.x = hfma2(__byte_perm(w0, 0x64646464u, 0x4140), m0, a0);
+        r.y = hfma2(__byte_perm(w0, 0x64646464u, 0x4342), m0, a0);
+        r.z = hfma2(__byte_perm(w1, 0x64646464u, 0x4140), m0, a0);
+        r.w = hfma2(__byte_perm(w1, 0x64646464u, 0x4342), m0, a0);
+    }
+    return r;
+}
+
+// A raw entry (16 tokens, the tile's from row0 on) into operands and tables, by a warp.  Tokens from `left` on come out as
+// zeros, and so do V's groups of NaN from `drafted` on, which some rows may not see (true: there were any).
+template <class X>
+__device__ __forceinline__ bool make_rows(const char* raw, char* stage, int row0, bool value, float c, int left, int drafted) {
+    constexpr int BITS = X::BITS, CH = X::kR / 16, CPG = CH / X::GR, T = X::kTile;
+    constexpr int kPer = BITS == 4 ? 4 : 2, kW = BITS == 4 ? 1 : 2;  // 8-dim words per piece, 32-bit words of one
     constexpr float kZ = BITS == 4 ? 8.f : 128.f;
+    constexpr int kMostE = BITS == 4 ? 12 : 8, kFastE = 5;
     const int lane = threadIdx.x & 31;
     bool found = false;
 #pragma unroll
     for (int j = 0; j < CH / 2; ++j) {
-        const int i = j * 32 + lane, c = (i >> 3) % CH, tok = (i & 7) + 8 * ((i >> 3) / CH), g = c / (CH / Z::kGroups);
-        const uint4 codes = *reinterpret_cast<const uint4*>(raw + tok * Z::kR + ((c ^ kv::turn(Z::kR, tok)) << 4));
-        const __half2 sb = *reinterpret_cast<const __half2*>(raw + 16 * Z::kR + tok * kv::sb_bytes(D) + g * 4);
+        const int i = j * 32 + lane, p = (i >> 3) % CH, tok = (i & 7) + 8 * ((i >> 3) / CH), g = p / CPG, row = row0 + tok;
+        const uint4 codes = *reinterpret_cast<const uint4*>(raw + tok * X::kR + ((p ^ kv::turn(X::kR, tok)) << 4));
+        const uint32_t sbw = *reinterpret_cast<const uint32_t*>(raw + 16 * X::kR + tok * kv::sb_bytes(X::kD) + g * 4);
+        const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&sbw));
         const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-        const __half s = __low2half(sb), b = __high2half(sb);
-        const float sf = __half2float(s), bf = __half2float(b);
-        const int row = row0 + tok;
-        uint4 out[kPer];
-        const uint32_t s2 = twice(s);
-        if (value) {
-            const bool hidden = tok >= left, bad = tok >= drafted && (sf != sf || bf != bf);
-            found = found || (bad && !hidden);
-            const uint32_t b2 = twice(b), keep = hidden || bad ? 0u : 0xffffffffu;
+        const bool none = tok >= left, flat = sb.x == 0.f, first = p % CPG == 0;
+        const int pair = (row >> 1) * 2 * X::GR + 2 * g + (row & 1);
+        if (!value) {
 #pragma unroll
             for (int x = 0; x < kPer; ++x) {
-                uint32_t r[4];
-                raised<BITS>(w[BITS == 4 ? x : 2 * x], w[BITS == 4 ? x : 2 * x + 1], r);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) r[k] = hfma2(hadd2(r[k], 0xE400E400u), s2, b2) & keep;
-                out[x] = make_uint4(r[0], r[1], r[2], r[3]);
+                const int c8 = p * kPer + x;                         // 8 dims
+                *reinterpret_cast<uint4*>(stage + (c8 >> 1) * (T * 32) + tc::kstep_off(row, (c8 & 1) * 8)) =
+                    codes8<BITS>(w[x * kW], w[x * kW + kW - 1], -10, false);
+            }
+            if (first) {
+                // b = 1 (0 - z + b + z) of a constant group
+                const float off = none ? 0.f : flat ? sb.y + kZ : __fdividef(sb.y, sb.x) + kZ;
+                reinterpret_cast<float*>(stage + X::kKTab)[pair] = none ? 0.f : (flat ? 1.f : sb.x) * c * 1024.f;
+                // (hi, 2^11 lo) of the mean against (off, off / 2^11), then against what these leave
+                const uint32_t a = split<0>(off * (kGroup / 1024.f)), b = split<0>(off * (kGroup / 1024.f / 2048.f));
+                *reinterpret_cast<uint2*>(stage + X::kKOffs + tc::kstep_off(row, 4 * g)) =
+                    make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
             }
         } else {
-            const bool wide = sf > kWide;
-            const __half e16 = __float2half_rn(-(1024.f + kZ) * sf);
-            const uint32_t e2 = twice(e16);
+            const bool nan = sb.x != sb.x || sb.y != sb.y, out = none || (nan && tok >= drafted);
+            found = found || (nan && !none && tok >= drafted);
+            int e = (int)((sbw >> 10) & 31) - 15;
+            e = max(-10, min(kMostE, e));
+            const bool zeros = out || nan || flat;
 #pragma unroll
             for (int x = 0; x < kPer; ++x) {
-                uint32_t r[4];
-                raised<BITS>(w[BITS == 4 ? x : 2 * x], w[BITS == 4 ? x : 2 * x + 1], r);
-                if (!wide) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) r[k] = hfma2(r[k], s2, e2);
-                } else {
-                    const uint32_t z2 = twice(__float2half_rn(0.5f - kZ));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) r[k] = hfma2(hadd2(hadd2(r[k], 0xE400E400u), z2), s2, 0x80008000u);
+                const int c8 = p * kPer + x;
+                uint4 v = codes8<BITS>(w[x * kW], w[x * kW + kW - 1], min(e, kFastE), zeros);
+                if (e > kFastE) {
+                    const uint32_t up = (uint32_t)(0x3C00 + ((e - kFastE) << 10)) * 0x10001u;
+                    v.x = hfma2(v.x, up, 0x80008000u);
+                    v.y = hfma2(v.y, up, 0x80008000u);
+                    v.z = hfma2(v.z, up, 0x80008000u);
+                    v.w = hfma2(v.w, up, 0x80008000u);
                 }
-                out[x] = make_uint4(r[0], r[1], r[2], r[3]);
+                *reinterpret_cast<uint4*>(stage + (g * (X::kCols / 8) + (c8 & 7)) * (T * 16) + row * 16) = v;
             }
-            if (c % (CH / Z::kGroups) == 0) {
-                const float off = wide ? fmaf(kZ - 0.5f, sf, bf) : bf - fmaf(1024.f, sf, __half2float(e16));
-                const __half hi = __float2half_rn(off), lo = __float2half_rn((off - __half2float(hi)) * 2048.f);
-                const __half2 p = __halves2half2(hi, lo), q = __halves2half2(hi, __ushort_as_half(0));
-                *reinterpret_cast<uint2*>(offsets + tc::kstep_off(row, 4 * g)) =
-                    make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+            if (first) {
+                const float m = out ? 0.f : nan ? __int_as_float(0x7fffffff) : flat ? 1.f : sb.x * __uint_as_float((uint32_t)(127 - e) << 23);
+                const float r = out || nan ? 0.f : flat ? sb.y : __fdividef(sb.y, m) + kZ * __uint_as_float((uint32_t)(127 + e) << 23);
+                reinterpret_cast<float*>(stage + X::kVTab)[pair] = m * kUpV;
+                *reinterpret_cast<uint4*>(stage + (g * (X::kCols / 8) + 8) * (T * 16) + row * 16) = make_uint4(split<0>(r), 0, 0, 0);
             }
-        }
-#pragma unroll
-        for (int x = 0; x < kPer; ++x) {
-            const int c8 = c * kPer + x;                             // 8 dims
-            *reinterpret_cast<uint4*>(entry + (c8 >> 3) * (Shape<D>::kEntry * 128) + swizzled(row, c8 & 7)) = out[x];
         }
     }
     return found;
 }
 
-template <int BITS, int D>
-__global__ void __launch_bounds__(kThreadsF, 1) attn_tree_kernel(const __grid_constant__ Tree<BITS, D> p, bool joins) {
-    using X = Shape<D>;
-    using Z = Shapes<BITS, D>;
-    using Src = Tree<BITS, D>;
+// ------------------------------------------------- the softmax warps ----
+template <class X>
+__device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, char* smem) {
+    constexpr int D = X::kD, GR = X::GR, T = X::kTile, NB = T / 16;             // 8-token blocks of a warp's half
+    const int wid = threadIdx.x >> 5, hf = wid >> 2, quad = wid & 3, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t tm = c.tmem + ((uint32_t)(32 * quad) << 16);
+    const unsigned long long limit = p.o.wait_ns;
+    // row 2 rh + k of a lane: fragment row g + 8 k of the quarter's half rh
+    auto local_of = [&](int r) { return 64 * (r >> 1) + 16 * quad + g + 8 * (r & 1); };
+    Walk<X, Tree<X>> walk(p, c.cut, blockIdx.x);
+    Item x;
+    int base = 0, blocks = 0, number = 0;
+    while (walk.next(x)) {
+        const int n = x.hi - x.lo;
+        const bool both = x.rows > 64;                               // else no row lies in the second half
+        bool ok = true;
+        if (n > 0) {
+            ++number;
+            // queries: a thread has a row's dims of some groups
+            const int local = 64 * (lane >> 4) + 16 * quad + (lane & 15);
+            const bool live = local < x.rows;
+            const int at = x.row0 + (live ? local : 0), token = at / p.G, head = x.h * p.G + at - token * p.G;
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(x.s.q0 + token) * p.ldq + (long long)head * D);
+#pragma unroll 1
+            for (int gr = hf; gr < GR; gr += 2) {
+                uint4 v[8];
+                uint32_t w[32];
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = live ? src[8 * gr + i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t q4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&q4[k]));
+                        sum += f.x + f.y;
+                    }
+                    w[4 * i] = X::BITS == 4 ? __byte_perm(v[i].x, v[i].z, 0x5410) : v[i].x;
+                    w[4 * i + 1] = X::BITS == 4 ? __byte_perm(v[i].x, v[i].z, 0x7632) : v[i].y;
+                    w[4 * i + 2] = X::BITS == 4 ? __byte_perm(v[i].y, v[i].w, 0x5410) : v[i].z;
+                    w[4 * i + 3] = X::BITS == 4 ? __byte_perm(v[i].y, v[i].w, 0x7632) : v[i].w;
+                }
+                // A mean is a multiple of 2^-30 (the queries' step is 2^-24 at least), 2^11 times what its first fp16 leaves one
+                // of 2^-19: exact, or within 2^-24 of the mean, however small the queries.
+                const uint32_t hl = split<11>(sum * (1.f / kGroup));
+                if constexpr (X::kQTmem) {
+                    uint32_t ext[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) ext[i] = i >> 1 == gr ? hl : 0u;
+                    tmem_st32(tm + X::kQ + gr * 32, w);
+                    tmem_st8(tm + X::kQ + GR * 32 + gr * 8, ext);
+                } else {
+                    const int row = 32 * quad + lane;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4*>(smem + (4 * gr + (i >> 1)) * (kRowsQ * 32) + tc::kstep_off(row, (i & 1) * 8)) =
+                            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    *reinterpret_cast<uint2*>(smem + X::kQBytes + gr * (kRowsQ * 32) + tc::kstep_off(row, 4 * gr)) = make_uint2(hl, hl);
+                }
+            }
+            if (X::kQTmem) tmem_wait_st();
+            else tc::fence_async_smem();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.q_full);
+        }
+        // of each row: reference mu (exponent units; not set while the row has seen nothing), sum
+        float mu[4] = {0.f, 0.f, 0.f, 0.f}, l[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t unset = 15;
+        for (int j = 0; j < n; ++j) {
+            const int tile = base + j, stage = tile % X::kStages, buf = tile % X::kBufs, tile_at = x.lo + j;
+            const uint32_t parity = (tile / X::kStages) & 1;
+            const char *sk = smem + X::kK + stage * X::kKStage, *sv = smem + X::kV + stage * X::kVStage;
+            const uint32_t s_at = tm + buf * X::kScores;
+            // (after a wait that gave up the warp goes on with what is there: pairs of warps meet at barriers, and the rows are
+            // marked in the end)
+            ok = wait_phase(&c.k_full[stage], parity, c.dead, limit) && ok;
+            ok = wait_phase(&c.s_full[buf], (tile / X::kBufs) & 1, c.dead, limit) && ok;
+            tc::fence_after_sync();
+            f2 S[2][NB][2];                                          // [rh][8 tokens][k]: tokens 2t, 2t + 1
+            const float* mk = reinterpret_cast<const float*>(sk + X::kKTab) + (hf * (T / 4) + t) * 2 * GR;
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr) {
+                f2 s2[NB];                                           // a token's scale serves the lane's four rows
+#pragma unroll
+                for (int b = 0; b < NB; ++b) s2[b] = *reinterpret_cast<const f2*>(mk + b * 8 * GR + 2 * gr);
+                uint32_t raw[2][4 * NB];
+                ld_frag<NB>(s_at + gr * T + hf * (T / 2), raw[0]);
+                if (both) ld_frag<NB>(s_at + (16u << 16) + gr * T + hf * (T / 2), raw[1]);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int rh = 0; rh < 2; ++rh) {
+                    if (rh && !both) continue;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const f2 v = pk(__uint_as_float(raw[rh][4 * b + 2 * k]), __uint_as_float(raw[rh][4 * b + 2 * k + 1]));
+                            S[rh][b][k] = fma2(v, s2[b], gr ? S[rh][b][k] : pk(-mu[2 * rh + k], -mu[2 * rh + k]));
+                        }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.k_freed[stage]);
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int rh = 0; rh < 2; ++rh) {
+                if (rh && !both) continue;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int r = 2 * rh + k;
+                    if (tile_at >= x.clear) {
+                        const int local = local_of(r);
+                        const uint32_t seen =
+                            local < x.rows ? p.seen_word(x, (x.row0 + local) / p.G, tile_at * T + hf * (T / 2)) >> (2 * t) : 0u;
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            float u, v;
+                            unpk(S[rh][b][k], u, v);
+                            S[rh][b][k] = pk((seen >> (8 * b)) & 1 ? u : -INFINITY, (seen >> (8 * b)) & 2 ? v : -INFINITY);
+                        }
+                    }
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        float u, v;
+                        unpk(S[rh][b][k], u, v);
+                        mx[r] = fmaxf(mx[r], fmaxf(u, v));
+                    }
+                }
+            }
+            bool want = false;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) want = want || mx[r] > ((unset >> r) & 1 ? -INFINITY : kRise);
+            if (any_of_64(4 + quad, want)) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+                    if (t == 0) c.part_max[hf][local_of(r)] = mx[r];
+                }
+                named_bar_sync(8 + quad, 64);
+                float f[4];
+                bool move = false;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float most = fmaxf(mx[r], c.part_max[hf ^ 1][local_of(r)]);
+                    const bool fresh = (unset >> r) & 1, moves = most > (fresh ? -INFINITY : kRise);
+                    const float by = moves ? most : 0.f;
+                    f[r] = !moves ? 1.f : fresh ? 0.f : ex2(-by);
+                    if (moves) unset &= ~(1u << r);
+                    move = move || moves;
+                    mu[r] += by;
+                    l[r] *= f[r];
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        if (r < 2 || both) S[r >> 1][b][r & 1] = add2(S[r >> 1][b][r & 1], pk(-by, -by));
+                }
+                // (the block's first tile overwrites the accumulators)
+                if (j > 0 && __any_sync(0xffffffffu, move)) {
+                    if (X::kBufs == 2) {        // (one buffer: the product was over before these scores were formed)
+                        ok = wait_phase(&c.o_step[(tile - 1) & 1], ((tile - 1) >> 1) & 1, c.dead, limit) && ok;
+                        tc::fence_after_sync();
+                    }
+#pragma unroll 1
+                    for (int q = hf; q < GR * (X::kCols / 16); q += 2)
+#pragma unroll 1
+                        for (int rh = 0; rh < (both ? 2 : 1); ++rh) {
+                            uint32_t a[8];
+                            const uint32_t o_at = tm + ((uint32_t)(16 * rh) << 16) + X::kO + 16 * q;
+                            ld_frag<2>(o_at, a);
+                            tc::tmem_wait_ld();
+                            const float f0 = rh ? f[2] : f[0], f1 = rh ? f[3] : f[1];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) a[i] = __float_as_uint(__uint_as_float(a[i]) * (i & 2 ? f1 : f0));
+                            st_frag2(o_at, a);
+                        }
+                }
+            }
+#pragma unroll
+            for (int rh = 0; rh < 2; ++rh) {
+                if (rh && !both) continue;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    f2 sum = 0;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        float u, v;
+                        unpk(S[rh][b][k], u, v);
+                        S[rh][b][k] = pk(ex2(u), ex2(v));
+                        sum = b ? add2(sum, S[rh][b][k]) : S[rh][b][k];
+                    }
+                    float u, v;
+                    unpk(sum, u, v);
+                    l[2 * rh + k] += u + v;
+                }
+            }
+            ok = wait_phase(&c.v_full[stage], parity, c.dead, limit) && ok;
+            const float* mv = reinterpret_cast<const float*>(sv + X::kVTab) + (hf * (T / 4) + t) * 2 * GR;
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr) {
+                f2 m2[NB];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) m2[b] = *reinterpret_cast<const f2*>(mv + b * 8 * GR + 2 * gr);
+#pragma unroll
+                for (int rh = 0; rh < 2; ++rh) {
+                    if (rh && !both) continue;
+                    uint32_t w[2 * NB];
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float u, v;
+                            unpk(mul2(S[rh][b][k], m2[b]), u, v);
+                            w[2 * b + k] = pack2(u, v);
+                        }
+                    st_pairs<NB>(s_at + ((uint32_t)(16 * rh) << 16) + gr * T + hf * (T / 2), w);
+                }
+            }
+            tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.p_full[buf]);
+        }
+        base += n;
+        uint32_t nans[4] = {0, 0, 0, 0};
+        if (n > 0) {
+            ok = wait_phase(&c.o_last, blocks++ & 1, c.dead, limit) && ok;
+            tc::fence_after_sync();
+            const bool special = *(volatile int*)&c.special[number & 15] == number;
+            // a row's sum: its 4 lanes, then both halves of the tokens
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+                if (!ok) l[r] = __int_as_float(0x7fffffff);
+                if (t == 0) c.sums[hf][local_of(r)] = l[r];
+            }
+            named_bar_sync(8 + quad, 64);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                l[r] += c.sums[hf ^ 1][local_of(r)];
+                if (special && local_of(r) < x.rows) nans[r] = p.nan_groups(x, (x.row0 + local_of(r)) / p.G);
+            }
+        }
+        const bool whole = x.part < 0;
+#pragma unroll
+        for (int rh = 0; rh < 2; ++rh) {
+            if (rh && !both) continue;
+#pragma unroll 1
+            for (int q = hf; q < D / 32; q += 2) {
+                const int gr = q >> 1;
+                uint32_t a[16], ext[4];
+                float add[2] = {0.f, 0.f};
+                if (n > 0) {
+                    const uint32_t o_at = tm + ((uint32_t)(16 * rh) << 16) + X::kO + gr * X::kCols;
+                    ld_frag<4>(o_at + (q & 1) * 32, a);
+                    ld_frag<1>(o_at + kGroup, ext);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        add[k] = __shfl_sync(0xffffffffu, __uint_as_float(ext[2 * k]) + __uint_as_float(ext[2 * k + 1]), lane & 28);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) a[i] = 0u;
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int r = 2 * rh + k, local = local_of(r);
+                    if (local >= x.rows) continue;
+                    const float sum = l[r];
+                    float f = whole ? (sum == 0.f ? 0.f : 1.f / (sum * kUpV)) : 1.f / kUpV;
+                    if (sum != sum) f = sum;
+                    if ((nans[r] >> gr) & 1) f = __int_as_float(0x7fffffff);
+                    const int at = x.row0 + local, token = at / p.G, head = x.h * p.G + at - token * p.G;
+                    __half* out = p.o.out + (long long)(x.s.q0 + token) * p.o.ldo + (long long)head * D + 32 * q;
+                    float* part = p.o.part_o + ((long long)x.part * X::kBlock + local) * D + 32 * q;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const float u = (__uint_as_float(a[4 * b + 2 * k]) + add[k]) * f, v = (__uint_as_float(a[4 * b + 2 * k + 1]) + add[k]) * f;
+                        if (X::BITS == 4) {                          // columns 2t, 2t + 1 hold dims t, t + 4
+                            if (whole) {
+                                out[8 * b + t] = __float2half_rn(u);
+                                out[8 * b + t + 4] = __float2half_rn(v);
+                            } else {
+                                part[8 * b + t] = u;
+                                part[8 * b + t + 4] = v;
+                            }
+                        } else if (whole) {
+                            *reinterpret_cast<uint32_t*>(out + 8 * b + 2 * t) = pack2(u, v);
+                        } else {
+                            *reinterpret_cast<float2*>(part + 8 * b + 2 * t) = make_float2(u, v);
+                        }
+                    }
+                }
+            }
+            if (!whole && hf == 0 && t == 0)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int r = 2 * rh + k;
+                    if (local_of(r) < x.rows)
+                        p.o.part_ml[(long long)x.part * X::kBlock + local_of(r)] = make_float2((unset >> r) & 1 ? -INFINITY : mu[r], l[r]);
+                }
+        }
+        tc::fence_before_sync();
+    }
+}
+
+// -------------------------------------------------------- the matrix warp ----
+template <class X>
+__device__ __forceinline__ void tree_matrix(const Tree<X>& p, TreeControl& c, char* smem) {
+    constexpr int GR = X::GR, T = X::kTile;
+    const uint32_t tm = c.tmem, lead_lane = elect();
+    const uint32_t k0 = smem_u32(smem + X::kK), v0 = smem_u32(smem + X::kV), q0 = smem_u32(smem);
+    const unsigned long long limit = p.o.wait_ns;
+    Walk<X, Tree<X>> walk(p, c.cut, blockIdx.x);
+    Item x;
+    int base = 0, blocks = 0;
+    auto scores = [&](int tile) {
+        const int stage = tile % X::kStages, buf = tile % X::kBufs;
+        if (!wait_phase(&c.k_full[stage], (tile / X::kStages) & 1, c.dead, limit)) return;
+        tc::fence_after_sync();
+        const uint32_t b = desc_lo(k0 + stage * X::kKStage, tc::kLbo), offs = desc_lo(k0 + stage * X::kKStage + X::kKOffs, tc::kLbo);
+#pragma unroll
+        for (int gr = 0; gr < GR; ++gr) {
+            const uint32_t d = tm + buf * X::kScores + gr * T;
+#pragma unroll
+            for (int ks = 0; ks < 5; ++ks) {                         // four of the dims, one of the mean
+                const uint64_t bd = desc_plain(ks < 4 ? b + (4 * gr + ks) * (T * 32 / 16) : offs, tc::kSbo);
+                if constexpr (X::kQTmem)
+                    mma_ts(d, tm + X::kQ + (ks < 4 ? gr * 32 + 8 * ks : GR * 32 + gr * 8), bd, tc::idesc_f16(kRowsQ, T), ks > 0, lead_lane);
+                else
+                    mma_ss(d, tc::smem_desc(q0 + (ks < 4 ? (4 * gr + ks) * (kRowsQ * 32) : X::kQBytes + gr * (kRowsQ * 32))), bd,
+                           tc::idesc_f16(kRowsQ, T), ks > 0, lead_lane);
+            }
+        }
+        commit(&c.k_freed[stage], lead_lane);
+        commit(&c.s_full[buf], lead_lane);
+    };
+    auto values = [&](int tile, bool first, bool last) {
+        const int stage = tile % X::kStages, buf = tile % X::kBufs;
+        if (!wait_phase(&c.p_full[buf], (tile / X::kBufs) & 1, c.dead, limit)) return;
+        if (!wait_phase(&c.v_full[stage], (tile / X::kStages) & 1, c.dead, limit)) return;
+        tc::fence_after_sync();
+        const uint32_t b = desc_lo(v0 + stage * X::kVStage, 128);
+#pragma unroll
+        for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+            for (int kk = 0; kk < T / 16; ++kk)
+                mma_ts(tm + X::kO + gr * X::kCols, tm + buf * X::kScores + gr * T + (kk / (T / 32)) * (T / 2) + (kk % (T / 32)) * 8,
+                       desc_plain(b + (gr * X::kCols * T * 2 + kk * 256) / 16, T * 16), tc::idesc_f16(kRowsQ, X::kCols) | (1u << 16),
+                       !first || kk > 0, lead_lane);
+        commit(&c.v_freed[stage], lead_lane);
+        commit(&c.o_step[buf], lead_lane);
+        if (last) commit(&c.o_last, lead_lane);
+    };
+    while (walk.next(x)) {
+        const int n = x.hi - x.lo;
+        if (n == 0) continue;
+        wait_phase(&c.q_full, blocks++ & 1, c.dead, limit);
+        tc::fence_after_sync();
+        scores(base);
+        for (int j = 0; j < n; ++j) {
+            if (X::kBufs == 2 && j + 1 < n) scores(base + j + 1);
+            values(base + j, j == 0, j + 1 == n);
+            if (X::kBufs == 1 && j + 1 < n) scores(base + j + 1);
+        }
+        base += n;
+    }
+}
+
+template <class X>
+__global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_constant__ Tree<X> p, bool joins) {
     extern __shared__ char start[];
-    char* smem = start + ((1024 - (smem_u32(start) & 1023)) & 1023);
-    Control& c = *reinterpret_cast<Control*>(smem + Z::kControl);
-    uint64_t *raw_full = reinterpret_cast<uint64_t*>(smem + Z::kBars), *raw_freed = raw_full + kMaxRaw;
+    char* smem = start + ((128 - (smem_u32(start) & 127)) & 127);
+    static_assert(sizeof(TreeControl) <= X::kControlBytes, "control");
+    TreeControl& c = *reinterpret_cast<TreeControl*>(smem + X::kControl);
     const int wid = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const unsigned long long limit = p.o.wait_ns;
     if (wid == 8) {
         tc::tmem_alloc(&c.tmem, 512);
         tc::tmem_relinquish();
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < Z::kRaws; ++i) {
-            mbar_init(&raw_full[i], 1);
-            mbar_init(&raw_freed[i], 1);
+        for (int i = 0; i < X::kStages; ++i) {
+            mbar_init(&c.k_full[i], X::kUnits);
+            mbar_init(&c.k_freed[i], 1 + kSoftmax / 32);             // the matrix steps, and the warps that read the table
+            mbar_init(&c.v_full[i], X::kUnits);
+            mbar_init(&c.v_freed[i], 1);
         }
-        control_init(c, Z::kUnits, 1, 1, p.o.wait_ns == 0);
+        for (int i = 0; i < X::kRaws; ++i) {
+            mbar_init(&c.raw_full[i], 1);
+            mbar_init(&c.raw_freed[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c.s_full[i], 1);
+            mbar_init(&c.p_full[i], kSoftmax / 32);
+            mbar_init(&c.o_step[i], 1);
+        }
+        mbar_init(&c.q_full, kSoftmax / 32);
+        mbar_init(&c.o_last, 1);
+        mbar_init(&c.drained, 1);
+        fence_mbar_init();
+        for (int i = 0; i < 16; ++i) c.special[i] = 0;
+        c.dead = limit == 0;                                         // (limit 0: given up from the start)
     }
-    // the steps of 16 for the offsets: zero where nothing is written later
-    for (int i = threadIdx.x; i < (Z::kRing - Z::kXq) / 16; i += kThreadsF) reinterpret_cast<uint4*>(smem + Z::kXq)[i] = make_uint4(0, 0, 0, 0);
-    for (int i = threadIdx.x; i < (Z::kRaw - Z::kXkAt) / 16; i += kThreadsF) reinterpret_cast<uint4*>(smem + Z::kXkAt)[i] = make_uint4(0, 0, 0, 0);
+    // means, offsets and V's extra columns: zero where nothing is written later
+    for (int i = X::kQBytes / 16 + threadIdx.x; i < X::kRaw / 16; i += kThreadsT) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     tc::fence_async_smem();
     tc::fence_before_sync();
     wait_predecessor();
     launch_dependents();
-    find_share<D>(static_cast<const Src&>(p), blockIdx.x, gridDim.x, reinterpret_cast<long long*>(smem), c.cut);
+    find_share<X>(static_cast<const Tree<X>&>(p), blockIdx.x, gridDim.x, reinterpret_cast<long long*>(smem + X::kRaw), c.cut);
     tc::fence_after_sync();
     if (joins && threadIdx.x == 0) p.o.places[blockIdx.x] = c.cut[0];
     if (blockIdx.x == 0 && threadIdx.x < p.B && p.status && p.over(threadIdx.x)) atomicExch(p.status, EDGE0_EINVAL);
 
-    // registers: 256 x 168 + 256 x 88, what the CTA was launched with (512 x 128)
     if (wid < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n");
-        softmax_warps<D, Src>(p, c, smem, smem + Z::kXq);
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-        if (wid == 8) {
-            matrix_warp<D, Z::kStages, Src>(p, c, smem_u32(smem), smem_u32(smem + Z::kRing), smem_u32(smem + Z::kXq), smem_u32(smem + Z::kXkAt));
-        } else if (wid == 9) {
-            Feed<D, Src> feed(p, c.cut, blockIdx.x);
-            int unit = 0;
-            bool ok = p.o.wait_ns != 0, more = feed.next();
-            // a lane: one of the entry's strips; behind the last token, that token's
-            auto source = [&]() { return p.place(feed.x.b, feed.x.h, min(feed.token() + 16 * (lane % Z::kUnits), feed.x.s.n_k - 1), feed.value); };
-            const char* src = more ? source() : nullptr;
-            while (ok && more) {
-                const int u = unit + lane % Z::kUnits, slot = u % Z::kRaws;
-                const char* from = src;
-                more = feed.next();
-                if (more) src = source();                            // on its way during the wait
-                // (the phase before a barrier's first counts as over)
-                ok = wait_phase(&raw_freed[slot], (u / Z::kRaws + 1) & 1, c, p.o.wait_ns);
-                if (!ok) break;
-                if (lane < Z::kUnits) {
-                    mbar_arrive_expect_tx(&raw_full[slot], Z::kHalf);
-                    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
-                                     smem_u32(smem + Z::kRaw + slot * Z::kHalf)),
-                                 "l"(from), "r"((uint32_t)Z::kHalf), "r"(smem_u32(&raw_full[slot]))
-                                 : "memory");
-                }
-                __syncwarp();
-                unit += Z::kUnits;
+        tree_softmax<X>(p, c, smem);
+    } else if (wid == 8) {
+        tree_matrix<X>(p, c, smem);
+    } else if (wid == 9) {
+        Feed<X, Tree<X>> feed(p, c.cut, blockIdx.x);
+        int unit = 0;
+        bool ok = limit != 0, more = feed.next();
+        // a lane: one of the tile's strips; behind the last token, that token's
+        auto source = [&]() { return p.place(feed.x.b, feed.x.h, min(feed.token() + 16 * (lane % X::kUnits), feed.x.s.n_k - 1), feed.value); };
+        const char* src = more ? source() : nullptr;
+        while (ok && more) {
+            const int u = unit + lane % X::kUnits, slot = u % X::kRaws;
+            const char* from = src;
+            more = feed.next();
+            if (more) src = source();                                // on its way during the wait
+            // (the phase before a barrier's first counts as over)
+            ok = wait_phase(&c.raw_freed[slot], (u / X::kRaws + 1) & 1, c.dead, limit);
+            if (!ok) break;
+            if (lane < X::kUnits) {
+                mbar_arrive_expect_tx(&c.raw_full[slot], X::kHalf);
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                                 smem_u32(smem + X::kRaw + slot * X::kHalf)),
+                             "l"(from), "r"((uint32_t)X::kHalf), "r"(smem_u32(&c.raw_full[slot]))
+                             : "memory");
             }
-            // nothing may land in this memory when it has become another CTA's
-            if (!ok) drain_copies_call(raw_full, unit > Z::kRaws ? unit - Z::kRaws : 0, unit, Z::kRaws);
-        } else {
-            Feed<D, Src> feed(p, c.cut, blockIdx.x);
-            int unit = 0;
-            for (int at = 0; feed.next(); ++at, unit += Z::kUnits) {
-                const int stage = at % Z::kStages;
-                const Item& x = feed.x;
-                bool ready = at < Z::kStages;
-                for (int i = (wid - 10 + kMakers - unit % kMakers) % kMakers; i < Z::kUnits; i += kMakers) {
-                    const int u = unit + i, slot = u % Z::kRaws;
-                    ready = ready || wait_phase(&c.freed[stage], (at / Z::kStages - 1) & 1, c, p.o.wait_ns);
-                    if (!ready || !wait_phase(&raw_full[slot], (u / Z::kRaws) & 1, c, p.o.wait_ns)) break;
-                    const int token = feed.token() + 16 * i;
-                    if (make_rows<BITS, D>(smem + Z::kRaw + slot * Z::kHalf, smem + Z::kRing + stage * X::kEntryBytes,
-                                           smem + Z::kXkAt + stage * Z::kXk, 16 * i, feed.value, x.s.n_k - token, x.s.ctx - token))
-                        special_of(c, feed.number) = feed.number;
-                    tc::fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&c.full[stage]);
-                        mbar_arrive(&raw_freed[slot]);
-                    }
+            __syncwarp();
+            unit += X::kUnits;
+        }
+        // nothing may land in this memory when it has become another CTA's
+        if (!ok) drain_copies_call(c.raw_full, unit > X::kRaws ? unit - X::kRaws : 0, unit, X::kRaws);
+    } else {
+        Feed<X, Tree<X>> feed(p, c.cut, blockIdx.x);
+        int unit = 0, tiles[2] = {0, 0};
+        for (; feed.next(); unit += X::kUnits) {
+            const Item& x = feed.x;
+            const bool v = feed.value;
+            const int tile = v ? tiles[1]++ : tiles[0]++, stage = tile % X::kStages;
+            uint64_t *full = v ? &c.v_full[stage] : &c.k_full[stage], *freed = v ? &c.v_freed[stage] : &c.k_freed[stage];
+            char* to = v ? smem + X::kV + stage * X::kVStage : smem + X::kK + stage * X::kKStage;
+            bool ready = tile < X::kStages;
+            for (int i = (wid - 10 + kMakers - unit % kMakers) % kMakers; i < X::kUnits; i += kMakers) {
+                const int u = unit + i, slot = u % X::kRaws, token = feed.token() + 16 * i;
+                ready = ready || wait_phase(freed, (tile / X::kStages - 1) & 1, c.dead, limit);
+                if (!ready || !wait_phase(&c.raw_full[slot], (u / X::kRaws) & 1, c.dead, limit)) break;
+                if (make_rows<X>(smem + X::kRaw + slot * X::kHalf, to, 16 * i, v, p.o.c, x.s.n_k - token, x.s.ctx - token))
+                    *(volatile int*)&c.special[feed.number & 15] = feed.number;
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(full);
+                    mbar_arrive(&c.raw_freed[slot]);
                 }
             }
         }
@@ -366,29 +782,29 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_tree_kernel(const __grid_co
 
 template <int BITS, int D>
 int launch(const TreeP& base, char* ws, cudaStream_t stream) {
-    using Z = Shapes<BITS, D>;
+    using X = Tile<BITS, D>;
     constexpr int kDevices = 64;
     static int set[kDevices];            // per device: multiprocessors, set on the first call
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return EDGE0_ECUDA;
     int sms = __atomic_load_n(&set[dev], __ATOMIC_ACQUIRE);
     if (sms == 0) {
-        if (cudaFuncSetAttribute(attn_tree_kernel<BITS, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::kSmem) != cudaSuccess ||
+        if (cudaFuncSetAttribute(attn_tree_kernel<X>, cudaFuncAttributeMaxDynamicSharedMemorySize, X::kSmem) != cudaSuccess ||
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return EDGE0_ECUDA;
         sms = sms < kMaxCtas ? sms : kMaxCtas;
         __atomic_store_n(&set[dev], sms, __ATOMIC_RELEASE);
     }
-    Tree<BITS, D> p;
+    Tree<X> p;
     static_cast<TreeP&>(p) = base;
-    lay_out<D>(ws, &p.o);
+    lay_out<X>(ws, &p.o);
     // blocks at most: no more CTAs than that
-    const long long blocks = ((long long)p.T * p.G / Shape<D>::kBlock + p.B) * p.H;
-    const bool joins = (p.cap + kTile - 1) / kTile >= kMinSplit;
+    const long long blocks = ((long long)p.T * p.G / X::kBlock + p.B) * p.H;
+    const bool joins = (p.cap + X::kTile - 1) / X::kTile >= X::kMinSplit;
     const int grid = joins || blocks > sms ? sms : (int)blocks;
-    const int rc = launch_early(attn_tree_kernel<BITS, D>, dim3(grid), kThreadsF, Z::kSmem, stream, p, joins);
+    const int rc = launch_early(attn_tree_kernel<X>, dim3(grid), kThreadsT, X::kSmem, stream, p, joins);
     if (rc || !joins || grid < 2) return rc;
-    return launch_early(flash_join<D, Tree<BITS, D>>, dim3(grid - 1, Shape<D>::kBlock / 32), 128, 0, stream, p);
+    return launch_early(flash_join<X, Tree<X>>, dim3(grid - 1, X::kBlock / 32), 128, 0, stream, p);
 }
 
 }  // namespace
@@ -398,7 +814,10 @@ using namespace edge0;
 
 extern "C" size_t edge0_attn_tree_workspace_bytes(const edge0_kv_cache* cache) {
     kv::View c;
-    return kv::view_of(cache, &c) ? 0 : edge0_attn_prompt_workspace_bytes(cache->head_dim);
+    if (kv::view_of(cache, &c)) return 0;
+    return cache->head_dim == 64    ? flash::workspace_bytes<Tile<4, 64>>()
+           : cache->head_dim == 128 ? flash::workspace_bytes<Tile<4, 128>>()
+                                    : flash::workspace_bytes<Tile<4, 256>>();
 }
 
 extern "C" int edge0_attn_tree(const edge0_kv_cache* cache, const uint16_t* q, long long ldq, int T, int n_q_heads,

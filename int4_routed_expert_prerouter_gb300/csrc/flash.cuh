@@ -35,14 +35,15 @@ namespace flash {
 constexpr int kTile = 128;            // tokens per step
 constexpr int kRowsQ = 128;           // rows of an accumulator
 constexpr int kMaxCtas = 160;         // shares at most (an SM each)
-constexpr int kMinSplit = 8;          // tiles that a block has at least to be cut
-constexpr int kMinShare = 4;          // tiles that a share has at least
 constexpr float kRise = 4.f;          // how far scores may exceed the reference, as a power of two
 constexpr float kUp = 11.f;           // weights are 2^kUp times as large: kRise + kUp = 15
 constexpr int kSoftmax = 256;         // threads of the two softmax warpgroups
 
+// What the shares go by: a block's rows, tokens per step, head width, tiles that a block has at least to be cut and that a
+// share has at least (a cut costs a start, parts of fp32 and their join).
 template <int D>
 struct Shape {
+    static constexpr int kD = D, kTile = flash::kTile, kMinSplit = 8, kMinShare = 4;
     static constexpr int kStreams = D <= 128 ? 2 : 1;
     static constexpr int kBlock = kStreams * kRowsQ;          // rows of a block
     static constexpr int kEntry = D == 256 ? 64 : kTile;      // tokens of a ring entry
@@ -50,6 +51,8 @@ struct Shape {
     static constexpr int kEntryBytes = kEntry * D * 2;
     static constexpr int kChunks = D / 64;                    // 128-byte swizzled columns of an operand
     static constexpr int kQBytes = kRowsQ * D * 2;
+    // how many tiles K runs ahead of V for a block of so many rows
+    __host__ __device__ static constexpr int lead(int rows) { return kStreams == 2 && rows > kRowsQ ? 1 : 2; }
     // TMEM columns: scores (or weights) of a stream or buffer, accumulators behind both
     static constexpr int kO = 2 * kTile;
 };
@@ -91,14 +94,15 @@ struct Item {
 // ----------------------------------------------------------------- shares ----
 // Costs count a (row of a token's group, token) pair as 1 / block rows of it: a block costs the tokens its last row
 // sees times G, and one tile more.
-template <int R>
+template <class Sh>
 struct Costs {
+    static constexpr int R = Sh::kBlock;
     long long per;        // cost of a tile: kTile G
     long long off, all;   // off G, n_k G
     int blocks;
 
     __device__ Costs(const Seq& s, int G) {
-        per = (long long)kTile * G;
+        per = (long long)Sh::kTile * G;
         off = (long long)s.off * G;
         all = (long long)s.n_k * G;
         blocks = (int)(((long long)s.n_q * G + R - 1) / R);
@@ -119,12 +123,11 @@ struct Costs {
 
 // The places of the cuts `first` and first + 1 of the CTAs' shares, by the whole CTA of at least 256 threads;
 // prefix: [EDGE0_MAX_BATCHED + 1] of scratch.
-template <int D, class Src>
+template <class Sh, class Src>
 __device__ void find_share(const Src& p, int cta, int ctas, long long* prefix, Place* out) {
-    constexpr int R = Shape<D>::kBlock;
     const int tid = threadIdx.x;
     long long mine = 0;
-    if (tid < p.B) mine = Costs<R>(p.seq(tid), p.G).total() * p.H;
+    if (tid < p.B) mine = Costs<Sh>(p.seq(tid), p.G).total() * p.H;
     if (tid < EDGE0_MAX_BATCHED) prefix[tid + 1] = mine;
     __syncthreads();
     if (tid < 32) {                                   // 8 sequences a lane
@@ -143,7 +146,7 @@ __device__ void find_share(const Src& p, int cta, int ctas, long long* prefix, P
     }
     __syncthreads();
     if (tid == 0 || tid == 32) {
-        const long long all = prefix[p.B], least = (long long)kMinShare * kTile * p.G;
+        const long long all = prefix[p.B], least = (long long)Sh::kMinShare * Sh::kTile * p.G;
         long long share = (all + ctas - 1) / ctas;
         if (share < least) share = least;             // (so that two cuts never fall on one tile of a block)
         const int i = cta + (tid == 32);
@@ -156,7 +159,7 @@ __device__ void find_share(const Src& p, int cta, int ctas, long long* prefix, P
                 if (prefix[mid] <= x) lo = mid;
                 else hi = mid;
             }
-            const Costs<R> c(p.seq(lo), p.G);
+            const Costs<Sh> c(p.seq(lo), p.G);
             const long long head = c.total();
             long long in = x - prefix[lo];
             at.b = lo;
@@ -174,7 +177,7 @@ __device__ void find_share(const Src& p, int cta, int ctas, long long* prefix, P
             const int tiles = (int)((seen + c.per - 1) / c.per);
             int tile = (int)((in - c.per / 2) / c.per);             // the nearest, less the block's own cost
             if (in < c.per) tile = 0;
-            if (tiles < kMinSplit || cost * 8 <= share) tile = 2 * in > cost ? tiles : 0;
+            if (tiles < Sh::kMinSplit || cost * 8 <= share) tile = 2 * in > cost ? tiles : 0;
             if (tile >= tiles && tile > 0) {          // the next block's start
                 tile = 0;
                 if (++at.t == c.blocks) {
@@ -194,7 +197,7 @@ __device__ void find_share(const Src& p, int cta, int ctas, long long* prefix, P
 }
 
 // Goes through a share's blocks.
-template <int D, class Src>
+template <class Sh, class Src>
 struct Walk {
     const Src& p;
     Place at, end;
@@ -206,7 +209,7 @@ struct Walk {
     __device__ void enter() {
         while (at.b < p.B) {
             s = p.seq(at.b);
-            blocks = (int)(((long long)s.n_q * p.G + Shape<D>::kBlock - 1) / Shape<D>::kBlock);
+            blocks = (int)(((long long)s.n_q * p.G + Sh::kBlock - 1) / Sh::kBlock);
             if (blocks) break;
             ++at.b;
         }
@@ -217,7 +220,7 @@ struct Walk {
             const bool last = same_block(at, end);
             if (at.b >= p.B || (last && end.tile <= at.tile)) return false;
             if (at.b > end.b || (at.b == end.b && (at.h > end.h || (at.h == end.h && at.t > end.t)))) return false;
-            constexpr int R = Shape<D>::kBlock;
+            constexpr int R = Sh::kBlock, kTile = Sh::kTile;
             const int all = s.n_q * p.G;
             x.b = at.b;
             x.h = at.h;
@@ -347,16 +350,16 @@ __device__ __forceinline__ volatile int& special_of(Control& c, int number) {
 }
 // Waits for a phase of a barrier, by a whole warp, which agrees on the answer; gives up after `limit` ns
 // or when another warp did.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, Control& c, unsigned long long limit) {
-    bool ok = !*(volatile int*)&c.dead && mbar_try_wait(bar, parity);
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int& dead, unsigned long long limit) {
+    bool ok = !*(volatile int*)&dead && mbar_try_wait(bar, parity);
     if (!__all_sync(0xffffffffu, ok)) {
         unsigned long long t0, now;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
         while (!ok) {
-            if (*(volatile int*)&c.dead) break;
+            if (*(volatile int*)&dead) break;
             ok = mbar_try_wait(bar, parity);
             asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-            if (!ok && now - t0 > limit) *(volatile int*)&c.dead = 1;
+            if (!ok && now - t0 > limit) *(volatile int*)&dead = 1;
         }
         ok = __all_sync(0xffffffffu, ok);
     }
@@ -379,22 +382,22 @@ struct Out {
 
 // -------------------------------------------------------- the matrix warp ----
 // A ring's entries in their order: K tiles run ahead of V's, by one where two streams share the tiles, else by two.
-template <int D, class Src>
+template <class Sh, class Src>
 struct Feed {
-    Walk<D, Src> walk;
+    Walk<Sh, Src> walk;
     Item x;
-    int n = 0, lead = 0, k = 0, v = 0, e = Shape<D>::kEntries, number = 0;
+    int n = 0, lead = 0, k = 0, v = 0, e = Sh::kEntries, number = 0;
     bool value = false;   // the entry is of V
     int tile = 0;         // of the share's part of the block
 
     __device__ Feed(const Src& p, const Place* cut, int cta) : walk(p, cut, cta) {}
     __device__ bool next() {
-        if (++e < Shape<D>::kEntries) return true;
+        if (++e < Sh::kEntries) return true;
         e = 0;
         while (v == n) {
             if (!walk.next(x)) return false;
             n = x.hi - x.lo;
-            lead = x.pair<D>() ? 1 : 2;
+            lead = Sh::lead(x.rows);
             k = v = 0;
             if (n > 0) ++number;
         }
@@ -403,19 +406,18 @@ struct Feed {
         return true;
     }
     // first token of the entry
-    __device__ int token() const { return (x.lo + tile) * kTile + e * Shape<D>::kEntry; }
+    __device__ int token() const { return (x.lo + tile) * Sh::kTile + e * Sh::kEntry; }
 };
 
-// Ring entries: STAGES of Shape<D>::kEntryBytes at `ring`; queries of a stream at q + stream * kQBytes (and, with
-// Src::kExtra, one step of 16 more of the scores' product at xq + stream * kRowsQ * 32 against xk + stage * kEntry * 32).
+// Ring entries: STAGES of Shape<D>::kEntryBytes at `ring`; queries of a stream at q + stream * kQBytes.
 template <int D, int STAGES, class Src>
-__device__ __forceinline__ void matrix_warp(const Src& p, Control& c, uint32_t q, uint32_t ring, uint32_t xq, uint32_t xk) {
+__device__ __forceinline__ void matrix_warp(const Src& p, Control& c, uint32_t q, uint32_t ring) {
     using X = Shape<D>;
     constexpr int E = X::kEntries;
     constexpr uint32_t kIdS = (1u << 4) | ((uint32_t)(X::kEntry >> 3) << 17) | ((uint32_t)(kRowsQ >> 4) << 24);
     constexpr uint32_t kIdO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRowsQ >> 4) << 24);
     const uint32_t tm = c.tmem;
-    Walk<D, Src> walk(p, c.cut, blockIdx.x);
+    Walk<Shape<D>, Src> walk(p, c.cut, blockIdx.x);
     Item x;
     int base = 0;                               // ring entries before the block's, in tiles
     uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
@@ -430,7 +432,7 @@ __device__ __forceinline__ void matrix_warp(const Src& p, Control& c, uint32_t q
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const int at = (base + k_entry(i, lead)) * E + e, stage = at % STAGES;
-                ok = wait_phase(&c.full[stage], (at / STAGES) & 1, c, p.o.wait_ns);
+                ok = wait_phase(&c.full[stage], (at / STAGES) & 1, c.dead, p.o.wait_ns);
                 if (!ok) break;
                 tc::fence_after_sync();
                 const uint32_t a = desc_lo(q + s * X::kQBytes, 16), b = desc_lo(ring + stage * X::kEntryBytes, 16);
@@ -439,20 +441,18 @@ __device__ __forceinline__ void matrix_warp(const Src& p, Control& c, uint32_t q
                 for (int ks = 0; ks < D / 16; ++ks)
                     mma_ss(d, desc128(a + (ks >> 2) * (kRowsQ * 128 / 16) + (ks & 3) * 2),
                            desc128(b + (ks >> 2) * (X::kEntry * 128 / 16) + (ks & 3) * 2), kIdS, ks > 0, lead_lane);
-                if (Src::kExtra)
-                    mma_ss(d, tc::smem_desc(xq + s * (kRowsQ * 32)), tc::smem_desc(xk + stage * (X::kEntry * 32)), kIdS, true, lead_lane);
                 if (release) commit(&c.freed[stage], lead_lane);
             }
             if (ok) commit(&c.s_full[buf], lead_lane);
         };
         auto values = [&](int s, int i, int j, int buf, bool release, bool last) {
-            bool ok = wait_phase(&c.p_full[buf], n_p[buf] & 1, c, p.o.wait_ns);
+            bool ok = wait_phase(&c.p_full[buf], n_p[buf] & 1, c.dead, p.o.wait_ns);
             ++n_p[buf];
             const uint32_t d = tm + X::kO + s * D;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const int at = (base + v_entry(i, lead, n)) * E + e, stage = at % STAGES;
-                ok = ok && wait_phase(Src::kLooked ? &c.clean[stage] : &c.full[stage], (at / STAGES) & 1, c, p.o.wait_ns);
+                ok = ok && wait_phase(&c.clean[stage], (at / STAGES) & 1, c.dead, p.o.wait_ns);
                 if (!ok) break;
                 tc::fence_after_sync();
                 const uint32_t b = desc_lo(ring + stage * X::kEntryBytes, X::kEntry * 128);
@@ -468,10 +468,10 @@ __device__ __forceinline__ void matrix_warp(const Src& p, Control& c, uint32_t q
         if constexpr (X::kStreams == 2) {
             const int n1 = x.of_stream<D>(1), n0 = x.of_stream<D>(0);
             auto tile = [&](int s, int j) { return x.tile_of<D>(s, j) - x.lo; };
-            wait_phase(&c.q_full[0], n_q[0]++ & 1, c, p.o.wait_ns);
+            wait_phase(&c.q_full[0], n_q[0]++ & 1, c.dead, p.o.wait_ns);
             scores(0, 0, 0, !pair);
             if (n1) {
-                wait_phase(&c.q_full[1], n_q[1]++ & 1, c, p.o.wait_ns);
+                wait_phase(&c.q_full[1], n_q[1]++ & 1, c.dead, p.o.wait_ns);
                 scores(1, tile(1, 0), 1, true);
             }
             for (int j = 0; j < n0; ++j) {
@@ -483,7 +483,7 @@ __device__ __forceinline__ void matrix_warp(const Src& p, Control& c, uint32_t q
                 }
             }
         } else {
-            wait_phase(&c.q_full[0], n_q[0]++ & 1, c, p.o.wait_ns);
+            wait_phase(&c.q_full[0], n_q[0]++ & 1, c.dead, p.o.wait_ns);
             // (a block's tile i has the score buffer (base + i) % 2: base counts two tiles, K's and V's, for each)
             const int g = base / 2;
             scores(0, 0, g & 1, true);
@@ -499,13 +499,13 @@ __device__ __forceinline__ void matrix_warp(const Src& p, Control& c, uint32_t q
 // ------------------------------------------------- the softmax warpgroups ----
 // Thread: one row of stream s.
 template <int D, class Src>
-__device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_smem, char* xq_smem) {
+__device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_smem) {
     using X = Shape<D>;
     const int s = threadIdx.x >> 7, quad = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = threadIdx.x & 127;
     if (s >= X::kStreams) return;
     const uint32_t tm = c.tmem + ((uint32_t)(32 * quad) << 16), o_at = tm + X::kO + s * D;
     char* my_q = q_smem + s * X::kQBytes;
-    Walk<D, Src> walk(p, c.cut, blockIdx.x);
+    Walk<Shape<D>, Src> walk(p, c.cut, blockIdx.x);
     Item x;
     uint32_t n_s[2] = {0, 0}, n_last = 0;
     int base = 0, number = 0;
@@ -513,13 +513,14 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
         if (x.hi > x.lo) ++number;
         const bool pair = x.pair<D>();
         const int n = x.of_stream<D>(s);
-        const int local = pair ? s * kRowsQ + row : row;
-        const bool live = local < x.rows;
+        // (of a block of one row tile the second stream turns its rows by 64, so that few rows fall to other
+        // quarters of the multiprocessor than the first's)
+        const int local = pair ? s * kRowsQ + row : row ^ (64 * s);
+        const bool live = local < x.rows, idle = (local & ~31) >= x.rows;
         const int at = x.row0 + (live ? local : 0), token = at / p.G, head = x.h * p.G + at - token * p.G;
-        const typename Src::Row view(p, x, token);
-        float cc = p.o.c;                        // from a score to the exponent
+        const float cc = p.o.c;                  // from a score to the exponent
         if (n > 0) {
-            p.load_queries(x, live, token, head, my_q, xq_smem + s * (kRowsQ * 32), row, cc);
+            p.load_queries(x, live, token, head, my_q, row);
             tc::fence_async_smem();
             mbar_arrive(&c.q_full[s]);
         }
@@ -528,36 +529,33 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
         for (int j = 0; j < n; ++j) {
             const int buf = X::kStreams == 2 ? s : (base + j) & 1;
             const uint32_t s_at = tm + buf * kTile;
-            ok = wait_phase(&c.s_full[buf], n_s[buf] & 1, c, p.o.wait_ns);
+            ok = wait_phase(&c.s_full[buf], n_s[buf] & 1, c.dead, p.o.wait_ns);
             ++n_s[buf];
             if (!ok) continue;
+            if (idle) {                              // no row of this warp's: whatever lies there
+                if (lane == 0) mbar_arrive(&c.p_full[buf]);
+                continue;
+            }
             tc::fence_after_sync();
-            constexpr int kN = Src::kHeld;           // scores held in registers; fewer than all are read twice
-            uint32_t v[kN];
+            uint32_t v[kTile];
+#pragma unroll
+            for (int k = 0; k < kTile; k += 32) tmem_ld32(s_at + k, v + k);
+            tc::tmem_wait_ld();
             const int tile = x.tile_of<D>(s, j);
-            auto read = [&](int from) {
+            if (tile >= x.clear) {
 #pragma unroll
-                for (int k = 0; k < kN; k += 32) tmem_ld32(s_at + from + k, v + k);
-                tc::tmem_wait_ld();
-                if (tile >= x.clear) {
+                for (int k = 0; k < kTile; k += 32) {
+                    const uint32_t seen = p.seen_word(x, token, tile * kTile + k);
 #pragma unroll
-                    for (int k = 0; k < kN; k += 32) {
-                        const uint32_t seen = view.seen(p, x, tile * kTile + from + k);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!((seen >> i) & 1)) v[k + i] = 0xff800000u;      // -infinity
-                    }
+                    for (int i = 0; i < 32; ++i)
+                        if (!((seen >> i) & 1)) v[k + i] = 0xff800000u;      // -infinity
                 }
-            };
+            }
             float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int from = 0; from < kTile; from += kN) {
-                read(from);
+            for (int k = 0; k < kTile; k += 8)
 #pragma unroll
-                for (int k = 0; k < kN; k += 8)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], fmaxf(__uint_as_float(v[k + 2 * i]), __uint_as_float(v[k + 2 * i + 1])));
-            }
+                for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], fmaxf(__uint_as_float(v[k + 2 * i]), __uint_as_float(v[k + 2 * i + 1])));
             const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * cc;
             const bool move = most > ref + kRise || (most > ref && ref == -INFINITY);
             if (__any_sync(0xffffffffu, move)) {
@@ -568,7 +566,7 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
                     // the product of the tile before, the other buffer's latest (with two streams it was issued
                     // before these scores)
                     const int g = base + j - 1;
-                    ok = wait_phase(&c.o_step[g & 1], (g >> 1) & 1, c, p.o.wait_ns);
+                    ok = wait_phase(&c.o_step[g & 1], (g >> 1) & 1, c.dead, p.o.wait_ns);
                     tc::fence_after_sync();
                 }
                 if (j > 0) {
@@ -587,18 +585,14 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
             const f2 c2 = pk(cc, cc), sub2 = pk(sub, sub);
             f2 sum[2] = {0, 0};
 #pragma unroll
-            for (int from = 0; from < kTile; from += kN) {
-                if (kN < kTile) read(from);          // (weights lie over scores that have been read for good)
-#pragma unroll
-                for (int k = 0; k < kN; k += 2) {
-                    float a, b;
-                    unpk(fma2(pk(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, sub2), a, b);
-                    a = ex2(a);
-                    b = ex2(b);
-                    sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pk(a, b));
-                    v[k >> 1] = pack2(a, b);
-                    if ((k & 63) == 62) tmem_st32(s_at + ((from + k) >> 6) * 32, v + (k >> 6) * 32);
-                }
+            for (int k = 0; k < kTile; k += 2) {
+                float a, b;
+                unpk(fma2(pk(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, sub2), a, b);
+                a = ex2(a);
+                b = ex2(b);
+                sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pk(a, b));
+                v[k >> 1] = pack2(a, b);
+                if ((k & 63) == 62) tmem_st32(s_at + (k >> 6) * 32, v + (k >> 6) * 32);
             }
             float a, b;
             unpk(add2(sum[0], sum[1]), a, b);
@@ -610,7 +604,7 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
         }
         if (X::kStreams == 1) base += n;
         if (n > 0) {
-            ok = wait_phase(&c.o_last[s], n_last++ & 1, c, p.o.wait_ns) && ok;
+            ok = wait_phase(&c.o_last[s], n_last++ & 1, c.dead, p.o.wait_ns) && ok;
             tc::fence_after_sync();
         }
         if (!ok) l = __int_as_float(0x7fffffff);
@@ -620,10 +614,10 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
         float f0 = 1.f, f1 = 0.f;
         const bool merge = X::kStreams == 2 && !pair && x.of_stream<D>(1) > 0;
         if (merge) {
-            if (s == 1) c.ml[row] = make_float2(ref, l);
+            if (s == 1) c.ml[local] = make_float2(ref, l);
             named_bar_sync(1, kSoftmax);
             if (s == 0) {
-                const float2 other = c.ml[row];
+                const float2 other = c.ml[local];
                 const float top = fmaxf(ref, other.x);
                 if (top != -INFINITY) {
                     f0 = ex2(ref - top);
@@ -651,7 +645,7 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
                         tmem_ld32(o_at + k + i, o);
                         tc::tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) swap[(i + e) * kRowsQ + row] = __uint_as_float(o[e]);
+                        for (int e = 0; e < 32; ++e) swap[(i + e) * kRowsQ + local] = __uint_as_float(o[e]);
                     }
                     named_bar_sync(3, kSoftmax);
                 } else {
@@ -667,14 +661,14 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     float a = __uint_as_float(raw[i]);
-                    if (merge) a = a * f0 + swap[(k % (D / 2) + i) * kRowsQ + row] * f1;
-                    o[(i & ~7) + Src::dim_of(i & 7)] = a;
+                    if (merge) a = a * f0 + swap[(k % (D / 2) + i) * kRowsQ + local] * f1;
+                    o[i] = a;
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = 0.f;
             }
-            if (fix && live) p.add_special(x, view, token, k, o);
+            if (fix && live) p.add_special(x, token, k, o);
             if (l == 0.f || l != l) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = nan;
@@ -719,9 +713,9 @@ __device__ __forceinline__ void control_init(Control& c, int full_count, int cle
 
 // ------------------------------------------------------------------- join ----
 // A CTA of four warps: 32 rows of the block that the cut in front of share blockIdx.x + 1 is the first to fall into.
-template <int D, class Src>
+template <class Sh, class Src>
 __global__ void __launch_bounds__(128) flash_join(const Src p) {
-    constexpr int kN = D / 32, R = Shape<D>::kBlock;
+    constexpr int D = Sh::kD, kN = D / 32, R = Sh::kBlock;
     wait_predecessor();
     launch_dependents();
     const int i = blockIdx.x + 1, ctas = gridDim.x + 1, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -763,16 +757,16 @@ __global__ void __launch_bounds__(128) flash_join(const Src p) {
 }
 
 // workspace: places, parts' statistics, parts
-template <int D>
+template <class Sh>
 inline long long workspace_bytes() {
-    return (long long)(kMaxCtas + 1) * sizeof(Place) + 15 + 2ll * kMaxCtas * Shape<D>::kBlock * (D * 4 + 8) + 16;
+    return (long long)(kMaxCtas + 1) * sizeof(Place) + 15 + 2ll * kMaxCtas * Sh::kBlock * (Sh::kD * 4 + 8) + 16;
 }
-template <int D>
+template <class Sh>
 inline void lay_out(char* ws, Out* o) {
     o->places = (Place*)ws;
     char* at = ws + ((kMaxCtas + 1) * sizeof(Place) + 15) / 16 * 16;
     o->part_ml = (float2*)at;
-    o->part_o = (float*)(at + 2ll * kMaxCtas * Shape<D>::kBlock * 8);
+    o->part_o = (float*)(at + 2ll * kMaxCtas * Sh::kBlock * 8);
 }
 
 }  // namespace flash

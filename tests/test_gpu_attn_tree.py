@@ -44,15 +44,17 @@ class Pool:
         self.codes, self.s, self.b = tile(codes).double(), tile(s).double(), tile(b).double()
 
     def tokens(self, pages, n):
-        """K, V [n, H, D], |s (q - z)| + |s z + b| of K, s (|q - z| + 1) of K."""
+        """K, V [n, H, D]; |s (q - z)| + |s z + b| of K and of V; what V's terms lose to a subnormal weight, which
+        meets V / m with s = m 2^e, m at least 1 where s is at least 2^-10 (twice: 2^10 instead of 2^11)."""
         z = 2.0 ** (self.bits - 1)
         pages = torch.as_tensor(np.asarray(pages)[:-(-n // self.page)], device=DEV)
         wide = lambda a: a[pages].repeat_interleave(64, -1)
         q, s, b = self.codes[pages], wide(self.s), wide(self.b)
         flat = lambda a: a.flatten(0, 1)[:n]
         x = s * q + b
-        k = s[:, 0] * (q[:, 0] - z)
-        return flat(x[:, 0]), flat(x[:, 1]), flat(k.abs() + (s[:, 0] * z + b[:, 0]).abs()), flat(s[:, 0] * ((q[:, 0] - z).abs() + 1))
+        parts = (s * (q - z)).abs() + (s * z + b).abs()
+        small = 2 * x[:, 1].abs() * torch.clamp(2.0 ** -10 / torch.where(s[:, 1] == 0, 1.0, s[:, 1]), min=1.0)
+        return flat(x[:, 0]), flat(x[:, 1]), flat(parts[:, 0]), flat(parts[:, 1]), flat(small)
 
 
 def visible(n, x, mask, device=DEV):
@@ -74,9 +76,8 @@ def check(got, pool, q, table, lens, cu, mask=None, scale=None):
         if n < 0 or x == 0:
             continue
         r = slice(cu[b], cu[b + 1])
-        k, v, k_abs, k_mag = pool.tokens(table[b], n + x)
-        o, bound = flash_ref.attend(q[r].double(), k, v, visible(n, x, None if mask is None else mask[r]), scale or D ** -0.5, k_abs, k_mag,
-                                    rounded=2.0 ** -11)
+        k, v, *parts = pool.tokens(table[b], n + x)
+        o, bound = flash_ref.attend(q[r].double(), k, v, visible(n, x, None if mask is None else mask[r]), scale or D ** -0.5, *parts)
         assert flash_ref.close(got[r], o, bound), (b, n, x, ((got[r].double() - o).abs() - bound).nan_to_num(0.0).max().item())
 
 
