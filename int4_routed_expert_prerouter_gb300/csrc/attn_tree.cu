@@ -207,16 +207,17 @@ __device__ __forceinline__ uint32_t split(float v) {
 }
 
 // ----------------------------------------------------------------- makers ----
-// (code - z) 2^e of 8 dims, e <= 5 (or, in two steps, up to where that leaves fp16); 4 bits: one word, dims in the order
-// 0 4 1 5 2 6 3 7; 8 bits: two words, in order.  0x6400 is 1024: a code below it adds itself, a nibble 4 bits up 16
-// times itself.  one: 2^e, or 0 for a group that has to come out as zeros.
+// (code - z) 2^e of 8 dims, e <= 5 (up to there the step stays within fp16), z half the code range less `less`, 0 or 1;
+// 4 bits: one word, dims in the order 0 4 1 5 2 6 3 7; 8 bits: two words, in order.  0x6400 is 1024: a code below it
+// adds itself, a nibble 4 bits up 16 times itself.  none: zeros.
 template <int BITS>
-__device__ __forceinline__ uint4 codes8(uint32_t w0, uint32_t w1, int e, bool none) {
+__device__ __forceinline__ uint4 codes8(uint32_t w0, uint32_t w1, int e, uint32_t less, bool none) {
     const uint32_t up = (uint32_t)(e << 10) * 0x10001u;
-    const uint32_t m0 = none ? 0u : 0x3C003C00u + up, a0 = none ? 0u : (BITS == 4 ? 0xE408E408u : 0xE480E480u) + up;
+    const uint32_t m0 = none ? 0u : 0x3C003C00u + up;
+    const uint32_t a0 = none ? 0u : (BITS == 4 ? 0xE408E408u : 0xE480E480u) - less * 0x10001u + up;
     uint4 r;
     if (BITS == 4) {
-        const uint32_t m1 = none ? 0u : 0x2C002C00u + up, a1 = none ? 0u : 0xD480D480u + up, h = w0 >> 8;
+        const uint32_t m1 = none ? 0u : 0x2C002C00u + up, a1 = none ? 0u : 0xD480D480u - less * 0x100010u + up, h = w0 >> 8;
         r.x = hfma2((w0 & 0x000F000Fu) | 0x64006400u, m0, a0);
         r.y = hfma2((w0 & 0x00F000F0u) | 0x64006400u, m1, a1);
         r.z = hfma2((h & 0x000F000Fu) | 0x64006400u, m0, a0);
@@ -254,7 +255,7 @@ __device__ __forceinline__ bool make_rows(const char* raw, char* stage, int row0
             for (int x = 0; x < kPer; ++x) {
                 const int c8 = p * kPer + x;                         // 8 dims
                 *reinterpret_cast<uint4*>(stage + (c8 >> 1) * (T * 32) + tc::kstep_off(row, (c8 & 1) * 8)) =
-                    codes8<BITS>(w[x * kW], w[x * kW + kW - 1], -10, false);
+                    codes8<BITS>(w[x * kW], w[x * kW + kW - 1], -10, 0, false);
             }
             if (first) {
                 // b = 1 (0 - z + b + z) of a constant group
@@ -268,13 +269,17 @@ __device__ __forceinline__ bool make_rows(const char* raw, char* stage, int row0
         } else {
             const bool nan = sb.x != sb.x || sb.y != sb.y, out = none || (nan && tok >= drafted);
             found = found || (nan && !none && tok >= drafted);
+            // z is 1 less in every other token: codes lie around half a step below half their range, and sums that grow with the
+            // context, of codes and offsets apart, would lose to the rounding of the matrix steps' accumulators, which
+            // is towards one side (after 25,000 tokens 1e-5 of V's size)
+            const uint32_t less = row & 1;
             int e = (int)((sbw >> 10) & 31) - 15;
             e = max(-10, min(kMostE, e));
             const bool zeros = out || nan || flat;
 #pragma unroll
             for (int x = 0; x < kPer; ++x) {
                 const int c8 = p * kPer + x;
-                uint4 v = codes8<BITS>(w[x * kW], w[x * kW + kW - 1], min(e, kFastE), zeros);
+                uint4 v = codes8<BITS>(w[x * kW], w[x * kW + kW - 1], min(e, kFastE), less, zeros);
                 if (e > kFastE) {
                     const uint32_t up = (uint32_t)(0x3C00 + ((e - kFastE) << 10)) * 0x10001u;
                     v.x = hfma2(v.x, up, 0x80008000u);
@@ -286,7 +291,7 @@ __device__ __forceinline__ bool make_rows(const char* raw, char* stage, int row0
             }
             if (first) {
                 const float m = out ? 0.f : nan ? __int_as_float(0x7fffffff) : flat ? 1.f : sb.x * __uint_as_float((uint32_t)(127 - e) << 23);
-                const float r = out || nan ? 0.f : flat ? sb.y : __fdividef(sb.y, m) + kZ * __uint_as_float((uint32_t)(127 + e) << 23);
+                const float r = out || nan ? 0.f : flat ? sb.y : __fdividef(sb.y, m) + (kZ - (float)less) * __uint_as_float((uint32_t)(127 + e) << 23);
                 reinterpret_cast<float*>(stage + X::kVTab)[pair] = m * kUpV;
                 *reinterpret_cast<uint4*>(stage + (g * (X::kCols / 8) + 8) * (T * 16) + row * 16) = make_uint4(split<0>(r), 0, 0, 0);
             }
