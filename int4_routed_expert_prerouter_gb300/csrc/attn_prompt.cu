@@ -26,6 +26,7 @@ struct PromptP {
     int B, H, G, T, Tk;
     const int* cu_q;
     const int* cu_k;
+    bool q_copied;                     // queries come by TMA: 64 rows are whole tokens' groups
 };
 
 template <int D>
@@ -77,9 +78,10 @@ struct Prompt : PromptP {
 
 template <int D>
 struct Ring {
-    static constexpr int kStages = D == 64 ? 8 : 5;
+    static constexpr int kStages = D == 64 ? 8 : 4;
     static constexpr int kQ = Shape<D>::kStreams * Shape<D>::kQBytes;
-    static constexpr int kBytes = kQ + kStages * Shape<D>::kEntryBytes;
+    static constexpr int kOut = kQ + kStages * Shape<D>::kEntryBytes;        // staging of the outputs
+    static constexpr int kBytes = kOut + Shape<D>::kStreams * kStageBytes;
     static constexpr int kSmem = kBytes + (int)sizeof(Control) + 1024;       // (1024: to begin on such a boundary)
 };
 static_assert(Ring<128>::kSmem <= 232448 && Ring<256>::kSmem <= 232448 && Ring<64>::kStages <= kMaxStages, "shared memory");
@@ -93,6 +95,7 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsF, 1) attn_prompt_kernel(const __grid_constant__ Prompt<D> p,
+                                                                   const __grid_constant__ CUtensorMap map_q,
                                                                    const __grid_constant__ CUtensorMap map_k,
                                                                    const __grid_constant__ CUtensorMap map_v, bool joins) {
     using X = Shape<D>;
@@ -107,7 +110,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_prompt_kernel(const __grid_
         tc::tmem_alloc(&c.tmem, 512);
         tc::tmem_relinquish();
     }
-    if (threadIdx.x == 0) control_init(c, 1, 2, 3, p.o.wait_ns == 0);
+    if (threadIdx.x == 0) control_init(c, 1, 2, 3, p.q_copied ? 1 : kRowsQ, p.o.wait_ns == 0);
     tc::fence_before_sync();
     wait_predecessor();
     launch_dependents();
@@ -115,20 +118,49 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_prompt_kernel(const __grid_
     tc::fence_after_sync();
     if (joins && threadIdx.x == 0) p.o.places[blockIdx.x] = c.cut[0];
 
-    // registers: 256 x 208 + 128 x 88, what the CTA was launched with (384 x 168)
+    // registers: 256 x 216 + 128 x 72, what the CTA was launched with (384 x 168)
     if (wid < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
-        softmax_warps<D, Src>(p, c, smem);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
+        softmax_warps<D, Src>(p, c, smem, smem + R::kOut);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
         if (wid == 8) {
             matrix_warp<D, R::kStages, Src>(p, c, smem_u32(smem), smem_u32(ring));
         } else if (wid == 9) {
             Feed<X, Src> feed(p, c.cut, blockIdx.x);
-            int at = 0;
+            int at = 0, block = 0;
             bool ok = p.o.wait_ns != 0;
             const uint32_t lead_lane = elect();
+            // a block's queries, 64 rows at a time, as soon as the one's before are done with; one row tile for both streams
+            // lies in the second's turned by 64 rows
+            auto queries = [&](const Item& x) {
+                const bool pair = x.pair<D>();
+#pragma unroll 1
+                for (int s = 0; s < X::kStreams; ++s) {
+                    if (x.of_stream<D>(s) == 0) continue;
+                    ok = ok && wait_phase(&c.q_freed[s], (c.q_loads[s] + 1) & 1, c.dead, p.o.wait_ns);
+                    if (!ok) return;
+                    if (lead_lane) {
+                        ++c.q_loads[s];
+                        mbar_arrive_expect_tx(&c.q_full[s], X::kQBytes);
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            const int from = pair ? s * kRowsQ + 64 * half : 64 * (half ^ s);
+#pragma unroll 1
+                            for (int k = 0; k < X::kChunks; ++k)
+                                tma_load(smem_u32(smem) + s * X::kQBytes + k * (kRowsQ * 128) + half * (64 * 128), &map_q, 64 * k, x.h * p.G,
+                                         x.s.q0 + (x.row0 + from) / p.G, &c.q_full[s]);
+                        }
+                    }
+                    __syncwarp();
+                }
+            };
             for (; ok && feed.next(); ++at) {
+                if (p.q_copied && feed.number != block) {
+                    block = feed.number;
+                    queries(feed.x);
+                    if (!ok) break;
+                }
                 const int stage = at % R::kStages;
                 if (at >= R::kStages) ok = wait_phase(&c.freed[stage], (at / R::kStages - 1) & 1, c.dead, p.o.wait_ns);
                 if (!ok) break;
@@ -142,6 +174,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_prompt_kernel(const __grid_
                 __syncwarp();
             }
             // nothing may land in this memory when it has become another CTA's
+            // (its queries: below)
             if (!ok) drain_copies_call(c.full, at > R::kStages ? at - R::kStages : 0, at, R::kStages);
         } else {
             Feed<X, Src> feed(p, c.cut, blockIdx.x);
@@ -183,6 +216,8 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_prompt_kernel(const __grid_
         if (c.dead) {                // matrix steps under way still read shared memory and write the accumulators
             commit(&c.drained, elect());
             wait_copy(&c.drained, 0, kDefaultWaitNs);
+            for (int s = 0; s < 2; ++s)
+                if (c.q_loads[s]) wait_copy(&c.q_full[s], (c.q_loads[s] - 1) & 1, kDefaultWaitNs);
         }
         tc::tmem_dealloc(c.tmem, 512);
     }
@@ -207,13 +242,13 @@ Encode encoder() {
     return g;
 }
 
-// rows of `heads` x D fp16, ld apart: boxes of 64 dims of one head of `rows` rows, 128-byte swizzled
-int make_map(CUtensorMap* map, const void* base, int T, int heads, int D, long long ld, int rows) {
+// rows of `heads` x D fp16, ld apart: boxes of 64 dims of `group` heads of `rows` rows, 128-byte swizzled
+int make_map(CUtensorMap* map, const void* base, int T, int heads, int D, long long ld, int group, int rows) {
     const Encode f = encoder();
     if (!f) return EDGE0_ECUDA;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows}, step[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)rows}, step[3] = {1, 1, 1};
     const CUresult r = f(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -238,18 +273,21 @@ int launch(const PromptP& base, const uint16_t* k, long long ldk, char* ws, cuda
     Prompt<D> p;
     static_cast<PromptP&>(p) = base;
     lay_out<Shape<D>>(ws, &p.o);
-    CUtensorMap mk, mv;
+    CUtensorMap mq, mk, mv;
+    p.q_copied = 64 % p.G == 0;
+    int rc = make_map(&mq, p.q, p.T, p.H * p.G, D, p.ldq, p.q_copied ? p.G : 1, p.q_copied ? 64 / p.G : 1);
+    if (rc) return rc;
     // without any key nothing is loaded, but a map has to describe something: the queries
     const bool none = p.Tk == 0;
-    int rc = make_map(&mk, none ? (const void*)p.q : k, none ? p.T : p.Tk, none ? p.H * p.G : p.H, D, none ? p.ldq : ldk, Shape<D>::kEntry);
+    rc = make_map(&mk, none ? (const void*)p.q : k, none ? p.T : p.Tk, none ? p.H * p.G : p.H, D, none ? p.ldq : ldk, 1, Shape<D>::kEntry);
     if (rc) return rc;
-    rc = make_map(&mv, none ? p.q : p.v, none ? p.T : p.Tk, none ? p.H * p.G : p.H, D, none ? p.ldq : p.ldv, Shape<D>::kEntry);
+    rc = make_map(&mv, none ? p.q : p.v, none ? p.T : p.Tk, none ? p.H * p.G : p.H, D, none ? p.ldq : p.ldv, 1, Shape<D>::kEntry);
     if (rc) return rc;
     // blocks at most: no more CTAs than that
     const long long blocks = ((long long)p.T * p.G / Shape<D>::kBlock + p.B) * p.H;
     const bool joins = (p.Tk + kTile - 1) / kTile >= Shape<D>::kMinSplit;
     const int grid = joins || blocks > sms ? sms : (int)blocks;
-    rc = launch_early(attn_prompt_kernel<D>, dim3(grid), kThreadsF, R::kSmem, stream, p, mk, mv, joins);
+    rc = launch_early(attn_prompt_kernel<D>, dim3(grid), kThreadsF, R::kSmem, stream, p, mq, mk, mv, joins);
     if (rc || !joins || grid < 2) return rc;
     return launch_early(flash_join<Shape<D>, Prompt<D>>, dim3(grid - 1, Shape<D>::kBlock / 32), 128, 0, stream, p);
 }

@@ -326,11 +326,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 // -------------------------------------------------------------------- CTA ----
 constexpr int kMaxStages = 8;
+constexpr int kStageBytes = kRowsQ * 128;       // staging of a stream's outputs: 64 dims
 struct Control {
     uint64_t full[kMaxStages];      // a ring entry has arrived
     uint64_t clean[kMaxStages];     // ... and been looked through
     uint64_t freed[kMaxStages];     // ... and is done with
-    uint64_t q_full[2];             // a stream's queries are in place
+    uint64_t q_full[2], q_freed[2]; // a stream's queries are in place, are done with
     uint64_t s_full[2];             // scores of a stream (two streams) or a buffer (one)
     uint64_t p_full[2];             // ... have become weights
     uint64_t o_step[2];             // one stream: the product with V of a tile of this buffer is done
@@ -338,6 +339,7 @@ struct Control {
     uint64_t drained;
     Place cut[2];
     uint32_t tmem;
+    int q_loads[2];                 // copies of a stream's queries so far
     int dead;                       // a wait ran out: nothing more is issued, what is not done becomes NaN
     int special[kMaxStages * 2];    // numbers of the share's blocks with non-finite V that some rows do not see, by their last bits
     float2 ml[kRowsQ];              // the second stream's (reference, sum)
@@ -427,7 +429,7 @@ __device__ __forceinline__ void matrix_warp(const Src& p, Control& c, uint32_t q
         if (n == 0) continue;
         const bool pair = x.pair<D>();
         const int lead = pair ? 1 : 2;
-        auto scores = [&](int s, int i, int buf, bool release) {        // of the share's tile i
+        auto scores = [&](int s, int i, int buf, bool release, bool last) {        // of the share's tile i
             bool ok = true;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -444,6 +446,7 @@ __device__ __forceinline__ void matrix_warp(const Src& p, Control& c, uint32_t q
                 if (release) commit(&c.freed[stage], lead_lane);
             }
             if (ok) commit(&c.s_full[buf], lead_lane);
+            if (ok && last) commit(&c.q_freed[s], lead_lane);
         };
         auto values = [&](int s, int i, int j, int buf, bool release, bool last) {
             bool ok = wait_phase(&c.p_full[buf], n_p[buf] & 1, c.dead, p.o.wait_ns);
@@ -469,26 +472,26 @@ __device__ __forceinline__ void matrix_warp(const Src& p, Control& c, uint32_t q
             const int n1 = x.of_stream<D>(1), n0 = x.of_stream<D>(0);
             auto tile = [&](int s, int j) { return x.tile_of<D>(s, j) - x.lo; };
             wait_phase(&c.q_full[0], n_q[0]++ & 1, c.dead, p.o.wait_ns);
-            scores(0, 0, 0, !pair);
+            scores(0, 0, 0, !pair, n0 == 1);
             if (n1) {
                 wait_phase(&c.q_full[1], n_q[1]++ & 1, c.dead, p.o.wait_ns);
-                scores(1, tile(1, 0), 1, true);
+                scores(1, tile(1, 0), 1, true, n1 == 1);
             }
             for (int j = 0; j < n0; ++j) {
                 values(0, tile(0, j), j, 0, !pair, j + 1 == n0);
-                if (j + 1 < n0) scores(0, tile(0, j + 1), 0, !pair);
+                if (j + 1 < n0) scores(0, tile(0, j + 1), 0, !pair, j + 2 == n0);
                 if (j < n1) {
                     values(1, tile(1, j), j, 1, true, j + 1 == n1);
-                    if (j + 1 < n1) scores(1, tile(1, j + 1), 1, true);
+                    if (j + 1 < n1) scores(1, tile(1, j + 1), 1, true, j + 2 == n1);
                 }
             }
         } else {
             wait_phase(&c.q_full[0], n_q[0]++ & 1, c.dead, p.o.wait_ns);
             // (a block's tile i has the score buffer (base + i) % 2: base counts two tiles, K's and V's, for each)
             const int g = base / 2;
-            scores(0, 0, g & 1, true);
+            scores(0, 0, g & 1, true, n == 1);
             for (int j = 0; j < n; ++j) {
-                if (j + 1 < n) scores(0, j + 1, (g + j + 1) & 1, true);
+                if (j + 1 < n) scores(0, j + 1, (g + j + 1) & 1, true, j + 2 == n);
                 values(0, j, j, (g + j) & 1, true, j + 1 == n);
             }
         }
@@ -499,7 +502,7 @@ __device__ __forceinline__ void matrix_warp(const Src& p, Control& c, uint32_t q
 // ------------------------------------------------- the softmax warpgroups ----
 // Thread: one row of stream s.
 template <int D, class Src>
-__device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_smem) {
+__device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_smem, char* stage_smem) {
     using X = Shape<D>;
     const int s = threadIdx.x >> 7, quad = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = threadIdx.x & 127;
     if (s >= X::kStreams) return;
@@ -519,7 +522,7 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
         const bool live = local < x.rows, idle = (local & ~31) >= x.rows;
         const int at = x.row0 + (live ? local : 0), token = at / p.G, head = x.h * p.G + at - token * p.G;
         const float cc = p.o.c;                  // from a score to the exponent
-        if (n > 0) {
+        if (n > 0 && !p.q_copied) {
             p.load_queries(x, live, token, head, my_q, row);
             tc::fence_async_smem();
             mbar_arrive(&c.q_full[s]);
@@ -610,7 +613,7 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
         if (!ok) l = __int_as_float(0x7fffffff);
         const bool fix = n > 0 && special_of(c, number) == number;
 
-        // a block of one row tile: the second stream's sums and accumulator come through its query rows' memory
+        // a block of one row tile: the second stream's sums and accumulator come through its staging memory
         float f0 = 1.f, f1 = 0.f;
         const bool merge = X::kStreams == 2 && !pair && x.of_stream<D>(1) > 0;
         if (merge) {
@@ -633,73 +636,82 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
         __half* out = p.o.out + (long long)(x.s.q0 + token) * p.o.ldo + (long long)head * D;
         float* part = p.o.part_o + ((long long)x.part * X::kBlock + local) * D;
         const bool writes = live && (s == 0 || pair);
-        float* swap = reinterpret_cast<float*>(q_smem + X::kQBytes * (X::kStreams - 1));      // [D / 2][kRowsQ]
+        float* swap = reinterpret_cast<float*>(stage_smem + kStageBytes);               // [32][kRowsQ], the second stream's
+        char* stage = stage_smem + s * kStageBytes + 4096 * quad;                       // the warp's [32 rows][64 dims], swizzled
 #pragma unroll 1
         for (int k = 0; k < D; k += 32) {
-            if (merge && k % (D / 2) == 0) {
-                if (k) named_bar_sync(2, kSoftmax);                 // the first half has been read
+            if (merge) {
                 if (s == 1) {
-#pragma unroll 1
-                    for (int i = 0; i < D / 2; i += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(o_at + k + i, o);
-                        tc::tmem_wait_ld();
+                    uint32_t o[32];
+                    tmem_ld32(o_at + k, o);
+                    tc::tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) swap[(i + e) * kRowsQ + local] = __uint_as_float(o[e]);
+                    for (int e = 0; e < 32; ++e) swap[e * kRowsQ + local] = __uint_as_float(o[e]);
+                }
+                named_bar_sync(3, kSoftmax);
+            }
+            if (X::kStreams == 1 || pair || s == 0) {
+                float o[32];                            // dims k .. k + 31
+                if (n > 0) {
+                    uint32_t raw[32];
+                    tmem_ld32(o_at + k, raw);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        o[i] = __uint_as_float(raw[i]);
+                        if (merge) o[i] = o[i] * f0 + swap[i * kRowsQ + local] * f1;
                     }
-                    named_bar_sync(3, kSoftmax);
                 } else {
-                    named_bar_sync(3, kSoftmax);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                }
+                if (fix && live) p.add_special(x, token, k, o);
+                if (l == 0.f || l != l) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = nan;
+                }
+                if (whole) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        *reinterpret_cast<uint4*>(stage + swizzled(lane, ((k & 32) + i) >> 3)) =
+                            make_uint4(pack2(o[i] * inv, o[i + 1] * inv), pack2(o[i + 2] * inv, o[i + 3] * inv),
+                                       pack2(o[i + 4] * inv, o[i + 5] * inv), pack2(o[i + 6] * inv, o[i + 7] * inv));
+                    if (k & 32) {
+                        // 64 dims of the warp's rows are there: eight lanes a row (a row per lane would take a line per lane and
+                        // access; 64 ragged prompts of up to 1,024 tokens then took 5,000 cycles a block for this)
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = 4 * i + (lane >> 3);
+                            const unsigned long long at = __shfl_sync(0xffffffffu, writes ? (unsigned long long)out : 0ull, r);
+                            const uint4 v = *reinterpret_cast<const uint4*>(stage + swizzled(r, lane & 7));
+                            if (at) *reinterpret_cast<uint4*>(reinterpret_cast<__half*>(at) + (k & ~32) + 8 * (lane & 7)) = v;
+                        }
+                        __syncwarp();
+                    }
+                } else if (writes) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<float4*>(part + k + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                 }
             }
-            if (X::kStreams == 2 && !pair && s == 1) continue;
-            float o[32];                            // dims k .. k + 31
-            if (n > 0) {
-                uint32_t raw[32];
-                tmem_ld32(o_at + k, raw);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float a = __uint_as_float(raw[i]);
-                    if (merge) a = a * f0 + swap[(k % (D / 2) + i) * kRowsQ + local] * f1;
-                    o[i] = a;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = 0.f;
-            }
-            if (fix && live) p.add_special(x, token, k, o);
-            if (l == 0.f || l != l) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = nan;
-            }
-            if (writes && whole) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 8)
-                    *reinterpret_cast<uint4*>(out + k + i) =
-                        make_uint4(pack2(o[i] * inv, o[i + 1] * inv), pack2(o[i + 2] * inv, o[i + 3] * inv),
-                                   pack2(o[i + 4] * inv, o[i + 5] * inv), pack2(o[i + 6] * inv, o[i + 7] * inv));
-            } else if (writes) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    *reinterpret_cast<float4*>(part + k + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-            }
+            if (merge) named_bar_sync(2, kSoftmax);                 // the second stream's dims have been read
         }
         if (writes && !whole) p.o.part_ml[(long long)x.part * X::kBlock + local] = make_float2(ref, l);
-        if (merge) named_bar_sync(2, kSoftmax);                     // the second half has been read
         tc::fence_before_sync();
     }
 }
 
 // Start of a CTA.  Barriers' counts: an entry's arrival 1 (full_count), its release 1 + free_extra.
-__device__ __forceinline__ void control_init(Control& c, int full_count, int clean_count, int free_count, bool dead) {
+__device__ __forceinline__ void control_init(Control& c, int full_count, int clean_count, int free_count, int q_count, bool dead) {
     for (int i = 0; i < kMaxStages; ++i) {
         mbar_init(&c.full[i], full_count);
         mbar_init(&c.clean[i], clean_count);
         mbar_init(&c.freed[i], free_count);
     }
     for (int i = 0; i < 2; ++i) {
-        mbar_init(&c.q_full[i], kRowsQ);
+        mbar_init(&c.q_full[i], q_count);
+        mbar_init(&c.q_freed[i], 1);
         mbar_init(&c.s_full[i], 1);
         mbar_init(&c.p_full[i], 4);
         mbar_init(&c.o_last[i], 1);
@@ -708,6 +720,7 @@ __device__ __forceinline__ void control_init(Control& c, int full_count, int cle
     mbar_init(&c.drained, 1);
     fence_mbar_init();
     c.dead = dead;
+    c.q_loads[0] = c.q_loads[1] = 0;
     for (int i = 0; i < kMaxStages * 2; ++i) c.special[i] = 0;
 }
 

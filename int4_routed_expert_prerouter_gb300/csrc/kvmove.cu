@@ -54,9 +54,9 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactP
                    ((long long)h * (p.c.page_tokens / kv::kStrip) + token / kv::kStrip) * kStripBytes + half * kHalf;
         return at + (pairs ? kv::kStrip * kR + row * kSb : row * kR + ((piece ^ kv::turn(kR, row)) << 4));
     };
-    for (int r0 = lo; r0 < hi; r0 += par * kMoveRows) {
-        uint4 v[kMoveRows];
-        char* to[kMoveRows];
+    uint4 v[2][kMoveRows];
+    char* to[2][kMoveRows];
+    auto load = [&](int r0, uint4 (&v)[kMoveRows], char* (&to)[kMoveRows]) {
 #pragma unroll
         for (int u = 0; u < kMoveRows; ++u) {
             const int r = r0 + sub + u * par;
@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactP
             else if (kSb == 8) *reinterpret_cast<uint2*>(&v[u]) = *reinterpret_cast<const uint2*>(s);
             else v[u] = *reinterpret_cast<const uint4*>(s);
         }
-        __syncthreads();
+    };
+    auto store = [&](const uint4 (&v)[kMoveRows], char* const (&to)[kMoveRows]) {
 #pragma unroll
         for (int u = 0; u < kMoveRows; ++u) {
             if (!to[u]) continue;
@@ -85,6 +86,18 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactP
             else if (kSb == 8) *reinterpret_cast<uint2*>(to[u]) = make_uint2(v[u].x, v[u].y);
             else *reinterpret_cast<uint4*>(to[u]) = v[u];
         }
+    };
+    // a chunk is read while the one before is still to be written: what that one writes lies in front of its sources
+    const int chunk = par * kMoveRows;
+    load(lo, v[0], to[0]);
+    for (int r0 = lo; r0 < hi; r0 += 2 * chunk) {
+        load(r0 + chunk, v[1], to[1]);
+        __syncthreads();
+        store(v[0], to[0]);
+        if (r0 + chunk >= hi) break;
+        load(r0 + 2 * chunk, v[0], to[0]);
+        __syncthreads();
+        store(v[1], to[1]);
     }
 }
 
@@ -97,7 +110,7 @@ struct CopyP {
 };
 
 constexpr int kCopyVec = 8;              // 16-byte loads that a thread has under way
-constexpr int kCopyPart = kMoveThreads * kCopyVec * 16;
+constexpr int kCopyPart = kMoveThreads * kCopyVec;      // pieces of 16 bytes of a part, at most
 
 __global__ void __launch_bounds__(kMoveThreads) kv_copy_pages_kernel(const CopyP p) {
     wait_predecessor();
@@ -111,27 +124,27 @@ __global__ void __launch_bounds__(kMoveThreads) kv_copy_pages_kernel(const CopyP
             if (p.status && part == 0 && threadIdx.x == 0) atomicExch(p.status, EDGE0_EINVAL);
             continue;
         }
-        const long long first = (long long)part * kCopyPart + threadIdx.x * 16;
-        const char* from = p.c.pages + s * p.c.page_bytes;
-        char* to = p.c.pages + d * p.c.page_bytes;
+        // parts of one length, so that none is nearly empty
+        const int pieces = (int)(p.c.page_bytes / 16), each = (pieces + p.parts - 1) / p.parts, first = part * each;
+        const int n = min(each, pieces - first);
+        const uint4* from = reinterpret_cast<const uint4*>(p.c.pages + s * p.c.page_bytes) + first;
+        uint4* to = reinterpret_cast<uint4*>(p.c.pages + d * p.c.page_bytes) + first;
         uint4 v[kCopyVec];
 #pragma unroll
         for (int u = 0; u < kCopyVec; ++u)
-            if (first + u * kMoveThreads * 16 < p.c.page_bytes)
-                v[u] = *reinterpret_cast<const uint4*>(from + first + u * kMoveThreads * 16);
+            if (u * kMoveThreads + (int)threadIdx.x < n) v[u] = from[u * kMoveThreads + threadIdx.x];
 #pragma unroll
         for (int u = 0; u < kCopyVec; ++u)
-            if (first + u * kMoveThreads * 16 < p.c.page_bytes)
-                *reinterpret_cast<uint4*>(to + first + u * kMoveThreads * 16) = v[u];
+            if (u * kMoveThreads + (int)threadIdx.x < n) to[u * kMoveThreads + threadIdx.x] = v[u];
     }
 }
 
 template <int BITS, int D>
 int launch_compact(CompactP p, int B, cudaStream_t stream) {
     constexpr int kPieces = kv::row_bytes(BITS, D) / 16 + 1;
-    // CTAs that share a (sequence, head, half): until two per SM are there; each a piece at least
+    // CTAs that share a (sequence, head, half): until four per SM are there; each a piece at least
     const long long ctas = (long long)B * p.c.H * 2;
-    const long long want = (304 + ctas - 1) / ctas;
+    const long long want = (608 + ctas - 1) / ctas;
     p.splits = want > kPieces ? kPieces : (int)want;
     return launch_early(kv_compact_kernel<BITS, D>, dim3(2 * p.splits, p.c.H, B), kMoveThreads, 0, stream, p);
 }
@@ -178,7 +191,7 @@ extern "C" int edge0_kv_copy_pages(const edge0_kv_cache* cache, const int32_t* s
     p.src = src;
     p.dst = dst;
     p.n = n;
-    p.parts = (int)((p.c.page_bytes + kCopyPart - 1) / kCopyPart);
+    p.parts = (int)((p.c.page_bytes / 16 + kCopyPart - 1) / kCopyPart);
     p.status = status;
     const long long units = (long long)n * p.parts, most = 152 * 8;
     return launch_early(kv_copy_pages_kernel, dim3((unsigned)(units < most ? units : most)), kMoveThreads, 0, stream, p);
