@@ -14,9 +14,11 @@
 // A step: 64 tokens (32 of 256-wide heads).  Tensor memory holds two buffers of scores (one for 256; weights lie
 // over the scores they come from), the accumulators and, up to 128 dims, the queries; with those in shared
 // memory a step's products would read them from there each time.
-// Warps: 0-7 softmax, 16-row fragments of four rows a lane, so that a token's scales, read from shared memory, serve
-// four rows, and half of a step's tokens each; the block's rows are dealt 16 to a quarter of tensor memory, so that
-// up to 64 rows cost all warps half; 8 the matrix steps; 9 copies strips' halves (16 tokens of K or of V, one run of
+// Warps: 0-7 softmax, fragments of 16 rows, two a lane, so that a token's scales, read from shared memory, serve
+// two rows; two sets of four take the steps in turn, so that one's latencies lie under the other's work, and hand
+// the rows' references on from step to step; the block's rows are dealt 16 to a quarter of tensor memory, so that up
+// to 64 rows cost all warps half; loops over fragments and pieces stay rolled: with all of it unrolled a third of the
+// stalls were for instructions to arrive; 8 the matrix steps; 9 copies strips' halves (16 tokens of K or of V, one run of
 // bytes) into a ring of raw ones; 10-15 turn those into operands and tables.
 #include "flash.cuh"
 
@@ -27,6 +29,7 @@ using namespace flash;
 
 constexpr int kMakers = 6;               // warps that turn codes into operands
 constexpr int kThreadsT = kSoftmax + 64 + 32 * kMakers;
+static_assert(kThreadsT == 512, "the register split");
 constexpr int kMaxRaw = 40;              // raw entries
 constexpr int kExt = 16;                 // columns of V' beside a group's 64 dims
 constexpr float kUpV = 1024.f;           // weights are that many times as large: p <= 2^4, m < 2.2
@@ -63,12 +66,13 @@ struct Tile {
 struct TreeControl {
     uint64_t k_full[4], k_freed[4], v_full[4], v_freed[4];           // stages
     uint64_t raw_full[kMaxRaw], raw_freed[kMaxRaw];
-    uint64_t q_full, s_full[2], p_full[2], o_step[2], o_last, drained;
+    uint64_t q_full, s_full[2], p_full[2], o_step[2], o_last, drained;      // (pairs: of even and of odd steps)
+    uint64_t ref_full[2][4];                                         // references of a quarter's halves after a step
     Place cut[2];
     uint32_t tmem;
     int dead;
     int special[16];      // numbers of the share's blocks with NaN of V that some rows do not see, by their last bits
-    float part_max[2][kRowsQ], sums[2][kRowsQ];
+    float ref[kRowsQ], sums[2][kRowsQ];
 };
 
 struct TreeP {
@@ -182,16 +186,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(a), EDGE0_I4(r, 0), EDGE0_I4(r, 4)
                  : "memory");
 }
-// whether any of the 64 threads that meet at a barrier wants it
-__device__ __forceinline__ bool any_of_64(int barrier, bool want) {
-    uint32_t r;
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-        : "=r"(r)
-        : "r"((uint32_t)want), "r"(barrier)
-        : "memory");
-    return r != 0;
-}
 // an operand's descriptor without swizzle: 8 x 16-byte blocks, `leading` in the low word and `stride` apart
 __device__ __forceinline__ uint64_t desc_plain(uint32_t lo, uint32_t stride) {
     uint64_t d;
@@ -241,70 +235,73 @@ __device__ __forceinline__ bool make_rows(const char* raw, char* stage, int row0
     constexpr int kMostE = BITS == 4 ? 12 : 8, kFastE = 5;
     const int lane = threadIdx.x & 31;
     bool found = false;
-#pragma unroll
+#pragma unroll 1
     for (int j = 0; j < CH / 2; ++j) {
         const int i = j * 32 + lane, p = (i >> 3) % CH, tok = (i & 7) + 8 * ((i >> 3) / CH), g = p / CPG, row = row0 + tok;
         const uint4 codes = *reinterpret_cast<const uint4*>(raw + tok * X::kR + ((p ^ kv::turn(X::kR, tok)) << 4));
         const uint32_t sbw = *reinterpret_cast<const uint32_t*>(raw + 16 * X::kR + tok * kv::sb_bytes(X::kD) + g * 4);
         const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&sbw));
         const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-        const bool none = tok >= left, flat = sb.x == 0.f, first = p % CPG == 0;
+        const bool none = tok >= left, flat = sb.x == 0.f, nan = sb.x != sb.x || sb.y != sb.y, out = none || (nan && tok >= drafted);
+        // V's z is 1 less in every other token: codes lie around half a step below half their range, and sums that grow with the
+        // context, of codes and offsets apart, would lose to the rounding of the matrix steps' accumulators, which
+        // is towards one side (after 25,000 tokens 1e-5 of V's size)
+        const uint32_t less = value ? row & 1 : 0;
+        const int exponent = (int)((sbw >> 10) & 31) - 15, e = value ? max(-10, min(kMostE, exponent)) : -10;
+        // a piece's 8-dim words lie `odd` and `twos` apart: K's in steps of 16 dims, V's in columns of 8
+        const int c8 = p * kPer, odd = value ? T * 16 : 128, twos = T * 32;
+        char* to = stage + (value ? (g * (X::kCols / 8) + (c8 & 7)) * (T * 16) + row * 16 : (c8 >> 1) * (T * 32) + tc::kstep_off(row, 0));
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+            uint4 v = codes8<BITS>(w[x * kW], w[x * kW + kW - 1], min(e, kFastE), less, value && (out || nan || flat));
+            if (e > kFastE) {
+                const uint32_t up = (uint32_t)(0x3C00 + ((e - kFastE) << 10)) * 0x10001u;
+                v.x = hfma2(v.x, up, 0x80008000u);
+                v.y = hfma2(v.y, up, 0x80008000u);
+                v.z = hfma2(v.z, up, 0x80008000u);
+                v.w = hfma2(v.w, up, 0x80008000u);
+            }
+            *reinterpret_cast<uint4*>(to + (x & 1) * odd + (x >> 1) * twos) = v;
+        }
+        if (p % CPG != 0) continue;
         const int pair = (row >> 1) * 2 * X::GR + 2 * g + (row & 1);
         if (!value) {
-#pragma unroll
-            for (int x = 0; x < kPer; ++x) {
-                const int c8 = p * kPer + x;                         // 8 dims
-                *reinterpret_cast<uint4*>(stage + (c8 >> 1) * (T * 32) + tc::kstep_off(row, (c8 & 1) * 8)) =
-                    codes8<BITS>(w[x * kW], w[x * kW + kW - 1], -10, 0, false);
-            }
-            if (first) {
-                // b = 1 (0 - z + b + z) of a constant group
-                const float off = none ? 0.f : flat ? sb.y + kZ : __fdividef(sb.y, sb.x) + kZ;
-                reinterpret_cast<float*>(stage + X::kKTab)[pair] = none ? 0.f : (flat ? 1.f : sb.x) * c * 1024.f;
-                // (hi, 2^11 lo) of the mean against (off, off / 2^11), then against what these leave
-                const uint32_t a = split<0>(off * (kGroup / 1024.f)), b = split<0>(off * (kGroup / 1024.f / 2048.f));
-                *reinterpret_cast<uint2*>(stage + X::kKOffs + tc::kstep_off(row, 4 * g)) =
-                    make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
-            }
+            // b = 1 (0 - z + b + z) of a constant group
+            const float off = none ? 0.f : flat ? sb.y + kZ : __fdividef(sb.y, sb.x) + kZ;
+            reinterpret_cast<float*>(stage + X::kKTab)[pair] = none ? 0.f : (flat ? 1.f : sb.x) * c * 1024.f;
+            // (hi, 2^11 lo) of the mean against (off, off / 2^11), then against what these leave
+            const uint32_t a = split<0>(off * (kGroup / 1024.f)), b = split<0>(off * (kGroup / 1024.f / 2048.f));
+            *reinterpret_cast<uint2*>(stage + X::kKOffs + tc::kstep_off(row, 4 * g)) =
+                make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
         } else {
-            const bool nan = sb.x != sb.x || sb.y != sb.y, out = none || (nan && tok >= drafted);
             found = found || (nan && !none && tok >= drafted);
-            // z is 1 less in every other token: codes lie around half a step below half their range, and sums that grow with the
-            // context, of codes and offsets apart, would lose to the rounding of the matrix steps' accumulators, which
-            // is towards one side (after 25,000 tokens 1e-5 of V's size)
-            const uint32_t less = row & 1;
-            int e = (int)((sbw >> 10) & 31) - 15;
-            e = max(-10, min(kMostE, e));
-            const bool zeros = out || nan || flat;
-#pragma unroll
-            for (int x = 0; x < kPer; ++x) {
-                const int c8 = p * kPer + x;
-                uint4 v = codes8<BITS>(w[x * kW], w[x * kW + kW - 1], min(e, kFastE), less, zeros);
-                if (e > kFastE) {
-                    const uint32_t up = (uint32_t)(0x3C00 + ((e - kFastE) << 10)) * 0x10001u;
-                    v.x = hfma2(v.x, up, 0x80008000u);
-                    v.y = hfma2(v.y, up, 0x80008000u);
-                    v.z = hfma2(v.z, up, 0x80008000u);
-                    v.w = hfma2(v.w, up, 0x80008000u);
-                }
-                *reinterpret_cast<uint4*>(stage + (g * (X::kCols / 8) + (c8 & 7)) * (T * 16) + row * 16) = v;
-            }
-            if (first) {
-                const float m = out ? 0.f : nan ? __int_as_float(0x7fffffff) : flat ? 1.f : sb.x * __uint_as_float((uint32_t)(127 - e) << 23);
-                const float r = out || nan ? 0.f : flat ? sb.y : __fdividef(sb.y, m) + (kZ - (float)less) * __uint_as_float((uint32_t)(127 + e) << 23);
-                reinterpret_cast<float*>(stage + X::kVTab)[pair] = m * kUpV;
-                *reinterpret_cast<uint4*>(stage + (g * (X::kCols / 8) + 8) * (T * 16) + row * 16) = make_uint4(split<0>(r), 0, 0, 0);
-            }
+            const float m = out ? 0.f : nan ? __int_as_float(0x7fffffff) : flat ? 1.f : sb.x * __uint_as_float((uint32_t)(127 - e) << 23);
+            const float r = out || nan ? 0.f : flat ? sb.y : __fdividef(sb.y, m) + (kZ - (float)less) * __uint_as_float((uint32_t)(127 + e) << 23);
+            reinterpret_cast<float*>(stage + X::kVTab)[pair] = m * kUpV;
+            *reinterpret_cast<uint4*>(stage + (g * (X::kCols / 8) + 8) * (T * 16) + row * 16) = make_uint4(split<0>(r), 0, 0, 0);
         }
     }
     return found;
 }
 
 // ------------------------------------------------- the softmax warps ----
+// Waits for a phase of a barrier, each thread by itself
+__device__ __forceinline__ bool wait_alone(uint64_t* bar, uint32_t parity, int& dead, unsigned long long limit) {
+    if (mbar_try_wait(bar, parity)) return true;
+    unsigned long long t0, now;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    for (;;) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*(volatile int*)&dead) return false;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        if (now - t0 > limit) *(volatile int*)&dead = 1;
+    }
+}
+
 template <class X>
 __device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, char* smem) {
-    constexpr int D = X::kD, GR = X::GR, T = X::kTile, NB = T / 16;             // 8-token blocks of a warp's half
-    const int wid = threadIdx.x >> 5, hf = wid >> 2, quad = wid & 3, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    constexpr int D = X::kD, GR = X::GR, T = X::kTile, NB = T / 16;             // 8-token blocks of half a tile
+    const int wid = threadIdx.x >> 5, set = wid >> 2, quad = wid & 3, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t tm = c.tmem + ((uint32_t)(32 * quad) << 16);
     const unsigned long long limit = p.o.wait_ns;
     // row 2 rh + k of a lane: fragment row g + 8 k of the quarter's half rh
@@ -324,7 +321,7 @@ __device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, c
             const int at = x.row0 + (live ? local : 0), token = at / p.G, head = x.h * p.G + at - token * p.G;
             const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(x.s.q0 + token) * p.ldq + (long long)head * D);
 #pragma unroll 1
-            for (int gr = hf; gr < GR; gr += 2) {
+            for (int gr = set; gr < GR; gr += 2) {
                 uint4 v[8];
                 uint32_t w[32];
                 float sum = 0.f;
@@ -367,191 +364,255 @@ __device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, c
             __syncwarp();
             if (lane == 0) mbar_arrive(&c.q_full);
         }
-        // of each row: reference mu (exponent units; not set while the row has seen nothing), sum
-        float mu[4] = {0.f, 0.f, 0.f, 0.f}, l[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t unset = 15;
-        for (int j = 0; j < n; ++j) {
+        // of each row: the reference that the warp has its sum at (exponent units; -infinity while the row has seen nothing,
+        // and then 0 in its place), and the sum of its steps
+        float refs[2][2], sums[2][2];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            refs[r >> 1][r & 1] = -INFINITY;
+            sums[r >> 1][r & 1] = 0.f;
+        }
+        auto off = [](float ref) { return ref == -INFINITY ? 0.f : -ref; };
+        // takes a sum to the reference that the row has by now
+        auto take = [](float& ref, float& l, float now) {
+            if (now != ref) {
+                l *= ref == -INFINITY ? 0.f : ex2(ref - now);
+                ref = now;
+            }
+        };
+        for (int j = (base + set) & 1; j < n; j += 2) {
             const int tile = base + j, stage = tile % X::kStages, buf = tile % X::kBufs, tile_at = x.lo + j;
             const uint32_t parity = (tile / X::kStages) & 1;
-            const char *sk = smem + X::kK + stage * X::kKStage, *sv = smem + X::kV + stage * X::kVStage;
-            const uint32_t s_at = tm + buf * X::kScores;
-            // (after a wait that gave up the warp goes on with what is there: pairs of warps meet at barriers, and the rows are
-            // marked in the end)
-            ok = wait_phase(&c.k_full[stage], parity, c.dead, limit) && ok;
-            ok = wait_phase(&c.s_full[buf], (tile / X::kBufs) & 1, c.dead, limit) && ok;
-            tc::fence_after_sync();
-            f2 S[2][NB][2];                                          // [rh][8 tokens][k]: tokens 2t, 2t + 1
-            const float* mk = reinterpret_cast<const float*>(sk + X::kKTab) + (hf * (T / 4) + t) * 2 * GR;
-#pragma unroll
-            for (int gr = 0; gr < GR; ++gr) {
-                f2 s2[NB];                                           // a token's scale serves the lane's four rows
-#pragma unroll
-                for (int b = 0; b < NB; ++b) s2[b] = *reinterpret_cast<const f2*>(mk + b * 8 * GR + 2 * gr);
-                uint32_t raw[2][4 * NB];
-                ld_frag<NB>(s_at + gr * T + hf * (T / 2), raw[0]);
-                if (both) ld_frag<NB>(s_at + (16u << 16) + gr * T + hf * (T / 2), raw[1]);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int rh = 0; rh < 2; ++rh) {
-                    if (rh && !both) continue;
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const f2 v = pk(__uint_as_float(raw[rh][4 * b + 2 * k]), __uint_as_float(raw[rh][4 * b + 2 * k + 1]));
-                            S[rh][b][k] = fma2(v, s2[b], gr ? S[rh][b][k] : pk(-mu[2 * rh + k], -mu[2 * rh + k]));
-                        }
-                }
-            }
+            const float* mk = reinterpret_cast<const float*>(smem + X::kK + stage * X::kKStage + X::kKTab) + t * 2 * GR;
+            const float* mv = reinterpret_cast<const float*>(smem + X::kV + stage * X::kVStage + X::kVTab) + t * 2 * GR;
+            // (after a wait that gave up the warp goes on with what is there; the rows are marked in the end)
+            ok = wait_alone(&c.k_full[stage], parity, c.dead, limit) && ok;
+            ok = wait_alone(&c.s_full[tile & 1], (tile >> 1) & 1, c.dead, limit) && ok;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&c.k_freed[stage]);
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int rh = 0; rh < 2; ++rh) {
-                if (rh && !both) continue;
+            tc::fence_after_sync();
+            if (!both && lane == 0) mbar_arrive(&c.ref_full[1][quad]);           // (its phases go with the steps)
+#pragma unroll 1
+            for (int rh = 0; rh < (both ? 2 : 1); ++rh) {
+                const uint32_t s_at = tm + ((uint32_t)(16 * rh) << 16) + buf * X::kScores;
+                float ref[2], l[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const int r = 2 * rh + k;
-                    if (tile_at >= x.clear) {
-                        const int local = local_of(r);
-                        const uint32_t seen =
-                            local < x.rows ? p.seen_word(x, (x.row0 + local) / p.G, tile_at * T + hf * (T / 2)) >> (2 * t) : 0u;
+                    ref[k] = rh ? refs[1][k] : refs[0][k];
+                    l[k] = rh ? sums[1][k] : sums[0][k];
+                }
+                f2 S[2 * NB][2];                                     // [8 tokens][k]: tokens 2t, 2t + 1; less the reference
+                {
+                    uint32_t raw[GR][2][4 * NB];
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) {
+                    for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) ld_frag<NB>(s_at + gr * T + h * (T / 2), raw[gr][h]);
+                    tc::tmem_wait_ld();
+                    const f2 from[2] = {pk(off(ref[0]), off(ref[0])), pk(off(ref[1]), off(ref[1]))};
+#pragma unroll
+                    for (int b = 0; b < 2 * NB; ++b)
+#pragma unroll
+                        for (int gr = 0; gr < GR; ++gr) {
+                            const f2 s2 = *reinterpret_cast<const f2*>(mk + b * 8 * GR + 2 * gr);
+                            const uint32_t* v = &raw[gr][b / NB][4 * (b % NB)];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                S[b][k] = fma2(pk(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), s2, gr ? S[b][k] : from[k]);
+                        }
+                }
+                if (rh || !both) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&c.k_freed[stage]);
+                }
+                if (tile_at >= x.clear) {
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {
+                        const int local = 64 * rh + 16 * quad + g + 8 * k;
+                        uint32_t seen[2] = {0, 0};
+                        if (local < x.rows) {
+                            const int token = (x.row0 + local) / p.G;
+                            seen[0] = p.seen_word(x, token, tile_at * T) >> (2 * t);
+                            seen[1] = p.seen_word(x, token, tile_at * T + T / 2) >> (2 * t);
+                        }
+#pragma unroll
+                        for (int b = 0; b < 2 * NB; ++b) {
                             float u, v;
-                            unpk(S[rh][b][k], u, v);
-                            S[rh][b][k] = pk((seen >> (8 * b)) & 1 ? u : -INFINITY, (seen >> (8 * b)) & 2 ? v : -INFINITY);
+                            const uint32_t bits = seen[b / NB] >> (8 * (b % NB));
+                            unpk(k ? S[b][1] : S[b][0], u, v);
+                            const f2 to = pk(bits & 1 ? u : -INFINITY, bits & 2 ? v : -INFINITY);
+                            S[b][0] = k ? S[b][0] : to;
+                            S[b][1] = k ? to : S[b][1];
                         }
                     }
+                }
+                float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
+                for (int b = 0; b < 2 * NB; ++b)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
                         float u, v;
-                        unpk(S[rh][b][k], u, v);
-                        mx[r] = fmaxf(mx[r], fmaxf(u, v));
+                        unpk(S[b][k], u, v);
+                        mx[k] = fmaxf(mx[k], fmaxf(u, v));
                     }
-                }
-            }
-            bool want = false;
+                // the references after the step before, of the other set; a block's first step starts afresh
+                ok = wait_alone(&c.ref_full[rh][quad], (tile + 1) & 1, c.dead, limit) && ok;
+                __syncwarp();
+                float* at = c.ref + 64 * rh + 16 * quad + g;
+                float now[2], by[2];
+                bool want = false;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) want = want || mx[r] > ((unset >> r) & 1 ? -INFINITY : kRise);
-            if (any_of_64(4 + quad, want)) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-                    if (t == 0) c.part_max[hf][local_of(r)] = mx[r];
+                for (int k = 0; k < 2; ++k) {
+                    now[k] = j ? at[8 * k] : -INFINITY;
+                    by[k] = off(now[k]) - off(ref[k]);               // what these scores lack
+                    mx[k] += by[k];
+                    want = want || mx[k] > (now[k] == -INFINITY ? -INFINITY : kRise);
                 }
-                named_bar_sync(8 + quad, 64);
-                float f[4];
+                float f[2] = {1.f, 1.f};
                 bool move = false;
+                if (__any_sync(0xffffffffu, want)) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float most = fmaxf(mx[r], c.part_max[hf ^ 1][local_of(r)]);
-                    const bool fresh = (unset >> r) & 1, moves = most > (fresh ? -INFINITY : kRise);
-                    const float by = moves ? most : 0.f;
-                    f[r] = !moves ? 1.f : fresh ? 0.f : ex2(-by);
-                    if (moves) unset &= ~(1u << r);
-                    move = move || moves;
-                    mu[r] += by;
-                    l[r] *= f[r];
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        if (r < 2 || both) S[r >> 1][b][r & 1] = add2(S[r >> 1][b][r & 1], pk(-by, -by));
-                }
-                // (the block's first tile overwrites the accumulators)
-                if (j > 0 && __any_sync(0xffffffffu, move)) {
-                    if (X::kBufs == 2) {        // (one buffer: the product was over before these scores were formed)
-                        ok = wait_phase(&c.o_step[(tile - 1) & 1], ((tile - 1) >> 1) & 1, c.dead, limit) && ok;
-                        tc::fence_after_sync();
+                    for (int k = 0; k < 2; ++k) {
+                        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+                        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+                        const bool fresh = now[k] == -INFINITY;
+                        if (mx[k] > (fresh ? -INFINITY : kRise)) {
+                            f[k] = fresh ? 0.f : ex2(-mx[k]);
+                            now[k] = mx[k] - off(now[k]);
+                            by[k] = off(now[k]) - off(ref[k]);
+                            move = true;
+                        }
                     }
+                }
+                if ((move || j == 0) && t == 0) {
+                    at[0] = now[0];
+                    at[8] = now[1];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.ref_full[rh][quad]);
+                if (__any_sync(0xffffffffu, by[0] != 0.f || by[1] != 0.f || now[0] != ref[0] || now[1] != ref[1])) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        take(ref[k], l[k], now[k]);
+#pragma unroll
+                        for (int b = 0; b < 2 * NB; ++b) S[b][k] = add2(S[b][k], pk(by[k], by[k]));
+                    }
+                    // (the block's first tile overwrites the accumulators)
+                    if (j > 0 && __any_sync(0xffffffffu, move)) {
+                        if (X::kBufs == 2) {    // (one buffer: the product was over before these scores were formed)
+                            ok = wait_alone(&c.o_step[(tile - 1) & 1], ((tile - 1) >> 1) & 1, c.dead, limit) && ok;
+                            __syncwarp();
+                            tc::fence_after_sync();
+                        }
 #pragma unroll 1
-                    for (int q = hf; q < GR * (X::kCols / 16); q += 2)
-#pragma unroll 1
-                        for (int rh = 0; rh < (both ? 2 : 1); ++rh) {
+                        for (int q = 0; q < GR * (X::kCols / 16); ++q) {
                             uint32_t a[8];
                             const uint32_t o_at = tm + ((uint32_t)(16 * rh) << 16) + X::kO + 16 * q;
                             ld_frag<2>(o_at, a);
                             tc::tmem_wait_ld();
-                            const float f0 = rh ? f[2] : f[0], f1 = rh ? f[3] : f[1];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) a[i] = __float_as_uint(__uint_as_float(a[i]) * (i & 2 ? f1 : f0));
+                            for (int i = 0; i < 8; ++i) a[i] = __float_as_uint(__uint_as_float(a[i]) * (i & 2 ? f[1] : f[0]));
                             st_frag2(o_at, a);
                         }
+                    }
                 }
-            }
-#pragma unroll
-            for (int rh = 0; rh < 2; ++rh) {
-                if (rh && !both) continue;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     f2 sum = 0;
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
+                    for (int b = 0; b < 2 * NB; ++b) {
                         float u, v;
-                        unpk(S[rh][b][k], u, v);
-                        S[rh][b][k] = pk(ex2(u), ex2(v));
-                        sum = b ? add2(sum, S[rh][b][k]) : S[rh][b][k];
+                        unpk(S[b][k], u, v);
+                        S[b][k] = pk(ex2(u), ex2(v));
+                        sum = b ? add2(sum, S[b][k]) : S[b][k];
                     }
                     float u, v;
                     unpk(sum, u, v);
-                    l[2 * rh + k] += u + v;
+                    l[k] += u + v;
+                    refs[0][k] = rh ? refs[0][k] : ref[k];
+                    refs[1][k] = rh ? ref[k] : refs[1][k];
+                    sums[0][k] = rh ? sums[0][k] : l[k];
+                    sums[1][k] = rh ? l[k] : sums[1][k];
                 }
-            }
-            ok = wait_phase(&c.v_full[stage], parity, c.dead, limit) && ok;
-            const float* mv = reinterpret_cast<const float*>(sv + X::kVTab) + (hf * (T / 4) + t) * 2 * GR;
+                if (rh == 0) {
+                    ok = wait_alone(&c.v_full[stage], parity, c.dead, limit) && ok;
+                    __syncwarp();
+                }
 #pragma unroll
-            for (int gr = 0; gr < GR; ++gr) {
-                f2 m2[NB];
+                for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
-                for (int b = 0; b < NB; ++b) m2[b] = *reinterpret_cast<const f2*>(mv + b * 8 * GR + 2 * gr);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t w[2 * NB];
 #pragma unroll
-                for (int rh = 0; rh < 2; ++rh) {
-                    if (rh && !both) continue;
-                    uint32_t w[2 * NB];
+                        for (int b = 0; b < NB; ++b) {
+                            const f2 m2 = *reinterpret_cast<const f2*>(mv + (h * NB + b) * 8 * GR + 2 * gr);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            float u, v;
-                            unpk(mul2(S[rh][b][k], m2[b]), u, v);
-                            w[2 * b + k] = pack2(u, v);
+                            for (int k = 0; k < 2; ++k) {
+                                float u, v;
+                                unpk(mul2(S[h * NB + b][k], m2), u, v);
+                                w[2 * b + k] = pack2(u, v);
+                            }
                         }
-                    st_pairs<NB>(s_at + ((uint32_t)(16 * rh) << 16) + gr * T + hf * (T / 2), w);
-                }
+                        st_pairs<NB>(s_at + gr * T + h * (T / 2), w);
+                    }
             }
             tmem_wait_st();
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&c.p_full[buf]);
+            if (lane == 0) mbar_arrive(&c.p_full[tile & 1]);
+        }
+        float ref[4], l[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            ref[r] = refs[r >> 1][r & 1];
+            l[r] = sums[r >> 1][r & 1];
         }
         base += n;
         uint32_t nans[4] = {0, 0, 0, 0};
         if (n > 0) {
-            ok = wait_phase(&c.o_last, blocks++ & 1, c.dead, limit) && ok;
+            ok = wait_alone(&c.ref_full[0][quad], (base - 1) & 1, c.dead, limit) && ok;
+            ok = wait_alone(&c.ref_full[1][quad], (base - 1) & 1, c.dead, limit) && ok;
+            ok = wait_alone(&c.o_last, blocks++ & 1, c.dead, limit) && ok;
+            __syncwarp();
             tc::fence_after_sync();
             const bool special = *(volatile int*)&c.special[number & 15] == number;
-            // a row's sum: its 4 lanes, then both halves of the tokens
+            // (once a wait has run out phases stand still, and a later one may look like one gone by)
+            ok = ok && !*(volatile int*)&c.dead;
+            // a row's sum at its last reference: its 4 lanes, then both sets' steps
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
+                if (r < 2 || both) take(ref[r], l[r], c.ref[local_of(r)]);
                 l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
                 l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
                 if (!ok) l[r] = __int_as_float(0x7fffffff);
-                if (t == 0) c.sums[hf][local_of(r)] = l[r];
+                if (t == 0) c.sums[set][local_of(r)] = l[r];
             }
             named_bar_sync(8 + quad, 64);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                l[r] += c.sums[hf ^ 1][local_of(r)];
+                l[r] += c.sums[set ^ 1][local_of(r)];
                 if (special && local_of(r) < x.rows) nans[r] = p.nan_groups(x, (x.row0 + local_of(r)) / p.G);
             }
         }
         const bool whole = x.part < 0;
+        // a row's place and factor
+        __half* out[4];
+        float* part[4];
+        float by[4];
 #pragma unroll
-        for (int rh = 0; rh < 2; ++rh) {
-            if (rh && !both) continue;
+        for (int r = 0; r < 4; ++r) {
+            const int local = local_of(r), at = x.row0 + min(local, x.rows - 1), token = at / p.G, head = x.h * p.G + at - token * p.G;
+            out[r] = local < x.rows && whole ? p.o.out + (long long)(x.s.q0 + token) * p.o.ldo + (long long)head * D : nullptr;
+            part[r] = local < x.rows && !whole ? p.o.part_o + ((long long)x.part * X::kBlock + local) * D : nullptr;
+            by[r] = whole ? (l[r] == 0.f ? 0.f : 1.f / (l[r] * kUpV)) : 1.f / kUpV;
+            if (l[r] != l[r]) by[r] = l[r];
+            if (part[r] && set == 0 && t == 0) p.o.part_ml[(long long)x.part * X::kBlock + local] = make_float2(ref[r], l[r]);
+        }
 #pragma unroll 1
-            for (int q = hf; q < D / 32; q += 2) {
-                const int gr = q >> 1;
+        for (int q = set; q < D / 32; q += 2) {
+            const int gr = q >> 1;
+#pragma unroll
+            for (int rh = 0; rh < 2; ++rh) {
+                if (rh && !both) continue;
                 uint32_t a[16], ext[4];
                 float add[2] = {0.f, 0.f};
                 if (n > 0) {
@@ -568,41 +629,27 @@ __device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, c
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const int r = 2 * rh + k, local = local_of(r);
-                    if (local >= x.rows) continue;
-                    const float sum = l[r];
-                    float f = whole ? (sum == 0.f ? 0.f : 1.f / (sum * kUpV)) : 1.f / kUpV;
-                    if (sum != sum) f = sum;
-                    if ((nans[r] >> gr) & 1) f = __int_as_float(0x7fffffff);
-                    const int at = x.row0 + local, token = at / p.G, head = x.h * p.G + at - token * p.G;
-                    __half* out = p.o.out + (long long)(x.s.q0 + token) * p.o.ldo + (long long)head * D + 32 * q;
-                    float* part = p.o.part_o + ((long long)x.part * X::kBlock + local) * D + 32 * q;
+                    const int r = 2 * rh + k;
+                    const float f = (nans[r] >> gr) & 1 ? __int_as_float(0x7fffffff) : by[r];
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
                         const float u = (__uint_as_float(a[4 * b + 2 * k]) + add[k]) * f, v = (__uint_as_float(a[4 * b + 2 * k + 1]) + add[k]) * f;
                         if (X::BITS == 4) {                          // columns 2t, 2t + 1 hold dims t, t + 4
-                            if (whole) {
-                                out[8 * b + t] = __float2half_rn(u);
-                                out[8 * b + t + 4] = __float2half_rn(v);
-                            } else {
-                                part[8 * b + t] = u;
-                                part[8 * b + t + 4] = v;
+                            if (out[r]) {
+                                out[r][32 * q + 8 * b + t] = __float2half_rn(u);
+                                out[r][32 * q + 8 * b + t + 4] = __float2half_rn(v);
+                            } else if (part[r]) {
+                                part[r][32 * q + 8 * b + t] = u;
+                                part[r][32 * q + 8 * b + t + 4] = v;
                             }
-                        } else if (whole) {
-                            *reinterpret_cast<uint32_t*>(out + 8 * b + 2 * t) = pack2(u, v);
-                        } else {
-                            *reinterpret_cast<float2*>(part + 8 * b + 2 * t) = make_float2(u, v);
+                        } else if (out[r]) {
+                            *reinterpret_cast<uint32_t*>(out[r] + 32 * q + 8 * b + 2 * t) = pack2(u, v);
+                        } else if (part[r]) {
+                            *reinterpret_cast<float2*>(part[r] + 32 * q + 8 * b + 2 * t) = make_float2(u, v);
                         }
                     }
                 }
             }
-            if (!whole && hf == 0 && t == 0)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int r = 2 * rh + k;
-                    if (local_of(r) < x.rows)
-                        p.o.part_ml[(long long)x.part * X::kBlock + local_of(r)] = make_float2((unset >> r) & 1 ? -INFINITY : mu[r], l[r]);
-                }
         }
         tc::fence_before_sync();
     }
@@ -637,11 +684,11 @@ __device__ __forceinline__ void tree_matrix(const Tree<X>& p, TreeControl& c, ch
             }
         }
         commit(&c.k_freed[stage], lead_lane);
-        commit(&c.s_full[buf], lead_lane);
+        commit(&c.s_full[tile & 1], lead_lane);
     };
     auto values = [&](int tile, bool first, bool last) {
         const int stage = tile % X::kStages, buf = tile % X::kBufs;
-        if (!wait_phase(&c.p_full[buf], (tile / X::kBufs) & 1, c.dead, limit)) return;
+        if (!wait_phase(&c.p_full[tile & 1], (tile >> 1) & 1, c.dead, limit)) return;
         if (!wait_phase(&c.v_full[stage], (tile / X::kStages) & 1, c.dead, limit)) return;
         tc::fence_after_sync();
         const uint32_t b = desc_lo(v0 + stage * X::kVStage, 128);
@@ -653,7 +700,7 @@ __device__ __forceinline__ void tree_matrix(const Tree<X>& p, TreeControl& c, ch
                        desc_plain(b + (gr * X::kCols * T * 2 + kk * 256) / 16, T * 16), tc::idesc_f16(kRowsQ, X::kCols) | (1u << 16),
                        !first || kk > 0, lead_lane);
         commit(&c.v_freed[stage], lead_lane);
-        commit(&c.o_step[buf], lead_lane);
+        commit(&c.o_step[tile & 1], lead_lane);
         if (last) commit(&c.o_last, lead_lane);
     };
     while (walk.next(x)) {
@@ -686,7 +733,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     if (threadIdx.x == 0) {
         for (int i = 0; i < X::kStages; ++i) {
             mbar_init(&c.k_full[i], X::kUnits);
-            mbar_init(&c.k_freed[i], 1 + kSoftmax / 32);             // the matrix steps, and the warps that read the table
+            mbar_init(&c.k_freed[i], 1 + 4);                         // the matrix steps, and the warps that read the table
             mbar_init(&c.v_full[i], X::kUnits);
             mbar_init(&c.v_freed[i], 1);
         }
@@ -696,10 +743,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c.s_full[i], 1);
-            mbar_init(&c.p_full[i], kSoftmax / 32);
+            mbar_init(&c.p_full[i], 4);
             mbar_init(&c.o_step[i], 1);
         }
         mbar_init(&c.q_full, kSoftmax / 32);
+        for (int i = 0; i < 8; ++i) mbar_init(&c.ref_full[0][i], 1);
         mbar_init(&c.o_last, 1);
         mbar_init(&c.drained, 1);
         fence_mbar_init();
@@ -717,6 +765,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     if (joins && threadIdx.x == 0) p.o.places[blockIdx.x] = c.cut[0];
     if (blockIdx.x == 0 && threadIdx.x < p.B && p.status && p.over(threadIdx.x)) atomicExch(p.status, EDGE0_EINVAL);
 
+    // registers: 256 x 160 + 256 x 96, what the CTA was launched with (512 x 128)
+    if (wid < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;\n");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
     if (wid < 8) {
         tree_softmax<X>(p, c, smem);
     } else if (wid == 8) {

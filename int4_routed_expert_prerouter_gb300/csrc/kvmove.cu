@@ -10,7 +10,7 @@ namespace edge0 {
 namespace {
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 4;             // rows that a thread has under way
+constexpr int kMoveRows = 2;             // rows that a thread has under way
 
 struct CompactP {
     kv::View c;
@@ -20,57 +20,71 @@ struct CompactP {
     const int* src;                      // [T]
     const int* cu;                       // [B + 1] or null: row b belongs to sequence b
     int T;
-    int splits;                          // CTAs that share the pieces of a (sequence, head, half)
     int* status;
 };
 
-// One CTA: some of the 16-byte pieces of one (sequence, head, K or V).  A row goes to a place
-// at or before its own, so no row's source is the destination of one before it: it is enough that
-// the CTA has read a chunk of rows before it writes them, and chunks follow in order.
-template <int BITS, int D>
-__global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactP p) {
-    constexpr int kR = kv::row_bytes(BITS, D), kCh = kR / 16, kSb = kv::sb_bytes(D), kPieces = kCh + 1;
+// One CTA: a (sequence, head, K or V).  A row goes to a place at or before its own, so no row's source is the
+// destination of one before it: it is enough that the CTA has read a chunk of rows before it writes them,
+// and chunks follow in order.  A chunk is read while the one before is still to be written, its rows' places are
+// looked up before that.
+template <int BITS, int D, int THREADS>
+__global__ void __launch_bounds__(THREADS) kv_compact_kernel(const CompactP p) {
+    constexpr int kR = kv::row_bytes(BITS, D), kSb = kv::sb_bytes(D), kPieces = kR / 16 + 1;
+    constexpr int kPar = THREADS / kPieces, kChunk = kPar * kMoveRows;
     constexpr int kStripBytes = kv::strip_bytes(BITS, D), kHalf = kv::half_bytes(BITS, D);
+    __shared__ long long from_s[2][kChunk], to_s[2][kChunk];         // strip's offset | row of the strip, or -1: nothing to do
     wait_predecessor();
     launch_dependents();
-    const int split = blockIdx.x % p.splits, half = (blockIdx.x / p.splits) & 1;
-    const int h = blockIdx.y, b = blockIdx.z;
-    const int lo = p.cu ? max(p.cu[b], 0) : b, hi = p.cu ? min(p.cu[b + 1], p.T) : b + 1;
+    const int h = blockIdx.x >> 1, half = blockIdx.x & 1, b = blockIdx.y;
     const int begin = p.cu ? p.cu[b] : b, start = p.start[b];
+    const int lo = max(begin, 0), hi = p.cu ? min(p.cu[b + 1], p.T) : b + 1;
     if (start < 0 || hi <= lo) return;
-    const int p0 = split * kPieces / p.splits, mine = (split + 1) * kPieces / p.splits - p0;
-    const int par = kMoveThreads / mine, sub = threadIdx.x / mine, piece = p0 + threadIdx.x - sub * mine;
-    const bool idle = sub >= par;
-    const bool pairs = piece == kCh;     // the row's (s, b) pairs
-    const bool tells = p.status && split == 0 && half == 0 && h == 0 && threadIdx.x == sub * mine;
-    // where the thread's piece of a position lies, or null
-    auto place = [&](long long pos) -> char* {
-        const long long pg = pos / p.c.page_tokens;
-        if (pos < 0 || pg >= p.W) return nullptr;
+    const int sub = threadIdx.x / kPieces, piece = threadIdx.x - sub * kPieces;
+    const bool idle = sub >= kPar, pairs = piece == kPieces - 1;     // the row's (s, b) pairs come last
+    char* base = p.c.pages + (long long)h * (p.c.page_tokens / kv::kStrip) * kStripBytes + half * kHalf;
+    auto strip_of = [&](unsigned pos) -> long long {
+        const unsigned pg = pos / (unsigned)p.c.page_tokens;
+        if (pg >= (unsigned)p.W) return -1;
         const int id = p.table[(long long)b * p.W + pg];
-        if (id < 0 || id >= p.c.n_pages) return nullptr;
-        const int token = (int)(pos - pg * p.c.page_tokens), row = token % kv::kStrip;
-        char* at = p.c.pages + id * p.c.page_bytes +
-                   ((long long)h * (p.c.page_tokens / kv::kStrip) + token / kv::kStrip) * kStripBytes + half * kHalf;
-        return at + (pairs ? kv::kStrip * kR + row * kSb : row * kR + ((piece ^ kv::turn(kR, row)) << 4));
+        if (id < 0 || id >= p.c.n_pages) return -1;
+        const unsigned token = pos - pg * p.c.page_tokens;
+        return id * p.c.page_bytes + (long long)(token / kv::kStrip) * kStripBytes + token % kv::kStrip;
+    };
+    auto look = [&](int r0, int buf) {
+        for (int i = threadIdx.x; i < kChunk; i += THREADS) {
+            const int r = r0 + i;
+            long long from = -1, to = -1;
+            if (r0 < hi && r < hi) {
+                const long long dst = (long long)start + r - begin;
+                const int src = p.src[r];
+                if (src != dst) {
+                    if (src > dst) {
+                        to = strip_of((unsigned)dst);
+                        from = strip_of((unsigned)src);
+                    }
+                    if (to < 0 || from < 0) {
+                        to = -1;
+                        if (p.status && h == 0 && half == 0) atomicExch(p.status, EDGE0_EINVAL);
+                    }
+                }
+            }
+            from_s[buf][i] = from;
+            to_s[buf][i] = to;
+        }
+    };
+    auto place = [&](long long strip) -> char* {
+        const int row = (int)(strip & 15);
+        return base + (strip - row) + (pairs ? kv::kStrip * kR + row * kSb : row * kR + ((piece ^ kv::turn(kR, row)) << 4));
     };
     uint4 v[2][kMoveRows];
     char* to[2][kMoveRows];
-    auto load = [&](int r0, uint4 (&v)[kMoveRows], char* (&to)[kMoveRows]) {
+    auto load = [&](int buf, uint4 (&v)[kMoveRows], char* (&to)[kMoveRows]) {
 #pragma unroll
         for (int u = 0; u < kMoveRows; ++u) {
-            const int r = r0 + sub + u * par;
             to[u] = nullptr;
-            if (idle || r >= hi) continue;
-            const long long dst = (long long)start + r - begin, src = p.src[r];
-            if (src == dst) continue;
-            char* t = src > dst ? place(dst) : nullptr;
-            const char* s = src > dst ? place(src) : nullptr;
-            if (!t || !s) {
-                if (tells) atomicExch(p.status, EDGE0_EINVAL);
-                continue;
-            }
-            to[u] = t;
+            if (idle || to_s[buf][sub + u * kPar] < 0) continue;
+            to[u] = place(to_s[buf][sub + u * kPar]);
+            const char* s = place(from_s[buf][sub + u * kPar]);
             if (!pairs) v[u] = *reinterpret_cast<const uint4*>(s);
             else if (kSb == 4) v[u].x = *reinterpret_cast<const uint32_t*>(s);
             else if (kSb == 8) *reinterpret_cast<uint2*>(&v[u]) = *reinterpret_cast<const uint2*>(s);
@@ -87,17 +101,25 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactP
             else *reinterpret_cast<uint4*>(to[u]) = v[u];
         }
     };
-    // a chunk is read while the one before is still to be written: what that one writes lies in front of its sources
-    const int chunk = par * kMoveRows;
-    load(lo, v[0], to[0]);
-    for (int r0 = lo; r0 < hi; r0 += 2 * chunk) {
-        load(r0 + chunk, v[1], to[1]);
-        __syncthreads();
+    look(lo, 0);
+    __syncthreads();
+    load(0, v[0], to[0]);
+    if (lo + kChunk < hi) look(lo + kChunk, 1);
+    for (int r0 = lo;; r0 += 2 * kChunk) {
+        __syncthreads();                         // chunk r0 has been read by all, the next one's places are there
+        if (r0 + kChunk < hi) {
+            load(1, v[1], to[1]);
+            look(r0 + 2 * kChunk, 0);
+        }
         store(v[0], to[0]);
-        if (r0 + chunk >= hi) break;
-        load(r0 + 2 * chunk, v[0], to[0]);
+        if (r0 + kChunk >= hi) break;
         __syncthreads();
+        if (r0 + 2 * kChunk < hi) {
+            load(0, v[0], to[0]);
+            look(r0 + 3 * kChunk, 1);
+        }
         store(v[1], to[1]);
+        if (r0 + 2 * kChunk >= hi) break;
     }
 }
 
@@ -135,18 +157,16 @@ __global__ void __launch_bounds__(kMoveThreads) kv_copy_pages_kernel(const CopyP
             if (u * kMoveThreads + (int)threadIdx.x < n) v[u] = from[u * kMoveThreads + threadIdx.x];
 #pragma unroll
         for (int u = 0; u < kCopyVec; ++u)
-            if (u * kMoveThreads + (int)threadIdx.x < n) to[u * kMoveThreads + threadIdx.x] = v[u];
+            if (u * kMoveThreads + (int)threadIdx.x < n) __stcs(&to[u * kMoveThreads + threadIdx.x], v[u]);      // (sources stay in the L2)
     }
 }
 
 template <int BITS, int D>
-int launch_compact(CompactP p, int B, cudaStream_t stream) {
-    constexpr int kPieces = kv::row_bytes(BITS, D) / 16 + 1;
-    // CTAs that share a (sequence, head, half): until four per SM are there; each a piece at least
-    const long long ctas = (long long)B * p.c.H * 2;
-    const long long want = (608 + ctas - 1) / ctas;
-    p.splits = want > kPieces ? kPieces : (int)want;
-    return launch_early(kv_compact_kernel<BITS, D>, dim3(2 * p.splits, p.c.H, B), kMoveThreads, 0, stream, p);
+int launch_compact(const CompactP& p, int B, cudaStream_t stream) {
+    // few rows per sequence: small CTAs, so that many fit; many: as many threads as there are, for chunks follow one another
+    // (7 contexts of 8,191 tokens of which up to 2,047 are kept, 256 and 1,024 threads: 27 and XX us)
+    if (p.T / B <= 64) return launch_early(kv_compact_kernel<BITS, D, 256>, dim3(2 * p.c.H, B), 256, 0, stream, p);
+    return launch_early(kv_compact_kernel<BITS, D, 1024>, dim3(2 * p.c.H, B), 1024, 0, stream, p);
 }
 
 }  // namespace
