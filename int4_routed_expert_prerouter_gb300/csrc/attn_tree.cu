@@ -60,7 +60,7 @@ struct Tile {
     static constexpr int kRoom = 232448 - 128 - kControlBytes - kRaw;
     static constexpr int kRaws = kRoom / kHalf < kMaxRaw ? kRoom / kHalf : kMaxRaw;
     static constexpr int kControl = kRaw + kRaws * kHalf, kSmem = kControl + kControlBytes + 128;
-    static_assert(kKStage % 128 == 0 && kVStage % 128 == 0 && kHalf % 16 == 0 && kRaws >= 2 * kUnits, "layout");
+    static_assert(kKStage % 128 == 0 && kVStage % 128 == 0 && kHalf % 16 == 0 && kRaws >= 2 * kUnits && kRaws >= kMakers * kUnits / 2, "layout");
 };
 
 struct TreeControl {
@@ -201,85 +201,115 @@ __device__ __forceinline__ uint32_t split(float v) {
 }
 
 // ----------------------------------------------------------------- makers ----
-// (code - z) 2^e of 8 dims, e <= 5 (up to there the step stays within fp16), z half the code range less `less`, 0 or 1;
-// 4 bits: one word, dims in the order 0 4 1 5 2 6 3 7; 8 bits: two words, in order.  0x6400 is 1024: a code below it
-// adds itself, a nibble 4 bits up 16 times itself.  none: zeros.
+// (code - z) 2^e of 8 dims; 4 bits: one word, dims in the order 0 4 1 5 2 6 3 7; 8 bits: two words, in order.  0x6400 is 1024:
+// a code below it adds itself, a nibble 4 bits up 16 times itself; m and a: 2^e and -(1024 + z) 2^e, 2^(e-4) and
+// -(64 + z) 2^e for such nibbles.
 template <int BITS>
-__device__ __forceinline__ uint4 codes8(uint32_t w0, uint32_t w1, int e, uint32_t less, bool none) {
-    const uint32_t up = (uint32_t)(e << 10) * 0x10001u;
-    const uint32_t m0 = none ? 0u : 0x3C003C00u + up;
-    const uint32_t a0 = none ? 0u : (BITS == 4 ? 0xE408E408u : 0xE480E480u) - less * 0x10001u + up;
+__device__ __forceinline__ uint4 codes8(uint32_t w0, uint32_t w1, const uint32_t (&m)[2], const uint32_t (&a)[2]) {
     uint4 r;
     if (BITS == 4) {
-        const uint32_t m1 = none ? 0u : 0x2C002C00u + up, a1 = none ? 0u : 0xD480D480u - less * 0x100010u + up, h = w0 >> 8;
-        r.x = hfma2((w0 & 0x000F000Fu) | 0x64006400u, m0, a0);
-        r.y = hfma2((w0 & 0x00F000F0u) | 0x64006400u, m1, a1);
-        r.z = hfma2((h & 0x000F000Fu) | 0x64006400u, m0, a0);
-        r.w = hfma2((h & 0x00F000F0u) | 0x64006400u, m1, a1);
+        const uint32_t h = w0 >> 8;
+        r.x = hfma2((w0 & 0x000F000Fu) | 0x64006400u, m[0], a[0]);
+        r.y = hfma2((w0 & 0x00F000F0u) | 0x64006400u, m[1], a[1]);
+        r.z = hfma2((h & 0x000F000Fu) | 0x64006400u, m[0], a[0]);
+        r.w = hfma2((h & 0x00F000F0u) | 0x64006400u, m[1], a[1]);
     } else {
-        r.x = hfma2(__byte_perm(w0, 0x64646464u, 0x4140), m0, a0);
-        r.y = hfma2(__byte_perm(w0, 0x64646464u, 0x4342), m0, a0);
-        r.z = hfma2(__byte_perm(w1, 0x64646464u, 0x4140), m0, a0);
-        r.w = hfma2(__byte_perm(w1, 0x64646464u, 0x4342), m0, a0);
+        r.x = hfma2(__byte_perm(w0, 0x64646464u, 0x4140), m[0], a[0]);
+        r.y = hfma2(__byte_perm(w0, 0x64646464u, 0x4342), m[0], a[0]);
+        r.z = hfma2(__byte_perm(w1, 0x64646464u, 0x4140), m[0], a[0]);
+        r.w = hfma2(__byte_perm(w1, 0x64646464u, 0x4342), m[0], a[0]);
     }
     return r;
 }
 
+constexpr int kFastE = 5;                // up to there the one step of codes8 stays within fp16
+constexpr uint32_t kZeros = 1u << 31;
+
 // A raw entry (16 tokens, the tile's from row0 on) into operands and tables, by a warp.  Tokens from `left` on come out as
 // zeros, and so do V's groups of NaN from `drafted` on, which some rows may not see (true: there were any).
-template <class X>
-__device__ __forceinline__ bool make_rows(const char* raw, char* stage, int row0, bool value, float c, int left, int drafted) {
-    constexpr int BITS = X::BITS, CH = X::kR / 16, CPG = CH / X::GR, T = X::kTile;
+template <class X, bool VALUE>
+__device__ __forceinline__ bool make_rows(const char* raw, char* stage, int row0, float c, int left, int drafted) {
+    constexpr int BITS = X::BITS, GR = X::GR, CH = X::kR / 16, CPG = CH / GR, T = X::kTile;
     constexpr int kPer = BITS == 4 ? 4 : 2, kW = BITS == 4 ? 1 : 2;  // 8-dim words per piece, 32-bit words of one
     constexpr float kZ = BITS == 4 ? 8.f : 128.f;
-    constexpr int kMostE = BITS == 4 ? 12 : 8, kFastE = 5;
+    constexpr int kMostE = BITS == 4 ? 12 : 8, kPass = (16 * GR + 31) / 32;
     const int lane = threadIdx.x & 31;
     bool found = false;
+    // tables and offsets, a (token, group) per lane; what V's codes need of them stays there: e, or kZeros
+    uint32_t kept[kPass];
+#pragma unroll
+    for (int q = 0; q < kPass; ++q) {
+        const int i = q * 32 + lane, tok = i / GR & 15, g = i % GR, row = row0 + tok;
+        const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(raw + 16 * X::kR + (tok * GR + g) * 4));
+        const bool none = tok >= left, flat = sb.x == 0.f;
+        float* table = reinterpret_cast<float*>(stage + (VALUE ? X::kVTab : X::kKTab)) + (row >> 1) * 2 * GR + 2 * g + (row & 1);
+        if (!VALUE) {
+            // b = 1 (0 - z + b + z) of a constant group
+            const float off = none ? 0.f : flat ? sb.y + kZ : __fdividef(sb.y, sb.x) + kZ;
+            // (hi, 2^11 lo) of the mean against (off, off / 2^11), then against what these leave
+            const uint32_t a = split<0>(off * (kGroup / 1024.f)), b = split<0>(off * (kGroup / 1024.f / 2048.f));
+            if (i < 16 * GR) {
+                *table = none ? 0.f : (flat ? 1.f : sb.x) * c * 1024.f;
+                *reinterpret_cast<uint2*>(stage + X::kKOffs + tc::kstep_off(row, 4 * g)) =
+                    make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+            }
+        } else {
+            const bool nan = sb.x != sb.x || sb.y != sb.y, out = none || (nan && tok >= drafted);
+            found = found || (nan && !none && tok >= drafted && i < 16 * GR);
+            // z is 1 less in every other token: codes lie around half a step below half their range, and sums that grow with the
+            // context, of codes and offsets apart, would lose to the rounding of the matrix steps' accumulators, which
+            // is towards one side (after 25,000 tokens 1e-5 of V's size)
+            const float z = kZ - (float)(row & 1);
+            const int e = max(-10, min(kMostE, (int)(__float_as_uint(sb.x) >> 23 & 255) - 127));
+            const float m = out ? 0.f : nan ? __int_as_float(0x7fffffff) : flat ? 1.f : sb.x * __uint_as_float((uint32_t)(127 - e) << 23);
+            const float r = out || nan ? 0.f : flat ? sb.y : __fdividef(sb.y, m) + z * __uint_as_float((uint32_t)(127 + e) << 23);
+            kept[q] = out || nan || flat ? kZeros : (uint32_t)(e + 16);
+            if (i < 16 * GR) {
+                *table = m * kUpV;
+                *reinterpret_cast<uint4*>(stage + (g * (X::kCols / 8) + 8) * (T * 16) + row * 16) = make_uint4(split<0>(r), 0, 0, 0);
+            }
+        }
+    }
 #pragma unroll 1
     for (int j = 0; j < CH / 2; ++j) {
         const int i = j * 32 + lane, p = (i >> 3) % CH, tok = (i & 7) + 8 * ((i >> 3) / CH), g = p / CPG, row = row0 + tok;
         const uint4 codes = *reinterpret_cast<const uint4*>(raw + tok * X::kR + ((p ^ kv::turn(X::kR, tok)) << 4));
-        const uint32_t sbw = *reinterpret_cast<const uint32_t*>(raw + 16 * X::kR + tok * kv::sb_bytes(X::kD) + g * 4);
-        const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&sbw));
         const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-        const bool none = tok >= left, flat = sb.x == 0.f, nan = sb.x != sb.x || sb.y != sb.y, out = none || (nan && tok >= drafted);
-        // V's z is 1 less in every other token: codes lie around half a step below half their range, and sums that grow with the
-        // context, of codes and offsets apart, would lose to the rounding of the matrix steps' accumulators, which
-        // is towards one side (after 25,000 tokens 1e-5 of V's size)
-        const uint32_t less = value ? row & 1 : 0;
-        const int exponent = (int)((sbw >> 10) & 31) - 15, e = value ? max(-10, min(kMostE, exponent)) : -10;
-        // a piece's 8-dim words lie `odd` and `twos` apart: K's in steps of 16 dims, V's in columns of 8
-        const int c8 = p * kPer, odd = value ? T * 16 : 128, twos = T * 32;
-        char* to = stage + (value ? (g * (X::kCols / 8) + (c8 & 7)) * (T * 16) + row * 16 : (c8 >> 1) * (T * 32) + tc::kstep_off(row, 0));
-#pragma unroll
-        for (int x = 0; x < kPer; ++x) {
-            uint4 v = codes8<BITS>(w[x * kW], w[x * kW + kW - 1], min(e, kFastE), less, value && (out || nan || flat));
-            if (e > kFastE) {
-                const uint32_t up = (uint32_t)(0x3C00 + ((e - kFastE) << 10)) * 0x10001u;
-                v.x = hfma2(v.x, up, 0x80008000u);
-                v.y = hfma2(v.y, up, 0x80008000u);
-                v.z = hfma2(v.z, up, 0x80008000u);
-                v.w = hfma2(v.w, up, 0x80008000u);
+        uint32_t m[2] = {0x14001400u, 0x04000400u}, a[2] = {BITS == 4 ? 0xBC08BC08u : 0xBC80BC80u, 0xAC80AC80u};     // K: e = -10
+        int e = -10;
+        if (VALUE) {
+            const int from = tok * GR + g;
+            uint32_t k = __shfl_sync(0xffffffffu, kept[0], from & 31);
+            if (kPass == 2) {
+                const uint32_t k1 = __shfl_sync(0xffffffffu, kept[kPass - 1], from & 31);
+                k = from >= 32 ? k1 : k;
             }
-            *reinterpret_cast<uint4*>(to + (x & 1) * odd + (x >> 1) * twos) = v;
+            e = (int)(k & 31) - 16;
+            const uint32_t up = (uint32_t)(min(e, kFastE) << 10) * 0x10001u, less = row & 1;
+            m[0] = 0x3C003C00u + up;
+            a[0] = (BITS == 4 ? 0xE408E408u : 0xE480E480u) - less * 0x10001u + up;
+            m[1] = 0x2C002C00u + up;
+            a[1] = 0xD480D480u - less * 0x100010u + up;
+            if (k & kZeros) m[0] = m[1] = a[0] = a[1] = 0u;
         }
-        if (p % CPG != 0) continue;
-        const int pair = (row >> 1) * 2 * X::GR + 2 * g + (row & 1);
-        if (!value) {
-            // b = 1 (0 - z + b + z) of a constant group
-            const float off = none ? 0.f : flat ? sb.y + kZ : __fdividef(sb.y, sb.x) + kZ;
-            reinterpret_cast<float*>(stage + X::kKTab)[pair] = none ? 0.f : (flat ? 1.f : sb.x) * c * 1024.f;
-            // (hi, 2^11 lo) of the mean against (off, off / 2^11), then against what these leave
-            const uint32_t a = split<0>(off * (kGroup / 1024.f)), b = split<0>(off * (kGroup / 1024.f / 2048.f));
-            *reinterpret_cast<uint2*>(stage + X::kKOffs + tc::kstep_off(row, 4 * g)) =
-                make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
-        } else {
-            found = found || (nan && !none && tok >= drafted);
-            const float m = out ? 0.f : nan ? __int_as_float(0x7fffffff) : flat ? 1.f : sb.x * __uint_as_float((uint32_t)(127 - e) << 23);
-            const float r = out || nan ? 0.f : flat ? sb.y : __fdividef(sb.y, m) + (kZ - (float)less) * __uint_as_float((uint32_t)(127 + e) << 23);
-            reinterpret_cast<float*>(stage + X::kVTab)[pair] = m * kUpV;
-            *reinterpret_cast<uint4*>(stage + (g * (X::kCols / 8) + 8) * (T * 16) + row * 16) = make_uint4(split<0>(r), 0, 0, 0);
+        // 8-dim words: K's in steps of 16 dims, V's in columns of 8
+        const int c8 = p * kPer;
+        char* to = stage + (VALUE ? (g * (X::kCols / 8) + (c8 & 7)) * (T * 16) + row * 16 : (c8 >> 1) * (T * 32) + tc::kstep_off(row, 0));
+        uint4 v[kPer];
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) v[x] = codes8<BITS>(w[x * kW], w[x * kW + kW - 1], m, a);
+        if (VALUE && __any_sync(0xffffffffu, e > kFastE)) {
+            const uint32_t up = (uint32_t)(0x3C00 + (max(e - kFastE, 0) << 10)) * 0x10001u;
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) {
+                v[x].x = hfma2(v[x].x, up, 0x80008000u);
+                v[x].y = hfma2(v[x].y, up, 0x80008000u);
+                v[x].z = hfma2(v[x].z, up, 0x80008000u);
+                v[x].w = hfma2(v[x].w, up, 0x80008000u);
+            }
         }
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) *reinterpret_cast<uint4*>(to + (VALUE ? x * (T * 16) : (x & 1) * 128 + (x >> 1) * (T * 32))) = v[x];
     }
     return found;
 }
@@ -732,9 +762,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < X::kStages; ++i) {
-            mbar_init(&c.k_full[i], X::kUnits);
+            mbar_init(&c.k_full[i], 2);                              // halves of the tile
             mbar_init(&c.k_freed[i], 1 + 4);                         // the matrix steps, and the warps that read the table
-            mbar_init(&c.v_full[i], X::kUnits);
+            mbar_init(&c.v_full[i], 2);
             mbar_init(&c.v_freed[i], 1);
         }
         for (int i = 0; i < X::kRaws; ++i) {
@@ -773,55 +803,101 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     } else if (wid == 8) {
         tree_matrix<X>(p, c, smem);
     } else if (wid == 9) {
+        // a lane: one of a tile's strips; behind the last token, that token's.  Pages' numbers are asked for kAhead tiles ahead.
+        constexpr int kAhead = 4;
         Feed<X, Tree<X>> feed(p, c.cut, blockIdx.x);
-        int unit = 0;
-        bool ok = limit != 0, more = feed.next();
-        // a lane: one of the tile's strips; behind the last token, that token's
-        auto source = [&]() { return p.place(feed.x.b, feed.x.h, min(feed.token() + 16 * (lane % X::kUnits), feed.x.s.n_k - 1), feed.value); };
-        const char* src = more ? source() : nullptr;
-        while (ok && more) {
-            const int u = unit + lane % X::kUnits, slot = u % X::kRaws;
-            const char* from = src;
-            more = feed.next();
-            if (more) src = source();                                // on its way during the wait
-            // (the phase before a barrier's first counts as over)
-            ok = wait_phase(&c.raw_freed[slot], (u / X::kRaws + 1) & 1, c.dead, limit);
-            if (!ok) break;
-            if (lane < X::kUnits) {
-                mbar_arrive_expect_tx(&c.raw_full[slot], X::kHalf);
-                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
-                                 smem_u32(smem + X::kRaw + slot * X::kHalf)),
-                             "l"(from), "r"((uint32_t)X::kHalf), "r"(smem_u32(&c.raw_full[slot]))
-                             : "memory");
+        int unit = 0, id[kAhead];
+        long long in_page[kAhead];
+        bool ok = limit != 0, more = true;
+        auto ask = [&](int& id, long long& in_page) {
+            more = more && feed.next();
+            id = -1;
+            if (!more) return;
+            const int token = min(feed.token() + 16 * (lane % X::kUnits), feed.x.s.n_k - 1);
+            const int pg = token / p.c.page_tokens, in = token - pg * p.c.page_tokens;
+            id = p.table[(long long)feed.x.b * p.W + pg];
+            in_page = ((long long)feed.x.h * (p.c.page_tokens / kv::kStrip) + in / kv::kStrip) * kv::strip_bytes(X::BITS, X::kD) +
+                      (feed.value ? X::kHalf : 0);
+        };
+        int asked = 0, had = 0;
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            ask(id[q], in_page[q]);
+            asked += more;
+        }
+        while (ok && had < asked) {
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                if (!ok || had >= asked) break;
+                ++had;
+                const int u = unit + lane % X::kUnits, slot = u % X::kRaws;
+                int page = id[q];
+                if (page < 0 || page >= p.c.n_pages) {
+                    page = 0;
+                    if (p.status) atomicExch(p.status, EDGE0_EINVAL);
+                }
+                const char* from = p.c.pages + page * p.c.page_bytes + in_page[q];
+                ask(id[q], in_page[q]);
+                asked += more;
+                // (the phase before a barrier's first counts as over)
+                ok = __all_sync(0xffffffffu, wait_alone(&c.raw_freed[slot], (u / X::kRaws + 1) & 1, c.dead, limit));
+                if (!ok) break;
+                if (lane < X::kUnits) {
+                    mbar_arrive_expect_tx(&c.raw_full[slot], X::kHalf);
+                    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                                     smem_u32(smem + X::kRaw + slot * X::kHalf)),
+                                 "l"(from), "r"((uint32_t)X::kHalf), "r"(smem_u32(&c.raw_full[slot]))
+                                 : "memory");
+                }
+                __syncwarp();
+                unit += X::kUnits;
             }
-            __syncwarp();
-            unit += X::kUnits;
         }
         // nothing may land in this memory when it has become another CTA's
         if (!ok) drain_copies_call(c.raw_full, unit > X::kRaws ? unit - X::kRaws : 0, unit, X::kRaws);
     } else {
-        Feed<X, Tree<X>> feed(p, c.cut, blockIdx.x);
-        int unit = 0, tiles[2] = {0, 0};
-        for (; feed.next(); unit += X::kUnits) {
-            const Item& x = feed.x;
-            const bool v = feed.value;
-            const int tile = v ? tiles[1]++ : tiles[0]++, stage = tile % X::kStages;
-            uint64_t *full = v ? &c.v_full[stage] : &c.k_full[stage], *freed = v ? &c.v_freed[stage] : &c.k_freed[stage];
-            char* to = v ? smem + X::kV + stage * X::kVStage : smem + X::kK + stage * X::kKStage;
-            bool ready = tile < X::kStages;
-            for (int i = (wid - 10 + kMakers - unit % kMakers) % kMakers; i < X::kUnits; i += kMakers) {
-                const int u = unit + i, slot = u % X::kRaws, token = feed.token() + 16 * i;
-                ready = ready || wait_phase(freed, (tile / X::kStages - 1) & 1, c.dead, limit);
-                if (!ready || !wait_phase(&c.raw_full[slot], (u / X::kRaws) & 1, c.dead, limit)) break;
-                if (make_rows<X>(smem + X::kRaw + slot * X::kHalf, to, 16 * i, v, p.o.c, x.s.n_k - token, x.s.ctx - token))
-                    *(volatile int*)&c.special[feed.number & 15] = feed.number;
+        // a maker: every kMakers-th half of a tile's K or V, in the ring's order
+        constexpr int kHalves = 2, kEach = X::kUnits / kHalves;
+        Walk<X, Tree<X>> walk(p, c.cut, blockIdx.x);
+        Item x;
+        int base = 0, number = 0, at = wid - 10;                     // tiles before the block; the next half, from the block's first on
+        while (walk.next(x)) {
+            const int n = x.hi - x.lo, lead = min(X::kBufs, n);
+            if (n > 0) ++number;
+            for (; at < 2 * n * kHalves; at += kMakers) {
+                // K tiles run `lead` ahead of V's, then V's alone are left
+                const int entry = at / kHalves, r = entry - lead, turns = 2 * (n - lead);
+                const bool v = r >= 0 && (r >= turns || !(r & 1));
+                const int i = r < 0 ? entry : r < turns ? (r >> 1) + (v ? 0 : lead) : r - (n - lead);
+                const int tile = base + i, stage = tile % X::kStages;
+                const uint32_t parity = (tile / X::kStages) & 1;
+                char* to = v ? smem + X::kV + stage * X::kVStage : smem + X::kK + stage * X::kKStage;
+                if (!__all_sync(0xffffffffu, wait_alone(v ? &c.v_freed[stage] : &c.k_freed[stage], parity ^ 1, c.dead, limit))) break;
+                bool found = false, ok = true;
+#pragma unroll 1
+                for (int k = 0; k < kEach; ++k) {
+                    const int strip = at % kHalves * kEach + k, u = (2 * base + entry) * X::kUnits + strip, slot = u % X::kRaws;
+                    const int token = (x.lo + i) * X::kTile + 16 * strip;
+                    const char* raw = smem + X::kRaw + slot * X::kHalf;
+                    // (first that the slot's entry before is done with: a maker skips slots' phases, and one that had fallen two
+                    // behind would look like the one it waits for.  The one before that is over: copies are issued in order,
+                    // and this warp has had a later one)
+                    ok = wait_alone(&c.raw_freed[slot], (u / X::kRaws + 1) & 1, c.dead, limit) && ok;
+                    ok = wait_alone(&c.raw_full[slot], (u / X::kRaws) & 1, c.dead, limit) && ok;
+                    __syncwarp();
+                    if (v) found = make_rows<X, true>(raw, to, 16 * strip, p.o.c, x.s.n_k - token, x.s.ctx - token) || found;
+                    else make_rows<X, false>(raw, to, 16 * strip, p.o.c, x.s.n_k - token, 0);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&c.raw_freed[slot]);
+                }
+                if (found) *(volatile int*)&c.special[number & 15] = number;
                 tc::fence_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(full);
-                    mbar_arrive(&c.raw_freed[slot]);
-                }
+                if (lane == 0 && ok) mbar_arrive(v ? &c.v_full[stage] : &c.k_full[stage]);
             }
+            if (*(volatile int*)&c.dead) break;
+            at -= 2 * n * kHalves;
+            base += n;
         }
     }
     tc::fence_before_sync();
