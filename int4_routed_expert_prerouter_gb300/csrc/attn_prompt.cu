@@ -183,24 +183,36 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_prompt_kernel(const __grid_
                 if (!wait_phase(&c.full[stage], (at / R::kStages) & 1, c.dead, p.o.wait_ns)) continue;
                 const Item& x = feed.x;
                 if (feed.value && x.lo + feed.tile >= x.clear) {
-                    char* entry = ring + stage * X::kEntryBytes;
+                    uint4* entry = reinterpret_cast<uint4*>(ring + stage * X::kEntryBytes) + (wid - 10) * 32 + lane;
+                    constexpr int kPieces = X::kEntryBytes / 16 / 64;
                     const int left = x.s.n_k - feed.token();
-                    bool found = false;
-#pragma unroll 4
-                    for (int k = (wid - 10) * 32 + lane; k < X::kEntryBytes / 16; k += 64) {
-                        uint4* piece = reinterpret_cast<uint4*>(entry) + k;
-                        const uint4 w = *piece;
-                        const uint32_t bx = __vcmpeq2(w.x & 0x7C007C00u, 0x7C007C00u), by = __vcmpeq2(w.y & 0x7C007C00u, 0x7C007C00u),
-                                       bz = __vcmpeq2(w.z & 0x7C007C00u, 0x7C007C00u), bw = __vcmpeq2(w.w & 0x7C007C00u, 0x7C007C00u);
-                        if (((k >> 3) & (X::kEntry - 1)) >= left) {
-                            *piece = make_uint4(0, 0, 0, 0);
-                        } else if ((bx | by | bz | bw) != 0) {
-                            *piece = make_uint4(w.x & ~bx, w.y & ~by, w.z & ~bz, w.w & ~bw);
-                            found = true;
-                        }
+                    // the largest magnitude; a NaN stays
+                    __half2 most = __halves2half2(__ushort_as_half(0), __ushort_as_half(0));
+#pragma unroll 8
+                    for (int k = 0; k < kPieces; ++k) {
+                        const uint4 w = entry[k * 64];
+                        const __half2* h = reinterpret_cast<const __half2*>(&w);
+                        const __half2 m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
+                        most = __hmax2_nan(most, m);
                     }
-                    if (found) special_of(c, feed.number) = feed.number;
-                    tc::fence_async_smem();
+                    const bool bad = !(__hlt(__low2half(most), __ushort_as_half(0x7C00)) && __hlt(__high2half(most), __ushort_as_half(0x7C00)));
+                    if (left < X::kEntry || __any_sync(0xffffffffu, bad)) {
+                        bool found = false;
+#pragma unroll 1
+                        for (int k = 0; k < kPieces; ++k) {
+                            const uint4 w = entry[k * 64];
+                            const uint32_t bx = __vcmpeq2(w.x & 0x7C007C00u, 0x7C007C00u), by = __vcmpeq2(w.y & 0x7C007C00u, 0x7C007C00u),
+                                           bz = __vcmpeq2(w.z & 0x7C007C00u, 0x7C007C00u), bw = __vcmpeq2(w.w & 0x7C007C00u, 0x7C007C00u);
+                            if (((((wid - 10) * 32 + lane + k * 64) >> 3) & (X::kEntry - 1)) >= left) {
+                                entry[k * 64] = make_uint4(0, 0, 0, 0);
+                            } else if ((bx | by | bz | bw) != 0) {
+                                entry[k * 64] = make_uint4(w.x & ~bx, w.y & ~by, w.z & ~bz, w.w & ~bw);
+                                found = true;
+                            }
+                        }
+                        if (found) special_of(c, feed.number) = feed.number;
+                        tc::fence_async_smem();
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) {
@@ -289,7 +301,7 @@ int launch(const PromptP& base, const uint16_t* k, long long ldk, char* ws, cuda
     const int grid = joins || blocks > sms ? sms : (int)blocks;
     rc = launch_early(attn_prompt_kernel<D>, dim3(grid), kThreadsF, R::kSmem, stream, p, mq, mk, mv, joins);
     if (rc || !joins || grid < 2) return rc;
-    return launch_early(flash_join<Shape<D>, Prompt<D>>, dim3(grid - 1, Shape<D>::kBlock / 32), 128, 0, stream, p);
+    return launch_early(flash_join<Shape<D>, Prompt<D>>, dim3(grid - 1, Shape<D>::kBlock / 32), 32 * kJoinWarps, 0, stream, p);
 }
 
 }  // namespace

@@ -936,7 +936,7 @@ int launch(const TreeP& base, char* ws, cudaStream_t stream) {
     const int grid = joins || blocks > sms ? sms : (int)blocks;
     const int rc = launch_early(attn_tree_kernel<X>, dim3(grid), kThreadsT, X::kSmem, stream, p, joins);
     if (rc || !joins || grid < 2) return rc;
-    return launch_early(flash_join<X, Tree<X>>, dim3(grid - 1, X::kBlock / 32), 128, 0, stream, p);
+    return launch_early(flash_join<X, Tree<X>>, dim3(grid - 1, X::kBlock / 32), 32 * kJoinWarps, 0, stream, p);
 }
 
 }  // namespace

@@ -113,13 +113,18 @@ struct Costs {
         return v < 0 ? 0 : v < all ? v : all;
     }
     __device__ long long before(int t) const {        // cost of the blocks 0 .. t - 1, t < blocks
-        long long from = off >= 0 ? 0 : -off / R;     // the first block with off + R (t + 1) > 0
+        long long from = off >= 0 ? 0 : -off / R;     // (R: a power of two) the first block with off + R (t + 1) > 0
         if (from > t) from = t;
         const long long n = t - from;
         return t * per + n * off + R * ((long long)t * (t + 1) - from * (from + 1)) / 2;
     }
     __device__ long long total() const { return blocks ? before(blocks - 1) + per + all : 0; }
 };
+
+// a / b, both not negative; 64-bit divisions take a microsecond together where 32 bits do
+__device__ __forceinline__ long long divide(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
 
 // The places of the cuts `first` and first + 1 of the CTAs' shares, by the whole CTA of at least 256 threads;
 // prefix: [EDGE0_MAX_BATCHED + 1] of scratch.
@@ -147,7 +152,7 @@ __device__ void find_share(const Src& p, int cta, int ctas, long long* prefix, P
     __syncthreads();
     if (tid == 0 || tid == 32) {
         const long long all = prefix[p.B], least = (long long)Sh::kMinShare * Sh::kTile * p.G;
-        long long share = (all + ctas - 1) / ctas;
+        long long share = divide(all + ctas - 1, ctas);
         if (share < least) share = least;             // (so that two cuts never fall on one tile of a block)
         const int i = cta + (tid == 32);
         const long long x = share * i;
@@ -163,7 +168,7 @@ __device__ void find_share(const Src& p, int cta, int ctas, long long* prefix, P
             const long long head = c.total();
             long long in = x - prefix[lo];
             at.b = lo;
-            at.h = (int)(in / head);
+            at.h = (int)divide(in, head);
             in -= at.h * head;
             int t0 = 0, t1 = c.blocks;
             while (t1 - t0 > 1) {
@@ -174,9 +179,9 @@ __device__ void find_share(const Src& p, int cta, int ctas, long long* prefix, P
             at.t = t0;
             in -= c.before(t0);
             const long long seen = c.tokens(t0), cost = seen + c.per;
-            const int tiles = (int)((seen + c.per - 1) / c.per);
-            int tile = (int)((in - c.per / 2) / c.per);             // the nearest, less the block's own cost
-            if (in < c.per) tile = 0;
+            const int tiles = (int)divide(seen + c.per - 1, c.per);
+            // the nearest, less the block's own cost
+            int tile = in < c.per ? 0 : (int)divide(in - c.per / 2, c.per);
             if (tiles < Sh::kMinSplit || cost * 8 <= share) tile = 2 * in > cost ? tiles : 0;
             if (tile >= tiles && tile > 0) {          // the next block's start
                 tile = 0;
@@ -638,6 +643,12 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
         const bool writes = live && (s == 0 || pair);
         float* swap = reinterpret_cast<float*>(stage_smem + kStageBytes);               // [32][kRowsQ], the second stream's
         char* stage = stage_smem + s * kStageBytes + 4096 * quad;                       // the warp's [32 rows][64 dims], swizzled
+        // rows that the lane writes 8 dims of at a time: eight lanes a row (a row per lane would take a line per lane and access)
+        __half* row_out[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            row_out[i] = reinterpret_cast<__half*>(
+                __shfl_sync(0xffffffffu, writes && whole ? (unsigned long long)out : 0ull, 4 * i + (lane >> 3)));
 #pragma unroll 1
         for (int k = 0; k < D; k += 32) {
             if (merge) {
@@ -672,21 +683,23 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
                 }
                 if (whole) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        *reinterpret_cast<uint4*>(stage + swizzled(lane, ((k & 32) + i) >> 3)) =
-                            make_uint4(pack2(o[i] * inv, o[i + 1] * inv), pack2(o[i + 2] * inv, o[i + 3] * inv),
-                                       pack2(o[i + 4] * inv, o[i + 5] * inv), pack2(o[i + 6] * inv, o[i + 7] * inv));
-                    if (k & 32) {
-                        // 64 dims of the warp's rows are there: eight lanes a row (a row per lane would take a line per lane and
-                        // access; 64 ragged prompts of up to 1,024 tokens then took 5,000 cycles a block for this)
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float u, v;
+                            unpk(mul2(pk(o[i + 2 * e], o[i + 2 * e + 1]), pk(inv, inv)), u, v);
+                            w[e] = pack2(u, v);
+                        }
+                        *reinterpret_cast<uint4*>(stage + swizzled(lane, ((k & 32) + i) >> 3)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (k & 32) {                       // 64 dims of the warp's rows are there
                         __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = 4 * i + (lane >> 3);
-                            const unsigned long long at = __shfl_sync(0xffffffffu, writes ? (unsigned long long)out : 0ull, r);
-                            const uint4 v = *reinterpret_cast<const uint4*>(stage + swizzled(r, lane & 7));
-                            if (at) *reinterpret_cast<uint4*>(reinterpret_cast<__half*>(at) + (k & ~32) + 8 * (lane & 7)) = v;
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            if (row_out[i])
+                                *reinterpret_cast<uint4*>(row_out[i] + (k & ~32) + 8 * (lane & 7)) =
+                                    *reinterpret_cast<const uint4*>(stage + swizzled(4 * i + (lane >> 3), lane & 7));
                         __syncwarp();
                     }
                 } else if (writes) {
@@ -725,41 +738,58 @@ __device__ __forceinline__ void control_init(Control& c, int full_count, int cle
 }
 
 // ------------------------------------------------------------------- join ----
-// A CTA of four warps: 32 rows of the block that the cut in front of share blockIdx.x + 1 is the first to fall into.
+// A CTA of 16 warps: 32 rows of the block that the cut in front of share blockIdx.x + 1 is the first to fall into, a warp
+// each, a few parts under way at a time (it is the latency of reads that wait for one another that counts).
+constexpr int kJoinWarps = 16;
 template <class Sh, class Src>
-__global__ void __launch_bounds__(128) flash_join(const Src p) {
-    constexpr int D = Sh::kD, kN = D / 32, R = Sh::kBlock;
+__global__ void __launch_bounds__(32 * kJoinWarps) flash_join(const Src p) {
+    constexpr int D = Sh::kD, kN = D / 32, R = Sh::kBlock, kBatch = D == 256 ? 4 : 8;
     wait_predecessor();
     launch_dependents();
     const int i = blockIdx.x + 1, ctas = gridDim.x + 1, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const Place at = p.o.places[i];
-    if (at.tile == 0) return;
-    const Place before = p.o.places[i - 1];
-    if (before.tile > 0 && same_block(before, at)) return;
+    const Place before = p.o.places[i - 1], at = p.o.places[i];
+    if (at.tile == 0 || (before.tile > 0 && same_block(before, at))) return;
     int last = i;                                   // the last share that begins in the block
-    while (last + 1 < ctas) {
-        const Place z = p.o.places[last + 1];
-        if (z.tile == 0 || !same_block(z, at)) break;
-        ++last;
+    for (int from = i + 1; from < ctas; from += 32) {
+        bool in = false;
+        if (from + lane < ctas) {
+            const Place z = p.o.places[from + lane];
+            in = z.tile > 0 && same_block(z, at);
+        }
+        const unsigned ins = __ballot_sync(0xffffffffu, in);
+        last += ins == 0xffffffffu ? 32 : __ffs(~ins) - 1;
+        if (ins != 0xffffffffu) break;
     }
     const Seq s = p.seq(at.b);
-    const int row0 = at.t * R, rows = min(R, s.n_q * p.G - row0);
-    for (int local = blockIdx.y * 32 + wid; local < min(rows, blockIdx.y * 32 + 32); local += 4) {
+    const int row0 = at.t * R, rows = min(R, s.n_q * p.G - row0), parts = last - i + 2;
+    for (int local = blockIdx.y * 32 + wid; local < min(rows, blockIdx.y * 32 + 32); local += kJoinWarps) {
+        auto slot = [&](int k) { return (long long)(2 * (i - 1 + k) + (k == 0 ? 1 : 0)) * R + local; };
         float top = -INFINITY;
-        auto slot = [&](int cta) { return (long long)(2 * cta + (cta == i - 1 ? 1 : 0)) * R + local; };
-        for (int k = i - 1 + lane; k <= last; k += 32) top = fmaxf(top, p.o.part_ml[slot(k)].x);
+        for (int k = lane; k < parts; k += 32) top = fmaxf(top, p.o.part_ml[slot(k)].x);
 #pragma unroll
         for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
         float v[kN], l = 0.f;
 #pragma unroll
         for (int e = 0; e < kN; ++e) v[e] = 0.f;
-        for (int k = i - 1; k <= last; ++k) {
-            const float2 ml = p.o.part_ml[slot(k)];
-            const float* o = p.o.part_o + slot(k) * D;
-            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-            l += ml.y != ml.y ? ml.y : ml.y * f;
+        for (int k0 = 0; k0 < parts; k0 += kBatch) {
+            float part[kBatch][kN];
+            float2 ml[kBatch];
 #pragma unroll
-            for (int e = 0; e < kN; ++e) v[e] = fmaf(o[e * 32 + lane], f, v[e]);
+            for (int u = 0; u < kBatch; ++u) {
+                if (k0 + u >= parts) break;
+                ml[u] = p.o.part_ml[slot(k0 + u)];
+                const float* o = p.o.part_o + slot(k0 + u) * D;
+#pragma unroll
+                for (int e = 0; e < kN; ++e) part[u][e] = o[e * 32 + lane];
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (k0 + u >= parts) break;
+                const float f = ml[u].x == -INFINITY ? 0.f : ex2(ml[u].x - top);
+                l += ml[u].y != ml[u].y ? ml[u].y : ml[u].y * f;
+#pragma unroll
+                for (int e = 0; e < kN; ++e) v[e] = fmaf(part[u][e], f, v[e]);
+            }
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int r = row0 + local, token = r / p.G, head = at.h * p.G + r - token * p.G;
