@@ -190,29 +190,25 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_prompt_kernel(const __grid_
                     __half2 most = __halves2half2(__ushort_as_half(0), __ushort_as_half(0));
 #pragma unroll 8
                     for (int k = 0; k < kPieces; ++k) {
-                        const uint4 w = entry[k * 64];
+                        uint4 w = entry[k * 64];
+                        if (((((wid - 10) * 32 + lane + k * 64) >> 3) & (X::kEntry - 1)) >= left)      // behind the last key
+                            entry[k * 64] = w = make_uint4(0, 0, 0, 0);
                         const __half2* h = reinterpret_cast<const __half2*>(&w);
                         const __half2 m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
                         most = __hmax2_nan(most, m);
                     }
                     const bool bad = !(__hlt(__low2half(most), __ushort_as_half(0x7C00)) && __hlt(__high2half(most), __ushort_as_half(0x7C00)));
-                    if (left < X::kEntry || __any_sync(0xffffffffu, bad)) {
-                        bool found = false;
+                    if (__any_sync(0xffffffffu, bad)) {
+                        if (bad) special_of(c, feed.number) = feed.number;
 #pragma unroll 1
                         for (int k = 0; k < kPieces; ++k) {
                             const uint4 w = entry[k * 64];
                             const uint32_t bx = __vcmpeq2(w.x & 0x7C007C00u, 0x7C007C00u), by = __vcmpeq2(w.y & 0x7C007C00u, 0x7C007C00u),
                                            bz = __vcmpeq2(w.z & 0x7C007C00u, 0x7C007C00u), bw = __vcmpeq2(w.w & 0x7C007C00u, 0x7C007C00u);
-                            if (((((wid - 10) * 32 + lane + k * 64) >> 3) & (X::kEntry - 1)) >= left) {
-                                entry[k * 64] = make_uint4(0, 0, 0, 0);
-                            } else if ((bx | by | bz | bw) != 0) {
-                                entry[k * 64] = make_uint4(w.x & ~bx, w.y & ~by, w.z & ~bz, w.w & ~bw);
-                                found = true;
-                            }
+                            if ((bx | by | bz | bw) != 0) entry[k * 64] = make_uint4(w.x & ~bx, w.y & ~by, w.z & ~bz, w.w & ~bw);
                         }
-                        if (found) special_of(c, feed.number) = feed.number;
-                        tc::fence_async_smem();
                     }
+                    tc::fence_async_smem();
                 }
                 __syncwarp();
                 if (lane == 0) {
