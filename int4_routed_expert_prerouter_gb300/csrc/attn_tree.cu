@@ -315,19 +315,6 @@ __device__ __forceinline__ bool make_rows(const char* raw, char* stage, int row0
 }
 
 // ------------------------------------------------- the softmax warps ----
-// Waits for a phase of a barrier, each thread by itself
-__device__ __forceinline__ bool wait_alone(uint64_t* bar, uint32_t parity, int& dead, unsigned long long limit) {
-    if (mbar_try_wait(bar, parity)) return true;
-    unsigned long long t0, now;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-    for (;;) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*(volatile int*)&dead) return false;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-        if (now - t0 > limit) *(volatile int*)&dead = 1;
-    }
-}
-
 template <class X>
 __device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, char* smem) {
     constexpr int D = X::kD, GR = X::GR, T = X::kTile, NB = T / 16;             // 8-token blocks of half a tile

@@ -350,27 +350,52 @@ struct Control {
     float2 ml[kRowsQ];              // the second stream's (reference, sum)
 };
 
-// Where a block of the share (numbers from 1, of those with tiles) is marked: whoever looks V through runs no more than the
-// ring's entries ahead.
-__device__ __forceinline__ volatile int& special_of(Control& c, int number) {
-    return *(volatile int*)&c.special[number & (kMaxStages * 2 - 1)];
+// One look at a phase.  What it orders is this CTA's alone: the scope of a cluster invalidates L1 with every look (one long
+// prompt 1,495 -> 1,418 us, drafts of 64 sequences 211 -> 200).  Looks that do not suspend cost more (1,535 and 207), and
+// so do those that name the time to suspend for (1,493 and 218) and sixteen looks in a row between two readings of the clock
+// (1,417 and 223).
+__device__ __forceinline__ bool look(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
-// Waits for a phase of a barrier, by a whole warp, which agrees on the answer; gives up after `limit` ns
-// or when another warp did.
+// Waits for a phase of a barrier, each thread by itself; gives up after `limit` ns or when another warp did
+__device__ __forceinline__ bool wait_alone(uint64_t* bar, uint32_t parity, int& dead, unsigned long long limit) {
+    if (look(bar, parity)) return true;
+    unsigned long long t0, now;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    for (;;) {
+        if (look(bar, parity)) return true;
+        if (*(volatile int*)&dead) return false;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        if (now - t0 > limit) *(volatile int*)&dead = 1;
+    }
+}
+// ... by a whole warp, which agrees on the answer
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int& dead, unsigned long long limit) {
-    bool ok = !*(volatile int*)&dead && mbar_try_wait(bar, parity);
+    bool ok = !*(volatile int*)&dead && look(bar, parity);
     if (!__all_sync(0xffffffffu, ok)) {
         unsigned long long t0, now;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
         while (!ok) {
             if (*(volatile int*)&dead) break;
-            ok = mbar_try_wait(bar, parity);
+            ok = look(bar, parity);
             asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
             if (!ok && now - t0 > limit) *(volatile int*)&dead = 1;
         }
         ok = __all_sync(0xffffffffu, ok);
     }
     return ok;
+}
+
+// Where a block of the share (numbers from 1, of those with tiles) is marked: whoever looks V through runs no more than the
+// ring's entries ahead.
+__device__ __forceinline__ volatile int& special_of(Control& c, int number) {
+    return *(volatile int*)&c.special[number & (kMaxStages * 2 - 1)];
 }
 
 // Place of a tile's first entry in the ring, counted from the block's first: K tiles run `lead` ahead of V's.
