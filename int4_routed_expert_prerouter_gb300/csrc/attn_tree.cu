@@ -37,7 +37,8 @@ constexpr float kUpV = 1024.f;           // weights are that many times as large
 template <int BITS_, int D>
 struct Tile {
     // what the shares go by
-    static constexpr int kD = D, kBlock = kRowsQ, kTile = D == 256 ? 32 : 64, kEntries = 1, kEntry = kTile, kMinSplit = 8, kMinShare = 4;
+    static constexpr int kD = D, kBlock = kRowsQ, kTile = D == 256 ? 32 : 64, kEntries = 1, kEntry = kTile, kMinSplit = 8, kMinWhole = 8,
+                         kMinShare = 4, kOwn = 4;
     static constexpr int kBufs = D == 256 ? 1 : 2;                   // of scores
     __host__ __device__ static constexpr int lead(int) { return kBufs; }
 

@@ -43,7 +43,7 @@ constexpr int kSoftmax = 256;         // threads of the two softmax warpgroups
 // share has at least (a cut costs a start, parts of fp32 and their join).
 template <int D>
 struct Shape {
-    static constexpr int kD = D, kTile = flash::kTile, kMinSplit = 8, kMinShare = 4;
+    static constexpr int kD = D, kTile = flash::kTile, kMinSplit = 8, kMinWhole = 32, kMinShare = 4, kOwn = 4;
     static constexpr int kStreams = D <= 128 ? 2 : 1;
     static constexpr int kBlock = kStreams * kRowsQ;          // rows of a block
     static constexpr int kEntry = D == 256 ? 64 : kTile;      // tokens of a ring entry
@@ -97,12 +97,13 @@ struct Item {
 template <class Sh>
 struct Costs {
     static constexpr int R = Sh::kBlock;
-    long long per;        // cost of a tile: kTile G
+    long long per, own;   // cost of a tile: kTile G; of a block beside its tiles
     long long off, all;   // off G, n_k G
     int blocks;
 
     __device__ Costs(const Seq& s, int G) {
         per = (long long)Sh::kTile * G;
+        own = Sh::kOwn * per;
         off = (long long)s.off * G;
         all = (long long)s.n_k * G;
         blocks = (int)(((long long)s.n_q * G + R - 1) / R);
@@ -116,9 +117,9 @@ struct Costs {
         long long from = off >= 0 ? 0 : -off / R;     // (R: a power of two) the first block with off + R (t + 1) > 0
         if (from > t) from = t;
         const long long n = t - from;
-        return t * per + n * off + R * ((long long)t * (t + 1) - from * (from + 1)) / 2;
+        return t * own + n * off + R * ((long long)t * (t + 1) - from * (from + 1)) / 2;
     }
-    __device__ long long total() const { return blocks ? before(blocks - 1) + per + all : 0; }
+    __device__ long long total() const { return blocks ? before(blocks - 1) + own + all : 0; }
 };
 
 // a / b, both not negative; 64-bit divisions take a microsecond together where 32 bits do
@@ -178,11 +179,11 @@ __device__ void find_share(const Src& p, int cta, int ctas, long long* prefix, P
             }
             at.t = t0;
             in -= c.before(t0);
-            const long long seen = c.tokens(t0), cost = seen + c.per;
+            const long long seen = c.tokens(t0), cost = seen + c.own;
             const int tiles = (int)divide(seen + c.per - 1, c.per);
             // the nearest, less the block's own cost
-            int tile = in < c.per ? 0 : (int)divide(in - c.per / 2, c.per);
-            if (tiles < Sh::kMinSplit || cost * 8 <= share) tile = 2 * in > cost ? tiles : 0;
+            int tile = in < c.own ? 0 : (int)divide(in - c.own + c.per / 2, c.per);
+            if (tiles < (cost >= 2 * share ? Sh::kMinSplit : Sh::kMinWhole) || cost * 8 <= share) tile = 2 * in > cost ? tiles : 0;
             if (tile >= tiles && tile > 0) {          // the next block's start
                 tile = 0;
                 if (++at.t == c.blocks) {
