@@ -315,6 +315,14 @@ __device__ __forceinline__ bool make_rows(const char* raw, char* stage, int row0
     return found;
 }
 
+// A block's entries: K of its tiles, X::kBufs of them ahead of V's, then V's that are left.
+template <class X>
+__device__ __forceinline__ int tile_of_entry(int entry, int n, bool& v) {
+    const int lead = min(X::kBufs, n), r = entry - lead, turns = 2 * (n - lead);
+    v = r >= 0 && (r >= turns || !(r & 1));
+    return r < 0 ? entry : r < turns ? (r >> 1) + (v ? 0 : lead) : r - (n - lead);
+}
+
 // ------------------------------------------------- the softmax warps ----
 template <class X>
 __device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, char* smem) {
@@ -791,26 +799,35 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     } else if (wid == 8) {
         tree_matrix<X>(p, c, smem);
     } else if (wid == 9) {
-        // a lane: one of a tile's strips; behind the last token, that token's.  Pages' numbers are asked for kAhead tiles ahead.
-        constexpr int kAhead = 4;
-        Feed<X, Tree<X>> feed(p, c.cut, blockIdx.x);
-        int unit = 0, id[kAhead];
-        long long in_page[kAhead];
-        bool ok = limit != 0, more = true;
-        auto ask = [&](int& id, long long& in_page) {
-            more = more && feed.next();
+        // a round: the ring's next two entries, a strip of one of them a lane; behind the last token, that token's.  Pages'
+        // numbers are asked for kAhead rounds ahead.  (One entry a round: this warp held up all others, 185 us for drafts
+        // of 64 sequences.)
+        constexpr int kAhead = 2, kLanes = 2 * X::kUnits;
+        const int place = lane % kLanes, strip = place % X::kUnits, strips = p.c.page_tokens / kv::kStrip;
+        Walk<X, Tree<X>> walk(p, c.cut, blockIdx.x);
+        Item x;
+        int n = 0, round = 0, unit = 0, slot = place, id[kAhead], at[kAhead];
+        uint32_t parity = 0;
+        bool ok = limit != 0, more = true, of_v[kAhead];
+        // asks for the page of the next round's strip; false: none is left
+        auto ask = [&](int& id, int& at, bool& of_v) {
+            if (more && ++round >= n) {
+                do more = walk.next(x);
+                while (more && x.hi == x.lo);
+                n = x.hi - x.lo;
+                round = 0;
+            }
             id = -1;
             if (!more) return;
-            const int token = min(feed.token() + 16 * (lane % X::kUnits), feed.x.s.n_k - 1);
-            const int pg = token / p.c.page_tokens, in = token - pg * p.c.page_tokens;
-            id = p.table[(long long)feed.x.b * p.W + pg];
-            in_page = ((long long)feed.x.h * (p.c.page_tokens / kv::kStrip) + in / kv::kStrip) * kv::strip_bytes(X::BITS, X::kD) +
-                      (feed.value ? X::kHalf : 0);
+            const int i = tile_of_entry<X>(2 * round + place / X::kUnits, n, of_v);
+            const int from = min((x.lo + i) * X::kTile / kv::kStrip + strip, (x.s.n_k - 1) / kv::kStrip), pg = from / strips;
+            id = p.table[(long long)x.b * p.W + pg];
+            at = x.h * strips + from - pg * strips;
         };
         int asked = 0, had = 0;
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
-            ask(id[q], in_page[q]);
+            ask(id[q], at[q], of_v[q]);
             asked += more;
         }
         while (ok && had < asked) {
@@ -818,19 +835,18 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
             for (int q = 0; q < kAhead; ++q) {
                 if (!ok || had >= asked) break;
                 ++had;
-                const int u = unit + lane % X::kUnits, slot = u % X::kRaws;
                 int page = id[q];
                 if (page < 0 || page >= p.c.n_pages) {
                     page = 0;
                     if (p.status) atomicExch(p.status, EDGE0_EINVAL);
                 }
-                const char* from = p.c.pages + page * p.c.page_bytes + in_page[q];
-                ask(id[q], in_page[q]);
+                const char* from = p.c.pages + page * p.c.page_bytes + (long long)at[q] * kv::strip_bytes(X::BITS, X::kD) + (of_v[q] ? X::kHalf : 0);
+                ask(id[q], at[q], of_v[q]);
                 asked += more;
                 // (the phase before a barrier's first counts as over)
-                ok = __all_sync(0xffffffffu, wait_alone(&c.raw_freed[slot], (u / X::kRaws + 1) & 1, c.dead, limit));
+                ok = __all_sync(0xffffffffu, wait_alone(&c.raw_freed[slot], parity ^ 1, c.dead, limit));
                 if (!ok) break;
-                if (lane < X::kUnits) {
+                if (lane < kLanes) {
                     mbar_arrive_expect_tx(&c.raw_full[slot], X::kHalf);
                     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
                                      smem_u32(smem + X::kRaw + slot * X::kHalf)),
@@ -838,7 +854,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
                                  : "memory");
                 }
                 __syncwarp();
-                unit += X::kUnits;
+                unit += kLanes;
+                if ((slot += kLanes) >= X::kRaws) {
+                    slot -= X::kRaws;
+                    parity ^= 1;
+                }
             }
         }
         // nothing may land in this memory when it has become another CTA's
@@ -850,13 +870,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         Item x;
         int base = 0, number = 0, at = wid - 10;                     // tiles before the block; the next half, from the block's first on
         while (walk.next(x)) {
-            const int n = x.hi - x.lo, lead = min(X::kBufs, n);
+            const int n = x.hi - x.lo;
             if (n > 0) ++number;
             for (; at < 2 * n * kHalves; at += kMakers) {
-                // K tiles run `lead` ahead of V's, then V's alone are left
-                const int entry = at / kHalves, r = entry - lead, turns = 2 * (n - lead);
-                const bool v = r >= 0 && (r >= turns || !(r & 1));
-                const int i = r < 0 ? entry : r < turns ? (r >> 1) + (v ? 0 : lead) : r - (n - lead);
+                bool v;
+                const int entry = at / kHalves, i = tile_of_entry<X>(entry, n, v);
                 const int tile = base + i, stage = tile % X::kStages;
                 const uint32_t parity = (tile / X::kStages) & 1;
                 char* to = v ? smem + X::kV + stage * X::kVStage : smem + X::kK + stage * X::kKStage;
