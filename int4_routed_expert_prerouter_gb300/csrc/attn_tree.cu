@@ -68,7 +68,7 @@ struct TreeControl {
     uint64_t k_full[4], k_freed[4], v_full[4], v_freed[4];           // stages
     uint64_t raw_full[kMaxRaw], raw_freed[kMaxRaw];
     uint64_t q_full, s_full[2], p_full[2], o_step[2], o_last, drained;      // (pairs: of even and of odd steps)
-    uint64_t ref_full[2][4];                                         // references of a quarter's halves after a step
+    uint64_t ref_full[4];                                            // a quarter's references after a step
     Place cut[2];
     uint32_t tmem;
     int dead;
@@ -334,7 +334,10 @@ __device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, c
     auto local_of = [&](int r) { return 64 * (r >> 1) + 16 * quad + g + 8 * (r & 1); };
     Walk<X, Tree<X>> walk(p, c.cut, blockIdx.x);
     Item x;
-    int base = 0, blocks = 0, number = 0;
+    int base = 0, blocks = 0, number = 0, links = 0;                 // (links: steps that passed references on)
+    // No wait of the warp's has given up so far.  From the first on it does not arrive any more where an arrival counts
+    // twice: phases stand still then, and it could be more than the one under way lacks, which is a fault.
+    bool alive = true;
     while (walk.next(x)) {
         const int n = x.hi - x.lo;
         const bool both = x.rows > 64;                               // else no row lies in the second half
@@ -390,14 +393,12 @@ __device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, c
             __syncwarp();
             if (lane == 0) mbar_arrive(&c.q_full);
         }
-        // of each row: the reference that the warp has its sum at (exponent units; -infinity while the row has seen nothing,
-        // and then 0 in its place), and the sum of its steps
-        float refs[2][2], sums[2][2];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            refs[r >> 1][r & 1] = -INFINITY;
-            sums[r >> 1][r & 1] = 0.f;
-        }
+        // of each of its two rows: the reference that the warp has its sum at (exponent units; -infinity while the row has seen
+        // nothing, and then 0 in its place), and the sum of its steps
+        float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        // Up to 64 rows the sets take the steps in turn, and a warp's arrival counts twice where both sets' are counted; else a
+        // set has half the rows.
+        const int rh = both ? set : 0, arrivals = both ? 1 : 2;
         auto off = [](float ref) { return ref == -INFINITY ? 0.f : -ref; };
         // takes a sum to the reference that the row has by now
         auto take = [](float& ref, float& l, float now) {
@@ -406,7 +407,7 @@ __device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, c
                 ref = now;
             }
         };
-        for (int j = (base + set) & 1; j < n; j += 2) {
+        for (int j = both ? 0 : (base + set) & 1; j < n; j += both ? 1 : 2) {
             const int tile = base + j, stage = tile % X::kStages, buf = tile % X::kBufs, tile_at = x.lo + j;
             const uint32_t parity = (tile / X::kStages) & 1;
             const float* mk = reinterpret_cast<const float*>(smem + X::kK + stage * X::kKStage + X::kKTab) + t * 2 * GR;
@@ -416,187 +417,177 @@ __device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, c
             ok = wait_alone(&c.s_full[tile & 1], (tile >> 1) & 1, c.dead, limit) && ok;
             __syncwarp();
             tc::fence_after_sync();
-            if (!both && lane == 0) mbar_arrive(&c.ref_full[1][quad]);           // (its phases go with the steps)
-#pragma unroll 1
-            for (int rh = 0; rh < (both ? 2 : 1); ++rh) {
-                const uint32_t s_at = tm + ((uint32_t)(16 * rh) << 16) + buf * X::kScores;
-                float ref[2], l[2];
+            const uint32_t s_at = tm + ((uint32_t)(16 * rh) << 16) + buf * X::kScores;
+            f2 S[2 * NB][2];                                     // [8 tokens][k]: tokens 2t, 2t + 1; less the reference
+            {
+                uint32_t raw[GR][2][4 * NB];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    ref[k] = rh ? refs[1][k] : refs[0][k];
-                    l[k] = rh ? sums[1][k] : sums[0][k];
-                }
-                f2 S[2 * NB][2];                                     // [8 tokens][k]: tokens 2t, 2t + 1; less the reference
-                {
-                    uint32_t raw[GR][2][4 * NB];
+                for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
-                    for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) ld_frag<NB>(s_at + gr * T + h * (T / 2), raw[gr][h]);
-                    tc::tmem_wait_ld();
-                    const f2 from[2] = {pk(off(ref[0]), off(ref[0])), pk(off(ref[1]), off(ref[1]))};
-#pragma unroll
-                    for (int b = 0; b < 2 * NB; ++b)
-#pragma unroll
-                        for (int gr = 0; gr < GR; ++gr) {
-                            const f2 s2 = *reinterpret_cast<const f2*>(mk + b * 8 * GR + 2 * gr);
-                            const uint32_t* v = &raw[gr][b / NB][4 * (b % NB)];
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                S[b][k] = fma2(pk(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), s2, gr ? S[b][k] : from[k]);
-                        }
-                }
-                if (rh || !both) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&c.k_freed[stage]);
-                }
-                if (tile_at >= x.clear) {
-#pragma unroll 1
-                    for (int k = 0; k < 2; ++k) {
-                        const int local = 64 * rh + 16 * quad + g + 8 * k;
-                        uint32_t seen[2] = {0, 0};
-                        if (local < x.rows) {
-                            const int token = (x.row0 + local) / p.G;
-                            seen[0] = p.seen_word(x, token, tile_at * T) >> (2 * t);
-                            seen[1] = p.seen_word(x, token, tile_at * T + T / 2) >> (2 * t);
-                        }
-#pragma unroll
-                        for (int b = 0; b < 2 * NB; ++b) {
-                            float u, v;
-                            const uint32_t bits = seen[b / NB] >> (8 * (b % NB));
-                            unpk(k ? S[b][1] : S[b][0], u, v);
-                            const f2 to = pk(bits & 1 ? u : -INFINITY, bits & 2 ? v : -INFINITY);
-                            S[b][0] = k ? S[b][0] : to;
-                            S[b][1] = k ? to : S[b][1];
-                        }
-                    }
-                }
-                float mx[2] = {-INFINITY, -INFINITY};
+                    for (int h = 0; h < 2; ++h) ld_frag<NB>(s_at + gr * T + h * (T / 2), raw[gr][h]);
+                tc::tmem_wait_ld();
+                const f2 from[2] = {pk(off(ref[0]), off(ref[0])), pk(off(ref[1]), off(ref[1]))};
 #pragma unroll
                 for (int b = 0; b < 2 * NB; ++b)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float u, v;
-                        unpk(S[b][k], u, v);
-                        mx[k] = fmaxf(mx[k], fmaxf(u, v));
+                    for (int gr = 0; gr < GR; ++gr) {
+                        const f2 s2 = *reinterpret_cast<const f2*>(mk + b * 8 * GR + 2 * gr);
+                        const uint32_t* v = &raw[gr][b / NB][4 * (b % NB)];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            S[b][k] = fma2(pk(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), s2, gr ? S[b][k] : from[k]);
                     }
-                // the references after the step before, of the other set; a block's first step starts afresh
-                ok = wait_alone(&c.ref_full[rh][quad], (tile + 1) & 1, c.dead, limit) && ok;
-                __syncwarp();
-                float* at = c.ref + 64 * rh + 16 * quad + g;
-                float now[2], by[2];
-                bool want = false;
+            }
+            __syncwarp();
+            alive = alive && ok;
+            if (lane == 0 && alive) mbar_arrive_n(&c.k_freed[stage], arrivals);
+            if (tile_at >= x.clear) {
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) {
+                    const int local = 64 * rh + 16 * quad + g + 8 * k;
+                    uint32_t seen[2] = {0, 0};
+                    if (local < x.rows) {
+                        const int token = (x.row0 + local) / p.G;
+                        seen[0] = p.seen_word(x, token, tile_at * T) >> (2 * t);
+                        seen[1] = p.seen_word(x, token, tile_at * T + T / 2) >> (2 * t);
+                    }
+#pragma unroll
+                    for (int b = 0; b < 2 * NB; ++b) {
+                        float u, v;
+                        const uint32_t bits = seen[b / NB] >> (8 * (b % NB));
+                        unpk(k ? S[b][1] : S[b][0], u, v);
+                        const f2 to = pk(bits & 1 ? u : -INFINITY, bits & 2 ? v : -INFINITY);
+                        S[b][0] = k ? S[b][0] : to;
+                        S[b][1] = k ? to : S[b][1];
+                    }
+                }
+            }
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int b = 0; b < 2 * NB; ++b)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    now[k] = j ? at[8 * k] : -INFINITY;
-                    by[k] = off(now[k]) - off(ref[k]);               // what these scores lack
-                    mx[k] += by[k];
-                    want = want || mx[k] > (now[k] == -INFINITY ? -INFINITY : kRise);
+                    float u, v;
+                    unpk(S[b][k], u, v);
+                    mx[k] = fmaxf(mx[k], fmaxf(u, v));
                 }
-                float f[2] = {1.f, 1.f};
-                bool move = false;
-                if (__any_sync(0xffffffffu, want)) {
+            // the references after the step before: its own, or the other set's (a block's first step starts afresh)
+            if (!both) {
+                ok = wait_alone(&c.ref_full[quad], (links + j + 1) & 1, c.dead, limit) && ok;
+                __syncwarp();
+            }
+            float* at = c.ref + 16 * quad + g;
+            float now[2], by[2];
+            bool want = false;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
-                        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
-                        const bool fresh = now[k] == -INFINITY;
-                        if (mx[k] > (fresh ? -INFINITY : kRise)) {
-                            f[k] = fresh ? 0.f : ex2(-mx[k]);
-                            now[k] = mx[k] - off(now[k]);
-                            by[k] = off(now[k]) - off(ref[k]);
-                            move = true;
-                        }
+            for (int k = 0; k < 2; ++k) {
+                now[k] = both ? ref[k] : j ? at[8 * k] : -INFINITY;
+                by[k] = off(now[k]) - off(ref[k]);               // what these scores lack
+                mx[k] += by[k];
+                want = want || mx[k] > (now[k] == -INFINITY ? -INFINITY : kRise);
+            }
+            float f[2] = {1.f, 1.f};
+            bool move = false;
+            if (__any_sync(0xffffffffu, want)) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+                    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+                    const bool fresh = now[k] == -INFINITY;
+                    if (mx[k] > (fresh ? -INFINITY : kRise)) {
+                        f[k] = fresh ? 0.f : ex2(-mx[k]);
+                        now[k] = mx[k] - off(now[k]);
+                        by[k] = off(now[k]) - off(ref[k]);
+                        move = true;
                     }
                 }
+            }
+            if (!both) {
                 if ((move || j == 0) && t == 0) {
                     at[0] = now[0];
                     at[8] = now[1];
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&c.ref_full[rh][quad]);
-                if (__any_sync(0xffffffffu, by[0] != 0.f || by[1] != 0.f || now[0] != ref[0] || now[1] != ref[1])) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        take(ref[k], l[k], now[k]);
-#pragma unroll
-                        for (int b = 0; b < 2 * NB; ++b) S[b][k] = add2(S[b][k], pk(by[k], by[k]));
-                    }
-                    // (the block's first tile overwrites the accumulators)
-                    if (j > 0 && __any_sync(0xffffffffu, move)) {
-                        if (X::kBufs == 2) {    // (one buffer: the product was over before these scores were formed)
-                            ok = wait_alone(&c.o_step[(tile - 1) & 1], ((tile - 1) >> 1) & 1, c.dead, limit) && ok;
-                            __syncwarp();
-                            tc::fence_after_sync();
-                        }
-#pragma unroll 1
-                        for (int q = 0; q < GR * (X::kCols / 16); ++q) {
-                            uint32_t a[8];
-                            const uint32_t o_at = tm + ((uint32_t)(16 * rh) << 16) + X::kO + 16 * q;
-                            ld_frag<2>(o_at, a);
-                            tc::tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) a[i] = __float_as_uint(__uint_as_float(a[i]) * (i & 2 ? f[1] : f[0]));
-                            st_frag2(o_at, a);
-                        }
-                    }
-                }
+                if (lane == 0) mbar_arrive(&c.ref_full[quad]);
+            }
+            if (__any_sync(0xffffffffu, by[0] != 0.f || by[1] != 0.f || now[0] != ref[0] || now[1] != ref[1])) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    f2 sum = 0;
+                    take(ref[k], l[k], now[k]);
 #pragma unroll
-                    for (int b = 0; b < 2 * NB; ++b) {
-                        float u, v;
-                        unpk(S[b][k], u, v);
-                        S[b][k] = pk(ex2(u), ex2(v));
-                        sum = b ? add2(sum, S[b][k]) : S[b][k];
-                    }
-                    float u, v;
-                    unpk(sum, u, v);
-                    l[k] += u + v;
-                    refs[0][k] = rh ? refs[0][k] : ref[k];
-                    refs[1][k] = rh ? ref[k] : refs[1][k];
-                    sums[0][k] = rh ? sums[0][k] : l[k];
-                    sums[1][k] = rh ? l[k] : sums[1][k];
+                    for (int b = 0; b < 2 * NB; ++b) S[b][k] = add2(S[b][k], pk(by[k], by[k]));
                 }
-                if (rh == 0) {
-                    ok = wait_alone(&c.v_full[stage], parity, c.dead, limit) && ok;
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t w[2 * NB];
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            const f2 m2 = *reinterpret_cast<const f2*>(mv + (h * NB + b) * 8 * GR + 2 * gr);
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                float u, v;
-                                unpk(mul2(S[h * NB + b][k], m2), u, v);
-                                w[2 * b + k] = pack2(u, v);
-                            }
-                        }
-                        st_pairs<NB>(s_at + gr * T + h * (T / 2), w);
+                // (the block's first tile overwrites the accumulators)
+                if (j > 0 && __any_sync(0xffffffffu, move)) {
+                    if (X::kBufs == 2) {    // (one buffer: the product was over before these scores were formed)
+                        ok = wait_alone(&c.o_step[(tile - 1) & 1], ((tile - 1) >> 1) & 1, c.dead, limit) && ok;
+                        __syncwarp();
+                        tc::fence_after_sync();
                     }
+#pragma unroll 1
+                    for (int q = 0; q < GR * (X::kCols / 16); ++q) {
+                        uint32_t a[8];
+                        const uint32_t o_at = tm + ((uint32_t)(16 * rh) << 16) + X::kO + 16 * q;
+                        ld_frag<2>(o_at, a);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) a[i] = __float_as_uint(__uint_as_float(a[i]) * (i & 2 ? f[1] : f[0]));
+                        st_frag2(o_at, a);
+                    }
+                }
             }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                f2 sum = 0;
+#pragma unroll
+                for (int b = 0; b < 2 * NB; ++b) {
+                    float u, v;
+                    unpk(S[b][k], u, v);
+                    S[b][k] = pk(ex2(u), ex2(v));
+                    sum = b ? add2(sum, S[b][k]) : S[b][k];
+                }
+                float u, v;
+                unpk(sum, u, v);
+                l[k] += u + v;
+            }
+            ok = wait_alone(&c.v_full[stage], parity, c.dead, limit) && ok;
+            __syncwarp();
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[2 * NB];
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const f2 m2 = *reinterpret_cast<const f2*>(mv + (h * NB + b) * 8 * GR + 2 * gr);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float u, v;
+                            unpk(mul2(S[h * NB + b][k], m2), u, v);
+                            w[2 * b + k] = pack2(u, v);
+                        }
+                    }
+                    st_pairs<NB>(s_at + gr * T + h * (T / 2), w);
+                }
             tmem_wait_st();
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&c.p_full[tile & 1]);
-        }
-        float ref[4], l[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            ref[r] = refs[r >> 1][r & 1];
-            l[r] = sums[r >> 1][r & 1];
+            alive = alive && ok;
+            if (lane == 0 && alive) mbar_arrive_n(&c.p_full[tile & 1], arrivals);
         }
         base += n;
+        float refs[4], sums[4];                                      // of the lane's rows of both halves
         uint32_t nans[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            refs[r] = -INFINITY;
+            sums[r] = 0.f;
+        }
         if (n > 0) {
-            ok = wait_alone(&c.ref_full[0][quad], (base - 1) & 1, c.dead, limit) && ok;
-            ok = wait_alone(&c.ref_full[1][quad], (base - 1) & 1, c.dead, limit) && ok;
+            if (!both) {
+                links += n;
+                ok = wait_alone(&c.ref_full[quad], (links + 1) & 1, c.dead, limit) && ok;
+            }
             ok = wait_alone(&c.o_last, blocks++ & 1, c.dead, limit) && ok;
             __syncwarp();
             tc::fence_after_sync();
@@ -605,18 +596,25 @@ __device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, c
             ok = ok && !*(volatile int*)&c.dead;
             // a row's sum at its last reference: its 4 lanes, then both sets' steps
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                if (r < 2 || both) take(ref[r], l[r], c.ref[local_of(r)]);
-                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-                if (!ok) l[r] = __int_as_float(0x7fffffff);
-                if (t == 0) c.sums[set][local_of(r)] = l[r];
+            for (int k = 0; k < 2; ++k) {
+                const int local = local_of(2 * rh + k);
+                if (!both) take(ref[k], l[k], c.ref[local]);
+                l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+                l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+                if (!ok) l[k] = __int_as_float(0x7fffffff);
+                if (t == 0) {
+                    c.sums[both ? 0 : set][local] = l[k];
+                    if (both) c.ref[local] = ref[k];
+                }
             }
             named_bar_sync(8 + quad, 64);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                l[r] += c.sums[set ^ 1][local_of(r)];
-                if (special && local_of(r) < x.rows) nans[r] = p.nan_groups(x, (x.row0 + local_of(r)) / p.G);
+                const int local = local_of(r);
+                if (r >= 2 && !both) continue;
+                refs[r] = c.ref[local];
+                sums[r] = both ? c.sums[0][local] : c.sums[0][local] + c.sums[1][local];
+                if (special && local < x.rows) nans[r] = p.nan_groups(x, (x.row0 + local) / p.G);
             }
         }
         const bool whole = x.part < 0;
@@ -629,9 +627,9 @@ __device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, c
             const int local = local_of(r), at = x.row0 + min(local, x.rows - 1), token = at / p.G, head = x.h * p.G + at - token * p.G;
             out[r] = local < x.rows && whole ? p.o.out + (long long)(x.s.q0 + token) * p.o.ldo + (long long)head * D : nullptr;
             part[r] = local < x.rows && !whole ? p.o.part_o + ((long long)x.part * X::kBlock + local) * D : nullptr;
-            by[r] = whole ? (l[r] == 0.f ? 0.f : 1.f / (l[r] * kUpV)) : 1.f / kUpV;
-            if (l[r] != l[r]) by[r] = l[r];
-            if (part[r] && set == 0 && t == 0) p.o.part_ml[(long long)x.part * X::kBlock + local] = make_float2(ref[r], l[r]);
+            by[r] = whole ? (sums[r] == 0.f ? 0.f : 1.f / (sums[r] * kUpV)) : 1.f / kUpV;
+            if (sums[r] != sums[r]) by[r] = sums[r];
+            if (part[r] && set == 0 && t == 0) p.o.part_ml[(long long)x.part * X::kBlock + local] = make_float2(refs[r], sums[r]);
         }
 #pragma unroll 1
         for (int q = set; q < D / 32; q += 2) {
@@ -759,7 +757,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     if (threadIdx.x == 0) {
         for (int i = 0; i < X::kStages; ++i) {
             mbar_init(&c.k_full[i], 2);                              // halves of the tile
-            mbar_init(&c.k_freed[i], 1 + 4);                         // the matrix steps, and the warps that read the table
+            mbar_init(&c.k_freed[i], 1 + 8);                         // the matrix steps, and the warps that read the table
             mbar_init(&c.v_full[i], 2);
             mbar_init(&c.v_freed[i], 1);
         }
@@ -769,11 +767,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c.s_full[i], 1);
-            mbar_init(&c.p_full[i], 4);
+            mbar_init(&c.p_full[i], 8);
             mbar_init(&c.o_step[i], 1);
         }
         mbar_init(&c.q_full, kSoftmax / 32);
-        for (int i = 0; i < 8; ++i) mbar_init(&c.ref_full[0][i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&c.ref_full[i], 1);
         mbar_init(&c.o_last, 1);
         mbar_init(&c.drained, 1);
         fence_mbar_init();
