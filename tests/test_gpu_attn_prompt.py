@@ -69,6 +69,32 @@ def test_rows_behind_more_keys_or_fewer(D, n, m):
     check(binding.attn_prompt(q, k, v, i32(cu), i32(ck)), q, k, v, cu, ck)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("counts", [[6000], [1, 4500, 130, 5000]])
+def test_blocks_cut_at_any_length(D, counts):
+    cu = cut(counts)
+    q, k, v = rows(cu[-1], 2, D), rows(cu[-1], 2, D), rows(cu[-1], 2, D)
+    check(binding.attn_prompt(q, k, v, i32(cu)), q, k, v, cu, cu)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_infinities_behind_a_row_in_blocks_that_are_cut(D):
+    """Keys of the last tiles that only some rows see, in a block that several shares have."""
+    n, m = 200, 7000
+    q, k, v = rows(n, 4, D), rows(m, 1, D), rows(m, 1, D)
+    for at, x in ((m - 150, float("inf")), (m - 90, float("nan")), (m - 1, float("-inf"))):
+        v[at, 0, at % D] = x
+    got = binding.attn_prompt(q, k, v, i32([0, n]), i32([0, m]))
+    seen = flash_ref.causal(n, m, DEV)
+    finite = torch.where(v.isfinite(), v, torch.zeros_like(v))
+    o, bound = flash_ref.attend(q.double(), k.double(), finite.double(), seen, D ** -0.5)
+    for at, x in ((m - 150, float("inf")), (m - 90, float("nan")), (m - 1, float("-inf"))):
+        o[seen[:, at], :, at % D] = x
+    inf = o.isinf()
+    assert torch.equal(got.double()[inf], o[inf])
+    assert flash_ref.close(got.masked_fill(inf, 0.0), o.masked_fill(inf, 0.0), bound)
+
+
 def test_without_any_key():
     q, k = rows(70, 4, 128), torch.empty(0, 2, 128, dtype=torch.float16, device=DEV)
     got = binding.attn_prompt(q, k, k, i32([0, 50, 70]), i32([0, 0, 0]))
