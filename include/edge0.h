@@ -586,9 +586,9 @@ int edge0_attn_prompt(const uint16_t* q, long long ldq, int T, int n_q_heads, co
  *   with mask NULL (mask_words 0): those up to itself, as for the next part of a prompt.
  * q, out: T rows of n_q_heads * head_dim fp16, ldq / ldo elements apart (16-byte aligned, multiples of 8); table
  * [B][W], lens [B], cu_rows: device int32.  Softmax, scale, the sharing of K/V heads, the workspace and waits
- * that run out as in edge0_attn_decode; V enters as edge0_kv_read returns it and K rounded to fp16 but for an
- * offset that a group's 64 dims share (2^-11 of what is left).  A row that sees nothing gets zeros, rows of no sequence and of one with
- * lens[b] < 0 are left as they were, and what a row does not see has no influence on it.  Tokens behind
+ * that run out as in edge0_attn_decode; K and V enter as the codes and their group's (s, b) stand for them, without a rounding of
+ * their own, and a weight times a group's scale of V is rounded to fp16 (2^-11 of it).  A row that sees nothing gets zeros, rows of no
+ * sequence and of one with lens[b] < 0 are left as they were, and what a row does not see has no influence on it.  Tokens behind
  * W * page_tokens (they are cut off), sequences of more than 32 mask_words drafted tokens and pages outside [0, n_pages)
  * (page 0 is read in their place) are recorded as EDGE0_EINVAL in *status. */
 size_t edge0_attn_tree_workspace_bytes(const edge0_kv_cache* cache);

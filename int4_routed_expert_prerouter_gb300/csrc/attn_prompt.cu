@@ -2,7 +2,7 @@
 // tokens, and row i sees the keys up to i + n_k - n_q.  The mathematics, the blocks and their shares: flash.cuh.
 //
 // Warps: 0-7 softmax, 8 the matrix steps, 9 K and V by TMA (tiles of 128 tokens, 64 of 256-wide heads, through a ring of
-// 5 entries of 32 KB, of 8 of 16 KB for 64-wide heads), 10 and 11 look the V tiles through that some
+// 4 entries of 32 KB, of 8 of 16 KB for 64-wide heads), 10 and 11 look the V tiles through that some
 // row does not see in whole: a weight of zero times an infinity or NaN would be NaN.  They put zeros
 // in place of such values and of other sequences' rows behind the last key; what the rows see of them is added
 // to the sums at the end.

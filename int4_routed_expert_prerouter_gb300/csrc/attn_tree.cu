@@ -15,11 +15,18 @@
 // over the scores they come from), the accumulators and, up to 128 dims, the queries; with those in shared
 // memory a step's products would read them from there each time.
 // Warps: 0-7 softmax, fragments of 16 rows, two a lane, so that a token's scales, read from shared memory, serve
-// two rows; two sets of four take the steps in turn, so that one's latencies lie under the other's work, and hand
-// the rows' references on from step to step; the block's rows are dealt 16 to a quarter of tensor memory, so that up
-// to 64 rows cost all warps half; loops over fragments and pieces stay rolled: with all of it unrolled a third of the
-// stalls were for instructions to arrive; 8 the matrix steps; 9 copies strips' halves (16 tokens of K or of V, one run of
+// two rows; a block's rows are dealt 16 to a quarter of tensor memory and half of it.  Of more than 64 rows each of two sets
+// of four warps has half (both halves a set, steps in turn: four contexts of 131,072 tokens 1,020 us instead of 915); up
+// to 64 the sets take the steps in turn, so that one's latencies lie under the other's work, and hand the rows' references on
+// from step to step.  Loops over pieces stay rolled: with all of it unrolled a third of the
+// stalls were for instructions to arrive.  8 the matrix steps; 9 copies strips' halves (16 tokens of K or of V, one run of
 // bytes) into a ring of raw ones; 10-15 turn those into operands and tables.
+//
+// What bounds it: neither bytes (0.6 TB/s) nor the tensor cores (20 % of their cycles) but the latencies between
+// the roles and their instructions, half of them spent on turning codes into operands: about 2,300 cycles a step of 64
+// tokens.  64 sequences of up to 4,000 tokens with up to 16 drafted ones: 157 us; four of up to 131,072 with up to 48: 915 us, 396
+// TFLOP/s; one of 777 tokens: 25.7 us.  Weights in columns of their own, so that the next scores need not wait for
+// their product, leave no room for the queries, which the steps then read from shared memory: 171 and 990 us.
 #include "flash.cuh"
 
 namespace edge0 {

@@ -19,9 +19,9 @@
 // weights lie within 2^15 and stay normal in fp16 down to 2^-25 of the largest; their rounding, 2^-11 of each,
 // is the only one beside the result's.  Statistics and sums are fp32.
 //
-// Shares.  All blocks of all sequences and heads in a row, each at the cost of the tokens it sees, are cut
-// into equal shares, one per CTA, from lengths read on the device; a cut that falls into a block
-// too small to be worth it moves to the block's edge.  Blocks cut leave parts (reference, sum, fp32 o),
+// Shares.  All blocks of all sequences and heads in a row, each at the cost of the tokens it sees and of
+// its start and end, are cut into equal shares, one per CTA, from lengths read on the device; a cut that falls
+// into a block too small to be worth it moves to the block's edge.  Blocks cut leave parts (reference, sum, fp32 o),
 // which flash_join adds up in the order of the tokens: the same bits on every run.
 #pragma once
 #include "kvcache.cuh"
@@ -39,8 +39,15 @@ constexpr float kRise = 4.f;          // how far scores may exceed the reference
 constexpr float kUp = 11.f;           // weights are 2^kUp times as large: kRise + kUp = 15
 constexpr int kSoftmax = 256;         // threads of the two softmax warpgroups
 
-// What the shares go by: a block's rows, tokens per step, head width, tiles that a block has at least to be cut and that a
-// share has at least (a cut costs a start, parts of fp32 and their join).
+// What the shares go by: a block's rows (kBlock), tokens per step (kTile), head width, and in tiles
+//   kOwn        what a block costs beside its tiles (its queries, the first scores, the last product, its outputs).  1 instead
+//               of 4: 64 prompts of up to 1,024 tokens 299 us instead of 279, drafts of 64 sequences 199 instead of 185;
+//               8: 298 and 190;
+//   kMinSplit   from which on a block may be cut (a cut costs a start and an end more, parts of fp32 and their join);
+//   kMinWhole   likewise, where a block is not as much as two shares: there it is only the shares' evenness that a cut
+//               serves.  8 instead of 32: a prompt of 2,000 tokens 64.5 us instead of 55, of 4,000 131 instead of 122; drafted
+//               tokens' blocks cost less to cut (8 and 32: 185 and 194 us);
+//   kMinShare   that a share has at least.  2, 4, 8, 12: one short prompt 10.6, 10.6, 15.5 and 19.9 us.
 template <int D>
 struct Shape {
     static constexpr int kD = D, kTile = flash::kTile, kMinSplit = 8, kMinWhole = 32, kMinShare = 4, kOwn = 4;
@@ -93,7 +100,7 @@ struct Item {
 
 // ----------------------------------------------------------------- shares ----
 // Costs count a (row of a token's group, token) pair as 1 / block rows of it: a block costs the tokens its last row
-// sees times G, and one tile more.
+// sees times G, and kOwn tiles.
 template <class Sh>
 struct Costs {
     static constexpr int R = Sh::kBlock;

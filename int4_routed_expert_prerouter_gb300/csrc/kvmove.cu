@@ -2,7 +2,10 @@
 // contexts), whole pages copied (forks).  Codes and (s, b) pairs move as they are.
 //
 // Both are bound by the bytes read and written, or by a few dependent reads where there is
-// little to move (row number, page numbers, the row).
+// little to move (row number, page numbers, the row).  Accepted ones of 64 sequences' 16 drafted tokens, 8 heads of
+// 128 dims in 4 bits: 4.6 us, hardly more than an empty kernel's.  A quarter of 7 contexts of 8,191 tokens in 8 bits: 19.6 us
+// for 31 MB; a sequence's chunks follow one another, each a read behind a look at the tables.  1,000 pages copied eight times over:
+// 143 us for 664 MB, 68 % of what a plain copy moves (the pages that several copies read come from the L2).
 #include "kvcache.cuh"
 #include "launch.cuh"
 
@@ -164,7 +167,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_copy_pages_kernel(const CopyP
 template <int BITS, int D>
 int launch_compact(const CompactP& p, int B, cudaStream_t stream) {
     // few rows per sequence: small CTAs, so that many fit; many: as many threads as there are, for chunks follow one another
-    // (7 contexts of 8,191 tokens of which up to 2,047 are kept, 256 and 1,024 threads: 27 and XX us)
+    // (7 contexts of 8,191 tokens of which up to 2,047 are kept, 256 and 1,024 threads: 27 and 19.6 us)
     if (p.T / B <= 64) return launch_early(kv_compact_kernel<BITS, D, 256>, dim3(2 * p.c.H, B), 256, 0, stream, p);
     return launch_early(kv_compact_kernel<BITS, D, 1024>, dim3(2 * p.c.H, B), 1024, 0, stream, p);
 }
