@@ -669,8 +669,8 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
             }
         }
         const bool whole = x.part < 0;
-        const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-        const float nan = l != l ? l : 0.f;
+        // (a row without weights: of finite values, those of V that it does not see among them; an l of NaN stays one)
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         __half* out = p.o.out + (long long)(x.s.q0 + token) * p.o.ldo + (long long)head * D;
         float* part = p.o.part_o + ((long long)x.part * X::kBlock + local) * D;
         const bool writes = live && (s == 0 || pair);
@@ -701,19 +701,16 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
                     tmem_ld32(o_at + k, raw);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        o[i] = __uint_as_float(raw[i]);
-                        if (merge) o[i] = o[i] * f0 + swap[i * kRowsQ + local] * f1;
+                    for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(raw[i]);
+                    if (merge) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = o[i] * f0 + swap[i * kRowsQ + local] * f1;
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0.f;
                 }
                 if (fix && live) p.add_special(x, token, k, o);
-                if (l == 0.f || l != l) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = nan;
-                }
                 if (whole) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
@@ -728,11 +725,12 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
                     }
                     if (k & 32) {                       // 64 dims of the warp's rows are there
                         __syncwarp();
+                        uint4 w[8];                     // (all under way together)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint4*>(stage + swizzled(4 * i + (lane >> 3), lane & 7));
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            if (row_out[i])
-                                *reinterpret_cast<uint4*>(row_out[i] + (k & ~32) + 8 * (lane & 7)) =
-                                    *reinterpret_cast<const uint4*>(stage + swizzled(4 * i + (lane >> 3), lane & 7));
+                            if (row_out[i]) *reinterpret_cast<uint4*>(row_out[i] + (k & ~32) + 8 * (lane & 7)) = w[i];
                         __syncwarp();
                     }
                 } else if (writes) {
