@@ -20,7 +20,7 @@
 // to 64 the sets take the steps in turn, so that one's latencies lie under the other's work, and hand the rows' references on
 // from step to step.  Loops over pieces stay rolled: with all of it unrolled a third of the
 // stalls were for instructions to arrive.  8 the matrix steps; 9 copies strips' halves (16 tokens of K or of V, one run of
-// bytes) into a ring of raw ones; 10-15 turn those into operands and tables.
+// bytes) into a ring of raw ones; the rest turn those into operands and tables.
 //
 // What bounds it: neither bytes (0.6 TB/s) nor the tensor cores (20 % of their cycles) but the latencies between
 // the roles and their instructions, half of them spent on turning codes into operands: about 2,300 cycles a step of 64
@@ -34,9 +34,6 @@ namespace {
 
 using namespace flash;
 
-constexpr int kMakers = 6;               // warps that turn codes into operands
-constexpr int kThreadsT = kSoftmax + 64 + 32 * kMakers;
-static_assert(kThreadsT == 512, "the register split");
 constexpr int kMaxRaw = 40;              // raw entries
 constexpr int kExt = 16;                 // columns of V' beside a group's 64 dims
 constexpr float kUpV = 1024.f;           // weights are that many times as large: p <= 2^4, m < 2.2
@@ -53,6 +50,11 @@ struct Tile {
     static constexpr int kUnits = kTile / kv::kStrip;                // raw entries of a tile's K or V
     static constexpr int kCols = kGroup + kExt;
     static constexpr bool kQTmem = D <= 128;
+    // Warps that turn codes into operands: six, and ten for twice the bytes of 128 dims in 8 bits (30 sequences of 3,000 tokens
+    // 98 us -> 92; 64 dims 76 -> 78, 128 in 4 bits, 64 sequences of up to 4,000, 157 -> 163).  Of 256 dims a warp may not
+    // be more than three entries ahead of its own last, or a stage could be two phases behind what the warp waits for.
+    static constexpr int kMakers = BITS_ == 8 && D == 128 ? 10 : 6;
+    static constexpr int kThreads = kSoftmax + 64 + 32 * kMakers;
     // TMEM columns
     static constexpr int kScores = GR * kTile, kO = kBufs * kScores, kQ = kO + GR * kCols, kAll = kQ + (kQTmem ? D / 2 + 8 * GR : 0);
     static_assert(kAll <= 512, "tensor memory");
@@ -750,7 +752,7 @@ __device__ __forceinline__ void tree_matrix(const Tree<X>& p, TreeControl& c, ch
 }
 
 template <class X>
-__global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_constant__ Tree<X> p, bool joins) {
+__global__ void __launch_bounds__(X::kThreads, 1) attn_tree_kernel(const __grid_constant__ Tree<X> p, bool joins) {
     extern __shared__ char start[];
     char* smem = start + ((128 - (smem_u32(start) & 127)) & 127);
     static_assert(sizeof(TreeControl) <= X::kControlBytes, "control");
@@ -786,7 +788,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         c.dead = limit == 0;                                         // (limit 0: given up from the start)
     }
     // means, offsets and V's extra columns: zero where nothing is written later
-    for (int i = X::kQBytes / 16 + threadIdx.x; i < X::kRaw / 16; i += kThreadsT) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = X::kQBytes / 16 + threadIdx.x; i < X::kRaw / 16; i += X::kThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     tc::fence_async_smem();
     tc::fence_before_sync();
     wait_predecessor();
@@ -796,9 +798,15 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     if (joins && threadIdx.x == 0) p.o.places[blockIdx.x] = c.cut[0];
     if (blockIdx.x == 0 && threadIdx.x < p.B && p.status && p.over(threadIdx.x)) atomicExch(p.status, EDGE0_EINVAL);
 
-    // registers: 256 x 160 + 256 x 96, what the CTA was launched with (512 x 128)
-    if (wid < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;\n");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
+    // registers, as many as the CTA was launched with: 256 x 160 + 256 x 96 of 512 x 128, or 256 x 144 + 384 x 64 of 640 x 96
+    static_assert(X::kMakers == 6 || X::kMakers == 10, "the register split");
+    if constexpr (X::kMakers == 6) {
+        if (wid < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;\n");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
+    } else {
+        if (wid < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;\n");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    }
     if (wid < 8) {
         tree_softmax<X>(p, c, smem);
     } else if (wid == 8) {
@@ -877,7 +885,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         while (walk.next(x)) {
             const int n = x.hi - x.lo;
             if (n > 0) ++number;
-            for (; at < 2 * n * kHalves; at += kMakers) {
+            for (; at < 2 * n * kHalves; at += X::kMakers) {
                 bool v;
                 const int entry = at / kHalves, i = tile_of_entry<X>(entry, n, v);
                 const int tile = base + i, stage = tile % X::kStages;
@@ -945,7 +953,7 @@ int launch(const TreeP& base, char* ws, cudaStream_t stream) {
     const long long blocks = ((long long)p.T * p.G / X::kBlock + p.B) * p.H;
     const bool joins = (p.cap + X::kTile - 1) / X::kTile >= X::kMinSplit;
     const int grid = joins || blocks > sms ? sms : (int)blocks;
-    const int rc = launch_early(attn_tree_kernel<X>, dim3(grid), kThreadsT, X::kSmem, stream, p, joins);
+    const int rc = launch_early(attn_tree_kernel<X>, dim3(grid), X::kThreads, X::kSmem, stream, p, joins);
     if (rc || !joins || grid < 2) return rc;
     return launch_early(flash_join<X, Tree<X>>, dim3(grid - 1, X::kBlock / 32), 32 * kJoinWarps, 0, stream, p);
 }
