@@ -43,7 +43,8 @@ constexpr int kSoftmax = 256;         // threads of the two softmax warpgroups
 //   kOwn        what a block costs beside its tiles (its queries, the first scores, the last product, its outputs).  1 instead
 //               of 4: 64 prompts of up to 1,024 tokens 299 us instead of 279, drafts of 64 sequences 199 instead of 185;
 //               8: 298 and 190;
-//   kMinSplit   from which on a block may be cut (a cut costs a start and an end more, parts of fp32 and their join);
+//   kMinSplit   from which on a block may be cut (a cut costs a start and an end more, parts of fp32 and their join).  4
+//               instead of 8: a prompt of 1,000 tokens 44 us instead of 33, drafts behind 300 tokens 18 instead of 15;
 //   kMinWhole   likewise, where a block is not as much as two shares: there it is only the shares' evenness that a cut
 //               serves.  8 instead of 32: a prompt of 2,000 tokens 64.5 us instead of 55, of 4,000 131 instead of 122; drafted
 //               tokens' blocks cost less to cut (8 and 32: 185 and 194 us);
