@@ -650,7 +650,6 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
             tc::fence_after_sync();
         }
         if (!ok) l = __int_as_float(0x7fffffff);
-        const bool fix = n > 0 && special_of(c, number) == number;
 
         // a block of one row tile: the second stream's sums and accumulator come through its staging memory
         float f0 = 1.f, f1 = 0.f;
@@ -669,6 +668,9 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
                 ref = top;
             }
         }
+        // (read only here: the first stream adds what the rows see of both streams' V tiles, and the second one's last has
+        // been looked through for certain when that stream's last product is done)
+        const bool fix = n > 0 && special_of(c, number) == number;
         const bool whole = x.part < 0;
         // (a row without weights: of finite values, those of V that it does not see among them; an l of NaN stays one)
         const float inv = l == 0.f ? 0.f : 1.f / l;

@@ -95,6 +95,30 @@ def test_infinities_behind_a_row_in_blocks_that_are_cut(D):
     assert flash_ref.close(got.masked_fill(inf, 0.0), o.masked_fill(inf, 0.0), bound)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [2, 30, 100])
+@pytest.mark.parametrize("m", [256, 512, 2048, 8192])
+def test_infinities_in_the_last_of_an_even_number_of_tiles(D, n, m):
+    """Blocks of one row tile, whose two streams take the tiles in turn: the last one, which only some rows see in whole, is the second
+    stream's, and its infinities are added by the first.  The same bits on every run."""
+    H = 24
+    q, k, v = rows(n, H, D), rows(m, H, D), rows(m, H, D)
+    at = m - n // 2
+    v[at, :, 5], v[at, :, 9] = float("nan"), float("inf")
+    seen = flash_ref.causal(n, m, DEV)
+    finite = torch.where(v.isfinite(), v, torch.zeros_like(v))
+    o, bound = flash_ref.attend(q.double(), k.double(), finite.double(), seen, D ** -0.5)
+    o[seen[:, at], :, 5], o[seen[:, at], :, 9] = float("nan"), float("inf")
+    inf, first = o.isinf(), None
+    args = q, k, v, i32([0, n]), i32([0, m])
+    for _ in range(60):
+        got = binding.attn_prompt(*args)
+        first = got if first is None else first
+        assert torch.equal(got.view(torch.int16), first.view(torch.int16))
+    assert torch.equal(got.isinf(), inf) and (got[inf] > 0).all()
+    assert flash_ref.close(got.masked_fill(inf, 0.0), o.masked_fill(inf, 0.0), bound)
+
+
 def test_without_any_key():
     q, k = rows(70, 4, 128), torch.empty(0, 2, 128, dtype=torch.float16, device=DEV)
     got = binding.attn_prompt(q, k, k, i32([0, 50, 70]), i32([0, 0, 0]))
