@@ -179,9 +179,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_prompt_kernel(const __grid_
                 }
                 __syncwarp();
             }
-            // nothing may land in this memory when it has become another CTA's
-            // (its queries: below)
-            if (!ok) drain_copies_call(c.full, at > R::kStages ? at - R::kStages : 0, at, R::kStages);
+            if (lead_lane) c.issued = at;
         } else {
             Feed<X, Src> feed(p, c.cut, blockIdx.x);
             for (int at = 0; feed.next(); ++at) {
@@ -230,6 +228,8 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_prompt_kernel(const __grid_
         if (c.dead) {                // matrix steps under way still read shared memory and write the accumulators
             commit(&c.drained, elect());
             wait_copy(&c.drained, 0, kDefaultWaitNs);
+            // ... and copies under way, whoever gave up, must not land in what has become another CTA's memory
+            drain_copies_call(c.full, c.issued > R::kStages ? c.issued - R::kStages : 0, c.issued, R::kStages);
             for (int s = 0; s < 2; ++s)
                 if (c.q_loads[s]) wait_copy(&c.q_full[s], (c.q_loads[s] - 1) & 1, kDefaultWaitNs);
         }

@@ -81,6 +81,7 @@ struct TreeControl {
     Place cut[2];
     uint32_t tmem;
     int dead;
+    int issued;           // copies into the raw ring in all, when the warp that issues them has ended
     int special[16];      // numbers of the share's blocks with NaN of V that some rows do not see, by their last bits
     float ref[kRowsQ], sums[2][kRowsQ];
 };
@@ -785,6 +786,7 @@ __global__ void __launch_bounds__(X::kThreads, 1) attn_tree_kernel(const __grid_
         mbar_init(&c.drained, 1);
         fence_mbar_init();
         for (int i = 0; i < 16; ++i) c.special[i] = 0;
+        c.issued = 0;
         c.dead = limit == 0;                                         // (limit 0: given up from the start)
     }
     // means, offsets and V's extra columns: zero where nothing is written later
@@ -874,8 +876,7 @@ __global__ void __launch_bounds__(X::kThreads, 1) attn_tree_kernel(const __grid_
                 }
             }
         }
-        // nothing may land in this memory when it has become another CTA's
-        if (!ok) drain_copies_call(c.raw_full, unit > X::kRaws ? unit - X::kRaws : 0, unit, X::kRaws);
+        if (lane == 0) c.issued = unit;
     } else {
         // a maker: every kMakers-th half of a tile's K or V, in the ring's order
         constexpr int kHalves = 2, kEach = X::kUnits / kHalves;
@@ -925,6 +926,8 @@ __global__ void __launch_bounds__(X::kThreads, 1) attn_tree_kernel(const __grid_
         if (c.dead) {                // matrix steps under way still read shared memory and write the accumulators
             commit(&c.drained, elect());
             wait_copy(&c.drained, 0, kDefaultWaitNs);
+            // ... and copies under way, whoever gave up, must not land in what has become another CTA's memory
+            drain_copies_call(c.raw_full, c.issued > X::kRaws ? c.issued - X::kRaws : 0, c.issued, X::kRaws);
             if (lane == 0 && p.status) atomicExch(p.status, EDGE0_ETIMEOUT);
         }
         tc::tmem_dealloc(c.tmem, 512);

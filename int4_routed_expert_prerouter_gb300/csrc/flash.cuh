@@ -354,6 +354,7 @@ struct Control {
     Place cut[2];
     uint32_t tmem;
     int q_loads[2];                 // copies of a stream's queries so far
+    int issued;                     // copies of ring entries in all, when the warp that issues them has ended
     int dead;                       // a wait ran out: nothing more is issued, what is not done becomes NaN
     int special[kMaxStages * 2];    // numbers of the share's blocks with non-finite V that some rows do not see, by their last bits
     float2 ml[kRowsQ];              // the second stream's (reference, sum)
@@ -767,7 +768,7 @@ __device__ __forceinline__ void control_init(Control& c, int full_count, int cle
     mbar_init(&c.drained, 1);
     fence_mbar_init();
     c.dead = dead;
-    c.q_loads[0] = c.q_loads[1] = 0;
+    c.q_loads[0] = c.q_loads[1] = c.issued = 0;
     for (int i = 0; i < kMaxStages * 2; ++i) c.special[i] = 0;
 }
 

@@ -280,6 +280,25 @@ def test_without_waiting(D, n, m):
         assert torch.equal(binding.attn_prompt(q, k, v, i32(cu), i32(ck), out=torch.full_like(q, 5.0)), clean)
 
 
+@pytest.mark.parametrize("D,G", [(64, 4), (128, 4), (256, 4), (128, 5), (128, 1)])
+@pytest.mark.parametrize("n,m", [([300, 5], [300, 5]), ([60, 7], [9000, 70]), ([1, 130, 64], [100, 700, 64])])
+def test_waits_that_run_out_on_the_way(D, G, n, m):
+    """Limits shorter than the call: rows that lack something are NaN, the others as they should be, and so is the next call."""
+    cu, ck = cut(n, 2), cut(m)
+    q, k, v = rows(cu[-1] + 3, 2 * G, D), rows(ck[-1], 2, D), rows(ck[-1], 2, D)
+    call = lambda: binding.attn_prompt(q, k, v, i32(cu), i32(ck), out=torch.full_like(q, 5.0))
+    clean = call()
+    for limit in (1, 500, 1000, 2000, 4000, 8000, 16000) * 3:
+        binding.set_wait_limit(limit)
+        try:
+            got = call()
+        finally:
+            binding.set_wait_limit()
+        lost = torch.isnan(got).all(2)
+        assert torch.equal(got[~lost], clean[~lost]) and not lost[:2].any() and not lost[cu[-1]:].any(), limit
+        assert torch.equal(call(), clean), limit
+
+
 def test_refusals():
     q, k, cu = rows(10, 4, 128), rows(10, 2, 128), i32([0, 10])
     bad = [lambda: binding.attn_prompt(q, k, k[:5], cu), lambda: binding.attn_prompt(q, k[:5], k[:5], cu),

@@ -270,6 +270,28 @@ def test_without_waiting(bits, D, lens):
         assert torch.equal(call(pool, q, table, lens, cu, mask, out=torch.full_like(q, 5.0)), clean) and pool.cache.error() == binding.EDGE0_OK
 
 
+@pytest.mark.parametrize("bits,D", [(4, 64), (4, 128), (4, 256), (8, 64), (8, 128), (8, 256)])
+@pytest.mark.parametrize("lens,counts", [([300, 5, -1], [10, 7, 3]), ([9000, 70, 0], [10, 30, 3]), ([40, 500, 900], [40, 5, 1])])
+def test_waits_that_run_out_on_the_way(bits, D, lens, counts):
+    """Limits shorter than the call: rows that lack something are NaN and reported, the others as they should be, and so is the next call."""
+    c = case(bits, D, 2, 4, 64, lens, counts)
+    pool, q = c[:2]
+    run = lambda: call(*c, out=torch.full_like(q, 5.0))
+    clean = run()
+    assert pool.cache.error() == binding.EDGE0_OK
+    for limit in (1, 500, 1000, 2000, 4000, 8000, 16000) * 3:
+        binding.set_wait_limit(limit)
+        try:
+            got = run()
+        finally:
+            binding.set_wait_limit()
+        lost = torch.isnan(got).all(2)
+        assert torch.equal(got[~lost], clean[~lost]), limit
+        error = pool.cache.error()          # (a wait may run out that no row lacks anything for)
+        assert error == binding.EDGE0_ETIMEOUT if lost.any() else error in (binding.EDGE0_OK, binding.EDGE0_ETIMEOUT), limit
+        assert torch.equal(run(), clean) and pool.cache.error() == binding.EDGE0_OK, limit
+
+
 @pytest.mark.parametrize("bits,D", [(4, 128), (8, 256), (4, 64)])
 @pytest.mark.parametrize("chain", [False, True])
 def test_blocks_of_few_and_of_many_rows_in_turn(bits, D, chain):
