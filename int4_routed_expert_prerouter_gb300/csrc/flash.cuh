@@ -540,6 +540,11 @@ __device__ __forceinline__ void matrix_warp(const Src& p, Control& c, uint32_t q
 }
 
 // ------------------------------------------------- the softmax warpgroups ----
+// References whose fp32 step is 1/2 or more.  The product S c in full, less a reference that is one rounded, may be half a step above
+// zero for the largest score itself, and a weight beyond fp16; rounded before the reference comes off, as the
+// reference was, it is not.  (Such scores are good to a few steps, whichever way they are formed.)
+__device__ __forceinline__ bool is_far(float ref) { return fabsf(ref) >= 0x1p22f && ref != -INFINITY; }
+
 // Thread: one row of stream s.
 template <int D, class Src>
 __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_smem, char* stage_smem) {
@@ -568,7 +573,7 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
             mbar_arrive(&c.q_full[s]);
         }
         float ref = -INFINITY, l = 0.f;
-        bool ok = true;
+        bool ok = true, far = false;
         for (int j = 0; j < n; ++j) {
             const int buf = X::kStreams == 2 ? s : (base + j) & 1;
             const uint32_t s_at = tm + buf * kTile;
@@ -599,33 +604,57 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
             for (int k = 0; k < kTile; k += 8)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], fmaxf(__uint_as_float(v[k + 2 * i]), __uint_as_float(v[k + 2 * i + 1])));
-            const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * cc;
-            const bool move = most > ref + kRise || (most > ref && ref == -INFINITY);
-            if (__any_sync(0xffffffffu, move)) {
+            const float most = __fmul_rn(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), cc);
+            const bool move = most - ref > kRise;
+            if (__any_sync(0xffffffffu, move || far)) {
                 const float to = move ? most : ref, f = to == ref ? 1.f : ex2(ref - to);
                 l *= f;
                 ref = to;
-                if (X::kStreams == 1 && j > 0) {
-                    // the product of the tile before, the other buffer's latest (with two streams it was issued
-                    // before these scores)
-                    const int g = base + j - 1;
-                    ok = wait_phase(&c.o_step[g & 1], (g >> 1) & 1, c.dead, p.o.wait_ns);
-                    tc::fence_after_sync();
-                }
-                if (j > 0) {
+                far = is_far(ref);
+                if (__any_sync(0xffffffffu, move)) {
+                    if (X::kStreams == 1 && j > 0) {
+                        // the product of the tile before, the other buffer's latest (with two streams it was issued
+                        // before these scores)
+                        const int g = base + j - 1;
+                        ok = wait_phase(&c.o_step[g & 1], (g >> 1) & 1, c.dead, p.o.wait_ns);
+                        tc::fence_after_sync();
+                    }
+                    if (j > 0) {
 #pragma unroll 1
-                    for (int k = 0; k < D; k += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(o_at + k, o);
-                        tc::tmem_wait_ld();
+                        for (int k = 0; k < D; k += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(o_at + k, o);
+                            tc::tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st32(o_at + k, o);
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st32(o_at + k, o);
+                        }
                     }
                 }
+                if (__any_sync(0xffffffffu, far)) {
+                    // rounded exponents less the reference in the scores' place, 32 at a time (all in registers, next to the
+                    // scores, cost calls without such rows 2 to 4 %); intrinsics: never one fused step
+#pragma unroll 1
+                    for (int k = 0; k < kTile; k += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(s_at + k, o);
+                        tc::tmem_wait_ld();
+                        const uint32_t seen = tile >= x.clear ? p.seen_word(x, token, tile * kTile + k) : 0xffffffffu;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float e = (seen >> i) & 1 ? __uint_as_float(o[i]) : -INFINITY;
+                            o[i] = __float_as_uint(far ? __fsub_rn(__fmul_rn(e, cc), ref) : e);
+                        }
+                        tmem_st32(s_at + k, o);
+                    }
+                    tmem_wait_st();
+#pragma unroll
+                    for (int k = 0; k < kTile; k += 32) tmem_ld32(s_at + k, v + k);
+                    tc::tmem_wait_ld();
+                }
             }
-            const float sub = ref == -INFINITY ? 0.f : kUp - ref;
-            const f2 c2 = pk(cc, cc), sub2 = pk(sub, sub);
+            const float by = far ? 1.f : cc, sub = far ? kUp : ref == -INFINITY ? 0.f : kUp - ref;
+            const f2 c2 = pk(by, by), sub2 = pk(sub, sub);
             f2 sum[2] = {0, 0};
 #pragma unroll
             for (int k = 0; k < kTile; k += 2) {

@@ -150,6 +150,65 @@ def test_scores_of_any_magnitude(D, q_scale, k_offset):
     check(binding.attn_prompt(q, k, v, i32(cu)), q, k, v, cu, cu)
 
 
+def equal_scores(T, D, q_size, k_size, q_heads, k_heads, gen):
+    """q and k of one dim each that is not zero, so that every score is one product of two fp16, exact in fp32: signs of either kind,
+    magnitudes of a few classes."""
+    power = lambda n, h, size: torch.where(torch.rand(n, h, generator=gen) < 0.3, -1.0, 1.0) * size * 0.5 ** torch.randint(0, 3, (n, h), generator=gen)
+    q, k = torch.zeros(T, q_heads, D), torch.zeros(T, k_heads, D)
+    q[..., 3], k[..., 3] = power(T, q_heads, q_size), power(T, k_heads, k_size)
+    return q.half().to(DEV), k.half().to(DEV)
+
+
+def means(q, k, v, seen):
+    """What scores far apart but for equal ones give, the mean of the v of a row's largest ones, and how far an fp16 result may be
+    off: its rounding, each weight's (the weights are the same number, so the sum's too) and fp32 sums."""
+    G = q.shape[1] // k.shape[1]
+    wide = lambda x: x.double().repeat_interleave(G, 1)
+    s = torch.einsum("nhd,mhd->hnm", q.double(), wide(k)).masked_fill(~seen, -float("inf"))
+    p = (s == s.amax(2, keepdim=True)).double()
+    p /= p.sum(2, keepdim=True)
+    o, a = (torch.einsum("hnm,mhd->nhd", p, x) for x in (wide(v), wide(v).abs()))
+    return o, 2.0 ** -11 * o.abs() + 2.0 ** -25 + (2.0 ** -11 + (k.shape[0] / 16 + 64) * 2.0 ** -23) * a
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_size,k_size,scale", [(2001.0, 1111.0, 1.0), (3001.0, 16008.0, None), (50016.0, 40032.0, None),
+                                                 (1.375, 1.125, 1e6), (60000.0, 50016.0, 1e6), (513.0, 1025.0, 3.0)])
+@pytest.mark.parametrize("n,m", [(300, 300), (40, 3000), (700, 700)])
+def test_scores_beyond_what_fp32_tells_apart(D, q_size, k_size, scale, n, m):
+    """Exponents of 2^21 up to 2^50, whose fp32 steps are up to 2^26: the largest scores of a row weigh the same, all others nothing."""
+    gen = torch.Generator().manual_seed(D + n)
+    q, k = equal_scores(m, D, q_size, k_size, 4, 2, gen)
+    q, v = q[:n].contiguous(), rows(m, 2, D)
+    got = binding.attn_prompt(q, k, v, i32([0, n]), i32([0, m]), scale=scale)
+    o, bound = means(q, k, v, flash_ref.causal(n, m, DEV))
+    assert ((got.double() - o).abs() <= bound).all(), ((got.double() - o).abs() - bound).nan_to_num(99.0).max().item()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_size,k_size,scale", [(20000.0, 10000.0, None), (3000.0, 3000.0, None), (3000.0, 10.0, 1e4), (1.0, 1.0, 1e6)])
+def test_rows_of_huge_scores_beside_ordinary_ones(D, q_size, k_size, scale):
+    """Finite, within the bound, and nothing to the rows beside them."""
+    n = 260
+    q, k, v = rows(n, 4, D), (rows(n, 2, D).float() * k_size).clamp(-60000, 60000).half(), rows(n, 2, D)
+    q = (q.float() / (k_size * (scale or D ** -0.5) * D ** 0.5)).half()
+    args = k, v, i32([0, n])
+    clean = binding.attn_prompt(q, *args, scale=scale)
+    far = torch.rand(n, device=DEV) < 0.3
+    huge = q.clone()
+    huge[far] = (rows(int(far.sum()), 4, D).float() * q_size).clamp(-60000, 60000).half()
+    got = binding.attn_prompt(huge, *args, scale=scale)
+    assert torch.equal(got[~far], clean[~far])
+    check(got, huge, k, v, [0, n], [0, n], scale=scale)
+    # (the bound says little of them; they lie between the values that they are means of)
+    seen = flash_ref.causal(n, n, DEV)
+    for h in range(4):
+        vv = v[:, h // 2].float()
+        lo = torch.where(seen[:, :, None], vv[None], torch.inf).amin(1)
+        hi = torch.where(seen[:, :, None], vv[None], -torch.inf).amax(1)
+        assert ((got[:, h].float() >= lo - 0.01) & (got[:, h].float() <= hi + 0.01)).all()
+
+
 def test_weights_far_below_the_largest():
     """A token of huge V and tiny weight beside small values: weights stay normal far below the largest."""
     n, D = 400, 128
