@@ -428,7 +428,9 @@ __device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, c
             __syncwarp();
             tc::fence_after_sync();
             const uint32_t s_at = tm + ((uint32_t)(16 * rh) << 16) + buf * X::kScores;
-            f2 S[2 * NB][2];                                     // [8 tokens][k]: tokens 2t, 2t + 1; less the reference
+            // what the sums begin with: less the reference, but where that is far (flash.cuh), when it comes off the rounded sum
+            const float start[2] = {is_far(ref[0]) ? 0.f : off(ref[0]), is_far(ref[1]) ? 0.f : off(ref[1])};
+            f2 S[2 * NB][2];                                     // [8 tokens][k]: tokens 2t, 2t + 1
             {
                 uint32_t raw[GR][2][4 * NB];
 #pragma unroll
@@ -436,7 +438,7 @@ __device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, c
 #pragma unroll
                     for (int h = 0; h < 2; ++h) ld_frag<NB>(s_at + gr * T + h * (T / 2), raw[gr][h]);
                 tc::tmem_wait_ld();
-                const f2 from[2] = {pk(off(ref[0]), off(ref[0])), pk(off(ref[1]), off(ref[1]))};
+                const f2 from[2] = {pk(start[0], start[0]), pk(start[1], start[1])};
 #pragma unroll
                 for (int b = 0; b < 2 * NB; ++b)
 #pragma unroll
@@ -492,9 +494,8 @@ __device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, c
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 now[k] = both ? ref[k] : j ? at[8 * k] : -INFINITY;
-                by[k] = off(now[k]) - off(ref[k]);               // what these scores lack
-                mx[k] += by[k];
-                want = want || mx[k] > (now[k] == -INFINITY ? -INFINITY : kRise);
+                by[k] = off(now[k]) - start[k];                  // what these scores lack
+                want = want || mx[k] + by[k] > (now[k] == -INFINITY ? -INFINITY : kRise);
             }
             float f[2] = {1.f, 1.f};
             bool move = false;
@@ -504,10 +505,11 @@ __device__ __forceinline__ void tree_softmax(const Tree<X>& p, TreeControl& c, c
                     mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
                     mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
                     const bool fresh = now[k] == -INFINITY;
-                    if (mx[k] > (fresh ? -INFINITY : kRise)) {
-                        f[k] = fresh ? 0.f : ex2(-mx[k]);
-                        now[k] = mx[k] - off(now[k]);
-                        by[k] = off(now[k]) - off(ref[k]);
+                    const float rise = mx[k] + by[k];
+                    if (rise > (fresh ? -INFINITY : kRise)) {
+                        f[k] = fresh ? 0.f : ex2(-rise);
+                        now[k] = mx[k] - start[k];
+                        by[k] = is_far(now[k]) ? -mx[k] : off(now[k]) - start[k];      // (the largest score becomes zero)
                         move = true;
                     }
                 }

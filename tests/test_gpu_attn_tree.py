@@ -1,5 +1,6 @@
 """Attention of drafted tokens over the cache on the GPU against its definition in 64 bits, and with the
 calls around it: rotary positions, append, compaction, decode attention."""
+import math
 import threading
 
 import numpy as np
@@ -143,6 +144,83 @@ def test_magnitudes(bits, D, q_scale, kw):
     c = list(case(bits, D, 1, 4, 32, [700, 20], [10, 40], **kw))
     c[1] = (c[1].float() * q_scale).half()
     check(call(*c), *c)
+
+
+def written(k, v, page, bits):
+    """A cache of the rows k, v [n, H, D] in pages in reverse order, with their table, what its groups stand for (K, V in 64 bits) and the
+    magnitudes of V's parts."""
+    n, H, D = k.shape
+    W = -(-n // page)
+    cache = binding.KVCache(W, page, H, D, bits, device=DEV)
+    table = i32(np.arange(W)[::-1].copy()[None])
+    binding.kv_append(cache, k, v, table, i32([0]), i32([0, n]))
+    out = []
+    for x in (k, v):
+        codes, s, b = (torch.from_numpy(np.ascontiguousarray(a)).to(DEV).double() for a in ref.quantise(x.cpu().numpy(), bits))
+        s, b, z = s.repeat_interleave(64, -1), b.repeat_interleave(64, -1), 2.0 ** (bits - 1)
+        out.append((s * codes + b, (s * (codes - z)).abs() + (s * z + b).abs()))
+    return cache, table, out[0][0], *out[1]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_size,k_size,scale", [(2001.0, 1111.0, 1.0), (3001.0, 16008.0, None), (50016.0, 40032.0, None),
+                                                 (1.375, 1.125, 1e6), (60000.0, 50016.0, 1e6), (513.0, 1025.0, 3.0)])
+@pytest.mark.parametrize("n,x", [(250, 12), (100, 60), (3000, 9)])
+def test_scores_beyond_what_fp32_tells_apart(bits, D, q_size, k_size, scale, n, x):
+    """Queries and keys of one dim each that is not zero, of a few classes: the largest scores of a row weigh the same, all others
+    nothing, whatever their size (exponents of 2^21 up to 2^50)."""
+    H, G, gen = 2, 4, torch.Generator().manual_seed(D + n)
+    size = lambda m, h, a: (torch.where(torch.rand(m, h, generator=gen) < 0.3, -a, a) * 0.5 ** torch.randint(0, 3, (m, h), generator=gen)).half().to(DEV)
+    q, k, v = (torch.zeros(m, h, D, dtype=torch.float16, device=DEV) for m, h in ((x, H * G), (n + x, H), (n + x, H)))
+    q[..., 3], k[..., 3], v = size(x, H * G, q_size), size(n + x, H, k_size), rows(n + x, H, D)
+    cache, table, kk, vv, parts = written(k, v, 32, bits)
+    mask = tree_words([x], 2, np.random.default_rng(n))
+    for m in (None, mask):
+        got = binding.attn_tree(cache, q, table, i32([n]), i32([0, x]), None if m is None else i32(m), scale=scale)
+        s = torch.einsum("nhd,mhd->hnm", q.double(), kk.repeat_interleave(G, 1)).masked_fill(~visible(n, x, m), -float("inf"))
+        p = (s == s.amax(2, keepdim=True)).double()
+        p /= p.sum(2, keepdim=True)
+        o, a, b = (torch.einsum("hnm,mhd->nhd", p, y.repeat_interleave(G, 1)) for y in (vv, vv.abs(), parts))
+        # the result's rounding, each weight's (one number, so the sum's too), fp32 sums
+        bound = 2.0 ** -11 * o.abs() + 2.0 ** -25 + 2.0 ** -11 * a + (((n + x) / 16 + 64) * 2.0 ** -23 + 2.0 ** -21) * b
+        # Exponents below 2^22: a score less the reference is formed in one fused step, but in the tile that sets the reference, where
+        # both are rounded sums, and by a set of warps whose reference is an older one, which adds their difference: two roundings
+        # by half an fp32 step e of the exponent, so equal scores' weights differ by a factor of up to 2^e, and with w in (1 - t, 1 + t),
+        # t = 2^e - 1, sum w p v / sum w p is off by at most t (sum p |v| + |o|).
+        top = (s.amax(2).abs() * (scale or D ** -0.5) * math.log2(math.e)).T[:, :, None]
+        e = torch.where(top < 2.0 ** 22, 2.0 ** (torch.floor(torch.log2(top)) - 23), 0.0)
+        bound += (2.0 ** e - 1) * (a + o.abs())
+        err = (got.double() - o).abs()
+        assert (err <= bound).all(), (err - bound).nan_to_num(99.0).max().item()
+    assert cache.error() == binding.EDGE0_OK
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_size,k_size,scale", [(20000.0, 10000.0, None), (3000.0, 3000.0, None), (3000.0, 10.0, 1e4), (1.0, 1.0, 1e6)])
+@pytest.mark.parametrize("x", [12, 60])
+def test_rows_of_huge_scores_beside_ordinary_ones(bits, D, q_size, k_size, scale, x):
+    """Finite, between the values that they are means of, and nothing to the rows beside them."""
+    n, H, G = 900, 2, 4
+    k, v = (rows(n + x, H, D).float() * k_size).clamp(-60000, 60000).half(), rows(n + x, H, D)
+    cache, table, kk, vv, _ = written(k, v, 16, bits)
+    q = (rows(x, H * G, D).float() / (k_size * (scale or D ** -0.5) * D ** 0.5)).half()
+    args = table, i32([n]), i32([0, x]), i32(tree_words([x], 2, np.random.default_rng(x)))
+    clean = binding.attn_tree(cache, q, *args, scale=scale)
+    far = torch.rand(x, H * G, device=DEV) < 0.3
+    huge = torch.where(far[:, :, None], (rows(x, H * G, D).float() * q_size).clamp(-60000, 60000).half(), q)
+    got = binding.attn_tree(cache, huge, *args, scale=scale)
+    assert torch.equal(got[~far], clean[~far])
+    wide = vv.repeat_interleave(G, 1)
+    assert ((got >= wide.amin(0) - 0.01) & (got <= wide.amax(0) + 0.01)).all() and cache.error() == binding.EDGE0_OK
+    # one token far ahead of the others is what a row gives
+    s = (scale or D ** -0.5) * torch.einsum("nhd,mhd->hnm", huge.double(), kk.repeat_interleave(G, 1))
+    s = s.masked_fill(~visible(n, x, args[3].cpu().numpy().view(np.uint32)), -float("inf"))
+    two = s.topk(2, dim=2)
+    ahead = (two.values[..., 0] - two.values[..., 1] > 40 + two.values.abs().amax(2) * 2.0 ** -14).T          # [x, heads]
+    best = torch.gather(wide.permute(1, 0, 2), 1, two.indices[..., :1].expand(-1, -1, D)).transpose(0, 1)       # [x, heads, D]
+    assert ahead[far].float().mean() > 0.2 and ((got.double() - best).abs() <= 2.0 ** -9 * best.abs() + 1e-4)[ahead].all()
 
 
 def test_masks():
