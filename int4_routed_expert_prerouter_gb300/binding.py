@@ -1034,9 +1034,9 @@ def _rope(plan, q, k, start, cu_rows, q_out, k_out, backward, stream):
     st = _ints(start, index, B, "rope: start")
     cu = None if cu_rows is None else _ints(cu_rows, index, B + 1, "rope: cu_rows")
     if T:
-        code = _lib.edge0_rope(plan.turns.data_ptr(), plan.head_dim, plan.rot_dim, plan.layout, plan.magnitude, bool(backward),
-                               args[0], args[1], args[2], args[3], args[4], args[5], args[6], args[7], args[8], args[9],
-                               T, st, cu, B, _raw_stream(index, stream))
+        # (a plan of the caller's own frequencies has not loaded the library)
+        code = (_lib or lib()).edge0_rope(plan.turns.data_ptr(), plan.head_dim, plan.rot_dim, plan.layout, plan.magnitude,
+                                          bool(backward), *args, T, st, cu, B, _raw_stream(index, stream))
         if code:
             raise Edge0Error(code, "edge0_rope")
     return outs[0], outs[1]

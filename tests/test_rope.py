@@ -5,8 +5,10 @@ import math
 
 import numpy as np
 import pytest
+import torch
 
 from int4_routed_expert_prerouter_gb300 import binding, build
+from test_block_ops_refusals import handed, on_gpu  # noqa: F401 (a fixture)
 
 EINVAL, EUNSUP = binding.EDGE0_EINVAL, binding.EDGE0_EUNSUPPORTED
 A = C.c_void_p(1 << 20)          # an aligned address that is never read
@@ -107,3 +109,15 @@ def test_move_refusals(lib):
         assert copy(**kw) == EINVAL, kw
     assert copy(n=0, src=None, dst=None) == 0
     assert copy(c=binding.KvCacheDesc(4, 2, 96, 64, 8, A)) == EUNSUP
+
+
+def test_own_frequencies_as_the_first_call_of_a_process(handed, monkeypatch):  # noqa: F811
+    """A plan of the caller's frequencies needs nothing of the library, so the call itself has to load it."""
+    recorder = binding._lib
+    monkeypatch.setattr(binding, "_lib", None)
+    monkeypatch.setattr(binding, "lib", lambda: recorder)
+    monkeypatch.setattr(torch.Tensor, "to", lambda t, *a, **kw: on_gpu(t))
+    plan = binding.RopePlan(64, radians=np.linspace(0, np.pi, 32))
+    q = on_gpu(torch.zeros(3, 2, 64, dtype=torch.float16))
+    binding._rope(plan, q, None, on_gpu(torch.zeros(3, dtype=torch.int32)), None, q, None, False, None)
+    assert [name for name, _ in handed] == ["edge0_rope"]
