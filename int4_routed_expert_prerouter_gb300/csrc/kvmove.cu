@@ -40,8 +40,9 @@ __global__ void __launch_bounds__(THREADS) kv_compact_kernel(const CompactP p) {
     launch_dependents();
     const int h = blockIdx.x >> 1, half = blockIdx.x & 1, b = blockIdx.y;
     const int begin = p.cu ? p.cu[b] : b, start = p.start[b];
-    const int lo = max(begin, 0), hi = p.cu ? min(p.cu[b + 1], p.T) : b + 1;
-    if (start < 0 || hi <= lo) return;
+    const int first = max(begin, 0), last = p.cu ? min(p.cu[b + 1], p.T) : b + 1;
+    if (start < 0 || last <= first) return;
+    const unsigned lo = first, hi = last;            // (a few chunks behind 2^31 - 1 rows still count up)
     const int sub = threadIdx.x / kPieces, piece = threadIdx.x - sub * kPieces;
     const bool idle = sub >= kPar, pairs = piece == kPieces - 1;     // the row's (s, b) pairs come last
     char* base = p.c.pages + (long long)h * (p.c.page_tokens / kv::kStrip) * kStripBytes + half * kHalf;
@@ -53,11 +54,11 @@ __global__ void __launch_bounds__(THREADS) kv_compact_kernel(const CompactP p) {
         const unsigned token = pos - pg * p.c.page_tokens;
         return id * p.c.page_bytes + (long long)(token / kv::kStrip) * kStripBytes + token % kv::kStrip;
     };
-    auto look = [&](int r0, int buf) {
+    auto look = [&](unsigned r0, int buf) {
         for (int i = threadIdx.x; i < kChunk; i += THREADS) {
-            const int r = r0 + i;
+            const unsigned r = r0 + i;
             long long from = -1, to = -1;
-            if (r0 < hi && r < hi) {
+            if (r < hi) {
                 const long long dst = (long long)start + r - begin;
                 const int src = p.src[r];
                 if (src != dst) {
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(THREADS) kv_compact_kernel(const CompactP p) {
     __syncthreads();
     load(0, v[0], to[0]);
     if (lo + kChunk < hi) look(lo + kChunk, 1);
-    for (int r0 = lo;; r0 += 2 * kChunk) {
+    for (unsigned r0 = lo;; r0 += 2 * kChunk) {
         __syncthreads();                         // chunk r0 has been read by all, the next one's places are there
         if (r0 + kChunk < hi) {
             load(1, v[1], to[1]);

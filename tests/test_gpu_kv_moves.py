@@ -87,6 +87,19 @@ def test_compact_of_one_row_each_and_of_repeated_sources():
     assert cache.error() == binding.EDGE0_OK
 
 
+def test_compact_of_the_last_rows_that_an_int_counts():
+    """Rows up to 2^31 - 1: a chunk behind the last one is none."""
+    bits, D, H, page, n, T = 4, 64, 1, 16, 300, 2 ** 31 - 1
+    pages = torch.randint(0, 256, (40, int(binding.lib().edge0_kv_page_bytes(bits, H, D, page))), dtype=torch.uint8, device=DEV)
+    cache = binding.KVCache(40, page, H, D, bits, pages=pages)
+    table, before = np.random.default_rng(0).permutation(40)[None], pages.cpu().numpy()
+    src = torch.empty(T, dtype=torch.int32, device=DEV)
+    src[-n:] = torch.arange(2 * n, device=DEV, dtype=torch.int32)[1::2]
+    binding.kv_compact(cache, i32(table), i32([0]), src, i32([T - n, T]))
+    want = compacted(before, bits, H, D, page, table, [0], range(1, 2 * n, 2), [0, n])
+    assert np.array_equal(pages.cpu().numpy(), want) and cache.error() == binding.EDGE0_OK
+
+
 def test_compact_reports_what_it_cannot_move():
     bits, D, H, page = 8, 64, 2, 16
     pages = torch.randint(0, 256, (6, int(binding.lib().edge0_kv_page_bytes(bits, H, D, page))), dtype=torch.uint8, device=DEV)
