@@ -244,9 +244,9 @@ extern "C" int edge0_rope(const unsigned long long* turns, int head_dim, int rot
     p.start = start;
     p.cu = cu_rows;
     // tokens per CTA: so many that four CTAs per SM cover T
-    const int want = ceil_div(T, 152 * 4);
-    p.rows_per_cta = want < 1 ? 1 : want > kRopeMaxRows ? kRopeMaxRows : want;
-    const int grid = ceil_div(T, p.rows_per_cta), smem = p.rows_per_cta * (rot_dim / 2) * (int)sizeof(float2);
+    const int want = (T - 1) / (152 * 4) + 1;                // (T up to the largest int)
+    p.rows_per_cta = want > kRopeMaxRows ? kRopeMaxRows : want;
+    const int grid = (T - 1) / p.rows_per_cta + 1, smem = p.rows_per_cta * (rot_dim / 2) * (int)sizeof(float2);
     // 16-byte places need every run of turned dims to begin and end on one
     if (layout == EDGE0_ROPE_HALF)
         return rot_dim % 16 == 0 ? launch_early(rope_kernel<true, 8>, dim3(grid), kRopeThreads, smem, stream, p)

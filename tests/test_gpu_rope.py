@@ -125,6 +125,18 @@ def test_special_values_stay_in_their_pair():
     assert torch.equal(got[~hit], clean[~hit]) and not torch.isfinite(got[hit]).any()
 
 
+def test_the_last_rows_that_an_int_counts():
+    """2^31 - 1 rows, in place; those of no sequence stay."""
+    T, n = 2 ** 31 - 1, 37
+    plan = binding.RopePlan(8, device=DEV)
+    q = torch.empty(T, 1, 8, dtype=torch.float16, device=DEV)
+    q[-2 * n:] = torch.randn(2 * n, 1, 8, device=DEV).half()
+    before = q[-2 * n:].clone()
+    binding.rope(plan, q, None, i32([1000]), i32([T - n, T]), q_out=q)
+    assert torch.equal(q[-2 * n:-n], before[:n])
+    check(q[-n:], before[n:], 1000 + np.arange(n), plan)
+
+
 def test_in_a_graph_and_on_another_stream():
     plan = binding.RopePlan(128, device=DEV)
     q, k = torch.randn(33, 4, 128, device=DEV).half(), torch.randn(33, 1, 128, device=DEV).half()
