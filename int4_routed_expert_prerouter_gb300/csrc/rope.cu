@@ -50,7 +50,7 @@ struct RopeP {
 // V: values of each half of a pair that a thread takes, 8 (a 16-byte access each) or 1.
 template <bool HALF, int V>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeP p) {
-    extern __shared__ float2 table[];                    // [rows_per_cta][rot / 2] (cos, sin)
+    extern __shared__ __align__(16) float2 table[];       // [rows_per_cta][rot / 2] (cos, sin), read in pairs
     __shared__ int cu_s[EDGE0_MAX_BATCHED + 1];
     __shared__ long long pos_s[kRopeMaxRows];            // -1: nothing to do
     const int r0 = blockIdx.x * p.rows_per_cta, n = min(p.rows_per_cta, p.T - r0);
