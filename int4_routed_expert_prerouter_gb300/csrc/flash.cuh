@@ -207,6 +207,7 @@ __device__ void find_share(const Src& p, int cta, int ctas, long long* prefix, P
         }
         out[tid == 32] = at;
     }
+    tc::fence_async_smem();                           // (copies come where the scratch was)
     __syncthreads();
 }
 
