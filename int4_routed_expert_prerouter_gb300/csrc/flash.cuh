@@ -108,26 +108,28 @@ struct Costs {
     long long per, own;   // cost of a tile: kTile G; of a block beside its tiles
     long long off, all;   // off G, n_k G
     int blocks;
+    long long some, whole;   // the first blocks that see a token, that see all (R: a power of two)
 
-    __device__ Costs(const Seq& s, int G) {
+    __host__ __device__ Costs(const Seq& s, int G) {
         per = (long long)Sh::kTile * G;
         own = Sh::kOwn * per;
         off = (long long)s.off * G;
         all = (long long)s.n_k * G;
         blocks = (int)(((long long)s.n_q * G + R - 1) / R);
+        some = off >= 0 ? 0 : -off / R;
+        whole = all <= off ? 0 : (all - off + R - 1) / R - 1;
     }
-    __device__ long long tokens(int t) const {        // times G
+    __host__ __device__ long long tokens(int t) const {        // times G
         if (t == blocks - 1) return all;
         const long long v = off + (long long)R * (t + 1);
         return v < 0 ? 0 : v < all ? v : all;
     }
-    __device__ long long before(int t) const {        // cost of the blocks 0 .. t - 1, t < blocks
-        long long from = off >= 0 ? 0 : -off / R;     // (R: a power of two) the first block with off + R (t + 1) > 0
-        if (from > t) from = t;
-        const long long n = t - from;
-        return t * own + n * off + R * ((long long)t * (t + 1) - from * (from + 1)) / 2;
+    __host__ __device__ long long before(int t) const {        // cost of the blocks 0 .. t - 1, t < blocks
+        // blocks some .. whole - 1 see off + R (their number + 1), those from there on all (drafted tokens with a mask, or cut off)
+        const long long from = some < t ? some : t, to = whole < from ? from : whole < t ? whole : t;
+        return t * own + (to - from) * off + R * (to * (to + 1) - from * (from + 1)) / 2 + (t - to) * all;
     }
-    __device__ long long total() const { return blocks ? before(blocks - 1) + own + all : 0; }
+    __host__ __device__ long long total() const { return blocks ? before(blocks - 1) + own + all : 0; }
 };
 
 // a / b, both not negative; 64-bit divisions take a microsecond together where 32 bits do
