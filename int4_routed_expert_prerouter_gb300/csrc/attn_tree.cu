@@ -5,8 +5,8 @@
 // K and V enter the tensor core as exact fp16 operands, code - z (z half the code range), so that the weights' rounding
 // to fp16 is the only one beside the result's; an earlier form with the values s q + b themselves as operands
 // was off by 4.3e-4 of the outputs' size against 64 bits, this one by 2.9e-4 (plain form: 2.1e-4).  Per group g of 64 dims
-//   S = sum_g s_g S_g,       S_g = Q_g (code - z) + 64 mean(Q_g) r_g,   r = b / s + z;
-//   o = sum_g P'_g V'_g,     P'_g = fp16(p m_g 2^10),  V' = (code - z) 2^e and r'_g = b / m + z 2^e beside it,
+//   S = sum_g s_g S_g,       S_g = Q_g (code - z) + 64 mean(Q_g) r_g,   r = (b + z s) / s;
+//   o = sum_g P'_g V'_g,     P'_g = fp16(p m_g 2^10),  V' = (code - z) 2^e and r'_g = (b + z s) / m beside it,
 // s = m 2^e with m in [1, 2): a weight's place in fp16's range does not depend on V's scales.  The mean's and the offsets'
 // products are part of the same matrix steps (one more step of 16 for S, two more columns for o), each factor as
 // two fp16 (2^-22).
@@ -255,8 +255,8 @@ __device__ __forceinline__ bool make_rows(const char* raw, char* stage, int row0
         const bool none = tok >= left, flat = sb.x == 0.f;
         float* table = reinterpret_cast<float*>(stage + (VALUE ? X::kVTab : X::kKTab)) + (row >> 1) * 2 * GR + 2 * g + (row & 1);
         if (!VALUE) {
-            // b = 1 (0 - z + b + z) of a constant group
-            const float off = none ? 0.f : flat ? sb.y + kZ : __fdividef(sb.y, sb.x) + kZ;
+            // b = 1 (0 - z + b + z) of a constant group; else (b + z s) / s, the sum first: it may be far smaller than b
+            const float off = none ? 0.f : flat ? sb.y + kZ : __fdividef(fmaf(kZ, sb.x, sb.y), sb.x);
             // (hi, 2^11 lo) of the mean against (off, off / 2^11), then against what these leave
             const uint32_t a = split<0>(off * (kGroup / 1024.f)), b = split<0>(off * (kGroup / 1024.f / 2048.f));
             if (i < 16 * GR) {
@@ -273,7 +273,7 @@ __device__ __forceinline__ bool make_rows(const char* raw, char* stage, int row0
             const float z = kZ - (float)(row & 1);
             const int e = max(-10, min(kMostE, (int)(__float_as_uint(sb.x) >> 23 & 255) - 127));
             const float m = out ? 0.f : nan ? __int_as_float(0x7fffffff) : flat ? 1.f : sb.x * __uint_as_float((uint32_t)(127 - e) << 23);
-            const float r = out || nan ? 0.f : flat ? sb.y : __fdividef(sb.y, m) + z * __uint_as_float((uint32_t)(127 + e) << 23);
+            const float r = out || nan ? 0.f : flat ? sb.y : __fdividef(fmaf(z, sb.x, sb.y), m);
             kept[q] = out || nan || flat ? kZeros : (uint32_t)(e + 16);
             if (i < 16 * GR) {
                 *table = m * kUpV;

@@ -223,6 +223,32 @@ def test_rows_of_huge_scores_beside_ordinary_ones(bits, D, q_size, k_size, scale
     assert ahead[far].float().mean() > 0.2 and ((got.double() - best).abs() <= 2.0 ** -9 * best.abs() + 1e-4)[ahead].all()
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_size", [1.0, 300.0])
+@pytest.mark.parametrize("n,x", [(0, 40), (150, 9)])
+def test_groups_around_zero(bits, D, q_size, n, x):
+    """Offsets that take off what the middle code stands for: most codes' values are a few steps, far smaller than the offset, and
+    those of the middle code are zero."""
+    H, G, page, z = 2, 4, 16, 2 ** (bits - 1)
+    pool = Pool(-(-(n + x) // page), page, H, D, bits)
+    rng, shape = np.random.default_rng(D), tuple(pool.codes.shape)
+    codes = rng.integers(z - 2, z + 3, shape)
+    s = (rng.uniform(0.01, 0.03, shape[:-1] + (D // 64,))).astype(np.float16)
+    b = (-s.astype(np.float64) * z).astype(np.float16)          # (a power of two times s: exact)
+    pool.image.copy_(torch.from_numpy(ref.page_image(codes.astype(np.uint8), s, b, bits)).to(DEV))
+    pool.codes, pool.s, pool.b = (torch.from_numpy(np.ascontiguousarray(a)).to(DEV).double() for a in (codes, s, b))
+    q, table = (rows(x, H * G, D).float() * q_size).half(), np.arange(shape[0])[None]
+    args = pool, q, table, [n], [0, x], None
+    # V's parts: every other token's codes are taken about z - 1.  Pool.tokens has them about z for all, where both parts of a middle
+    # code are 0; about z - 1 they are s and -s, and fp32 sums of them are off by 2^-21 (s + s) at most, not by 0.
+    tokens, odd = pool.tokens, torch.arange(n + x, device=DEV)[:, None, None] % 2
+    wide = lambda a: a[:, 1].flatten(0, 1)[:n + x].repeat_interleave(64, -1)
+    ws, wb, wq = wide(pool.s), wide(pool.b), pool.codes[:, 1].flatten(0, 1)[:n + x]
+    pool.tokens = lambda pages, m: (*tokens(pages, m)[:3], (ws * (wq - (z - odd))).abs() + (ws * (z - odd) + wb).abs(), tokens(pages, m)[4])
+    check(call(*args), *args)
+
+
 def test_masks():
     """Rows that see nothing, drafted tokens behind the row, bits behind the sequence's tokens, words beyond need."""
     pool, q, table, lens, cu, _ = case(4, 128, 2, 4, 16, [0, 50, 0], [40, 40, 3])
