@@ -265,6 +265,23 @@ def test_the_same_bits_whatever_else_is_packed():
     assert torch.equal(binding.attn_prompt(q2, k2, v2, i32(cu))[cu[2]:], a[cu[2]:])
 
 
+@pytest.mark.parametrize("D,Hq", [(64, 8), (128, 8), (256, 10)])
+def test_rows_behind_2_31_elements(D, Hq):
+    T, ld, H = 290, 1 << 23, 2
+    wide = torch.empty(T, ld, dtype=torch.float16, device=DEV)
+    at = np.cumsum([0, Hq * D, H * D, H * D, Hq * D])
+    q, k, v, out = (wide[:, a:b].unflatten(1, (-1, D)) for a, b in zip(at, at[1:]))
+    for x in (q, k, v):
+        x.copy_(rows(*x.shape))
+    v[200, 1, 3] = float("inf")
+    cu = [0, 20, T]
+    binding.attn_prompt(q, k, v, i32(cu), out=out)
+    dense = [x.contiguous() for x in (q, k, v)]
+    assert torch.equal(out, binding.attn_prompt(*dense, i32(cu)))
+    dense[2][200, 1, 3] = 0
+    check(out.contiguous().masked_fill(out.isinf(), 0.0)[:200], *dense, [0, 20, 200], [0, 20, 200])
+
+
 def test_bounds_outside_the_rows_touch_nothing():
     D = 128
     q, k, v = rows(100, 2, D), rows(100, 1, D), rows(100, 1, D)

@@ -330,6 +330,20 @@ def test_what_lies_outside_is_reported():
     check(got, pool, q, table, lens, cu, mask[:, :1])
 
 
+@pytest.mark.parametrize("bits,D", [(8, 128), (4, 256)])
+def test_pages_behind_2_31_bytes(bits, D):
+    H, G, page, lens, counts = 4, 4, 128, [1500, 60], [9, 40]
+    pool, q, table, lens, cu, mask = case(bits, D, H, G, page, lens, counts)
+    few = pool.image.shape[0]
+    times = (5 << 30) // pool.image.numel()
+    pool.cache = binding.KVCache(few * times, page, H, D, bits, pages=pool.image.repeat(times, 1))
+    rng = np.random.default_rng(0)
+    far = np.where(table < 0, -1, table + few * rng.integers(times // 2, times, table.shape))
+    got = call(pool, q, far, lens, cu, mask)
+    check(got, pool, q, table, lens, cu, mask)
+    assert pool.cache.error() == binding.EDGE0_OK
+
+
 def test_bounds_outside_the_rows_touch_nothing():
     pool, q, table, lens, _, _ = case(4, 128, 1, 2, 16, [30, 20, 10, 5], [10, 10, 10, 10])
     guard = torch.full((120, 2, 128), 9.0, dtype=torch.float16, device=DEV)
