@@ -9,10 +9,10 @@
 //
 // What bounds it.  Long prompts: a stream's chain of scores, weights and product (about 2,900 cycles a tile, of which
 // the tensor core works 2,048 for both streams) and the power it takes; 16,384 tokens, 32 heads of 128: 1,420 to 1,580 us with
-// the clocks, 1,390 to 1,550 TFLOP/s.  Short ones: a block's start and end; 64 prompts of up to 1,024 tokens 269 us, of
+// the clocks, 1,390 to 1,550 TFLOP/s.  Short ones: a block's start and end; 64 prompts of up to 1,024 tokens 263 us, of
 // which each CTA spends a fifth on outputs (their reads from staging one by one instead of together, and a look at
-// empty rows apart: 279).  One prompt of 131 tokens, heads of 256: 10 us.  Weights formed before the maximum is known, and the
-// maximum looked for only of too large a sum, gained nothing (269 and 273).
+// empty rows apart: 279 instead of 269).  One prompt of 131 tokens, heads of 256: 10 us.  Weights formed before the maximum is
+// known, and the maximum looked for only of too large a sum, gained nothing (273 instead of 269 at that time).
 #include "flash.cuh"
 
 #include <cuda.h>

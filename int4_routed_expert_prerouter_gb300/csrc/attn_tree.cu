@@ -22,11 +22,13 @@
 // stalls were for instructions to arrive.  8 the matrix steps; 9 copies strips' halves (16 tokens of K or of V, one run of
 // bytes) into a ring of raw ones; the rest turn those into operands and tables.
 //
-// What bounds it: neither bytes (0.6 TB/s) nor the tensor cores (20 % of their cycles) but the latencies between
+// What bounds it: neither bytes (15 % of DRAM's cycles) nor the tensor cores (28 % of theirs) but the latencies between
 // the roles and their instructions, half of them spent on turning codes into operands: about 2,300 cycles a step of 64
-// tokens.  64 sequences of up to 4,000 tokens with up to 16 drafted ones: 157 us; four of up to 131,072 with up to 48: 915 us, 396
-// TFLOP/s; one of 777 tokens: 25.7 us.  Weights in columns of their own, so that the next scores need not wait for
-// their product, leave no room for the queries, which the steps then read from shared memory: 171 and 990 us.
+// tokens.  64 sequences of up to 4,000 tokens with up to 16 drafted ones: 157 us; four of up to 131,072 with up to 48: 925
+// us, 393 TFLOP/s; one of 777 tokens: 25.6 us.  A block costs nearly the same whatever its rows: chains of 2 and of 8 tokens
+// over those four contexts take 386 and 390 us, where a single token's attention takes 112.
+// Weights in columns of their own, so that the next scores need not wait for their product, leave no room for the queries, which the
+// steps then read from shared memory: 171 and 990 us.
 #include "flash.cuh"
 
 namespace edge0 {

@@ -41,14 +41,15 @@ constexpr int kSoftmax = 256;         // threads of the two softmax warpgroups
 
 // What the shares go by: a block's rows (kBlock), tokens per step (kTile), head width, and in tiles
 //   kOwn        what a block costs beside its tiles (its queries, the first scores, the last product, its outputs).  1 instead
-//               of 4: 64 prompts of up to 1,024 tokens 299 us instead of 279, drafts of 64 sequences 199 instead of 185;
-//               8: 298 and 190;
+//               of 4: 64 prompts of up to 1,024 tokens 279 us instead of 263, one short prompt 18 instead of 10, drafts of 64
+//               sequences of 500 to 4,000 tokens 179 instead of 159; 8: 278, 10 and 150;
 //   kMinSplit   from which on a block may be cut (a cut costs a start and an end more, parts of fp32 and their join).  4
-//               instead of 8: a prompt of 1,000 tokens 44 us instead of 33, drafts behind 300 tokens 18 instead of 15;
+//               instead of 8: drafts behind 300 tokens 17.7 us instead of 14.5, prompts the same;
 //   kMinWhole   likewise, where a block is not as much as two shares: there it is only the shares' evenness that a cut
-//               serves.  8 instead of 32: a prompt of 2,000 tokens 64.5 us instead of 55, of 4,000 131 instead of 122; drafted
-//               tokens' blocks cost less to cut (8 and 32: 185 and 194 us);
-//   kMinShare   that a share has at least.  2, 4, 8, 12: one short prompt 10.6, 10.6, 15.5 and 19.9 us.
+//               serves.  8 instead of 32: a prompt of 1,000 tokens 31.6 us instead of 25, of 2,000 63 instead of 54, of 4,000
+//               129 instead of 120; drafted tokens' blocks cost less to cut (8 and 32: drafts of 64 sequences 159.6 and 160.5 us);
+//   kMinShare   that a share has at least.  2, 4, 8, 12: one short prompt 10.0, 10.0, 14.0 and 18.3 us, drafts behind 2,000
+//               tokens 20.9, 20.1, 24.0 and 25.0.
 template <int D>
 struct Shape {
     static constexpr int kD = D, kTile = flash::kTile, kMinSplit = 8, kMinWhole = 32, kMinShare = 4, kOwn = 4;
@@ -364,7 +365,7 @@ struct Control {
 };
 
 // One look at a phase.  What it orders is this CTA's alone: the scope of a cluster invalidates L1 with every look (one long
-// prompt 1,495 -> 1,418 us, drafts of 64 sequences 211 -> 200).  Looks that do not suspend cost more (1,535 and 207), and
+// prompt 1,495 -> 1,418 us, drafts of 64 sequences 211 -> 200 when it came in).  Looks that do not suspend cost more (1,535 and 207), and
 // so do those that name the time to suspend for (1,493 and 218) and sixteen looks in a row between two readings of the clock
 // (1,417 and 223).
 __device__ __forceinline__ bool look(uint64_t* bar, uint32_t parity) {
@@ -782,7 +783,8 @@ __device__ __forceinline__ void softmax_warps(const Src& p, Control& c, char* q_
     }
 }
 
-// Start of a CTA.  Barriers' counts: an entry's arrival 1 (full_count), its release 1 + free_extra.
+// Start of a CTA.  Barriers' counts: arrivals of a ring entry's copy, of those that have looked it through, of those that
+// are done with it, of a stream's queries.
 __device__ __forceinline__ void control_init(Control& c, int full_count, int clean_count, int free_count, int q_count, bool dead) {
     for (int i = 0; i < kMaxStages; ++i) {
         mbar_init(&c.full[i], full_count);

@@ -1,11 +1,11 @@
 // Moves inside the quantised KV cache: kept rows drawn together (accepted drafts, evicted
 // contexts), whole pages copied (forks).  Codes and (s, b) pairs move as they are.
 //
-// Both are bound by the bytes read and written, or by a few dependent reads where there is
-// little to move (row number, page numbers, the row).  Accepted ones of 64 sequences' 16 drafted tokens, 8 heads of
-// 128 dims in 4 bits: 4.6 us, hardly more than an empty kernel's.  A quarter of 7 contexts of 8,191 tokens in 8 bits: 19.6 us
-// for 31 MB; a sequence's chunks follow one another, each a read behind a look at the tables.  1,000 pages copied eight times over:
-// 131 us for 664 MB, 74 % of what a plain copy moves.
+// Copies of pages are bound by the bytes; rows by reads that depend on one another (row number, page numbers, the
+// row), a chunk of rows after the other.  Accepted ones of 64 sequences' 16 drafted tokens, 8 heads of
+// 128 dims in 4 bits: 4.5 us, hardly more than an empty kernel's.  A quarter of 7 contexts of 8,191 tokens in 8 bits: 19.5 us
+// for 31 MB: the longest sequence's CTAs go through ten chunks while the others have ended.  1,000 pages copied eight times over:
+// 131 to 140 us for 664 MB, 70 to 74 % of what a plain copy moves.
 #include "kvcache.cuh"
 #include "launch.cuh"
 

@@ -13,9 +13,10 @@
 // in the row, 2 x 8 dims (half layout) or 8 dims (interleaved), and goes through its CTA's tokens,
 // kRopeRows of them under way.
 //
-// Bound by the bytes: 8,192 tokens of prompts, 32 + 8 heads of 128 of which 64 dims turn, 31.4 us for 158 MB, 0.74 of a copy.
+// 8,192 tokens of prompts, 32 + 8 heads of 128 of which 64 dims turn: 31.5 us for 158 MB, 0.74 of a copy.  What bounds it is
+// latency: one wave of CTAs, all of which form sines first and load afterwards (DRAM 44 %, issue slots 47 %, warps 40 %).
 // (First values under way while the sines are formed: 36.7; places and tokens as one row of units, so that no thread
-// is left over: 32.4; at most 8 tokens a CTA: 33.4.)  A step of 64 tokens: 4.5 us, launch and two dependent reads.
+// is left over: 32.4; at most 8 tokens a CTA: 33.4.)  A step of 64 tokens: 4.6 us, launch and two dependent reads.
 #include "kvcache.cuh"
 #include "launch.cuh"
 
